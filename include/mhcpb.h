@@ -383,6 +383,149 @@ mhcpb_status_t mhcpb_gate_backward(int64_t T, int n_iter, const float* proj, con
                                    const float* alpha, const float* bias, const float* grad_h,
                                    float* grad_proj, float* grad_r, float* dlogits, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the stage: what a model needs between its token ids,
+ * the residual streams X and a sublayer (n = 4 streams of hidden size D, so
+ * K = 4 D):
+ *
+ *     mhcpb_embed_*          token ids -> X, and the embedding table's gradient
+ *     mhcpb_layernorm_*      a norm of any [T, D] activations
+ *     mhcpb_collapse_norm_*  X and the gates H_pre -> the sublayer's normalised input
+ *     mhcpb_dropout          dropout without a stored mask
+ *     mhcpb_update_*         X, H_res, H_post and the sublayer's output -> the next X
+ *
+ * One sublayer is mhcpb_forward_gates (proj, r and h from X), collapse_norm
+ * (y), the caller's sublayer, update (the next X).  Its backward is
+ * update_backward (the sublayer output's gradient and columns 4..23 of
+ * grad_h), the caller's sublayer, collapse_norm_backward (columns 0..3 of
+ * grad_h, and the part of dX that does not go through the projection),
+ * mhcpb_gate_backward (grad_proj and grad_r from grad_h), and mhcpb_execute
+ * with that part of dX as its grad_x_addend.
+ *
+ * Common rules.  No plan: the calls run on the calling thread's current
+ * device, where every operand must be device memory
+ * (MHCPB_ERR_WRONG_DEVICE).  Nothing is allocated and nothing synchronises;
+ * the calls are enqueued on `stream` and can be captured into a CUDA graph.
+ * FP32 arithmetic; each output is rounded once, to its own type.  Every result
+ * is bitwise reproducible for the same sizes and alignment.  Outputs are
+ * overwritten (parameter gradients are added to with MHCPB_ACCUMULATE_DW) and
+ * overlap no other operand (MHCPB_ERR_ALIASING), except where "in place" is
+ * said.  Layouts are compact and row-major unless a stride is given; a stride
+ * counts elements between rows, at least the row's width (else
+ * MHCPB_ERR_UNSUPPORTED_SHAPE) and at most 2^24.  Pointers are aligned to
+ * their element's size (MHCPB_ERR_MISALIGNED); streams, their gradients and
+ * collapse_norm's and update's other BF16 operands, and workspaces, to 16
+ * bytes.  Sizes that are multiples of 8, on 16-byte aligned pointers, run
+ * fastest.  T = 0 is valid: there is nothing to write but the parameter
+ * gradients, which are then 0 (or unchanged when accumulating); operands with
+ * no elements may be NULL.  1 <= D, with D <= MHCPB_MAX_K for mhcpb_layernorm_*,
+ * 4 D <= MHCPB_MAX_K for the streams, n_streams * D <= MHCPB_MAX_K for
+ * mhcpb_embed_*; 0 <= T <= MHCPB_MAX_T (else MHCPB_ERR_UNSUPPORTED_SHAPE).
+ * Unknown types or flags: MHCPB_ERR_INVALID_ARG.  Non-finite values propagate
+ * as the formulas say and never leave their token (parameter gradients apart). */
+enum {                      /* element types */
+    MHCPB_BF16 = 0,
+    MHCPB_FP16 = 1,
+    MHCPB_FP32 = 2
+};
+#define MHCPB_MAX_VOCAB (1 << 24)
+#define MHCPB_MAX_STREAMS 16
+
+/* x[t, s, :] = bf16(scale * table[ids[t], :]) for each of n_streams streams s.
+ * table: `type` [V, D]; ids: [T] signed integers of id_bytes = 4 or 8 bytes; x: BF16
+ * [T, n_streams * D].  An id outside [0, V), such as a padding id of -1, gives
+ * a row of zeros.  1 <= V <= MHCPB_MAX_VOCAB, 1 <= n_streams <= MHCPB_MAX_STREAMS. */
+mhcpb_status_t mhcpb_embed_forward(int64_t T, int64_t V, int64_t D, int n_streams, int type,
+                                   const void* table, const void* ids, int id_bytes, float scale,
+                                   void* x, void* stream);
+/* grad_table[v, :] = scale * sum over tokens t with ids[t] = v and streams s of
+ * grad_x[t, s, :], FP32 [V, D]; rows no token names are written as zeros, or
+ * left alone with MHCPB_ACCUMULATE_DW.  grad_x: BF16 [T, n_streams * D].  Ids
+ * outside [0, V) contribute nothing.  The tokens are sorted by id and each
+ * row is summed in a fixed order (no atomic adds). */
+mhcpb_status_t mhcpb_embed_workspace_bytes(int64_t T, int64_t V, int64_t D, size_t* bytes);
+mhcpb_status_t mhcpb_embed_backward(int64_t T, int64_t V, int64_t D, int n_streams,
+                                    const void* grad_x, const void* ids, int id_bytes, float scale,
+                                    uint32_t flags, float* grad_table, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Layer norm over the last axis of x: `type` [T, D] with a row stride:
+ *     mean = sum x / D, rstd = 1 / sqrt(sum (x - mean)^2 / D + eps)
+ *     y    = (x - mean) * rstd * gamma + beta
+ * gamma, beta: FP32 [D], NULL for ones and zeros.  y: `type`.  mean and rstd:
+ * FP32 [T], both NULL where no backward follows.  eps finite and >= 0. */
+mhcpb_status_t mhcpb_layernorm_forward(int64_t T, int64_t D, int type, const void* x,
+                                       int64_t x_stride, const float* gamma, const float* beta,
+                                       float eps, void* y, int64_t y_stride, float* mean,
+                                       float* rstd, void* stream);
+/* Its gradient from x, grad_y (`type`) and the forward's mean and rstd, with
+ * z = (x - mean) rstd, w = grad_y gamma:
+ *     grad_x = rstd (w - sum w / D - z sum(w z) / D)           `type`
+ *     grad_gamma = sum_t grad_y z,  grad_beta = sum_t grad_y   FP32 [D], each may be NULL
+ * `workspace` is not looked at (and may be NULL) when both are. */
+mhcpb_status_t mhcpb_layernorm_workspace_bytes(int64_t T, int64_t D, size_t* bytes);
+mhcpb_status_t mhcpb_layernorm_backward(int64_t T, int64_t D, int type, const void* x,
+                                        int64_t x_stride, const void* grad_y, int64_t grad_y_stride,
+                                        const float* gamma, const float* mean, const float* rstd,
+                                        void* grad_x, int64_t grad_x_stride, float* grad_gamma,
+                                        float* grad_beta, uint32_t flags, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* y[e] = x[e] / (1 - p) where element e is kept, else 0 (whatever x[e] holds).
+ * The mask comes from a counter and is never stored: element e is kept when
+ *     word e % 4 of Philox4x32-10(counter {e / 4, rng[1] + sequence}, key rng[0])
+ * is at least floor(p 2^32 + 1/2).  (Philox: Salmon, Moraes, Dror, Shaw, SC
+ * 2011; counter and key words low half first, sums modulo 2^64.)  rng: two
+ * 64-bit integers in device memory, 8-byte aligned, read when the call runs,
+ * so that a captured graph draws new masks when the caller advances rng[1]
+ * between replays; `sequence` tells the dropouts of one step apart.  The
+ * gradient is the same call on the gradient.  0 <= p < 1; with p = 0, rng is
+ * not looked at and may be NULL.  y may be x (in place). */
+mhcpb_status_t mhcpb_dropout(int64_t n, int type, const void* x, float p, const void* rng,
+                             uint64_t sequence, void* y, void* stream);
+
+/* The sublayer's input: u = sum_s h[t, s] X[t, s, :] over the four streams
+ * (H_pre is columns 0..3 of h [T, 24]), kept in FP32, then the layer norm of u
+ * as above.  x: BF16 [T, 4 D]; y: BF16 [T, D]; mean and rstd of u. */
+mhcpb_status_t mhcpb_collapse_norm_forward(int64_t T, int64_t D, const void* x, const float* h,
+                                           const float* gamma, const float* beta, float eps,
+                                           void* y, float* mean, float* rstd, void* stream);
+/* Its gradient, with the residual path's share of dX (u is formed again from X):
+ *     du = the layer norm's grad_x of grad_y
+ *     grad_x[t, j, :] = h[t, j] du + sum_i H_res[t][i][j] grad_x_out[t, i, :]
+ *     grad_h[t, j]    = <X[t, j, :], du>    j < 4; columns 4..23 are not touched
+ * grad_x_out: BF16 [T, 4 D], the gradient of the streams after the sublayer;
+ * NULL leaves that sum out.  grad_x: BF16 [T, 4 D].  grad_gamma, grad_beta,
+ * flags and workspace as for mhcpb_layernorm_backward. */
+mhcpb_status_t mhcpb_collapse_norm_workspace_bytes(int64_t T, int64_t D, size_t* bytes);
+mhcpb_status_t mhcpb_collapse_norm_backward(int64_t T, int64_t D, const void* x, const float* h,
+                                            const void* grad_y, const float* gamma,
+                                            const float* mean, const float* rstd,
+                                            const void* grad_x_out, void* grad_x, float* grad_h,
+                                            float* grad_gamma, float* grad_beta, uint32_t flags,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* The streams after the sublayer, with dropout of its output y (as
+ * mhcpb_dropout on y [T, D]; p = 0: none):
+ *     x_out[t, i, :] = sum_j H_res[t][i][j] X[t, j, :] + H_post[t][i] drop(y)[t, :]
+ * H_post is columns 4..7 of h [T, 24], H_res columns 8 + 4 i + j.  x, x_out:
+ * BF16 [T, 4 D], x_out may be x (in place); y: BF16 [T, D]. */
+mhcpb_status_t mhcpb_update_forward(int64_t T, int64_t D, const void* x, const void* y,
+                                    const float* h, float p, const void* rng, uint64_t sequence,
+                                    void* x_out, void* stream);
+/* Its gradient but for X (mhcpb_collapse_norm_backward adds that):
+ *     grad_y = drop(sum_i H_post[t][i] grad_x_out[t, i, :])                BF16 [T, D]
+ *     grad_h[t, 4 + i]         = <grad_x_out[t, i, :], drop(y)[t, :]>
+ *     grad_h[t, 8 + 4 i + j]   = <grad_x_out[t, i, :], X[t, j, :]>;  columns 0..3 are not touched */
+mhcpb_status_t mhcpb_update_backward(int64_t T, int64_t D, const void* x, const void* y,
+                                     const float* h, float p, const void* rng, uint64_t sequence,
+                                     const void* grad_x_out, void* grad_y, float* grad_h,
+                                     void* stream);
+
+/* mhcpb_debug_checked_sites for the operators above: sites[3] = {embedding,
+ * norms, dropout and update}, read and cleared apart from that call's words. */
+mhcpb_status_t mhcpb_debug_checked_operator_sites(uint32_t* sites, int* checked);
+
 /* Releases the plan (and its status word).  Safe on NULL. */
 mhcpb_status_t mhcpb_destroy(mhcpb_plan_t plan);
 

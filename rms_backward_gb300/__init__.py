@@ -172,3 +172,23 @@ def mhc_gate_backward(proj, r, alpha, bias, grad_h, grad_proj, grad_r, dlogits=N
                             bias.data_ptr(), grad_h.data_ptr(), grad_proj.data_ptr(),
                             grad_r.data_ptr(), None if dlogits is None else dlogits.data_ptr(),
                             _stream_handle(stream, proj))
+
+
+_OPERATORS = (
+    "mhc_embed_forward", "mhc_embed_workspace_bytes", "mhc_embed_backward", "mhc_layernorm_forward",
+    "mhc_layernorm_workspace_bytes", "mhc_layernorm_backward", "mhc_dropout", "mhc_collapse_norm_forward",
+    "mhc_collapse_norm_workspace_bytes", "mhc_collapse_norm_backward", "mhc_update_forward", "mhc_update_backward",
+)
+
+
+def __getattr__(name):
+    """The operators of :mod:`.operators`, imported (with torch) at first use."""
+    if name in _OPERATORS:
+        from . import operators
+        globals().update({n: getattr(operators, n) for n in _OPERATORS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted([*globals(), *_OPERATORS])

@@ -42,6 +42,12 @@ def MHCPB_PARTIAL_TOKENS(T: int) -> int:
 MHCPB_STATIC_SCRATCH_BYTES = 16 << 20
 MHCPB_GATE_MAX_ITER = 64
 
+MHCPB_BF16 = 0
+MHCPB_FP16 = 1
+MHCPB_FP32 = 2
+MHCPB_MAX_VOCAB = 1 << 24
+MHCPB_MAX_STREAMS = 16
+
 QUERY = {"T": 0, "K": 1, "S": 2, "grid": 3, "flags": 4, "smem": 5, "token_tile": 6, "strip": 7,
          "partial_tokens": 8}
 
@@ -51,7 +57,12 @@ EXPORTED = ("mhcpb_plan_create", "mhcpb_workspace_bytes", "mhcpb_execute", "mhcp
             "mhcpb_execute_static_scratch", "mhcpb_plan_set_max_ctas", "mhcpb_execute_dx",
             "mhcpb_reduce_dw", "mhcpb_forward_workspace_bytes", "mhcpb_forward",
             "mhcpb_forward_profiled", "mhcpb_gate_forward", "mhcpb_gate_backward",
-            "mhcpb_debug_checked_sites", "mhcpb_forward_gates")
+            "mhcpb_debug_checked_sites", "mhcpb_forward_gates",
+            "mhcpb_embed_forward", "mhcpb_embed_workspace_bytes", "mhcpb_embed_backward",
+            "mhcpb_layernorm_forward", "mhcpb_layernorm_workspace_bytes", "mhcpb_layernorm_backward",
+            "mhcpb_dropout", "mhcpb_collapse_norm_forward", "mhcpb_collapse_norm_workspace_bytes",
+            "mhcpb_collapse_norm_backward", "mhcpb_update_forward", "mhcpb_update_backward",
+            "mhcpb_debug_checked_operator_sites")
 
 
 class MhcpbError(RuntimeError):
@@ -95,6 +106,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mhcpb_gate_forward.argtypes = [I64, I32, P, P, P, P, P, P]
     lib.mhcpb_gate_backward.argtypes = [I64, I32, P, P, P, P, P, P, P, P, P]
     lib.mhcpb_debug_checked_sites.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(I32)]
+    F32, U64 = ctypes.c_float, ctypes.c_uint64
+    lib.mhcpb_embed_forward.argtypes = [I64, I64, I64, I32, I32, P, P, I32, F32, P, P]
+    lib.mhcpb_embed_workspace_bytes.argtypes = [I64, I64, I64, ctypes.POINTER(SZ)]
+    lib.mhcpb_embed_backward.argtypes = [I64, I64, I64, I32, P, P, I32, F32, U32, P, P, SZ, P]
+    lib.mhcpb_layernorm_forward.argtypes = [I64, I64, I32, P, I64, P, P, F32, P, I64, P, P, P]
+    lib.mhcpb_layernorm_workspace_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+    lib.mhcpb_layernorm_backward.argtypes = [I64, I64, I32, P, I64, P, I64, P, P, P, P, I64, P, P, U32, P, SZ, P]
+    lib.mhcpb_dropout.argtypes = [I64, I32, P, F32, P, U64, P, P]
+    lib.mhcpb_collapse_norm_forward.argtypes = [I64, I64, P, P, P, P, F32, P, P, P, P]
+    lib.mhcpb_collapse_norm_workspace_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+    lib.mhcpb_collapse_norm_backward.argtypes = [I64, I64, P, P, P, P, P, P, P, P, P, P, P, U32, P, SZ, P]
+    lib.mhcpb_update_forward.argtypes = [I64, I64, P, P, P, F32, P, U64, P, P]
+    lib.mhcpb_update_backward.argtypes = [I64, I64, P, P, P, F32, P, U64, P, P, P, P]
+    lib.mhcpb_debug_checked_operator_sites.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(I32)]
     lib.mhcpb_destroy.argtypes = [P]
     lib.mhcpb_status_string.argtypes = [I32]
     lib.mhcpb_status_string.restype = ctypes.c_char_p
@@ -106,7 +131,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "mhcpb_plan_set_max_ctas", "mhcpb_execute_dx", "mhcpb_reduce_dw",
                  "mhcpb_forward_workspace_bytes", "mhcpb_forward", "mhcpb_forward_profiled",
                  "mhcpb_gate_forward", "mhcpb_gate_backward", "mhcpb_debug_checked_sites",
-                 "mhcpb_forward_gates"):
+                 "mhcpb_forward_gates", "mhcpb_embed_forward", "mhcpb_embed_workspace_bytes",
+                 "mhcpb_embed_backward", "mhcpb_layernorm_forward", "mhcpb_layernorm_workspace_bytes",
+                 "mhcpb_layernorm_backward", "mhcpb_dropout", "mhcpb_collapse_norm_forward",
+                 "mhcpb_collapse_norm_workspace_bytes", "mhcpb_collapse_norm_backward",
+                 "mhcpb_update_forward", "mhcpb_update_backward", "mhcpb_debug_checked_operator_sites"):
         getattr(lib, name).restype = I32
     _lib = lib
     return lib
@@ -250,3 +279,97 @@ def mhcpb_debug_checked_sites():
     checked = ctypes.c_int()
     _check(load().mhcpb_debug_checked_sites(sites, ctypes.byref(checked)), "mhcpb_debug_checked_sites")
     return bool(checked.value), dict(zip(CHECKED_FAMILIES, list(sites)))
+
+
+def _size(name: str, *args: int) -> int:
+    n = ctypes.c_size_t()
+    _check(getattr(load(), name)(*args, ctypes.byref(n)), name)
+    return n.value
+
+
+def mhcpb_embed_forward(T: int, V: int, D: int, n_streams: int, type_: int, table: int, ids: int, id_bytes: int,
+                        scale: float, x: int, stream: int | None) -> None:
+    """x[t, s, :] = scale * table[ids[t], :] for each of n_streams streams."""
+    _check(load().mhcpb_embed_forward(T, V, D, n_streams, type_, table, ids, id_bytes, scale, x, stream or None),
+           "mhcpb_embed_forward")
+
+
+def mhcpb_embed_workspace_bytes(T: int, V: int, D: int) -> int:
+    return _size("mhcpb_embed_workspace_bytes", T, V, D)
+
+
+def mhcpb_embed_backward(T: int, V: int, D: int, n_streams: int, grad_x: int, ids: int, id_bytes: int, scale: float,
+                         flags: int, grad_table: int, workspace: int, workspace_bytes: int,
+                         stream: int | None) -> None:
+    """grad_table [V, D] from grad_x, summed by token in a fixed order."""
+    _check(load().mhcpb_embed_backward(T, V, D, n_streams, grad_x, ids, id_bytes, scale, flags, grad_table, workspace,
+                                       workspace_bytes, stream or None), "mhcpb_embed_backward")
+
+
+def mhcpb_layernorm_forward(T: int, D: int, type_: int, x: int, x_stride: int, gamma: int | None, beta: int | None,
+                            eps: float, y: int, y_stride: int, mean: int | None, rstd: int | None,
+                            stream: int | None) -> None:
+    _check(load().mhcpb_layernorm_forward(T, D, type_, x, x_stride, gamma, beta, eps, y, y_stride, mean, rstd,
+                                          stream or None), "mhcpb_layernorm_forward")
+
+
+def mhcpb_layernorm_workspace_bytes(T: int, D: int) -> int:
+    return _size("mhcpb_layernorm_workspace_bytes", T, D)
+
+
+def mhcpb_layernorm_backward(T: int, D: int, type_: int, x: int, x_stride: int, grad_y: int, grad_y_stride: int,
+                             gamma: int | None, mean: int, rstd: int, grad_x: int, grad_x_stride: int,
+                             grad_gamma: int | None, grad_beta: int | None, flags: int, workspace: int | None,
+                             workspace_bytes: int, stream: int | None) -> None:
+    _check(load().mhcpb_layernorm_backward(T, D, type_, x, x_stride, grad_y, grad_y_stride, gamma, mean, rstd, grad_x,
+                                           grad_x_stride, grad_gamma, grad_beta, flags, workspace, workspace_bytes,
+                                           stream or None), "mhcpb_layernorm_backward")
+
+
+def mhcpb_dropout(n: int, type_: int, x: int, p: float, rng: int | None, sequence: int, y: int,
+                  stream: int | None) -> None:
+    _check(load().mhcpb_dropout(n, type_, x, p, rng, sequence, y, stream or None), "mhcpb_dropout")
+
+
+def mhcpb_collapse_norm_forward(T: int, D: int, x: int, h: int, gamma: int | None, beta: int | None, eps: float,
+                                y: int, mean: int | None, rstd: int | None, stream: int | None) -> None:
+    _check(load().mhcpb_collapse_norm_forward(T, D, x, h, gamma, beta, eps, y, mean, rstd, stream or None),
+           "mhcpb_collapse_norm_forward")
+
+
+def mhcpb_collapse_norm_workspace_bytes(T: int, D: int) -> int:
+    return _size("mhcpb_collapse_norm_workspace_bytes", T, D)
+
+
+def mhcpb_collapse_norm_backward(T: int, D: int, x: int, h: int, grad_y: int, gamma: int | None, mean: int, rstd: int,
+                                 grad_x_out: int | None, grad_x: int, grad_h: int, grad_gamma: int | None,
+                                 grad_beta: int | None, flags: int, workspace: int | None, workspace_bytes: int,
+                                 stream: int | None) -> None:
+    _check(load().mhcpb_collapse_norm_backward(T, D, x, h, grad_y, gamma, mean, rstd, grad_x_out, grad_x, grad_h,
+                                               grad_gamma, grad_beta, flags, workspace, workspace_bytes,
+                                               stream or None), "mhcpb_collapse_norm_backward")
+
+
+def mhcpb_update_forward(T: int, D: int, x: int, y: int, h: int, p: float, rng: int | None, sequence: int, x_out: int,
+                         stream: int | None) -> None:
+    _check(load().mhcpb_update_forward(T, D, x, y, h, p, rng, sequence, x_out, stream or None),
+           "mhcpb_update_forward")
+
+
+def mhcpb_update_backward(T: int, D: int, x: int, y: int, h: int, p: float, rng: int | None, sequence: int,
+                          grad_x_out: int, grad_y: int, grad_h: int, stream: int | None) -> None:
+    _check(load().mhcpb_update_backward(T, D, x, y, h, p, rng, sequence, grad_x_out, grad_y, grad_h, stream or None),
+           "mhcpb_update_backward")
+
+
+OPERATOR_FAMILIES = ("embedding", "norms", "dropout and update")
+
+
+def mhcpb_debug_checked_operator_sites():
+    """(checked, sites) as :func:`mhcpb_debug_checked_sites`, for the operators
+    around the stage."""
+    sites = (ctypes.c_uint32 * 3)()
+    checked = ctypes.c_int()
+    _check(load().mhcpb_debug_checked_operator_sites(sites, ctypes.byref(checked)),
+           "mhcpb_debug_checked_operator_sites")
+    return bool(checked.value), dict(zip(OPERATOR_FAMILIES, list(sites)))

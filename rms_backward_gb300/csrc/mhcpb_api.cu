@@ -16,6 +16,7 @@
 #include "mhcpb.h"
 #include "mhcpb_check.cuh"
 #include "mhcpb_internal.h"
+#include "mhcs_internal.h"
 
 using namespace mhcpb;
 
@@ -163,6 +164,7 @@ const char* encode_tc_maps(CUtensorMap (&m)[6], int64_t T, int64_t K, const void
     return encode_maps(m, T, K, x, dx, add, gp, gr, r);
 }
 int record_cuda_error(cudaError_t e, const char* what) { return (int)cuda_fail(e, what); }
+int check_device_pointer(const void* ptr, int device) { return (int)check_device_ptr(ptr, device); }
 }  // namespace mhcpb
 
 extern "C" {

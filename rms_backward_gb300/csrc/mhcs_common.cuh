@@ -1,0 +1,185 @@
+// Shared device code of the operators around the projection stage (embedding,
+// layer norm, dropout, stream collapse and update): element types, packed
+// loads and stores, the counter-based generator and block reductions.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "mhcpb_check.cuh"
+
+namespace mhcpb {
+namespace ops {
+
+constexpr unsigned kFullMask = 0xffffffffu;
+
+// ------------------------------------------------------------ element types
+template <typename E>
+struct Elem;   // kPack elements make one 16-byte access
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr int kPack = 8;
+    static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<__half> {
+    static constexpr int kPack = 8;
+    static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+};
+template <>
+struct Elem<float> {
+    static constexpr int kPack = 4;
+    static __device__ __forceinline__ float to_float(float v) { return v; }
+    static __device__ __forceinline__ float from_float(float v) { return v; }
+};
+
+// N consecutive elements as FP32.  N > 1: one or two 16-byte accesses, so the
+// address is 16-byte aligned; N == 1: an element access.
+template <typename E, int N>
+__device__ __forceinline__ void load(const E* p, float (&v)[N]) {
+    if constexpr (N == 1) {
+        v[0] = Elem<E>::to_float(*p);
+    } else {
+        constexpr int kPack = Elem<E>::kPack;
+        static_assert(N % kPack == 0, "whole 16-byte accesses");
+#pragma unroll
+        for (int i = 0; i < N / kPack; ++i) {
+            const uint4 raw = reinterpret_cast<const uint4*>(p)[i];
+            const E* e = reinterpret_cast<const E*>(&raw);
+#pragma unroll
+            for (int j = 0; j < kPack; ++j) v[i * kPack + j] = Elem<E>::to_float(e[j]);
+        }
+    }
+}
+template <typename E, int N>
+__device__ __forceinline__ void store(E* p, const float (&v)[N]) {
+    if constexpr (N == 1) {
+        *p = Elem<E>::from_float(v[0]);
+    } else {
+        constexpr int kPack = Elem<E>::kPack;
+        static_assert(N % kPack == 0, "whole 16-byte accesses");
+#pragma unroll
+        for (int i = 0; i < N / kPack; ++i) {
+            uint4 raw;
+            E* e = reinterpret_cast<E*>(&raw);
+#pragma unroll
+            for (int j = 0; j < kPack; ++j) e[j] = Elem<E>::from_float(v[i * kPack + j]);
+            reinterpret_cast<uint4*>(p)[i] = raw;
+        }
+    }
+}
+
+// [base, base + count) of one operand: what a checked build holds accesses to.
+template <typename E>
+struct Span {
+    E* p;
+    size_t count;
+    // whether N elements at index i lie inside (always true in a normal build)
+    __device__ __forceinline__ bool has(size_t i, int n, uint32_t site) const {
+        return check::in(p + i, (size_t)n * sizeof(E), p, count * sizeof(E), site);
+    }
+};
+template <int N, typename E, typename F>
+__device__ __forceinline__ void load_at(const Span<E>& s, size_t i, F (&v)[N], uint32_t site) {
+    if (s.has(i, N, site)) {
+        load<typename std::remove_const<E>::type, N>(s.p + i, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = 0.f;
+    }
+}
+template <int N, typename E>
+__device__ __forceinline__ void store_at(const Span<E>& s, size_t i, const float (&v)[N], uint32_t site) {
+    if (s.has(i, N, site)) store<E, N>(s.p + i, v);
+}
+
+// ------------------------------------------------------------ generator
+// Philox4x32 with 10 rounds (Salmon, Moraes, Dror and Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011): a 128-bit counter and a 64-bit key
+// give four 32-bit words, with no state between calls.
+struct Words {
+    uint32_t w[4];
+};
+__device__ __forceinline__ Words philox(uint64_t counter_lo, uint64_t counter_hi, uint64_t key) {
+    uint32_t c0 = (uint32_t)counter_lo, c1 = (uint32_t)(counter_lo >> 32);
+    uint32_t c2 = (uint32_t)counter_hi, c3 = (uint32_t)(counter_hi >> 32);
+    uint32_t k0 = (uint32_t)key, k1 = (uint32_t)(key >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return Words{{c0, c1, c2, c3}};
+}
+
+// Dropout of one tensor: element e (row-major index) is kept when word e % 4
+// of counter (e / 4, rng[1] + sequence) under key rng[0] is >= threshold, and
+// then multiplied by `scale`.
+struct Drop {
+    const uint64_t* rng;   // device: {key, step}; null when nothing is dropped
+    uint64_t sequence;
+    uint32_t threshold;    // round(p 2^32)
+    float scale;           // 1 / (1 - p)
+};
+struct DropKey {
+    uint64_t key, step;
+};
+__device__ __forceinline__ DropKey drop_key(const Drop& d) {
+    if (d.rng == nullptr) return DropKey{0, 0};
+    return DropKey{d.rng[0], d.rng[1] + d.sequence};
+}
+// v[k] <- dropout of element e + k; N > 1 needs e % 4 == 0.  Dropped elements
+// become 0 whatever they hold (a product with 0 would keep NaN and infinity).
+template <int N>
+__device__ __forceinline__ void drop(const Drop& d, const DropKey& key, uint64_t e, float (&v)[N]) {
+    if (d.rng == nullptr) return;
+    if constexpr (N == 1) {
+        const Words w = philox(e >> 2, key.step, key.key);
+        const int k = (int)(e & 3);
+        const uint32_t r = k == 0 ? w.w[0] : k == 1 ? w.w[1] : k == 2 ? w.w[2] : w.w[3];
+        v[0] = r >= d.threshold ? v[0] * d.scale : 0.f;
+    } else {
+        static_assert(N % 4 == 0, "whole counters");
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const Words w = philox((e >> 2) + i, key.step, key.key);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[i * 4 + j] = w.w[j] >= d.threshold ? v[i * 4 + j] * d.scale : 0.f;
+        }
+    }
+}
+
+// ------------------------------------------------------------ reductions
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+// Sums N values over the block in a fixed order; every thread gets them.
+// scratch: N * 32 floats of shared memory, free again after the call.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float* scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) scratch[i * 32 + warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? scratch[i * 32 + lane] : 0.f);
+    __syncthreads();
+}
+
+}  // namespace ops
+}  // namespace mhcpb
