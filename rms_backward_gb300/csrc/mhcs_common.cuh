@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
+#include <type_traits>
 
 #include "mhcpb_check.cuh"
 
@@ -73,6 +75,89 @@ __device__ __forceinline__ void store(E* p, const float (&v)[N]) {
     }
 }
 
+// ------------------------------------------------------------ pairs
+// The kernels that hold 16-byte vectors compute on pairs: one packed FP32
+// instruction (fma.rn.f32x2 and the like) per two elements, each rounded as
+// its scalar form.
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+template <typename E>
+__device__ __forceinline__ void unpack(const uint4& raw, float2 (&v)[Elem<E>::kPack / 2]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (sizeof(E) == 4) {
+        v[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        v[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+                v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            } else {
+                __half2 h;
+                memcpy(&h, &w[i], 4);
+                v[i] = __half22float2(h);
+            }
+        }
+    }
+}
+template <typename E>
+__device__ __forceinline__ uint4 pack(const float2 (&v)[Elem<E>::kPack / 2]) {
+    uint32_t w[4];
+    if constexpr (sizeof(E) == 4) {
+        w[0] = __float_as_uint(v[0].x);
+        w[1] = __float_as_uint(v[0].y);
+        w[2] = __float_as_uint(v[1].x);
+        w[3] = __float_as_uint(v[1].y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+                const __nv_bfloat162 b = __float22bfloat162_rn(v[i]);
+                memcpy(&w[i], &b, 4);
+            } else {
+                const __half2 h = __float22half2_rn(v[i]);
+                memcpy(&w[i], &h, 4);
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Four elements: half a vector of a 16-bit type, a whole one of FP32.
+template <typename E>
+__device__ __forceinline__ void unpack_half(const uint2& raw, float2 (&v)[2]) {
+    const uint32_t w[2] = {raw.x, raw.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+            v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+            __half2 h;
+            memcpy(&h, &w[i], 4);
+            v[i] = __half22float2(h);
+        }
+    }
+}
+template <typename E>
+__device__ __forceinline__ void pack_half(const float2 (&v)[2], uint32_t* w) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (sizeof(E) == 4) {
+            w[2 * i] = __float_as_uint(v[i].x);
+            w[2 * i + 1] = __float_as_uint(v[i].y);
+        } else if constexpr (std::is_same<E, __nv_bfloat16>::value) {
+            const __nv_bfloat162 b = __float22bfloat162_rn(v[i]);
+            memcpy(&w[i], &b, 4);
+        } else {
+            const __half2 h = __float22half2_rn(v[i]);
+            memcpy(&w[i], &h, 4);
+        }
+    }
+}
+
 // [base, base + count) of one operand: what a checked build holds accesses to.
 template <typename E>
 struct Span {
@@ -81,6 +166,9 @@ struct Span {
     // whether N elements at index i lie inside (always true in a normal build)
     __device__ __forceinline__ bool has(size_t i, int n, uint32_t site) const {
         return check::in(p + i, (size_t)n * sizeof(E), p, count * sizeof(E), site);
+    }
+    __device__ __forceinline__ bool holds(const E* at, int n, uint32_t site) const {
+        return check::in(at, (size_t)n * sizeof(E), p, count * sizeof(E), site);
     }
 };
 template <int N, typename E, typename F>
@@ -164,6 +252,25 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
     return v;
+}
+// Two values at once: lanes below 16 end with the sum of a, the others with b's.
+__device__ __forceinline__ float warp_sum_two(float a, float b) {
+    const bool high = threadIdx.x & 16;
+    float v = (high ? b : a) + __shfl_xor_sync(kFullMask, high ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+// Four values: lanes 8 j .. 8 j + 7 end with the sum of v[j].  The first steps
+// halve what a lane carries, so 6 shuffles do instead of 20.
+__device__ __forceinline__ float warp_sum_four(const float (&v)[4]) {
+    const bool high = threadIdx.x & 16, mid = threadIdx.x & 8;
+    const float a = (high ? v[2] : v[0]) + __shfl_xor_sync(kFullMask, high ? v[0] : v[2], 16);
+    const float b = (high ? v[3] : v[1]) + __shfl_xor_sync(kFullMask, high ? v[1] : v[3], 16);
+    float s = (mid ? b : a) + __shfl_xor_sync(kFullMask, mid ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+    return s;
 }
 // Sums N values over the block in a fixed order; every thread gets them.
 // scratch: N * 32 floats of shared memory, free again after the call.

@@ -17,6 +17,7 @@
 // the same bits on every call and GPU.
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
+#include "mhcs_ring.cuh"
 
 namespace mhcpb {
 namespace ops {
@@ -26,7 +27,9 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 256;
-constexpr int kMaxParts = 304;   // row groups of the parameter gradients
+constexpr int kSms = 152;            // persistent grids: a constant, so that results do not depend on the GPU
+constexpr int kMaxParts = 2 * kSms;  // most row groups of the parameter gradients
+constexpr int kMaxShared = 227 * 1024;   // shared memory of a block
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int64_t part_count(int64_t T) { return T < kMaxParts ? T : kMaxParts; }
@@ -221,22 +224,341 @@ __global__ void __launch_bounds__(kThreads) backward_columns_any_kernel(Params<E
     store_at<1>(a.partial, (size_t)((part * 2 + 1) * a.D + c), b1, 9);
 }
 
-// Parameter gradients: the partials of a column in order.  blockIdx.y: 0 gamma, 1 beta.
-__global__ void __launch_bounds__(kThreads) reduce_parts_kernel(int64_t D, int64_t parts, bool accumulate,
-                                                                Span<float> partial, Span<float> gamma,
-                                                                Span<float> beta) {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const Span<float> out = blockIdx.y == 0 ? gamma : beta;
-    if (c >= D || out.p == nullptr) return;
-    float s = 0.f;
-    for (int64_t q = 0; q < parts; ++q) {
-        float v[1];
-        load_at<1>(partial, (size_t)((q * 2 + blockIdx.y) * D + c), v, 10);
-        s += v[0];
+// ------------------------------------------------------------ backward, rows in shared memory
+// A group of G threads takes a row at a time; thread i owns the same vectors
+// i, i + G, ... (VPT of 16 bytes) of every row, so the parameter gradients of
+// its columns stay in registers until the end.  The row's inputs come through
+// per-thread copies, S rows ahead.  The first half of a row forms its two sums,
+// sum w and sum w z; after the group's one barrier, the second half reads the
+// slots again (cheaper than holding u and w in registers), writes the
+// gradients and refills each slot as it leaves it.  The other groups of the
+// block compute while one waits.
+template <typename E, bool MIX, int VPT, int S>
+struct RowsShape {
+    static constexpr int N = Elem<E>::kPack;
+    static constexpr int kMaxThreads = 640;
+    static constexpr int kArrays = MIX ? 2 * kStreams + 1 : 2;      // x, grad_y, residual gradient
+    static constexpr int kStage = VPT * kArrays;                    // 16-byte slots of a row
+    // Slot k of every thread of the block lies together, so that a warp's copy
+    // writes whole 128-byte lines; the pitch is a constant, for immediate
+    // offsets.
+    static constexpr int kPitch = kMaxThreads;
+    static constexpr int kSlots = S * kStage;
+    static constexpr int kGammaSlots = VPT * N / 4;                 // per thread of a group, FP32
+    static constexpr int kWarpFloats = S * 32;                      // per row: 24 gates, mean, rstd
+    static constexpr int kSums = 2 + (MIX ? kStreams : 0);
+    static constexpr int kGroupFloats = 2 * kSums * 32;
+    static size_t bytes(int G, int R) {
+        return (size_t)kPitch * kSlots * 16 + (size_t)G * kGammaSlots * 16 +
+               (size_t)R * (G / 32 * kWarpFloats * 4 + kGroupFloats * 4);
     }
-    float o[1] = {0.f};
-    if (accumulate) load_at<1>(out, (size_t)c, o, 11);
-    o[0] += s;
+};
+
+template <typename E, bool MIX, int VPT, int S>
+__global__ void __launch_bounds__((RowsShape<E, MIX, VPT, S>::kMaxThreads), 1)
+    backward_rows_kernel(Params<E> a, int G, int R) {
+    using Shape = RowsShape<E, MIX, VPT, S>;
+    constexpr int N = Shape::N, H = N / 2, P = Shape::kPitch, A = Shape::kArrays;
+    constexpr int XA = MIX ? kStreams : 1;   // slots of a vector: x (XA), grad_y, residual gradient
+    extern __shared__ uint4 slots[];
+    const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
+    const int warp = i >> 5, warps = G >> 5;
+    uint4* const mine = slots + tid;
+    float4* const gammas = reinterpret_cast<float4*>(slots + P * Shape::kSlots);   // [kGammaSlots][G]
+    float* const floats = reinterpret_cast<float*>(gammas + Shape::kGammaSlots * G);
+    float* const scalars = floats + (tid >> 5) * Shape::kWarpFloats;
+    float* const sums = floats + (NT >> 5) * Shape::kWarpFloats + group * Shape::kGroupFloats;   // [2][kSums][32]
+    const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group, T = (int)a.T;
+    const bool residual = MIX && a.grad_x_out.p != nullptr;
+    const int c0 = i * N, step = G * N, D = (int)a.D;   // this thread's columns: c0 + v * step
+
+    // Columns past D: their slots stay 0, so they add nothing to the sums.
+#pragma unroll
+    for (int k = 0; k < Shape::kSlots; ++k) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+    if (group == 0)
+#pragma unroll
+        for (int k = 0; k < Shape::kGammaSlots; ++k) {
+            const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
+            float g[4] = {0.f, 0.f, 0.f, 0.f};
+            if (c < D) vector_at<4>(a.gamma, c, 1.f, g, 2);
+            gammas[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
+        }
+    __syncthreads();
+
+    // Element offset of row t of an array at this thread's first column, formed
+    // where it is needed: cheaper than a 64-bit pointer per array kept and moved.
+    const auto at_row = [&](int t, int64_t stride) {
+        return (size_t)((uint64_t)(uint32_t)t * (uint32_t)stride + (uint32_t)c0);
+    };
+    const auto fetch_vector = [&](uint4* dst, int t, int v) {
+        if (c0 + v * step < D) {
+            const size_t xo = at_row(t, a.x_stride) + v * step, go = at_row(t, a.gy_stride) + v * step;
+#pragma unroll
+            for (int s = 0; s < XA; ++s)
+                if (a.x.has(xo + s * D, N, 0)) copy16(dst + (v * A + s) * P, a.x.p + xo + s * D);
+            if (a.grad_y.has(go, N, 5)) copy16(dst + (v * A + XA) * P, a.grad_y.p + go);
+            if (MIX && residual)
+#pragma unroll
+                for (int s = 0; s < kStreams; ++s)
+                    if (a.grad_x_out.has(xo + s * D, N, 7))   // the streams' layout, as x
+                        copy16(dst + (v * A + XA + 1 + s) * P, a.grad_x_out.p + xo + s * D);
+        }
+    };
+    const auto fetch_scalars = [&](int t, int stage) {
+        float* const dst = scalars + stage * 32 + lane;
+        if (lane < kGates) {
+            if (MIX && a.h.has((size_t)t * kGates + lane, 1, 1)) copy4(dst, a.h.p + (size_t)t * kGates + lane);
+        } else if (lane == kGates) {
+            if (a.mean.has((size_t)t, 1, 4)) copy4(dst, a.mean.p + t);
+        } else if (lane == kGates + 1) {
+            if (a.rstd.has((size_t)t, 1, 4)) copy4(dst, a.rstd.p + t);
+        }
+    };
+    // the dot products <X_j, du> of row t, left in sums[parity] by its warps
+    const auto write_dots = [&](int t, int parity) {
+        if (warp == 0) {
+            const float* d = sums + (parity * Shape::kSums + 2 + (lane >> 3)) * 32;
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if ((lane & 7) + 8 * k < warps) v += d[(lane & 7) + 8 * k];
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+            const float o[1] = {v};
+            if ((lane & 7) == 0) store_at<1>(a.grad_h, (size_t)t * kGates + (lane >> 3), o, 8);
+        }
+    };
+
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+        if (first + q * groups < T) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) fetch_vector(mine + q * (Shape::kStage * P), first + q * groups, v);
+            fetch_scalars(first + q * groups, q);
+        }
+        copies_commit();
+    }
+
+    float2 gg[VPT][H], gb[VPT][H];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int k = 0; k < H; ++k) gg[v][k] = gb[v][k] = pair(0.f);
+    const float inv_d = 1.f / (float)D;
+    int stage = 0, parity = 0, before = -1;
+    for (int t = first; t < T; t += groups) {
+        copies_wait<S - 1>();
+        __syncwarp();
+        const float4* const gates = reinterpret_cast<const float4*>(scalars + stage * 32);
+        uint4* const row = mine + stage * (Shape::kStage * P);
+        const float2 stat = reinterpret_cast<const float2*>(gates)[kGates / 2];
+        // z = u rstd - mean rstd
+        const float2 rstd2 = pair(stat.y), shift2 = pair(-stat.x * stat.y);
+        const float4 pre = MIX ? gates[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float p4[kStreams] = {pre.x, pre.y, pre.z, pre.w};
+        float2 sw = pair(0.f), swz = pair(0.f);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            float2 z[H], w[H];
+            unpack<E>(row[v * A * P], z);
+            if constexpr (MIX) {
+#pragma unroll
+                for (int k = 0; k < H; ++k) z[k] = mul2(z[k], pair(p4[0]));
+#pragma unroll
+                for (int s = 1; s < XA; ++s) {
+                    float2 x[H];
+                    unpack<E>(row[(v * A + s) * P], x);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) z[k] = fma2(pair(p4[s]), x[k], z[k]);
+                }
+            }
+            unpack<E>(row[(v * A + XA) * P], w);
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                if ((k & 1) == 0) {
+                    const float4 g = gammas[(v * (N / 4) + k / 2) * G + i];
+                    z[k] = fma2(z[k], rstd2, shift2);
+                    z[k + 1] = fma2(z[k + 1], rstd2, shift2);
+                    gg[v][k] = fma2(w[k], z[k], gg[v][k]);
+                    gg[v][k + 1] = fma2(w[k + 1], z[k + 1], gg[v][k + 1]);
+                    gb[v][k] = add2(gb[v][k], w[k]);
+                    gb[v][k + 1] = add2(gb[v][k + 1], w[k + 1]);
+                    w[k] = mul2(w[k], make_float2(g.x, g.y));
+                    w[k + 1] = mul2(w[k + 1], make_float2(g.z, g.w));
+                    sw = add2(sw, add2(w[k], w[k + 1]));
+                    swz = fma2(w[k], z[k], fma2(w[k + 1], z[k + 1], swz));
+                }
+            }
+        }
+        float* const s0 = sums + parity * (Shape::kSums * 32);
+        const float both = warp_sum_two(sw.x + sw.y, swz.x + swz.y);
+        if ((lane & 15) == 0) s0[(lane >> 4) * 32 + warp] = both;
+        group_sync(group, G);
+        if constexpr (MIX)
+            if (before >= 0) write_dots(before, parity ^ 1);
+        float q = 0.f;   // lanes 0..7 add up the first sum, 8..15 the second
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if ((lane & 7) + 8 * k < warps) q += s0[(lane >> 3 & 1) * 32 + (lane & 7) + 8 * k];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(kFullMask, q, o);
+        const float mw = __shfl_sync(kFullMask, q, 0) * inv_d, mwz = __shfl_sync(kFullMask, q, 8) * inv_d;
+        // du = rstd (w - mw - z mwz)
+        const float2 a2 = pair(-stat.y * mw), b2 = pair(-stat.y * mwz);
+        float2 dot[kStreams];
+#pragma unroll
+        for (int j = 0; j < kStreams; ++j) dot[j] = pair(0.f);
+        const bool more = t + S * groups < T;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            uint32_t out[XA][4];   // packed results
+#pragma unroll
+            for (int half = 0; half < N / 4; ++half) {
+                // four columns of every array at a time, to bound the registers
+                const auto four = [&](int slot, float2 (&f)[2]) {
+                    if constexpr (sizeof(E) == 4) {
+                        const float4 raw = *reinterpret_cast<const float4*>(row + (v * A + slot) * P);
+                        f[0] = make_float2(raw.x, raw.y);
+                        f[1] = make_float2(raw.z, raw.w);
+                    } else {
+                        unpack_half<E>(reinterpret_cast<const uint2*>(row + (v * A + slot) * P)[half], f);
+                    }
+                };
+                const float4 g = gammas[(v * (N / 4) + half) * G + i];
+                float2 x[XA][2], z[2], w[2];
+#pragma unroll
+                for (int s = 0; s < XA; ++s) four(s, x[s]);
+                four(XA, w);
+                w[0] = mul2(w[0], make_float2(g.x, g.y));
+                w[1] = mul2(w[1], make_float2(g.z, g.w));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    z[k] = x[0][k];
+                    if constexpr (MIX) {
+                        z[k] = mul2(z[k], pair(p4[0]));
+#pragma unroll
+                        for (int s = 1; s < XA; ++s) z[k] = fma2(pair(p4[s]), x[s][k], z[k]);
+                    }
+                    z[k] = fma2(z[k], rstd2, shift2);
+                    w[k] = fma2(z[k], b2, fma2(w[k], rstd2, a2));
+                }
+                if constexpr (!MIX) {
+                    pack_half<E>(w, &out[0][half * 2]);
+                } else {
+                    float2 o[kStreams][2];
+#pragma unroll
+                    for (int j = 0; j < kStreams; ++j)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            dot[j] = fma2(x[j][k], w[k], dot[j]);
+                            o[j][k] = mul2(pair(p4[j]), w[k]);
+                        }
+                    if (residual)
+#pragma unroll
+                        for (int s = 0; s < kStreams; ++s) {
+                            const float4 r = gates[2 + s];   // H_res[s][0..3]
+                            const float r4[kStreams] = {r.x, r.y, r.z, r.w};
+                            float2 f[2];
+                            four(XA + 1 + s, f);
+#pragma unroll
+                            for (int j = 0; j < kStreams; ++j)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) o[j][k] = fma2(pair(r4[j]), f[k], o[j][k]);
+                        }
+#pragma unroll
+                    for (int j = 0; j < kStreams; ++j) pack_half<E>(o[j], &out[j][half * 2]);
+                }
+            }
+            if (c0 + v * step < D) {
+                const size_t o = at_row(t, a.gx_stride) + v * step;
+#pragma unroll
+                for (int j = 0; j < XA; ++j)
+                    if (a.grad_x.has(o + j * D, N, 6))
+                        *reinterpret_cast<uint4*>(a.grad_x.p + o + j * D) =
+                            make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]);
+            }
+            if (more) fetch_vector(row, t + S * groups, v);
+        }
+        if constexpr (MIX) {
+            float d4[4] = {dot[0].x + dot[0].y, dot[1].x + dot[1].y, dot[2].x + dot[2].y, dot[3].x + dot[3].y};
+            const float d = warp_sum_four(d4);
+            if ((lane & 7) == 0) s0[(2 + (lane >> 3)) * 32 + warp] = d;
+        }
+        __syncwarp();   // every lane has read the row's scalars
+        if (more) fetch_scalars(t + S * groups, stage);
+        copies_commit();
+        stage = stage + 1 == S ? 0 : stage + 1;
+        parity ^= 1;
+        before = t;
+    }
+    copies_wait<0>();
+    if constexpr (MIX) {
+        group_sync(group, G);
+        if (before >= 0) write_dots(before, parity ^ 1);
+    }
+    if (a.grad_gamma.p == nullptr && a.grad_beta.p == nullptr) return;
+    // the block's parameter gradients: its groups in order (the slots are free now)
+    float2* const acc = reinterpret_cast<float2*>(slots);   // [2][VPT][H][G]
+    for (int g = 0; g < R; ++g) {
+        __syncthreads();
+        if (g != group) continue;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                float2* const p = acc + (v * H + k) * G + i;
+                float2* const q = p + VPT * H * G;
+                if (g > 0) {
+                    gg[v][k] = add2(gg[v][k], *p);
+                    gb[v][k] = add2(gb[v][k], *q);
+                }
+                if (g + 1 < R) {
+                    *p = gg[v][k];
+                    *q = gb[v][k];
+                }
+            }
+    }
+    if (group + 1 < R) return;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = c0 + v * step;
+        if (c < D) {
+            float o[N];
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    const float2 q = part == 0 ? gg[v][k] : gb[v][k];
+                    o[2 * k] = q.x;
+                    o[2 * k + 1] = q.y;
+                }
+                store_at<N>(a.partial, ((size_t)blockIdx.x * 2 + part) * D + c, o, 9);
+            }
+        }
+    }
+}
+
+// Parameter gradients: the partials of a column in a fixed order (16 threads
+// each add every 16th part, then their sums are added in order).
+// blockIdx.y: 0 gamma, 1 beta.
+__global__ void __launch_bounds__(512) reduce_parts_kernel(int64_t D, int64_t parts, bool accumulate,
+                                                           Span<float> partial, Span<float> gamma, Span<float> beta) {
+    __shared__ float s[16][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    const Span<float> out = blockIdx.y == 0 ? gamma : beta;
+    if (out.p == nullptr) return;
+    float sum = 0.f;
+    if (c < D)
+#pragma unroll 8
+        for (int64_t q = threadIdx.y; q < parts; q += 16) sum += scalar_at(partial, (q * 2 + blockIdx.y) * D + c, 10);
+    s[threadIdx.y][threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.y != 0 || c >= D) return;
+    float o[1] = {accumulate ? scalar_at(out, c, 11) : 0.f};
+    sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) sum += s[q][threadIdx.x];
+    o[0] += sum;
     store_at<1>(out, (size_t)c, o, 11);
 }
 
@@ -288,24 +610,64 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// Launches backward_rows_kernel where the row fits its shape; false otherwise.
+// *parts: the row groups it writes partial parameter gradients for.
+template <typename E, bool MIX, int VPT, int S>
+bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStream_t stream) {
+    using Shape = RowsShape<E, MIX, VPT, S>;
+    const int64_t vectors = p.D / Shape::N, threads = (vectors + VPT - 1) / VPT;
+    if (threads > Shape::kMaxThreads) return false;
+    const int G = (int)((threads + 31) / 32 * 32);
+    const int64_t blocks = kSms;
+    int R = Shape::kMaxThreads / G;
+    if (R > 15) R = 15;                                        // named barriers of a block
+    const int64_t spread = (p.T + blocks - 1) / blocks;        // no more groups than rows to spread over the blocks
+    if (R > spread) R = (int)spread;
+    while (R > 1 && Shape::bytes(G, R) > kMaxShared) --R;
+    const size_t shared = Shape::bytes(G, R);
+    if (shared > kMaxShared) return false;
+    const int64_t grid = (p.T + R - 1) / R < blocks ? (p.T + R - 1) / R : blocks;
+    *parts = grid;
+    auto kernel = backward_rows_kernel<E, MIX, VPT, S>;
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    if (*e != cudaSuccess) return true;
+    kernel<<<(unsigned)grid, (unsigned)(G * R), shared, stream>>>(p, G, R);
+    *e = cudaGetLastError();
+    return true;
+}
+
 template <typename E, bool MIX>
 cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
-    const Params<E> p = params_of<E, MIX>(a);
-    constexpr int N = 8;
+    Params<E> p = params_of<E, MIX>(a);
+    constexpr int N = Elem<E>::kPack;
     const bool packed = a.D % N == 0 && rows_packed(a.x, a.x_stride, N) && rows_packed(a.grad_y, a.gy_stride, N) &&
                         rows_packed(a.grad_x, a.gx_stride, N) && aligned16(a.gamma) && aligned16(a.grad_x_out);
-    const unsigned column_blocks = (unsigned)((a.D + kThreads - 1) / kThreads);
+    const bool params = a.grad_gamma != nullptr || a.grad_beta != nullptr;
+    cudaError_t e = cudaSuccess;
     if (a.T > 0) {
-        if (packed)
-            backward_rows_any_kernel<E, MIX, N><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
-        else
-            backward_rows_any_kernel<E, MIX, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
-        if (a.grad_gamma != nullptr || a.grad_beta != nullptr)
-            backward_columns_any_kernel<E, MIX><<<dim3(column_blocks, (unsigned)p.parts), kThreads, 0, stream>>>(p);
+        bool done = false;
+        if (packed) {
+            if constexpr (MIX)
+                done = backward_rows<E, true, 1, 2>(p, &p.parts, &e, stream) || backward_rows<E, true, 2, 1>(p, &p.parts, &e, stream);
+            else
+                done = backward_rows<E, false, 16 / N, 3>(p, &p.parts, &e, stream);
+        }
+        if (!done) {
+            constexpr int W = 8;
+            if (packed && a.D % W == 0)
+                backward_rows_any_kernel<E, MIX, W><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
+            else
+                backward_rows_any_kernel<E, MIX, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
+            if (params)
+                backward_columns_any_kernel<E, MIX>
+                    <<<dim3((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)p.parts), kThreads, 0, stream>>>(p);
+            e = cudaGetLastError();
+        }
+        if (e != cudaSuccess) return e;
     }
-    if (a.grad_gamma != nullptr || a.grad_beta != nullptr)
-        reduce_parts_kernel<<<dim3(column_blocks, 2), kThreads, 0, stream>>>(a.D, p.parts, a.accumulate, p.partial,
-                                                                            p.grad_gamma, p.grad_beta);
+    if (params)
+        reduce_parts_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), dim3(32, 16), 0, stream>>>(
+            a.D, p.parts, a.accumulate, p.partial, p.grad_gamma, p.grad_beta);
     return cudaGetLastError();
 }
 
