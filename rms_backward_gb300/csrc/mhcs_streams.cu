@@ -10,6 +10,7 @@
 // three are bound by HBM: 4, 18 and 20 bytes per BF16 element of y.
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
+#include "mhcs_ring.cuh"
 
 namespace mhcpb {
 namespace ops {
@@ -19,25 +20,64 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 256;
+constexpr int kSms = 152;
+constexpr int64_t kShortCounters = (int64_t)1 << 34;   // elements below which ShortPhilox serves
+constexpr int kMaxShared = 227 * 1024;   // shared memory of a block
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename E, int N>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
+// Any alignment and size: an element per thread and step.
+template <typename E>
+__global__ void __launch_bounds__(kThreads) dropout_any_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
     const DropKey key = drop_key(d);
-    const int64_t step = (int64_t)gridDim.x * kThreads * N;
-    for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * N; e < n; e += step) {
+    const int64_t step = (int64_t)gridDim.x * kThreads;
+    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n; e += step) {
+        float v[1];
+        load_at<1>(x, e, v, 0);
+        drop<1>(d, key, e, v);
+        store_at<1>(y, e, v, 1);
+    }
+}
+
+// kDropPacks vectors of 16 bytes per thread, a block's width apart; needs
+// n < kShortCounters and aligned pointers.  The last, partial vector is one thread's.
+constexpr int kDropPacks = 2;
+template <typename E>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
+    constexpr int N = Elem<E>::kPack;
+    const DropKey key = drop_key(d);
+    const int64_t first = ((int64_t)blockIdx.x * kDropPacks * kThreads + threadIdx.x) * N;
+    uint4 raw[kDropPacks];
+#pragma unroll
+    for (int v = 0; v < kDropPacks; ++v) {
+        const int64_t e = first + (int64_t)v * kThreads * N;
+        if (e + N <= n && x.has(e, N, 0)) raw[v] = *reinterpret_cast<const uint4*>(x.p + e);
+    }
+    const ShortPhilox random(key);
+    const float2 scale = pair(d.scale);
+#pragma unroll
+    for (int v = 0; v < kDropPacks; ++v) {
+        const int64_t e = first + (int64_t)v * kThreads * N;
         if (e + N <= n) {
-            float v[N];
-            load_at<N>(x, e, v, 0);
-            drop<N>(d, key, e, v);
-            store_at<N>(y, e, v, 1);
+            float2 f[N / 2];
+            unpack<E>(raw[v], f);
+            if (d.rng != nullptr) {
+                uint32_t w[N / 4][4];
+                random.words<N / 4>((uint32_t)(e >> 2), w);
+#pragma unroll
+                for (int k = 0; k < N / 2; ++k) {
+                    f[k] = mul2(f[k], scale);
+                    f[k].x = w[k / 2][k % 2 * 2] >= d.threshold ? f[k].x : 0.f;
+                    f[k].y = w[k / 2][k % 2 * 2 + 1] >= d.threshold ? f[k].y : 0.f;
+                }
+            }
+            if (y.has(e, N, 1)) *reinterpret_cast<uint4*>(y.p + e) = pack<E>(f);
         } else {
             for (int64_t i = e; i < n; ++i) {
-                float v[1];
-                load_at<1>(x, i, v, 0);
-                drop<1>(d, key, i, v);
-                store_at<1>(y, i, v, 1);
+                float one[1];
+                load_at<1>(x, i, one, 0);
+                drop<1>(d, key, i, one);
+                store_at<1>(y, i, one, 1);
             }
         }
     }
@@ -131,17 +171,267 @@ __global__ void __launch_bounds__(kThreads) update_backward_kernel(int64_t D, Sp
     }
 }
 
+// ------------------------------------------------------------ update, 16-byte vectors
+// The gates of token t: 4 of H_post and 16 of H_res.
+__device__ __forceinline__ void gates_at(const Span<const float>& h, int64_t t, bool aligned, float (&g)[20]) {
+    if (aligned) {
+#pragma unroll
+        for (int q = 0; q < 5; ++q) {
+            const size_t at = (size_t)t * kGates + 4 + 4 * q;
+            const float4 v = h.has(at, 4, 2) ? *reinterpret_cast<const float4*>(h.p + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            g[4 * q] = v.x;
+            g[4 * q + 1] = v.y;
+            g[4 * q + 2] = v.z;
+            g[4 * q + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 20; ++q) {
+            const size_t at = (size_t)t * kGates + 4 + q;
+            g[q] = h.has(at, 1, 2) ? h.p[at] : 0.f;
+        }
+    }
+}
+// f <- dropout of the eight elements from e on; *keep: which are kept
+__device__ __forceinline__ void drop_eight(const Drop& d, const ShortPhilox& random, uint64_t e, float2 (&f)[4],
+                                           uint32_t* keep) {
+    *keep = 0xffu;
+    if (d.rng == nullptr) return;
+    uint32_t w[2][4];
+    random.words<2>((uint32_t)(e >> 2), w);
+    *keep = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) *keep |= (w[k / 4][k % 4] >= d.threshold ? 1u : 0u) << k;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[k] = mul2(f[k], pair(d.scale));
+        f[k].x = *keep >> (2 * k) & 1u ? f[k].x : 0.f;
+        f[k].y = *keep >> (2 * k + 1) & 1u ? f[k].y : 0.f;
+    }
+}
+
+// One vector of every stream per thread, everything loaded before anything is
+// used.  A block holds `tokens` whole tokens of `vectors` vectors, or, when a
+// token has more vectors than the block has threads, one of its `tiles` tiles.
+__global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
+    int64_t T, int64_t D, int tokens, int tiles, bool gates_aligned, Span<const bf16> x, Span<const bf16> y,
+    Span<const float> h, Drop d, Span<bf16> x_out) {
+    constexpr int N = 8, H = 4;
+    const int vectors = (int)(D / N);
+    int64_t t;
+    int c;
+    if (tiles == 1) {
+        t = (int64_t)blockIdx.x * tokens + threadIdx.x / vectors;
+        c = (int)(threadIdx.x % vectors) * N;
+        if (threadIdx.x >= tokens * vectors || t >= T) return;
+    } else {
+        t = blockIdx.x / tiles;
+        c = ((int)(blockIdx.x % tiles) * (int)blockDim.x + (int)threadIdx.x) * N;
+        if (c >= D) return;
+    }
+    const size_t row = (size_t)t * (kStreams * D) + c, flat = (size_t)t * D + c;
+    uint4 xs[kStreams], yr = make_uint4(0u, 0u, 0u, 0u);
+    if (y.has(flat, N, 3)) yr = *reinterpret_cast<const uint4*>(y.p + flat);
+#pragma unroll
+    for (int j = 0; j < kStreams; ++j)
+        xs[j] = x.has(row + j * D, N, 4) ? *reinterpret_cast<const uint4*>(x.p + row + j * D) : make_uint4(0u, 0u, 0u, 0u);
+    float g[20];
+    gates_at(h, t, gates_aligned, g);
+    const DropKey key = drop_key(d);
+    float2 yv[H], o[kStreams][H];
+    uint32_t keep;
+    unpack<bf16>(yr, yv);
+    drop_eight(d, ShortPhilox(key), flat, yv, &keep);
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i)
+#pragma unroll
+        for (int k = 0; k < H; ++k) o[i][k] = mul2(pair(g[i]), yv[k]);
+#pragma unroll
+    for (int j = 0; j < kStreams; ++j) {
+        float2 v[H];
+        unpack<bf16>(xs[j], v);
+#pragma unroll
+        for (int i = 0; i < kStreams; ++i)
+#pragma unroll
+            for (int k = 0; k < H; ++k) o[i][k] = fma2(pair(g[4 + 4 * i + j]), v[k], o[i][k]);
+    }
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i)
+        if (x_out.has(row + i * D, N, 5)) *reinterpret_cast<uint4*>(x_out.p + row + i * D) = pack<bf16>(o[i]);
+}
+
+// A group of G threads takes a token at a time (thread i owns vectors i, i + G,
+// ... of it, VPT of them), its inputs copied S tokens ahead into per-thread
+// slots.  The token's 20 dot products are left in shared memory by each warp
+// and added up after the group's barrier, which the outputs do not wait for.
+template <int VPT, int S>
+struct TokenShape {
+    static constexpr int kMaxThreads = 640;
+    static constexpr int kArrays = 2 * kStreams + 1;   // x, grad_x_out, y
+    static constexpr int kStage = VPT * kArrays;
+    static constexpr int kPitch = kMaxThreads;
+    static constexpr int kDots = 20;
+    static constexpr int kDotPitch = 33;               // one warp reads a column: 20 different banks
+    static size_t bytes(int G, int R) {
+        return (size_t)kPitch * S * kStage * 16 + (size_t)R * (G / 32 * S * 4 + 2 * kDots * kDotPitch) * 4;
+    }
+};
+template <int VPT, int S>
+__global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
+    update_backward_tokens_kernel(int T, int D, int G, int R, Span<const bf16> x, Span<const bf16> y,
+                                  Span<const float> h, Drop d, Span<const bf16> gout, Span<bf16> gy, Span<float> gh) {
+    using Shape = TokenShape<VPT, S>;
+    constexpr int N = 8, P = Shape::kPitch, A = Shape::kArrays;
+    extern __shared__ uint4 slots[];
+    const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
+    const int warp = i >> 5, warps = G >> 5;
+    uint4* const mine = slots + tid;
+    float* const floats = reinterpret_cast<float*>(slots + P * S * Shape::kStage);
+    float* const posts = floats + (tid >> 5) * (S * 4);                                   // [S][4] per warp
+    float* const dots = floats + (NT >> 5) * (S * 4) + group * (2 * Shape::kDots * Shape::kDotPitch);
+    const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group;
+    const int c0 = i * N, step = G * N;
+#pragma unroll
+    for (int k = 0; k < S * Shape::kStage; ++k) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);   // columns past D
+    const DropKey key = drop_key(d);
+    const ShortPhilox random(key);
+
+    const auto fetch_vector = [&](uint4* dst, int t, int v) {
+        const int c = c0 + v * step;
+        if (c < D) {
+            const size_t flat = (size_t)((uint64_t)(uint32_t)t * (uint32_t)D + (uint32_t)c);
+            const size_t row = (size_t)((uint64_t)(uint32_t)t * (uint32_t)(kStreams * D) + (uint32_t)c);
+#pragma unroll
+            for (int s = 0; s < kStreams; ++s) {
+                if (x.has(row + s * D, N, 4)) copy16(dst + (v * A + s) * P, x.p + row + s * D);
+                if (gout.has(row + s * D, N, 6)) copy16(dst + (v * A + kStreams + s) * P, gout.p + row + s * D);
+            }
+            if (y.has(flat, N, 3)) copy16(dst + (v * A + 2 * kStreams) * P, y.p + flat);
+        }
+    };
+    const auto fetch_post = [&](int t, int stage) {
+        if (lane < kStreams && h.has((size_t)t * kGates + 4 + lane, 1, 2))
+            copy4(posts + stage * 4 + lane, h.p + (size_t)t * kGates + 4 + lane);
+    };
+    const auto write_dots = [&](int t, int parity) {
+        if (warp == 0 && lane < Shape::kDots) {
+            const float* const p = dots + (parity * Shape::kDots + lane) * Shape::kDotPitch;
+            float v[1] = {0.f};
+            for (int w = 0; w < warps; ++w) v[0] += p[w];
+            store_at<1>(gh, (size_t)t * kGates + 4 + lane, v, 8);
+        }
+    };
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+        if (first + q * groups < T) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) fetch_vector(mine + q * (Shape::kStage * P), first + q * groups, v);
+            fetch_post(first + q * groups, q);
+        }
+        copies_commit();
+    }
+    int stage = 0, parity = 0;
+    for (int t = first; t < T; t += groups) {
+        copies_wait<S - 1>();
+        __syncwarp();
+        uint4* const row = mine + stage * (Shape::kStage * P);
+        const float4 post = *reinterpret_cast<const float4*>(posts + stage * 4);
+        const float p4[kStreams] = {post.x, post.y, post.z, post.w};
+        const bool more = t + S * groups < T;
+        float d16[16], d4[4];   // not pairs: 20 registers less
+#pragma unroll
+        for (int k = 0; k < 16; ++k) d16[k] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d4[k] = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = c0 + v * step;
+            const size_t flat = (size_t)((uint64_t)(uint32_t)t * (uint32_t)D + (uint32_t)c);
+            float2 yv[4];
+            uint32_t keep, out[4];
+            unpack<bf16>(row[(v * A + 2 * kStreams) * P], yv);
+            drop_eight(d, random, flat, yv, &keep);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float2 xs[kStreams][2], o[2] = {pair(0.f), pair(0.f)};
+#pragma unroll
+                for (int j = 0; j < kStreams; ++j)
+                    unpack_half<bf16>(reinterpret_cast<const uint2*>(row + (v * A + j) * P)[half], xs[j]);
+#pragma unroll
+                for (int s = 0; s < kStreams; ++s) {
+                    float2 g[2];
+                    unpack_half<bf16>(reinterpret_cast<const uint2*>(row + (v * A + kStreams + s) * P)[half], g);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        o[k] = fma2(pair(p4[s]), g[k], o[k]);
+                        d4[s] = fmaf(g[k].x, yv[half * 2 + k].x, fmaf(g[k].y, yv[half * 2 + k].y, d4[s]));
+#pragma unroll
+                        for (int j = 0; j < kStreams; ++j)
+                            d16[4 * s + j] = fmaf(g[k].x, xs[j][k].x, fmaf(g[k].y, xs[j][k].y, d16[4 * s + j]));
+                    }
+                }
+                if (d.rng != nullptr)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        o[k] = mul2(o[k], pair(d.scale));
+                        o[k].x = keep >> (half * 4 + 2 * k) & 1u ? o[k].x : 0.f;
+                        o[k].y = keep >> (half * 4 + 2 * k + 1) & 1u ? o[k].y : 0.f;
+                    }
+                pack_half<bf16>(o, out + half * 2);
+            }
+            if (c < D && gy.has(flat, N, 7)) *reinterpret_cast<uint4*>(gy.p + flat) = make_uint4(out[0], out[1], out[2], out[3]);
+            if (more) fetch_vector(row, t + S * groups, v);
+        }
+        const float res = warp_sum_sixteen(d16), pos = warp_sum_four(d4);
+        float* const mine_dots = dots + parity * (Shape::kDots * Shape::kDotPitch) + warp;
+        if ((lane & 1) == 0) mine_dots[(4 + (lane >> 1)) * Shape::kDotPitch] = res;
+        if ((lane & 7) == 0) mine_dots[(lane >> 3) * Shape::kDotPitch] = pos;
+        __syncwarp();   // every lane has read the token's gates
+        if (more) fetch_post(t + S * groups, stage);
+        copies_commit();
+        // The other parity's sums are read after the barrier two tokens later at
+        // the earliest, so one barrier per token orders both buffers.
+        group_sync(group, G);
+        write_dots(t, parity);
+        stage = stage + 1 == S ? 0 : stage + 1;
+        parity ^= 1;
+    }
+    copies_wait<0>();
+}
+
+// Launches update_backward_tokens_kernel where a token fits its shape.
+template <int VPT, int S>
+bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, const Span<const bf16>& y,
+                            const Span<const float>& h, const Drop& d, const Span<const bf16>& gout,
+                            const Span<bf16>& gy, const Span<float>& gh, cudaError_t* e, cudaStream_t stream) {
+    using Shape = TokenShape<VPT, S>;
+    const int64_t threads = (D / 8 + VPT - 1) / VPT;
+    if (threads > Shape::kMaxThreads) return false;
+    const int G = (int)((threads + 31) / 32 * 32);
+    int R = Shape::kMaxThreads / G;
+    if (R > 15) R = 15;                                // named barriers of a block
+    const int64_t spread = (T + kSms - 1) / kSms;      // no more groups than tokens to spread over the blocks
+    if (R > spread) R = (int)spread;
+    const int64_t grid = (T + R - 1) / R < kSms ? (T + R - 1) / R : kSms;
+    auto kernel = update_backward_tokens_kernel<VPT, S>;
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    if (*e != cudaSuccess) return true;
+    kernel<<<(unsigned)grid, (unsigned)(G * R), Shape::bytes(G, R), stream>>>((int)T, (int)D, G, R, x, y, h, d, gout, gy,
+                                                                              gh);
+    *e = cudaGetLastError();
+    return true;
+}
+
 template <typename E>
 cudaError_t dropout_typed(int64_t n, const void* x, void* y, const Drop& d, cudaStream_t stream) {
-    constexpr int N = 8;
     const Span<const E> xs{static_cast<const E*>(x), (size_t)n};
     const Span<E> ys{static_cast<E*>(y), (size_t)n};
-    if (aligned16(x) && aligned16(y)) {
-        const int64_t blocks = (n + kThreads * N - 1) / (kThreads * N);
-        dropout_kernel<E, N><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), kThreads, 0, stream>>>(n, xs, ys, d);
+    if (aligned16(x) && aligned16(y) && n < kShortCounters) {
+        const int64_t block = (int64_t)kThreads * Elem<E>::kPack * kDropPacks;
+        dropout_kernel<E><<<(unsigned)((n + block - 1) / block), kThreads, 0, stream>>>(n, xs, ys, d);
     } else {
         const int64_t blocks = (n + kThreads - 1) / kThreads;
-        dropout_kernel<E, 1><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), kThreads, 0, stream>>>(n, xs, ys, d);
+        dropout_any_kernel<E><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), kThreads, 0, stream>>>(n, xs, ys, d);
     }
     return cudaGetLastError();
 }
@@ -162,6 +452,31 @@ cudaError_t update_forward(int64_t T, int64_t D, const void* x, const void* y, c
     const Span<const bf16> ys{static_cast<const bf16*>(y), (size_t)(T * D)};
     const Span<const float> hs{h, (size_t)(T * kGates)};
     const Span<bf16> os{static_cast<bf16*>(x_out), (size_t)(T * kStreams * D)};
+    if (D % 8 == 0 && T * D < kShortCounters) {
+        const bool gates_aligned = aligned16(h);
+        const int64_t vectors = D / 8;
+        // whole tokens per block where several fit, else the tile width that leaves the fewest threads idle
+        int threads = kThreads, tokens = 1, tiles = 1;
+        if (vectors <= kThreads / 2) {
+            tokens = kThreads / (int)vectors;
+        } else {
+            int64_t least = INT64_MAX;
+            for (int w = 128; w <= kThreads; w += 32) {
+                const int64_t used = (vectors + w - 1) / w * w;
+                if (used <= least) {
+                    least = used;
+                    threads = w;
+                }
+            }
+            tiles = (int)((vectors + threads - 1) / threads);
+        }
+        const int64_t blocks = tiles > 1 ? T * tiles : (T + tokens - 1) / tokens;
+        if (blocks <= INT32_MAX) {
+            update_forward_vectors_kernel<<<(unsigned)blocks, threads, 0, stream>>>(T, D, tokens, tiles, gates_aligned,
+                                                                                    xs, ys, hs, d, os);
+            return cudaGetLastError();
+        }
+    }
     if (D % 8 == 0)
         update_forward_kernel<8><<<(unsigned)T, kThreads, 0, stream>>>(D, xs, ys, hs, d, os);
     else
@@ -179,6 +494,12 @@ cudaError_t update_backward(int64_t T, int64_t D, const void* x, const void* y, 
     const Span<const bf16> gs{static_cast<const bf16*>(grad_x_out), (size_t)(T * kStreams * D)};
     const Span<bf16> gys{static_cast<bf16*>(grad_y), (size_t)(T * D)};
     const Span<float> ghs{grad_h, (size_t)(T * kGates)};
+    if (D % 8 == 0 && T * D < kShortCounters) {
+        cudaError_t e = cudaSuccess;
+        if (update_backward_tokens<1, 2>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
+            update_backward_tokens<2, 1>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream))
+            return e;
+    }
     if (D % 8 == 0)
         update_backward_kernel<8><<<(unsigned)T, kThreads, 0, stream>>>(D, xs, ys, hs, d, gs, gys, ghs);
     else
