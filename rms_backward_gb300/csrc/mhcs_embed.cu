@@ -6,17 +6,27 @@
 //
 // The backward orders the tokens by (id, t) and sums each run of equal ids in
 // that order, without atomics, so the same inputs give the same bits on every
-// call.  Sorting: tiles of 4096 tokens in shared memory, then, above 4096
-// tokens, passes that merge 16 sorted runs at a time (an element's place is
-// its place in its own run plus, for each other run, the number of smaller
-// elements there; (id, t) pairs are all different, so places are too).
+// call.
+//
+// Ordering: a token's place in its tile is the number of smaller (id, t) pairs
+// there, counted by comparing it with the whole tile in shared memory; the
+// comparisons of one tile are spread over many blocks.  For 4096 tokens that is
+// 17 M comparisons, a few microseconds on the whole GPU (a bitonic network in
+// one block took 37).  Above 4096 tokens the tiles have 1024, and passes merge
+// 16 sorted runs at a time: an element's place is its place in its own run
+// plus, for each other run, the number of smaller elements, found by one lane
+// per run.
 // Summing: the ordered tokens are cut into chunks; a block sums one chunk over
 // one slab of columns.  A run inside one chunk is written at once; the pieces
 // of a run that crosses chunks go to the workspace and a last kernel adds them
 // in order, so that one frequent token does not leave one block with most of
 // the work.  Rows without tokens are zeroed by blocks of the summing kernel.
+// Bound by HBM: grad_x is read once and the table's gradient written once.
+#include "mhcpb.h"
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
+#include "mhcs_ring.cuh"
+#include "ptx.cuh"
 
 namespace mhcpb {
 namespace ops {
@@ -26,11 +36,13 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 128;
-constexpr int kSortTile = 4096;      // tokens per sorted tile: 32 KiB of shared memory
-constexpr int kSortThreads = 1024;
+constexpr int kOneTile = 4096;       // tokens ordered in one tile
+constexpr int kTile = 1024;          // tokens per tile when there are more
+constexpr int kRanked = 32;          // tokens a ranking block places, 8 threads each
 constexpr int kFan = 16;             // runs per merge pass
-constexpr int kBatch = 32;           // ordered tokens read ahead at a time
-constexpr int kZeroRows = 32;        // table rows per zeroing block
+constexpr int kBatch = 32;           // ordered tokens per listing of rows
+constexpr int kAhead = 8;            // rows copied ahead of the one being added
+constexpr int kZeroRows = 16;        // table rows per zeroing block, 4 a warp
 constexpr int kMaxChunks = 1024;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -75,31 +87,44 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(int64_t V, int64_t D, 
 // ------------------------------------------------------------ ordering
 // (id, t) as one 64-bit number; ids outside the table come last, as id V
 template <typename I>
-__global__ void __launch_bounds__(kSortThreads) sort_tiles_kernel(int64_t T, int64_t V, Span<const I> ids,
-                                                                  Span<uint64_t> order) {
-    __shared__ uint64_t s[kSortTile];
-    const int64_t base = (int64_t)blockIdx.x * kSortTile;
-    const int n = (int)(T - base < kSortTile ? T - base : kSortTile);
-    int padded = 2;
-    while (padded < n) padded *= 2;
-    for (int i = threadIdx.x; i < padded; i += kSortThreads)
-        s[i] = i < n ? ((uint64_t)id_at(ids, base + i, V, 3) << 32) | (uint64_t)(base + i) : ~0ull;
-    __syncthreads();
-    // bitonic network: the elements are all different, so no stability is needed
-    for (int k = 2; k <= padded; k *= 2)
-        for (int j = k / 2; j > 0; j /= 2) {
-            for (int p = threadIdx.x; p < padded / 2; p += kSortThreads) {
-                const int a = 2 * p - (p & (j - 1)), b = a + j;
-                const uint64_t va = s[a], vb = s[b];
-                if ((va > vb) == ((a & k) == 0)) {
-                    s[a] = vb;
-                    s[b] = va;
-                }
-            }
-            __syncthreads();
+__global__ void __launch_bounds__(256) rank_kernel(int64_t T, int64_t V, int tile, Span<const I> ids,
+                                                   Span<uint64_t> order) {
+    __shared__ uint4 quads[kOneTile / 4];
+    uint32_t* const keys = reinterpret_cast<uint32_t*>(quads);
+    ptx::grid_launch_dependents();
+    const int blocks_per_tile = tile / kRanked;
+    const int64_t base = (int64_t)(blockIdx.x / blocks_per_tile) * tile;
+    const int n = (int)(T - base < tile ? T - base : tile), padded = (n + 31) / 32 * 32;
+    constexpr int kPer = 16 / sizeof(I);   // ids per 16-byte read
+    const int packed = (reinterpret_cast<uintptr_t>(ids.p) & 15u) == 0 ? n / kPer * kPer : 0;
+#pragma unroll 8
+    for (int k = threadIdx.x * kPer; k < packed; k += 256 * kPer)
+        if (ids.has((size_t)(base + k), kPer, 3)) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(ids.p + base + k);
+            const I* const v = reinterpret_cast<const I*>(&raw);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) keys[k + q] = v[q] < 0 || v[q] >= V ? (uint32_t)V : (uint32_t)v[q];
         }
-    for (int i = threadIdx.x; i < n; i += kSortThreads)
-        if (order.has((size_t)(base + i), 1, 4)) order.p[base + i] = s[i];
+    for (int k = packed + threadIdx.x; k < padded; k += 256)
+        keys[k] = k < n ? (uint32_t)id_at(ids, base + k, V, 3) : 0xffffffffu;
+    __syncthreads();
+    const int i = (int)(blockIdx.x % blocks_per_tile) * kRanked + (threadIdx.x >> 3), part = threadIdx.x & 7;
+    const uint32_t key = i < n ? keys[i] : 0u;
+    int before = 0;
+#pragma unroll 4
+    for (int q = part; q < padded / 4; q += 8) {
+        const uint4 v = quads[q];
+        // an equal id counts when its token comes first
+        const uint32_t bound = q < i / 4 ? key + 1 : key;
+        before += (v.x < bound) + (v.y < bound) + (v.z < bound) + (v.w < bound);
+    }
+    if ((i / 4 & 7) == part && i < n)
+        for (int k = i / 4 * 4; k < i; ++k) before += keys[k] == key;   // the token's own four
+    before += __shfl_xor_sync(kFullMask, before, 1);
+    before += __shfl_xor_sync(kFullMask, before, 2);
+    before += __shfl_xor_sync(kFullMask, before, 4);
+    if (part == 0 && i < n && order.has((size_t)(base + before), 1, 4))
+        order.p[base + before] = (uint64_t)key << 32 | (uint64_t)(base + i);
 }
 
 __device__ __forceinline__ uint64_t order_at(const Span<const uint64_t>& o, int64_t i, uint32_t site) {
@@ -109,34 +134,38 @@ __device__ __forceinline__ int64_t key_at(const Span<const uint64_t>& o, int64_t
     return (int64_t)(order_at(o, i, site) >> 32);
 }
 
+// 16 lanes per element, one for each run of its group.
 __global__ void __launch_bounds__(256) merge_runs_kernel(int64_t T, int64_t run, Span<const uint64_t> in,
                                                          Span<uint64_t> out) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= T) return;
-    const uint64_t v = order_at(in, i, 5);
-    const int64_t group = i / (run * kFan) * (run * kFan);
-    int64_t place = group;
-    for (int r = 0; r < kFan; ++r) {
-        const int64_t lo = group + r * run;
-        if (lo >= T) break;
-        const int64_t hi = lo + run < T ? lo + run : T;
+    const int64_t i = (int64_t)blockIdx.x * (256 / kFan) + threadIdx.x / kFan;
+    const int r = threadIdx.x % kFan;
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const bool valid = i < T;
+    const uint64_t v = valid ? order_at(in, i, 5) : 0;
+    const int64_t group = i / (run * kFan) * (run * kFan), lo = group + r * run;
+    const int64_t hi = lo + run < T ? lo + run : T;
+    int64_t below = 0;
+    if (valid && lo < T) {
         if (i >= lo && i < hi) {
-            place += i - lo;
-            continue;
-        }
-        int64_t a = lo, n = hi - lo;   // the number of elements below v
-        while (n > 0) {
-            const int64_t half = n / 2;
-            if (order_at(in, a + half, 5) < v) {
-                a += half + 1;
-                n -= half + 1;
-            } else {
-                n = half;
+            below = i - lo;
+        } else {
+            int64_t a = lo, n = hi - lo;
+            while (n > 0) {
+                const int64_t half = n / 2;
+                if (order_at(in, a + half, 5) < v) {
+                    a += half + 1;
+                    n -= half + 1;
+                } else {
+                    n = half;
+                }
             }
+            below = a - lo;
         }
-        place += a - lo;
     }
-    if (out.has((size_t)place, 1, 6)) out.p[place] = v;
+#pragma unroll
+    for (int o = kFan / 2; o > 0; o >>= 1) below += __shfl_xor_sync(kFullMask, below, o);
+    if (valid && r == 0 && out.has((size_t)(group + below), 1, 6)) out.p[group + below] = v;
 }
 
 // ------------------------------------------------------------ summing
@@ -168,114 +197,248 @@ struct SumArgs {
     Span<float> pieces;   // [chunks][2][D]: of the run that began before the chunk, and of the one that goes on after it
 };
 
+// FP32 row pieces: 32-byte accesses where the address allows them (two of 16
+// bytes, 32 apart, touch every sector twice).
 template <int N>
-__device__ __forceinline__ void write_row(const SumArgs& a, int64_t key, int64_t c, const float (&acc)[N],
-                                          uint32_t site) {
-    float v[N];
-    const size_t at = (size_t)(key * a.D + c);
-    if (a.accumulate) {
-        load_at<N>(a.table, at, v, site);
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = fmaf(a.scale, acc[k], v[k]);
+__device__ __forceinline__ void load_floats(const Span<float>& s, size_t at, float (&v)[N], uint32_t site) {
+    if (N == 8 && (reinterpret_cast<uintptr_t>(s.p + at) & 31u) == 0 && s.has(at, N, site)) {
+        asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1 % N]), "=f"(v[2 % N]), "=f"(v[3 % N]), "=f"(v[4 % N]), "=f"(v[5 % N]),
+                       "=f"(v[6 % N]), "=f"(v[7 % N])
+                     : "l"(s.p + at)
+                     : "memory");
     } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = a.scale * acc[k];
+        load_at<N>(s, at, v, site);
     }
-    store_at<N>(a.table, at, v, site);
+}
+template <int N>
+__device__ __forceinline__ void store_floats(const Span<float>& s, size_t at, const float (&v)[N], uint32_t site) {
+    if (N == 8 && (reinterpret_cast<uintptr_t>(s.p + at) & 31u) == 0) {
+        if (s.has(at, N, site))
+            asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(s.p + at), "f"(v[0]), "f"(v[1 % N]),
+                         "f"(v[2 % N]), "f"(v[3 % N]), "f"(v[4 % N]), "f"(v[5 % N]), "f"(v[6 % N]), "f"(v[7 % N])
+                         : "memory");
+    } else {
+        store_at<N>(s, at, v, site);
+    }
 }
 
+// A finished row of the gradient.  When accumulating, its old values are read
+// when the row is finished and added when the next one is (or at the end), so
+// that the read's latency is not waited for.
+template <int N>
+struct RowWriter {
+    int64_t key = -1;
+    float sum[N], old[N];
+    __device__ __forceinline__ void complete(const SumArgs& a, int64_t c) {
+        if (key < 0) return;
+#pragma unroll
+        for (int k = 0; k < N; ++k) old[k] = fmaf(a.scale, sum[k], old[k]);
+        store_floats<N>(a.table, (size_t)(key * a.D + c), old, 12);
+        key = -1;
+    }
+    __device__ __forceinline__ void write(const SumArgs& a, int64_t row, int64_t c, const float (&acc)[N]) {
+        if (!a.accumulate) {
+            float v[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = a.scale * acc[k];
+            store_floats<N>(a.table, (size_t)(row * a.D + c), v, 12);
+            return;
+        }
+        complete(a, c);
+        key = row;
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k] = acc[k];
+        load_floats<N>(a.table, (size_t)(row * a.D + c), old, 12);
+    }
+};
+
+// Each warp zeroes the absent ones of its own kZeroRows / 4 rows.
 template <int N>
 __device__ void zero_rows(const SumArgs& a, int64_t first) {
-    __shared__ uint32_t present;
-    const int64_t last = first + kZeroRows < a.V ? first + kZeroRows : a.V;
-    if (threadIdx.x == 0) present = 0;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int64_t lo = lower_bound_warp(a.order, a.T, first), hi = lower_bound_warp(a.order, a.T, last);
-        uint32_t bits = 0;
-        for (int64_t i = lo + threadIdx.x; i < hi; i += 32) bits |= 1u << (key_at(a.order, i, 8) - first);
-        atomicOr(&present, bits);
-    }
-    __syncthreads();
-    const uint32_t rows = present;
-    const float zero[N] = {};
+    constexpr int kPerWarp = kZeroRows / (kThreads / 32);
+    const int lane = threadIdx.x & 31;
+    first += (threadIdx.x >> 5) * kPerWarp;
+    const int64_t last = first + kPerWarp < a.V ? first + kPerWarp : a.V;
+    int64_t at = -1, next = -1;   // next: the first id at or above the row, at its place
     for (int64_t v = first; v < last; ++v) {
-        if (rows >> (v - first) & 1u) continue;
-        for (int64_t c = (int64_t)threadIdx.x * N; c < a.D; c += kThreads * N)
-            store_at<N>(a.table, (size_t)(v * a.D + c), zero, 9);
+        if (next < v) {
+            at = lower_bound_warp(a.order, a.T, v);
+            next = at < a.T ? key_at(a.order, at, 8) : a.V;
+        }
+        if (next == v) continue;
+        constexpr int W = N == 8 ? 4 : 1;   // 16-byte stores
+        const float zero[W] = {};
+        for (int64_t c = lane * W; c < a.D; c += 32 * W) store_at<W>(a.table, (size_t)(v * a.D + c), zero, 9);
     }
+}
+
+// Writes the sum of the run that ends at an item, or its piece in this chunk.
+template <int N>
+__device__ __forceinline__ void flush(const SumArgs& a, RowWriter<N>& out, int64_t chunk, int64_t key, int64_t c,
+                                      bool whole, bool began, float (&acc)[N]) {
+    if (c < a.D) {
+        if (whole)
+            out.write(a, key, c, acc);
+        else
+            store_floats<N>(a.pieces, (size_t)((chunk * 2 + (began ? 1 : 0)) * a.D + c), acc, 13);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
 }
 
 // Blocks 0 .. chunks * slabs - 1 sum; the others zero kZeroRows rows each.
+//
+// The rows of a batch of ordered tokens (each token's streams in turn) are
+// listed in shared memory with where runs end; a thread adds its N columns of
+// one row after another.  N = 8: the rows come through per-thread copies,
+// kAhead rows ahead; N = 1: kAhead loads are issued together.
+constexpr uint32_t kRunEnds = 1u << 31, kFlush = 1u << 30, kRowMask = kFlush - 1;   // T n_streams <= 2^28
 template <int N>
 __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
+    ptx::grid_dependency_wait();
     if ((int64_t)blockIdx.x >= a.chunks * a.slabs) {
         zero_rows<N>(a, ((int64_t)blockIdx.x - a.chunks * a.slabs) * kZeroRows);
         return;
     }
-    __shared__ uint64_t s[kBatch + 1];
+    __shared__ uint32_t rows[kBatch * MHCPB_MAX_STREAMS];
+    __shared__ uint32_t ids[kBatch];
+    __shared__ int listed;
+    __shared__ uint4 ring[N == 8 ? kAhead * kThreads : 1];
     const int64_t chunk = blockIdx.x / a.slabs;
     const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * N;
     const int64_t begin = chunk * a.chunk;
     const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
-    bool began_here = begin == 0 || key_at(a.order, begin - 1, 10) != key_at(a.order, begin, 10);
+    bool began = begin == 0 || key_at(a.order, begin - 1, 10) != key_at(a.order, begin, 10);
+    RowWriter<N> out;
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
     for (int64_t b = begin; b < end; b += kBatch) {
         __syncthreads();
-        if (threadIdx.x <= kBatch) s[threadIdx.x] = b + threadIdx.x < a.T ? order_at(a.order, b + threadIdx.x, 10) : ~0ull;
+        if (threadIdx.x < kBatch) {
+            const int64_t at = b + threadIdx.x;
+            const bool in = at < end;
+            const uint64_t v = in ? order_at(a.order, at, 10) : ~0ull;
+            const int64_t key = (int64_t)(v >> 32), next = at + 1 < a.T ? key_at(a.order, at + 1, 10) : -1;
+            const bool counts = in && key < a.V;   // ids outside the table come last
+            const bool ends = next != key;
+            const int valid = __popc(__ballot_sync(kFullMask, counts));
+            if (threadIdx.x == 0) listed = valid * a.n_streams;
+            ids[threadIdx.x] = (uint32_t)key;
+            if (counts)
+                for (int s = 0; s < a.n_streams; ++s) {
+                    uint32_t row = (uint32_t)v * (uint32_t)a.n_streams + s;
+                    if (s + 1 == a.n_streams && (ends || at + 1 == end)) row |= kFlush | (ends ? kRunEnds : 0u);
+                    rows[threadIdx.x * a.n_streams + s] = row;
+                }
+        }
         __syncthreads();
-        const int m = (int)(end - b < kBatch ? end - b : kBatch);
-        for (int i = 0; i < m; ++i) {
-            const int64_t key = (int64_t)(s[i] >> 32), t = (int64_t)(uint32_t)s[i];
-            if (key >= a.V) break;   // only ids outside the table follow
-            if (c < a.D)
-                for (int st = 0; st < a.n_streams; ++st) {
-                    float v[N];
-                    load_at<N>(a.grad_x, (size_t)((t * a.n_streams + st) * a.D + c), v, 11);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) acc[k] += v[k];
+        const int items = listed;
+        if (items == 0) break;
+        if constexpr (N == 8) {
+            uint4* const mine = ring + threadIdx.x;
+            const auto fetch = [&](int item) {
+                if (item < items && c < a.D) {
+                    const size_t at = (size_t)(rows[item] & kRowMask) * a.D + c;
+                    if (a.grad_x.has(at, N, 11)) copy16(mine + item % kAhead * kThreads, a.grad_x.p + at);
                 }
-            const bool ends = (int64_t)(s[i + 1] >> 32) != key;
-            if (ends || b + i + 1 == end) {
-                if (c < a.D) {
-                    if (began_here && ends)
-                        write_row<N>(a, key, c, acc, 12);
-                    else
-                        store_at<N>(a.pieces, (size_t)((chunk * 2 + (began_here ? 1 : 0)) * a.D + c), acc, 13);
-                }
-                began_here = true;
+                copies_commit();
+            };
 #pragma unroll
-                for (int k = 0; k < N; ++k) acc[k] = 0.f;
+            for (int q = 0; q < kAhead; ++q) fetch(q);
+            int position = 0, stream = 0;
+            for (int item = 0; item < items; ++item) {
+                copies_wait<kAhead - 1>();
+                float2 v[4];
+                unpack<bf16>(mine[item % kAhead * kThreads], v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[2 * k] += v[k].x;
+                    acc[2 * k + 1] += v[k].y;
+                }
+                fetch(item + kAhead);
+                const uint32_t row = rows[item];
+                if (row & kFlush) {
+                    flush<N>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
+                    began = true;
+                }
+                if (++stream == a.n_streams) {
+                    stream = 0;
+                    ++position;
+                }
+            }
+            copies_wait<0>();
+        } else {
+            int position = 0, stream = 0;
+            for (int item = 0; item < items; item += kAhead) {
+                float v[kAhead][N];
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q)
+                    if (item + q < items && c < a.D)
+                        load_at<N>(a.grad_x, (size_t)(rows[item + q] & kRowMask) * a.D + c, v[q], 11);
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q)
+                    if (item + q < items) {
+#pragma unroll
+                        for (int k = 0; k < N; ++k) acc[k] += v[q][k];
+                        const uint32_t row = rows[item + q];
+                        if (row & kFlush) {
+                            flush<N>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
+                            began = true;
+                        }
+                        if (++stream == a.n_streams) {
+                            stream = 0;
+                            ++position;
+                        }
+                    }
             }
         }
     }
+    out.complete(a, c);
 }
 
 // Block (chunk, slab): if a run begins in this chunk and goes on after it,
 // adds its pieces in order.
 template <int N>
 __global__ void __launch_bounds__(kThreads) join_runs_kernel(SumArgs a) {
+    ptx::grid_dependency_wait();
     const int64_t chunk = blockIdx.x / a.slabs;
     const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * N;
     const int64_t begin = chunk * a.chunk;
-    int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
-    const int64_t key = key_at(a.order, end - 1, 14);
-    if (key >= a.V || end >= a.T || key_at(a.order, end, 14) != key) return;
-    if (begin > 0 && key_at(a.order, begin - 1, 14) == key) return;
+    const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
+    const int64_t key = key_at(a.order, end - 1, 14), next = end < a.T ? key_at(a.order, end, 14) : -1;
+    const int64_t previous = begin > 0 ? key_at(a.order, begin - 1, 14) : -1;
+    if (key >= a.V || next != key || previous == key) return;
+    const int64_t last = (lower_bound_warp(a.order, a.T, key + 1) - 1) / a.chunk;   // the chunk it ends in
     if (c >= a.D) return;
     float acc[N];
-    load_at<N>(a.pieces, (size_t)((chunk * 2 + 1) * a.D + c), acc, 15);
-    for (int64_t q = chunk + 1; q < a.chunks; ++q) {
+    load_floats<N>(a.pieces, (size_t)((chunk * 2 + 1) * a.D + c), acc, 15);
+#pragma unroll 4
+    for (int64_t q = chunk + 1; q <= last; ++q) {
         float v[N];
-        load_at<N>(a.pieces, (size_t)(q * 2 * a.D + c), v, 15);
+        load_floats<N>(a.pieces, (size_t)(q * 2 * a.D + c), v, 15);
 #pragma unroll
         for (int k = 0; k < N; ++k) acc[k] += v[k];
-        end = (q + 1) * a.chunk;
-        if (end >= a.T || key_at(a.order, end, 14) != key) break;
     }
-    write_row<N>(a, key, c, acc, 16);
+    RowWriter<N> out;
+    out.write(a, key, c, acc);
+    out.complete(a, c);
+}
+
+// Launches a kernel that waits by itself (griddepcontrol.wait) for the one before it.
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(grid);
+    config.blockDim = dim3(threads);
+    config.stream = stream;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, args...);
 }
 
 template <typename E, typename I>
@@ -298,11 +461,9 @@ template <int N>
 cudaError_t sum_typed(SumArgs s, cudaStream_t stream) {
     s.slabs = (s.D + kThreads * N - 1) / (kThreads * N);
     const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
-    sum_runs_kernel<N><<<(unsigned)(s.chunks * s.slabs + zeroing), kThreads, 0, stream>>>(s);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_after(sum_runs_kernel<N>, (unsigned)(s.chunks * s.slabs + zeroing), kThreads, stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
-    join_runs_kernel<N><<<(unsigned)(s.chunks * s.slabs), kThreads, 0, stream>>>(s);
-    return cudaGetLastError();
+    return launch_after(join_runs_kernel<N>, (unsigned)(s.chunks * s.slabs), kThreads, stream, s);
 }
 
 }  // namespace
@@ -324,19 +485,20 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
     uint64_t* other = reinterpret_cast<uint64_t*>(ws + order_bytes(a.T));
     cudaError_t e;
     if (a.T > 0) {
-        const unsigned tiles = (unsigned)((a.T + kSortTile - 1) / kSortTile);
+        const int tile = a.T <= kOneTile ? kOneTile : kTile;
+        const unsigned blocks = (unsigned)((a.T + kRanked - 1) / kRanked);
         const Span<uint64_t> out{order, (size_t)a.T};
         if (a.id_bytes == 8)
-            sort_tiles_kernel<int64_t><<<tiles, kSortThreads, 0, stream>>>(
-                a.T, a.V, Span<const int64_t>{static_cast<const int64_t*>(a.ids), (size_t)a.T}, out);
+            rank_kernel<int64_t><<<blocks, 256, 0, stream>>>(
+                a.T, a.V, tile, Span<const int64_t>{static_cast<const int64_t*>(a.ids), (size_t)a.T}, out);
         else
-            sort_tiles_kernel<int32_t><<<tiles, kSortThreads, 0, stream>>>(
-                a.T, a.V, Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out);
+            rank_kernel<int32_t><<<blocks, 256, 0, stream>>>(
+                a.T, a.V, tile, Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        for (int64_t run = kSortTile; run < a.T; run *= kFan) {
-            merge_runs_kernel<<<(unsigned)((a.T + 255) / 256), 256, 0, stream>>>(
-                a.T, run, Span<const uint64_t>{order, (size_t)a.T}, Span<uint64_t>{other, (size_t)a.T});
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        for (int64_t run = tile; run < a.T; run *= kFan) {
+            e = launch_after(merge_runs_kernel, (unsigned)((a.T + 256 / kFan - 1) / (256 / kFan)), 256, stream, a.T, run,
+                             Span<const uint64_t>{order, (size_t)a.T}, Span<uint64_t>{other, (size_t)a.T});
+            if (e != cudaSuccess) return e;
             uint64_t* const swap = order;
             order = other;
             other = swap;
