@@ -426,21 +426,6 @@ __global__ void __launch_bounds__(kThreads) join_runs_kernel(SumArgs a) {
     out.complete(a, c);
 }
 
-// Launches a kernel that waits by itself (griddepcontrol.wait) for the one before it.
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(grid);
-    config.blockDim = dim3(threads);
-    config.stream = stream;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    config.attrs = &early;
-    config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, kernel, args...);
-}
-
 template <typename E, typename I>
 cudaError_t lookup_typed(const Args& a, cudaStream_t stream) {
     const Span<const E> table{static_cast<const E*>(a.table), (size_t)(a.V * a.D)};
@@ -461,9 +446,9 @@ template <int N>
 cudaError_t sum_typed(SumArgs s, cudaStream_t stream) {
     s.slabs = (s.D + kThreads * N - 1) / (kThreads * N);
     const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
-    cudaError_t e = launch_after(sum_runs_kernel<N>, (unsigned)(s.chunks * s.slabs + zeroing), kThreads, stream, s);
+    cudaError_t e = launch_early(sum_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
-    return launch_after(join_runs_kernel<N>, (unsigned)(s.chunks * s.slabs), kThreads, stream, s);
+    return launch_early(join_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs)), dim3(kThreads), stream, s);
 }
 
 }  // namespace
@@ -496,7 +481,7 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
                 a.T, a.V, tile, Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         for (int64_t run = tile; run < a.T; run *= kFan) {
-            e = launch_after(merge_runs_kernel, (unsigned)((a.T + 256 / kFan - 1) / (256 / kFan)), 256, stream, a.T, run,
+            e = launch_early(merge_runs_kernel, dim3((unsigned)((a.T + 256 / kFan - 1) / (256 / kFan))), dim3(256), stream, a.T, run,
                              Span<const uint64_t>{order, (size_t)a.T}, Span<uint64_t>{other, (size_t)a.T});
             if (e != cudaSuccess) return e;
             uint64_t* const swap = order;

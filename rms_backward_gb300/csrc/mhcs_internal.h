@@ -25,6 +25,22 @@ struct DropArgs {                // see Drop in mhcs_common.cuh
     float scale;
 };
 
+// Launches a kernel that may start before the one ahead of it in the stream has
+// ended, and waits for it by itself (griddepcontrol.wait).
+template <typename... Params, typename... Values>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, Values... values) {
+    cudaLaunchConfig_t config{};
+    config.gridDim = grid;
+    config.blockDim = block;
+    config.stream = stream;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, static_cast<Params>(values)...);
+}
+
 namespace embed {
 struct Args {
     int64_t T, V, D;

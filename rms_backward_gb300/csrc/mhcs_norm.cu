@@ -18,6 +18,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
+#include "ptx.cuh"
 
 namespace mhcpb {
 namespace ops {
@@ -126,6 +127,238 @@ __global__ void __launch_bounds__(kThreads) forward_any_kernel(Params<E> a) {
         store_at<1>(a.mean, (size_t)t, m, 4);
         store_at<1>(a.rstd, (size_t)t, r, 4);
     }
+}
+
+// ------------------------------------------------------------ forward, rows in registers
+// A group of G threads holds one row, VPT pieces of N columns per thread (N is
+// a 16-byte vector, or 1 for rows that are not aligned), everything loaded
+// before anything is used.  Blocks are small and many, so that some load
+// while others reduce or store.
+template <typename E, bool MIX, int N, int VPT>
+__global__ void __launch_bounds__(640) forward_rows_kernel(Params<E> a, int G, int R) {
+    __shared__ float sums[2][32];   // by warp of the block
+    const int tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
+    const int warp = tid >> 5, warp0 = group * (G >> 5), warps = G >> 5;
+    const int64_t t = (int64_t)blockIdx.x * R + group;
+    const bool valid = t < a.T;     // the last block's other groups still meet their barriers
+    const int D = (int)a.D, c0 = i * N, step = G * N;
+    float gate[kStreams] = {};
+    if constexpr (MIX)
+        if (valid)
+#pragma unroll
+            for (int s = 0; s < kStreams; ++s) gate[s] = scalar_at(a.h, t * kGates + s, 1);
+    float u[VPT][N];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        if (valid && c0 + v * step < D) {
+            row_at<E, MIX, N>(a, gate, t, c0 + v * step, u[v]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) u[v][k] = 0.f;
+        }
+    }
+    const float inv_d = 1.f / (float)D;
+    const auto total = [&](float s, int which) {
+        s = warp_sum(s);
+        if (lane == 0) sums[which][warp] = s;
+        group_sync(group, G);
+        return warp_sum(lane < warps ? sums[which][warp0 + lane] : 0.f);
+    };
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int k = 0; k < N; ++k) s += u[v][k];
+    const float mean = total(s, 0) * inv_d;
+    s = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+        if (c0 + v * step < D)
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                u[v][k] -= mean;
+                s = fmaf(u[v][k], u[v][k], s);
+            }
+    const float rstd = 1.f / sqrtf(total(s, 1) * inv_d + a.eps);
+    if (!valid) return;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = c0 + v * step;
+        if (c < D) {
+            float g[N], b[N];
+            vector_at<N>(a.gamma, c, 1.f, g, 2);
+            vector_at<N>(a.beta, c, 0.f, b, 2);
+#pragma unroll
+            for (int k = 0; k < N; ++k) u[v][k] = fmaf(u[v][k] * rstd, g[k], b[k]);
+            store_at<N>(a.y, (size_t)(t * a.y_stride + c), u[v], 3);
+        }
+    }
+    if (i == 0 && a.mean.p != nullptr) {
+        const float m[1] = {mean}, r[1] = {rstd};
+        store_at<1>(a.mean, (size_t)t, m, 4);
+        store_at<1>(a.rstd, (size_t)t, r, 4);
+    }
+}
+
+// ------------------------------------------------------------ forward, rows through shared memory
+// Groups, per-thread copies S rows ahead and columns as in backward_rows_kernel
+// below.  Each warp centres its own columns (their mean m_w, then the squares
+// about it) and publishes both, so that one barrier gives the row's statistics
+// without cancellation: mean = sum n_w m_w / D and
+// D var = sum q_w + sum n_w (m_w - mean)^2.
+template <typename E, bool MIX, int VPT, int S>
+struct ForwardShape {
+    static constexpr int N = Elem<E>::kPack;
+    static constexpr int kMaxThreads = 640;
+    static constexpr int kArrays = MIX ? kStreams : 1;
+    static constexpr int kStage = VPT * kArrays;
+    static constexpr int kPitch = kMaxThreads;
+    static constexpr int kSlots = S * kStage;
+    static constexpr int kVectorSlots = 2 * VPT * N / 4;   // gamma and beta of a thread's columns
+    static size_t bytes(int G, int R) {
+        return (size_t)kPitch * kSlots * 16 + (size_t)G * kVectorSlots * 16 + (size_t)R * (G / 32 * S * 16 + 2 * 2 * 32 * 4);
+    }
+};
+
+template <typename E, bool MIX, int VPT, int S>
+__global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1)
+    forward_ring_kernel(Params<E> a, int G, int R) {
+    using Shape = ForwardShape<E, MIX, VPT, S>;
+    constexpr int N = Shape::N, H = N / 2, P = Shape::kPitch, A = Shape::kArrays;
+    extern __shared__ uint4 slots[];
+    const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
+    const int warp = i >> 5, warps = G >> 5;
+    uint4* const mine = slots + tid;
+    float4* const vectors = reinterpret_cast<float4*>(slots + P * Shape::kSlots);   // [2][VPT N / 4][G]
+    float* const floats = reinterpret_cast<float*>(vectors + Shape::kVectorSlots * G);
+    float* const gates = floats + (tid >> 5) * (S * 4);                             // [S][4] per warp
+    float* const sums = floats + (NT >> 5) * (S * 4) + group * (2 * 2 * 32);        // [2][2][32]
+    const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group, T = (int)a.T;
+    const int c0 = i * N, step = G * N, D = (int)a.D;
+
+#pragma unroll
+    for (int k = 0; k < Shape::kSlots; ++k) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+    if (group == 0)
+#pragma unroll
+        for (int k = 0; k < Shape::kVectorSlots / 2; ++k) {
+            const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
+            float g[4] = {}, b[4] = {};
+            if (c < D) {
+                vector_at<4>(a.gamma, c, 1.f, g, 2);
+                vector_at<4>(a.beta, c, 0.f, b, 2);
+            }
+            vectors[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
+            vectors[(Shape::kVectorSlots / 2 + k) * G + i] = make_float4(b[0], b[1], b[2], b[3]);
+        }
+    __syncthreads();
+
+    const auto fetch = [&](int t, int stage) {
+        if (t < T) {
+            const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.x_stride + (uint32_t)c0);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+                if (c0 + v * step < D)
+#pragma unroll
+                    for (int s = 0; s < A; ++s)
+                        if (a.x.has(at + v * step + s * D, N, 0))
+                            copy16(mine + ((stage * VPT + v) * A + s) * P, a.x.p + at + v * step + s * D);
+            if (MIX && lane < kStreams && a.h.has((size_t)t * kGates + lane, 1, 1))
+                copy4(gates + stage * 4 + lane, a.h.p + (size_t)t * kGates + lane);
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int q = 0; q < S; ++q) fetch(first + q * groups, q);
+
+    // this warp's share of the columns, and lane w's: warp w's
+    const auto share = [&](int w) {
+        int n = 0;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int left = D - (w * 32 * N + v * step);
+            n += left < 0 ? 0 : left < 32 * N ? left : 32 * N;
+        }
+        return (float)n;
+    };
+    const float n_mine = share(warp), inv_mine = n_mine > 0.f ? 1.f / n_mine : 0.f;
+    const float n_lane = lane < warps ? share(lane) : 0.f, inv_d = 1.f / (float)D;
+    int stage = 0, parity = 0;
+    for (int t = first; t < T; t += groups) {
+        copies_wait<S - 1>();
+        __syncwarp();
+        const uint4* const row = mine + stage * (Shape::kStage * P);
+        float2 u[VPT][H], s2 = pair(0.f);
+        float p4[kStreams] = {};
+        if constexpr (MIX) {
+            const float4 pre = *reinterpret_cast<const float4*>(gates + stage * 4);
+            p4[0] = pre.x;
+            p4[1] = pre.y;
+            p4[2] = pre.z;
+            p4[3] = pre.w;
+        }
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            unpack<E>(row[v * A * P], u[v]);
+            if constexpr (MIX) {
+#pragma unroll
+                for (int k = 0; k < H; ++k) u[v][k] = mul2(u[v][k], pair(p4[0]));
+#pragma unroll
+                for (int s = 1; s < A; ++s) {
+                    float2 x[H];
+                    unpack<E>(row[(v * A + s) * P], x);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) u[v][k] = fma2(pair(p4[s]), x[k], u[v][k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < H; ++k) s2 = add2(s2, u[v][k]);
+        }
+        __syncwarp();   // every lane has read the gates
+        fetch(t + S * groups, stage);
+        stage = stage + 1 == S ? 0 : stage + 1;
+        const float m_mine = warp_sum(s2.x + s2.y) * inv_mine;
+        float2 q2 = pair(0.f);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            if (c0 + v * step < D)
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    const float2 d = add2(u[v][k], pair(-m_mine));
+                    q2 = fma2(d, d, q2);
+                }
+        const float q_mine = warp_sum(q2.x + q2.y);
+        float* const s0 = sums + parity * (2 * 32);
+        if (lane == 0) {
+            s0[warp] = m_mine;
+            s0[32 + warp] = q_mine;
+        }
+        group_sync(group, G);
+        const float m = lane < warps ? s0[lane] : 0.f, q = lane < warps ? s0[32 + lane] : 0.f;
+        const float mean = warp_sum(n_lane * m) * inv_d;
+        const float var = warp_sum(fmaf(n_lane * (m - mean), m - mean, q)) * inv_d;
+        const float rstd = 1.f / sqrtf(var + a.eps);
+        const float2 mean2 = pair(-mean), rstd2 = pair(rstd);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            float2 o[H];
+#pragma unroll
+            for (int k = 0; k < H / 2; ++k) {
+                const float4 g = vectors[(v * (N / 4) + k) * G + i];
+                const float4 b = vectors[(Shape::kVectorSlots / 2 + v * (N / 4) + k) * G + i];
+                o[2 * k] = fma2(mul2(add2(u[v][2 * k], mean2), rstd2), make_float2(g.x, g.y), make_float2(b.x, b.y));
+                o[2 * k + 1] = fma2(mul2(add2(u[v][2 * k + 1], mean2), rstd2), make_float2(g.z, g.w), make_float2(b.z, b.w));
+            }
+            const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.y_stride + (uint32_t)(c0 + v * step));
+            if (c0 + v * step < D && a.y.has(at, N, 3)) *reinterpret_cast<uint4*>(a.y.p + at) = pack<E>(o);
+        }
+        if (i == 0 && a.mean.p != nullptr) {
+            const float o1[1] = {mean}, o2[1] = {rstd};
+            store_at<1>(a.mean, (size_t)t, o1, 4);
+            store_at<1>(a.rstd, (size_t)t, o2, 4);
+        }
+        parity ^= 1;
+    }
+    copies_wait<0>();
 }
 
 // One row per block: its input gradient (and the gates').
@@ -538,12 +771,153 @@ __global__ void __launch_bounds__((RowsShape<E, MIX, VPT, S>::kMaxThreads), 1)
     }
 }
 
+// ------------------------------------------------------------ backward, unaligned rows in registers
+// As backward_rows_kernel, an element at a time (rows whose addresses are not
+// multiples of 16 bytes): thread i owns columns i, i + G, ..., VPT of them,
+// and loads its part of a row directly.
+template <typename E, bool MIX, int VPT, int MAX>
+__global__ void __launch_bounds__(MAX, 1) backward_elements_kernel(Params<E> a, int G, int R) {
+    extern __shared__ float shared[];   // [R][2][2 or 6][32] sums, then [2][VPT][G] parameter gradients
+    constexpr int XA = MIX ? kStreams : 1, kSums = MIX ? 2 + kStreams : 2;
+    const int tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
+    const int warp = i >> 5, warps = G >> 5, D = (int)a.D, T = (int)a.T;
+    float* const sums = shared + group * (2 * kSums * 32);
+    const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group;
+    const bool residual = MIX && a.grad_x_out.p != nullptr;
+    const float inv_d = 1.f / (float)D;
+    float gg[VPT], gb[VPT], gam[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        gg[v] = gb[v] = 0.f;
+        float g[1] = {0.f};
+        if (i + v * G < D) vector_at<1>(a.gamma, i + v * G, 1.f, g, 2);
+        gam[v] = g[0];
+    }
+    int parity = 0;
+    for (int t = first; t < T; t += groups) {
+        float x[VPT][XA], w[VPT], gate[kGates];
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = i + v * G;
+            float one[1] = {0.f};
+            w[v] = 0.f;
+#pragma unroll
+            for (int s = 0; s < XA; ++s) x[v][s] = 0.f;
+            if (c < D) {
+#pragma unroll
+                for (int s = 0; s < XA; ++s) {
+                    load_at<1>(a.x, (size_t)t * a.x_stride + s * D + c, one, 0);
+                    x[v][s] = one[0];
+                }
+                load_at<1>(a.grad_y, (size_t)t * a.gy_stride + c, one, 5);
+                w[v] = one[0];
+            }
+        }
+        if constexpr (MIX)
+#pragma unroll
+            for (int k = 0; k < kGates; ++k)
+                if (k < kStreams || k >= 2 * kStreams) gate[k] = scalar_at(a.h, (int64_t)t * kGates + k, 1);
+        const float mean = scalar_at(a.mean, t, 4), rstd = scalar_at(a.rstd, t, 4);
+        float z[VPT], sw = 0.f, swz = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            float u = x[v][0];
+            if constexpr (MIX) {
+                u *= gate[0];
+#pragma unroll
+                for (int s = 1; s < XA; ++s) u = fmaf(gate[s], x[v][s], u);
+            }
+            z[v] = (u - mean) * rstd;
+            gg[v] = fmaf(w[v], z[v], gg[v]);
+            gb[v] += w[v];
+            w[v] *= gam[v];
+            sw += w[v];
+            swz = fmaf(w[v], z[v], swz);
+        }
+        float* const s0 = sums + parity * (kSums * 32);
+        const float both = warp_sum_two(sw, swz);
+        if ((lane & 15) == 0) s0[(lane >> 4) * 32 + warp] = both;
+        group_sync(group, G);
+        const float mw = warp_sum(lane < warps ? s0[lane] : 0.f) * inv_d;
+        const float mwz = warp_sum(lane < warps ? s0[32 + lane] : 0.f) * inv_d;
+        float dot[kStreams] = {};
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = i + v * G;
+            if (c < D) {
+                const float du = rstd * (w[v] - mw - z[v] * mwz);
+                float o[XA];
+                if constexpr (!MIX) {
+                    o[0] = du;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < XA; ++j) {
+                        dot[j] = fmaf(x[v][j], du, dot[j]);
+                        o[j] = gate[j] * du;
+                    }
+                    if (residual)
+#pragma unroll
+                        for (int s = 0; s < kStreams; ++s) {
+                            float g[1];
+                            load_at<1>(a.grad_x_out, ((size_t)t * kStreams + s) * D + c, g, 7);
+#pragma unroll
+                            for (int j = 0; j < XA; ++j) o[j] = fmaf(gate[8 + 4 * s + j], g[0], o[j]);
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < XA; ++j) {
+                    const float one[1] = {o[j]};
+                    store_at<1>(a.grad_x, (size_t)t * a.gx_stride + j * D + c, one, 6);
+                }
+            }
+        }
+        if constexpr (MIX) {
+            const float d = warp_sum_four(dot);
+            if ((lane & 7) == 0) s0[(2 + (lane >> 3)) * 32 + warp] = d;
+            group_sync(group, G);
+            if (warp == 0) {
+                float q = 0.f;
+                for (int k = lane & 7; k < warps; k += 8) q += s0[(2 + (lane >> 3)) * 32 + k];
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(kFullMask, q, o);
+                const float one[1] = {q};
+                if ((lane & 7) == 0) store_at<1>(a.grad_h, (size_t)t * kGates + (lane >> 3), one, 8);
+            }
+        }
+        parity ^= 1;
+    }
+    if (a.grad_gamma.p == nullptr && a.grad_beta.p == nullptr) return;
+    float* const acc = shared + R * (2 * kSums * 32);
+    for (int g = 0; g < R; ++g) {   // the block's groups in order
+        __syncthreads();
+        if (g != group) continue;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            float* const p = acc + v * G + i;
+            float* const q = p + VPT * G;
+            if (g > 0) {
+                gg[v] += *p;
+                gb[v] += *q;
+            }
+            if (g + 1 < R) {
+                *p = gg[v];
+                *q = gb[v];
+            } else if (i + v * G < D) {
+                const float o1[1] = {gg[v]}, o2[1] = {gb[v]};
+                store_at<1>(a.partial, ((size_t)blockIdx.x * 2 + 0) * D + i + v * G, o1, 9);
+                store_at<1>(a.partial, ((size_t)blockIdx.x * 2 + 1) * D + i + v * G, o2, 9);
+            }
+        }
+    }
+}
+
 // Parameter gradients: the partials of a column in a fixed order (16 threads
 // each add every 16th part, then their sums are added in order).
 // blockIdx.y: 0 gamma, 1 beta.
 __global__ void __launch_bounds__(512) reduce_parts_kernel(int64_t D, int64_t parts, bool accumulate,
                                                            Span<float> partial, Span<float> gamma, Span<float> beta) {
     __shared__ float s[16][33];
+    ptx::grid_dependency_wait();
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     const Span<float> out = blockIdx.y == 0 ? gamma : beta;
     if (out.p == nullptr) return;
@@ -597,14 +971,57 @@ Params<E> params_of(const Args& a) {
 
 bool rows_packed(const void* p, int64_t stride, int pack) { return aligned16(p) && stride % pack == 0; }
 
+// Launches forward_rows_kernel where the row fits its registers; false otherwise.
+template <typename E, bool MIX, int N, int VPT>
+bool forward_rows(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
+    const int64_t threads = ((p.D + N - 1) / N + VPT - 1) / VPT;
+    if (threads > 640) return false;
+    const int G = (int)((threads + 31) / 32 * 32);
+    int R = 256 / G < 1 ? 1 : 256 / G;             // blocks of about 256 threads
+    while (R > 1 && (p.T + R - 1) / R < kSms) --R; // but first a block per SM
+    forward_rows_kernel<E, MIX, N, VPT><<<(unsigned)((p.T + R - 1) / R), (unsigned)(G * R), 0, stream>>>(p, G, R);
+    *e = cudaGetLastError();
+    return true;
+}
+
+// Likewise forward_ring_kernel.
+template <typename E, bool MIX, int VPT, int S>
+bool forward_ring(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
+    using Shape = ForwardShape<E, MIX, VPT, S>;
+    const int64_t threads = (p.D / Shape::N + VPT - 1) / VPT;
+    if (threads > Shape::kMaxThreads) return false;
+    const int G = (int)((threads + 31) / 32 * 32);
+    int R = Shape::kMaxThreads / G > 15 ? 15 : Shape::kMaxThreads / G;
+    const int64_t spread = (p.T + kSms - 1) / kSms;
+    if (R > spread) R = (int)spread;
+    const size_t shared = Shape::bytes(G, R);
+    if (shared > kMaxShared) return false;
+    const int64_t grid = (p.T + R - 1) / R < kSms ? (p.T + R - 1) / R : kSms;
+    auto kernel = forward_ring_kernel<E, MIX, VPT, S>;
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    if (*e != cudaSuccess) return true;
+    kernel<<<(unsigned)grid, (unsigned)(G * R), shared, stream>>>(p, G, R);
+    *e = cudaGetLastError();
+    return true;
+}
+
 template <typename E, bool MIX>
 cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
     const Params<E> p = params_of<E, MIX>(a);
-    constexpr int N = 8;
+    constexpr int N = Elem<E>::kPack;
     const bool packed = a.D % N == 0 && rows_packed(a.x, a.x_stride, N) && rows_packed(a.y, a.y_stride, N) &&
                         aligned16(a.gamma) && aligned16(a.beta);
-    if (packed)
-        forward_any_kernel<E, MIX, N><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
+    cudaError_t e = cudaSuccess;
+    if (packed) {
+        // few rows: more threads each, for latency
+        if ((a.T <= kSms && forward_rows<E, MIX, N, 1>(p, &e, stream)) ||
+            forward_ring<E, MIX, 16 / N, MIX ? 2 : 4>(p, &e, stream) || forward_rows<E, MIX, N, 16 / N>(p, &e, stream))
+            return e;
+    } else if (forward_rows<E, MIX, 1, 4>(p, &e, stream) || forward_rows<E, MIX, 1, 16>(p, &e, stream)) {
+        return e;
+    }
+    if (packed && a.D % 8 == 0)
+        forward_any_kernel<E, MIX, 8><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
     else
         forward_any_kernel<E, MIX, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
@@ -636,6 +1053,26 @@ bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStrea
     return true;
 }
 
+// Likewise backward_elements_kernel.
+template <typename E, bool MIX, int VPT, int MAX>
+bool backward_elements(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStream_t stream) {
+    const int64_t threads = (p.D + VPT - 1) / VPT;
+    if (threads > MAX) return false;
+    const int G = (int)((threads + 31) / 32 * 32);
+    int R = MAX / G > 15 ? 15 : MAX / G;
+    const int64_t spread = (p.T + kSms - 1) / kSms;
+    if (R > spread) R = (int)spread;
+    const int64_t grid = (p.T + R - 1) / R < kSms ? (p.T + R - 1) / R : kSms;
+    *parts = grid;
+    const size_t shared = ((size_t)R * 2 * (MIX ? 6 : 2) * 32 + 2 * VPT * G) * sizeof(float);
+    auto kernel = backward_elements_kernel<E, MIX, VPT, MAX>;
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    if (*e != cudaSuccess) return true;
+    kernel<<<(unsigned)grid, (unsigned)(G * R), shared, stream>>>(p, G, R);
+    *e = cudaGetLastError();
+    return true;
+}
+
 template <typename E, bool MIX>
 cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
     Params<E> p = params_of<E, MIX>(a);
@@ -651,6 +1088,13 @@ cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
                 done = backward_rows<E, true, 1, 2>(p, &p.parts, &e, stream) || backward_rows<E, true, 2, 1>(p, &p.parts, &e, stream);
             else
                 done = backward_rows<E, false, 16 / N, 3>(p, &p.parts, &e, stream);
+        } else {
+            if constexpr (MIX)
+                done = backward_elements<E, true, 4, 640>(p, &p.parts, &e, stream) ||
+                       backward_elements<E, true, 8, 512>(p, &p.parts, &e, stream);
+            else
+                done = backward_elements<E, false, 8, 640>(p, &p.parts, &e, stream) ||
+                       backward_elements<E, false, 16, 512>(p, &p.parts, &e, stream);
         }
         if (!done) {
             constexpr int W = 8;
@@ -665,10 +1109,9 @@ cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
         }
         if (e != cudaSuccess) return e;
     }
-    if (params)
-        reduce_parts_kernel<<<dim3((unsigned)((a.D + 31) / 32), 2), dim3(32, 16), 0, stream>>>(
-            a.D, p.parts, a.accumulate, p.partial, p.grad_gamma, p.grad_beta);
-    return cudaGetLastError();
+    if (!params) return cudaSuccess;
+    return launch_early(reduce_parts_kernel, dim3((unsigned)((a.D + 31) / 32), 2), dim3(32, 16), stream, a.D, p.parts,
+                        a.accumulate, p.partial, p.grad_gamma, p.grad_beta);
 }
 
 }  // namespace
