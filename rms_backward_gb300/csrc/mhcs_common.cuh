@@ -256,40 +256,46 @@ struct ShortPhilox {
     uint32_t r1_lo;       // round 1: low word of the step's product
     uint32_t r2_hi, r2_lo;// round 2: product of round 1's first word, which no element enters
     __device__ __forceinline__ explicit ShortPhilox(const DropKey& d) {
-        k0 = (uint32_t)d.key;
-        k1 = (uint32_t)(d.key >> 32);
-        c3 = (uint32_t)(d.step >> 32);
-        const uint64_t b = (uint64_t)(uint32_t)d.step * 0xCD9E8D57u;
+        // The key is the same in every lane; a warp reduction says so to the
+        // compiler, which then keeps the key schedule off the vector units.
+        k0 = __reduce_or_sync(__activemask(), (uint32_t)d.key);
+        k1 = __reduce_or_sync(__activemask(), (uint32_t)(d.key >> 32));
+        c3 = __reduce_or_sync(__activemask(), (uint32_t)(d.step >> 32));
+        const uint64_t b = (uint64_t)__reduce_or_sync(__activemask(), (uint32_t)d.step) * 0xCD9E8D57u;
         r1_lo = (uint32_t)b;
         const uint64_t a = (uint64_t)((uint32_t)(b >> 32) ^ k0) * 0xD2511F53u;
         r2_hi = (uint32_t)(a >> 32);
         r2_lo = (uint32_t)a;
     }
-    // words of counters i, i + 1, ...: COUNT of them together, so that they share the key schedule
-    template <int COUNT>
-    __device__ __forceinline__ void words(uint32_t i, uint32_t (&w)[COUNT][4]) const {
+    // words of counters i[g], i[g] + 1, ... (COUNT each), all together, so that they share the key schedule
+    template <int GROUPS, int COUNT>
+    __device__ __forceinline__ void words(const uint32_t (&i)[GROUPS], uint32_t (&w)[GROUPS][COUNT][4]) const {
         uint32_t a0 = k0 + 0x9E3779B9u, a1 = k1 + 0xBB67AE85u;
 #pragma unroll
-        for (int n = 0; n < COUNT; ++n) {
-            const uint64_t a = (uint64_t)(i + n) * 0xD2511F53u;
-            const uint64_t b = (uint64_t)((uint32_t)(a >> 32) ^ c3 ^ k1) * 0xCD9E8D57u;
-            w[n][0] = (uint32_t)(b >> 32) ^ r1_lo ^ a0;
-            w[n][1] = (uint32_t)b;
-            w[n][2] = r2_hi ^ (uint32_t)a ^ a1;
-            w[n][3] = r2_lo;
-        }
+        for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+            for (int n = 0; n < COUNT; ++n) {
+                const uint64_t a = (uint64_t)(i[g] + n) * 0xD2511F53u;
+                const uint64_t b = (uint64_t)((uint32_t)(a >> 32) ^ c3 ^ k1) * 0xCD9E8D57u;
+                w[g][n][0] = (uint32_t)(b >> 32) ^ r1_lo ^ a0;
+                w[g][n][1] = (uint32_t)b;
+                w[g][n][2] = r2_hi ^ (uint32_t)a ^ a1;
+                w[g][n][3] = r2_lo;
+            }
 #pragma unroll
         for (int r = 2; r < 10; ++r) {
             a0 += 0x9E3779B9u;
             a1 += 0xBB67AE85u;
 #pragma unroll
-            for (int n = 0; n < COUNT; ++n) {
-                const uint64_t a = (uint64_t)w[n][0] * 0xD2511F53u, b = (uint64_t)w[n][2] * 0xCD9E8D57u;
-                w[n][0] = (uint32_t)(b >> 32) ^ w[n][1] ^ a0;
-                w[n][1] = (uint32_t)b;
-                w[n][2] = (uint32_t)(a >> 32) ^ w[n][3] ^ a1;
-                w[n][3] = (uint32_t)a;
-            }
+            for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+                for (int n = 0; n < COUNT; ++n) {
+                    const uint64_t a = (uint64_t)w[g][n][0] * 0xD2511F53u, b = (uint64_t)w[g][n][2] * 0xCD9E8D57u;
+                    w[g][n][0] = (uint32_t)(b >> 32) ^ w[g][n][1] ^ a0;
+                    w[g][n][1] = (uint32_t)b;
+                    w[g][n][2] = (uint32_t)(a >> 32) ^ w[g][n][3] ^ a1;
+                    w[g][n][3] = (uint32_t)a;
+                }
         }
     }
 };

@@ -236,22 +236,10 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
     const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group, T = (int)a.T;
     const int c0 = i * N, step = G * N, D = (int)a.D;
 
+    // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
-    for (int k = 0; k < Shape::kSlots; ++k) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
-    if (group == 0)
-#pragma unroll
-        for (int k = 0; k < Shape::kVectorSlots / 2; ++k) {
-            const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
-            float g[4] = {}, b[4] = {};
-            if (c < D) {
-                vector_at<4>(a.gamma, c, 1.f, g, 2);
-                vector_at<4>(a.beta, c, 0.f, b, 2);
-            }
-            vectors[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
-            vectors[(Shape::kVectorSlots / 2 + k) * G + i] = make_float4(b[0], b[1], b[2], b[3]);
-        }
-    __syncthreads();
-
+    for (int k = 0; k < Shape::kSlots; ++k)
+        if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
     const auto fetch = [&](int t, int stage) {
         if (t < T) {
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.x_stride + (uint32_t)c0);
@@ -269,6 +257,19 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
     };
 #pragma unroll
     for (int q = 0; q < S; ++q) fetch(first + q * groups, q);
+    if (group == 0)
+#pragma unroll
+        for (int k = 0; k < Shape::kVectorSlots / 2; ++k) {
+            const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
+            float g[4] = {}, b[4] = {};
+            if (c < D) {
+                vector_at<4>(a.gamma, c, 1.f, g, 2);
+                vector_at<4>(a.beta, c, 0.f, b, 2);
+            }
+            vectors[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
+            vectors[(Shape::kVectorSlots / 2 + k) * G + i] = make_float4(b[0], b[1], b[2], b[3]);
+        }
+    __syncthreads();
 
     // this warp's share of the columns, and lane w's: warp w's
     const auto share = [&](int w) {
@@ -327,15 +328,18 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
                     q2 = fma2(d, d, q2);
                 }
         const float q_mine = warp_sum(q2.x + q2.y);
-        float* const s0 = sums + parity * (2 * 32);
-        if (lane == 0) {
-            s0[warp] = m_mine;
-            s0[32 + warp] = q_mine;
+        float mean = m_mine, var = q_mine * inv_d;
+        if (warps > 1) {
+            float* const s0 = sums + parity * (2 * 32);
+            if (lane == 0) {
+                s0[warp] = m_mine;
+                s0[32 + warp] = q_mine;
+            }
+            group_sync(group, G);
+            const float m = lane < warps ? s0[lane] : 0.f, q = lane < warps ? s0[32 + lane] : 0.f;
+            mean = warp_sum(n_lane * m) * inv_d;
+            var = warp_sum(fmaf(n_lane * (m - mean), m - mean, q)) * inv_d;
         }
-        group_sync(group, G);
-        const float m = lane < warps ? s0[lane] : 0.f, q = lane < warps ? s0[32 + lane] : 0.f;
-        const float mean = warp_sum(n_lane * m) * inv_d;
-        const float var = warp_sum(fmaf(n_lane * (m - mean), m - mean, q)) * inv_d;
         const float rstd = 1.f / sqrtf(var + a.eps);
         const float2 mean2 = pair(-mean), rstd2 = pair(rstd);
 #pragma unroll
@@ -505,18 +509,10 @@ __global__ void __launch_bounds__((RowsShape<E, MIX, VPT, S>::kMaxThreads), 1)
     const bool residual = MIX && a.grad_x_out.p != nullptr;
     const int c0 = i * N, step = G * N, D = (int)a.D;   // this thread's columns: c0 + v * step
 
-    // Columns past D: their slots stay 0, so they add nothing to the sums.
+    // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
-    for (int k = 0; k < Shape::kSlots; ++k) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
-    if (group == 0)
-#pragma unroll
-        for (int k = 0; k < Shape::kGammaSlots; ++k) {
-            const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
-            float g[4] = {0.f, 0.f, 0.f, 0.f};
-            if (c < D) vector_at<4>(a.gamma, c, 1.f, g, 2);
-            gammas[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
-        }
-    __syncthreads();
+    for (int k = 0; k < Shape::kSlots; ++k)
+        if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
 
     // Element offset of row t of an array at this thread's first column, formed
     // where it is needed: cheaper than a 64-bit pointer per array kept and moved.
@@ -571,6 +567,16 @@ __global__ void __launch_bounds__((RowsShape<E, MIX, VPT, S>::kMaxThreads), 1)
         }
         copies_commit();
     }
+
+    if (group == 0)
+#pragma unroll
+        for (int k = 0; k < Shape::kGammaSlots; ++k) {
+            const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
+            float g[4] = {0.f, 0.f, 0.f, 0.f};
+            if (c < D) vector_at<4>(a.gamma, c, 1.f, g, 2);
+            gammas[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
+        }
+    __syncthreads();
 
     float2 gg[VPT][H], gb[VPT][H];
 #pragma unroll
@@ -1015,7 +1021,7 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
     if (packed) {
         // few rows: more threads each, for latency
         if ((a.T <= kSms && forward_rows<E, MIX, N, 1>(p, &e, stream)) ||
-            forward_ring<E, MIX, 16 / N, MIX ? 2 : 4>(p, &e, stream) || forward_rows<E, MIX, N, 16 / N>(p, &e, stream))
+            forward_ring<E, MIX, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) || forward_rows<E, MIX, N, 16 / N>(p, &e, stream))
             return e;
     } else if (forward_rows<E, MIX, 1, 4>(p, &e, stream) || forward_rows<E, MIX, 1, 16>(p, &e, stream)) {
         return e;

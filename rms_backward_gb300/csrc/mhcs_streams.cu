@@ -55,6 +55,13 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const
     }
     const ShortPhilox random(key);
     const float2 scale = pair(d.scale);
+    uint32_t w[kDropPacks][N / 4][4];
+    if (d.rng != nullptr) {
+        uint32_t counters[kDropPacks];
+#pragma unroll
+        for (int v = 0; v < kDropPacks; ++v) counters[v] = (uint32_t)((first + (int64_t)v * kThreads * N) >> 2);
+        random.words<kDropPacks, N / 4>(counters, w);
+    }
 #pragma unroll
     for (int v = 0; v < kDropPacks; ++v) {
         const int64_t e = first + (int64_t)v * kThreads * N;
@@ -62,13 +69,11 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const
             float2 f[N / 2];
             unpack<E>(raw[v], f);
             if (d.rng != nullptr) {
-                uint32_t w[N / 4][4];
-                random.words<N / 4>((uint32_t)(e >> 2), w);
 #pragma unroll
                 for (int k = 0; k < N / 2; ++k) {
                     f[k] = mul2(f[k], scale);
-                    f[k].x = w[k / 2][k % 2 * 2] >= d.threshold ? f[k].x : 0.f;
-                    f[k].y = w[k / 2][k % 2 * 2 + 1] >= d.threshold ? f[k].y : 0.f;
+                    f[k].x = w[v][k / 2][k % 2 * 2] >= d.threshold ? f[k].x : 0.f;
+                    f[k].y = w[v][k / 2][k % 2 * 2 + 1] >= d.threshold ? f[k].y : 0.f;
                 }
             }
             if (y.has(e, N, 1)) *reinterpret_cast<uint4*>(y.p + e) = pack<E>(f);
@@ -197,11 +202,12 @@ __device__ __forceinline__ void drop_eight(const Drop& d, const ShortPhilox& ran
                                            uint32_t* keep) {
     *keep = 0xffu;
     if (d.rng == nullptr) return;
-    uint32_t w[2][4];
-    random.words<2>((uint32_t)(e >> 2), w);
+    uint32_t w[1][2][4];
+    const uint32_t counter[1] = {(uint32_t)(e >> 2)};
+    random.words<1, 2>(counter, w);
     *keep = 0u;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) *keep |= (w[k / 4][k % 4] >= d.threshold ? 1u : 0u) << k;
+    for (int k = 0; k < 8; ++k) *keep |= (w[0][k / 4][k % 4] >= d.threshold ? 1u : 0u) << k;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         f[k] = mul2(f[k], pair(d.scale));
@@ -271,9 +277,8 @@ struct TokenShape {
     static constexpr int kStage = VPT * kArrays;
     static constexpr int kPitch = kMaxThreads;
     static constexpr int kDots = 20;
-    static constexpr int kDotPitch = 33;               // one warp reads a column: 20 different banks
     static size_t bytes(int G, int R) {
-        return (size_t)kPitch * S * kStage * 16 + (size_t)R * (G / 32 * S * 4 + 2 * kDots * kDotPitch) * 4;
+        return (size_t)kPitch * S * kStage * 16 + (size_t)R * (G / 32 * S * 4 + 2 * kDots * (G / 32 | 1)) * 4;
     }
 };
 template <int VPT, int S>
@@ -288,13 +293,14 @@ __global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
     uint4* const mine = slots + tid;
     float* const floats = reinterpret_cast<float*>(slots + P * S * Shape::kStage);
     float* const posts = floats + (tid >> 5) * (S * 4);                                   // [S][4] per warp
-    float* const dots = floats + (NT >> 5) * (S * 4) + group * (2 * Shape::kDots * Shape::kDotPitch);
+    float* const dots = floats + (NT >> 5) * (S * 4) + group * (2 * Shape::kDots * (warps | 1));
+    const int dot_pitch = warps | 1;   // odd: the 20 lanes that read a column meet 20 banks
     const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group;
     const int c0 = i * N, step = G * N;
+    // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
-    for (int k = 0; k < S * Shape::kStage; ++k) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);   // columns past D
-    const DropKey key = drop_key(d);
-    const ShortPhilox random(key);
+    for (int k = 0; k < S * Shape::kStage; ++k)
+        if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
 
     const auto fetch_vector = [&](uint4* dst, int t, int v) {
         const int c = c0 + v * step;
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
     };
     const auto write_dots = [&](int t, int parity) {
         if (warp == 0 && lane < Shape::kDots) {
-            const float* const p = dots + (parity * Shape::kDots + lane) * Shape::kDotPitch;
+            const float* const p = dots + (parity * Shape::kDots + lane) * dot_pitch;
             float v[1] = {0.f};
             for (int w = 0; w < warps; ++w) v[0] += p[w];
             store_at<1>(gh, (size_t)t * kGates + 4 + lane, v, 8);
@@ -330,6 +336,8 @@ __global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
         }
         copies_commit();
     }
+    const DropKey key = drop_key(d);   // after the first copies are on their way
+    const ShortPhilox random(key);
     int stage = 0, parity = 0;
     for (int t = first; t < T; t += groups) {
         copies_wait<S - 1>();
@@ -383,9 +391,9 @@ __global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
             if (more) fetch_vector(row, t + S * groups, v);
         }
         const float res = warp_sum_sixteen(d16), pos = warp_sum_four(d4);
-        float* const mine_dots = dots + parity * (Shape::kDots * Shape::kDotPitch) + warp;
-        if ((lane & 1) == 0) mine_dots[(4 + (lane >> 1)) * Shape::kDotPitch] = res;
-        if ((lane & 7) == 0) mine_dots[(lane >> 3) * Shape::kDotPitch] = pos;
+        float* const mine_dots = dots + parity * (Shape::kDots * dot_pitch) + warp;
+        if ((lane & 1) == 0) mine_dots[(4 + (lane >> 1)) * dot_pitch] = res;
+        if ((lane & 7) == 0) mine_dots[(lane >> 3) * dot_pitch] = pos;
         __syncwarp();   // every lane has read the token's gates
         if (more) fetch_post(t + S * groups, stage);
         copies_commit();
@@ -412,6 +420,8 @@ bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, con
     if (R > 15) R = 15;                                // named barriers of a block
     const int64_t spread = (T + kSms - 1) / kSms;      // no more groups than tokens to spread over the blocks
     if (R > spread) R = (int)spread;
+    while (R > 1 && Shape::bytes(G, R) > kMaxShared) --R;
+    if (Shape::bytes(G, R) > kMaxShared) return false;
     const int64_t grid = (T + R - 1) / R < kSms ? (T + R - 1) / R : kSms;
     auto kernel = update_backward_tokens_kernel<VPT, S>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);

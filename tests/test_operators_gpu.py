@@ -234,6 +234,32 @@ def test_update_in_place(D):
     C.update_case(37, D, 0.25, seed=2, in_place=True)
 
 
+# every number of warps per row and of rows per block that the hidden size can lead to
+GROUP_SIZES = [8, 16, 32, 64, 104, 256, 264, 320, 512, 520, 640, 1024, 1280, 1288, 2560, 2568, 5120, 5128, 8192, 10240,
+               10248]
+
+
+@pytest.mark.parametrize("D", GROUP_SIZES)
+def test_group_shapes(D):
+    T = min(2400, 3_000_000 // D)
+    C.norm_forward_case(T, D, "bf16", seed=D)
+    C.norm_backward_case(T, D, "bf16", seed=D)
+    C.collapse_case(T, D, seed=D)
+    C.update_case(T, D, 0.0, seed=D)
+    if D <= 10240 // 2:
+        C.norm_forward_case(T, D, "fp32", seed=D)
+        C.norm_backward_case(T, D, "fp32", seed=D)
+
+
+@pytest.mark.parametrize("D", [31, 33, 127, 257, 511, 1281, 2561, 4097])
+def test_group_shapes_unaligned(D):
+    T = min(2400, 2_000_000 // D)
+    C.norm_forward_case(T, D, "bf16", seed=D)
+    C.norm_backward_case(T, D, "fp32", seed=D)
+    C.collapse_case(T, D, seed=D)
+    C.update_case(T, D, 0.0, seed=D)
+
+
 def test_streams_no_tokens():
     x, y, h = torch.empty(0, 32, dtype=BF, device=DEV), torch.empty(0, 8, dtype=BF, device=DEV), torch.empty(0, 24, device=DEV)
     e, gg, gb = torch.empty(0, device=DEV), empty(8), empty(8)
