@@ -68,6 +68,7 @@ template <typename E, typename I, int N>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(int64_t V, int64_t D, int n_streams, float scale,
                                                           Span<const E> table, Span<const I> ids,
                                                           Span<bf16> x) {
+    ptx::grid_dependency_wait();
     const int64_t t = blockIdx.x;
     const int64_t id = id_at(ids, t, V, 0);
     for (int64_t c = (int64_t)threadIdx.x * N; c < D; c += kThreads * N) {
@@ -92,6 +93,7 @@ __global__ void __launch_bounds__(256) rank_kernel(int64_t T, int64_t V, int til
     __shared__ uint4 quads[kOneTile / 4];
     uint32_t* const keys = reinterpret_cast<uint32_t*>(quads);
     ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     const int blocks_per_tile = tile / kRanked;
     const int64_t base = (int64_t)(blockIdx.x / blocks_per_tile) * tile;
     const int n = (int)(T - base < tile ? T - base : tile), padded = (n + 31) / 32 * 32;
@@ -431,11 +433,9 @@ cudaError_t lookup_typed(const Args& a, cudaStream_t stream) {
     const Span<const E> table{static_cast<const E*>(a.table), (size_t)(a.V * a.D)};
     const Span<const I> ids{static_cast<const I*>(a.ids), (size_t)a.T};
     const Span<bf16> x{static_cast<bf16*>(a.x), (size_t)(a.T * a.n_streams * a.D)};
-    if (a.D % 8 == 0 && aligned16(a.table) && aligned16(a.x))
-        lookup_kernel<E, I, 8><<<(unsigned)a.T, kThreads, 0, stream>>>(a.V, a.D, a.n_streams, a.scale, table, ids, x);
-    else
-        lookup_kernel<E, I, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(a.V, a.D, a.n_streams, a.scale, table, ids, x);
-    return cudaGetLastError();
+    const bool packed = a.D % 8 == 0 && aligned16(a.table) && aligned16(a.x);
+    return launch_early(packed ? lookup_kernel<E, I, 8> : lookup_kernel<E, I, 1>, dim3((unsigned)a.T), dim3(kThreads), 0,
+                        stream, a.V, a.D, a.n_streams, a.scale, table, ids, x);
 }
 template <typename E>
 cudaError_t lookup_ids(const Args& a, cudaStream_t stream) {
@@ -446,9 +446,9 @@ template <int N>
 cudaError_t sum_typed(SumArgs s, cudaStream_t stream) {
     s.slabs = (s.D + kThreads * N - 1) / (kThreads * N);
     const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
-    cudaError_t e = launch_early(sum_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), stream, s);
+    cudaError_t e = launch_early(sum_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
-    return launch_early(join_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs)), dim3(kThreads), stream, s);
+    return launch_early(join_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs)), dim3(kThreads), 0, stream, s);
 }
 
 }  // namespace
@@ -474,14 +474,14 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
         const unsigned blocks = (unsigned)((a.T + kRanked - 1) / kRanked);
         const Span<uint64_t> out{order, (size_t)a.T};
         if (a.id_bytes == 8)
-            rank_kernel<int64_t><<<blocks, 256, 0, stream>>>(
-                a.T, a.V, tile, Span<const int64_t>{static_cast<const int64_t*>(a.ids), (size_t)a.T}, out);
+            e = launch_early(rank_kernel<int64_t>, dim3(blocks), dim3(256), 0, stream, a.T, a.V, tile,
+                             Span<const int64_t>{static_cast<const int64_t*>(a.ids), (size_t)a.T}, out);
         else
-            rank_kernel<int32_t><<<blocks, 256, 0, stream>>>(
-                a.T, a.V, tile, Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            e = launch_early(rank_kernel<int32_t>, dim3(blocks), dim3(256), 0, stream, a.T, a.V, tile,
+                             Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out);
+        if (e != cudaSuccess) return e;
         for (int64_t run = tile; run < a.T; run *= kFan) {
-            e = launch_early(merge_runs_kernel, dim3((unsigned)((a.T + 256 / kFan - 1) / (256 / kFan))), dim3(256), stream, a.T, run,
+            e = launch_early(merge_runs_kernel, dim3((unsigned)((a.T + 256 / kFan - 1) / (256 / kFan))), dim3(256), 0, stream, a.T, run,
                              Span<const uint64_t>{order, (size_t)a.T}, Span<uint64_t>{other, (size_t)a.T});
             if (e != cudaSuccess) return e;
             uint64_t* const swap = order;

@@ -25,13 +25,16 @@ struct DropArgs {                // see Drop in mhcs_common.cuh
     float scale;
 };
 
-// Launches a kernel that may start before the one ahead of it in the stream has
-// ended, and waits for it by itself (griddepcontrol.wait).
+// Launches a kernel whose blocks may start before the kernel ahead of it in the
+// stream has ended; each of these kernels waits for that one by itself
+// (griddepcontrol.wait) before its first global access.
 template <typename... Params, typename... Values>
-cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, Values... values) {
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t shared, cudaStream_t stream,
+                         Values... values) {
     cudaLaunchConfig_t config{};
     config.gridDim = grid;
     config.blockDim = block;
+    config.dynamicSmemBytes = shared;
     config.stream = stream;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -90,6 +90,7 @@ __device__ __forceinline__ float scalar_at(const Span<F>& s, int64_t i, uint32_t
 // Any row length: the row is read again for each pass (from L1 or L2).
 template <typename E, bool MIX, int N>
 __global__ void __launch_bounds__(kThreads) forward_any_kernel(Params<E> a) {
+    ptx::grid_dependency_wait();
     __shared__ float gate[kGates], scratch[32];
     const int64_t t = blockIdx.x;
     if constexpr (MIX) {
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) forward_any_kernel(Params<E> a) {
 // while others reduce or store.
 template <typename E, bool MIX, int N, int VPT>
 __global__ void __launch_bounds__(640) forward_rows_kernel(Params<E> a, int G, int R) {
+    ptx::grid_dependency_wait();
     __shared__ float sums[2][32];   // by warp of the block
     const int tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
     const int warp = tid >> 5, warp0 = group * (G >> 5), warps = G >> 5;
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
 #pragma unroll
     for (int k = 0; k < Shape::kSlots; ++k)
         if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::grid_dependency_wait();
     const auto fetch = [&](int t, int stage) {
         if (t < T) {
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.x_stride + (uint32_t)c0);
@@ -368,6 +371,7 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
 // One row per block: its input gradient (and the gates').
 template <typename E, bool MIX, int N>
 __global__ void __launch_bounds__(kThreads) backward_rows_any_kernel(Params<E> a) {
+    ptx::grid_dependency_wait();
     __shared__ float gate[kGates], scratch[4 * 32];
     const int64_t t = blockIdx.x;
     if constexpr (MIX) {
@@ -439,6 +443,7 @@ __global__ void __launch_bounds__(kThreads) backward_rows_any_kernel(Params<E> a
 // Partial parameter gradients: block (column block, part), a thread per column.
 template <typename E, bool MIX>
 __global__ void __launch_bounds__(kThreads) backward_columns_any_kernel(Params<E> a) {
+    ptx::grid_dependency_wait();
     const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t part = blockIdx.y;
     if (c >= a.D) return;
@@ -470,10 +475,10 @@ __global__ void __launch_bounds__(kThreads) backward_columns_any_kernel(Params<E
 // slots again (cheaper than holding u and w in registers), writes the
 // gradients and refills each slot as it leaves it.  The other groups of the
 // block compute while one waits.
-template <typename E, bool MIX, int VPT, int S>
+template <typename E, bool MIX, int VPT, int S, int MAX>
 struct RowsShape {
     static constexpr int N = Elem<E>::kPack;
-    static constexpr int kMaxThreads = 640;
+    static constexpr int kMaxThreads = MAX;   // 640: 96 registers a thread; 512: 128
     static constexpr int kArrays = MIX ? 2 * kStreams + 1 : 2;      // x, grad_y, residual gradient
     static constexpr int kStage = VPT * kArrays;                    // 16-byte slots of a row
     // Slot k of every thread of the block lies together, so that a warp's copy
@@ -491,10 +496,9 @@ struct RowsShape {
     }
 };
 
-template <typename E, bool MIX, int VPT, int S>
-__global__ void __launch_bounds__((RowsShape<E, MIX, VPT, S>::kMaxThreads), 1)
-    backward_rows_kernel(Params<E> a, int G, int R) {
-    using Shape = RowsShape<E, MIX, VPT, S>;
+template <typename E, bool MIX, int VPT, int S, int MAX>
+__global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int G, int R) {
+    using Shape = RowsShape<E, MIX, VPT, S, MAX>;
     constexpr int N = Shape::N, H = N / 2, P = Shape::kPitch, A = Shape::kArrays;
     constexpr int XA = MIX ? kStreams : 1;   // slots of a vector: x (XA), grad_y, residual gradient
     extern __shared__ uint4 slots[];
@@ -513,6 +517,7 @@ __global__ void __launch_bounds__((RowsShape<E, MIX, VPT, S>::kMaxThreads), 1)
 #pragma unroll
     for (int k = 0; k < Shape::kSlots; ++k)
         if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::grid_dependency_wait();
 
     // Element offset of row t of an array at this thread's first column, formed
     // where it is needed: cheaper than a 64-bit pointer per array kept and moved.
@@ -783,6 +788,7 @@ __global__ void __launch_bounds__((RowsShape<E, MIX, VPT, S>::kMaxThreads), 1)
 // and loads its part of a row directly.
 template <typename E, bool MIX, int VPT, int MAX>
 __global__ void __launch_bounds__(MAX, 1) backward_elements_kernel(Params<E> a, int G, int R) {
+    ptx::grid_dependency_wait();
     extern __shared__ float shared[];   // [R][2][2 or 6][32] sums, then [2][VPT][G] parameter gradients
     constexpr int XA = MIX ? kStreams : 1, kSums = MIX ? 2 + kStreams : 2;
     const int tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
@@ -985,8 +991,8 @@ bool forward_rows(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
     const int G = (int)((threads + 31) / 32 * 32);
     int R = 256 / G < 1 ? 1 : 256 / G;             // blocks of about 256 threads
     while (R > 1 && (p.T + R - 1) / R < kSms) --R; // but first a block per SM
-    forward_rows_kernel<E, MIX, N, VPT><<<(unsigned)((p.T + R - 1) / R), (unsigned)(G * R), 0, stream>>>(p, G, R);
-    *e = cudaGetLastError();
+    *e = launch_early(forward_rows_kernel<E, MIX, N, VPT>, dim3((unsigned)((p.T + R - 1) / R)), dim3((unsigned)(G * R)), 0,
+                      stream, p, G, R);
     return true;
 }
 
@@ -1006,8 +1012,7 @@ bool forward_ring(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
     auto kernel = forward_ring_kernel<E, MIX, VPT, S>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
-    kernel<<<(unsigned)grid, (unsigned)(G * R), shared, stream>>>(p, G, R);
-    *e = cudaGetLastError();
+    *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
     return true;
 }
 
@@ -1026,18 +1031,15 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
     } else if (forward_rows<E, MIX, 1, 4>(p, &e, stream) || forward_rows<E, MIX, 1, 16>(p, &e, stream)) {
         return e;
     }
-    if (packed && a.D % 8 == 0)
-        forward_any_kernel<E, MIX, 8><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
-    else
-        forward_any_kernel<E, MIX, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(packed && a.D % 8 == 0 ? forward_any_kernel<E, MIX, 8> : forward_any_kernel<E, MIX, 1>,
+                        dim3((unsigned)a.T), dim3(kThreads), 0, stream, p);
 }
 
 // Launches backward_rows_kernel where the row fits its shape; false otherwise.
 // *parts: the row groups it writes partial parameter gradients for.
-template <typename E, bool MIX, int VPT, int S>
+template <typename E, bool MIX, int VPT, int S, int MAX>
 bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStream_t stream) {
-    using Shape = RowsShape<E, MIX, VPT, S>;
+    using Shape = RowsShape<E, MIX, VPT, S, MAX>;
     const int64_t vectors = p.D / Shape::N, threads = (vectors + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
@@ -1051,11 +1053,10 @@ bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStrea
     if (shared > kMaxShared) return false;
     const int64_t grid = (p.T + R - 1) / R < blocks ? (p.T + R - 1) / R : blocks;
     *parts = grid;
-    auto kernel = backward_rows_kernel<E, MIX, VPT, S>;
+    auto kernel = backward_rows_kernel<E, MIX, VPT, S, MAX>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
-    kernel<<<(unsigned)grid, (unsigned)(G * R), shared, stream>>>(p, G, R);
-    *e = cudaGetLastError();
+    *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
     return true;
 }
 
@@ -1074,8 +1075,7 @@ bool backward_elements(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaS
     auto kernel = backward_elements_kernel<E, MIX, VPT, MAX>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
-    kernel<<<(unsigned)grid, (unsigned)(G * R), shared, stream>>>(p, G, R);
-    *e = cudaGetLastError();
+    *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
     return true;
 }
 
@@ -1091,9 +1091,11 @@ cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
         bool done = false;
         if (packed) {
             if constexpr (MIX)
-                done = backward_rows<E, true, 1, 2>(p, &p.parts, &e, stream) || backward_rows<E, true, 2, 1>(p, &p.parts, &e, stream);
+                done = backward_rows<E, true, 1, 2, 640>(p, &p.parts, &e, stream) ||
+                       backward_rows<E, true, 2, 1, 512>(p, &p.parts, &e, stream) ||
+                       backward_rows<E, true, 2, 1, 640>(p, &p.parts, &e, stream);
             else
-                done = backward_rows<E, false, 16 / N, 3>(p, &p.parts, &e, stream);
+                done = backward_rows<E, false, 16 / N, sizeof(E) == 4 ? 2 : 3, 640>(p, &p.parts, &e, stream);
         } else {
             if constexpr (MIX)
                 done = backward_elements<E, true, 4, 640>(p, &p.parts, &e, stream) ||
@@ -1103,20 +1105,16 @@ cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
                        backward_elements<E, false, 16, 512>(p, &p.parts, &e, stream);
         }
         if (!done) {
-            constexpr int W = 8;
-            if (packed && a.D % W == 0)
-                backward_rows_any_kernel<E, MIX, W><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
-            else
-                backward_rows_any_kernel<E, MIX, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(p);
-            if (params)
-                backward_columns_any_kernel<E, MIX>
-                    <<<dim3((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)p.parts), kThreads, 0, stream>>>(p);
-            e = cudaGetLastError();
+            e = launch_early(packed && a.D % 8 == 0 ? backward_rows_any_kernel<E, MIX, 8> : backward_rows_any_kernel<E, MIX, 1>,
+                             dim3((unsigned)a.T), dim3(kThreads), 0, stream, p);
+            if (e == cudaSuccess && params)
+                e = launch_early(backward_columns_any_kernel<E, MIX>,
+                                 dim3((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)p.parts), dim3(kThreads), 0, stream, p);
         }
         if (e != cudaSuccess) return e;
     }
     if (!params) return cudaSuccess;
-    return launch_early(reduce_parts_kernel, dim3((unsigned)((a.D + 31) / 32), 2), dim3(32, 16), stream, a.D, p.parts,
+    return launch_early(reduce_parts_kernel, dim3((unsigned)((a.D + 31) / 32), 2), dim3(32, 16), 0, stream, a.D, p.parts,
                         a.accumulate, p.partial, p.grad_gamma, p.grad_beta);
 }
 

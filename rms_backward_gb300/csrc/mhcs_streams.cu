@@ -11,6 +11,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
+#include "ptx.cuh"
 
 namespace mhcpb {
 namespace ops {
@@ -29,6 +30,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Any alignment and size: an element per thread and step.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) dropout_any_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
+    ptx::grid_dependency_wait();
     const DropKey key = drop_key(d);
     const int64_t step = (int64_t)gridDim.x * kThreads;
     for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n; e += step) {
@@ -44,6 +46,7 @@ __global__ void __launch_bounds__(kThreads) dropout_any_kernel(int64_t n, Span<c
 constexpr int kDropPacks = 2;
 template <typename E>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
+    ptx::grid_dependency_wait();
     constexpr int N = Elem<E>::kPack;
     const DropKey key = drop_key(d);
     const int64_t first = ((int64_t)blockIdx.x * kDropPacks * kThreads + threadIdx.x) * N;
@@ -93,6 +96,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads) update_forward_kernel(int64_t D, Span<const bf16> x,
                                                                   Span<const bf16> y, Span<const float> h,
                                                                   Drop d, Span<bf16> x_out) {
+    ptx::grid_dependency_wait();
     __shared__ float gate[kGates];
     const int64_t t = blockIdx.x;
     if (threadIdx.x < kGates) {
@@ -128,6 +132,7 @@ __global__ void __launch_bounds__(kThreads) update_backward_kernel(int64_t D, Sp
                                                                    Span<const bf16> y, Span<const float> h,
                                                                    Drop d, Span<const bf16> gout,
                                                                    Span<bf16> gy, Span<float> gh) {
+    ptx::grid_dependency_wait();
     __shared__ float post[kStreams];
     __shared__ float scratch[20 * 32];
     const int64_t t = blockIdx.x;
@@ -222,6 +227,7 @@ __device__ __forceinline__ void drop_eight(const Drop& d, const ShortPhilox& ran
 __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
     int64_t T, int64_t D, int tokens, int tiles, bool gates_aligned, Span<const bf16> x, Span<const bf16> y,
     Span<const float> h, Drop d, Span<bf16> x_out) {
+    ptx::grid_dependency_wait();
     constexpr int N = 8, H = 4;
     const int vectors = (int)(D / N);
     int64_t t;
@@ -270,9 +276,9 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
 // ... of it, VPT of them), its inputs copied S tokens ahead into per-thread
 // slots.  The token's 20 dot products are left in shared memory by each warp
 // and added up after the group's barrier, which the outputs do not wait for.
-template <int VPT, int S>
+template <int VPT, int S, int MAX>
 struct TokenShape {
-    static constexpr int kMaxThreads = 640;
+    static constexpr int kMaxThreads = MAX;            // 640: 96 registers a thread; 512: 128
     static constexpr int kArrays = 2 * kStreams + 1;   // x, grad_x_out, y
     static constexpr int kStage = VPT * kArrays;
     static constexpr int kPitch = kMaxThreads;
@@ -281,11 +287,11 @@ struct TokenShape {
         return (size_t)kPitch * S * kStage * 16 + (size_t)R * (G / 32 * S * 4 + 2 * kDots * (G / 32 | 1)) * 4;
     }
 };
-template <int VPT, int S>
-__global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
+template <int VPT, int S, int MAX>
+__global__ void __launch_bounds__(MAX, 1)
     update_backward_tokens_kernel(int T, int D, int G, int R, Span<const bf16> x, Span<const bf16> y,
                                   Span<const float> h, Drop d, Span<const bf16> gout, Span<bf16> gy, Span<float> gh) {
-    using Shape = TokenShape<VPT, S>;
+    using Shape = TokenShape<VPT, S, MAX>;
     constexpr int N = 8, P = Shape::kPitch, A = Shape::kArrays;
     extern __shared__ uint4 slots[];
     const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
@@ -301,6 +307,7 @@ __global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
 #pragma unroll
     for (int k = 0; k < S * Shape::kStage; ++k)
         if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::grid_dependency_wait();
 
     const auto fetch_vector = [&](uint4* dst, int t, int v) {
         const int c = c0 + v * step;
@@ -408,11 +415,11 @@ __global__ void __launch_bounds__((TokenShape<VPT, S>::kMaxThreads), 1)
 }
 
 // Launches update_backward_tokens_kernel where a token fits its shape.
-template <int VPT, int S>
+template <int VPT, int S, int MAX>
 bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, const Span<const bf16>& y,
                             const Span<const float>& h, const Drop& d, const Span<const bf16>& gout,
                             const Span<bf16>& gy, const Span<float>& gh, cudaError_t* e, cudaStream_t stream) {
-    using Shape = TokenShape<VPT, S>;
+    using Shape = TokenShape<VPT, S, MAX>;
     const int64_t threads = (D / 8 + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
@@ -423,12 +430,11 @@ bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, con
     while (R > 1 && Shape::bytes(G, R) > kMaxShared) --R;
     if (Shape::bytes(G, R) > kMaxShared) return false;
     const int64_t grid = (T + R - 1) / R < kSms ? (T + R - 1) / R : kSms;
-    auto kernel = update_backward_tokens_kernel<VPT, S>;
+    auto kernel = update_backward_tokens_kernel<VPT, S, MAX>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
-    kernel<<<(unsigned)grid, (unsigned)(G * R), Shape::bytes(G, R), stream>>>((int)T, (int)D, G, R, x, y, h, d, gout, gy,
-                                                                              gh);
-    *e = cudaGetLastError();
+    *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), Shape::bytes(G, R), stream, (int)T, (int)D, G,
+                      R, x, y, h, d, gout, gy, gh);
     return true;
 }
 
@@ -438,12 +444,12 @@ cudaError_t dropout_typed(int64_t n, const void* x, void* y, const Drop& d, cuda
     const Span<E> ys{static_cast<E*>(y), (size_t)n};
     if (aligned16(x) && aligned16(y) && n < kShortCounters) {
         const int64_t block = (int64_t)kThreads * Elem<E>::kPack * kDropPacks;
-        dropout_kernel<E><<<(unsigned)((n + block - 1) / block), kThreads, 0, stream>>>(n, xs, ys, d);
-    } else {
-        const int64_t blocks = (n + kThreads - 1) / kThreads;
-        dropout_any_kernel<E><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), kThreads, 0, stream>>>(n, xs, ys, d);
+        return launch_early(dropout_kernel<E>, dim3((unsigned)((n + block - 1) / block)), dim3(kThreads), 0, stream, n, xs,
+                            ys, d);
     }
-    return cudaGetLastError();
+    const int64_t blocks = (n + kThreads - 1) / kThreads;
+    return launch_early(dropout_any_kernel<E>, dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(kThreads), 0,
+                        stream, n, xs, ys, d);
 }
 
 }  // namespace
@@ -481,17 +487,12 @@ cudaError_t update_forward(int64_t T, int64_t D, const void* x, const void* y, c
             tiles = (int)((vectors + threads - 1) / threads);
         }
         const int64_t blocks = tiles > 1 ? T * tiles : (T + tokens - 1) / tokens;
-        if (blocks <= INT32_MAX) {
-            update_forward_vectors_kernel<<<(unsigned)blocks, threads, 0, stream>>>(T, D, tokens, tiles, gates_aligned,
-                                                                                    xs, ys, hs, d, os);
-            return cudaGetLastError();
-        }
+        if (blocks <= INT32_MAX)
+            return launch_early(update_forward_vectors_kernel, dim3((unsigned)blocks), dim3(threads), 0, stream, T, D, tokens,
+                                tiles, gates_aligned, xs, ys, hs, d, os);
     }
-    if (D % 8 == 0)
-        update_forward_kernel<8><<<(unsigned)T, kThreads, 0, stream>>>(D, xs, ys, hs, d, os);
-    else
-        update_forward_kernel<1><<<(unsigned)T, kThreads, 0, stream>>>(D, xs, ys, hs, d, os);
-    return cudaGetLastError();
+    return launch_early(D % 8 == 0 ? update_forward_kernel<8> : update_forward_kernel<1>, dim3((unsigned)T), dim3(kThreads),
+                        0, stream, D, xs, ys, hs, d, os);
 }
 
 cudaError_t update_backward(int64_t T, int64_t D, const void* x, const void* y, const float* h,
@@ -506,15 +507,13 @@ cudaError_t update_backward(int64_t T, int64_t D, const void* x, const void* y, 
     const Span<float> ghs{grad_h, (size_t)(T * kGates)};
     if (D % 8 == 0 && T * D < kShortCounters) {
         cudaError_t e = cudaSuccess;
-        if (update_backward_tokens<1, 2>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
-            update_backward_tokens<2, 1>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream))
+        if (update_backward_tokens<1, 2, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
+            update_backward_tokens<2, 1, 512>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
+            update_backward_tokens<2, 1, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream))
             return e;
     }
-    if (D % 8 == 0)
-        update_backward_kernel<8><<<(unsigned)T, kThreads, 0, stream>>>(D, xs, ys, hs, d, gs, gys, ghs);
-    else
-        update_backward_kernel<1><<<(unsigned)T, kThreads, 0, stream>>>(D, xs, ys, hs, d, gs, gys, ghs);
-    return cudaGetLastError();
+    return launch_early(D % 8 == 0 ? update_backward_kernel<8> : update_backward_kernel<1>, dim3((unsigned)T),
+                        dim3(kThreads), 0, stream, D, xs, ys, hs, d, gs, gys, ghs);
 }
 
 cudaError_t setup() { return cudaSuccess; }
