@@ -41,16 +41,19 @@ constexpr int kTile = 1024;          // tokens per tile when there are more
 constexpr int kRanked = 32;          // tokens a ranking block places, 8 threads each
 constexpr int kFan = 16;             // runs per merge pass
 constexpr int kBatch = 32;           // ordered tokens per listing of rows
-constexpr int kAhead = 8;            // rows copied ahead of the one being added
+constexpr int kAhead = 8;            // rows loaded ahead of the one being added
 constexpr int kZeroRows = 16;        // table rows per zeroing block, 4 a warp
 constexpr int kMaxChunks = 1024;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Ordered tokens per summing chunk: 32, or more where that would make over 1024 chunks.
+// Ordered tokens per summing chunk: T / 128 between 4 and 32, so that a short
+// batch too is spread over the GPU, and more where that would make over 1024.
 int64_t chunk_tokens(int64_t T) {
-    const int64_t c = (T + kMaxChunks - 1) / kMaxChunks;
-    return c < kBatch ? kBatch : (c + kBatch - 1) / kBatch * kBatch;
+    int64_t c = T / 128;
+    c = c < 4 ? 4 : c > kBatch ? kBatch : c;
+    const int64_t least = (T + kMaxChunks - 1) / kMaxChunks;
+    return c >= least ? c : (least + kBatch - 1) / kBatch * kBatch;
 }
 int64_t chunk_count(int64_t T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
 
@@ -136,38 +139,52 @@ __device__ __forceinline__ int64_t key_at(const Span<const uint64_t>& o, int64_t
     return (int64_t)(order_at(o, i, site) >> 32);
 }
 
-// 16 lanes per element, one for each run of its group.
-__global__ void __launch_bounds__(256) merge_runs_kernel(int64_t T, int64_t run, Span<const uint64_t> in,
+// 16 lanes per kMergeEach consecutive elements, one lane for each run of their
+// group; a lane searches for its elements side by side.
+constexpr int kMergeEach = 4;   // divides every run but the last
+__global__ void __launch_bounds__(256) merge_runs_kernel(int64_t T, int64_t run, int steps, Span<const uint64_t> in,
                                                          Span<uint64_t> out) {
-    const int64_t i = (int64_t)blockIdx.x * (256 / kFan) + threadIdx.x / kFan;
+    const int64_t i = ((int64_t)blockIdx.x * (256 / kFan) + threadIdx.x / kFan) * kMergeEach;
     const int r = threadIdx.x % kFan;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const bool valid = i < T;
-    const uint64_t v = valid ? order_at(in, i, 5) : 0;
     const int64_t group = i / (run * kFan) * (run * kFan), lo = group + r * run;
     const int64_t hi = lo + run < T ? lo + run : T;
-    int64_t below = 0;
-    if (valid && lo < T) {
+    uint64_t v[kMergeEach];
+    int64_t below[kMergeEach] = {};
+#pragma unroll
+    for (int e = 0; e < kMergeEach; ++e) v[e] = i + e < T ? order_at(in, i + e, 5) : 0;
+    if (lo < T && i < T) {
         if (i >= lo && i < hi) {
-            below = i - lo;
+#pragma unroll
+            for (int e = 0; e < kMergeEach; ++e) below[e] = i + e - lo;
         } else {
-            int64_t a = lo, n = hi - lo;
-            while (n > 0) {
-                const int64_t half = n / 2;
-                if (order_at(in, a + half, 5) < v) {
-                    a += half + 1;
-                    n -= half + 1;
-                } else {
-                    n = half;
-                }
+            int64_t a[kMergeEach], n[kMergeEach];   // the answer lies in [a, a + n]
+#pragma unroll
+            for (int e = 0; e < kMergeEach; ++e) {
+                a[e] = lo;
+                n[e] = hi - lo;
             }
-            below = a - lo;
+            for (int s = 0; s < steps; ++s)
+#pragma unroll
+                for (int e = 0; e < kMergeEach; ++e)
+                    if (n[e] > 0) {
+                        const int64_t half = n[e] / 2;
+                        const bool less = order_at(in, a[e] + half, 5) < v[e];
+                        a[e] = less ? a[e] + half + 1 : a[e];
+                        n[e] = less ? n[e] - half - 1 : half;
+                    }
+#pragma unroll
+            for (int e = 0; e < kMergeEach; ++e) below[e] = a[e] - lo;
         }
     }
 #pragma unroll
-    for (int o = kFan / 2; o > 0; o >>= 1) below += __shfl_xor_sync(kFullMask, below, o);
-    if (valid && r == 0 && out.has((size_t)(group + below), 1, 6)) out.p[group + below] = v;
+    for (int e = 0; e < kMergeEach; ++e) {
+#pragma unroll
+        for (int o = kFan / 2; o > 0; o >>= 1) below[e] += __shfl_xor_sync(kFullMask, below[e], o);
+        const int64_t place = group + below[e];
+        if (r == 0 && i + e < T && out.has((size_t)place, 1, 6)) out.p[place] = v[e];
+    }
 }
 
 // ------------------------------------------------------------ summing
@@ -291,22 +308,25 @@ __device__ __forceinline__ void flush(const SumArgs& a, RowWriter<N>& out, int64
 
 // Blocks 0 .. chunks * slabs - 1 sum; the others zero kZeroRows rows each.
 //
-// The rows of a batch of ordered tokens (each token's streams in turn) are
-// listed in shared memory with where runs end; a thread adds its N columns of
-// one row after another.  N = 8: the rows come through per-thread copies,
-// kAhead rows ahead; N = 1: kAhead loads are issued together.
+// The rows of a batch of ordered tokens are listed in shared memory, NS rows
+// (the streams of a token, or one row when n_streams is not 4) to an item,
+// with where runs end; a thread adds its N columns of one item after another.
+// N = 8: the rows come through per-thread copies, kAhead items of one row or
+// kAhead / 2 of four ahead; N = 1: kAhead loads are issued together.
 constexpr uint32_t kRunEnds = 1u << 31, kFlush = 1u << 30, kRowMask = kFlush - 1;   // T n_streams <= 2^28
-template <int N>
+template <int N, int NS>
 __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
     ptx::grid_dependency_wait();
     if ((int64_t)blockIdx.x >= a.chunks * a.slabs) {
         zero_rows<N>(a, ((int64_t)blockIdx.x - a.chunks * a.slabs) * kZeroRows);
         return;
     }
-    __shared__ uint32_t rows[kBatch * MHCPB_MAX_STREAMS];
+    constexpr int kItems = NS == 1 ? kAhead : kAhead / 2;
+    __shared__ uint32_t rows[kBatch * (NS == 1 ? MHCPB_MAX_STREAMS : 1)];
     __shared__ uint32_t ids[kBatch];
     __shared__ int listed;
-    __shared__ uint4 ring[N == 8 ? kAhead * kThreads : 1];
+    __shared__ uint4 ring[N == 8 ? kItems * NS * kThreads : 1];
+    const int per_token = NS == 1 ? a.n_streams : 1;   // items
     const int64_t chunk = blockIdx.x / a.slabs;
     const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * N;
     const int64_t begin = chunk * a.chunk;
@@ -326,73 +346,79 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
             const bool counts = in && key < a.V;   // ids outside the table come last
             const bool ends = next != key;
             const int valid = __popc(__ballot_sync(kFullMask, counts));
-            if (threadIdx.x == 0) listed = valid * a.n_streams;
+            if (threadIdx.x == 0) listed = valid * per_token;
             ids[threadIdx.x] = (uint32_t)key;
             if (counts)
-                for (int s = 0; s < a.n_streams; ++s) {
+                for (int s = 0; s < per_token; ++s) {
                     uint32_t row = (uint32_t)v * (uint32_t)a.n_streams + s;
-                    if (s + 1 == a.n_streams && (ends || at + 1 == end)) row |= kFlush | (ends ? kRunEnds : 0u);
-                    rows[threadIdx.x * a.n_streams + s] = row;
+                    if (s + 1 == per_token && (ends || at + 1 == end)) row |= kFlush | (ends ? kRunEnds : 0u);
+                    rows[threadIdx.x * per_token + s] = row;
                 }
         }
         __syncthreads();
         const int items = listed;
         if (items == 0) break;
+        int position = 0, part = 0;   // of the item: its token in the batch, its row of the token
+        const auto finish = [&](uint32_t row) {
+            if (row & kFlush) {
+                flush<N>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
+                began = true;
+            }
+            if (NS > 1 || ++part == per_token) {
+                part = 0;
+                ++position;
+            }
+        };
         if constexpr (N == 8) {
             uint4* const mine = ring + threadIdx.x;
             const auto fetch = [&](int item) {
                 if (item < items && c < a.D) {
                     const size_t at = (size_t)(rows[item] & kRowMask) * a.D + c;
-                    if (a.grad_x.has(at, N, 11)) copy16(mine + item % kAhead * kThreads, a.grad_x.p + at);
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+                        if (a.grad_x.has(at + s * a.D, N, 11))
+                            copy16(mine + (item % kItems * NS + s) * kThreads, a.grad_x.p + at + s * a.D);
                 }
                 copies_commit();
             };
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) fetch(q);
-            int position = 0, stream = 0;
+            for (int q = 0; q < kItems; ++q) fetch(q);
             for (int item = 0; item < items; ++item) {
-                copies_wait<kAhead - 1>();
-                float2 v[4];
-                unpack<bf16>(mine[item % kAhead * kThreads], v);
+                copies_wait<kItems - 1>();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[2 * k] += v[k].x;
-                    acc[2 * k + 1] += v[k].y;
+                for (int s = 0; s < NS; ++s) {
+                    float2 v[4];
+                    unpack<bf16>(mine[(item % kItems * NS + s) * kThreads], v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        acc[2 * k] += v[k].x;
+                        acc[2 * k + 1] += v[k].y;
+                    }
                 }
-                fetch(item + kAhead);
-                const uint32_t row = rows[item];
-                if (row & kFlush) {
-                    flush<N>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
-                    began = true;
-                }
-                if (++stream == a.n_streams) {
-                    stream = 0;
-                    ++position;
-                }
+                fetch(item + kItems);
+                finish(rows[item]);
             }
             copies_wait<0>();
         } else {
-            int position = 0, stream = 0;
-            for (int item = 0; item < items; item += kAhead) {
-                float v[kAhead][N];
+            constexpr int kTogether = NS == 1 ? kAhead : kAhead / NS;
+            for (int item = 0; item < items; item += kTogether) {
+                float v[kTogether][NS];
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q)
+                for (int q = 0; q < kTogether; ++q)
                     if (item + q < items && c < a.D)
-                        load_at<N>(a.grad_x, (size_t)(rows[item + q] & kRowMask) * a.D + c, v[q], 11);
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q)
+                        for (int s = 0; s < NS; ++s) {
+                            float one[1];
+                            load_at<1>(a.grad_x, ((size_t)(rows[item + q] & kRowMask) + s) * a.D + c, one, 11);
+                            v[q][s] = one[0];
+                        }
+#pragma unroll
+                for (int q = 0; q < kTogether; ++q)
                     if (item + q < items) {
+                        if (c < a.D)
 #pragma unroll
-                        for (int k = 0; k < N; ++k) acc[k] += v[q][k];
-                        const uint32_t row = rows[item + q];
-                        if (row & kFlush) {
-                            flush<N>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
-                            began = true;
-                        }
-                        if (++stream == a.n_streams) {
-                            stream = 0;
-                            ++position;
-                        }
+                            for (int s = 0; s < NS; ++s) acc[0] += v[q][s];
+                        finish(rows[item + q]);
                     }
             }
         }
@@ -416,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) join_runs_kernel(SumArgs a) {
     if (c >= a.D) return;
     float acc[N];
     load_floats<N>(a.pieces, (size_t)((chunk * 2 + 1) * a.D + c), acc, 15);
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t q = chunk + 1; q <= last; ++q) {
         float v[N];
         load_floats<N>(a.pieces, (size_t)(q * 2 * a.D + c), v, 15);
@@ -446,7 +472,7 @@ template <int N>
 cudaError_t sum_typed(SumArgs s, cudaStream_t stream) {
     s.slabs = (s.D + kThreads * N - 1) / (kThreads * N);
     const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
-    cudaError_t e = launch_early(sum_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
+    cudaError_t e = launch_early(s.n_streams == 4 ? sum_runs_kernel<N, 4> : sum_runs_kernel<N, 1>, dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
     return launch_early(join_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs)), dim3(kThreads), 0, stream, s);
 }
@@ -481,8 +507,11 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
                              Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out);
         if (e != cudaSuccess) return e;
         for (int64_t run = tile; run < a.T; run *= kFan) {
-            e = launch_early(merge_runs_kernel, dim3((unsigned)((a.T + 256 / kFan - 1) / (256 / kFan))), dim3(256), 0, stream, a.T, run,
-                             Span<const uint64_t>{order, (size_t)a.T}, Span<uint64_t>{other, (size_t)a.T});
+            int steps = 1;   // halvings that leave nothing of a run
+            while (((int64_t)1 << steps) <= run) ++steps;
+            const int64_t each = 256 / kFan * kMergeEach;
+            e = launch_early(merge_runs_kernel, dim3((unsigned)((a.T + each - 1) / each)), dim3(256), 0, stream, a.T, run,
+                             steps, Span<const uint64_t>{order, (size_t)a.T}, Span<uint64_t>{other, (size_t)a.T});
             if (e != cudaSuccess) return e;
             uint64_t* const swap = order;
             order = other;
