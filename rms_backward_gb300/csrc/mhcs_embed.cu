@@ -14,8 +14,7 @@
 // 17 M comparisons, a few microseconds on the whole GPU (a bitonic network in
 // one block took 37).  Above 4096 tokens the tiles have 1024, and passes merge
 // 16 sorted runs at a time: an element's place is its place in its own run
-// plus, for each other run, the number of smaller elements, found by one lane
-// per run.
+// plus, for each other run, the number of smaller elements.
 // Summing: the ordered tokens are cut into chunks; a block sums one chunk over
 // one slab of columns.  A run inside one chunk is written at once; the pieces
 // of a run that crosses chunks go to the workspace and a last kernel adds them
@@ -43,12 +42,13 @@ constexpr int kFan = 16;             // runs per merge pass
 constexpr int kBatch = 32;           // ordered tokens per listing of rows
 constexpr int kAhead = 8;            // rows loaded ahead of the one being added
 constexpr int kZeroRows = 16;        // table rows per zeroing block, 4 a warp
-constexpr int kMaxChunks = 1024;
+constexpr int kMaxChunks = 4096;
+constexpr int kJoinBlocks = 4 * 152;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Ordered tokens per summing chunk: T / 128 between 4 and 32, so that a short
-// batch too is spread over the GPU, and more where that would make over 1024.
+// batch too is spread over the GPU, and more where that would make over 4096.
 int64_t chunk_tokens(int64_t T) {
     int64_t c = T / 128;
     c = c < 4 ? 4 : c > kBatch ? kBatch : c;
@@ -58,6 +58,7 @@ int64_t chunk_tokens(int64_t T) {
 int64_t chunk_count(int64_t T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
 
 size_t order_bytes(int64_t T) { return ((size_t)T * 8 + 255) / 256 * 256; }
+size_t heads_bytes(int64_t T) { return ((size_t)(1 + chunk_count(T)) * 4 + 255) / 256 * 256; }
 
 template <typename I>
 __device__ __forceinline__ int64_t id_at(const Span<const I>& ids, int64_t t, int64_t V, uint32_t site) {
@@ -92,11 +93,12 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(int64_t V, int64_t D, 
 // (id, t) as one 64-bit number; ids outside the table come last, as id V
 template <typename I>
 __global__ void __launch_bounds__(256) rank_kernel(int64_t T, int64_t V, int tile, Span<const I> ids,
-                                                   Span<uint64_t> order) {
+                                                   Span<uint64_t> order, uint32_t* heads) {
     __shared__ uint4 quads[kOneTile / 4];
     uint32_t* const keys = reinterpret_cast<uint32_t*>(quads);
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *heads = 0;   // for the summing kernel
     const int blocks_per_tile = tile / kRanked;
     const int64_t base = (int64_t)(blockIdx.x / blocks_per_tile) * tile;
     const int n = (int)(T - base < tile ? T - base : tile), padded = (n + 31) / 32 * 32;
@@ -139,52 +141,91 @@ __device__ __forceinline__ int64_t key_at(const Span<const uint64_t>& o, int64_t
     return (int64_t)(order_at(o, i, site) >> 32);
 }
 
-// 16 lanes per kMergeEach consecutive elements, one lane for each run of their
-// group; a lane searches for its elements side by side.
-constexpr int kMergeEach = 4;   // divides every run but the last
-__global__ void __launch_bounds__(256) merge_runs_kernel(int64_t T, int64_t run, int steps, Span<const uint64_t> in,
-                                                         Span<uint64_t> out) {
-    const int64_t i = ((int64_t)blockIdx.x * (256 / kFan) + threadIdx.x / kFan) * kMergeEach;
-    const int r = threadIdx.x % kFan;
+// Places kMergePlaced consecutive elements in the merge of their group of 16
+// runs.  The runs hold consecutive tokens, so an equal id counts when its run
+// comes before the element's.  The block searches kSamples ids of every run in
+// shared memory, then what lies between two of them in global memory (with
+// 1024 samples, reading them cost more than the two halvings they save).
+constexpr int kSamples = 256;         // per run; divides every run but the last
+constexpr int kSamplePitch = kSamples + 1;   // the 16 runs' searches start at the same place: in 16 banks
+constexpr int kMergeThreads = 512;
+constexpr int kMergePlaced = 256;
+constexpr int kMergeSide = 4;         // searches of a thread side by side
+constexpr size_t kMergeShared = (size_t)kFan * kSamplePitch * 4 + kMergePlaced * 8;
+__global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(int64_t T, int64_t run, Span<const uint64_t> in,
+                                                                   Span<uint64_t> out) {
+    extern __shared__ uint32_t samples[];   // [kFan][kSamplePitch], then the places
+    uint64_t* const places = reinterpret_cast<uint64_t*>(samples + kFan * kSamplePitch);
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const int64_t group = i / (run * kFan) * (run * kFan), lo = group + r * run;
-    const int64_t hi = lo + run < T ? lo + run : T;
-    uint64_t v[kMergeEach];
-    int64_t below[kMergeEach] = {};
+    const int64_t first = (int64_t)blockIdx.x * kMergePlaced, group = first / (run * kFan) * (run * kFan);
+    const int64_t stride = run / kSamples;
+#pragma unroll 8
+    for (int k = threadIdx.x; k < kFan * kSamples; k += kMergeThreads) {
+        const int64_t at = group + k / kSamples * run + k % kSamples * stride;
+        samples[k / kSamples * kSamplePitch + k % kSamples] = at < T ? (uint32_t)key_at(in, at, 5) : 0xffffffffu;
+    }
+    for (int k = threadIdx.x; k < kMergePlaced; k += kMergeThreads) places[k] = 0;
+    __syncthreads();
+    // thread: run r of elements e, e + kMergeThreads / kFan, ...
+    const int r = threadIdx.x % kFan;
+    const int64_t lo = group + r * run;
+    const int64_t length = lo >= T ? 0 : lo + run < T ? run : T - lo;
+    const int sampled = (int)((length + stride - 1) / stride);
+    constexpr int kElements = kMergeThreads / kFan;
+    for (int base = threadIdx.x / kFan; base < kMergePlaced; base += kElements * kMergeSide) {
+        uint32_t bound[kMergeSide];
+        int a[kMergeSide], n[kMergeSide];   // samples below the bound: in [a, a + n]
+        int64_t below[kMergeSide];
 #pragma unroll
-    for (int e = 0; e < kMergeEach; ++e) v[e] = i + e < T ? order_at(in, i + e, 5) : 0;
-    if (lo < T && i < T) {
-        if (i >= lo && i < hi) {
+        for (int s = 0; s < kMergeSide; ++s) {
+            const int64_t i = first + base + s * kElements;
+            const uint32_t key = i < T ? (uint32_t)key_at(in, i, 5) : 0u;
+            bound[s] = lo + run <= i ? key + 1 : key;
+            a[s] = 0;
+            n[s] = sampled;
+        }
+#pragma unroll 1
+        for (int step = kSamples; step > 0; step >>= 1)
 #pragma unroll
-            for (int e = 0; e < kMergeEach; ++e) below[e] = i + e - lo;
-        } else {
-            int64_t a[kMergeEach], n[kMergeEach];   // the answer lies in [a, a + n]
+            for (int s = 0; s < kMergeSide; ++s)
+                if (n[s] > 0) {
+                    const int half = n[s] >> 1;
+                    const bool less = samples[r * kSamplePitch + a[s] + half] < bound[s];
+                    a[s] = less ? a[s] + half + 1 : a[s];
+                    n[s] = less ? n[s] - half - 1 : half;
+                }
 #pragma unroll
-            for (int e = 0; e < kMergeEach; ++e) {
-                a[e] = lo;
-                n[e] = hi - lo;
-            }
-            for (int s = 0; s < steps; ++s)
-#pragma unroll
-                for (int e = 0; e < kMergeEach; ++e)
-                    if (n[e] > 0) {
-                        const int64_t half = n[e] / 2;
-                        const bool less = order_at(in, a[e] + half, 5) < v[e];
-                        a[e] = less ? a[e] + half + 1 : a[e];
-                        n[e] = less ? n[e] - half - 1 : half;
+        for (int s = 0; s < kMergeSide; ++s) {
+            const int64_t i = first + base + s * kElements;
+            if (i >= lo && i < lo + run) {
+                below[s] = i - lo;   // its own run
+            } else if (a[s] == 0) {
+                below[s] = 0;
+            } else {
+                int64_t from = (a[s] - 1) * stride + 1, left = a[s] * stride < length ? stride - 1 : length - from;
+                while (left > 0) {
+                    const int64_t half = left / 2;
+                    if ((uint32_t)key_at(in, lo + from + half, 5) < bound[s]) {
+                        from += half + 1;
+                        left -= half + 1;
+                    } else {
+                        left = half;
                     }
+                }
+                below[s] = from;
+            }
+        }
 #pragma unroll
-            for (int e = 0; e < kMergeEach; ++e) below[e] = a[e] - lo;
+        for (int s = 0; s < kMergeSide; ++s) {
+#pragma unroll
+            for (int o = kFan / 2; o > 0; o >>= 1) below[s] += __shfl_xor_sync(kFullMask, below[s], o);
+            if (r == 0) places[base + s * kElements] = (uint64_t)(group + below[s]);
         }
     }
-#pragma unroll
-    for (int e = 0; e < kMergeEach; ++e) {
-#pragma unroll
-        for (int o = kFan / 2; o > 0; o >>= 1) below[e] += __shfl_xor_sync(kFullMask, below[e], o);
-        const int64_t place = group + below[e];
-        if (r == 0 && i + e < T && out.has((size_t)place, 1, 6)) out.p[place] = v[e];
-    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < kMergePlaced; k += kMergeThreads)
+        if (first + k < T && out.has((size_t)places[k], 1, 6)) out.p[places[k]] = order_at(in, first + k, 5);
 }
 
 // ------------------------------------------------------------ summing
@@ -213,6 +254,7 @@ struct SumArgs {
     Span<const bf16> grad_x;
     Span<const uint64_t> order;
     Span<float> table;
+    Span<uint32_t> heads; // count, then the chunks in which a run begins that goes on after them, in any order
     Span<float> pieces;   // [chunks][2][D]: of the run that began before the chunk, and of the one that goes on after it
 };
 
@@ -301,6 +343,10 @@ __device__ __forceinline__ void flush(const SumArgs& a, RowWriter<N>& out, int64
             out.write(a, key, c, acc);
         else
             store_floats<N>(a.pieces, (size_t)((chunk * 2 + (began ? 1 : 0)) * a.D + c), acc, 13);
+        if (!whole && began && c == 0) {
+            const uint32_t at = 1 + atomicAdd(a.heads.p, 1u);
+            if (a.heads.has(at, 1, 17)) a.heads.p[at] = (uint32_t)chunk;
+        }
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
@@ -426,32 +472,51 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
     out.complete(a, c);
 }
 
-// Block (chunk, slab): if a run begins in this chunk and goes on after it,
-// adds its pieces in order.
+// Adds the pieces of each run that crosses chunks, over one slab of columns at
+// a time: each of kJoinParts groups of threads a part of them in order, then
+// the parts in order.
+constexpr int kJoinParts = 4;
 template <int N>
-__global__ void __launch_bounds__(kThreads) join_runs_kernel(SumArgs a) {
+__global__ void __launch_bounds__(kThreads * kJoinParts) join_runs_kernel(SumArgs a) {
+    __shared__ float sums[kJoinParts - 1][N][kThreads];
     ptx::grid_dependency_wait();
-    const int64_t chunk = blockIdx.x / a.slabs;
-    const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * N;
-    const int64_t begin = chunk * a.chunk;
-    const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
-    const int64_t key = key_at(a.order, end - 1, 14), next = end < a.T ? key_at(a.order, end, 14) : -1;
-    const int64_t previous = begin > 0 ? key_at(a.order, begin - 1, 14) : -1;
-    if (key >= a.V || next != key || previous == key) return;
-    const int64_t last = (lower_bound_warp(a.order, a.T, key + 1) - 1) / a.chunk;   // the chunk it ends in
-    if (c >= a.D) return;
-    float acc[N];
-    load_floats<N>(a.pieces, (size_t)((chunk * 2 + 1) * a.D + c), acc, 15);
-#pragma unroll 8
-    for (int64_t q = chunk + 1; q <= last; ++q) {
-        float v[N];
-        load_floats<N>(a.pieces, (size_t)(q * 2 * a.D + c), v, 15);
+    const int lane = threadIdx.x % kThreads, part = threadIdx.x / kThreads;
+    const int64_t work = (int64_t)a.heads.p[0] * a.slabs;
+    for (int64_t item = blockIdx.x; item < work; item += gridDim.x) {
+        const size_t head = 1 + (size_t)(item / a.slabs);
+        const int64_t chunk = a.heads.has(head, 1, 17) ? a.heads.p[head] : 0;
+        const int64_t c = (item % a.slabs * kThreads + lane) * N;
+        const int64_t key = key_at(a.order, (chunk + 1) * a.chunk - 1, 14);
+        // piece 0 is this chunk's; then one for each next chunk that begins with the id
+        int64_t count = 1;
+        for (int more = kThreads * kJoinParts; more == kThreads * kJoinParts; count += more) {
+            const int64_t at = (chunk + count + (int)threadIdx.x) * a.chunk;
+            more = __syncthreads_count(at < a.T && key_at(a.order, at, 14) == key);
+        }
+        float acc[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] += v[k];
+        for (int k = 0; k < N; ++k) acc[k] = 0.f;
+        if (c < a.D)
+#pragma unroll 8
+            for (int64_t q = count * part / kJoinParts; q < count * (part + 1) / kJoinParts; ++q) {
+                float v[N];
+                load_floats<N>(a.pieces, (size_t)(((chunk + q) * 2 + (q == 0 ? 1 : 0)) * a.D + c), v, 15);
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k] += v[k];
+            }
+        if (part > 0)   // the barriers above: the sums of the item before have been read
+#pragma unroll
+            for (int k = 0; k < N; ++k) sums[part - 1][k][lane] = acc[k];
+        __syncthreads();
+        if (part > 0 || c >= a.D) continue;
+#pragma unroll
+        for (int p = 0; p < kJoinParts - 1; ++p)
+#pragma unroll
+            for (int k = 0; k < N; ++k) acc[k] += sums[p][k][lane];
+        RowWriter<N> out;
+        out.write(a, key, c, acc);
+        out.complete(a, c);
     }
-    RowWriter<N> out;
-    out.write(a, key, c, acc);
-    out.complete(a, c);
 }
 
 template <typename E, typename I>
@@ -474,14 +539,15 @@ cudaError_t sum_typed(SumArgs s, cudaStream_t stream) {
     const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
     cudaError_t e = launch_early(s.n_streams == 4 ? sum_runs_kernel<N, 4> : sum_runs_kernel<N, 1>, dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
-    return launch_early(join_runs_kernel<N>, dim3((unsigned)(s.chunks * s.slabs)), dim3(kThreads), 0, stream, s);
+    const int64_t most = s.chunks * s.slabs < kJoinBlocks ? s.chunks * s.slabs : kJoinBlocks;
+    return launch_early(join_runs_kernel<N>, dim3((unsigned)most), dim3(kThreads * kJoinParts), 0, stream, s);
 }
 
 }  // namespace
 
 size_t workspace_bytes(int64_t T, int64_t /*V*/, int64_t D) {
     if (T == 0) return 0;
-    return 2 * order_bytes(T) + (size_t)chunk_count(T) * 2 * (size_t)D * sizeof(float);
+    return 2 * order_bytes(T) + heads_bytes(T) + (size_t)chunk_count(T) * 2 * (size_t)D * sizeof(float);
 }
 
 cudaError_t forward(const Args& a, cudaStream_t stream) {
@@ -499,19 +565,18 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
         const int tile = a.T <= kOneTile ? kOneTile : kTile;
         const unsigned blocks = (unsigned)((a.T + kRanked - 1) / kRanked);
         const Span<uint64_t> out{order, (size_t)a.T};
+        uint32_t* const heads = reinterpret_cast<uint32_t*>(ws + 2 * order_bytes(a.T));
         if (a.id_bytes == 8)
             e = launch_early(rank_kernel<int64_t>, dim3(blocks), dim3(256), 0, stream, a.T, a.V, tile,
-                             Span<const int64_t>{static_cast<const int64_t*>(a.ids), (size_t)a.T}, out);
+                             Span<const int64_t>{static_cast<const int64_t*>(a.ids), (size_t)a.T}, out, heads);
         else
             e = launch_early(rank_kernel<int32_t>, dim3(blocks), dim3(256), 0, stream, a.T, a.V, tile,
-                             Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out);
+                             Span<const int32_t>{static_cast<const int32_t*>(a.ids), (size_t)a.T}, out, heads);
         if (e != cudaSuccess) return e;
         for (int64_t run = tile; run < a.T; run *= kFan) {
-            int steps = 1;   // halvings that leave nothing of a run
-            while (((int64_t)1 << steps) <= run) ++steps;
-            const int64_t each = 256 / kFan * kMergeEach;
-            e = launch_early(merge_runs_kernel, dim3((unsigned)((a.T + each - 1) / each)), dim3(256), 0, stream, a.T, run,
-                             steps, Span<const uint64_t>{order, (size_t)a.T}, Span<uint64_t>{other, (size_t)a.T});
+            e = launch_early(merge_runs_kernel, dim3((unsigned)((a.T + kMergePlaced - 1) / kMergePlaced)), dim3(kMergeThreads),
+                             kMergeShared, stream, a.T, run, Span<const uint64_t>{order, (size_t)a.T},
+                             Span<uint64_t>{other, (size_t)a.T});
             if (e != cudaSuccess) return e;
             uint64_t* const swap = order;
             order = other;
@@ -530,13 +595,16 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
     s.grad_x = Span<const bf16>{static_cast<const bf16*>(a.grad_x), (size_t)(a.T * a.n_streams * a.D)};
     s.order = Span<const uint64_t>{order, (size_t)a.T};
     s.table = Span<float>{a.grad_table, (size_t)(a.V * a.D)};
-    s.pieces = Span<float>{reinterpret_cast<float*>(ws + 2 * order_bytes(a.T)), (size_t)(s.chunks * 2 * a.D)};
+    s.heads = Span<uint32_t>{reinterpret_cast<uint32_t*>(ws + 2 * order_bytes(a.T)), (size_t)(1 + s.chunks)};
+    s.pieces = Span<float>{reinterpret_cast<float*>(ws + 2 * order_bytes(a.T) + heads_bytes(a.T)), (size_t)(s.chunks * 2 * a.D)};
     if (a.T == 0 && a.accumulate) return cudaSuccess;
     if (a.D % 8 == 0 && aligned16(a.grad_x) && aligned16(a.grad_table)) return sum_typed<8>(s, stream);
     return sum_typed<1>(s, stream);
 }
 
-cudaError_t setup() { return cudaSuccess; }
+cudaError_t setup() {
+    return cudaFuncSetAttribute(merge_runs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMergeShared);
+}
 cudaError_t checked_site(uint32_t* site) { return check::read_and_clear(site); }
 
 }  // namespace embed

@@ -27,7 +27,8 @@ def test_embed_forward(T, V, D, n, type_, wide):
 
 
 @pytest.mark.parametrize("T,V,D,n", [(1, 1, 1, 1), (1, 70, 8, 4), (31, 33, 72, 4), (33, 5, 1285, 1), (500, 2000, 40, 4),
-                                     (4096, 37, 16, 2), (4097, 5000, 8, 1), (9001, 64, 3, 4), (70000, 900, 8, 1)])
+                                     (4096, 37, 16, 2), (4097, 5000, 8, 1), (9001, 64, 3, 4), (70000, 900, 8, 1),
+                                     (16385, 100000, 8, 1), (300000, 5000, 1, 1)])   # one, two and three merges
 @pytest.mark.parametrize("wide,accumulate", [(True, False), (False, True)])
 def test_embed_backward(T, V, D, n, wide, accumulate):
     C.embed_backward_case(T, V, D, n, wide, accumulate, seed=T + D)
