@@ -185,6 +185,49 @@ __device__ __forceinline__ void store_at(const Span<E>& s, size_t i, const float
     if (s.has(i, N, site)) store<E, N>(s.p + i, v);
 }
 
+// One thread per vector of a row, without loops: a block holds several whole
+// rows, or one of the tiles of a longer one, whichever leaves few threads idle.
+struct VectorPlace {
+    int64_t token;
+    int vector;
+    bool valid;           // the thread has a vector (of a token below T)
+    bool before, after;   // the lanes below and above hold the vectors next to it in the row
+};
+struct VectorGrid {
+    int vectors, threads, tokens, tiles;
+    VectorGrid(int64_t per_row, int most) : vectors((int)per_row), threads(most), tokens(1), tiles(1) {
+        if (per_row <= most / 2) {
+            tokens = most / vectors;
+            return;
+        }
+        int64_t least = INT64_MAX;
+        for (int w = 128; w <= most; w += 32) {
+            const int64_t used = (per_row + w - 1) / w * w;
+            if (used <= least) {
+                least = used;
+                threads = w;
+            }
+        }
+        tiles = (int)((per_row + threads - 1) / threads);
+    }
+    unsigned blocks(int64_t T) const { return (unsigned)(tiles > 1 ? T * tiles : (T + tokens - 1) / tokens); }
+    __device__ __forceinline__ VectorPlace place(int64_t T) const {
+        VectorPlace p;
+        if (tiles == 1) {
+            p.token = (int64_t)blockIdx.x * tokens + threadIdx.x / vectors;
+            p.vector = (int)(threadIdx.x % vectors);
+            p.valid = threadIdx.x < tokens * vectors && p.token < T;
+        } else {
+            p.token = blockIdx.x / tiles;
+            p.vector = (int)(blockIdx.x % tiles) * (int)blockDim.x + (int)threadIdx.x;
+            p.valid = p.vector < vectors;
+        }
+        p.before = (threadIdx.x & 31) > 0 && p.vector > 0;
+        p.after = (threadIdx.x & 31) < 31 && p.vector + 1 < vectors;
+        return p;
+    }
+};
+
 // ------------------------------------------------------------ generator
 // Philox4x32 with 10 rounds (Salmon, Moraes, Dror and Shaw, "Parallel random
 // numbers: as easy as 1, 2, 3", SC 2011): a 128-bit counter and a 64-bit key

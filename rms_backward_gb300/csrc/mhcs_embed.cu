@@ -25,6 +25,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
+#include "mhcs_shift.cuh"
 #include "ptx.cuh"
 
 namespace mhcpb {
@@ -35,6 +36,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 128;
+constexpr int kLookupThreads = 256;
 constexpr int kOneTile = 4096;       // tokens ordered in one tile
 constexpr int kTile = 1024;          // tokens per tile when there are more
 constexpr int kRanked = 32;          // tokens a ranking block places, 8 threads each
@@ -57,6 +59,7 @@ int64_t chunk_tokens(int64_t T) {
 }
 int64_t chunk_count(int64_t T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
 
+int64_t piece_pitch(int64_t D) { return (D + 7) / 8 * 8; }
 size_t order_bytes(int64_t T) { return ((size_t)T * 8 + 255) / 256 * 256; }
 size_t heads_bytes(int64_t T) { return ((size_t)(1 + chunk_count(T)) * 4 + 255) / 256 * 256; }
 
@@ -68,24 +71,46 @@ __device__ __forceinline__ int64_t id_at(const Span<const I>& ids, int64_t t, in
 }
 
 // ------------------------------------------------------------ forward
-template <typename E, typename I, int N>
-__global__ void __launch_bounds__(kThreads) lookup_kernel(int64_t V, int64_t D, int n_streams, float scale,
-                                                          Span<const E> table, Span<const I> ids,
-                                                          Span<bf16> x) {
+// Eight columns per thread; SHIFT: rows at any address, D of any size.
+template <typename E, typename I, bool SHIFT>
+__global__ void __launch_bounds__(kLookupThreads) lookup_kernel(int64_t T, int64_t V, int64_t D, VectorGrid grid,
+                                                                int n_streams, float scale, Span<const E> table,
+                                                                Span<const I> ids, Span<bf16> x) {
     ptx::grid_dependency_wait();
-    const int64_t t = blockIdx.x;
-    const int64_t id = id_at(ids, t, V, 0);
-    for (int64_t c = (int64_t)threadIdx.x * N; c < D; c += kThreads * N) {
-        float v[N];
-        if (id < V) {
-            load_at<N>(table, (size_t)(id * D + c), v, 1);
+    constexpr int N = 8, kParts = N / Elem<E>::kPack, H = Elem<E>::kPack / 2;
+    const VectorPlace place = grid.place(T);
+    const int64_t t = place.token;
+    const int c = place.vector * N, valid = place.valid ? (int)D - c : 0;
+    if (!SHIFT && valid <= 0) return;
+    const int64_t id = valid > 0 ? id_at(ids, t, V, 0) : V;
+    float2 v[N / 2];
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] *= scale;
-        } else {
+    for (int k = 0; k < N / 2; ++k) v[k] = pair(0.f);
+    if (id < V) {
+        const size_t at = (size_t)(id * D + c);
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = 0.f;
+        for (int q = 0; q < kParts; ++q) {
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            const size_t piece = at + q * Elem<E>::kPack;
+            if constexpr (SHIFT) {
+                if (valid > q * Elem<E>::kPack) raw = load_shifted(table, piece, valid - q * Elem<E>::kPack, 1);
+            } else {
+                if (table.has(piece, Elem<E>::kPack, 1)) raw = *reinterpret_cast<const uint4*>(table.p + piece);
+            }
+            float2 f[H];
+            unpack<E>(raw, f);
+#pragma unroll
+            for (int k = 0; k < H; ++k) v[q * H + k] = mul2(f[k], pair(scale));
         }
-        for (int s = 0; s < n_streams; ++s) store_at<N>(x, (size_t)((t * n_streams + s) * D + c), v, 2);
+    }
+    const uint4 out = pack<bf16>(v);
+    for (int s = 0; s < n_streams; ++s) {
+        const size_t at = (size_t)((t * n_streams + s) * D + c);
+        if constexpr (SHIFT) {
+            store_shifted(x, at, valid, place.before, place.after, out, 2);
+        } else {
+            if (x.has(at, N, 2)) *reinterpret_cast<uint4*>(x.p + at) = out;
+        }
     }
 }
 
@@ -246,8 +271,11 @@ __device__ __forceinline__ int64_t lower_bound_warp(const Span<const uint64_t>& 
     return lo;
 }
 
+// A thread's columns: eight of a row.  SHIFT: rows of grad_x and of the table at
+// any address (mhcs_shift.cuh); the workspace's rows have a pitch of whole
+// vectors.
 struct SumArgs {
-    int64_t T, V, D, chunk, chunks, slabs;
+    int64_t T, V, D, pitch, chunk, chunks, slabs;
     int n_streams;
     float scale;
     bool accumulate;
@@ -255,39 +283,92 @@ struct SumArgs {
     Span<const uint64_t> order;
     Span<float> table;
     Span<uint32_t> heads; // count, then the chunks in which a run begins that goes on after them, in any order
-    Span<float> pieces;   // [chunks][2][D]: of the run that began before the chunk, and of the one that goes on after it
+    Span<float> pieces;   // [chunks][2][pitch]: of the run that began before the chunk, and of the one that goes on after it
 };
+constexpr int N = 8;
 
-// FP32 row pieces: 32-byte accesses where the address allows them (two of 16
+// Eight FP32 values: one 32-byte access where the address allows it (two of 16
 // bytes, 32 apart, touch every sector twice).
-template <int N>
 __device__ __forceinline__ void load_floats(const Span<float>& s, size_t at, float (&v)[N], uint32_t site) {
-    if (N == 8 && (reinterpret_cast<uintptr_t>(s.p + at) & 31u) == 0 && s.has(at, N, site)) {
+    if ((reinterpret_cast<uintptr_t>(s.p + at) & 31u) == 0 && s.has(at, N, site)) {
         asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=f"(v[0]), "=f"(v[1 % N]), "=f"(v[2 % N]), "=f"(v[3 % N]), "=f"(v[4 % N]), "=f"(v[5 % N]),
-                       "=f"(v[6 % N]), "=f"(v[7 % N])
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                      : "l"(s.p + at)
                      : "memory");
     } else {
         load_at<N>(s, at, v, site);
     }
 }
-template <int N>
 __device__ __forceinline__ void store_floats(const Span<float>& s, size_t at, const float (&v)[N], uint32_t site) {
-    if (N == 8 && (reinterpret_cast<uintptr_t>(s.p + at) & 31u) == 0) {
+    if ((reinterpret_cast<uintptr_t>(s.p + at) & 31u) == 0) {
         if (s.has(at, N, site))
-            asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(s.p + at), "f"(v[0]), "f"(v[1 % N]),
-                         "f"(v[2 % N]), "f"(v[3 % N]), "f"(v[4 % N]), "f"(v[5 % N]), "f"(v[6 % N]), "f"(v[7 % N])
+            asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(s.p + at), "f"(v[0]), "f"(v[1]),
+                         "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                          : "memory");
     } else {
         store_at<N>(s, at, v, site);
     }
 }
+// The same for rows at any address: all lanes of a warp, lane l holding columns
+// c + 8 l ..., `valid` of them in the row.  As store_shifted, with two 16-byte
+// vectors per lane: two whole chunks, then what the next lane's first covers.
+__device__ __forceinline__ void store_floats_shifted(const Span<float>& s, size_t at, int valid, const float (&v)[N],
+                                                     uint32_t site) {
+    const auto word = [](const float* f) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    };
+    const int lane = threadIdx.x & 31;
+    const uint4 a = word(v), b = word(v + 4);
+    uint4 low;
+    low.x = __shfl_up_sync(kFullMask, b.x, 1);
+    low.y = __shfl_up_sync(kFullMask, b.y, 1);
+    low.z = __shfl_up_sync(kFullMask, b.z, 1);
+    low.w = __shfl_up_sync(kFullMask, b.w, 1);
+    if (valid <= 0) return;
+    const int m = misaligned(s.p + at), head = 4 - m;
+    const bool first = (m == 0 || lane > 0) && valid >= head, second = valid >= 4 + head;
+    if (first && s.has(at - m, 4, site))
+        *reinterpret_cast<uint4*>(s.p + at - m) = m == 0 ? a : shift_take<float>(low, a, head);
+    if (second && s.has(at + head, 4, site))
+        *reinterpret_cast<uint4*>(s.p + at + head) = m == 0 ? b : shift_take<float>(a, b, head);
+    // the lane above covers the last m, if its first chunk is whole
+    const bool rest = m > 0 && second && !(lane < 31 && valid - N >= head);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const bool covered = k < head ? first : k < 4 + head ? second : !rest && second;
+        if (!covered && k < valid && s.has(at + k, 1, site)) s.p[at + k] = v[k];
+    }
+}
+template <bool SHIFT>
+__device__ __forceinline__ void load_row(const SumArgs& a, size_t at, int valid, float (&v)[N], uint32_t site) {
+    if constexpr (!SHIFT) {
+        if (valid > 0) load_floats(a.table, at, v, site);
+    } else {
+        const Span<const float> in{a.table.p, a.table.count};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float2 f[2] = {pair(0.f), pair(0.f)};
+            if (valid > 4 * q) unpack<float>(load_shifted(in, at + 4 * q, valid - 4 * q, site), f);
+            v[4 * q] = f[0].x;
+            v[4 * q + 1] = f[0].y;
+            v[4 * q + 2] = f[1].x;
+            v[4 * q + 3] = f[1].y;
+        }
+    }
+}
+template <bool SHIFT>
+__device__ __forceinline__ void store_row(const SumArgs& a, size_t at, int valid, const float (&v)[N], uint32_t site) {
+    if constexpr (!SHIFT) {
+        if (valid > 0) store_floats(a.table, at, v, site);
+    } else {
+        store_floats_shifted(a.table, at, valid, v, site);
+    }
+}
 
 // A finished row of the gradient.  When accumulating, its old values are read
 // when the row is finished and added when the next one is (or at the end), so
-// that the read's latency is not waited for.
-template <int N>
+// that the read's latency is not waited for.  All lanes of a warp call it.
+template <bool SHIFT>
 struct RowWriter {
     int64_t key = -1;
     float sum[N], old[N];
@@ -295,58 +376,62 @@ struct RowWriter {
         if (key < 0) return;
 #pragma unroll
         for (int k = 0; k < N; ++k) old[k] = fmaf(a.scale, sum[k], old[k]);
-        store_floats<N>(a.table, (size_t)(key * a.D + c), old, 12);
+        store_row<SHIFT>(a, (size_t)(key * a.D + c), (int)(a.D - c), old, 12);
         key = -1;
     }
     __device__ __forceinline__ void write(const SumArgs& a, int64_t row, int64_t c, const float (&acc)[N]) {
+        const size_t at = (size_t)(row * a.D + c);
         if (!a.accumulate) {
             float v[N];
 #pragma unroll
             for (int k = 0; k < N; ++k) v[k] = a.scale * acc[k];
-            store_floats<N>(a.table, (size_t)(row * a.D + c), v, 12);
+            store_row<SHIFT>(a, at, (int)(a.D - c), v, 12);
             return;
         }
         complete(a, c);
         key = row;
 #pragma unroll
         for (int k = 0; k < N; ++k) sum[k] = acc[k];
-        load_floats<N>(a.table, (size_t)(row * a.D + c), old, 12);
+        load_row<SHIFT>(a, at, (int)(a.D - c), old, 12);
     }
 };
 
 // Each warp zeroes the absent ones of its own kZeroRows / 4 rows.
-template <int N>
+template <bool SHIFT>
 __device__ void zero_rows(const SumArgs& a, int64_t first) {
     constexpr int kPerWarp = kZeroRows / (kThreads / 32);
     const int lane = threadIdx.x & 31;
     first += (threadIdx.x >> 5) * kPerWarp;
     const int64_t last = first + kPerWarp < a.V ? first + kPerWarp : a.V;
     int64_t at = -1, next = -1;   // next: the first id at or above the row, at its place
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f}, one[1] = {0.f};
     for (int64_t v = first; v < last; ++v) {
         if (next < v) {
             at = lower_bound_warp(a.order, a.T, v);
             next = at < a.T ? key_at(a.order, at, 8) : a.V;
         }
         if (next == v) continue;
-        constexpr int W = N == 8 ? 4 : 1;   // 16-byte stores
-        const float zero[W] = {};
-        for (int64_t c = lane * W; c < a.D; c += 32 * W) store_at<W>(a.table, (size_t)(v * a.D + c), zero, 9);
+        // whole chunks, and single elements before the first and after the last
+        const size_t row = (size_t)(v * a.D);
+        const int m = SHIFT ? misaligned(a.table.p + row) : 0;
+        const int64_t lead = m == 0 ? 0 : 4 - m < a.D ? 4 - m : a.D, body = (a.D - lead) / 4;
+        if (lane < lead) store_at<1>(a.table, row + lane, one, 9);
+        for (int64_t k = lane; k < body; k += 32) store_at<4>(a.table, row + lead + 4 * k, zero, 9);
+        if (lane < a.D - lead - 4 * body) store_at<1>(a.table, row + lead + 4 * body + lane, one, 9);
     }
 }
 
 // Writes the sum of the run that ends at an item, or its piece in this chunk.
-template <int N>
-__device__ __forceinline__ void flush(const SumArgs& a, RowWriter<N>& out, int64_t chunk, int64_t key, int64_t c,
+template <bool SHIFT>
+__device__ __forceinline__ void flush(const SumArgs& a, RowWriter<SHIFT>& out, int64_t chunk, int64_t key, int64_t c,
                                       bool whole, bool began, float (&acc)[N]) {
-    if (c < a.D) {
-        if (whole)
-            out.write(a, key, c, acc);
-        else
-            store_floats<N>(a.pieces, (size_t)((chunk * 2 + (began ? 1 : 0)) * a.D + c), acc, 13);
-        if (!whole && began && c == 0) {
-            const uint32_t at = 1 + atomicAdd(a.heads.p, 1u);
-            if (a.heads.has(at, 1, 17)) a.heads.p[at] = (uint32_t)chunk;
-        }
+    if (whole)
+        out.write(a, key, c, acc);
+    else if (c < a.D)
+        store_floats(a.pieces, (size_t)((chunk * 2 + (began ? 1 : 0)) * a.pitch + c), acc, 13);
+    if (!whole && began && c == 0) {
+        const uint32_t at = 1 + atomicAdd(a.heads.p, 1u);
+        if (a.heads.has(at, 1, 17)) a.heads.p[at] = (uint32_t)chunk;
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
@@ -356,29 +441,31 @@ __device__ __forceinline__ void flush(const SumArgs& a, RowWriter<N>& out, int64
 //
 // The rows of a batch of ordered tokens are listed in shared memory, NS rows
 // (the streams of a token, or one row when n_streams is not 4) to an item,
-// with where runs end; a thread adds its N columns of one item after another.
-// N = 8: the rows come through per-thread copies, kAhead items of one row or
-// kAhead / 2 of four ahead; N = 1: kAhead loads are issued together.
+// with where runs end; a thread adds its columns of one item after another.
+// The rows come through per-thread copies, kAhead items of one row or
+// kAhead / 2 of four ahead.
 constexpr uint32_t kRunEnds = 1u << 31, kFlush = 1u << 30, kRowMask = kFlush - 1;   // T n_streams <= 2^28
-template <int N, int NS>
+template <bool SHIFT, int NS>
 __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
     ptx::grid_dependency_wait();
     if ((int64_t)blockIdx.x >= a.chunks * a.slabs) {
-        zero_rows<N>(a, ((int64_t)blockIdx.x - a.chunks * a.slabs) * kZeroRows);
+        zero_rows<SHIFT>(a, ((int64_t)blockIdx.x - a.chunks * a.slabs) * kZeroRows);
         return;
     }
     constexpr int kItems = NS == 1 ? kAhead : kAhead / 2;
+    constexpr int P = SHIFT ? kThreads / 32 * 33 : kThreads;
     __shared__ uint32_t rows[kBatch * (NS == 1 ? MHCPB_MAX_STREAMS : 1)];
     __shared__ uint32_t ids[kBatch];
     __shared__ int listed;
-    __shared__ uint4 ring[N == 8 ? kItems * NS * kThreads : 1];
+    __shared__ uint4 ring[kItems * NS * P];
     const int per_token = NS == 1 ? a.n_streams : 1;   // items
     const int64_t chunk = blockIdx.x / a.slabs;
     const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * N;
     const int64_t begin = chunk * a.chunk;
     const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
     bool began = begin == 0 || key_at(a.order, begin - 1, 10) != key_at(a.order, begin, 10);
-    RowWriter<N> out;
+    uint4* const mine = ring + (SHIFT ? (threadIdx.x >> 5) * 33 + (threadIdx.x & 31) : threadIdx.x);
+    RowWriter<SHIFT> out;
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
@@ -404,70 +491,57 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
         __syncthreads();
         const int items = listed;
         if (items == 0) break;
+        const auto row_of = [&](int item) { return (size_t)(rows[item] & kRowMask) * a.D; };
+        const auto fetch = [&](int item) {
+            if (item < items) {
+                const size_t at = row_of(item) + c;
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    uint4* const slot = mine + (item % kItems * NS + s) * P;
+                    if constexpr (SHIFT) {
+                        copy_shifted(slot, a.grad_x, at + s * a.D, (int)c, (int)a.D, 11);
+                    } else if (c < a.D) {
+                        if (a.grad_x.has(at + s * a.D, N, 11)) copy16(slot, a.grad_x.p + at + s * a.D);
+                    }
+                }
+            }
+            copies_commit();
+        };
+#pragma unroll
+        for (int q = 0; q < kItems; ++q) fetch(q);
         int position = 0, part = 0;   // of the item: its token in the batch, its row of the token
-        const auto finish = [&](uint32_t row) {
+        for (int item = 0; item < items; ++item) {
+            copies_wait<kItems - 1>();
+            if (SHIFT) __syncwarp();   // a lane reads the next lane's chunk too
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const uint4* const slot = mine + (item % kItems * NS + s) * P;
+                uint4 raw = slot[0];
+                if constexpr (SHIFT) {
+                    const int m = misaligned(a.grad_x.p + row_of(item) + s * a.D);
+                    if (m > 0) raw = shift_take<bf16>(raw, slot[1], m);
+                }
+                float2 v[4];
+                unpack<bf16>(raw, v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[2 * k] += v[k].x;
+                    acc[2 * k + 1] += v[k].y;
+                }
+            }
+            if (SHIFT) __syncwarp();
+            const uint32_t row = rows[item];
+            fetch(item + kItems);
             if (row & kFlush) {
-                flush<N>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
+                flush<SHIFT>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
                 began = true;
             }
             if (NS > 1 || ++part == per_token) {
                 part = 0;
                 ++position;
             }
-        };
-        if constexpr (N == 8) {
-            uint4* const mine = ring + threadIdx.x;
-            const auto fetch = [&](int item) {
-                if (item < items && c < a.D) {
-                    const size_t at = (size_t)(rows[item] & kRowMask) * a.D + c;
-#pragma unroll
-                    for (int s = 0; s < NS; ++s)
-                        if (a.grad_x.has(at + s * a.D, N, 11))
-                            copy16(mine + (item % kItems * NS + s) * kThreads, a.grad_x.p + at + s * a.D);
-                }
-                copies_commit();
-            };
-#pragma unroll
-            for (int q = 0; q < kItems; ++q) fetch(q);
-            for (int item = 0; item < items; ++item) {
-                copies_wait<kItems - 1>();
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    float2 v[4];
-                    unpack<bf16>(mine[(item % kItems * NS + s) * kThreads], v);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        acc[2 * k] += v[k].x;
-                        acc[2 * k + 1] += v[k].y;
-                    }
-                }
-                fetch(item + kItems);
-                finish(rows[item]);
-            }
-            copies_wait<0>();
-        } else {
-            constexpr int kTogether = NS == 1 ? kAhead : kAhead / NS;
-            for (int item = 0; item < items; item += kTogether) {
-                float v[kTogether][NS];
-#pragma unroll
-                for (int q = 0; q < kTogether; ++q)
-                    if (item + q < items && c < a.D)
-#pragma unroll
-                        for (int s = 0; s < NS; ++s) {
-                            float one[1];
-                            load_at<1>(a.grad_x, ((size_t)(rows[item + q] & kRowMask) + s) * a.D + c, one, 11);
-                            v[q][s] = one[0];
-                        }
-#pragma unroll
-                for (int q = 0; q < kTogether; ++q)
-                    if (item + q < items) {
-                        if (c < a.D)
-#pragma unroll
-                            for (int s = 0; s < NS; ++s) acc[0] += v[q][s];
-                        finish(rows[item + q]);
-                    }
-            }
         }
+        copies_wait<0>();
     }
     out.complete(a, c);
 }
@@ -476,7 +550,7 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
 // a time: each of kJoinParts groups of threads a part of them in order, then
 // the parts in order.
 constexpr int kJoinParts = 4;
-template <int N>
+template <bool SHIFT>
 __global__ void __launch_bounds__(kThreads * kJoinParts) join_runs_kernel(SumArgs a) {
     __shared__ float sums[kJoinParts - 1][N][kThreads];
     ptx::grid_dependency_wait();
@@ -500,7 +574,7 @@ __global__ void __launch_bounds__(kThreads * kJoinParts) join_runs_kernel(SumArg
 #pragma unroll 8
             for (int64_t q = count * part / kJoinParts; q < count * (part + 1) / kJoinParts; ++q) {
                 float v[N];
-                load_floats<N>(a.pieces, (size_t)(((chunk + q) * 2 + (q == 0 ? 1 : 0)) * a.D + c), v, 15);
+                load_floats(a.pieces, (size_t)(((chunk + q) * 2 + (q == 0 ? 1 : 0)) * a.pitch + c), v, 15);
 #pragma unroll
                 for (int k = 0; k < N; ++k) acc[k] += v[k];
             }
@@ -508,12 +582,12 @@ __global__ void __launch_bounds__(kThreads * kJoinParts) join_runs_kernel(SumArg
 #pragma unroll
             for (int k = 0; k < N; ++k) sums[part - 1][k][lane] = acc[k];
         __syncthreads();
-        if (part > 0 || c >= a.D) continue;
+        if (part > 0) continue;
 #pragma unroll
         for (int p = 0; p < kJoinParts - 1; ++p)
 #pragma unroll
             for (int k = 0; k < N; ++k) acc[k] += sums[p][k][lane];
-        RowWriter<N> out;
+        RowWriter<SHIFT> out;
         out.write(a, key, c, acc);
         out.complete(a, c);
     }
@@ -525,29 +599,30 @@ cudaError_t lookup_typed(const Args& a, cudaStream_t stream) {
     const Span<const I> ids{static_cast<const I*>(a.ids), (size_t)a.T};
     const Span<bf16> x{static_cast<bf16*>(a.x), (size_t)(a.T * a.n_streams * a.D)};
     const bool packed = a.D % 8 == 0 && aligned16(a.table) && aligned16(a.x);
-    return launch_early(packed ? lookup_kernel<E, I, 8> : lookup_kernel<E, I, 1>, dim3((unsigned)a.T), dim3(kThreads), 0,
-                        stream, a.V, a.D, a.n_streams, a.scale, table, ids, x);
+    const VectorGrid grid((a.D + 7) / 8, kLookupThreads);
+    return launch_early(packed ? lookup_kernel<E, I, false> : lookup_kernel<E, I, true>, dim3(grid.blocks(a.T)),
+                        dim3(grid.threads), 0, stream, a.T, a.V, a.D, grid, a.n_streams, a.scale, table, ids, x);
 }
 template <typename E>
 cudaError_t lookup_ids(const Args& a, cudaStream_t stream) {
     return a.id_bytes == 8 ? lookup_typed<E, int64_t>(a, stream) : lookup_typed<E, int32_t>(a, stream);
 }
 
-template <int N>
-cudaError_t sum_typed(SumArgs s, cudaStream_t stream) {
-    s.slabs = (s.D + kThreads * N - 1) / (kThreads * N);
+template <bool SHIFT>
+cudaError_t sum_typed(const SumArgs& s, cudaStream_t stream) {
     const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
-    cudaError_t e = launch_early(s.n_streams == 4 ? sum_runs_kernel<N, 4> : sum_runs_kernel<N, 1>, dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
+    cudaError_t e = launch_early(s.n_streams == 4 ? sum_runs_kernel<SHIFT, 4> : sum_runs_kernel<SHIFT, 1>,
+                                 dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
     const int64_t most = s.chunks * s.slabs < kJoinBlocks ? s.chunks * s.slabs : kJoinBlocks;
-    return launch_early(join_runs_kernel<N>, dim3((unsigned)most), dim3(kThreads * kJoinParts), 0, stream, s);
+    return launch_early(join_runs_kernel<SHIFT>, dim3((unsigned)most), dim3(kThreads * kJoinParts), 0, stream, s);
 }
 
 }  // namespace
 
 size_t workspace_bytes(int64_t T, int64_t /*V*/, int64_t D) {
     if (T == 0) return 0;
-    return 2 * order_bytes(T) + heads_bytes(T) + (size_t)chunk_count(T) * 2 * (size_t)D * sizeof(float);
+    return 2 * order_bytes(T) + heads_bytes(T) + (size_t)chunk_count(T) * 2 * (size_t)piece_pitch(D) * sizeof(float);
 }
 
 cudaError_t forward(const Args& a, cudaStream_t stream) {
@@ -587,6 +662,8 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
     s.T = a.T;
     s.V = a.V;
     s.D = a.D;
+    s.pitch = piece_pitch(a.D);
+    s.slabs = (a.D + kThreads * N - 1) / (kThreads * N);
     s.chunk = chunk_tokens(a.T);
     s.chunks = chunk_count(a.T);
     s.n_streams = a.n_streams;
@@ -596,10 +673,10 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
     s.order = Span<const uint64_t>{order, (size_t)a.T};
     s.table = Span<float>{a.grad_table, (size_t)(a.V * a.D)};
     s.heads = Span<uint32_t>{reinterpret_cast<uint32_t*>(ws + 2 * order_bytes(a.T)), (size_t)(1 + s.chunks)};
-    s.pieces = Span<float>{reinterpret_cast<float*>(ws + 2 * order_bytes(a.T) + heads_bytes(a.T)), (size_t)(s.chunks * 2 * a.D)};
+    s.pieces = Span<float>{reinterpret_cast<float*>(ws + 2 * order_bytes(a.T) + heads_bytes(a.T)), (size_t)(s.chunks * 2 * s.pitch)};
     if (a.T == 0 && a.accumulate) return cudaSuccess;
-    if (a.D % 8 == 0 && aligned16(a.grad_x) && aligned16(a.grad_table)) return sum_typed<8>(s, stream);
-    return sum_typed<1>(s, stream);
+    if (a.D % 8 == 0 && aligned16(a.grad_x) && aligned16(a.grad_table)) return sum_typed<false>(s, stream);
+    return sum_typed<true>(s, stream);
 }
 
 cudaError_t setup() {

@@ -18,6 +18,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
+#include "mhcs_shift.cuh"
 #include "ptx.cuh"
 
 namespace mhcpb {
@@ -78,6 +79,21 @@ __device__ __forceinline__ void vector_at(const Span<const float>& s, int64_t c,
     } else {
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = other;
+    }
+}
+// columns c .. c + 3 of a parameter (other where there is none, 0 past D);
+// ANY: of any alignment, and D of any size
+template <bool ANY>
+__device__ __forceinline__ void four_at(const Span<const float>& s, int c, int D, float other, float (&v)[4]) {
+    if constexpr (!ANY) {
+        if (c < D) vector_at<4>(s, c, other, v, 2);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float one[1] = {0.f};
+            if (c + k < D) vector_at<1>(s, c + k, other, one, 2);
+            v[k] = one[0];
+        }
     }
 }
 template <typename F>
@@ -208,13 +224,13 @@ __global__ void __launch_bounds__(640) forward_rows_kernel(Params<E> a, int G, i
 // about it) and publishes both, so that one barrier gives the row's statistics
 // without cancellation: mean = sum n_w m_w / D and
 // D var = sum q_w + sum n_w (m_w - mean)^2.
-template <typename E, bool MIX, int VPT, int S>
+template <typename E, bool MIX, bool SHIFT, int VPT, int S>
 struct ForwardShape {
     static constexpr int N = Elem<E>::kPack;
     static constexpr int kMaxThreads = 640;
     static constexpr int kArrays = MIX ? kStreams : 1;
     static constexpr int kStage = VPT * kArrays;
-    static constexpr int kPitch = kMaxThreads;
+    static constexpr int kPitch = SHIFT ? kMaxThreads / 32 * 33 : kMaxThreads;
     static constexpr int kSlots = S * kStage;
     static constexpr int kVectorSlots = 2 * VPT * N / 4;   // gamma and beta of a thread's columns
     static size_t bytes(int G, int R) {
@@ -222,15 +238,15 @@ struct ForwardShape {
     }
 };
 
-template <typename E, bool MIX, int VPT, int S>
-__global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1)
+template <typename E, bool MIX, bool SHIFT, int VPT, int S>
+__global__ void __launch_bounds__((ForwardShape<E, MIX, SHIFT, VPT, S>::kMaxThreads), 1)
     forward_ring_kernel(Params<E> a, int G, int R) {
-    using Shape = ForwardShape<E, MIX, VPT, S>;
+    using Shape = ForwardShape<E, MIX, SHIFT, VPT, S>;
     constexpr int N = Shape::N, H = N / 2, P = Shape::kPitch, A = Shape::kArrays;
     extern __shared__ uint4 slots[];
     const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
     const int warp = i >> 5, warps = G >> 5;
-    uint4* const mine = slots + tid;
+    uint4* const mine = slots + (SHIFT ? (tid >> 5) * 33 + lane : tid);
     float4* const vectors = reinterpret_cast<float4*>(slots + P * Shape::kSlots);   // [2][VPT N / 4][G]
     float* const floats = reinterpret_cast<float*>(vectors + Shape::kVectorSlots * G);
     float* const gates = floats + (tid >> 5) * (S * 4);                             // [S][4] per warp
@@ -241,18 +257,22 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
     // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
     for (int k = 0; k < Shape::kSlots; ++k)
-        if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+        if (!SHIFT && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
     ptx::grid_dependency_wait();
     const auto fetch = [&](int t, int stage) {
         if (t < T) {
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.x_stride + (uint32_t)c0);
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
-                if (c0 + v * step < D)
 #pragma unroll
-                    for (int s = 0; s < A; ++s)
-                        if (a.x.has(at + v * step + s * D, N, 0))
-                            copy16(mine + ((stage * VPT + v) * A + s) * P, a.x.p + at + v * step + s * D);
+                for (int s = 0; s < A; ++s) {
+                    uint4* const slot = mine + ((stage * VPT + v) * A + s) * P;
+                    if constexpr (SHIFT) {
+                        copy_shifted(slot, a.x, at + v * step + s * D, c0 + v * step, D, 0);
+                    } else if (c0 + v * step < D) {
+                        if (a.x.has(at + v * step + s * D, N, 0)) copy16(slot, a.x.p + at + v * step + s * D);
+                    }
+                }
             if (MIX && lane < kStreams && a.h.has((size_t)t * kGates + lane, 1, 1))
                 copy4(gates + stage * 4 + lane, a.h.p + (size_t)t * kGates + lane);
         }
@@ -265,10 +285,8 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
         for (int k = 0; k < Shape::kVectorSlots / 2; ++k) {
             const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
             float g[4] = {}, b[4] = {};
-            if (c < D) {
-                vector_at<4>(a.gamma, c, 1.f, g, 2);
-                vector_at<4>(a.beta, c, 0.f, b, 2);
-            }
+            four_at<SHIFT>(a.gamma, c, D, 1.f, g);
+            four_at<SHIFT>(a.beta, c, D, 0.f, b);
             vectors[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
             vectors[(Shape::kVectorSlots / 2 + k) * G + i] = make_float4(b[0], b[1], b[2], b[3]);
         }
@@ -290,7 +308,11 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
     for (int t = first; t < T; t += groups) {
         copies_wait<S - 1>();
         __syncwarp();
-        const uint4* const row = mine + stage * (Shape::kStage * P);
+        uint4* const row = mine + stage * (Shape::kStage * P);
+        if constexpr (SHIFT)
+#pragma unroll
+            for (int k = 0; k < Shape::kStage; ++k)
+                realign<E>(row + k * P, misaligned(a.x.p + (size_t)t * a.x_stride + k % A * D), D - (c0 + k / A * step));
         float2 u[VPT][H], s2 = pair(0.f);
         float p4[kStreams] = {};
         if constexpr (MIX) {
@@ -327,7 +349,11 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
             if (c0 + v * step < D)
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
-                    const float2 d = add2(u[v][k], pair(-m_mine));
+                    float2 d = add2(u[v][k], pair(-m_mine));
+                    if (SHIFT) {   // a row may end inside the vector
+                        if (c0 + v * step + 2 * k >= D) d.x = 0.f;
+                        if (c0 + v * step + 2 * k + 1 >= D) d.y = 0.f;
+                    }
                     q2 = fma2(d, d, q2);
                 }
         const float q_mine = warp_sum(q2.x + q2.y);
@@ -356,7 +382,11 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, VPT, S>::kMaxThreads), 1
                 o[2 * k + 1] = fma2(mul2(add2(u[v][2 * k + 1], mean2), rstd2), make_float2(g.z, g.w), make_float2(b.z, b.w));
             }
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.y_stride + (uint32_t)(c0 + v * step));
-            if (c0 + v * step < D && a.y.has(at, N, 3)) *reinterpret_cast<uint4*>(a.y.p + at) = pack<E>(o);
+            if constexpr (SHIFT) {
+                store_shifted(a.y, at, D - (c0 + v * step), lane > 0, lane < 31, pack<E>(o), 3);
+            } else {
+                if (c0 + v * step < D && a.y.has(at, N, 3)) *reinterpret_cast<uint4*>(a.y.p + at) = pack<E>(o);
+            }
         }
         if (i == 0 && a.mean.p != nullptr) {
             const float o1[1] = {mean}, o2[1] = {rstd};
@@ -475,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) backward_columns_any_kernel(Params<E
 // slots again (cheaper than holding u and w in registers), writes the
 // gradients and refills each slot as it leaves it.  The other groups of the
 // block compute while one waits.
-template <typename E, bool MIX, int VPT, int S, int MAX>
+template <typename E, bool MIX, bool SHIFT, int VPT, int S, int MAX>
 struct RowsShape {
     static constexpr int N = Elem<E>::kPack;
     static constexpr int kMaxThreads = MAX;   // 640: 96 registers a thread; 512: 128
@@ -483,8 +513,8 @@ struct RowsShape {
     static constexpr int kStage = VPT * kArrays;                    // 16-byte slots of a row
     // Slot k of every thread of the block lies together, so that a warp's copy
     // writes whole 128-byte lines; the pitch is a constant, for immediate
-    // offsets.
-    static constexpr int kPitch = kMaxThreads;
+    // offsets.  SHIFT: rows at any address, a warp's 33 chunks (mhcs_shift.cuh).
+    static constexpr int kPitch = SHIFT ? kMaxThreads / 32 * 33 : kMaxThreads;
     static constexpr int kSlots = S * kStage;
     static constexpr int kGammaSlots = VPT * N / 4;                 // per thread of a group, FP32
     static constexpr int kWarpFloats = S * 32;                      // per row: 24 gates, mean, rstd
@@ -496,15 +526,15 @@ struct RowsShape {
     }
 };
 
-template <typename E, bool MIX, int VPT, int S, int MAX>
+template <typename E, bool MIX, bool SHIFT, int VPT, int S, int MAX>
 __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int G, int R) {
-    using Shape = RowsShape<E, MIX, VPT, S, MAX>;
+    using Shape = RowsShape<E, MIX, SHIFT, VPT, S, MAX>;
     constexpr int N = Shape::N, H = N / 2, P = Shape::kPitch, A = Shape::kArrays;
     constexpr int XA = MIX ? kStreams : 1;   // slots of a vector: x (XA), grad_y, residual gradient
     extern __shared__ uint4 slots[];
     const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
     const int warp = i >> 5, warps = G >> 5;
-    uint4* const mine = slots + tid;
+    uint4* const mine = slots + (SHIFT ? (tid >> 5) * 33 + lane : tid);
     float4* const gammas = reinterpret_cast<float4*>(slots + P * Shape::kSlots);   // [kGammaSlots][G]
     float* const floats = reinterpret_cast<float*>(gammas + Shape::kGammaSlots * G);
     float* const scalars = floats + (tid >> 5) * Shape::kWarpFloats;
@@ -516,7 +546,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
     // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
     for (int k = 0; k < Shape::kSlots; ++k)
-        if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+        if (!SHIFT && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
     ptx::grid_dependency_wait();
 
     // Element offset of row t of an array at this thread's first column, formed
@@ -525,7 +555,17 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
         return (size_t)((uint64_t)(uint32_t)t * (uint32_t)stride + (uint32_t)c0);
     };
     const auto fetch_vector = [&](uint4* dst, int t, int v) {
-        if (c0 + v * step < D) {
+        if constexpr (SHIFT) {
+            const size_t xo = at_row(t, a.x_stride) + v * step, go = at_row(t, a.gy_stride) + v * step;
+            const int c = c0 + v * step;
+#pragma unroll
+            for (int s = 0; s < XA; ++s) copy_shifted(dst + (v * A + s) * P, a.x, xo + s * D, c, D, 0);
+            copy_shifted(dst + (v * A + XA) * P, a.grad_y, go, c, D, 5);
+            if (MIX && residual)
+#pragma unroll
+                for (int s = 0; s < kStreams; ++s)
+                    copy_shifted(dst + (v * A + XA + 1 + s) * P, a.grad_x_out, xo + s * D, c, D, 7);
+        } else if (c0 + v * step < D) {
             const size_t xo = at_row(t, a.x_stride) + v * step, go = at_row(t, a.gy_stride) + v * step;
 #pragma unroll
             for (int s = 0; s < XA; ++s)
@@ -578,7 +618,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
         for (int k = 0; k < Shape::kGammaSlots; ++k) {
             const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
             float g[4] = {0.f, 0.f, 0.f, 0.f};
-            if (c < D) vector_at<4>(a.gamma, c, 1.f, g, 2);
+            four_at<SHIFT>(a.gamma, c, D, 1.f, g);
             gammas[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
         }
     __syncthreads();
@@ -595,6 +635,15 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
         __syncwarp();
         const float4* const gates = reinterpret_cast<const float4*>(scalars + stage * 32);
         uint4* const row = mine + stage * (Shape::kStage * P);
+        if constexpr (SHIFT)
+#pragma unroll
+            for (int k = 0; k < Shape::kStage; ++k) {
+                const int s = k % A;   // x, grad_y or the residual path's gradient
+                const E* const p = s < XA ? a.x.p + (size_t)t * a.x_stride + s * D
+                                   : s == XA ? a.grad_y.p + (size_t)t * a.gy_stride
+                                             : a.grad_x_out.p + (size_t)t * a.x_stride + (s - XA - 1) * D;
+                if (s <= XA || residual) realign<E>(row + k * P, misaligned(p), D - (c0 + k / A * step));
+            }
         const float2 stat = reinterpret_cast<const float2*>(gates)[kGates / 2];
         // z = u rstd - mean rstd
         const float2 rstd2 = pair(stat.y), shift2 = pair(-stat.x * stat.y);
@@ -713,7 +762,13 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
                     for (int j = 0; j < kStreams; ++j) pack_half<E>(o[j], &out[j][half * 2]);
                 }
             }
-            if (c0 + v * step < D) {
+            if constexpr (SHIFT) {
+                const size_t o = at_row(t, a.gx_stride) + v * step;
+#pragma unroll
+                for (int j = 0; j < XA; ++j)
+                    store_shifted(a.grad_x, o + j * D, D - (c0 + v * step), lane > 0, lane < 31,
+                                  make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]), 6);
+            } else if (c0 + v * step < D) {
                 const size_t o = at_row(t, a.gx_stride) + v * step;
 #pragma unroll
                 for (int j = 0; j < XA; ++j)
@@ -776,148 +831,16 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
                     o[2 * k] = q.x;
                     o[2 * k + 1] = q.y;
                 }
-                store_at<N>(a.partial, ((size_t)blockIdx.x * 2 + part) * D + c, o, 9);
-            }
-        }
-    }
-}
-
-// ------------------------------------------------------------ backward, unaligned rows in registers
-// As backward_rows_kernel, an element at a time (rows whose addresses are not
-// multiples of 16 bytes): thread i owns columns i, i + G, ..., VPT of them,
-// and loads its part of a row directly.
-template <typename E, bool MIX, int VPT, int MAX>
-__global__ void __launch_bounds__(MAX, 1) backward_elements_kernel(Params<E> a, int G, int R) {
-    ptx::grid_dependency_wait();
-    extern __shared__ float shared[];   // [R][2][2 or 6][32] sums, then [2][VPT][G] parameter gradients
-    constexpr int XA = MIX ? kStreams : 1, kSums = MIX ? 2 + kStreams : 2;
-    const int tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
-    const int warp = i >> 5, warps = G >> 5, D = (int)a.D, T = (int)a.T;
-    float* const sums = shared + group * (2 * kSums * 32);
-    const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group;
-    const bool residual = MIX && a.grad_x_out.p != nullptr;
-    const float inv_d = 1.f / (float)D;
-    float gg[VPT], gb[VPT], gam[VPT];
+                const size_t at = ((size_t)blockIdx.x * 2 + part) * D + c;
+                if constexpr (SHIFT) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        gg[v] = gb[v] = 0.f;
-        float g[1] = {0.f};
-        if (i + v * G < D) vector_at<1>(a.gamma, i + v * G, 1.f, g, 2);
-        gam[v] = g[0];
-    }
-    int parity = 0;
-    for (int t = first; t < T; t += groups) {
-        float x[VPT][XA], w[VPT], gate[kGates];
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int c = i + v * G;
-            float one[1] = {0.f};
-            w[v] = 0.f;
-#pragma unroll
-            for (int s = 0; s < XA; ++s) x[v][s] = 0.f;
-            if (c < D) {
-#pragma unroll
-                for (int s = 0; s < XA; ++s) {
-                    load_at<1>(a.x, (size_t)t * a.x_stride + s * D + c, one, 0);
-                    x[v][s] = one[0];
-                }
-                load_at<1>(a.grad_y, (size_t)t * a.gy_stride + c, one, 5);
-                w[v] = one[0];
-            }
-        }
-        if constexpr (MIX)
-#pragma unroll
-            for (int k = 0; k < kGates; ++k)
-                if (k < kStreams || k >= 2 * kStreams) gate[k] = scalar_at(a.h, (int64_t)t * kGates + k, 1);
-        const float mean = scalar_at(a.mean, t, 4), rstd = scalar_at(a.rstd, t, 4);
-        float z[VPT], sw = 0.f, swz = 0.f;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            float u = x[v][0];
-            if constexpr (MIX) {
-                u *= gate[0];
-#pragma unroll
-                for (int s = 1; s < XA; ++s) u = fmaf(gate[s], x[v][s], u);
-            }
-            z[v] = (u - mean) * rstd;
-            gg[v] = fmaf(w[v], z[v], gg[v]);
-            gb[v] += w[v];
-            w[v] *= gam[v];
-            sw += w[v];
-            swz = fmaf(w[v], z[v], swz);
-        }
-        float* const s0 = sums + parity * (kSums * 32);
-        const float both = warp_sum_two(sw, swz);
-        if ((lane & 15) == 0) s0[(lane >> 4) * 32 + warp] = both;
-        group_sync(group, G);
-        const float mw = warp_sum(lane < warps ? s0[lane] : 0.f) * inv_d;
-        const float mwz = warp_sum(lane < warps ? s0[32 + lane] : 0.f) * inv_d;
-        float dot[kStreams] = {};
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int c = i + v * G;
-            if (c < D) {
-                const float du = rstd * (w[v] - mw - z[v] * mwz);
-                float o[XA];
-                if constexpr (!MIX) {
-                    o[0] = du;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < XA; ++j) {
-                        dot[j] = fmaf(x[v][j], du, dot[j]);
-                        o[j] = gate[j] * du;
+                    for (int k = 0; k < N; ++k) {
+                        const float one[1] = {o[k]};
+                        if (c + k < D) store_at<1>(a.partial, at + k, one, 9);
                     }
-                    if (residual)
-#pragma unroll
-                        for (int s = 0; s < kStreams; ++s) {
-                            float g[1];
-                            load_at<1>(a.grad_x_out, ((size_t)t * kStreams + s) * D + c, g, 7);
-#pragma unroll
-                            for (int j = 0; j < XA; ++j) o[j] = fmaf(gate[8 + 4 * s + j], g[0], o[j]);
-                        }
+                } else {
+                    store_at<N>(a.partial, at, o, 9);
                 }
-#pragma unroll
-                for (int j = 0; j < XA; ++j) {
-                    const float one[1] = {o[j]};
-                    store_at<1>(a.grad_x, (size_t)t * a.gx_stride + j * D + c, one, 6);
-                }
-            }
-        }
-        if constexpr (MIX) {
-            const float d = warp_sum_four(dot);
-            if ((lane & 7) == 0) s0[(2 + (lane >> 3)) * 32 + warp] = d;
-            group_sync(group, G);
-            if (warp == 0) {
-                float q = 0.f;
-                for (int k = lane & 7; k < warps; k += 8) q += s0[(2 + (lane >> 3)) * 32 + k];
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(kFullMask, q, o);
-                const float one[1] = {q};
-                if ((lane & 7) == 0) store_at<1>(a.grad_h, (size_t)t * kGates + (lane >> 3), one, 8);
-            }
-        }
-        parity ^= 1;
-    }
-    if (a.grad_gamma.p == nullptr && a.grad_beta.p == nullptr) return;
-    float* const acc = shared + R * (2 * kSums * 32);
-    for (int g = 0; g < R; ++g) {   // the block's groups in order
-        __syncthreads();
-        if (g != group) continue;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            float* const p = acc + v * G + i;
-            float* const q = p + VPT * G;
-            if (g > 0) {
-                gg[v] += *p;
-                gb[v] += *q;
-            }
-            if (g + 1 < R) {
-                *p = gg[v];
-                *q = gb[v];
-            } else if (i + v * G < D) {
-                const float o1[1] = {gg[v]}, o2[1] = {gb[v]};
-                store_at<1>(a.partial, ((size_t)blockIdx.x * 2 + 0) * D + i + v * G, o1, 9);
-                store_at<1>(a.partial, ((size_t)blockIdx.x * 2 + 1) * D + i + v * G, o2, 9);
             }
         }
     }
@@ -997,10 +920,10 @@ bool forward_rows(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
 }
 
 // Likewise forward_ring_kernel.
-template <typename E, bool MIX, int VPT, int S>
+template <typename E, bool MIX, bool SHIFT, int VPT, int S>
 bool forward_ring(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
-    using Shape = ForwardShape<E, MIX, VPT, S>;
-    const int64_t threads = (p.D / Shape::N + VPT - 1) / VPT;
+    using Shape = ForwardShape<E, MIX, SHIFT, VPT, S>;
+    const int64_t threads = ((p.D + Shape::N - 1) / Shape::N + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
     int R = Shape::kMaxThreads / G > 15 ? 15 : Shape::kMaxThreads / G;
@@ -1009,7 +932,7 @@ bool forward_ring(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
     const size_t shared = Shape::bytes(G, R);
     if (shared > kMaxShared) return false;
     const int64_t grid = (p.T + R - 1) / R < kSms ? (p.T + R - 1) / R : kSms;
-    auto kernel = forward_ring_kernel<E, MIX, VPT, S>;
+    auto kernel = forward_ring_kernel<E, MIX, SHIFT, VPT, S>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
@@ -1026,9 +949,11 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
     if (packed) {
         // few rows: more threads each, for latency
         if ((a.T <= kSms && forward_rows<E, MIX, N, 1>(p, &e, stream)) ||
-            forward_ring<E, MIX, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) || forward_rows<E, MIX, N, 16 / N>(p, &e, stream))
+            forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) ||
+            forward_rows<E, MIX, N, 16 / N>(p, &e, stream))
             return e;
-    } else if (forward_rows<E, MIX, 1, 4>(p, &e, stream) || forward_rows<E, MIX, 1, 16>(p, &e, stream)) {
+    } else if ((a.T <= kSms && forward_rows<E, MIX, 1, 4>(p, &e, stream)) ||
+               forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream)) {
         return e;
     }
     return launch_early(packed && a.D % 8 == 0 ? forward_any_kernel<E, MIX, 8> : forward_any_kernel<E, MIX, 1>,
@@ -1037,10 +962,10 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
 
 // Launches backward_rows_kernel where the row fits its shape; false otherwise.
 // *parts: the row groups it writes partial parameter gradients for.
-template <typename E, bool MIX, int VPT, int S, int MAX>
+template <typename E, bool MIX, bool SHIFT, int VPT, int S, int MAX>
 bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStream_t stream) {
-    using Shape = RowsShape<E, MIX, VPT, S, MAX>;
-    const int64_t vectors = p.D / Shape::N, threads = (vectors + VPT - 1) / VPT;
+    using Shape = RowsShape<E, MIX, SHIFT, VPT, S, MAX>;
+    const int64_t vectors = (p.D + Shape::N - 1) / Shape::N, threads = (vectors + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
     const int64_t blocks = kSms;
@@ -1053,26 +978,7 @@ bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStrea
     if (shared > kMaxShared) return false;
     const int64_t grid = (p.T + R - 1) / R < blocks ? (p.T + R - 1) / R : blocks;
     *parts = grid;
-    auto kernel = backward_rows_kernel<E, MIX, VPT, S, MAX>;
-    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
-    if (*e != cudaSuccess) return true;
-    *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
-    return true;
-}
-
-// Likewise backward_elements_kernel.
-template <typename E, bool MIX, int VPT, int MAX>
-bool backward_elements(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStream_t stream) {
-    const int64_t threads = (p.D + VPT - 1) / VPT;
-    if (threads > MAX) return false;
-    const int G = (int)((threads + 31) / 32 * 32);
-    int R = MAX / G > 15 ? 15 : MAX / G;
-    const int64_t spread = (p.T + kSms - 1) / kSms;
-    if (R > spread) R = (int)spread;
-    const int64_t grid = (p.T + R - 1) / R < kSms ? (p.T + R - 1) / R : kSms;
-    *parts = grid;
-    const size_t shared = ((size_t)R * 2 * (MIX ? 6 : 2) * 32 + 2 * VPT * G) * sizeof(float);
-    auto kernel = backward_elements_kernel<E, MIX, VPT, MAX>;
+    auto kernel = backward_rows_kernel<E, MIX, SHIFT, VPT, S, MAX>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
@@ -1089,20 +995,18 @@ cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     if (a.T > 0) {
         bool done = false;
-        if (packed) {
-            if constexpr (MIX)
-                done = backward_rows<E, true, 1, 2, 640>(p, &p.parts, &e, stream) ||
-                       backward_rows<E, true, 2, 1, 512>(p, &p.parts, &e, stream) ||
-                       backward_rows<E, true, 2, 1, 640>(p, &p.parts, &e, stream);
+        if constexpr (MIX) {
+            if (packed)
+                done = backward_rows<E, true, false, 1, 2, 640>(p, &p.parts, &e, stream) ||
+                       backward_rows<E, true, false, 2, 1, 512>(p, &p.parts, &e, stream) ||
+                       backward_rows<E, true, false, 2, 1, 640>(p, &p.parts, &e, stream);
             else
-                done = backward_rows<E, false, 16 / N, sizeof(E) == 4 ? 2 : 3, 640>(p, &p.parts, &e, stream);
+                done = backward_rows<E, true, true, 1, 2, 512>(p, &p.parts, &e, stream) ||
+                       backward_rows<E, true, true, 2, 1, 512>(p, &p.parts, &e, stream);
         } else {
-            if constexpr (MIX)
-                done = backward_elements<E, true, 4, 640>(p, &p.parts, &e, stream) ||
-                       backward_elements<E, true, 8, 512>(p, &p.parts, &e, stream);
-            else
-                done = backward_elements<E, false, 8, 640>(p, &p.parts, &e, stream) ||
-                       backward_elements<E, false, 16, 512>(p, &p.parts, &e, stream);
+            constexpr int S = sizeof(E) == 4 ? 2 : 3;
+            done = packed ? backward_rows<E, false, false, 16 / N, S, 640>(p, &p.parts, &e, stream)
+                          : backward_rows<E, false, true, 16 / N, S, 640>(p, &p.parts, &e, stream);
         }
         if (!done) {
             e = launch_early(packed && a.D % 8 == 0 ? backward_rows_any_kernel<E, MIX, 8> : backward_rows_any_kernel<E, MIX, 1>,

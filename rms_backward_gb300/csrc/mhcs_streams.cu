@@ -11,6 +11,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
+#include "mhcs_shift.cuh"
 #include "ptx.cuh"
 
 namespace mhcpb {
@@ -91,12 +92,12 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const
     }
 }
 
-// One block per token; N columns of every stream per thread and step.
-template <int N>
-__global__ void __launch_bounds__(kThreads) update_forward_kernel(int64_t D, Span<const bf16> x,
+// Any size: one block per token, a column of every stream per thread and step.
+__global__ void __launch_bounds__(kThreads) update_forward_any_kernel(int64_t D, Span<const bf16> x,
                                                                   Span<const bf16> y, Span<const float> h,
                                                                   Drop d, Span<bf16> x_out) {
     ptx::grid_dependency_wait();
+    constexpr int N = 1;
     __shared__ float gate[kGates];
     const int64_t t = blockIdx.x;
     if (threadIdx.x < kGates) {
@@ -127,12 +128,12 @@ __global__ void __launch_bounds__(kThreads) update_forward_kernel(int64_t D, Spa
     }
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads) update_backward_kernel(int64_t D, Span<const bf16> x,
+__global__ void __launch_bounds__(kThreads) update_backward_any_kernel(int64_t D, Span<const bf16> x,
                                                                    Span<const bf16> y, Span<const float> h,
                                                                    Drop d, Span<const bf16> gout,
                                                                    Span<bf16> gy, Span<float> gh) {
     ptx::grid_dependency_wait();
+    constexpr int N = 1;
     __shared__ float post[kStreams];
     __shared__ float scratch[20 * 32];
     const int64_t t = blockIdx.x;
@@ -202,58 +203,64 @@ __device__ __forceinline__ void gates_at(const Span<const float>& h, int64_t t, 
         }
     }
 }
-// f <- dropout of the eight elements from e on; *keep: which are kept
+// f <- dropout of the eight elements from e on; *keep: which are kept.  ANY: e
+// need not be a multiple of 4, so the eight words come from three counters.
+template <bool ANY>
 __device__ __forceinline__ void drop_eight(const Drop& d, const ShortPhilox& random, uint64_t e, float2 (&f)[4],
                                            uint32_t* keep) {
     *keep = 0xffu;
     if (d.rng == nullptr) return;
-    uint32_t w[1][2][4];
+    constexpr int kCounters = ANY ? 3 : 2;
+    uint32_t w[1][kCounters][4];
     const uint32_t counter[1] = {(uint32_t)(e >> 2)};
-    random.words<1, 2>(counter, w);
-    *keep = 0u;
+    random.words<1, kCounters>(counter, w);
+    uint32_t bits = 0u;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) *keep |= (w[0][k / 4][k % 4] >= d.threshold ? 1u : 0u) << k;
+    for (int k = 0; k < 4 * kCounters; ++k) bits |= (w[0][k / 4][k % 4] >= d.threshold ? 1u : 0u) << k;
+    if (ANY) bits >>= (uint32_t)e & 3u;
+    *keep = bits & 0xffu;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         f[k] = mul2(f[k], pair(d.scale));
-        f[k].x = *keep >> (2 * k) & 1u ? f[k].x : 0.f;
-        f[k].y = *keep >> (2 * k + 1) & 1u ? f[k].y : 0.f;
+        f[k].x = bits >> (2 * k) & 1u ? f[k].x : 0.f;
+        f[k].y = bits >> (2 * k + 1) & 1u ? f[k].y : 0.f;
     }
 }
 
 // One vector of every stream per thread, everything loaded before anything is
-// used.  A block holds `tokens` whole tokens of `vectors` vectors, or, when a
-// token has more vectors than the block has threads, one of its `tiles` tiles.
+// used.  SHIFT: rows at any address (mhcs_shift.cuh), D of any size.
+template <bool SHIFT>
 __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
-    int64_t T, int64_t D, int tokens, int tiles, bool gates_aligned, Span<const bf16> x, Span<const bf16> y,
+    int64_t T, int64_t D, VectorGrid grid, bool gates_aligned, Span<const bf16> x, Span<const bf16> y,
     Span<const float> h, Drop d, Span<bf16> x_out) {
     ptx::grid_dependency_wait();
     constexpr int N = 8, H = 4;
-    const int vectors = (int)(D / N);
-    int64_t t;
-    int c;
-    if (tiles == 1) {
-        t = (int64_t)blockIdx.x * tokens + threadIdx.x / vectors;
-        c = (int)(threadIdx.x % vectors) * N;
-        if (threadIdx.x >= tokens * vectors || t >= T) return;
-    } else {
-        t = blockIdx.x / tiles;
-        c = ((int)(blockIdx.x % tiles) * (int)blockDim.x + (int)threadIdx.x) * N;
-        if (c >= D) return;
-    }
+    const VectorPlace place = grid.place(T);
+    const int64_t t = place.token;
+    const int c = place.vector * N, valid = place.valid ? (int)D - c : 0;
+    if (!SHIFT && valid <= 0) return;
     const size_t row = (size_t)t * (kStreams * D) + c, flat = (size_t)t * D + c;
-    uint4 xs[kStreams], yr = make_uint4(0u, 0u, 0u, 0u);
-    if (y.has(flat, N, 3)) yr = *reinterpret_cast<const uint4*>(y.p + flat);
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 xs[kStreams] = {none, none, none, none}, yr = none;
+    float g[20] = {};
+    if (valid > 0) {
+        if constexpr (SHIFT) {
+            yr = load_shifted(y, flat, valid, 3);
 #pragma unroll
-    for (int j = 0; j < kStreams; ++j)
-        xs[j] = x.has(row + j * D, N, 4) ? *reinterpret_cast<const uint4*>(x.p + row + j * D) : make_uint4(0u, 0u, 0u, 0u);
-    float g[20];
-    gates_at(h, t, gates_aligned, g);
+            for (int j = 0; j < kStreams; ++j) xs[j] = load_shifted(x, row + j * D, valid, 4);
+        } else {
+            if (y.has(flat, N, 3)) yr = *reinterpret_cast<const uint4*>(y.p + flat);
+#pragma unroll
+            for (int j = 0; j < kStreams; ++j)
+                if (x.has(row + j * D, N, 4)) xs[j] = *reinterpret_cast<const uint4*>(x.p + row + j * D);
+        }
+        gates_at(h, t, gates_aligned, g);
+    }
     const DropKey key = drop_key(d);
     float2 yv[H], o[kStreams][H];
     uint32_t keep;
     unpack<bf16>(yr, yv);
-    drop_eight(d, ShortPhilox(key), flat, yv, &keep);
+    drop_eight<SHIFT>(d, ShortPhilox(key), flat, yv, &keep);
 #pragma unroll
     for (int i = 0; i < kStreams; ++i)
 #pragma unroll
@@ -268,35 +275,40 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
             for (int k = 0; k < H; ++k) o[i][k] = fma2(pair(g[4 + 4 * i + j]), v[k], o[i][k]);
     }
 #pragma unroll
-    for (int i = 0; i < kStreams; ++i)
-        if (x_out.has(row + i * D, N, 5)) *reinterpret_cast<uint4*>(x_out.p + row + i * D) = pack<bf16>(o[i]);
+    for (int i = 0; i < kStreams; ++i) {
+        if constexpr (SHIFT) {
+            store_shifted(x_out, row + i * D, valid, place.before, place.after, pack<bf16>(o[i]), 5);
+        } else {
+            if (x_out.has(row + i * D, N, 5)) *reinterpret_cast<uint4*>(x_out.p + row + i * D) = pack<bf16>(o[i]);
+        }
+    }
 }
 
 // A group of G threads takes a token at a time (thread i owns vectors i, i + G,
 // ... of it, VPT of them), its inputs copied S tokens ahead into per-thread
 // slots.  The token's 20 dot products are left in shared memory by each warp
 // and added up after the group's barrier, which the outputs do not wait for.
-template <int VPT, int S, int MAX>
+template <bool SHIFT, int VPT, int S, int MAX>
 struct TokenShape {
     static constexpr int kMaxThreads = MAX;            // 640: 96 registers a thread; 512: 128
     static constexpr int kArrays = 2 * kStreams + 1;   // x, grad_x_out, y
     static constexpr int kStage = VPT * kArrays;
-    static constexpr int kPitch = kMaxThreads;
+    static constexpr int kPitch = SHIFT ? MAX / 32 * 33 : MAX;
     static constexpr int kDots = 20;
     static size_t bytes(int G, int R) {
         return (size_t)kPitch * S * kStage * 16 + (size_t)R * (G / 32 * S * 4 + 2 * kDots * (G / 32 | 1)) * 4;
     }
 };
-template <int VPT, int S, int MAX>
+template <bool SHIFT, int VPT, int S, int MAX>
 __global__ void __launch_bounds__(MAX, 1)
     update_backward_tokens_kernel(int T, int D, int G, int R, Span<const bf16> x, Span<const bf16> y,
                                   Span<const float> h, Drop d, Span<const bf16> gout, Span<bf16> gy, Span<float> gh) {
-    using Shape = TokenShape<VPT, S, MAX>;
+    using Shape = TokenShape<SHIFT, VPT, S, MAX>;
     constexpr int N = 8, P = Shape::kPitch, A = Shape::kArrays;
     extern __shared__ uint4 slots[];
     const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
     const int warp = i >> 5, warps = G >> 5;
-    uint4* const mine = slots + tid;
+    uint4* const mine = slots + (SHIFT ? (tid >> 5) * 33 + lane : tid);
     float* const floats = reinterpret_cast<float*>(slots + P * S * Shape::kStage);
     float* const posts = floats + (tid >> 5) * (S * 4);                                   // [S][4] per warp
     float* const dots = floats + (NT >> 5) * (S * 4) + group * (2 * Shape::kDots * (warps | 1));
@@ -306,14 +318,21 @@ __global__ void __launch_bounds__(MAX, 1)
     // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
     for (int k = 0; k < S * Shape::kStage; ++k)
-        if (c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+        if (!SHIFT && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
     ptx::grid_dependency_wait();
 
     const auto fetch_vector = [&](uint4* dst, int t, int v) {
         const int c = c0 + v * step;
-        if (c < D) {
-            const size_t flat = (size_t)((uint64_t)(uint32_t)t * (uint32_t)D + (uint32_t)c);
-            const size_t row = (size_t)((uint64_t)(uint32_t)t * (uint32_t)(kStreams * D) + (uint32_t)c);
+        const size_t flat = (size_t)((uint64_t)(uint32_t)t * (uint32_t)D + (uint32_t)c);
+        const size_t row = (size_t)((uint64_t)(uint32_t)t * (uint32_t)(kStreams * D) + (uint32_t)c);
+        if constexpr (SHIFT) {
+#pragma unroll
+            for (int s = 0; s < kStreams; ++s) {
+                copy_shifted(dst + (v * A + s) * P, x, row + s * D, c, D, 4);
+                copy_shifted(dst + (v * A + kStreams + s) * P, gout, row + s * D, c, D, 6);
+            }
+            copy_shifted(dst + (v * A + 2 * kStreams) * P, y, flat, c, D, 3);
+        } else if (c < D) {
 #pragma unroll
             for (int s = 0; s < kStreams; ++s) {
                 if (x.has(row + s * D, N, 4)) copy16(dst + (v * A + s) * P, x.p + row + s * D);
@@ -350,6 +369,15 @@ __global__ void __launch_bounds__(MAX, 1)
         copies_wait<S - 1>();
         __syncwarp();
         uint4* const row = mine + stage * (Shape::kStage * P);
+        if constexpr (SHIFT)
+#pragma unroll
+            for (int k = 0; k < Shape::kStage; ++k) {
+                const int s = k % A;   // x, grad_x_out or y
+                const bf16* const p = s < kStreams ? x.p + (size_t)t * (kStreams * D) + s * D
+                                      : s < 2 * kStreams ? gout.p + (size_t)t * (kStreams * D) + (s - kStreams) * D
+                                                         : y.p + (size_t)t * D;
+                realign<bf16>(row + k * P, misaligned(p), D - (c0 + k / A * step));
+            }
         const float4 post = *reinterpret_cast<const float4*>(posts + stage * 4);
         const float p4[kStreams] = {post.x, post.y, post.z, post.w};
         const bool more = t + S * groups < T;
@@ -365,7 +393,7 @@ __global__ void __launch_bounds__(MAX, 1)
             float2 yv[4];
             uint32_t keep, out[4];
             unpack<bf16>(row[(v * A + 2 * kStreams) * P], yv);
-            drop_eight(d, random, flat, yv, &keep);
+            drop_eight<SHIFT>(d, random, flat, yv, &keep);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 float2 xs[kStreams][2], o[2] = {pair(0.f), pair(0.f)};
@@ -394,7 +422,12 @@ __global__ void __launch_bounds__(MAX, 1)
                     }
                 pack_half<bf16>(o, out + half * 2);
             }
-            if (c < D && gy.has(flat, N, 7)) *reinterpret_cast<uint4*>(gy.p + flat) = make_uint4(out[0], out[1], out[2], out[3]);
+            const uint4 packed = make_uint4(out[0], out[1], out[2], out[3]);
+            if constexpr (SHIFT) {
+                store_shifted(gy, flat, D - c, lane > 0, lane < 31, packed, 7);
+            } else {
+                if (c < D && gy.has(flat, N, 7)) *reinterpret_cast<uint4*>(gy.p + flat) = packed;
+            }
             if (more) fetch_vector(row, t + S * groups, v);
         }
         const float res = warp_sum_sixteen(d16), pos = warp_sum_four(d4);
@@ -415,12 +448,12 @@ __global__ void __launch_bounds__(MAX, 1)
 }
 
 // Launches update_backward_tokens_kernel where a token fits its shape.
-template <int VPT, int S, int MAX>
+template <bool SHIFT, int VPT, int S, int MAX>
 bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, const Span<const bf16>& y,
                             const Span<const float>& h, const Drop& d, const Span<const bf16>& gout,
                             const Span<bf16>& gy, const Span<float>& gh, cudaError_t* e, cudaStream_t stream) {
-    using Shape = TokenShape<VPT, S, MAX>;
-    const int64_t threads = (D / 8 + VPT - 1) / VPT;
+    using Shape = TokenShape<SHIFT, VPT, S, MAX>;
+    const int64_t threads = ((D + 7) / 8 + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
     int R = Shape::kMaxThreads / G;
@@ -430,7 +463,7 @@ bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, con
     while (R > 1 && Shape::bytes(G, R) > kMaxShared) --R;
     if (Shape::bytes(G, R) > kMaxShared) return false;
     const int64_t grid = (T + R - 1) / R < kSms ? (T + R - 1) / R : kSms;
-    auto kernel = update_backward_tokens_kernel<VPT, S, MAX>;
+    auto kernel = update_backward_tokens_kernel<SHIFT, VPT, S, MAX>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), Shape::bytes(G, R), stream, (int)T, (int)D, G,
@@ -468,31 +501,13 @@ cudaError_t update_forward(int64_t T, int64_t D, const void* x, const void* y, c
     const Span<const bf16> ys{static_cast<const bf16*>(y), (size_t)(T * D)};
     const Span<const float> hs{h, (size_t)(T * kGates)};
     const Span<bf16> os{static_cast<bf16*>(x_out), (size_t)(T * kStreams * D)};
-    if (D % 8 == 0 && T * D < kShortCounters) {
-        const bool gates_aligned = aligned16(h);
-        const int64_t vectors = D / 8;
-        // whole tokens per block where several fit, else the tile width that leaves the fewest threads idle
-        int threads = kThreads, tokens = 1, tiles = 1;
-        if (vectors <= kThreads / 2) {
-            tokens = kThreads / (int)vectors;
-        } else {
-            int64_t least = INT64_MAX;
-            for (int w = 128; w <= kThreads; w += 32) {
-                const int64_t used = (vectors + w - 1) / w * w;
-                if (used <= least) {
-                    least = used;
-                    threads = w;
-                }
-            }
-            tiles = (int)((vectors + threads - 1) / threads);
-        }
-        const int64_t blocks = tiles > 1 ? T * tiles : (T + tokens - 1) / tokens;
-        if (blocks <= INT32_MAX)
-            return launch_early(update_forward_vectors_kernel, dim3((unsigned)blocks), dim3(threads), 0, stream, T, D, tokens,
-                                tiles, gates_aligned, xs, ys, hs, d, os);
+    if (D >= 8 && T * D < kShortCounters && (D + 7) / 8 * T <= INT32_MAX) {
+        const VectorGrid grid((D + 7) / 8, kThreads);
+        return launch_early(D % 8 == 0 ? update_forward_vectors_kernel<false> : update_forward_vectors_kernel<true>,
+                            dim3(grid.blocks(T)), dim3(grid.threads), 0, stream, T, D, grid, aligned16(h), xs, ys, hs, d,
+                            os);
     }
-    return launch_early(D % 8 == 0 ? update_forward_kernel<8> : update_forward_kernel<1>, dim3((unsigned)T), dim3(kThreads),
-                        0, stream, D, xs, ys, hs, d, os);
+    return launch_early(update_forward_any_kernel, dim3((unsigned)T), dim3(kThreads), 0, stream, D, xs, ys, hs, d, os);
 }
 
 cudaError_t update_backward(int64_t T, int64_t D, const void* x, const void* y, const float* h,
@@ -505,15 +520,16 @@ cudaError_t update_backward(int64_t T, int64_t D, const void* x, const void* y, 
     const Span<const bf16> gs{static_cast<const bf16*>(grad_x_out), (size_t)(T * kStreams * D)};
     const Span<bf16> gys{static_cast<bf16*>(grad_y), (size_t)(T * D)};
     const Span<float> ghs{grad_h, (size_t)(T * kGates)};
-    if (D % 8 == 0 && T * D < kShortCounters) {
-        cudaError_t e = cudaSuccess;
-        if (update_backward_tokens<1, 2, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
-            update_backward_tokens<2, 1, 512>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
-            update_backward_tokens<2, 1, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream))
-            return e;
-    }
-    return launch_early(D % 8 == 0 ? update_backward_kernel<8> : update_backward_kernel<1>, dim3((unsigned)T),
-                        dim3(kThreads), 0, stream, D, xs, ys, hs, d, gs, gys, ghs);
+    cudaError_t e = cudaSuccess;
+    if (D >= 8 && T * D < kShortCounters &&
+        (D % 8 == 0 ? update_backward_tokens<false, 1, 2, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
+                          update_backward_tokens<false, 2, 1, 512>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
+                          update_backward_tokens<false, 2, 1, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream)
+                    : update_backward_tokens<true, 1, 2, 512>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
+                          update_backward_tokens<true, 2, 1, 512>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream)))
+        return e;
+    return launch_early(update_backward_any_kernel, dim3((unsigned)T), dim3(kThreads), 0, stream, D, xs, ys, hs, d, gs, gys,
+                        ghs);
 }
 
 cudaError_t setup() { return cudaSuccess; }

@@ -58,27 +58,33 @@ def check(name, got, ref, mag, chain, out="fp32"):
     assert ok, f"{name}: {worst:.3g} times the bound"
 
 
+def off_by(t, offset):
+    """A contiguous copy on the GPU that starts `offset` elements past an allocation's start."""
+    flat = torch.empty(t.numel() + offset, dtype=t.dtype, device=DEV)[offset:]
+    return flat.view(t.shape).copy_(t)
+
+
 # ---------------------------------------------------------------- embedding
-def embed_forward_case(T, V, D, n, type_, wide, seed, scale=0.7):
+def embed_forward_case(T, V, D, n, type_, wide, seed, scale=0.7, offset=0):
     g = gen(seed)
     table = normal(g, V, D, dtype=DTYPES[type_])
     ids = torch.randint(-1, V + 1, (T,), generator=g, dtype=torch.int64 if wide else torch.int32)
-    x = empty(T, n * D, dtype=torch.bfloat16)
-    m.mhc_embed_forward(ids.to(DEV), table.to(DEV), x, scale=scale)
+    x = off_by(empty(T, n * D, dtype=torch.bfloat16), 3 * offset)
+    m.mhc_embed_forward(off_by(ids, offset), off_by(table, offset), x, scale=scale)
     ref = S.embed_forward(ids.numpy(), np64(table), n, scale)
     check("x", x, ref, np.abs(ref), 2, "bf16")
 
 
-def embed_backward_case(T, V, D, n, wide, accumulate, seed, skew=False, scale=0.7):
+def embed_backward_case(T, V, D, n, wide, accumulate, seed, skew=False, scale=0.7, offset=0):
     g = gen(seed)
     ids = torch.randint(-1, V + 1, (T,), generator=g, dtype=torch.int64 if wide else torch.int32)
     if skew:   # most tokens are one id, some its neighbours
         ids[torch.rand(T, generator=g) < 0.8] = V // 2
     gx = normal(g, T, n * D, dtype=torch.bfloat16)
     start = normal(g, V, D) if accumulate else None
-    out = start.to(DEV) if accumulate else empty(V, D)
+    out = off_by(start if accumulate else empty(V, D), offset)
     ws = scratch(m.mhc_embed_workspace_bytes(T, V, D))
-    m.mhc_embed_backward(ids.to(DEV), gx.to(DEV), out, ws, scale=scale, accumulate=accumulate)
+    m.mhc_embed_backward(off_by(ids, offset), off_by(gx, 3 * offset), out, ws, scale=scale, accumulate=accumulate)
     ref, mag, chain = S.embed_backward(ids.numpy(), np64(gx), V, D, scale, None if start is None else np64(start))
     check("grad_table", out, ref, mag, chain)
     if not accumulate:

@@ -41,6 +41,23 @@ def test_embed_backward_one_frequent_id(T, V, D, accumulate):
     C.embed_backward_case(T, V, D, 4, True, accumulate, seed=T, skew=True)
 
 
+@pytest.mark.parametrize("D", [8, 40, 1031, 1032, 2056])
+@pytest.mark.parametrize("offset", [1, 2, 5])
+def test_embed_unaligned(D, offset):
+    """Tensors that start anywhere: rows begin and end inside 16-byte chunks."""
+    C.embed_forward_case(37, 50, D, 3, "fp32", True, seed=D, offset=offset)
+    C.embed_forward_case(37, 50, D, 4, "bf16", False, seed=D, offset=offset)
+    C.embed_backward_case(300, 41, D, 4, True, False, seed=D, offset=offset)
+    C.embed_backward_case(300, 41, D, 1, False, True, seed=D, offset=offset, skew=True)
+
+
+@pytest.mark.parametrize("D", [1, 2, 3, 5, 7, 9, 11, 13])
+def test_embed_rows_shorter_than_a_vector(D):
+    C.embed_forward_case(700, 30, D, 4, "bf16", True, seed=D)
+    C.embed_backward_case(700, 30, D, 4, True, False, seed=D)
+    C.embed_backward_case(700, 30, D, 2, True, True, seed=D)
+
+
 def test_embed_backward_same_bits():
     g = gen(5)
     T, V, D = 9000, 50, 264
@@ -252,7 +269,7 @@ def test_group_shapes(D):
         C.norm_backward_case(T, D, "fp32", seed=D)
 
 
-@pytest.mark.parametrize("D", [31, 33, 127, 257, 511, 1281, 2561, 4097])
+@pytest.mark.parametrize("D", [9, 15, 31, 33, 127, 255, 257, 511, 1281, 2049, 2561, 4095, 4097, 5119, 8191, 8193])
 def test_group_shapes_unaligned(D):
     T = min(2400, 2_000_000 // D)
     C.norm_forward_case(T, D, "bf16", seed=D)
