@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(int64_t T, int64
             uint4 raw = make_uint4(0u, 0u, 0u, 0u);
             const size_t piece = at + q * Elem<E>::kPack;
             if constexpr (SHIFT) {
-                if (valid > q * Elem<E>::kPack) raw = load_shifted(table, piece, valid - q * Elem<E>::kPack, 1);
+                if (valid > q * Elem<E>::kPack) raw = load_shifted<true>(table, piece, valid - q * Elem<E>::kPack, 1);
             } else {
                 if (table.has(piece, Elem<E>::kPack, 1)) raw = *reinterpret_cast<const uint4*>(table.p + piece);
             }
@@ -348,7 +348,7 @@ __device__ __forceinline__ void load_row(const SumArgs& a, size_t at, int valid,
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float2 f[2] = {pair(0.f), pair(0.f)};
-            if (valid > 4 * q) unpack<float>(load_shifted(in, at + 4 * q, valid - 4 * q, site), f);
+            if (valid > 4 * q) unpack<float>(load_shifted<true>(in, at + 4 * q, valid - 4 * q, site), f);
             v[4 * q] = f[0].x;
             v[4 * q + 1] = f[0].y;
             v[4 * q + 2] = f[1].x;
@@ -495,6 +495,13 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
         const auto fetch = [&](int item) {
             if (item < items) {
                 const size_t at = row_of(item) + c;
+                const uint32_t row = rows[item] & kRowMask;
+                if (SHIFT && (row == 0 || row + NS == (uint32_t)(a.T * a.n_streams))) {
+#pragma unroll 1
+                    for (int s = 0; s < NS; ++s)
+                        copy_shifted_edge(mine + (item % kItems * NS + s) * P, a.grad_x.p, a.grad_x.count, at + s * a.D,
+                                          (int)c, (int)a.D, 11);
+                } else
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
                     uint4* const slot = mine + (item % kItems * NS + s) * P;

@@ -262,6 +262,12 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, SHIFT, VPT, S>::kMaxThre
     const auto fetch = [&](int t, int stage) {
         if (t < T) {
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.x_stride + (uint32_t)c0);
+            if (SHIFT && (t == 0 || t == T - 1)) {
+#pragma unroll 1
+                for (int k = 0; k < Shape::kStage; ++k)
+                    copy_shifted_edge(mine + (stage * Shape::kStage + k) * P, a.x.p, a.x.count, at + k / A * step + k % A * D,
+                                      c0 + k / A * step, D, 0);
+            } else
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -558,6 +564,15 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
         if constexpr (SHIFT) {
             const size_t xo = at_row(t, a.x_stride) + v * step, go = at_row(t, a.gy_stride) + v * step;
             const int c = c0 + v * step;
+            if (t == 0 || t == T - 1) {
+#pragma unroll 1
+                for (int s = 0; s < A; ++s) {
+                    const Span<const E>& in = s < XA ? a.x : s == XA ? a.grad_y : a.grad_x_out;
+                    const size_t at = s < XA ? xo + s * D : s == XA ? go : xo + (s - XA - 1) * D;
+                    if (s <= XA || residual) copy_shifted_edge(dst + (v * A + s) * P, in.p, in.count, at, c, D, 0);
+                }
+                return;
+            }
 #pragma unroll
             for (int s = 0; s < XA; ++s) copy_shifted(dst + (v * A + s) * P, a.x, xo + s * D, c, D, 0);
             copy_shifted(dst + (v * A + XA) * P, a.grad_y, go, c, D, 5);

@@ -3,8 +3,9 @@
 // A row is still read and written in whole aligned 16-byte chunks: a vector of
 // kPack columns that starts m elements into a chunk lies in that chunk and the
 // next, and is put together from both with selects and funnel shifts.  A chunk
-// may hold elements of the neighbouring rows (read, never used); only chunks
-// that stick out of the operand itself are read element by element.
+// may hold elements of the neighbouring rows (read, never used); the chunks
+// that stick out of the operand itself, in its first and last row, are read
+// element by element.
 #pragma once
 #include "mhcs_common.cuh"
 #include "mhcs_ring.cuh"
@@ -69,26 +70,28 @@ __device__ __forceinline__ bool whole_chunk(const Span<const E>& in, ptrdiff_t f
     return first >= 0 && first + Elem<E>::kPack <= (ptrdiff_t)in.count;
 }
 
-// Copies the chunk whose first element is in.p[first] into a slot.
-template <typename E>
-__device__ __forceinline__ void copy_chunk(uint4* slot, const Span<const E>& in, ptrdiff_t first, uint32_t site) {
-    if (whole_chunk(in, first)) {
-        if (in.has((size_t)first, Elem<E>::kPack, site)) copy16(slot, in.p + first);
-    } else {
-        *slot = edge_chunk(in.p, in.count, first, site);
-    }
-}
 // A lane's share of a row of `width` columns for vectors of which the lane's
 // starts at element `at`, column c: its chunk, and lane 31's next one too.  The
-// warp's slots are 33 in a row.
+// warp's slots are 33 in a row.  Only the operand's first and last row can
+// have chunks that stick out of it: `edge` says that this is one of them.
 template <typename E>
 __device__ __forceinline__ void copy_shifted(uint4* slot, const Span<const E>& in, size_t at, int c, int width,
                                              uint32_t site) {
     constexpr int kPack = Elem<E>::kPack;
     const int m = misaligned(in.p + at);
-    if (c - m < width) copy_chunk(slot, in, (ptrdiff_t)at - m, site);
+    const size_t first = at - m;
+    if (c - m < width && in.has(first, kPack, site)) copy16(slot, in.p + first);
+    if ((threadIdx.x & 31) == 31 && m > 0 && c + kPack - m < width && in.has(first + kPack, kPack, site))
+        copy16(slot + 1, in.p + first + kPack);
+}
+template <typename E>
+__device__ __noinline__ void copy_shifted_edge(uint4* slot, const E* p, size_t count, size_t at, int c, int width,
+                                               uint32_t site) {
+    constexpr int kPack = Elem<E>::kPack;
+    const int m = misaligned(p + at);
+    if (c - m < width) slot[0] = edge_chunk(p, count, (ptrdiff_t)at - m, site);
     if ((threadIdx.x & 31) == 31 && m > 0 && c + kPack - m < width)
-        copy_chunk(slot + 1, in, (ptrdiff_t)at - m + kPack, site);
+        slot[1] = edge_chunk(p, count, (ptrdiff_t)at - m + kPack, site);
 }
 // The lane's vector in place of its chunk, columns past the row 0.  The whole
 // warp, after its copies have arrived and a __syncwarp.
@@ -102,20 +105,22 @@ __device__ __forceinline__ void realign(uint4* slot, int m, int valid) {
 }
 
 // The vector at element `at` of which `valid` columns belong to the row (the
-// others come back as 0).
-template <typename E>
+// others come back as 0).  CHECKED: it may lie in the operand's first or last
+// chunk; otherwise its chunks are known to be inside.
+template <bool CHECKED, typename E>
 __device__ __forceinline__ uint4 load_shifted(const Span<const E>& in, size_t at, int valid, uint32_t site) {
     constexpr int kPack = Elem<E>::kPack;
     const int m = misaligned(in.p + at);
-    const ptrdiff_t first = (ptrdiff_t)at - m;
     const auto chunk = [&](ptrdiff_t f) {
-        if (whole_chunk(in, f))
+        if (!CHECKED || whole_chunk(in, f))
             return in.has((size_t)f, kPack, site) ? *reinterpret_cast<const uint4*>(in.p + f) : make_uint4(0u, 0u, 0u, 0u);
         return edge_chunk(in.p, in.count, f, site);
     };
-    uint4 v = chunk(first);
-    if (m > 0) v = shift_take<E>(v, valid > kPack - m ? chunk(first + kPack) : make_uint4(0u, 0u, 0u, 0u), m);
-    return valid < kPack ? keep_first<E>(v, valid) : v;
+    const ptrdiff_t first = (ptrdiff_t)at - m;
+    uint4 a = chunk(first), b = make_uint4(0u, 0u, 0u, 0u);
+    if (m > 0 && valid > kPack - m) b = chunk(first + kPack);
+    a = shift_take<E>(a, b, m);
+    return valid < kPack ? keep_first<E>(a, valid) : a;
 }
 
 // Stores the lane's vector at element `at`, `valid` columns of it (all lanes of

@@ -92,40 +92,54 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const
     }
 }
 
-// Any size: one block per token, a column of every stream per thread and step.
-__global__ void __launch_bounds__(kThreads) update_forward_any_kernel(int64_t D, Span<const bf16> x,
-                                                                  Span<const bf16> y, Span<const float> h,
-                                                                  Drop d, Span<bf16> x_out) {
-    ptx::grid_dependency_wait();
-    constexpr int N = 1;
-    __shared__ float gate[kGates];
-    const int64_t t = blockIdx.x;
-    if (threadIdx.x < kGates) {
-        float v[1];
-        load_at<1>(h, t * kGates + threadIdx.x, v, 2);
-        gate[threadIdx.x] = v[0];
-    }
-    __syncthreads();
-    const DropKey key = drop_key(d);
-    const int64_t row = t * kStreams * D;
-    for (int64_t c = (int64_t)threadIdx.x * N; c < D; c += kThreads * N) {
-        float xs[kStreams][N], yv[N];
-        load_at<N>(y, t * D + c, yv, 3);
+// The gates of token t: 4 of H_post and 16 of H_res.
+__device__ __forceinline__ void gates_at(const Span<const float>& h, int64_t t, bool aligned, float (&g)[20]) {
+    if (aligned) {
 #pragma unroll
-        for (int j = 0; j < kStreams; ++j) load_at<N>(x, row + j * D + c, xs[j], 4);
-        drop<N>(d, key, (uint64_t)(t * D + c), yv);
+        for (int q = 0; q < 5; ++q) {
+            const size_t at = (size_t)t * kGates + 4 + 4 * q;
+            const float4 v = h.has(at, 4, 2) ? *reinterpret_cast<const float4*>(h.p + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            g[4 * q] = v.x;
+            g[4 * q + 1] = v.y;
+            g[4 * q + 2] = v.z;
+            g[4 * q + 3] = v.w;
+        }
+    } else {
 #pragma unroll
-        for (int i = 0; i < kStreams; ++i) {
-            float o[N];
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                o[k] = gate[4 + i] * yv[k];
-#pragma unroll
-                for (int j = 0; j < kStreams; ++j) o[k] = fmaf(gate[8 + 4 * i + j], xs[j][k], o[k]);
-            }
-            store_at<N>(x_out, row + i * D + c, o, 5);
+        for (int q = 0; q < 20; ++q) {
+            const size_t at = (size_t)t * kGates + 4 + q;
+            g[q] = h.has(at, 1, 2) ? h.p[at] : 0.f;
         }
     }
+}
+// One column of a token; gate: H_post and H_res.
+__device__ __forceinline__ void update_column(int64_t t, int64_t c, int64_t D, const float* gate, const Span<const bf16>& x,
+                                              const Span<const bf16>& y, const Drop& d, const DropKey& key,
+                                              const Span<bf16>& x_out) {
+    float xs[kStreams][1], yv[1];
+    load_at<1>(y, t * D + c, yv, 3);
+#pragma unroll
+    for (int j = 0; j < kStreams; ++j) load_at<1>(x, (t * kStreams + j) * D + c, xs[j], 4);
+    drop<1>(d, key, (uint64_t)(t * D + c), yv);
+#pragma unroll
+    for (int i = 0; i < kStreams; ++i) {
+        float o[1] = {gate[i] * yv[0]};
+#pragma unroll
+        for (int j = 0; j < kStreams; ++j) o[0] = fmaf(gate[4 + 4 * i + j], xs[j][0], o[0]);
+        store_at<1>(x_out, (t * kStreams + i) * D + c, o, 5);
+    }
+}
+
+// Any size: one block per token, a column of every stream per thread and step.
+__global__ void __launch_bounds__(kThreads) update_forward_any_kernel(int64_t D, Span<const bf16> x,
+                                                                      Span<const bf16> y, Span<const float> h,
+                                                                      Drop d, Span<bf16> x_out) {
+    ptx::grid_dependency_wait();
+    const int64_t t = blockIdx.x;
+    float gate[20];
+    gates_at(h, t, false, gate);
+    const DropKey key = drop_key(d);
+    for (int64_t c = threadIdx.x; c < D; c += kThreads) update_column(t, c, D, gate, x, y, d, key, x_out);
 }
 
 __global__ void __launch_bounds__(kThreads) update_backward_any_kernel(int64_t D, Span<const bf16> x,
@@ -183,26 +197,6 @@ __global__ void __launch_bounds__(kThreads) update_backward_any_kernel(int64_t D
 }
 
 // ------------------------------------------------------------ update, 16-byte vectors
-// The gates of token t: 4 of H_post and 16 of H_res.
-__device__ __forceinline__ void gates_at(const Span<const float>& h, int64_t t, bool aligned, float (&g)[20]) {
-    if (aligned) {
-#pragma unroll
-        for (int q = 0; q < 5; ++q) {
-            const size_t at = (size_t)t * kGates + 4 + 4 * q;
-            const float4 v = h.has(at, 4, 2) ? *reinterpret_cast<const float4*>(h.p + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-            g[4 * q] = v.x;
-            g[4 * q + 1] = v.y;
-            g[4 * q + 2] = v.z;
-            g[4 * q + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < 20; ++q) {
-            const size_t at = (size_t)t * kGates + 4 + q;
-            g[q] = h.has(at, 1, 2) ? h.p[at] : 0.f;
-        }
-    }
-}
 // f <- dropout of the eight elements from e on; *keep: which are kept.  ANY: e
 // need not be a multiple of 4, so the eight words come from three counters.
 template <bool ANY>
@@ -237,26 +231,31 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
     constexpr int N = 8, H = 4;
     const VectorPlace place = grid.place(T);
     const int64_t t = place.token;
-    const int c = place.vector * N, valid = place.valid ? (int)D - c : 0;
+    const int c = place.vector * N;
+    int valid = place.valid ? (int)D - c : 0;
     if (!SHIFT && valid <= 0) return;
     const size_t row = (size_t)t * (kStreams * D) + c, flat = (size_t)t * D + c;
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     uint4 xs[kStreams] = {none, none, none, none}, yr = none;
     float g[20] = {};
+    const DropKey key = drop_key(d);
     if (valid > 0) {
-        if constexpr (SHIFT) {
-            yr = load_shifted(y, flat, valid, 3);
-#pragma unroll
-            for (int j = 0; j < kStreams; ++j) xs[j] = load_shifted(x, row + j * D, valid, 4);
-        } else {
+        gates_at(h, t, gates_aligned, g);
+        if constexpr (!SHIFT) {
             if (y.has(flat, N, 3)) yr = *reinterpret_cast<const uint4*>(y.p + flat);
 #pragma unroll
             for (int j = 0; j < kStreams; ++j)
                 if (x.has(row + j * D, N, 4)) xs[j] = *reinterpret_cast<const uint4*>(x.p + row + j * D);
+        } else if (t == 0 || t == T - 1) {
+            // these tokens' chunks may stick out of the operands
+            for (int k = 0; k < N && k < valid; ++k) update_column(t, c + k, D, g, x, y, d, key, x_out);
+            valid = 0;
+        } else {
+            yr = load_shifted<false>(y, flat, valid, 3);
+#pragma unroll
+            for (int j = 0; j < kStreams; ++j) xs[j] = load_shifted<false>(x, row + j * D, valid, 4);
         }
-        gates_at(h, t, gates_aligned, g);
     }
-    const DropKey key = drop_key(d);
     float2 yv[H], o[kStreams][H];
     uint32_t keep;
     unpack<bf16>(yr, yv);
@@ -326,6 +325,15 @@ __global__ void __launch_bounds__(MAX, 1)
         const size_t flat = (size_t)((uint64_t)(uint32_t)t * (uint32_t)D + (uint32_t)c);
         const size_t row = (size_t)((uint64_t)(uint32_t)t * (uint32_t)(kStreams * D) + (uint32_t)c);
         if constexpr (SHIFT) {
+            if (t == 0 || t == T - 1) {
+#pragma unroll 1
+                for (int s = 0; s < A; ++s) {
+                    const Span<const bf16>& in = s < kStreams ? x : s < 2 * kStreams ? gout : y;
+                    const size_t at = s < 2 * kStreams ? row + (s % kStreams) * D : flat;
+                    copy_shifted_edge(dst + (v * A + s) * P, in.p, in.count, at, c, D, 4);
+                }
+                return;
+            }
 #pragma unroll
             for (int s = 0; s < kStreams; ++s) {
                 copy_shifted(dst + (v * A + s) * P, x, row + s * D, c, D, 4);
