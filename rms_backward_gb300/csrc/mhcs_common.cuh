@@ -187,15 +187,18 @@ __device__ __forceinline__ void store_at(const Span<E>& s, size_t i, const float
 
 // One thread per vector of a row, without loops: a block holds several whole
 // rows, or one of the tiles of a longer one, whichever leaves few threads idle.
+// whole_warps: every warp's vectors are of one row (its last ones may lie past
+// the row's end).
 struct VectorPlace {
     int64_t token;
     int vector;
-    bool valid;           // the thread has a vector (of a token below T)
-    bool before, after;   // the lanes below and above hold the vectors next to it in the row
+    bool valid;   // the thread has a vector of a token below T
 };
 struct VectorGrid {
     int vectors, threads, tokens, tiles;
-    VectorGrid(int64_t per_row, int most) : vectors((int)per_row), threads(most), tokens(1), tiles(1) {
+    VectorGrid(int64_t per_row, int most, bool whole_warps) : threads(most), tokens(1), tiles(1) {
+        if (whole_warps) per_row = (per_row + 31) / 32 * 32;
+        vectors = (int)per_row;
         if (per_row <= most / 2) {
             tokens = most / vectors;
             return;
@@ -217,13 +220,12 @@ struct VectorGrid {
             p.token = (int64_t)blockIdx.x * tokens + threadIdx.x / vectors;
             p.vector = (int)(threadIdx.x % vectors);
             p.valid = threadIdx.x < tokens * vectors && p.token < T;
+            if (threadIdx.x >= tokens * vectors) p.token = T;   // no row
         } else {
             p.token = blockIdx.x / tiles;
             p.vector = (int)(blockIdx.x % tiles) * (int)blockDim.x + (int)threadIdx.x;
             p.valid = p.vector < vectors;
         }
-        p.before = (threadIdx.x & 31) > 0 && p.vector > 0;
-        p.after = (threadIdx.x & 31) < 31 && p.vector + 1 < vectors;
         return p;
     }
 };

@@ -25,7 +25,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
-#include "mhcs_shift.cuh"
+#include "mhcs_words.cuh"
 #include "ptx.cuh"
 
 namespace mhcpb {
@@ -71,30 +71,58 @@ __device__ __forceinline__ int64_t id_at(const Span<const I>& ids, int64_t t, in
 }
 
 // ------------------------------------------------------------ forward
-// Eight columns per thread; SHIFT: rows at any address, D of any size.
-template <typename E, typename I, bool SHIFT>
+// Eight columns per thread; WORDS: rows at any address (mhcs_words.cuh), D of any size.
+template <typename E, typename I, bool WORDS>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(int64_t T, int64_t V, int64_t D, VectorGrid grid,
                                                                 int n_streams, float scale, Span<const E> table,
                                                                 Span<const I> ids, Span<bf16> x) {
-    ptx::grid_dependency_wait();
     constexpr int N = 8, kParts = N / Elem<E>::kPack, H = Elem<E>::kPack / 2;
+    __shared__ uint4 parts[WORDS ? kLookupThreads / 32 * kParts * kWarpSlots : 1];
+    ptx::grid_dependency_wait();
     const VectorPlace place = grid.place(T);
     const int64_t t = place.token;
-    const int c = place.vector * N, valid = place.valid ? (int)D - c : 0;
-    if (!SHIFT && valid <= 0) return;
-    const int64_t id = valid > 0 ? id_at(ids, t, V, 0) : V;
+    const int c = place.vector * N, lane = threadIdx.x & 31;
+    if (WORDS ? t >= T : !place.valid) return;   // WORDS: whole warps of one token
+    const int64_t id = id_at(ids, t, V, 0);
     float2 v[N / 2];
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) v[k] = pair(0.f);
+    uint4* const mine = parts + (WORDS ? (threadIdx.x >> 5) * (kParts * kWarpSlots) : 0);
     if (id < V) {
         const size_t at = (size_t)(id * D + c);
+        if constexpr (WORDS) {
+            // FP32: two parts of 32 vectors, traded so that a lane gets eight columns
+            const bool edge = id == 0 || id == V - 1;
+            const size_t first = at - lane * N;
+            const int width = (int)D - c + lane * N;
+            if (edge) {
+#pragma unroll 1
+                for (int q = 0; q < kParts; ++q)
+                    copy_edge(mine + q * kWarpSlots, table.p, table.count, first + q * 32 * Elem<E>::kPack,
+                                  width - q * 32 * Elem<E>::kPack, 1);
+            } else {
+#pragma unroll
+                for (int q = 0; q < kParts; ++q)
+                    copy_chunks(mine + q * kWarpSlots, table, first + q * 32 * Elem<E>::kPack,
+                                width - q * 32 * Elem<E>::kPack, 1);
+            }
+            copies_commit();
+            copies_wait<0>();
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+                align_chunks<E>(mine + q * kWarpSlots, misaligned(table.p + first),
+                                width - (q * 32 + lane) * Elem<E>::kPack);
+            __syncwarp();
+        }
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
             uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-            const size_t piece = at + q * Elem<E>::kPack;
-            if constexpr (SHIFT) {
-                if (valid > q * Elem<E>::kPack) raw = load_shifted<true>(table, piece, valid - q * Elem<E>::kPack, 1);
+            if constexpr (WORDS) {
+                const int vector = lane * kParts + q;
+                raw = mine[vector / 32 * kWarpSlots + vector % 32];
             } else {
+                const size_t piece = at + q * Elem<E>::kPack;
                 if (table.has(piece, Elem<E>::kPack, 1)) raw = *reinterpret_cast<const uint4*>(table.p + piece);
             }
             float2 f[H];
@@ -102,12 +130,13 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(int64_t T, int64
 #pragma unroll
             for (int k = 0; k < H; ++k) v[q * H + k] = mul2(f[k], pair(scale));
         }
+        if (WORDS) __syncwarp();
     }
     const uint4 out = pack<bf16>(v);
     for (int s = 0; s < n_streams; ++s) {
         const size_t at = (size_t)((t * n_streams + s) * D + c);
-        if constexpr (SHIFT) {
-            store_shifted(x, at, valid, place.before, place.after, out, 2);
+        if constexpr (WORDS) {
+            store_words(mine, x, at - lane * N, (int)D - c + lane * N, out, 2);
         } else {
             if (x.has(at, N, 2)) *reinterpret_cast<uint4*>(x.p + at) = out;
         }
@@ -271,8 +300,8 @@ __device__ __forceinline__ int64_t lower_bound_warp(const Span<const uint64_t>& 
     return lo;
 }
 
-// A thread's columns: eight of a row.  SHIFT: rows of grad_x and of the table at
-// any address (mhcs_shift.cuh); the workspace's rows have a pitch of whole
+// A thread's columns: eight of a row.  WORDS: rows of grad_x and of the table at
+// any address (mhcs_words.cuh); the workspace's rows have a pitch of whole
 // vectors.
 struct SumArgs {
     int64_t T, V, D, pitch, chunk, chunks, slabs;
@@ -309,95 +338,78 @@ __device__ __forceinline__ void store_floats(const Span<float>& s, size_t at, co
         store_at<N>(s, at, v, site);
     }
 }
-// The same for rows at any address: all lanes of a warp, lane l holding columns
-// c + 8 l ..., `valid` of them in the row.  As store_shifted, with two 16-byte
-// vectors per lane: two whole chunks, then what the next lane's first covers.
-__device__ __forceinline__ void store_floats_shifted(const Span<float>& s, size_t at, int valid, const float (&v)[N],
-                                                     uint32_t site) {
-    const auto word = [](const float* f) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    };
-    const int lane = threadIdx.x & 31;
-    const uint4 a = word(v), b = word(v + 4);
-    uint4 low;
-    low.x = __shfl_up_sync(kFullMask, b.x, 1);
-    low.y = __shfl_up_sync(kFullMask, b.y, 1);
-    low.z = __shfl_up_sync(kFullMask, b.z, 1);
-    low.w = __shfl_up_sync(kFullMask, b.w, 1);
-    if (valid <= 0) return;
-    const int m = misaligned(s.p + at), head = 4 - m;
-    const bool first = (m == 0 || lane > 0) && valid >= head, second = valid >= 4 + head;
-    if (first && s.has(at - m, 4, site))
-        *reinterpret_cast<uint4*>(s.p + at - m) = m == 0 ? a : shift_take<float>(low, a, head);
-    if (second && s.has(at + head, 4, site))
-        *reinterpret_cast<uint4*>(s.p + at + head) = m == 0 ? b : shift_take<float>(a, b, head);
-    // the lane above covers the last m, if its first chunk is whole
-    const bool rest = m > 0 && second && !(lane < 31 && valid - N >= head);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const bool covered = k < head ? first : k < 4 + head ? second : !rest && second;
-        if (!covered && k < valid && s.has(at + k, 1, site)) s.p[at + k] = v[k];
-    }
-}
-template <bool SHIFT>
-__device__ __forceinline__ void load_row(const SumArgs& a, size_t at, int valid, float (&v)[N], uint32_t site) {
-    if constexpr (!SHIFT) {
-        if (valid > 0) load_floats(a.table, at, v, site);
-    } else {
-        const Span<const float> in{a.table.p, a.table.count};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float2 f[2] = {pair(0.f), pair(0.f)};
-            if (valid > 4 * q) unpack<float>(load_shifted<true>(in, at + 4 * q, valid - 4 * q, site), f);
-            v[4 * q] = f[0].x;
-            v[4 * q + 1] = f[0].y;
-            v[4 * q + 2] = f[1].x;
-            v[4 * q + 3] = f[1].y;
-        }
-    }
-}
-template <bool SHIFT>
-__device__ __forceinline__ void store_row(const SumArgs& a, size_t at, int valid, const float (&v)[N], uint32_t site) {
-    if constexpr (!SHIFT) {
-        if (valid > 0) store_floats(a.table, at, v, site);
-    } else {
-        store_floats_shifted(a.table, at, valid, v, site);
-    }
-}
-
 // A finished row of the gradient.  When accumulating, its old values are read
 // when the row is finished and added when the next one is (or at the end), so
 // that the read's latency is not waited for.  All lanes of a warp call it.
-template <bool SHIFT>
+// WORDS: the lanes first trade their eight columns for columns lane, lane + 32,
+// ... of the warp's 256, so that each access takes consecutive words.
+template <bool WORDS>
 struct RowWriter {
     int64_t key = -1;
     float sum[N], old[N];
+    float* trade;         // WORDS: the warp's 256 floats of shared memory
+
+    // the thread's columns of row `row`: at() + k * kStride for k < N, those below D
+    static constexpr int kStride = WORDS ? 32 : 1;
+    static __device__ __forceinline__ int64_t column(int64_t c) {
+        const int lane = threadIdx.x & 31;
+        return WORDS ? c - lane * N + lane : c;
+    }
+    __device__ __forceinline__ void store(const SumArgs& a, int64_t row, int64_t c, const float (&v)[N]) {
+        const size_t at = (size_t)(row * a.D + column(c));
+        if constexpr (!WORDS) {
+            if (c < a.D) store_floats(a.table, at, v, 12);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (column(c) + 32 * k < a.D && a.table.has(at + 32 * k, 1, 12)) a.table.p[at + 32 * k] = v[k];
+        }
+    }
     __device__ __forceinline__ void complete(const SumArgs& a, int64_t c) {
         if (key < 0) return;
 #pragma unroll
         for (int k = 0; k < N; ++k) old[k] = fmaf(a.scale, sum[k], old[k]);
-        store_row<SHIFT>(a, (size_t)(key * a.D + c), (int)(a.D - c), old, 12);
+        store(a, key, c, old);
         key = -1;
     }
     __device__ __forceinline__ void write(const SumArgs& a, int64_t row, int64_t c, const float (&acc)[N]) {
-        const size_t at = (size_t)(row * a.D + c);
-        if (!a.accumulate) {
-            float v[N];
+        float v[N];
+        if constexpr (WORDS) {
+            const int lane = threadIdx.x & 31;
+            __syncwarp();
+            float4* const mine = reinterpret_cast<float4*>(trade) + 2 * lane;
+            mine[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            mine[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            __syncwarp();
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = a.scale * acc[k];
-            store_row<SHIFT>(a, at, (int)(a.D - c), v, 12);
+            for (int k = 0; k < N; ++k) v[k] = trade[lane + 32 * k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = acc[k];
+        }
+        if (!a.accumulate) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] *= a.scale;
+            store(a, row, c, v);
             return;
         }
         complete(a, c);
         key = row;
+        const size_t at = (size_t)(row * a.D + column(c));
 #pragma unroll
-        for (int k = 0; k < N; ++k) sum[k] = acc[k];
-        load_row<SHIFT>(a, at, (int)(a.D - c), old, 12);
+        for (int k = 0; k < N; ++k) sum[k] = v[k];
+        if constexpr (!WORDS) {
+            if (c < a.D) load_floats(a.table, at, old, 12);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                old[k] = column(c) + 32 * k < a.D && a.table.has(at + 32 * k, 1, 12) ? a.table.p[at + 32 * k] : 0.f;
+        }
     }
 };
 
 // Each warp zeroes the absent ones of its own kZeroRows / 4 rows.
-template <bool SHIFT>
+template <bool WORDS>
 __device__ void zero_rows(const SumArgs& a, int64_t first) {
     constexpr int kPerWarp = kZeroRows / (kThreads / 32);
     const int lane = threadIdx.x & 31;
@@ -413,7 +425,7 @@ __device__ void zero_rows(const SumArgs& a, int64_t first) {
         if (next == v) continue;
         // whole chunks, and single elements before the first and after the last
         const size_t row = (size_t)(v * a.D);
-        const int m = SHIFT ? misaligned(a.table.p + row) : 0;
+        const int m = WORDS ? (int)(reinterpret_cast<uintptr_t>(a.table.p + row) >> 2 & 3) : 0;
         const int64_t lead = m == 0 ? 0 : 4 - m < a.D ? 4 - m : a.D, body = (a.D - lead) / 4;
         if (lane < lead) store_at<1>(a.table, row + lane, one, 9);
         for (int64_t k = lane; k < body; k += 32) store_at<4>(a.table, row + lead + 4 * k, zero, 9);
@@ -422,8 +434,8 @@ __device__ void zero_rows(const SumArgs& a, int64_t first) {
 }
 
 // Writes the sum of the run that ends at an item, or its piece in this chunk.
-template <bool SHIFT>
-__device__ __forceinline__ void flush(const SumArgs& a, RowWriter<SHIFT>& out, int64_t chunk, int64_t key, int64_t c,
+template <bool WORDS>
+__device__ __forceinline__ void flush(const SumArgs& a, RowWriter<WORDS>& out, int64_t chunk, int64_t key, int64_t c,
                                       bool whole, bool began, float (&acc)[N]) {
     if (whole)
         out.write(a, key, c, acc);
@@ -445,27 +457,30 @@ __device__ __forceinline__ void flush(const SumArgs& a, RowWriter<SHIFT>& out, i
 // The rows come through per-thread copies, kAhead items of one row or
 // kAhead / 2 of four ahead.
 constexpr uint32_t kRunEnds = 1u << 31, kFlush = 1u << 30, kRowMask = kFlush - 1;   // T n_streams <= 2^28
-template <bool SHIFT, int NS>
+template <bool WORDS, int NS>
 __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
     ptx::grid_dependency_wait();
     if ((int64_t)blockIdx.x >= a.chunks * a.slabs) {
-        zero_rows<SHIFT>(a, ((int64_t)blockIdx.x - a.chunks * a.slabs) * kZeroRows);
+        zero_rows<WORDS>(a, ((int64_t)blockIdx.x - a.chunks * a.slabs) * kZeroRows);
         return;
     }
     constexpr int kItems = NS == 1 ? kAhead : kAhead / 2;
-    constexpr int P = SHIFT ? kThreads / 32 * 33 : kThreads;
+    constexpr int P = WORDS ? kThreads / 32 * kWarpSlots : kThreads;
     __shared__ uint32_t rows[kBatch * (NS == 1 ? MHCPB_MAX_STREAMS : 1)];
     __shared__ uint32_t ids[kBatch];
     __shared__ int listed;
     __shared__ uint4 ring[kItems * NS * P];
+    __shared__ float trade[WORDS ? kThreads * N : 1];
     const int per_token = NS == 1 ? a.n_streams : 1;   // items
     const int64_t chunk = blockIdx.x / a.slabs;
     const int64_t c = ((int64_t)(blockIdx.x % a.slabs) * kThreads + threadIdx.x) * N;
     const int64_t begin = chunk * a.chunk;
     const int64_t end = begin + a.chunk < a.T ? begin + a.chunk : a.T;
     bool began = begin == 0 || key_at(a.order, begin - 1, 10) != key_at(a.order, begin, 10);
-    uint4* const mine = ring + (SHIFT ? (threadIdx.x >> 5) * 33 + (threadIdx.x & 31) : threadIdx.x);
-    RowWriter<SHIFT> out;
+    const int lane = threadIdx.x & 31;
+    uint4* const mine = ring + (WORDS ? (threadIdx.x >> 5) * kWarpSlots + lane : threadIdx.x);
+    RowWriter<WORDS> out;
+    out.trade = trade + (WORDS ? (threadIdx.x >> 5) * 32 * N : 0);
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
@@ -494,19 +509,20 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
         const auto row_of = [&](int item) { return (size_t)(rows[item] & kRowMask) * a.D; };
         const auto fetch = [&](int item) {
             if (item < items) {
-                const size_t at = row_of(item) + c;
                 const uint32_t row = rows[item] & kRowMask;
-                if (SHIFT && (row == 0 || row + NS == (uint32_t)(a.T * a.n_streams))) {
+                const size_t at = (size_t)row * a.D + c;
+                const int width = (int)(a.D - c) + lane * N;   // from the warp's first column on
+                if (WORDS && (row == 0 || row + NS == (uint32_t)(a.T * a.n_streams))) {
 #pragma unroll 1
                     for (int s = 0; s < NS; ++s)
-                        copy_shifted_edge(mine + (item % kItems * NS + s) * P, a.grad_x.p, a.grad_x.count, at + s * a.D,
-                                          (int)c, (int)a.D, 11);
+                        copy_edge(mine + (item % kItems * NS + s) * P - lane, a.grad_x.p, a.grad_x.count,
+                                      at + s * a.D - lane * N, width, 11);
                 } else
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
                     uint4* const slot = mine + (item % kItems * NS + s) * P;
-                    if constexpr (SHIFT) {
-                        copy_shifted(slot, a.grad_x, at + s * a.D, (int)c, (int)a.D, 11);
+                    if constexpr (WORDS) {
+                        copy_chunks(slot - lane, a.grad_x, at + s * a.D - lane * N, width, 11);
                     } else if (c < a.D) {
                         if (a.grad_x.has(at + s * a.D, N, 11)) copy16(slot, a.grad_x.p + at + s * a.D);
                     }
@@ -519,28 +535,27 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
         int position = 0, part = 0;   // of the item: its token in the batch, its row of the token
         for (int item = 0; item < items; ++item) {
             copies_wait<kItems - 1>();
-            if (SHIFT) __syncwarp();   // a lane reads the next lane's chunk too
+            if (WORDS) __syncwarp();
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
-                const uint4* const slot = mine + (item % kItems * NS + s) * P;
-                uint4 raw = slot[0];
-                if constexpr (SHIFT) {
-                    const int m = misaligned(a.grad_x.p + row_of(item) + s * a.D);
-                    if (m > 0) raw = shift_take<bf16>(raw, slot[1], m);
+                uint4* const slot = mine + (item % kItems * NS + s) * P;
+                if constexpr (WORDS) {
+                    const bf16* const p = a.grad_x.p + row_of(item) + s * a.D + (c - lane * N);
+                    align_chunks<bf16>(slot - lane, misaligned(p), (int)(a.D - c));
                 }
                 float2 v[4];
-                unpack<bf16>(raw, v);
+                unpack<bf16>(slot[0], v);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     acc[2 * k] += v[k].x;
                     acc[2 * k + 1] += v[k].y;
                 }
             }
-            if (SHIFT) __syncwarp();
+            if (WORDS) __syncwarp();
             const uint32_t row = rows[item];
             fetch(item + kItems);
             if (row & kFlush) {
-                flush<SHIFT>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
+                flush<WORDS>(a, out, chunk, ids[position], c, began && (row & kRunEnds), began, acc);
                 began = true;
             }
             if (NS > 1 || ++part == per_token) {
@@ -557,9 +572,10 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
 // a time: each of kJoinParts groups of threads a part of them in order, then
 // the parts in order.
 constexpr int kJoinParts = 4;
-template <bool SHIFT>
+template <bool WORDS>
 __global__ void __launch_bounds__(kThreads * kJoinParts) join_runs_kernel(SumArgs a) {
     __shared__ float sums[kJoinParts - 1][N][kThreads];
+    __shared__ float trade[WORDS ? kThreads * N : 1];
     ptx::grid_dependency_wait();
     const int lane = threadIdx.x % kThreads, part = threadIdx.x / kThreads;
     const int64_t work = (int64_t)a.heads.p[0] * a.slabs;
@@ -594,7 +610,8 @@ __global__ void __launch_bounds__(kThreads * kJoinParts) join_runs_kernel(SumArg
         for (int p = 0; p < kJoinParts - 1; ++p)
 #pragma unroll
             for (int k = 0; k < N; ++k) acc[k] += sums[p][k][lane];
-        RowWriter<SHIFT> out;
+        RowWriter<WORDS> out;
+        out.trade = trade + (WORDS ? (lane >> 5) * 32 * N : 0);
         out.write(a, key, c, acc);
         out.complete(a, c);
     }
@@ -606,7 +623,7 @@ cudaError_t lookup_typed(const Args& a, cudaStream_t stream) {
     const Span<const I> ids{static_cast<const I*>(a.ids), (size_t)a.T};
     const Span<bf16> x{static_cast<bf16*>(a.x), (size_t)(a.T * a.n_streams * a.D)};
     const bool packed = a.D % 8 == 0 && aligned16(a.table) && aligned16(a.x);
-    const VectorGrid grid((a.D + 7) / 8, kLookupThreads);
+    const VectorGrid grid((a.D + 7) / 8, kLookupThreads, !packed);
     return launch_early(packed ? lookup_kernel<E, I, false> : lookup_kernel<E, I, true>, dim3(grid.blocks(a.T)),
                         dim3(grid.threads), 0, stream, a.T, a.V, a.D, grid, a.n_streams, a.scale, table, ids, x);
 }
@@ -615,14 +632,14 @@ cudaError_t lookup_ids(const Args& a, cudaStream_t stream) {
     return a.id_bytes == 8 ? lookup_typed<E, int64_t>(a, stream) : lookup_typed<E, int32_t>(a, stream);
 }
 
-template <bool SHIFT>
+template <bool WORDS>
 cudaError_t sum_typed(const SumArgs& s, cudaStream_t stream) {
     const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
-    cudaError_t e = launch_early(s.n_streams == 4 ? sum_runs_kernel<SHIFT, 4> : sum_runs_kernel<SHIFT, 1>,
+    cudaError_t e = launch_early(s.n_streams == 4 ? sum_runs_kernel<WORDS, 4> : sum_runs_kernel<WORDS, 1>,
                                  dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
     const int64_t most = s.chunks * s.slabs < kJoinBlocks ? s.chunks * s.slabs : kJoinBlocks;
-    return launch_early(join_runs_kernel<SHIFT>, dim3((unsigned)most), dim3(kThreads * kJoinParts), 0, stream, s);
+    return launch_early(join_runs_kernel<WORDS>, dim3((unsigned)most), dim3(kThreads * kJoinParts), 0, stream, s);
 }
 
 }  // namespace

@@ -18,7 +18,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
-#include "mhcs_shift.cuh"
+#include "mhcs_words.cuh"
 #include "ptx.cuh"
 
 namespace mhcpb {
@@ -224,61 +224,63 @@ __global__ void __launch_bounds__(640) forward_rows_kernel(Params<E> a, int G, i
 // about it) and publishes both, so that one barrier gives the row's statistics
 // without cancellation: mean = sum n_w m_w / D and
 // D var = sum q_w + sum n_w (m_w - mean)^2.
-template <typename E, bool MIX, bool SHIFT, int VPT, int S>
+template <typename E, bool MIX, bool WORDS, int VPT, int S>
 struct ForwardShape {
     static constexpr int N = Elem<E>::kPack;
     static constexpr int kMaxThreads = 640;
     static constexpr int kArrays = MIX ? kStreams : 1;
     static constexpr int kStage = VPT * kArrays;
-    static constexpr int kPitch = SHIFT ? kMaxThreads / 32 * 33 : kMaxThreads;
+    static constexpr int kPitch = WORDS ? kMaxThreads / 32 * kWarpSlots : kMaxThreads;
     static constexpr int kSlots = S * kStage;
     static constexpr int kVectorSlots = 2 * VPT * N / 4;   // gamma and beta of a thread's columns
     static size_t bytes(int G, int R) {
-        return (size_t)kPitch * kSlots * 16 + (size_t)G * kVectorSlots * 16 + (size_t)R * (G / 32 * S * 16 + 2 * 2 * 32 * 4);
+        return (size_t)kPitch * kSlots * 16 + (size_t)G * kVectorSlots * 16 + (size_t)R * (G / 32 * S * 16 + 2 * 2 * 32 * 4) +
+               (WORDS ? (size_t)R * G * 16 : 0);   // what a warp stores
     }
 };
 
-template <typename E, bool MIX, bool SHIFT, int VPT, int S>
-__global__ void __launch_bounds__((ForwardShape<E, MIX, SHIFT, VPT, S>::kMaxThreads), 1)
+template <typename E, bool MIX, bool WORDS, int VPT, int S>
+__global__ void __launch_bounds__((ForwardShape<E, MIX, WORDS, VPT, S>::kMaxThreads), 1)
     forward_ring_kernel(Params<E> a, int G, int R) {
-    using Shape = ForwardShape<E, MIX, SHIFT, VPT, S>;
+    using Shape = ForwardShape<E, MIX, WORDS, VPT, S>;
     constexpr int N = Shape::N, H = N / 2, P = Shape::kPitch, A = Shape::kArrays;
     extern __shared__ uint4 slots[];
     const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
     const int warp = i >> 5, warps = G >> 5;
-    uint4* const mine = slots + (SHIFT ? (tid >> 5) * 33 + lane : tid);
+    uint4* const mine = slots + (WORDS ? (tid >> 5) * kWarpSlots + lane : tid);
     float4* const vectors = reinterpret_cast<float4*>(slots + P * Shape::kSlots);   // [2][VPT N / 4][G]
     float* const floats = reinterpret_cast<float*>(vectors + Shape::kVectorSlots * G);
     float* const gates = floats + (tid >> 5) * (S * 4);                             // [S][4] per warp
     float* const sums = floats + (NT >> 5) * (S * 4) + group * (2 * 2 * 32);        // [2][2][32]
+    uint4* const buffer = reinterpret_cast<uint4*>(floats + (NT >> 5) * (S * 4) + R * (2 * 2 * 32)) + (tid >> 5) * 32;
     const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group, T = (int)a.T;
     const int c0 = i * N, step = G * N, D = (int)a.D;
 
     // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
     for (int k = 0; k < Shape::kSlots; ++k)
-        if (!SHIFT && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+        if (!WORDS && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
     ptx::grid_dependency_wait();
     const auto fetch = [&](int t, int stage) {
         if (t < T) {
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.x_stride + (uint32_t)c0);
-            if (SHIFT && (t == 0 || t == T - 1)) {
+            if (WORDS && (t == 0 || t == T - 1)) {
 #pragma unroll 1
                 for (int k = 0; k < Shape::kStage; ++k)
-                    copy_shifted_edge(mine + (stage * Shape::kStage + k) * P, a.x.p, a.x.count, at + k / A * step + k % A * D,
-                                      c0 + k / A * step, D, 0);
-            } else
+                    copy_edge(mine - lane + (stage * Shape::kStage + k) * P, a.x.p, a.x.count,
+                                  at + k / A * step + k % A * D - lane * N, D - (c0 + k / A * step) + lane * N, 0);
+            } else {
 #pragma unroll
-            for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                for (int s = 0; s < A; ++s) {
-                    uint4* const slot = mine + ((stage * VPT + v) * A + s) * P;
-                    if constexpr (SHIFT) {
-                        copy_shifted(slot, a.x, at + v * step + s * D, c0 + v * step, D, 0);
-                    } else if (c0 + v * step < D) {
-                        if (a.x.has(at + v * step + s * D, N, 0)) copy16(slot, a.x.p + at + v * step + s * D);
+                for (int k = 0; k < Shape::kStage; ++k) {
+                    uint4* const slot = mine + (stage * Shape::kStage + k) * P;
+                    const size_t from = at + k / A * step + k % A * D;
+                    if constexpr (WORDS) {
+                        copy_chunks(slot - lane, a.x, from - lane * N, D - (c0 + k / A * step) + lane * N, 0);
+                    } else if (c0 + k / A * step < D) {
+                        if (a.x.has(from, N, 0)) copy16(slot, a.x.p + from);
                     }
                 }
+            }
             if (MIX && lane < kStreams && a.h.has((size_t)t * kGates + lane, 1, 1))
                 copy4(gates + stage * 4 + lane, a.h.p + (size_t)t * kGates + lane);
         }
@@ -291,8 +293,8 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, SHIFT, VPT, S>::kMaxThre
         for (int k = 0; k < Shape::kVectorSlots / 2; ++k) {
             const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
             float g[4] = {}, b[4] = {};
-            four_at<SHIFT>(a.gamma, c, D, 1.f, g);
-            four_at<SHIFT>(a.beta, c, D, 0.f, b);
+            four_at<WORDS>(a.gamma, c, D, 1.f, g);
+            four_at<WORDS>(a.beta, c, D, 0.f, b);
             vectors[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
             vectors[(Shape::kVectorSlots / 2 + k) * G + i] = make_float4(b[0], b[1], b[2], b[3]);
         }
@@ -315,10 +317,10 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, SHIFT, VPT, S>::kMaxThre
         copies_wait<S - 1>();
         __syncwarp();
         uint4* const row = mine + stage * (Shape::kStage * P);
-        if constexpr (SHIFT)
+        if constexpr (WORDS)
 #pragma unroll
             for (int k = 0; k < Shape::kStage; ++k)
-                realign<E>(row + k * P, misaligned(a.x.p + (size_t)t * a.x_stride + k % A * D), D - (c0 + k / A * step));
+                align_chunks<E>(row - lane + k * P, misaligned(a.x.p + (size_t)t * a.x_stride + k % A * D), D - (c0 + k / A * step));
         float2 u[VPT][H], s2 = pair(0.f);
         float p4[kStreams] = {};
         if constexpr (MIX) {
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, SHIFT, VPT, S>::kMaxThre
 #pragma unroll
                 for (int k = 0; k < H; ++k) {
                     float2 d = add2(u[v][k], pair(-m_mine));
-                    if (SHIFT) {   // a row may end inside the vector
+                    if (WORDS) {   // a row may end inside the vector
                         if (c0 + v * step + 2 * k >= D) d.x = 0.f;
                         if (c0 + v * step + 2 * k + 1 >= D) d.y = 0.f;
                     }
@@ -388,8 +390,8 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, SHIFT, VPT, S>::kMaxThre
                 o[2 * k + 1] = fma2(mul2(add2(u[v][2 * k + 1], mean2), rstd2), make_float2(g.z, g.w), make_float2(b.z, b.w));
             }
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.y_stride + (uint32_t)(c0 + v * step));
-            if constexpr (SHIFT) {
-                store_shifted(a.y, at, D - (c0 + v * step), lane > 0, lane < 31, pack<E>(o), 3);
+            if constexpr (WORDS) {
+                store_words(buffer, a.y, at - lane * N, D - (c0 + v * step) + lane * N, pack<E>(o), 3);
             } else {
                 if (c0 + v * step < D && a.y.has(at, N, 3)) *reinterpret_cast<uint4*>(a.y.p + at) = pack<E>(o);
             }
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) backward_columns_any_kernel(Params<E
 // slots again (cheaper than holding u and w in registers), writes the
 // gradients and refills each slot as it leaves it.  The other groups of the
 // block compute while one waits.
-template <typename E, bool MIX, bool SHIFT, int VPT, int S, int MAX>
+template <typename E, bool MIX, bool WORDS, int VPT, int S, int MAX>
 struct RowsShape {
     static constexpr int N = Elem<E>::kPack;
     static constexpr int kMaxThreads = MAX;   // 640: 96 registers a thread; 512: 128
@@ -519,8 +521,8 @@ struct RowsShape {
     static constexpr int kStage = VPT * kArrays;                    // 16-byte slots of a row
     // Slot k of every thread of the block lies together, so that a warp's copy
     // writes whole 128-byte lines; the pitch is a constant, for immediate
-    // offsets.  SHIFT: rows at any address, a warp's 33 chunks (mhcs_shift.cuh).
-    static constexpr int kPitch = SHIFT ? kMaxThreads / 32 * 33 : kMaxThreads;
+    // offsets.  WORDS: rows at any address (mhcs_words.cuh).
+    static constexpr int kPitch = WORDS ? kMaxThreads / 32 * kWarpSlots : kMaxThreads;
     static constexpr int kSlots = S * kStage;
     static constexpr int kGammaSlots = VPT * N / 4;                 // per thread of a group, FP32
     static constexpr int kWarpFloats = S * 32;                      // per row: 24 gates, mean, rstd
@@ -528,23 +530,25 @@ struct RowsShape {
     static constexpr int kGroupFloats = 2 * kSums * 32;
     static size_t bytes(int G, int R) {
         return (size_t)kPitch * kSlots * 16 + (size_t)G * kGammaSlots * 16 +
-               (size_t)R * (G / 32 * kWarpFloats * 4 + kGroupFloats * 4);
+               (size_t)R * (G / 32 * kWarpFloats * 4 + kGroupFloats * 4) + (WORDS ? (size_t)R * G * 16 : 0);
     }
 };
 
-template <typename E, bool MIX, bool SHIFT, int VPT, int S, int MAX>
+template <typename E, bool MIX, bool WORDS, int VPT, int S, int MAX>
 __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int G, int R) {
-    using Shape = RowsShape<E, MIX, SHIFT, VPT, S, MAX>;
+    using Shape = RowsShape<E, MIX, WORDS, VPT, S, MAX>;
     constexpr int N = Shape::N, H = N / 2, P = Shape::kPitch, A = Shape::kArrays;
     constexpr int XA = MIX ? kStreams : 1;   // slots of a vector: x (XA), grad_y, residual gradient
     extern __shared__ uint4 slots[];
     const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
     const int warp = i >> 5, warps = G >> 5;
-    uint4* const mine = slots + (SHIFT ? (tid >> 5) * 33 + lane : tid);
+    uint4* const mine = slots + (WORDS ? (tid >> 5) * kWarpSlots + lane : tid);
     float4* const gammas = reinterpret_cast<float4*>(slots + P * Shape::kSlots);   // [kGammaSlots][G]
     float* const floats = reinterpret_cast<float*>(gammas + Shape::kGammaSlots * G);
     float* const scalars = floats + (tid >> 5) * Shape::kWarpFloats;
     float* const sums = floats + (NT >> 5) * Shape::kWarpFloats + group * Shape::kGroupFloats;   // [2][kSums][32]
+    uint4* const buffer =   // WORDS: what the warp stores
+        reinterpret_cast<uint4*>(floats + (NT >> 5) * Shape::kWarpFloats + R * Shape::kGroupFloats) + (tid >> 5) * 32;
     const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group, T = (int)a.T;
     const bool residual = MIX && a.grad_x_out.p != nullptr;
     const int c0 = i * N, step = G * N, D = (int)a.D;   // this thread's columns: c0 + v * step
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
     // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
     for (int k = 0; k < Shape::kSlots; ++k)
-        if (!SHIFT && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+        if (!WORDS && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
     ptx::grid_dependency_wait();
 
     // Element offset of row t of an array at this thread's first column, formed
@@ -561,25 +565,26 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
         return (size_t)((uint64_t)(uint32_t)t * (uint32_t)stride + (uint32_t)c0);
     };
     const auto fetch_vector = [&](uint4* dst, int t, int v) {
-        if constexpr (SHIFT) {
-            const size_t xo = at_row(t, a.x_stride) + v * step, go = at_row(t, a.gy_stride) + v * step;
-            const int c = c0 + v * step;
+        if constexpr (WORDS) {
+            const int width = D - (c0 + v * step) + lane * N;   // from the warp's first column on
+            const size_t xo = at_row(t, a.x_stride) + v * step - lane * N, go = at_row(t, a.gy_stride) + v * step - lane * N;
+            dst -= lane;
             if (t == 0 || t == T - 1) {
 #pragma unroll 1
                 for (int s = 0; s < A; ++s) {
                     const Span<const E>& in = s < XA ? a.x : s == XA ? a.grad_y : a.grad_x_out;
                     const size_t at = s < XA ? xo + s * D : s == XA ? go : xo + (s - XA - 1) * D;
-                    if (s <= XA || residual) copy_shifted_edge(dst + (v * A + s) * P, in.p, in.count, at, c, D, 0);
+                    if (s <= XA || residual) copy_edge(dst + (v * A + s) * P, in.p, in.count, at, width, 0);
                 }
                 return;
             }
 #pragma unroll
-            for (int s = 0; s < XA; ++s) copy_shifted(dst + (v * A + s) * P, a.x, xo + s * D, c, D, 0);
-            copy_shifted(dst + (v * A + XA) * P, a.grad_y, go, c, D, 5);
+            for (int s = 0; s < XA; ++s) copy_chunks(dst + (v * A + s) * P, a.x, xo + s * D, width, 0);
+            copy_chunks(dst + (v * A + XA) * P, a.grad_y, go, width, 5);
             if (MIX && residual)
 #pragma unroll
                 for (int s = 0; s < kStreams; ++s)
-                    copy_shifted(dst + (v * A + XA + 1 + s) * P, a.grad_x_out, xo + s * D, c, D, 7);
+                    copy_chunks(dst + (v * A + XA + 1 + s) * P, a.grad_x_out, xo + s * D, width, 7);
         } else if (c0 + v * step < D) {
             const size_t xo = at_row(t, a.x_stride) + v * step, go = at_row(t, a.gy_stride) + v * step;
 #pragma unroll
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
         for (int k = 0; k < Shape::kGammaSlots; ++k) {
             const int c = c0 + k / (N / 4) * step + k % (N / 4) * 4;
             float g[4] = {0.f, 0.f, 0.f, 0.f};
-            four_at<SHIFT>(a.gamma, c, D, 1.f, g);
+            four_at<WORDS>(a.gamma, c, D, 1.f, g);
             gammas[k * G + i] = make_float4(g[0], g[1], g[2], g[3]);
         }
     __syncthreads();
@@ -650,14 +655,14 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
         __syncwarp();
         const float4* const gates = reinterpret_cast<const float4*>(scalars + stage * 32);
         uint4* const row = mine + stage * (Shape::kStage * P);
-        if constexpr (SHIFT)
+        if constexpr (WORDS)
 #pragma unroll
             for (int k = 0; k < Shape::kStage; ++k) {
                 const int s = k % A;   // x, grad_y or the residual path's gradient
                 const E* const p = s < XA ? a.x.p + (size_t)t * a.x_stride + s * D
                                    : s == XA ? a.grad_y.p + (size_t)t * a.gy_stride
                                              : a.grad_x_out.p + (size_t)t * a.x_stride + (s - XA - 1) * D;
-                if (s <= XA || residual) realign<E>(row + k * P, misaligned(p), D - (c0 + k / A * step));
+                if (s <= XA || residual) align_chunks<E>(row - lane + k * P, misaligned(p), D - (c0 + k / A * step));
             }
         const float2 stat = reinterpret_cast<const float2*>(gates)[kGates / 2];
         // z = u rstd - mean rstd
@@ -777,12 +782,12 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
                     for (int j = 0; j < kStreams; ++j) pack_half<E>(o[j], &out[j][half * 2]);
                 }
             }
-            if constexpr (SHIFT) {
+            if constexpr (WORDS) {
                 const size_t o = at_row(t, a.gx_stride) + v * step;
 #pragma unroll
                 for (int j = 0; j < XA; ++j)
-                    store_shifted(a.grad_x, o + j * D, D - (c0 + v * step), lane > 0, lane < 31,
-                                  make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]), 6);
+                    store_words(buffer, a.grad_x, o + j * D - lane * N, D - (c0 + v * step) + lane * N,
+                                make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]), 6);
             } else if (c0 + v * step < D) {
                 const size_t o = at_row(t, a.gx_stride) + v * step;
 #pragma unroll
@@ -847,7 +852,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
                     o[2 * k + 1] = q.y;
                 }
                 const size_t at = ((size_t)blockIdx.x * 2 + part) * D + c;
-                if constexpr (SHIFT) {
+                if constexpr (WORDS) {
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
                         const float one[1] = {o[k]};
@@ -935,9 +940,9 @@ bool forward_rows(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
 }
 
 // Likewise forward_ring_kernel.
-template <typename E, bool MIX, bool SHIFT, int VPT, int S>
+template <typename E, bool MIX, bool WORDS, int VPT, int S>
 bool forward_ring(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
-    using Shape = ForwardShape<E, MIX, SHIFT, VPT, S>;
+    using Shape = ForwardShape<E, MIX, WORDS, VPT, S>;
     const int64_t threads = ((p.D + Shape::N - 1) / Shape::N + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
@@ -947,7 +952,7 @@ bool forward_ring(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
     const size_t shared = Shape::bytes(G, R);
     if (shared > kMaxShared) return false;
     const int64_t grid = (p.T + R - 1) / R < kSms ? (p.T + R - 1) / R : kSms;
-    auto kernel = forward_ring_kernel<E, MIX, SHIFT, VPT, S>;
+    auto kernel = forward_ring_kernel<E, MIX, WORDS, VPT, S>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
@@ -977,9 +982,9 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
 
 // Launches backward_rows_kernel where the row fits its shape; false otherwise.
 // *parts: the row groups it writes partial parameter gradients for.
-template <typename E, bool MIX, bool SHIFT, int VPT, int S, int MAX>
+template <typename E, bool MIX, bool WORDS, int VPT, int S, int MAX>
 bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStream_t stream) {
-    using Shape = RowsShape<E, MIX, SHIFT, VPT, S, MAX>;
+    using Shape = RowsShape<E, MIX, WORDS, VPT, S, MAX>;
     const int64_t vectors = (p.D + Shape::N - 1) / Shape::N, threads = (vectors + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
@@ -993,7 +998,7 @@ bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStrea
     if (shared > kMaxShared) return false;
     const int64_t grid = (p.T + R - 1) / R < blocks ? (p.T + R - 1) / R : blocks;
     *parts = grid;
-    auto kernel = backward_rows_kernel<E, MIX, SHIFT, VPT, S, MAX>;
+    auto kernel = backward_rows_kernel<E, MIX, WORDS, VPT, S, MAX>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);

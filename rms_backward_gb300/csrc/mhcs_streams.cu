@@ -11,7 +11,7 @@
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
-#include "mhcs_shift.cuh"
+#include "mhcs_words.cuh"
 #include "ptx.cuh"
 
 namespace mhcpb {
@@ -222,44 +222,61 @@ __device__ __forceinline__ void drop_eight(const Drop& d, const ShortPhilox& ran
 }
 
 // One vector of every stream per thread, everything loaded before anything is
-// used.  SHIFT: rows at any address (mhcs_shift.cuh), D of any size.
-template <bool SHIFT>
+// used.  WORDS: rows at any address (mhcs_words.cuh), D of any size.
+template <bool WORDS>
 __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
     int64_t T, int64_t D, VectorGrid grid, bool gates_aligned, Span<const bf16> x, Span<const bf16> y,
     Span<const float> h, Drop d, Span<bf16> x_out) {
-    ptx::grid_dependency_wait();
     constexpr int N = 8, H = 4;
+    __shared__ uint4 parts[WORDS ? kThreads / 32 * (kStreams + 1) * kWarpSlots : 1];
+    ptx::grid_dependency_wait();
     const VectorPlace place = grid.place(T);
     const int64_t t = place.token;
-    const int c = place.vector * N;
-    int valid = place.valid ? (int)D - c : 0;
-    if (!SHIFT && valid <= 0) return;
+    const int c = place.vector * N, lane = threadIdx.x & 31;
     const size_t row = (size_t)t * (kStreams * D) + c, flat = (size_t)t * D + c;
-    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-    uint4 xs[kStreams] = {none, none, none, none}, yr = none;
-    float g[20] = {};
-    const DropKey key = drop_key(d);
-    if (valid > 0) {
+    uint4 xs[kStreams], yr;
+    float g[20];
+    if constexpr (!WORDS) {
+        if (!place.valid) return;
+        yr = y.has(flat, N, 3) ? *reinterpret_cast<const uint4*>(y.p + flat) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < kStreams; ++j)
+            xs[j] = x.has(row + j * D, N, 4) ? *reinterpret_cast<const uint4*>(x.p + row + j * D) : make_uint4(0u, 0u, 0u, 0u);
         gates_at(h, t, gates_aligned, g);
-        if constexpr (!SHIFT) {
-            if (y.has(flat, N, 3)) yr = *reinterpret_cast<const uint4*>(y.p + flat);
-#pragma unroll
-            for (int j = 0; j < kStreams; ++j)
-                if (x.has(row + j * D, N, 4)) xs[j] = *reinterpret_cast<const uint4*>(x.p + row + j * D);
-        } else if (t == 0 || t == T - 1) {
-            // these tokens' chunks may stick out of the operands
-            for (int k = 0; k < N && k < valid; ++k) update_column(t, c + k, D, g, x, y, d, key, x_out);
-            valid = 0;
+    } else {
+        // a warp's vectors are all of one token (VectorGrid's whole warps)
+        if (t >= T) return;
+        uint4* const mine = parts + (threadIdx.x >> 5) * ((kStreams + 1) * kWarpSlots);
+        const int width = (int)D - c + lane * N;
+        const size_t row0 = row - lane * N, flat0 = flat - lane * N;
+        if (t == 0 || t == T - 1) {
+#pragma unroll 1
+            for (int j = 0; j <= kStreams; ++j)
+                copy_edge(mine + j * kWarpSlots, j < kStreams ? x.p : y.p, j < kStreams ? x.count : y.count,
+                              j < kStreams ? row0 + j * D : flat0, width, 4);
         } else {
-            yr = load_shifted<false>(y, flat, valid, 3);
+            copy_chunks(mine + kStreams * kWarpSlots, y, flat0, width, 3);
 #pragma unroll
-            for (int j = 0; j < kStreams; ++j) xs[j] = load_shifted<false>(x, row + j * D, valid, 4);
+            for (int j = 0; j < kStreams; ++j) copy_chunks(mine + j * kWarpSlots, x, row0 + j * D, width, 4);
         }
+        copies_commit();
+        gates_at(h, t, gates_aligned, g);
+        copies_wait<0>();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kStreams; ++j) {
+            align_chunks<bf16>(mine + j * kWarpSlots, misaligned(x.p + row0 + j * D), (int)D - c);
+            xs[j] = mine[j * kWarpSlots + lane];
+        }
+        align_chunks<bf16>(mine + kStreams * kWarpSlots, misaligned(y.p + flat0), (int)D - c);
+        yr = mine[kStreams * kWarpSlots + lane];
+        __syncwarp();
     }
+    const DropKey key = drop_key(d);
     float2 yv[H], o[kStreams][H];
     uint32_t keep;
     unpack<bf16>(yr, yv);
-    drop_eight<SHIFT>(d, ShortPhilox(key), flat, yv, &keep);
+    drop_eight<WORDS>(d, ShortPhilox(key), flat, yv, &keep);
 #pragma unroll
     for (int i = 0; i < kStreams; ++i)
 #pragma unroll
@@ -275,8 +292,9 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
     }
 #pragma unroll
     for (int i = 0; i < kStreams; ++i) {
-        if constexpr (SHIFT) {
-            store_shifted(x_out, row + i * D, valid, place.before, place.after, pack<bf16>(o[i]), 5);
+        if constexpr (WORDS) {
+            store_words(parts + (threadIdx.x >> 5) * ((kStreams + 1) * kWarpSlots), x_out, row - lane * N + i * D,
+                        (int)D - c + lane * N, pack<bf16>(o[i]), 5);
         } else {
             if (x_out.has(row + i * D, N, 5)) *reinterpret_cast<uint4*>(x_out.p + row + i * D) = pack<bf16>(o[i]);
         }
@@ -287,59 +305,66 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
 // ... of it, VPT of them), its inputs copied S tokens ahead into per-thread
 // slots.  The token's 20 dot products are left in shared memory by each warp
 // and added up after the group's barrier, which the outputs do not wait for.
-template <bool SHIFT, int VPT, int S, int MAX>
+template <bool WORDS, int VPT, int S, int MAX>
 struct TokenShape {
     static constexpr int kMaxThreads = MAX;            // 640: 96 registers a thread; 512: 128
     static constexpr int kArrays = 2 * kStreams + 1;   // x, grad_x_out, y
     static constexpr int kStage = VPT * kArrays;
-    static constexpr int kPitch = SHIFT ? MAX / 32 * 33 : MAX;
+    static constexpr int kPitch = WORDS ? MAX / 32 * kWarpSlots : MAX;
     static constexpr int kDots = 20;
     static size_t bytes(int G, int R) {
-        return (size_t)kPitch * S * kStage * 16 + (size_t)R * (G / 32 * S * 4 + 2 * kDots * (G / 32 | 1)) * 4;
+        return (size_t)kPitch * S * kStage * 16 + (size_t)R * ((G / 32 * S * 4 + 2 * kDots * (G / 32 | 1)) * 4) +
+               (WORDS ? 16 + (size_t)R * G * 16 : 0);   // what a warp stores
     }
 };
-template <bool SHIFT, int VPT, int S, int MAX>
+template <bool WORDS, int VPT, int S, int MAX>
 __global__ void __launch_bounds__(MAX, 1)
     update_backward_tokens_kernel(int T, int D, int G, int R, Span<const bf16> x, Span<const bf16> y,
                                   Span<const float> h, Drop d, Span<const bf16> gout, Span<bf16> gy, Span<float> gh) {
-    using Shape = TokenShape<SHIFT, VPT, S, MAX>;
+    using Shape = TokenShape<WORDS, VPT, S, MAX>;
     constexpr int N = 8, P = Shape::kPitch, A = Shape::kArrays;
     extern __shared__ uint4 slots[];
     const int NT = G * R, tid = threadIdx.x, group = tid / G, i = tid - group * G, lane = tid & 31;
     const int warp = i >> 5, warps = G >> 5;
-    uint4* const mine = slots + (SHIFT ? (tid >> 5) * 33 + lane : tid);
+    uint4* const mine = slots + (WORDS ? (tid >> 5) * kWarpSlots + lane : tid);
     float* const floats = reinterpret_cast<float*>(slots + P * S * Shape::kStage);
     float* const posts = floats + (tid >> 5) * (S * 4);                                   // [S][4] per warp
     float* const dots = floats + (NT >> 5) * (S * 4) + group * (2 * Shape::kDots * (warps | 1));
+    uint4* buffer = nullptr;   // WORDS: what the warp stores, on the next 16-byte boundary
+    if (WORDS)
+        buffer = slots + P * S * Shape::kStage + (((NT >> 5) * (S * 4) + R * (2 * Shape::kDots * (warps | 1))) + 3) / 4 +
+                 (tid >> 5) * 32;
     const int dot_pitch = warps | 1;   // odd: the 20 lanes that read a column meet 20 banks
     const int groups = (int)gridDim.x * R, first = (int)blockIdx.x * R + group;
     const int c0 = i * N, step = G * N;
     // columns past D: never copied, they stay 0 and add nothing
 #pragma unroll
     for (int k = 0; k < S * Shape::kStage; ++k)
-        if (!SHIFT && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
+        if (!WORDS && c0 + k % Shape::kStage / A * step >= D) mine[k * P] = make_uint4(0u, 0u, 0u, 0u);
     ptx::grid_dependency_wait();
 
     const auto fetch_vector = [&](uint4* dst, int t, int v) {
         const int c = c0 + v * step;
         const size_t flat = (size_t)((uint64_t)(uint32_t)t * (uint32_t)D + (uint32_t)c);
         const size_t row = (size_t)((uint64_t)(uint32_t)t * (uint32_t)(kStreams * D) + (uint32_t)c);
-        if constexpr (SHIFT) {
+        if constexpr (WORDS) {
+            const int width = D - c + lane * N;   // from the warp's first column on
+            uint4* const warps_dst = dst - lane;
             if (t == 0 || t == T - 1) {
 #pragma unroll 1
                 for (int s = 0; s < A; ++s) {
                     const Span<const bf16>& in = s < kStreams ? x : s < 2 * kStreams ? gout : y;
                     const size_t at = s < 2 * kStreams ? row + (s % kStreams) * D : flat;
-                    copy_shifted_edge(dst + (v * A + s) * P, in.p, in.count, at, c, D, 4);
+                    copy_edge(warps_dst + (v * A + s) * P, in.p, in.count, at - lane * N, width, 4);
                 }
                 return;
             }
 #pragma unroll
             for (int s = 0; s < kStreams; ++s) {
-                copy_shifted(dst + (v * A + s) * P, x, row + s * D, c, D, 4);
-                copy_shifted(dst + (v * A + kStreams + s) * P, gout, row + s * D, c, D, 6);
+                copy_chunks(warps_dst + (v * A + s) * P, x, row - lane * N + s * D, width, 4);
+                copy_chunks(warps_dst + (v * A + kStreams + s) * P, gout, row - lane * N + s * D, width, 6);
             }
-            copy_shifted(dst + (v * A + 2 * kStreams) * P, y, flat, c, D, 3);
+            copy_chunks(warps_dst + (v * A + 2 * kStreams) * P, y, flat - lane * N, width, 3);
         } else if (c < D) {
 #pragma unroll
             for (int s = 0; s < kStreams; ++s) {
@@ -377,14 +402,14 @@ __global__ void __launch_bounds__(MAX, 1)
         copies_wait<S - 1>();
         __syncwarp();
         uint4* const row = mine + stage * (Shape::kStage * P);
-        if constexpr (SHIFT)
+        if constexpr (WORDS)
 #pragma unroll
             for (int k = 0; k < Shape::kStage; ++k) {
                 const int s = k % A;   // x, grad_x_out or y
                 const bf16* const p = s < kStreams ? x.p + (size_t)t * (kStreams * D) + s * D
                                       : s < 2 * kStreams ? gout.p + (size_t)t * (kStreams * D) + (s - kStreams) * D
                                                          : y.p + (size_t)t * D;
-                realign<bf16>(row + k * P, misaligned(p), D - (c0 + k / A * step));
+                align_chunks<bf16>(row - lane + k * P, misaligned(p), D - (c0 + k / A * step));
             }
         const float4 post = *reinterpret_cast<const float4*>(posts + stage * 4);
         const float p4[kStreams] = {post.x, post.y, post.z, post.w};
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(MAX, 1)
             float2 yv[4];
             uint32_t keep, out[4];
             unpack<bf16>(row[(v * A + 2 * kStreams) * P], yv);
-            drop_eight<SHIFT>(d, random, flat, yv, &keep);
+            drop_eight<WORDS>(d, random, flat, yv, &keep);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 float2 xs[kStreams][2], o[2] = {pair(0.f), pair(0.f)};
@@ -431,8 +456,8 @@ __global__ void __launch_bounds__(MAX, 1)
                 pack_half<bf16>(o, out + half * 2);
             }
             const uint4 packed = make_uint4(out[0], out[1], out[2], out[3]);
-            if constexpr (SHIFT) {
-                store_shifted(gy, flat, D - c, lane > 0, lane < 31, packed, 7);
+            if constexpr (WORDS) {
+                store_words(buffer, gy, flat - lane * N, D - c + lane * N, packed, 7);
             } else {
                 if (c < D && gy.has(flat, N, 7)) *reinterpret_cast<uint4*>(gy.p + flat) = packed;
             }
@@ -456,11 +481,11 @@ __global__ void __launch_bounds__(MAX, 1)
 }
 
 // Launches update_backward_tokens_kernel where a token fits its shape.
-template <bool SHIFT, int VPT, int S, int MAX>
+template <bool WORDS, int VPT, int S, int MAX>
 bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, const Span<const bf16>& y,
                             const Span<const float>& h, const Drop& d, const Span<const bf16>& gout,
                             const Span<bf16>& gy, const Span<float>& gh, cudaError_t* e, cudaStream_t stream) {
-    using Shape = TokenShape<SHIFT, VPT, S, MAX>;
+    using Shape = TokenShape<WORDS, VPT, S, MAX>;
     const int64_t threads = ((D + 7) / 8 + VPT - 1) / VPT;
     if (threads > Shape::kMaxThreads) return false;
     const int G = (int)((threads + 31) / 32 * 32);
@@ -471,7 +496,7 @@ bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, con
     while (R > 1 && Shape::bytes(G, R) > kMaxShared) --R;
     if (Shape::bytes(G, R) > kMaxShared) return false;
     const int64_t grid = (T + R - 1) / R < kSms ? (T + R - 1) / R : kSms;
-    auto kernel = update_backward_tokens_kernel<SHIFT, VPT, S, MAX>;
+    auto kernel = update_backward_tokens_kernel<WORDS, VPT, S, MAX>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), Shape::bytes(G, R), stream, (int)T, (int)D, G,
@@ -510,7 +535,7 @@ cudaError_t update_forward(int64_t T, int64_t D, const void* x, const void* y, c
     const Span<const float> hs{h, (size_t)(T * kGates)};
     const Span<bf16> os{static_cast<bf16*>(x_out), (size_t)(T * kStreams * D)};
     if (D >= 8 && T * D < kShortCounters && (D + 7) / 8 * T <= INT32_MAX) {
-        const VectorGrid grid((D + 7) / 8, kThreads);
+        const VectorGrid grid((D + 7) / 8, kThreads, D % 8 != 0);
         return launch_early(D % 8 == 0 ? update_forward_vectors_kernel<false> : update_forward_vectors_kernel<true>,
                             dim3(grid.blocks(T)), dim3(grid.threads), 0, stream, T, D, grid, aligned16(h), xs, ys, hs, d,
                             os);
