@@ -84,7 +84,7 @@ def embed_forward(ids, table, n_streams, scale):
 
 def embed_backward(ids, grad_x, V, D, scale, start=None):
     """(gradient, magnitude, chain per row): the longest chain of additions of a row."""
-    g = np.asarray(grad_x, dtype=np.float64).reshape(len(ids), -1, D)
+    g = np.asarray(grad_x, dtype=np.float64).reshape(len(ids), np.shape(grad_x)[1] // D, D)
     out = np.zeros((V, D)) if start is None else np.asarray(start, dtype=np.float64).copy()
     mag, count = np.abs(out), np.zeros((V, 1))
     s = float(np.float32(scale))

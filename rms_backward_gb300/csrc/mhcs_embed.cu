@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(int64_t T, int64
         const size_t at = (size_t)(id * D + c);
         if constexpr (WORDS) {
             // FP32: two parts of 32 vectors, traded so that a lane gets eight columns
-            const bool edge = id == 0 || id == V - 1;
+            const bool edge = edge_row<E>(id, V, D);
             const size_t first = at - lane * N;
             const int width = (int)D - c + lane * N;
             if (edge) {
@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
                 const uint32_t row = rows[item] & kRowMask;
                 const size_t at = (size_t)row * a.D + c;
                 const int width = (int)(a.D - c) + lane * N;   // from the warp's first column on
-                if (WORDS && (row == 0 || row + NS == (uint32_t)(a.T * a.n_streams))) {
+                const int64_t all = a.T * a.n_streams;
+                if (WORDS && (edge_row<bf16>(row, all, a.D) || edge_row<bf16>(row + NS - 1, all, a.D))) {
 #pragma unroll 1
                     for (int s = 0; s < NS; ++s)
                         copy_edge(mine + (item % kItems * NS + s) * P - lane, a.grad_x.p, a.grad_x.count,

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, WORDS, VPT, S>::kMaxThre
     const auto fetch = [&](int t, int stage) {
         if (t < T) {
             const size_t at = (size_t)((uint64_t)(uint32_t)t * (uint32_t)a.x_stride + (uint32_t)c0);
-            if (WORDS && (t == 0 || t == T - 1)) {
+            if (WORDS && edge_row<E>(t, T, D)) {
 #pragma unroll 1
                 for (int k = 0; k < Shape::kStage; ++k)
                     copy_edge(mine - lane + (stage * Shape::kStage + k) * P, a.x.p, a.x.count,
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
             const int width = D - (c0 + v * step) + lane * N;   // from the warp's first column on
             const size_t xo = at_row(t, a.x_stride) + v * step - lane * N, go = at_row(t, a.gy_stride) + v * step - lane * N;
             dst -= lane;
-            if (t == 0 || t == T - 1) {
+            if (edge_row<E>(t, T, D)) {
 #pragma unroll 1
                 for (int s = 0; s < A; ++s) {
                     const Span<const E>& in = s < XA ? a.x : s == XA ? a.grad_y : a.grad_x_out;

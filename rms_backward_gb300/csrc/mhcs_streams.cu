@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
         uint4* const mine = parts + (threadIdx.x >> 5) * ((kStreams + 1) * kWarpSlots);
         const int width = (int)D - c + lane * N;
         const size_t row0 = row - lane * N, flat0 = flat - lane * N;
-        if (t == 0 || t == T - 1) {
+        if (edge_row<bf16>(t, T, D)) {
 #pragma unroll 1
             for (int j = 0; j <= kStreams; ++j)
                 copy_edge(mine + j * kWarpSlots, j < kStreams ? x.p : y.p, j < kStreams ? x.count : y.count,
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(MAX, 1)
         if constexpr (WORDS) {
             const int width = D - c + lane * N;   // from the warp's first column on
             uint4* const warps_dst = dst - lane;
-            if (t == 0 || t == T - 1) {
+            if (edge_row<bf16>(t, T, D)) {
 #pragma unroll 1
                 for (int s = 0; s < A; ++s) {
                     const Span<const bf16>& in = s < kStreams ? x : s < 2 * kStreams ? gout : y;

@@ -5,8 +5,8 @@
 // elements into a chunk lies in that chunk and the next; each lane puts its own
 // together from both with selects and funnel shifts, once, and it is used as an
 // aligned vector from then on.  A chunk may hold elements of neighbouring rows
-// (copied, never used); in the operand's first and last row, parts whose chunks
-// stick out of the operand are copied as single elements instead.  (4-byte
+// (copied, never used); parts whose chunks stick out of the operand, at its
+// beginning or end, are copied as single elements instead.  (4-byte
 // copies need no putting together but four times the copies: the collapse
 // gradient at T=4096, D=1285 took 93 us instead of 66.)
 // Stores: a warp's vectors go through shared memory and leave in 4-byte words,
@@ -26,6 +26,15 @@ template <typename E>
 __device__ __forceinline__ int misaligned(const E* p) {
     return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(E)) & (Elem<E>::kPack - 1);
 }
+// Whether chunks of row r of `rows`, which are `width` elements and more apart,
+// can stick out of the operand: a chunk reaches up to kPack - 1 elements past
+// its row on either side.
+template <typename E>
+__device__ __forceinline__ bool edge_row(int64_t r, int64_t rows, int64_t width) {
+    constexpr int64_t kReach = Elem<E>::kPack - 1;
+    const int64_t reach = width >= kReach ? 1 : (kReach - 1 + width) / width;   // rows
+    return r < reach || r >= rows - reach;
+}
 // 1 if p lies in the middle of a 4-byte word (16-bit types), else 0.
 template <typename E>
 __device__ __forceinline__ int half_word(const E* p) {
@@ -33,8 +42,8 @@ __device__ __forceinline__ int half_word(const E* p) {
 }
 
 // Starts copying a warp's part of a row, `width` elements (cut to its 32
-// vectors; none if <= 0) from element `at` on, into its slots.  Not for the
-// operand's first and last row.  The whole warp.
+// vectors; none if <= 0) from element `at` on, into its slots.  Not for
+// edge_row()s.  The whole warp.
 template <typename E>
 __device__ __forceinline__ void copy_chunks(uint4* slots, const Span<const E>& in, size_t at, int width, uint32_t site) {
     constexpr int kPack = Elem<E>::kPack;
@@ -44,8 +53,8 @@ __device__ __forceinline__ void copy_chunks(uint4* slots, const Span<const E>& i
     if (lane == 31 && m > 0 && 32 * kPack - m < width && in.has(first + kPack, kPack, site))
         copy16(slots + 32, in.p + first + kPack);
 }
-// The same in the operand's first and last row: a part whose chunks stick out
-// of the operand is copied element by element, at once.  A call, in a loop over
+// The same for any row: a part whose chunks stick out of the operand is copied
+// element by element, at once.  A call, in a loop over
 // the arrays: inlined beside every copy it cost the rows' kernels registers.
 template <typename E>
 __device__ __noinline__ void copy_edge(uint4* slots, const E* p, size_t count, size_t at, int width, uint32_t site) {
