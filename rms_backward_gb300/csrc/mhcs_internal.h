@@ -2,6 +2,7 @@
 // (mhcs_embed.cu, mhcs_norm.cu, mhcs_streams.cu) and their host checks
 // (mhcs_api.cu).
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -24,6 +25,19 @@ struct DropArgs {                // see Drop in mhcs_common.cuh
     uint32_t threshold;
     float scale;
 };
+
+// Lets a kernel's blocks have `bytes` of dynamic shared memory, once per device
+// (`done` is the kernel's own; devices above 63 are set each time).
+template <typename Kernel>
+cudaError_t allow_shared(Kernel* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+    if (e != cudaSuccess || (done.load(std::memory_order_acquire) & bit) != 0) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Launches a kernel whose blocks may start before the kernel ahead of it in the
 // stream has ended; each of these kernels waits for that one by itself

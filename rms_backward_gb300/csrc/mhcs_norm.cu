@@ -953,7 +953,8 @@ bool forward_ring(const Params<E>& p, cudaError_t* e, cudaStream_t stream) {
     if (shared > kMaxShared) return false;
     const int64_t grid = (p.T + R - 1) / R < kSms ? (p.T + R - 1) / R : kSms;
     auto kernel = forward_ring_kernel<E, MIX, WORDS, VPT, S>;
-    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    static std::atomic<uint64_t> done{0};
+    *e = allow_shared(kernel, kMaxShared, done);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
     return true;
@@ -999,7 +1000,8 @@ bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStrea
     const int64_t grid = (p.T + R - 1) / R < blocks ? (p.T + R - 1) / R : blocks;
     *parts = grid;
     auto kernel = backward_rows_kernel<E, MIX, WORDS, VPT, S, MAX>;
-    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    static std::atomic<uint64_t> done{0};
+    *e = allow_shared(kernel, kMaxShared, done);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), shared, stream, p, G, R);
     return true;

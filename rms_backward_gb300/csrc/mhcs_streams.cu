@@ -497,7 +497,8 @@ bool update_backward_tokens(int64_t T, int64_t D, const Span<const bf16>& x, con
     if (Shape::bytes(G, R) > kMaxShared) return false;
     const int64_t grid = (T + R - 1) / R < kSms ? (T + R - 1) / R : kSms;
     auto kernel = update_backward_tokens_kernel<WORDS, VPT, S, MAX>;
-    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    static std::atomic<uint64_t> done{0};
+    *e = allow_shared(kernel, kMaxShared, done);
     if (*e != cudaSuccess) return true;
     *e = launch_early(kernel, dim3((unsigned)grid), dim3((unsigned)(G * R)), Shape::bytes(G, R), stream, (int)T, (int)D, G,
                       R, x, y, h, d, gout, gy, gh);

@@ -23,10 +23,18 @@ _TYPES = {torch.bfloat16: abi.MHCPB_BF16, torch.float16: abi.MHCPB_FP16, torch.f
 _BF16, _F32 = torch.bfloat16, torch.float32
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _handle(stream, like):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(like.get_device()) if like.is_cuda else 0
+        device = like.get_device()
+        return _raw_stream(device) if device >= 0 else None   # the library refuses host tensors
     return getattr(stream, "cuda_stream", stream)
+
+
+def _lib():
+    return abi._lib or abi.load()
 
 
 def _need(t, name, shape, dtype):
@@ -43,6 +51,8 @@ def _maybe(t, name, shape, dtype):
 
 def _rows(t, name, shape, dtype):
     """(pointer, row stride) of a [T, D] tensor whose rows are compact."""
+    if t.dtype is dtype and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr(), shape[1]
     if t.dtype is not dtype or t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} with compact rows, "
                          f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
@@ -94,9 +104,11 @@ def mhc_embed_forward(ids, table, x, *, scale: float = 1.0, stream=None):
     Ids outside [0, V) give rows of zeros."""
     V, _ = _two_dims(table, "table")
     T, D, n = _ids(ids, table.shape, x, "x")
-    abi.mhcpb_embed_forward(T, V, D, n, _type(table, "table"), _need(table, "table", table.shape, table.dtype),
+    status = _lib().mhcpb_embed_forward(T, V, D, n, _type(table, "table"), _need(table, "table", table.shape, table.dtype),
                             ids.data_ptr(), ids.element_size(), scale, _need(x, "x", x.shape, _BF16),
                             _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_embed_forward")
 
 
 def mhc_embed_workspace_bytes(T: int, V: int, D: int) -> int:
@@ -111,10 +123,12 @@ def mhc_embed_backward(ids, grad_x, grad_table, workspace, *, scale: float = 1.0
     ``accumulate``), summed in a fixed order."""
     V, _ = _two_dims(grad_table, "grad_table")
     T, D, n = _ids(ids, grad_table.shape, grad_x, "grad_x")
-    abi.mhcpb_embed_backward(T, V, D, n, _need(grad_x, "grad_x", grad_x.shape, _BF16), ids.data_ptr(),
+    status = _lib().mhcpb_embed_backward(T, V, D, n, _need(grad_x, "grad_x", grad_x.shape, _BF16), ids.data_ptr(),
                              ids.element_size(), scale, abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
                              _need(grad_table, "grad_table", grad_table.shape, _F32), workspace.data_ptr(),
                              workspace.nbytes, _handle(stream, grad_x))
+    if status:
+        abi._check(status, "mhcpb_embed_backward")
 
 
 # ---------------------------------------------------------------- layer norm
@@ -125,9 +139,11 @@ def mhc_layernorm_forward(x, gamma, beta, y, mean=None, rstd=None, *, eps: float
     T, D = _two_dims(x, "x")
     xp, xs = _rows(x, "x", x.shape, x.dtype)
     yp, ys = _rows(y, "y", x.shape, x.dtype)
-    abi.mhcpb_layernorm_forward(T, D, _type(x, "x"), xp, xs, _maybe(gamma, "gamma", (D,), _F32),
+    status = _lib().mhcpb_layernorm_forward(T, D, _type(x, "x"), xp, xs, _maybe(gamma, "gamma", (D,), _F32),
                                 _maybe(beta, "beta", (D,), _F32), eps, yp, ys, _maybe(mean, "mean", (T,), _F32),
                                 _maybe(rstd, "rstd", (T,), _F32), _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_layernorm_forward")
 
 
 def mhc_layernorm_workspace_bytes(T: int, D: int) -> int:
@@ -143,13 +159,15 @@ def mhc_layernorm_backward(x, grad_y, gamma, mean, rstd, grad_x, grad_gamma=None
     xp, xs = _rows(x, "x", x.shape, x.dtype)
     gp, gs = _rows(grad_y, "grad_y", x.shape, x.dtype)
     dp, ds = _rows(grad_x, "grad_x", x.shape, x.dtype)
-    abi.mhcpb_layernorm_backward(T, D, _type(x, "x"), xp, xs, gp, gs, _maybe(gamma, "gamma", (D,), _F32),
+    status = _lib().mhcpb_layernorm_backward(T, D, _type(x, "x"), xp, xs, gp, gs, _maybe(gamma, "gamma", (D,), _F32),
                                  _need(mean, "mean", (T,), _F32), _need(rstd, "rstd", (T,), _F32), dp, ds,
                                  _maybe(grad_gamma, "grad_gamma", (D,), _F32),
                                  _maybe(grad_beta, "grad_beta", (D,), _F32),
                                  abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
                                  0 if workspace is None else workspace.data_ptr(),
                                  0 if workspace is None else workspace.nbytes, _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_layernorm_backward")
 
 
 # ---------------------------------------------------------------- dropout
@@ -157,18 +175,22 @@ def mhc_dropout(x, y, rng=None, *, p: float, sequence: int = 0, stream=None):
     """y = x / (1 - p) where kept, else 0; the mask comes from ``rng`` (an int64
     CUDA tensor {key, step}), ``sequence`` and the element's index, so the same
     call on the gradient is the gradient.  y may be x."""
-    abi.mhcpb_dropout(x.numel(), _type(x, "x"), _need(x, "x", x.shape, x.dtype), p, _rng(rng, p), sequence,
+    status = _lib().mhcpb_dropout(x.numel(), _type(x, "x"), _need(x, "x", x.shape, x.dtype), p, _rng(rng, p), sequence,
                       _need(y, "y", x.shape, x.dtype), _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_dropout")
 
 
 # ---------------------------------------------------------------- collapse and norm
 def mhc_collapse_norm_forward(x, h, gamma, beta, y, mean=None, rstd=None, *, eps: float = 1e-5, stream=None):
     """y = layer norm of sum_s h[:, s] x_s: the sublayer's input [T, D] BF16."""
     T, D = _streams(x, "x")
-    abi.mhcpb_collapse_norm_forward(T, D, _need(x, "x", x.shape, _BF16), _need(h, "h", (T, 24), _F32),
+    status = _lib().mhcpb_collapse_norm_forward(T, D, _need(x, "x", x.shape, _BF16), _need(h, "h", (T, 24), _F32),
                                     _maybe(gamma, "gamma", (D,), _F32), _maybe(beta, "beta", (D,), _F32), eps,
                                     _need(y, "y", (T, D), _BF16), _maybe(mean, "mean", (T,), _F32),
                                     _maybe(rstd, "rstd", (T,), _F32), _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_collapse_norm_forward")
 
 
 def mhc_collapse_norm_workspace_bytes(T: int, D: int) -> int:
@@ -181,7 +203,7 @@ def mhc_collapse_norm_backward(x, h, grad_y, gamma, mean, rstd, grad_x, grad_h, 
     """grad_x [T, 4 D] (with the residual path's share H_res^T grad_x_out, where
     given) and columns 0..3 of grad_h [T, 24] from grad_y [T, D]."""
     T, D = _streams(x, "x")
-    abi.mhcpb_collapse_norm_backward(
+    status = _lib().mhcpb_collapse_norm_backward(
         T, D, _need(x, "x", x.shape, _BF16), _need(h, "h", (T, 24), _F32), _need(grad_y, "grad_y", (T, D), _BF16),
         _maybe(gamma, "gamma", (D,), _F32), _need(mean, "mean", (T,), _F32), _need(rstd, "rstd", (T,), _F32),
         _maybe(grad_x_out, "grad_x_out", x.shape, _BF16), _need(grad_x, "grad_x", x.shape, _BF16),
@@ -189,6 +211,8 @@ def mhc_collapse_norm_backward(x, h, grad_y, gamma, mean, rstd, grad_x, grad_h, 
         _maybe(grad_beta, "grad_beta", (D,), _F32), abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
         0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
         _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_collapse_norm_backward")
 
 
 # ---------------------------------------------------------------- stream update
@@ -196,9 +220,11 @@ def mhc_update_forward(x, y, h, x_out, rng=None, *, p: float = 0.0, sequence: in
     """x_out_i = sum_j H_res[i, j] x_j + H_post[i] dropout(y), H_post and H_res
     from h [T, 24]; x_out may be x."""
     T, D = _streams(x, "x")
-    abi.mhcpb_update_forward(T, D, _need(x, "x", x.shape, _BF16), _need(y, "y", (T, D), _BF16),
+    status = _lib().mhcpb_update_forward(T, D, _need(x, "x", x.shape, _BF16), _need(y, "y", (T, D), _BF16),
                              _need(h, "h", (T, 24), _F32), p, _rng(rng, p), sequence,
                              _need(x_out, "x_out", x.shape, _BF16), _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_update_forward")
 
 
 def mhc_update_backward(x, y, h, grad_x_out, grad_y, grad_h, rng=None, *, p: float = 0.0, sequence: int = 0,
@@ -206,7 +232,9 @@ def mhc_update_backward(x, y, h, grad_x_out, grad_y, grad_h, rng=None, *, p: flo
     """grad_y [T, D] and columns 4..23 of grad_h [T, 24] from grad_x_out [T, 4 D];
     the streams' own gradient is :func:`mhc_collapse_norm_backward`'s."""
     T, D = _streams(x, "x")
-    abi.mhcpb_update_backward(T, D, _need(x, "x", x.shape, _BF16), _need(y, "y", (T, D), _BF16),
+    status = _lib().mhcpb_update_backward(T, D, _need(x, "x", x.shape, _BF16), _need(y, "y", (T, D), _BF16),
                               _need(h, "h", (T, 24), _F32), p, _rng(rng, p), sequence,
                               _need(grad_x_out, "grad_x_out", x.shape, _BF16), _need(grad_y, "grad_y", (T, D), _BF16),
                               _need(grad_h, "grad_h", (T, 24), _F32), _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_update_backward")
