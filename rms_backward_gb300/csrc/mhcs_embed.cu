@@ -43,16 +43,16 @@ constexpr int kRanked = 32;          // tokens a ranking block places, 8 threads
 constexpr int kFan = 16;             // runs per merge pass
 constexpr int kBatch = 32;           // ordered tokens per listing of rows
 constexpr int kAhead = 8;            // rows loaded ahead of the one being added
-constexpr int kZeroRows = 16;        // table rows per zeroing block, 4 a warp
+constexpr int kZeroRows = 4;         // table rows per zeroing block, one a warp
 constexpr int kMaxChunks = 4096;
 constexpr int kJoinBlocks = 4 * 152;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Ordered tokens per summing chunk: T / 128 between 4 and 32, so that a short
+// Ordered tokens per summing chunk: T / 256 between 4 and 32, so that a short
 // batch too is spread over the GPU, and more where that would make over 4096.
 int64_t chunk_tokens(int64_t T) {
-    int64_t c = T / 128;
+    int64_t c = T / 256;
     c = c < 4 ? 4 : c > kBatch ? kBatch : c;
     const int64_t least = (T + kMaxChunks - 1) / kMaxChunks;
     return c >= least ? c : (least + kBatch - 1) / kBatch * kBatch;

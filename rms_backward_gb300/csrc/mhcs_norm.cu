@@ -373,9 +373,12 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, WORDS, VPT, S>::kMaxThre
                 s0[32 + warp] = q_mine;
             }
             group_sync(group, G);
-            const float m = lane < warps ? s0[lane] : 0.f, q = lane < warps ? s0[32 + lane] : 0.f;
-            mean = warp_sum(n_lane * m) * inv_d;
-            var = warp_sum(fmaf(n_lane * (m - mean), m - mean, q)) * inv_d;
+            // about warp 0's mean, so that both sums are formed at once
+            const float shift = s0[0], d = lane < warps ? s0[lane] - shift : 0.f, nd = n_lane * d;
+            const float both = warp_sum_two(nd, fmaf(nd, d, lane < warps ? s0[32 + lane] : 0.f));
+            const float off = __shfl_sync(kFullMask, both, 0) * inv_d;   // mean - shift
+            mean = shift + off;
+            var = fmaf(__shfl_sync(kFullMask, both, 16), inv_d, -off * off);
         }
         const float rstd = 1.f / sqrtf(var + a.eps);
         const float2 mean2 = pair(-mean), rstd2 = pair(rstd);
@@ -971,10 +974,12 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
         // few rows: more threads each, for latency
         if ((a.T <= kSms && forward_rows<E, MIX, N, 1>(p, &e, stream)) ||
             forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) ||
-            forward_rows<E, MIX, N, 16 / N>(p, &e, stream))
+            forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream) ||
+            (sizeof(E) == 4 && forward_rows<E, MIX, N, 8>(p, &e, stream)))
             return e;
     } else if ((a.T <= kSms && forward_rows<E, MIX, 1, 4>(p, &e, stream)) ||
-               forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream)) {
+               forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) ||
+               forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream)) {
         return e;
     }
     return launch_early(packed && a.D % 8 == 0 ? forward_any_kernel<E, MIX, 8> : forward_any_kernel<E, MIX, 1>,
@@ -1027,8 +1032,10 @@ cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
                        backward_rows<E, true, true, 2, 1, 512>(p, &p.parts, &e, stream);
         } else {
             constexpr int S = sizeof(E) == 4 ? 2 : 3;
-            done = packed ? backward_rows<E, false, false, 16 / N, S, 640>(p, &p.parts, &e, stream)
-                          : backward_rows<E, false, true, 16 / N, S, 640>(p, &p.parts, &e, stream);
+            done = packed ? backward_rows<E, false, false, 16 / N, S, 640>(p, &p.parts, &e, stream) ||
+                                backward_rows<E, false, false, 32 / N, 1, 512>(p, &p.parts, &e, stream)
+                          : backward_rows<E, false, true, 16 / N, S, 640>(p, &p.parts, &e, stream) ||
+                                backward_rows<E, false, true, 32 / N, 1, 512>(p, &p.parts, &e, stream);
         }
         if (!done) {
             e = launch_early(packed && a.D % 8 == 0 ? backward_rows_any_kernel<E, MIX, 8> : backward_rows_any_kernel<E, MIX, 1>,

@@ -28,23 +28,28 @@ constexpr int kMaxShared = 227 * 1024;   // shared memory of a block
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Any alignment and size: an element per thread and step.
+// Any alignment and size: the four elements of a counter per thread and step.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) dropout_any_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
     ptx::grid_dependency_wait();
     const DropKey key = drop_key(d);
-    const int64_t step = (int64_t)gridDim.x * kThreads;
-    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n; e += step) {
-        float v[1];
-        load_at<1>(x, e, v, 0);
-        drop<1>(d, key, e, v);
-        store_at<1>(y, e, v, 1);
+    const int64_t step = (int64_t)gridDim.x * kThreads * 4;
+    for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4; e < n; e += step) {
+        const int here = n - e < 4 ? (int)(n - e) : 4;
+        float v[4] = {};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < here && x.has(e + k, 1, 0)) v[k] = Elem<E>::to_float(x.p[e + k]);
+        drop<4>(d, key, e, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < here && y.has(e + k, 1, 1)) y.p[e + k] = Elem<E>::from_float(v[k]);
     }
 }
 
 // kDropPacks vectors of 16 bytes per thread, a block's width apart; needs
 // n < kShortCounters and aligned pointers.  The last, partial vector is one thread's.
-constexpr int kDropPacks = 2;
+constexpr int kDropPacks = 4;
 template <typename E>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
     ptx::grid_dependency_wait();
@@ -514,7 +519,7 @@ cudaError_t dropout_typed(int64_t n, const void* x, void* y, const Drop& d, cuda
         return launch_early(dropout_kernel<E>, dim3((unsigned)((n + block - 1) / block)), dim3(kThreads), 0, stream, n, xs,
                             ys, d);
     }
-    const int64_t blocks = (n + kThreads - 1) / kThreads;
+    const int64_t blocks = ((n + 3) / 4 + kThreads - 1) / kThreads;
     return launch_early(dropout_any_kernel<E>, dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(kThreads), 0,
                         stream, n, xs, ys, d);
 }
@@ -535,7 +540,7 @@ cudaError_t update_forward(int64_t T, int64_t D, const void* x, const void* y, c
     const Span<const bf16> ys{static_cast<const bf16*>(y), (size_t)(T * D)};
     const Span<const float> hs{h, (size_t)(T * kGates)};
     const Span<bf16> os{static_cast<bf16*>(x_out), (size_t)(T * kStreams * D)};
-    if (D >= 8 && T * D < kShortCounters && (D + 7) / 8 * T <= INT32_MAX) {
+    if ((D % 8 == 0 || D >= 128) && T * D < kShortCounters && (D + 7) / 8 * T <= INT32_MAX) {
         const VectorGrid grid((D + 7) / 8, kThreads, D % 8 != 0);
         return launch_early(D % 8 == 0 ? update_forward_vectors_kernel<false> : update_forward_vectors_kernel<true>,
                             dim3(grid.blocks(T)), dim3(grid.threads), 0, stream, T, D, grid, aligned16(h), xs, ys, hs, d,
@@ -555,7 +560,7 @@ cudaError_t update_backward(int64_t T, int64_t D, const void* x, const void* y, 
     const Span<bf16> gys{static_cast<bf16*>(grad_y), (size_t)(T * D)};
     const Span<float> ghs{grad_h, (size_t)(T * kGates)};
     cudaError_t e = cudaSuccess;
-    if (D >= 8 && T * D < kShortCounters &&
+    if (T * D < kShortCounters &&
         (D % 8 == 0 ? update_backward_tokens<false, 1, 2, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
                           update_backward_tokens<false, 2, 1, 512>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream) ||
                           update_backward_tokens<false, 2, 1, 640>(T, D, xs, ys, hs, d, gs, gys, ghs, &e, stream)

@@ -47,7 +47,7 @@ def embedding():
 
 def norms():
     for T, D in ((1, 1), (1, 5120), (3, 2), (5, 7), (33, 40), (300, 128), (17, 1285), (9, 8200), (2, 20000), (3, 70001),
-                 (700, 64), (2, 131072), (400, 5120), (200, 10240)):
+                 (700, 64), (2, 131072), (400, 5120), (200, 10240), (160, 12288), (3, 16383), (2, 16384)):
         for type_ in ("bf16", "fp32"):
             C.norm_forward_case(T, D, type_, seed=T + D)
             C.norm_backward_case(T, D, type_, seed=T + D)
@@ -70,7 +70,7 @@ def streams():
         C.update_case(T, D, 0.3, seed=T, in_place=True)
         C.collapse_case(T, D, seed=T, residual=False, params=False)
         no_sites(f"update with dropout T={T} D={D}")
-    for shape, offset in (((1, 1), 0), ((3, 5), 0), ((64, 40), 0), ((7, 1285), 1)):
+    for shape, offset in (((1, 1), 0), ((3, 5), 0), ((64, 40), 0), ((7, 1285), 1), ((130, 1001), 3)):
         for type_ in ("bf16", "fp32"):
             C.dropout_case(shape, type_, 0.25, seed=1, offset=offset)
             no_sites(f"dropout {shape} {type_}")
