@@ -43,7 +43,6 @@ constexpr int kRanked = 32;          // tokens a ranking block places, 8 threads
 constexpr int kFan = 16;             // runs per merge pass
 constexpr int kBatch = 32;           // ordered tokens per listing of rows
 constexpr int kAhead = 8;            // rows loaded ahead of the one being added
-constexpr int kZeroRows = 4;         // table rows per zeroing block, one a warp
 constexpr int kMaxChunks = 4096;
 constexpr int kJoinBlocks = 4 * 152;
 
@@ -58,6 +57,14 @@ int64_t chunk_tokens(int64_t T) {
     return c >= least ? c : (least + kBatch - 1) / kBatch * kBatch;
 }
 int64_t chunk_count(int64_t T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
+
+// Table rows that a zeroing warp looks after: 2048 floats, between one row and
+// eight.  One row: T=4096, D=5120, V=32768 takes 130 us (four: 140), but D=64,
+// V=65536 34 us (eight: 19) and T=512, D=515 41 us (three: 29).
+int64_t zero_rows_of(int64_t D) {
+    const int64_t rows = 2048 / D;
+    return rows < 1 ? 1 : rows > 8 ? 8 : rows;
+}
 
 int64_t piece_pitch(int64_t D) { return (D + 7) / 8 * 8; }
 size_t order_bytes(int64_t T) { return ((size_t)T * 8 + 255) / 256 * 256; }
@@ -203,8 +210,8 @@ __device__ __forceinline__ int64_t key_at(const Span<const uint64_t>& o, int64_t
 constexpr int kSamples = 256;         // per run; divides every run but the last
 constexpr int kSamplePitch = kSamples + 1;   // the 16 runs' searches start at the same place: in 16 banks
 constexpr int kMergeThreads = 512;
-constexpr int kMergePlaced = 256;
-constexpr int kMergeSide = 4;         // searches of a thread side by side
+constexpr int kMergePlaced = 64;
+constexpr int kMergeSide = 2;         // searches of a thread side by side
 constexpr size_t kMergeShared = (size_t)kFan * kSamplePitch * 4 + kMergePlaced * 8;
 __global__ void __launch_bounds__(kMergeThreads) merge_runs_kernel(int64_t T, int64_t run, Span<const uint64_t> in,
                                                                    Span<uint64_t> out) {
@@ -304,7 +311,7 @@ __device__ __forceinline__ int64_t lower_bound_warp(const Span<const uint64_t>& 
 // any address (mhcs_words.cuh); the workspace's rows have a pitch of whole
 // vectors.
 struct SumArgs {
-    int64_t T, V, D, pitch, chunk, chunks, slabs;
+    int64_t T, V, D, pitch, chunk, chunks, slabs, zero_rows;   // zero_rows: of a warp
     int n_streams;
     float scale;
     bool accumulate;
@@ -408,13 +415,11 @@ struct RowWriter {
     }
 };
 
-// Each warp zeroes the absent ones of its own kZeroRows / 4 rows.
+// A warp zeroes the absent ones of zero_rows rows.
 template <bool WORDS>
 __device__ void zero_rows(const SumArgs& a, int64_t first) {
-    constexpr int kPerWarp = kZeroRows / (kThreads / 32);
     const int lane = threadIdx.x & 31;
-    first += (threadIdx.x >> 5) * kPerWarp;
-    const int64_t last = first + kPerWarp < a.V ? first + kPerWarp : a.V;
+    const int64_t last = first + a.zero_rows < a.V ? first + a.zero_rows : a.V;
     int64_t at = -1, next = -1;   // next: the first id at or above the row, at its place
     const float zero[4] = {0.f, 0.f, 0.f, 0.f}, one[1] = {0.f};
     for (int64_t v = first; v < last; ++v) {
@@ -449,7 +454,7 @@ __device__ __forceinline__ void flush(const SumArgs& a, RowWriter<WORDS>& out, i
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
 }
 
-// Blocks 0 .. chunks * slabs - 1 sum; the others zero kZeroRows rows each.
+// Blocks 0 .. chunks * slabs - 1 sum; the warps of the others zero rows of the table.
 //
 // The rows of a batch of ordered tokens are listed in shared memory, NS rows
 // (the streams of a token, or one row when n_streams is not 4) to an item,
@@ -461,7 +466,7 @@ template <bool WORDS, int NS>
 __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
     ptx::grid_dependency_wait();
     if ((int64_t)blockIdx.x >= a.chunks * a.slabs) {
-        zero_rows<WORDS>(a, ((int64_t)blockIdx.x - a.chunks * a.slabs) * kZeroRows);
+        zero_rows<WORDS>(a, (((int64_t)blockIdx.x - a.chunks * a.slabs) * (kThreads / 32) + (threadIdx.x >> 5)) * a.zero_rows);
         return;
     }
     constexpr int kItems = NS == 1 ? kAhead : kAhead / 2;
@@ -635,7 +640,8 @@ cudaError_t lookup_ids(const Args& a, cudaStream_t stream) {
 
 template <bool WORDS>
 cudaError_t sum_typed(const SumArgs& s, cudaStream_t stream) {
-    const int64_t zeroing = s.accumulate ? 0 : (s.V + kZeroRows - 1) / kZeroRows;
+    const int64_t per_block = s.zero_rows * (kThreads / 32);
+    const int64_t zeroing = s.accumulate ? 0 : (s.V + per_block - 1) / per_block;
     cudaError_t e = launch_early(s.n_streams == 4 ? sum_runs_kernel<WORDS, 4> : sum_runs_kernel<WORDS, 1>,
                                  dim3((unsigned)(s.chunks * s.slabs + zeroing)), dim3(kThreads), 0, stream, s);
     if (e != cudaSuccess || s.chunks < 2) return e;
@@ -691,6 +697,7 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
     s.slabs = (a.D + kThreads * N - 1) / (kThreads * N);
     s.chunk = chunk_tokens(a.T);
     s.chunks = chunk_count(a.T);
+    s.zero_rows = zero_rows_of(a.D);
     s.n_streams = a.n_streams;
     s.scale = a.scale;
     s.accumulate = a.accumulate;
