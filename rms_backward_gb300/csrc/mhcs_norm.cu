@@ -871,7 +871,9 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
 
 // Parameter gradients: the partials of a column in a fixed order (16 threads
 // each add every 16th part, then their sums are added in order).
-// blockIdx.y: 0 gamma, 1 beta.
+// blockIdx.y: 0 gamma, 1 beta.  A thread's loads are all under way at once: the
+// kernel is little but their latency.
+constexpr int kReduceBatch = (kSms + 15) / 16;   // parts of the rows' kernels in one batch
 __global__ void __launch_bounds__(512) reduce_parts_kernel(int64_t D, int64_t parts, bool accumulate,
                                                            Span<float> partial, Span<float> gamma, Span<float> beta) {
     __shared__ float s[16][33];
@@ -879,14 +881,23 @@ __global__ void __launch_bounds__(512) reduce_parts_kernel(int64_t D, int64_t pa
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
     const Span<float> out = blockIdx.y == 0 ? gamma : beta;
     if (out.p == nullptr) return;
-    float sum = 0.f;
-    if (c < D)
-#pragma unroll 8
-        for (int64_t q = threadIdx.y; q < parts; q += 16) sum += scalar_at(partial, (q * 2 + blockIdx.y) * D + c, 10);
+    float sum = 0.f, o[1] = {0.f};
+    if (c < D) {
+        if (threadIdx.y == 0 && accumulate) o[0] = scalar_at(out, c, 11);
+        for (int64_t first = threadIdx.y; first < parts; first += 16 * kReduceBatch) {
+            float v[kReduceBatch];
+#pragma unroll
+            for (int k = 0; k < kReduceBatch; ++k) {
+                const int64_t q = first + 16 * k;
+                v[k] = q < parts ? scalar_at(partial, (q * 2 + blockIdx.y) * D + c, 10) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kReduceBatch; ++k) sum += v[k];
+        }
+    }
     s[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
     if (threadIdx.y != 0 || c >= D) return;
-    float o[1] = {accumulate ? scalar_at(out, c, 11) : 0.f};
     sum = 0.f;
 #pragma unroll
     for (int q = 0; q < 16; ++q) sum += s[q][threadIdx.x];
@@ -970,14 +981,21 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
     const bool packed = a.D % N == 0 && rows_packed(a.x, a.x_stride, N) && rows_packed(a.y, a.y_stride, N) &&
                         aligned16(a.gamma) && aligned16(a.beta);
     cudaError_t e = cudaSuccess;
+    // Few rows: in registers.  A ring's start (its slots, gamma and beta in
+    // shared memory) pays from more than one wave of blocks on: T=1, D=5120
+    // takes 2.3 us in registers, 3.0 in the ring; T=304 3.2 and 3.7, T=608 5.9
+    // and 4.6; D=1280: T=608 2.5 and 3.2, T=912 3.7 and 3.5.  Unaligned: D=1285:
+    // T=1216 5.9 and 6.4, T=2432 10.4 and 10.5.
+    const int64_t per_sm = a.T * a.D / kSms;
+    const bool few = a.T <= 2 * kSms || per_sm <= (packed ? 5120 : 10240);
     if (packed) {
-        // few rows: more threads each, for latency
-        if ((a.T <= kSms && forward_rows<E, MIX, N, 1>(p, &e, stream)) ||
+        if ((few && forward_rows<E, MIX, N, 1>(p, &e, stream)) ||
             forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) ||
-            forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream) ||
-            (sizeof(E) == 4 && forward_rows<E, MIX, N, 8>(p, &e, stream)))
+            forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream))
             return e;
-    } else if ((a.T <= kSms && forward_rows<E, MIX, 1, 4>(p, &e, stream)) ||
+        if constexpr (sizeof(E) == 4)
+            if (forward_rows<E, MIX, N, 8>(p, &e, stream)) return e;
+    } else if ((few && forward_rows<E, MIX, 1, 4>(p, &e, stream)) ||
                forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) ||
                forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream)) {
         return e;
@@ -1031,10 +1049,9 @@ cudaError_t backward_typed(const Args& a, cudaStream_t stream) {
                 done = backward_rows<E, true, true, 1, 2, 512>(p, &p.parts, &e, stream) ||
                        backward_rows<E, true, true, 2, 1, 512>(p, &p.parts, &e, stream);
         } else {
-            constexpr int S = sizeof(E) == 4 ? 2 : 3;
-            done = packed ? backward_rows<E, false, false, 16 / N, S, 640>(p, &p.parts, &e, stream) ||
+            done = packed ? backward_rows<E, false, false, 16 / N, 2, 640>(p, &p.parts, &e, stream) ||
                                 backward_rows<E, false, false, 32 / N, 1, 512>(p, &p.parts, &e, stream)
-                          : backward_rows<E, false, true, 16 / N, S, 640>(p, &p.parts, &e, stream) ||
+                          : backward_rows<E, false, true, 16 / N, 2, 640>(p, &p.parts, &e, stream) ||
                                 backward_rows<E, false, true, 32 / N, 1, 512>(p, &p.parts, &e, stream);
         }
         if (!done) {
