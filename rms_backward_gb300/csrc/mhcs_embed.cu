@@ -14,13 +14,20 @@
 // 17 M comparisons, a few microseconds on the whole GPU (a bitonic network in
 // one block took 37).  Above 4096 tokens the tiles have 1024, and passes merge
 // 16 sorted runs at a time: an element's place is its place in its own run
-// plus, for each other run, the number of smaller elements.
+// plus, for each other run, the number of smaller elements.  (One tile against
+// tiles of 1024 and a pass, T=4096, D=5120: 59 and 64 us; sixteen tiles of 4096
+// and a pass against tiles of 1024 and two, T=65536, D=1024: 200 and 177.)
 // Summing: the ordered tokens are cut into chunks; a block sums one chunk over
 // one slab of columns.  A run inside one chunk is written at once; the pieces
 // of a run that crosses chunks go to the workspace and a last kernel adds them
 // in order, so that one frequent token does not leave one block with most of
 // the work.  Rows without tokens are zeroed by blocks of the summing kernel.
 // Bound by HBM: grad_x is read once and the table's gradient written once.
+// T=4096, four streams of 5120 into V=32768 rows: 130.5 us written (95% of the
+// 6.77 TB/s of a plain copy), 59 added (63%: ordering takes 8 us and joining 6,
+// launches' latencies, and the sum 38).  T=16384: 170 us added (79%); T=65536,
+// D=1024: 177 (57%: ordering 50).  T=1000, one stream of 1285: 12 us, three
+// launches and the trips to memory that follow one another.
 #include "mhcpb.h"
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
@@ -50,6 +57,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // Ordered tokens per summing chunk: T / 256 between 4 and 32, so that a short
 // batch too is spread over the GPU, and more where that would make over 4096.
+// (32 always: T=512, D=5120 takes 27.1 us instead of 13.3, T=4096 64.8 instead
+// of 59.9.  At most 16: T=65536, D=1024 184.8 instead of 177.0.)
 int64_t chunk_tokens(int64_t T) {
     int64_t c = T / 256;
     c = c < 4 ? 4 : c > kBatch ? kBatch : c;
@@ -79,6 +88,8 @@ __device__ __forceinline__ int64_t id_at(const Span<const I>& ids, int64_t t, in
 
 // ------------------------------------------------------------ forward
 // Eight columns per thread; WORDS: rows at any address (mhcs_words.cuh), D of any size.
+// The streams' rows are written from registers, so a table row is read once for
+// all of them.  T=16384, D=5120, four streams: 113 us (96%).
 template <typename E, typename I, bool WORDS>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(int64_t T, int64_t V, int64_t D, VectorGrid grid,
                                                                 int n_streams, float scale, Span<const E> table,
@@ -203,7 +214,11 @@ __device__ __forceinline__ int64_t key_at(const Span<const uint64_t>& o, int64_t
 }
 
 // Places kMergePlaced consecutive elements in the merge of their group of 16
-// runs.  The runs hold consecutive tokens, so an equal id counts when its run
+// runs.  Few per block, so that a short batch occupies the GPU: 512, 256, 128, 64
+// take 69, 62, 54, 55 us for the whole gradient at T=16384, D=1280, one stream,
+// and 79, 70, 67, 64 at T=8192, D=2560.  Runs of 8 a pass instead of 16: 163 us
+// instead of 177 at T=65536, but 61 instead of 55 at T=16384 (a pass more).
+//  The runs hold consecutive tokens, so an equal id counts when its run
 // comes before the element's.  The block searches kSamples ids of every run in
 // shared memory, then what lies between two of them in global memory (with
 // 1024 samples, reading them cost more than the two halvings they save).
@@ -460,7 +475,8 @@ __device__ __forceinline__ void flush(const SumArgs& a, RowWriter<WORDS>& out, i
 // (the streams of a token, or one row when n_streams is not 4) to an item,
 // with where runs end; a thread adds its columns of one item after another.
 // The rows come through per-thread copies, kAhead items of one row or
-// kAhead / 2 of four ahead.
+// kAhead / 2 of four ahead (twice that: T=16384, D=5120 added 185 us instead of
+// 176).  Four rows to an item: T=4096, D=5120 140 us, one 152.
 constexpr uint32_t kRunEnds = 1u << 31, kFlush = 1u << 30, kRowMask = kFlush - 1;   // T n_streams <= 2^28
 template <bool WORDS, int NS>
 __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
@@ -522,15 +538,16 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
 #pragma unroll 1
                     for (int s = 0; s < NS; ++s)
                         copy_edge(mine + (item % kItems * NS + s) * P - lane, a.grad_x.p, a.grad_x.count,
-                                      at + s * a.D - lane * N, width, 11);
-                } else
+                                  at + s * a.D - lane * N, width, 11);
+                } else {
 #pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    uint4* const slot = mine + (item % kItems * NS + s) * P;
-                    if constexpr (WORDS) {
-                        copy_chunks(slot - lane, a.grad_x, at + s * a.D - lane * N, width, 11);
-                    } else if (c < a.D) {
-                        if (a.grad_x.has(at + s * a.D, N, 11)) copy16(slot, a.grad_x.p + at + s * a.D);
+                    for (int s = 0; s < NS; ++s) {
+                        uint4* const slot = mine + (item % kItems * NS + s) * P;
+                        if constexpr (WORDS) {
+                            copy_chunks(slot - lane, a.grad_x, at + s * a.D - lane * N, width, 11);
+                        } else if (c < a.D) {
+                            if (a.grad_x.has(at + s * a.D, N, 11)) copy16(slot, a.grad_x.p + at + s * a.D);
+                        }
                     }
                 }
             }
@@ -576,7 +593,8 @@ __global__ void __launch_bounds__(kThreads) sum_runs_kernel(SumArgs a) {
 
 // Adds the pieces of each run that crosses chunks, over one slab of columns at
 // a time: each of kJoinParts groups of threads a part of them in order, then
-// the parts in order.
+// the parts in order.  A few trips to memory that follow one another: 6 to 14
+// us.  2, 4, 8 parts: 182, 177, 184 us for the whole at T=65536, D=1024.
 constexpr int kJoinParts = 4;
 template <bool WORDS>
 __global__ void __launch_bounds__(kThreads * kJoinParts) join_runs_kernel(SumArgs a) {

@@ -11,6 +11,12 @@
 // with dX' the gradient of the streams after the sublayer, so that the
 // residual path's share is added in FP32 and rounded once.
 //
+// Bound by HBM in long batches: 4 bytes per BF16 element forward and 6 for the
+// gradient; collapsed rows 10 and 26 per column, so the streams are read once
+// and neither u nor du ever goes to memory.  The fractions below are of the
+// 6.77 TB/s that a plain copy reaches; "replayed" times are calls captured in
+// a graph, without the host's share.
+//
 // FP32 statistics and sums; the variance is centred (two passes over the row),
 // not a difference of squares.  The parameter gradients are summed over a
 // number of row groups that depends on T alone, then over the groups in order:
@@ -103,7 +109,10 @@ __device__ __forceinline__ float scalar_at(const Span<F>& s, int64_t i, uint32_t
     return v[0];
 }
 
-// Any row length: the row is read again for each pass (from L1 or L2).
+// Rows too long for the kernels below (16-bit types above 18,432 columns, not
+// aligned 16,384; FP32 20,480 and 10,240; collapsed 10,240): a block reads its
+// row again for each pass, from L1 or L2.  T=2048, D=16384 takes 36.5 us here,
+// 29.7 through shared memory.
 template <typename E, bool MIX, int N>
 __global__ void __launch_bounds__(kThreads) forward_any_kernel(Params<E> a) {
     ptx::grid_dependency_wait();
@@ -149,8 +158,11 @@ __global__ void __launch_bounds__(kThreads) forward_any_kernel(Params<E> a) {
 // ------------------------------------------------------------ forward, rows in registers
 // A group of G threads holds one row, VPT pieces of N columns per thread (N is
 // a 16-byte vector, or 1 for rows that are not aligned), everything loaded
-// before anything is used.  Blocks are small and many, so that some load
-// while others reduce or store.
+// before anything is used.  For few rows, where a launch and one trip to
+// memory are all there is: one vector per thread, so that a row has many.
+// T=1, D=5120: 2.3 us replayed, of which an empty launch is about 1.6.
+// Also FP32 rows of 10,241 to 20,480 columns, eight vectors per thread
+// (T=2048, D=16384: 48.2 us, 82%; the kernel above 71.9).
 template <typename E, bool MIX, int N, int VPT>
 __global__ void __launch_bounds__(640) forward_rows_kernel(Params<E> a, int G, int R) {
     ptx::grid_dependency_wait();
@@ -221,9 +233,20 @@ __global__ void __launch_bounds__(640) forward_rows_kernel(Params<E> a, int G, i
 // ------------------------------------------------------------ forward, rows through shared memory
 // Groups, per-thread copies S rows ahead and columns as in backward_rows_kernel
 // below.  Each warp centres its own columns (their mean m_w, then the squares
-// about it) and publishes both, so that one barrier gives the row's statistics
-// without cancellation: mean = sum n_w m_w / D and
-// D var = sum q_w + sum n_w (m_w - mean)^2.
+// q_w about it) and publishes both, so that one barrier gives the row's
+// statistics.  With d_w = m_w - m_0:
+//   mean = m_0 + sum n_w d_w / D,
+//   var = (sum q_w + sum n_w d_w^2) / D - (mean - m_0)^2.
+// m_0 is the mean of n_0 of the row's own columns, so the difference cancels at
+// most a factor D / n_0, the number of warps, however far the row is from zero.
+// T=16384, D=5120: 55.7 us (89%); collapsed 133 (93%).  T=4096: 20.5 (61%) and
+// 35.5 (87%): about 8 and 4 us are the first rows' way in and the last ones'
+// out.  In between it is the SM's own work that binds, 37% of the issue slots
+// and 46% of the shared-memory pipe in use by 20 warps.  Taken because, for
+// T=4096 / 16384: rows in registers 30.7 / 113 us; two vectors and four rows
+// ahead 21.7 / 68.5; two rows at a time, for gamma's and beta's loads, 22.4 /
+// 65.8.  One row ahead less where that makes longer rows fit: collapsed above
+// 8,192 columns (not aligned 6,656), plain above 13,312 (12,288).
 template <typename E, bool MIX, bool WORDS, int VPT, int S>
 struct ForwardShape {
     static constexpr int N = Elem<E>::kPack;
@@ -409,7 +432,10 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, WORDS, VPT, S>::kMaxThre
     copies_wait<0>();
 }
 
-// One row per block: its input gradient (and the gates').
+// Rows too long for the kernel below (above 16,384 columns; collapsed 10,240, not
+// aligned 8,192), one per block, read twice; the parameter gradients read
+// everything once more.  T=2048, D=10240 collapsed takes 329 us
+// here, 153 below.
 template <typename E, bool MIX, int N>
 __global__ void __launch_bounds__(kThreads) backward_rows_any_kernel(Params<E> a) {
     ptx::grid_dependency_wait();
@@ -516,6 +542,22 @@ __global__ void __launch_bounds__(kThreads) backward_columns_any_kernel(Params<E
 // slots again (cheaper than holding u and w in registers), writes the
 // gradients and refills each slot as it leaves it.  The other groups of the
 // block compute while one waits.
+//
+// T=16384, D=5120: 84.7 us (88%); collapsed 333 (97%, a copy of nine arrays to
+// four through the same slots takes 325).  T=4096: 28.3 (66%) and 92.6 (87%).
+// Register spills cost more than anything else here (the collapsed gradient
+// fell from 480 us to 337 when the last 88 bytes went), so what a row needs is
+// formed when it is needed and the shapes are as wide as registers allow.
+// Collapsed, T=4096:
+//   1 vector, 2 rows ahead, 640 threads   D=5120:  92.7 us   (up to D=5120)
+//   2 vectors, 1 ahead, 512 threads       D=5120: 113.2      (up to D=8192: 174 us, 74%)
+//   2 vectors, 1 ahead, 640 threads       D=8192: 253        (up to D=10240; it spills)
+// Plain rows: two 16-bit vectors or four of FP32, 2 rows ahead (FP32 T=4096 /
+// 16384: 46.7 / 172 us; 1 ahead 49.7 / 161; 3 ahead slower), and up to D=16384
+// twice as many with 512 threads, 1 ahead (T=2048, D=16384: 57 us; the kernels
+// above 105).
+// Rows at any address take 2 to 3 times as long (T=4096, D=1285: 19.7 us,
+// collapsed 66): bound by the instructions that put vectors together.
 template <typename E, bool MIX, bool WORDS, int VPT, int S, int MAX>
 struct RowsShape {
     static constexpr int N = Elem<E>::kPack;
@@ -990,15 +1032,19 @@ cudaError_t forward_typed(const Args& a, cudaStream_t stream) {
     const bool few = a.T <= 2 * kSms || per_sm <= (packed ? 5120 : 10240);
     if (packed) {
         if ((few && forward_rows<E, MIX, N, 1>(p, &e, stream)) ||
-            forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) ||
-            forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream))
+            forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream))
             return e;
-        if constexpr (sizeof(E) == 4)
+        if constexpr (sizeof(E) == 2) {
+            if (forward_ring<E, MIX, false, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream)) return e;
+        } else {
             if (forward_rows<E, MIX, N, 8>(p, &e, stream)) return e;
-    } else if ((few && forward_rows<E, MIX, 1, 4>(p, &e, stream)) ||
-               forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream) ||
-               forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream)) {
-        return e;
+        }
+    } else {
+        if ((few && forward_rows<E, MIX, 1, 4>(p, &e, stream)) ||
+            forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 2 : 3>(p, &e, stream))
+            return e;
+        if constexpr (sizeof(E) == 2)
+            if (forward_ring<E, MIX, true, MIX ? 2 : 4, MIX ? 1 : 2>(p, &e, stream)) return e;
     }
     return launch_early(packed && a.D % 8 == 0 ? forward_any_kernel<E, MIX, 8> : forward_any_kernel<E, MIX, 1>,
                         dim3((unsigned)a.T), dim3(kThreads), 0, stream, p);

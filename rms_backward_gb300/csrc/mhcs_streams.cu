@@ -6,8 +6,11 @@
 //                    dH_post[i] = <dX'_i, drop(y)>,  dH_res[i][j] = <dX'_i, X_j>
 //
 // FP32 arithmetic, one rounding to BF16 at each store.  The mask is drawn
-// again from the counter wherever it is needed, so it takes no memory.  All
-// three are bound by HBM: 4, 18 and 20 bytes per BF16 element of y.
+// again from the counter wherever it is needed, so it takes no memory.  4, 18
+// and 20 bytes per BF16 element of y: the update and its gradient are bound by
+// HBM, dropout of a 16-bit type by the generator.  Fractions are of the 6.77
+// TB/s that a plain copy reaches; "replayed" times are calls captured in a
+// graph, without the host's share.
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"
@@ -28,7 +31,9 @@ constexpr int kMaxShared = 227 * 1024;   // shared memory of a block
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Any alignment and size: the four elements of a counter per thread and step.
+// Tensors that do not begin on a 16-byte boundary, and of 2^34 elements and more:
+// the four elements of a counter per thread and step.  4096 x 5120 BF16, one
+// element off: 35 us; on the boundary, below: 18.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) dropout_any_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
     ptx::grid_dependency_wait();
@@ -49,6 +54,11 @@ __global__ void __launch_bounds__(kThreads) dropout_any_kernel(int64_t n, Span<c
 
 // kDropPacks vectors of 16 bytes per thread, a block's width apart; needs
 // n < kShortCounters and aligned pointers.  The last, partial vector is one thread's.
+// T=16384, D=5120 BF16: 68.6 us (72%), T=4096 18.3: the generator's 18
+// multiplications of 32 by 32 bits for four elements alone take 61 of the 69
+// us.  FP32, with twice the bytes per counter, runs at HBM's rate (T=8192: 48.6
+// us).  A thread's vectors share the key schedule; 1, 2, 4, 8 vectors: 77.3,
+// 70.9, 68.6, 83.4 us.
 constexpr int kDropPacks = 4;
 template <typename E>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(int64_t n, Span<const E> x, Span<E> y, Drop d) {
@@ -135,7 +145,11 @@ __device__ __forceinline__ void update_column(int64_t t, int64_t c, int64_t D, c
     }
 }
 
-// Any size: one block per token, a column of every stream per thread and step.
+// Rows at any address and of any size, one block per token, a column of every
+// stream per thread and step.  For short odd rows, where putting vectors
+// together costs more than it saves: D=63 (T=32768) 30.0 us here and 48.5 with
+// vectors, D=127 (T=16384) 21.7 and 26.4, D=129 25.2 and 24.7, D=255 35.6 and
+// 26.4.
 __global__ void __launch_bounds__(kThreads) update_forward_any_kernel(int64_t D, Span<const bf16> x,
                                                                       Span<const bf16> y, Span<const float> h,
                                                                       Drop d, Span<bf16> x_out) {
@@ -147,6 +161,8 @@ __global__ void __launch_bounds__(kThreads) update_forward_any_kernel(int64_t D,
     for (int64_t c = threadIdx.x; c < D; c += kThreads) update_column(t, c, D, gate, x, y, d, key, x_out);
 }
 
+// Tokens of more columns than update_backward_tokens_kernel takes (10,240; not
+// aligned: 8,192).  T=2048, D=10240 takes 296 us here, 84 there.
 __global__ void __launch_bounds__(kThreads) update_backward_any_kernel(int64_t D, Span<const bf16> x,
                                                                    Span<const bf16> y, Span<const float> h,
                                                                    Drop d, Span<const bf16> gout,
@@ -227,7 +243,10 @@ __device__ __forceinline__ void drop_eight(const Drop& d, const ShortPhilox& ran
 }
 
 // One vector of every stream per thread, everything loaded before anything is
-// used.  WORDS: rows at any address (mhcs_words.cuh), D of any size.
+// used: five loads per thread keep enough on their way, and nothing is shared
+// between threads.  T=4096, D=5120 with dropout: 60.8 us (92%), T=16384 233
+// (96%); one token 1.6 us replayed, an empty launch's time.  WORDS: rows at any
+// address (mhcs_words.cuh), D of any size (T=4096, D=1285: 33 us).
 template <bool WORDS>
 __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
     int64_t T, int64_t D, VectorGrid grid, bool gates_aligned, Span<const bf16> x, Span<const bf16> y,
@@ -310,6 +329,12 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
 // ... of it, VPT of them), its inputs copied S tokens ahead into per-thread
 // slots.  The token's 20 dot products are left in shared memory by each warp
 // and added up after the group's barrier, which the outputs do not wait for.
+// T=4096, D=5120 with dropout: 73.0 us (85%), T=16384 277 (90%); without, 66.4
+// and 100%: the generator's instructions bind.  Shapes, T=4096: 1 vector, 2
+// tokens ahead, 640 threads: D=5120 73.5 us, T=16384 277; 2 vectors, 1 ahead,
+// 512 threads: 77.6 and 294, D=8192 100.9 (99%); 2 vectors by 640 threads: D=8192
+// 131 (spills), kept for up to 10,240 columns.  Short odd rows stay here: T=65536,
+// D=7 takes 134 us, element by element 454.
 template <bool WORDS, int VPT, int S, int MAX>
 struct TokenShape {
     static constexpr int kMaxThreads = MAX;            // 640: 96 registers a thread; 512: 128
@@ -540,6 +565,7 @@ cudaError_t update_forward(int64_t T, int64_t D, const void* x, const void* y, c
     const Span<const bf16> ys{static_cast<const bf16*>(y), (size_t)(T * D)};
     const Span<const float> hs{h, (size_t)(T * kGates)};
     const Span<bf16> os{static_cast<bf16*>(x_out), (size_t)(T * kStreams * D)};
+    // 32-bit vector numbers and counters
     if ((D % 8 == 0 || D >= 128) && T * D < kShortCounters && (D + 7) / 8 * T <= INT32_MAX) {
         const VectorGrid grid((D + 7) / 8, kThreads, D % 8 != 0);
         return launch_early(D % 8 == 0 ? update_forward_vectors_kernel<false> : update_forward_vectors_kernel<true>,
