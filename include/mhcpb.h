@@ -305,8 +305,9 @@ mhcpb_status_t mhcpb_execute_static_scratch(int64_t T, int64_t K, uint32_t flags
  * backward reads grad_proj in); r FP32 [T] (overwritten).  One streaming
  * kernel (tensor cores for the projection, CUDA cores for the squares) and a
  * fixed-order reduction of per-512-column partials: bitwise reproducible and
- * independent of the SM count.  The stream collapse the page's forward also
- * fuses needs weights the pages do not define and is not part of it.
+ * independent of the SM count.  The stream collapse that the page's
+ * forward also fuses is a call of its own here (mhcpb_collapse_norm_forward,
+ * by the gates H_pre).
  *
  * Uses the plan's T and K (any flags).  `eps` must be finite and >= 0.
  * Workspace: mhcpb_forward_workspace_bytes (ceil(K/512) * 25 * T' * 4 bytes,
@@ -442,7 +443,7 @@ mhcpb_status_t mhcpb_embed_forward(int64_t T, int64_t V, int64_t D, int n_stream
  * grad_x[t, s, :], FP32 [V, D]; rows no token names are written as zeros, or
  * left alone with MHCPB_ACCUMULATE_DW.  grad_x: BF16 [T, n_streams * D].  Ids
  * outside [0, V) contribute nothing.  The tokens are sorted by id and each
- * row is summed in a fixed order (no atomic adds). */
+ * row is summed in a fixed order (no sum uses atomics). */
 mhcpb_status_t mhcpb_embed_workspace_bytes(int64_t T, int64_t V, int64_t D, size_t* bytes);
 mhcpb_status_t mhcpb_embed_backward(int64_t T, int64_t V, int64_t D, int n_streams,
                                     const void* grad_x, const void* ids, int id_bytes, float scale,

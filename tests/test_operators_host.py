@@ -76,7 +76,7 @@ def test_workspace_sizes(lib):
         assert fn(*[4] * k, ctypes.byref(n)) == abi.MHCPB_OK and n.value > 0
     # order (two buffers) and a list of chunks, in 256-byte multiples, and two FP32 rows (of whole vectors) per chunk of ordered tokens
     assert m.mhc_embed_workspace_bytes(33, 7, 10) == 2 * 512 + 256 + 9 * 2 * 16 * 4
-    assert m.mhc_embed_workspace_bytes(4096, 7, 10) == 2 * 32768 + 768 + 128 * 2 * 16 * 4
+    assert m.mhc_embed_workspace_bytes(4096, 7, 10) == 2 * 32768 + 1280 + 256 * 2 * 16 * 4
 
 
 def test_checked_operator_sites_in_a_normal_build(lib):
