@@ -17,10 +17,12 @@
 // 6.77 TB/s that a plain copy reaches; "replayed" times are calls captured in
 // a graph, without the host's share.
 //
-// FP32 statistics and sums; the variance is centred (two passes over the row),
-// not a difference of squares.  The parameter gradients are summed over a
-// number of row groups that depends on T alone, then over the groups in order:
-// the same bits on every call and GPU.
+// FP32 statistics and sums; the variance is of centred values, not a difference
+// of squares.  z is formed as u rs - mu rs in the gradient: one product less, and
+// its error, 2^-24 |mu| rs, is what rounding mu to FP32 costs anyway.  The
+// parameter gradients are summed over row groups whose number depends on T, D
+// and the type alone, then over the groups in order: the same bits on every
+// call and GPU.
 #include "mhcs_common.cuh"
 #include "mhcs_internal.h"
 #include "mhcs_ring.cuh"

@@ -45,6 +45,21 @@ def _need(t, name, shape, dtype):
     return t.data_ptr()
 
 
+def _compact(t, name, dtype=None):
+    """t is a compact tensor (of this type, where given)."""
+    if (dtype is not None and t.dtype is not dtype) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype or t.dtype} tensor, got {t.dtype} {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _scratch(workspace):
+    """(pointer, bytes) of a workspace, or of none."""
+    if workspace is None:
+        return None, 0
+    return _compact(workspace, "workspace"), workspace.nbytes
+
+
 def _maybe(t, name, shape, dtype):
     return None if t is None else _need(t, name, shape, dtype)
 
@@ -67,9 +82,10 @@ def _type(t, name):
 
 
 def _two_dims(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a [T, D] tensor, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a [T, D] tensor, got shape {tuple(shape)}")
+    return shape
 
 
 def _streams(x, name):
@@ -104,9 +120,9 @@ def mhc_embed_forward(ids, table, x, *, scale: float = 1.0, stream=None):
     Ids outside [0, V) give rows of zeros."""
     V, _ = _two_dims(table, "table")
     T, D, n = _ids(ids, table.shape, x, "x")
-    status = _lib().mhcpb_embed_forward(T, V, D, n, _type(table, "table"), _need(table, "table", table.shape, table.dtype),
-                            ids.data_ptr(), ids.element_size(), scale, _need(x, "x", x.shape, _BF16),
-                            _handle(stream, x))
+    status = _lib().mhcpb_embed_forward(T, V, D, n, _type(table, "table"), _compact(table, "table"),
+                                        ids.data_ptr(), ids.element_size(), scale, _compact(x, "x", _BF16),
+                                        _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_embed_forward")
 
@@ -123,10 +139,10 @@ def mhc_embed_backward(ids, grad_x, grad_table, workspace, *, scale: float = 1.0
     ``accumulate``), summed in a fixed order."""
     V, _ = _two_dims(grad_table, "grad_table")
     T, D, n = _ids(ids, grad_table.shape, grad_x, "grad_x")
-    status = _lib().mhcpb_embed_backward(T, V, D, n, _need(grad_x, "grad_x", grad_x.shape, _BF16), ids.data_ptr(),
-                             ids.element_size(), scale, abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
-                             _need(grad_table, "grad_table", grad_table.shape, _F32), workspace.data_ptr(),
-                             workspace.nbytes, _handle(stream, grad_x))
+    status = _lib().mhcpb_embed_backward(T, V, D, n, _compact(grad_x, "grad_x", _BF16), ids.data_ptr(),
+                                         ids.element_size(), scale, abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
+                                         _compact(grad_table, "grad_table", _F32), *_scratch(workspace),
+                                         _handle(stream, grad_x))
     if status:
         abi._check(status, "mhcpb_embed_backward")
 
@@ -136,12 +152,14 @@ def mhc_layernorm_forward(x, gamma, beta, y, mean=None, rstd=None, *, eps: float
     """y = (x - mean) * rstd * gamma + beta over the last axis of x [T, D] (BF16,
     FP16 or FP32; x and y may have a row stride).  gamma, beta: FP32 [D] or
     None; mean, rstd: FP32 [T], both None where no backward follows."""
-    T, D = _two_dims(x, "x")
-    xp, xs = _rows(x, "x", x.shape, x.dtype)
-    yp, ys = _rows(y, "y", x.shape, x.dtype)
+    T, D = shape = _two_dims(x, "x")
+    dtype = x.dtype
+    xp, xs = _rows(x, "x", shape, dtype)
+    yp, ys = _rows(y, "y", shape, dtype)
     status = _lib().mhcpb_layernorm_forward(T, D, _type(x, "x"), xp, xs, _maybe(gamma, "gamma", (D,), _F32),
-                                _maybe(beta, "beta", (D,), _F32), eps, yp, ys, _maybe(mean, "mean", (T,), _F32),
-                                _maybe(rstd, "rstd", (T,), _F32), _handle(stream, x))
+                                            _maybe(beta, "beta", (D,), _F32), eps, yp, ys,
+                                            _maybe(mean, "mean", (T,), _F32), _maybe(rstd, "rstd", (T,), _F32),
+                                            _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_layernorm_forward")
 
@@ -155,17 +173,17 @@ def mhc_layernorm_backward(x, grad_y, gamma, mean, rstd, grad_x, grad_gamma=None
                            accumulate: bool = False, stream=None):
     """grad_x, and grad_gamma and grad_beta where given (added to with
     ``accumulate``), from the forward's x, mean and rstd."""
-    T, D = _two_dims(x, "x")
-    xp, xs = _rows(x, "x", x.shape, x.dtype)
-    gp, gs = _rows(grad_y, "grad_y", x.shape, x.dtype)
-    dp, ds = _rows(grad_x, "grad_x", x.shape, x.dtype)
+    T, D = shape = _two_dims(x, "x")
+    dtype = x.dtype
+    xp, xs = _rows(x, "x", shape, dtype)
+    gp, gs = _rows(grad_y, "grad_y", shape, dtype)
+    dp, ds = _rows(grad_x, "grad_x", shape, dtype)
     status = _lib().mhcpb_layernorm_backward(T, D, _type(x, "x"), xp, xs, gp, gs, _maybe(gamma, "gamma", (D,), _F32),
-                                 _need(mean, "mean", (T,), _F32), _need(rstd, "rstd", (T,), _F32), dp, ds,
-                                 _maybe(grad_gamma, "grad_gamma", (D,), _F32),
-                                 _maybe(grad_beta, "grad_beta", (D,), _F32),
-                                 abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
-                                 0 if workspace is None else workspace.data_ptr(),
-                                 0 if workspace is None else workspace.nbytes, _handle(stream, x))
+                                             _need(mean, "mean", (T,), _F32), _need(rstd, "rstd", (T,), _F32), dp, ds,
+                                             _maybe(grad_gamma, "grad_gamma", (D,), _F32),
+                                             _maybe(grad_beta, "grad_beta", (D,), _F32),
+                                             abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
+                                             *_scratch(workspace), _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_layernorm_backward")
 
@@ -175,8 +193,8 @@ def mhc_dropout(x, y, rng=None, *, p: float, sequence: int = 0, stream=None):
     """y = x / (1 - p) where kept, else 0; the mask comes from ``rng`` (an int64
     CUDA tensor {key, step}), ``sequence`` and the element's index, so the same
     call on the gradient is the gradient.  y may be x."""
-    status = _lib().mhcpb_dropout(x.numel(), _type(x, "x"), _need(x, "x", x.shape, x.dtype), p, _rng(rng, p), sequence,
-                      _need(y, "y", x.shape, x.dtype), _handle(stream, x))
+    status = _lib().mhcpb_dropout(x.numel(), _type(x, "x"), _compact(x, "x"), p, _rng(rng, p), sequence,
+                                  _need(y, "y", x.shape, x.dtype), _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_dropout")
 
@@ -185,10 +203,11 @@ def mhc_dropout(x, y, rng=None, *, p: float, sequence: int = 0, stream=None):
 def mhc_collapse_norm_forward(x, h, gamma, beta, y, mean=None, rstd=None, *, eps: float = 1e-5, stream=None):
     """y = layer norm of sum_s h[:, s] x_s: the sublayer's input [T, D] BF16."""
     T, D = _streams(x, "x")
-    status = _lib().mhcpb_collapse_norm_forward(T, D, _need(x, "x", x.shape, _BF16), _need(h, "h", (T, 24), _F32),
-                                    _maybe(gamma, "gamma", (D,), _F32), _maybe(beta, "beta", (D,), _F32), eps,
-                                    _need(y, "y", (T, D), _BF16), _maybe(mean, "mean", (T,), _F32),
-                                    _maybe(rstd, "rstd", (T,), _F32), _handle(stream, x))
+    status = _lib().mhcpb_collapse_norm_forward(T, D, _compact(x, "x", _BF16), _need(h, "h", (T, 24), _F32),
+                                                _maybe(gamma, "gamma", (D,), _F32),
+                                                _maybe(beta, "beta", (D,), _F32), eps,
+                                                _need(y, "y", (T, D), _BF16), _maybe(mean, "mean", (T,), _F32),
+                                                _maybe(rstd, "rstd", (T,), _F32), _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_collapse_norm_forward")
 
@@ -204,13 +223,12 @@ def mhc_collapse_norm_backward(x, h, grad_y, gamma, mean, rstd, grad_x, grad_h, 
     given) and columns 0..3 of grad_h [T, 24] from grad_y [T, D]."""
     T, D = _streams(x, "x")
     status = _lib().mhcpb_collapse_norm_backward(
-        T, D, _need(x, "x", x.shape, _BF16), _need(h, "h", (T, 24), _F32), _need(grad_y, "grad_y", (T, D), _BF16),
+        T, D, _compact(x, "x", _BF16), _need(h, "h", (T, 24), _F32), _need(grad_y, "grad_y", (T, D), _BF16),
         _maybe(gamma, "gamma", (D,), _F32), _need(mean, "mean", (T,), _F32), _need(rstd, "rstd", (T,), _F32),
         _maybe(grad_x_out, "grad_x_out", x.shape, _BF16), _need(grad_x, "grad_x", x.shape, _BF16),
         _need(grad_h, "grad_h", (T, 24), _F32), _maybe(grad_gamma, "grad_gamma", (D,), _F32),
         _maybe(grad_beta, "grad_beta", (D,), _F32), abi.MHCPB_ACCUMULATE_DW if accumulate else 0,
-        0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
-        _handle(stream, x))
+        *_scratch(workspace), _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_collapse_norm_backward")
 
@@ -220,9 +238,9 @@ def mhc_update_forward(x, y, h, x_out, rng=None, *, p: float = 0.0, sequence: in
     """x_out_i = sum_j H_res[i, j] x_j + H_post[i] dropout(y), H_post and H_res
     from h [T, 24]; x_out may be x."""
     T, D = _streams(x, "x")
-    status = _lib().mhcpb_update_forward(T, D, _need(x, "x", x.shape, _BF16), _need(y, "y", (T, D), _BF16),
-                             _need(h, "h", (T, 24), _F32), p, _rng(rng, p), sequence,
-                             _need(x_out, "x_out", x.shape, _BF16), _handle(stream, x))
+    status = _lib().mhcpb_update_forward(T, D, _compact(x, "x", _BF16), _need(y, "y", (T, D), _BF16),
+                                         _need(h, "h", (T, 24), _F32), p, _rng(rng, p), sequence,
+                                         _need(x_out, "x_out", x.shape, _BF16), _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_update_forward")
 
@@ -232,9 +250,10 @@ def mhc_update_backward(x, y, h, grad_x_out, grad_y, grad_h, rng=None, *, p: flo
     """grad_y [T, D] and columns 4..23 of grad_h [T, 24] from grad_x_out [T, 4 D];
     the streams' own gradient is :func:`mhc_collapse_norm_backward`'s."""
     T, D = _streams(x, "x")
-    status = _lib().mhcpb_update_backward(T, D, _need(x, "x", x.shape, _BF16), _need(y, "y", (T, D), _BF16),
-                              _need(h, "h", (T, 24), _F32), p, _rng(rng, p), sequence,
-                              _need(grad_x_out, "grad_x_out", x.shape, _BF16), _need(grad_y, "grad_y", (T, D), _BF16),
-                              _need(grad_h, "grad_h", (T, 24), _F32), _handle(stream, x))
+    status = _lib().mhcpb_update_backward(T, D, _compact(x, "x", _BF16), _need(y, "y", (T, D), _BF16),
+                                          _need(h, "h", (T, 24), _F32), p, _rng(rng, p), sequence,
+                                          _need(grad_x_out, "grad_x_out", x.shape, _BF16),
+                                          _need(grad_y, "grad_y", (T, D), _BF16),
+                                          _need(grad_h, "grad_h", (T, 24), _F32), _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_update_backward")

@@ -114,3 +114,16 @@ def _t(*shape, dtype=BF):
 def test_python_checks(call):
     with pytest.raises(ValueError):
         call()
+
+
+def test_workspaces_are_compact():
+    """A workspace's size is its bytes, so it has to hold them: none that is expanded or strided."""
+    f32 = lambda *s: _t(*s, dtype=torch.float32)  # noqa: E731
+    for ws in (_t(1, dtype=torch.uint8).expand(1 << 20), _t(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            m.mhc_embed_backward(_t(3, dtype=torch.int64), _t(3, 8), f32(5, 8), ws)
+        with pytest.raises(ValueError, match="workspace"):
+            m.mhc_layernorm_backward(_t(3, 8), _t(3, 8), f32(8), f32(3), f32(3), _t(3, 8), f32(8), f32(8), ws)
+        with pytest.raises(ValueError, match="workspace"):
+            m.mhc_collapse_norm_backward(_t(3, 32), f32(3, 24), _t(3, 8), f32(8), f32(3), f32(3), _t(3, 32), f32(3, 24),
+                                         f32(8), f32(8), ws)
