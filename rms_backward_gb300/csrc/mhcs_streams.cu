@@ -329,12 +329,15 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
 // ... of it, VPT of them), its inputs copied S tokens ahead into per-thread
 // slots.  The token's 20 dot products are left in shared memory by each warp
 // and added up after the group's barrier, which the outputs do not wait for.
-// T=4096, D=5120 with dropout: 73.0 us (85%), T=16384 277 (90%); without, 66.4
-// and 100%: the generator's instructions bind.  Shapes, T=4096: 1 vector, 2
-// tokens ahead, 640 threads: D=5120 73.5 us, T=16384 277; 2 vectors, 1 ahead,
-// 512 threads: 77.6 and 294, D=8192 100.9 (99%); 2 vectors by 640 threads: D=8192
-// 131 (spills), kept for up to 10,240 columns.  Short odd rows stay here: T=65536,
-// D=7 takes 134 us, element by element 454.
+// T=4096, D=5120 with dropout: 67.8 us (91%), T=16384 255 (97%): HBM's rate.  The
+// products are packed over pairs of the gradient's streams, so that 20 sums
+// take 10 register pairs and half the instructions (one sum at a time: 73.0 and
+// 276 us; pairs of columns would take 20 registers more).  Shapes, measured
+// before that, T=4096: 1 vector, 2 tokens ahead, 640 threads: D=5120 73.5 us,
+// T=16384 277; 2 vectors, 1 ahead, 512 threads: 77.6 and 294, D=8192 100.9 (now
+// 99.5, 100%); 2 vectors by 640 threads: D=8192 131 (spills), kept for up to
+// 10,240 columns.  Short odd rows stay here: T=65536, D=7 takes 134 us, element
+// by element 454.
 template <bool WORDS, int VPT, int S, int MAX>
 struct TokenShape {
     static constexpr int kMaxThreads = MAX;            // 640: 96 registers a thread; 512: 128
@@ -444,11 +447,14 @@ __global__ void __launch_bounds__(MAX, 1)
         const float4 post = *reinterpret_cast<const float4*>(posts + stage * 4);
         const float p4[kStreams] = {post.x, post.y, post.z, post.w};
         const bool more = t + S * groups < T;
-        float d16[16], d4[4];   // not pairs: 20 registers less
+        // pairs of streams i: the dot products of dX'_2q and dX'_2q+1 with X_j and y
+        float2 d16p[2][kStreams], d4p[2];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) d16[k] = 0.f;
+        for (int q = 0; q < 2; ++q) {
+            d4p[q] = pair(0.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d4[k] = 0.f;
+            for (int j = 0; j < kStreams; ++j) d16p[q][j] = pair(0.f);
+        }
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int c = c0 + v * step;
@@ -459,23 +465,29 @@ __global__ void __launch_bounds__(MAX, 1)
             drop_eight<WORDS>(d, random, flat, yv, &keep);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float2 xs[kStreams][2], o[2] = {pair(0.f), pair(0.f)};
+                float2 xs[kStreams][2], g[kStreams][2], o[2];
 #pragma unroll
-                for (int j = 0; j < kStreams; ++j)
+                for (int j = 0; j < kStreams; ++j) {
                     unpack_half<bf16>(reinterpret_cast<const uint2*>(row + (v * A + j) * P)[half], xs[j]);
-#pragma unroll
-                for (int s = 0; s < kStreams; ++s) {
-                    float2 g[2];
-                    unpack_half<bf16>(reinterpret_cast<const uint2*>(row + (v * A + kStreams + s) * P)[half], g);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        o[k] = fma2(pair(p4[s]), g[k], o[k]);
-                        d4[s] = fmaf(g[k].x, yv[half * 2 + k].x, fmaf(g[k].y, yv[half * 2 + k].y, d4[s]));
-#pragma unroll
-                        for (int j = 0; j < kStreams; ++j)
-                            d16[4 * s + j] = fmaf(g[k].x, xs[j][k].x, fmaf(g[k].y, xs[j][k].y, d16[4 * s + j]));
-                    }
+                    unpack_half<bf16>(reinterpret_cast<const uint2*>(row + (v * A + kStreams + j) * P)[half], g[j]);
                 }
+                const auto column = [&](const float2 (&f)[2], int k) { return k & 1 ? f[k >> 1].y : f[k >> 1].x; };
+                float oc[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float2 sum = pair(0.f);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float2 gq = make_float2(column(g[2 * q], k), column(g[2 * q + 1], k));
+                        sum = fma2(make_float2(p4[2 * q], p4[2 * q + 1]), gq, sum);
+                        d4p[q] = fma2(gq, pair(k & 1 ? yv[half * 2 + (k >> 1)].y : yv[half * 2 + (k >> 1)].x), d4p[q]);
+#pragma unroll
+                        for (int j = 0; j < kStreams; ++j) d16p[q][j] = fma2(gq, pair(column(xs[j], k)), d16p[q][j]);
+                    }
+                    oc[k] = sum.x + sum.y;
+                }
+                o[0] = make_float2(oc[0], oc[1]);
+                o[1] = make_float2(oc[2], oc[3]);
                 if (d.rng != nullptr)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -492,6 +504,15 @@ __global__ void __launch_bounds__(MAX, 1)
                 if (c < D && gy.has(flat, N, 7)) *reinterpret_cast<uint4*>(gy.p + flat) = packed;
             }
             if (more) fetch_vector(row, t + S * groups, v);
+        }
+        float d16[16];
+        const float d4[4] = {d4p[0].x, d4p[0].y, d4p[1].x, d4p[1].y};
+#pragma unroll
+        for (int j = 0; j < kStreams; ++j) {
+            d16[j] = d16p[0][j].x;
+            d16[4 + j] = d16p[0][j].y;
+            d16[8 + j] = d16p[1][j].x;
+            d16[12 + j] = d16p[1][j].y;
         }
         const float res = warp_sum_sixteen(d16), pos = warp_sum_four(d4);
         float* const mine_dots = dots + parity * (Shape::kDots * dot_pitch) + warp;
