@@ -22,7 +22,7 @@ struct Operand {
     size_t bytes;       // 0: no elements, the pointer is not looked at
     unsigned align;     // bytes, a power of two
     bool output;
-    const void* in_place = nullptr;   // an input this output may be (all of it, element for element)
+    int in_place = -1;  // which of the call's operands, an input, this output may be (all of it, element for element)
 };
 
 mhcpb_status_t cuda_failed(cudaError_t e, const char* what) {
@@ -66,7 +66,7 @@ mhcpb_status_t check_operands(const Operand (&o)[N]) {
         const uintptr_t lo = reinterpret_cast<uintptr_t>(o[i].ptr), hi = lo + o[i].bytes;
         for (int j = 0; j < N; ++j) {
             if (j == i || o[j].bytes == 0) continue;
-            if (o[i].in_place != nullptr && o[j].ptr == o[i].in_place && o[j].ptr == o[i].ptr && !o[j].output) continue;
+            if (j == o[i].in_place && o[j].ptr == o[i].ptr) continue;
             const uintptr_t l = reinterpret_cast<uintptr_t>(o[j].ptr), h = l + o[j].bytes;
             if (lo < h && l < hi) return MHCPB_ERR_ALIASING;
         }
@@ -270,7 +270,7 @@ mhcpb_status_t mhcpb_dropout(int64_t n, int type, const void* x, float p, const 
     const int es = type_bytes(type);
     const Operand o[3] = {{x, (size_t)n * es, (unsigned)es, false},
                           {rng, p > 0.f ? (size_t)16 : 0, 8, false},
-                          {y, (size_t)n * es, (unsigned)es, true, x}};
+                          {y, (size_t)n * es, (unsigned)es, true, 0}};
     const mhcpb_status_t s = check_operands(o);
     if (s != MHCPB_OK || n == 0) return s;
     const cudaError_t e = ops::streams::dropout(n, type, x, y, d, reinterpret_cast<cudaStream_t>(stream));
@@ -376,7 +376,7 @@ mhcpb_status_t mhcpb_update_forward(int64_t T, int64_t D, const void* x, const v
                           {y, td * 2, 16, false},
                           {h, (size_t)(T * ops::kGates) * 4, 4, false},
                           {rng, p > 0.f && T > 0 ? (size_t)16 : 0, 8, false},
-                          {x_out, td * ops::kStreams * 2, 16, true, x}};
+                          {x_out, td * ops::kStreams * 2, 16, true, 0}};
     const mhcpb_status_t s = check_operands(o);
     if (s != MHCPB_OK || T == 0) return s;
     const cudaError_t e = ops::streams::update_forward(T, D, x, y, h, d, x_out, reinterpret_cast<cudaStream_t>(stream));
