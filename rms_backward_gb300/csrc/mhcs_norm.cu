@@ -18,8 +18,9 @@
 // a graph, without the host's share.
 //
 // FP32 statistics and sums; the variance is of centred values, not a difference
-// of squares.  z is formed as u rs - mu rs in the gradient: one product less, and
-// its error, 2^-24 |mu| rs, is what rounding mu to FP32 costs anyway.  The
+// of squares.  z is (u - mu) rs, the subtraction first: u rs - mu rs would save a
+// product, but the rounding of mu rs, 2^-24 |mu| rs, enters every column of a
+// row, 300 times z's own rounding where a row lies 300 deviations from zero.  The
 // parameter gradients are summed over row groups whose number depends on T, D
 // and the type alone, then over the groups in order: the same bits on every
 // call and GPU.
@@ -714,8 +715,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
                 if (s <= XA || residual) align_chunks<E>(row - lane + k * P, misaligned(p), D - (c0 + k / A * step));
             }
         const float2 stat = reinterpret_cast<const float2*>(gates)[kGates / 2];
-        // z = u rstd - mean rstd
-        const float2 rstd2 = pair(stat.y), shift2 = pair(-stat.x * stat.y);
+        const float2 rstd2 = pair(stat.y), mean2 = pair(-stat.x);
         const float4 pre = MIX ? gates[0] : make_float4(0.f, 0.f, 0.f, 0.f);
         const float p4[kStreams] = {pre.x, pre.y, pre.z, pre.w};
         float2 sw = pair(0.f), swz = pair(0.f);
@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
             for (int k = 0; k < H; ++k) {
                 if ((k & 1) == 0) {
                     const float4 g = gammas[(v * (N / 4) + k / 2) * G + i];
-                    z[k] = fma2(z[k], rstd2, shift2);
-                    z[k + 1] = fma2(z[k + 1], rstd2, shift2);
+                    z[k] = mul2(add2(z[k], mean2), rstd2);
+                    z[k + 1] = mul2(add2(z[k + 1], mean2), rstd2);
                     gg[v][k] = fma2(w[k], z[k], gg[v][k]);
                     gg[v][k + 1] = fma2(w[k + 1], z[k + 1], gg[v][k + 1]);
                     gb[v][k] = add2(gb[v][k], w[k]);
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
 #pragma unroll
                         for (int s = 1; s < XA; ++s) z[k] = fma2(pair(p4[s]), x[s][k], z[k]);
                     }
-                    z[k] = fma2(z[k], rstd2, shift2);
+                    z[k] = mul2(add2(z[k], mean2), rstd2);
                     w[k] = fma2(z[k], b2, fma2(w[k], rstd2, a2));
                 }
                 if constexpr (!MIX) {
