@@ -62,10 +62,13 @@ typedef struct mhcpb_plan_s* mhcpb_plan_t;
 typedef enum {
     MHCPB_OK = 0,
     MHCPB_ERR_INVALID_ARG = 1,        /* NULL plan/pointer, addend presence disagreeing with the plan */
-    MHCPB_ERR_UNSUPPORTED_SHAPE = 2,  /* T < 0, K not a positive multiple of 8, or above the maxima below */
-    MHCPB_ERR_MISALIGNED = 3,         /* a pointer not 16-byte aligned (4-byte for the gate operands) */
+    MHCPB_ERR_UNSUPPORTED_SHAPE = 2,  /* a size, count or stride outside the call's limits: T < 0, a plan's K
+                                         not a positive multiple of 8, above the maxima below */
+    MHCPB_ERR_MISALIGNED = 3,         /* a pointer not aligned as the call requires (a plan's calls: 16 bytes,
+                                         4 for the gate operands) */
     MHCPB_ERR_ALIASING = 4,           /* two operands (or workspace) share bytes */
-    MHCPB_ERR_WRONG_DEVICE = 5,       /* a pointer not in device memory of the plan's device */
+    MHCPB_ERR_WRONG_DEVICE = 5,       /* a pointer not in device memory of the plan's device, or without a
+                                         plan of the current device */
     MHCPB_ERR_TF32_NOT_ALLOWED = 6,   /* flags lack MHCPB_ALLOW_TF32 */
     MHCPB_ERR_WORKSPACE_TOO_SMALL = 7,
     MHCPB_ERR_CUDA = 8,               /* a CUDA runtime/driver call failed (see mhcpb_last_cuda_error) */

@@ -173,10 +173,10 @@ const char* mhcpb_status_string(mhcpb_status_t s) {
     switch (s) {
         case MHCPB_OK: return "ok";
         case MHCPB_ERR_INVALID_ARG: return "invalid argument";
-        case MHCPB_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (T >= 1, K a positive multiple of 8, within limits)";
-        case MHCPB_ERR_MISALIGNED: return "pointer not 16-byte aligned";
+        case MHCPB_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (a size, count or stride outside the call's limits)";
+        case MHCPB_ERR_MISALIGNED: return "pointer not aligned as the call requires";
         case MHCPB_ERR_ALIASING: return "operands overlap";
-        case MHCPB_ERR_WRONG_DEVICE: return "pointer not in device memory of the plan's device";
+        case MHCPB_ERR_WRONG_DEVICE: return "pointer not in device memory of the call's device";
         case MHCPB_ERR_TF32_NOT_ALLOWED: return "MHCPB_ALLOW_TF32 is required";
         case MHCPB_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
         case MHCPB_ERR_CUDA: return "CUDA error";
