@@ -2,9 +2,9 @@
 // shape, pointer, alignment and overlap checks, then the launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 
 #include "mhcpb.h"
 #include "mhcpb_check.cuh"
@@ -29,28 +29,26 @@ mhcpb_status_t cuda_failed(cudaError_t e, const char* what) {
     return (mhcpb_status_t)record_cuda_error(e, what);
 }
 
-// One-time set-up of the current device's kernels.
+// One-time set-up of the current device's kernels.  Only success is kept: after
+// an error the next call tries again.  (Two first calls at once may both set up;
+// what they set is the same.)
 mhcpb_status_t device_ready(int device) {
     constexpr int kMaxDevices = 64;
-    static std::once_flag once[kMaxDevices];
-    static mhcpb_status_t status[kMaxDevices];
+    static std::atomic<uint64_t> ready{0};
     if (device < 0 || device >= kMaxDevices) return MHCPB_ERR_INVALID_ARG;
-    std::call_once(once[device], [device] {
-        int major = 0, minor = 0;
-        cudaError_t e;
-        if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device)) != cudaSuccess ||
-            (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device)) != cudaSuccess) {
-            status[device] = cuda_failed(e, "cudaDeviceGetAttribute");
-        } else if (major != 10 || minor != 3) {
-            status[device] = MHCPB_ERR_UNSUPPORTED_DEVICE;
-        } else if ((e = ops::embed::setup()) != cudaSuccess || (e = ops::norm::setup()) != cudaSuccess ||
-                   (e = ops::streams::setup()) != cudaSuccess) {
-            status[device] = cuda_failed(e, "setup (operators)");
-        } else {
-            status[device] = MHCPB_OK;
-        }
-    });
-    return status[device];
+    const uint64_t bit = (uint64_t)1 << device;
+    if ((ready.load(std::memory_order_acquire) & bit) != 0) return MHCPB_OK;
+    int major = 0, minor = 0;
+    cudaError_t e;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device)) != cudaSuccess)
+        return cuda_failed(e, "cudaDeviceGetAttribute");
+    if (major != 10 || minor != 3) return MHCPB_ERR_UNSUPPORTED_DEVICE;
+    if ((e = ops::embed::setup()) != cudaSuccess || (e = ops::norm::setup()) != cudaSuccess ||
+        (e = ops::streams::setup()) != cudaSuccess)
+        return cuda_failed(e, "setup (operators)");
+    ready.fetch_or(bit, std::memory_order_release);
+    return MHCPB_OK;
 }
 
 // An operand with elements needs a pointer, aligned, in memory of the current
