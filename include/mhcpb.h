@@ -416,7 +416,9 @@ mhcpb_status_t mhcpb_gate_backward(int64_t T, int n_iter, const float* proj, con
  * overlap no other operand (MHCPB_ERR_ALIASING), except where "in place" is
  * said.  Layouts are compact and row-major unless a stride is given; a stride
  * counts elements between rows, at least the row's width (else
- * MHCPB_ERR_UNSUPPORTED_SHAPE) and at most 2^24.  Pointers are aligned to
+ * MHCPB_ERR_UNSUPPORTED_SHAPE) and at most 2^24.  Operands with the same stride
+ * may lie in each other's gaps, as column slices of one buffer do; with other
+ * operands the gaps count as the operand's own.  Pointers are aligned to
  * their element's size (MHCPB_ERR_MISALIGNED); streams, their gradients and
  * collapse_norm's and update's other BF16 operands, and workspaces, to 16
  * bytes.  Sizes that are multiples of 8, on 16-byte aligned pointers, run

@@ -23,6 +23,8 @@ struct Operand {
     unsigned align;     // bytes, a power of two
     bool output;
     int in_place = -1;  // which of the call's operands, an input, this output may be (all of it, element for element)
+    size_t pitch = 0;   // bytes from row to row and in a row of a strided operand; 0: compact
+    size_t row = 0;
 };
 
 mhcpb_status_t cuda_failed(cudaError_t e, const char* what) {
@@ -51,6 +53,19 @@ mhcpb_status_t device_ready(int device) {
     return MHCPB_OK;
 }
 
+// Whether two operands share a byte.  Of two with one distance between rows, the
+// rows of one may lie between the other's, such as column slices of one buffer.
+// (The kernels copy whole 16-byte chunks, whose bytes of other columns they do
+// not use, and store nothing outside a row's columns.)  Otherwise the gaps
+// between rows count as the operand's.
+bool share_bytes(const Operand& a, const Operand& b) {
+    const uintptr_t la = reinterpret_cast<uintptr_t>(a.ptr), lb = reinterpret_cast<uintptr_t>(b.ptr);
+    if (la >= lb + b.bytes || lb >= la + a.bytes) return false;
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    const size_t ahead = lb >= la ? (lb - la) % a.pitch : (a.pitch - (la - lb) % a.pitch) % a.pitch;
+    return ahead < a.row || ahead + b.row > a.pitch;   // from a row of a to the next row of b
+}
+
 // An operand with elements needs a pointer, aligned, in memory of the current
 // device; an output overlaps no other operand (but may be its in_place input).
 template <int N>
@@ -61,12 +76,10 @@ mhcpb_status_t check_operands(const Operand (&o)[N]) {
         if (a.bytes > 0 && (reinterpret_cast<uintptr_t>(a.ptr) & (a.align - 1u)) != 0) return MHCPB_ERR_MISALIGNED;
     for (int i = 0; i < N; ++i) {
         if (!o[i].output || o[i].bytes == 0) continue;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(o[i].ptr), hi = lo + o[i].bytes;
         for (int j = 0; j < N; ++j) {
             if (j == i || o[j].bytes == 0) continue;
             if (j == o[i].in_place && o[j].ptr == o[i].ptr) continue;
-            const uintptr_t l = reinterpret_cast<uintptr_t>(o[j].ptr), h = l + o[j].bytes;
-            if (lo < h && l < hi) return MHCPB_ERR_ALIASING;
+            if (share_bytes(o[i], o[j])) return MHCPB_ERR_ALIASING;
         }
     }
     int device = 0;
@@ -86,8 +99,9 @@ bool tokens_ok(int64_t T) { return T >= 0 && T <= MHCPB_MAX_T; }
 bool hidden_ok(int64_t D, int64_t n) { return D >= 1 && D <= MHCPB_MAX_K / n; }
 // rows of `width` elements, `stride` apart
 bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride <= kMaxStride; }
-size_t rows_bytes(int64_t T, int64_t stride, int64_t width, int es) {
-    return T == 0 ? 0 : (size_t)((T - 1) * stride + width) * (size_t)es;
+Operand rows_of(const void* p, int64_t T, int64_t stride, int64_t width, int es, bool output) {
+    const size_t bytes = T == 0 ? 0 : (size_t)((T - 1) * stride + width) * (size_t)es;
+    return {p, bytes, (unsigned)es, output, -1, (size_t)stride * es, (size_t)width * es};
 }
 
 bool drop_args(float p, const void* rng, uint64_t sequence, ops::DropArgs* d) {
@@ -181,10 +195,10 @@ mhcpb_status_t mhcpb_layernorm_forward(int64_t T, int64_t D, int type, const voi
         return MHCPB_ERR_UNSUPPORTED_SHAPE;
     const int es = type_bytes(type);
     const size_t t4 = (size_t)T * 4, d4 = (size_t)D * 4;
-    const Operand o[6] = {{x, rows_bytes(T, x_stride, D, es), (unsigned)es, false},
+    const Operand o[6] = {rows_of(x, T, x_stride, D, es, false),
                           {gamma, gamma ? d4 : 0, 4, false},
                           {beta, beta ? d4 : 0, 4, false},
-                          {y, rows_bytes(T, y_stride, D, es), (unsigned)es, true},
+                          rows_of(y, T, y_stride, D, es, true),
                           {mean, mean ? t4 : 0, 4, true},
                           {rstd, rstd ? t4 : 0, 4, true}};
     const mhcpb_status_t s = check_operands(o);
@@ -227,12 +241,12 @@ mhcpb_status_t mhcpb_layernorm_backward(int64_t T, int64_t D, int type, const vo
     if (workspace_bytes < need) return MHCPB_ERR_WORKSPACE_TOO_SMALL;
     const int es = type_bytes(type);
     const size_t t4 = (size_t)T * 4, d4 = (size_t)D * 4;
-    const Operand o[9] = {{x, rows_bytes(T, x_stride, D, es), (unsigned)es, false},
-                          {grad_y, rows_bytes(T, grad_y_stride, D, es), (unsigned)es, false},
+    const Operand o[9] = {rows_of(x, T, x_stride, D, es, false),
+                          rows_of(grad_y, T, grad_y_stride, D, es, false),
                           {gamma, gamma ? d4 : 0, 4, false},
                           {mean, t4, 4, false},
                           {rstd, t4, 4, false},
-                          {grad_x, rows_bytes(T, grad_x_stride, D, es), (unsigned)es, true},
+                          rows_of(grad_x, T, grad_x_stride, D, es, true),
                           {grad_gamma, grad_gamma ? d4 : 0, 4, true},
                           {grad_beta, grad_beta ? d4 : 0, 4, true},
                           {workspace, need, 16, true}};
