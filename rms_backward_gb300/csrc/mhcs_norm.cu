@@ -716,6 +716,12 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
             }
         const float2 stat = reinterpret_cast<const float2*>(gates)[kGates / 2];
         const float2 rstd2 = pair(stat.y), mean2 = pair(-stat.x);
+        // minus the mean at columns c, c + 1 of a vector from column `first` on; past D
+        // 0, so that z is 0 there too: 0 - mean could overflow when multiplied by rstd
+        const auto centre = [&](int first, int c) {
+            if constexpr (!WORDS) return pair(first < D ? mean2.x : 0.f);
+            return make_float2(first + c < D ? mean2.x : 0.f, first + c + 1 < D ? mean2.x : 0.f);
+        };
         const float4 pre = MIX ? gates[0] : make_float4(0.f, 0.f, 0.f, 0.f);
         const float p4[kStreams] = {pre.x, pre.y, pre.z, pre.w};
         float2 sw = pair(0.f), swz = pair(0.f);
@@ -739,8 +745,8 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
             for (int k = 0; k < H; ++k) {
                 if ((k & 1) == 0) {
                     const float4 g = gammas[(v * (N / 4) + k / 2) * G + i];
-                    z[k] = mul2(add2(z[k], mean2), rstd2);
-                    z[k + 1] = mul2(add2(z[k + 1], mean2), rstd2);
+                    z[k] = mul2(add2(z[k], centre(c0 + v * step, 2 * k)), rstd2);
+                    z[k + 1] = mul2(add2(z[k + 1], centre(c0 + v * step, 2 * k + 2)), rstd2);
                     gg[v][k] = fma2(w[k], z[k], gg[v][k]);
                     gg[v][k + 1] = fma2(w[k + 1], z[k + 1], gg[v][k + 1]);
                     gb[v][k] = add2(gb[v][k], w[k]);
@@ -801,7 +807,7 @@ __global__ void __launch_bounds__(MAX, 1) backward_rows_kernel(Params<E> a, int 
 #pragma unroll
                         for (int s = 1; s < XA; ++s) z[k] = fma2(pair(p4[s]), x[s][k], z[k]);
                     }
-                    z[k] = mul2(add2(z[k], mean2), rstd2);
+                    z[k] = mul2(add2(z[k], MIX ? centre(c0 + v * step, half * 4 + 2 * k) : mean2), rstd2);
                     w[k] = fma2(z[k], b2, fma2(w[k], rstd2, a2));
                 }
                 if constexpr (!MIX) {
