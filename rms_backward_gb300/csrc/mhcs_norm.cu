@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(640) forward_rows_kernel(Params<E> a, int G, i
 // and 46% of the shared-memory pipe in use by 20 warps.  Taken because, for
 // T=4096 / 16384: rows in registers 30.7 / 113 us; two vectors and four rows
 // ahead 21.7 / 68.5; two rows at a time, for gamma's and beta's loads, 22.4 /
-// 65.8.  One row ahead less where that makes longer rows fit: collapsed above
+// 65.8.  The 16-bit types' unaligned shapes spill 36 to 40 bytes a thread.  One row
+// ahead less where that makes longer rows fit: collapsed above
 // 8,192 columns (not aligned 6,656), plain above 13,312 (12,288).
 template <typename E, bool MIX, bool WORDS, int VPT, int S>
 struct ForwardShape {
@@ -437,8 +438,8 @@ __global__ void __launch_bounds__((ForwardShape<E, MIX, WORDS, VPT, S>::kMaxThre
 
 // Rows too long for the kernel below (above 16,384 columns; collapsed 10,240, not
 // aligned 8,192), one per block, read twice; the parameter gradients read
-// everything once more.  T=2048, D=10240 collapsed takes 329 us
-// here, 153 below.
+// everything once more.  T=2048, D=10240 collapsed takes 326 us
+// here, 148 below.
 template <typename E, bool MIX, int N>
 __global__ void __launch_bounds__(kThreads) backward_rows_any_kernel(Params<E> a) {
     ptx::grid_dependency_wait();
@@ -546,21 +547,25 @@ __global__ void __launch_bounds__(kThreads) backward_columns_any_kernel(Params<E
 // gradients and refills each slot as it leaves it.  The other groups of the
 // block compute while one waits.
 //
-// T=16384, D=5120: 84.7 us (88%); collapsed 333 (97%, a copy of nine arrays to
-// four through the same slots takes 325).  T=4096: 28.3 (66%) and 92.6 (87%).
+// T=16384, D=5120: 87.3 us (85%); collapsed 334 (96%, a copy of nine arrays to
+// four through the same slots takes 325).  T=4096: 29.2 (64%) and 92.4 (87%).
 // Register spills cost more than anything else here (the collapsed gradient
 // fell from 480 us to 337 when the last 88 bytes went), so what a row needs is
 // formed when it is needed and the shapes are as wide as registers allow.
 // Collapsed, T=4096:
-//   1 vector, 2 rows ahead, 640 threads   D=5120:  92.7 us   (up to D=5120)
-//   2 vectors, 1 ahead, 512 threads       D=5120: 113.2      (up to D=8192: 174 us, 74%)
-//   2 vectors, 1 ahead, 640 threads       D=8192: 253        (up to D=10240; it spills)
+//   1 vector, 2 rows ahead, 640 threads   D=5120:  92.4 us   (up to D=5120)
+//   2 vectors, 1 ahead, 512 threads       D=5120: 114        (up to D=8192: 175 us, 73%)
+//   2 vectors, 1 ahead, 640 threads       D=8192: 237        (up to D=10240: T=2048 148 us, 54%)
 // Plain rows: two 16-bit vectors or four of FP32, 2 rows ahead (FP32 T=4096 /
-// 16384: 46.7 / 172 us; 1 ahead 49.7 / 161; 3 ahead slower), and up to D=16384
-// twice as many with 512 threads, 1 ahead (T=2048, D=16384: 57 us; the kernels
-// above 105).
-// Rows at any address take 2 to 3 times as long (T=4096, D=1285: 19.7 us,
-// collapsed 66): bound by the instructions that put vectors together.
+// 16384: 45.8 / 171 us; 1 ahead 48.5 / 158; 3 ahead slower), and up to D=16384
+// twice as many with 512 threads, 1 ahead (T=2048, D=16384: 58 us; the kernels
+// above 102).
+// The shapes for long rows still spill, bytes a thread stores / loads: two
+// vectors collapsed by 640 threads 112 / 236, by 512 unaligned 44 / 48; the
+// 16-bit types' four vectors 36 / 60 unaligned, BF16's 8 / 12 aligned; eight of
+// FP32 44 / 100 aligned.  They are kept because the kernels above take longer.
+// Rows at any address take 2 to 3 times as long (T=4096, D=1285: 19.4 us,
+// collapsed 66.9): bound by the instructions that put vectors together.
 template <typename E, bool MIX, bool WORDS, int VPT, int S, int MAX>
 struct RowsShape {
     static constexpr int N = Elem<E>::kPack;
@@ -1109,8 +1114,8 @@ bool backward_rows(const Params<E>& p, int64_t* parts, cudaError_t* e, cudaStrea
         return true;
     };
     // Six groups and more join their parameter gradients at once: T=16384, D=320
-    // (15 groups) 14.1 us instead of 16.6, T=4096, D=64 6.1 instead of 8.6; with two,
-    // T=1000, D=5120 FP32, 21.0 instead of 19.4.  (Collapsed rows would spill
+    // (15 groups) 13.7 us instead of 16.1, T=4096, D=64 6.1 instead of 8.4; with two,
+    // T=1000, D=5120 FP32, 19.9 instead of 18.8.  (Collapsed rows would spill
     // registers; the wide shape has one group.)
     if constexpr (!MIX && S == 2) {
         static std::atomic<uint64_t> many{0};

@@ -54,10 +54,13 @@ __global__ void __launch_bounds__(kThreads) dropout_any_kernel(int64_t n, Span<c
 
 // kDropPacks vectors of 16 bytes per thread, a block's width apart; needs
 // n < kShortCounters and aligned pointers.  The last, partial vector is one thread's.
-// T=16384, D=5120 BF16: 68.6 us (72%), T=4096 18.3: the generator's 18
-// multiplications of 32 by 32 bits for four elements alone take 61 of the 69
-// us.  FP32, with twice the bytes per counter, runs at HBM's rate (T=8192: 48.6
-// us).  A thread's vectors share the key schedule; 1, 2, 4, 8 vectors: 77.3,
+// T=16384, D=5120 BF16: 68.4 us (72%), T=4096 18.3 (68%).  FP32, with twice the bytes
+// per counter, runs at HBM's rate (T=8192: 48.6 us), so it is the generator's
+// arithmetic that the 16-bit types wait for, but no one unit is full: in a
+// capture at T=4096 the pipe that multiplies is busy 57% of the time, the other
+// integer pipe 49%, the issue slots 50%, DRAM 27%, with 24 warps on an SM (80
+// registers a thread).  The BF16 kernel spills 20 bytes a thread (28 loaded).
+// A thread's vectors share the key schedule; 1, 2, 4, 8 vectors: 77.3,
 // 70.9, 68.6, 83.4 us.
 constexpr int kDropPacks = 4;
 template <typename E>
@@ -335,8 +338,8 @@ __global__ void __launch_bounds__(kThreads) update_forward_vectors_kernel(
 // 276 us; pairs of columns would take 20 registers more).  Shapes, measured
 // before that, T=4096: 1 vector, 2 tokens ahead, 640 threads: D=5120 73.5 us,
 // T=16384 277; 2 vectors, 1 ahead, 512 threads: 77.6 and 294, D=8192 100.9 (now
-// 99.5, 100%); 2 vectors by 640 threads: D=8192 131 (spills), kept for up to
-// 10,240 columns.  Short odd rows stay here: T=65536, D=7 takes 134 us, element
+// 99.5, 100%); 2 vectors by 640 threads: D=8192 131 (it spills 20 bytes a
+// thread, 28 loaded), kept for up to 10,240 columns.  Two unaligned vectors spill 8 / 12.  Short odd rows stay here: T=65536, D=7 takes 134 us, element
 // by element 454.
 template <bool WORDS, int VPT, int S, int MAX>
 struct TokenShape {
