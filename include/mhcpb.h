@@ -532,6 +532,81 @@ mhcpb_status_t mhcpb_update_backward(int64_t T, int64_t D, const void* x, const 
  * norms, dropout and update}, read and cleared apart from that call's words. */
 mhcpb_status_t mhcpb_debug_checked_operator_sites(uint32_t* sites, int* checked);
 
+/* ---------------------------------------------------------------------------
+ * A sublayer, and the update of its weights: the gated feed-forward block with
+ * its gradient, and the orthogonalised update of a matrix.  The common rules
+ * above hold, with these of their own:
+ *  - every pointer is aligned to 16 bytes (MHCPB_ERR_MISALIGNED);
+ *  - a row stride is the row's width, or a larger multiple of 8 (else
+ *    MHCPB_ERR_UNSUPPORTED_SHAPE);
+ *  - matrix products take 16-bit operands with FP32 accumulators; what a product
+ *    reads that another call's line forms (a, dg, du; X, A, B) is rounded to 16 bits
+ *    between the two, everything else once, at the output;
+ *  - the waits inside the kernels are bounded (1 s): one that runs out leaves wrong
+ *    outputs and is reported by mhcpb_operators_device_status. */
+enum {                      /* activations */
+    MHCPB_SILU = 0,         /* act(g) = g / (1 + exp(-g)) */
+    MHCPB_GELU = 1          /* act(g) = g (1 + erf(g / sqrt 2)) / 2 */
+};
+
+/* The gated feed-forward block:
+ *     g = x Wg^T,  u = x Wu^T,  y = (act(g) u) Wd^T
+ * x, y: `type` (BF16 or FP16) [T, D] with row strides; w_gate, w_up: `type`
+ * [F, D]; w_down: `type` [D, F].  gate and up: `type` [T, F], receive g and u for
+ * the backward; both NULL where none follows.  1 <= D, F <= MHCPB_MAX_K.  D and
+ * F that are multiples of 8 run fastest (others are copied to padded rows in the
+ * workspace).  Any number of tokens; for one or a few, the time is the weights'
+ * way from memory. */
+mhcpb_status_t mhcpb_ffn_forward_workspace_bytes(int64_t T, int64_t D, int64_t F, size_t* bytes);
+mhcpb_status_t mhcpb_ffn_forward(int64_t T, int64_t D, int64_t F, int type, int activation,
+                                 const void* x, int64_t x_stride, const void* w_gate,
+                                 const void* w_up, const void* w_down, void* y, int64_t y_stride,
+                                 void* gate, void* up, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+/* Its gradient from the forward's inputs, gate and up, with da = grad_y Wd,
+ * dg = da u act'(g), du = da act(g), a = act(g) u:
+ *     grad_x = dg Wg + du Wu                                      `type` [T, D]
+ *     grad_w_gate = dg^T x,  grad_w_up = du^T x                   `grad_type` [F, D]
+ *     grad_w_down = grad_y^T a                                    `grad_type` [D, F]
+ * Each output may be NULL and is then not computed.  grad_type: `type`, or
+ * MHCPB_FP32 (a sum over micro-batches loses nothing there; dg, du and a are
+ * still rounded to `type`, so one call's share has that type's precision).
+ * flags: MHCPB_ACCUMULATE_DW adds to the weights' gradients;
+ * MHCPB_TEST_INJECT_STALL makes a wait run out. */
+mhcpb_status_t mhcpb_ffn_backward_workspace_bytes(int64_t T, int64_t D, int64_t F, size_t* bytes);
+mhcpb_status_t mhcpb_ffn_backward(int64_t T, int64_t D, int64_t F, int type, int activation,
+                                  const void* x, int64_t x_stride, const void* w_gate,
+                                  const void* w_up, const void* w_down, const void* gate,
+                                  const void* up, const void* grad_y, int64_t grad_y_stride,
+                                  void* grad_x, int64_t grad_x_stride, int grad_type,
+                                  void* grad_w_gate, void* grad_w_up, void* grad_w_down,
+                                  uint32_t flags, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* The orthogonalised update: X = G / (|G|_F + eps), then `steps` times
+ *     A = X X^T,  B = b A + c A^2,  X = a X + B X       (a, b, c) = (3.4445, -4.7750, 2.0315)
+ * (for m > n the same by columns), and out = scale X: each singular value of X
+ * goes through a s + b s^3 + c s^5, singular vectors stay.  g: `type` (BF16, FP16
+ * or FP32) [m, n], out: BF16 [m, n], both with row strides.  1 <= m, n <=
+ * MHCPB_MAX_K, 1 <= steps <= MHCPB_ORTH_MAX_STEPS, eps finite and >= 0 (a zero G
+ * with eps = 0 gives NaN, else 0), scale finite.  A non-finite element makes all
+ * of out NaN. */
+#define MHCPB_ORTH_MAX_STEPS 32
+mhcpb_status_t mhcpb_orthogonalize_workspace_bytes(int64_t m, int64_t n, size_t* bytes);
+mhcpb_status_t mhcpb_orthogonalize(int64_t m, int64_t n, int type, const void* g, int64_t g_stride,
+                                   int steps, float eps, float scale, void* out,
+                                   int64_t out_stride, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* MHCPB_OK, or MHCPB_ERR_DEVICE_TIMEOUT once a wait inside a kernel of the calls
+ * of this section has run out on the calling thread's current device; `clear` sets
+ * it back.  Waits for the device's work. */
+mhcpb_status_t mhcpb_operators_device_status(mhcpb_status_t* status, int clear);
+
+/* mhcpb_debug_checked_sites for the calls of this section: sites[2] =
+ * {feed-forward, orthogonalisation}. */
+mhcpb_status_t mhcpb_debug_checked_matrix_sites(uint32_t* sites, int* checked);
+
 /* Releases the plan (and its status word).  Safe on NULL. */
 mhcpb_status_t mhcpb_destroy(mhcpb_plan_t plan);
 

@@ -178,6 +178,8 @@ _OPERATORS = (
     "mhc_embed_forward", "mhc_embed_workspace_bytes", "mhc_embed_backward", "mhc_layernorm_forward",
     "mhc_layernorm_workspace_bytes", "mhc_layernorm_backward", "mhc_dropout", "mhc_collapse_norm_forward",
     "mhc_collapse_norm_workspace_bytes", "mhc_collapse_norm_backward", "mhc_update_forward", "mhc_update_backward",
+    "mhc_ffn_forward_workspace_bytes", "mhc_ffn_forward", "mhc_ffn_backward_workspace_bytes", "mhc_ffn_backward",
+    "mhc_orthogonalize_workspace_bytes", "mhc_orthogonalize", "mhc_operators_device_status",
 )
 
 

@@ -48,6 +48,10 @@ MHCPB_FP32 = 2
 MHCPB_MAX_VOCAB = 1 << 24
 MHCPB_MAX_STREAMS = 16
 
+MHCPB_SILU = 0
+MHCPB_GELU = 1
+MHCPB_ORTH_MAX_STEPS = 32
+
 QUERY = {"T": 0, "K": 1, "S": 2, "grid": 3, "flags": 4, "smem": 5, "token_tile": 6, "strip": 7,
          "partial_tokens": 8}
 
@@ -62,7 +66,10 @@ EXPORTED = ("mhcpb_plan_create", "mhcpb_workspace_bytes", "mhcpb_execute", "mhcp
             "mhcpb_layernorm_forward", "mhcpb_layernorm_workspace_bytes", "mhcpb_layernorm_backward",
             "mhcpb_dropout", "mhcpb_collapse_norm_forward", "mhcpb_collapse_norm_workspace_bytes",
             "mhcpb_collapse_norm_backward", "mhcpb_update_forward", "mhcpb_update_backward",
-            "mhcpb_debug_checked_operator_sites")
+            "mhcpb_debug_checked_operator_sites",
+            "mhcpb_ffn_forward_workspace_bytes", "mhcpb_ffn_forward", "mhcpb_ffn_backward_workspace_bytes",
+            "mhcpb_ffn_backward", "mhcpb_orthogonalize_workspace_bytes", "mhcpb_orthogonalize",
+            "mhcpb_operators_device_status", "mhcpb_debug_checked_matrix_sites")
 
 
 class MhcpbError(RuntimeError):
@@ -120,6 +127,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mhcpb_update_forward.argtypes = [I64, I64, P, P, P, F32, P, U64, P, P]
     lib.mhcpb_update_backward.argtypes = [I64, I64, P, P, P, F32, P, U64, P, P, P, P]
     lib.mhcpb_debug_checked_operator_sites.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(I32)]
+    lib.mhcpb_ffn_forward_workspace_bytes.argtypes = [I64, I64, I64, ctypes.POINTER(SZ)]
+    lib.mhcpb_ffn_forward.argtypes = [I64, I64, I64, I32, I32, P, I64, P, P, P, P, I64, P, P, P, SZ, P]
+    lib.mhcpb_ffn_backward_workspace_bytes.argtypes = [I64, I64, I64, ctypes.POINTER(SZ)]
+    lib.mhcpb_ffn_backward.argtypes = [I64, I64, I64, I32, I32, P, I64, P, P, P, P, P, P, I64, P, I64, I32, P, P, P, U32,
+                                       P, SZ, P]
+    lib.mhcpb_orthogonalize_workspace_bytes.argtypes = [I64, I64, ctypes.POINTER(SZ)]
+    lib.mhcpb_orthogonalize.argtypes = [I64, I64, I32, P, I64, I32, F32, F32, P, I64, P, SZ, P]
+    lib.mhcpb_operators_device_status.argtypes = [ctypes.POINTER(I32), I32]
+    lib.mhcpb_debug_checked_matrix_sites.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(I32)]
     lib.mhcpb_destroy.argtypes = [P]
     lib.mhcpb_status_string.argtypes = [I32]
     lib.mhcpb_status_string.restype = ctypes.c_char_p
@@ -135,7 +151,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                  "mhcpb_embed_backward", "mhcpb_layernorm_forward", "mhcpb_layernorm_workspace_bytes",
                  "mhcpb_layernorm_backward", "mhcpb_dropout", "mhcpb_collapse_norm_forward",
                  "mhcpb_collapse_norm_workspace_bytes", "mhcpb_collapse_norm_backward",
-                 "mhcpb_update_forward", "mhcpb_update_backward", "mhcpb_debug_checked_operator_sites"):
+                 "mhcpb_update_forward", "mhcpb_update_backward", "mhcpb_debug_checked_operator_sites",
+                 "mhcpb_ffn_forward_workspace_bytes", "mhcpb_ffn_forward", "mhcpb_ffn_backward_workspace_bytes",
+                 "mhcpb_ffn_backward", "mhcpb_orthogonalize_workspace_bytes", "mhcpb_orthogonalize",
+                 "mhcpb_operators_device_status", "mhcpb_debug_checked_matrix_sites"):
         getattr(lib, name).restype = I32
     _lib = lib
     return lib
@@ -373,3 +392,59 @@ def mhcpb_debug_checked_operator_sites():
     _check(load().mhcpb_debug_checked_operator_sites(sites, ctypes.byref(checked)),
            "mhcpb_debug_checked_operator_sites")
     return bool(checked.value), dict(zip(OPERATOR_FAMILIES, list(sites)))
+
+
+def mhcpb_ffn_forward_workspace_bytes(T: int, D: int, F: int) -> int:
+    return _size("mhcpb_ffn_forward_workspace_bytes", T, D, F)
+
+
+def mhcpb_ffn_forward(T: int, D: int, F: int, type_: int, activation: int, x: int, x_stride: int, w_gate: int,
+                      w_up: int, w_down: int, y: int, y_stride: int, gate: int | None, up: int | None, workspace: int,
+                      workspace_bytes: int, stream: int | None) -> None:
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T; gate and up receive the two projections."""
+    _check(load().mhcpb_ffn_forward(T, D, F, type_, activation, x, x_stride, w_gate, w_up, w_down, y, y_stride, gate,
+                                    up, workspace, workspace_bytes, stream or None), "mhcpb_ffn_forward")
+
+
+def mhcpb_ffn_backward_workspace_bytes(T: int, D: int, F: int) -> int:
+    return _size("mhcpb_ffn_backward_workspace_bytes", T, D, F)
+
+
+def mhcpb_ffn_backward(T: int, D: int, F: int, type_: int, activation: int, x: int, x_stride: int, w_gate: int,
+                       w_up: int, w_down: int, gate: int, up: int, grad_y: int, grad_y_stride: int,
+                       grad_x: int | None, grad_x_stride: int, grad_type: int, grad_w_gate: int | None,
+                       grad_w_up: int | None, grad_w_down: int | None, flags: int, workspace: int,
+                       workspace_bytes: int, stream: int | None) -> None:
+    _check(load().mhcpb_ffn_backward(T, D, F, type_, activation, x, x_stride, w_gate, w_up, w_down, gate, up, grad_y,
+                                     grad_y_stride, grad_x, grad_x_stride, grad_type, grad_w_gate, grad_w_up,
+                                     grad_w_down, flags, workspace, workspace_bytes, stream or None),
+           "mhcpb_ffn_backward")
+
+
+def mhcpb_orthogonalize_workspace_bytes(m: int, n: int) -> int:
+    return _size("mhcpb_orthogonalize_workspace_bytes", m, n)
+
+
+def mhcpb_orthogonalize(m: int, n: int, type_: int, g: int, g_stride: int, steps: int, eps: float, scale: float,
+                        out: int, out_stride: int, workspace: int, workspace_bytes: int, stream: int | None) -> None:
+    """out = scale * the orthogonalised g."""
+    _check(load().mhcpb_orthogonalize(m, n, type_, g, g_stride, steps, eps, scale, out, out_stride, workspace,
+                                      workspace_bytes, stream or None), "mhcpb_orthogonalize")
+
+
+def mhcpb_operators_device_status(clear: bool = False) -> int:
+    s = ctypes.c_int()
+    _check(load().mhcpb_operators_device_status(ctypes.byref(s), 1 if clear else 0), "mhcpb_operators_device_status")
+    return s.value
+
+
+MATRIX_FAMILIES = ("feed-forward", "orthogonalisation")
+
+
+def mhcpb_debug_checked_matrix_sites():
+    """(checked, sites) as :func:`mhcpb_debug_checked_sites`, for the
+    feed-forward block and the orthogonalised update."""
+    sites = (ctypes.c_uint32 * 2)()
+    checked = ctypes.c_int()
+    _check(load().mhcpb_debug_checked_matrix_sites(sites, ctypes.byref(checked)), "mhcpb_debug_checked_matrix_sites")
+    return bool(checked.value), dict(zip(MATRIX_FAMILIES, list(sites)))

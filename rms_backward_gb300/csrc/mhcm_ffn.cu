@@ -1,0 +1,280 @@
+// The gated feed-forward block and its gradient (sm_103a):
+//
+//   g = x Wg^T,  u = x Wu^T,  a = act(g) u,  y = a Wd^T
+//   da = dy Wd,  dg = da u act'(g),  du = da act(g)
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T a
+//
+// Each line is made of products (mhcm_product.cuh) whose epilogues do the rest:
+// the forward's first product forms g and u side by side and writes a (and g and
+// u where a backward follows); the backward's first forms da and writes dg, du
+// and a again from the stored g and u, so a is not kept between the two.  dx is
+// one sum over both halves.  a, dg and du are operands of further products and so
+// are rounded to the operands' 16-bit type; everything else is FP32 until the
+// output is stored.  Rows that are not a multiple of 8 elements long are copied
+// to rows that are (the tensor maps' 16-byte rule).
+#include "mhcm_product.cuh"
+
+namespace mhcpb {
+namespace ffn {
+
+namespace {
+
+using product::Matrix;
+using product::Shape;
+
+// act(g) and act'(g)
+__device__ __forceinline__ float2 activate(float g, int kind) {
+    if (kind == MHCPB_SILU) {
+        const float q = __fdividef(1.f, 1.f + __expf(-g));
+        return make_float2(g * q, q * (1.f + g * (1.f - q)));
+    }
+    const float p = 0.5f * erfcf(g * -0.70710678f);   // the normal distribution function, accurate in its tail
+    return make_float2(g * p, p + g * (0.39894228f * __expf(-0.5f * g * g)));
+}
+
+template <class T>
+struct GatedEpilogue : product::Nothing {
+    static constexpr bool kDual = true;
+    Matrix<T> hidden, gate, up;
+    int activation;
+    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&g)[8],
+                                               const float (&u)[8], float) const {
+        float a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = activate(g[i], activation).x * u[i];
+        hidden.store(row, col, count, a, 0);
+        if (gate.ptr != nullptr) {
+            gate.store(row, col, count, g, 1);
+            up.store(row, col, count, u, 2);
+        }
+    }
+};
+
+template <class T>
+struct GradEpilogue : product::Nothing {
+    static constexpr bool kDual = false;
+    Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
+    int activation;
+    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&da)[8],
+                                               const float (&)[8], float) const {
+        float g[8], u[8], a[8];
+        gate.load(row, col, count, g, 3);
+        up.load(row, col, count, u, 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = activate(g[i], activation);
+            a[i] = f.x * u[i];
+            g[i] = da[i] * u[i] * f.y;
+            u[i] = da[i] * f.x;
+        }
+        grad_gate.store(row, col, count, g, 5);
+        grad_up.store(row, col, count, u, 6);
+        hidden.store(row, col, count, a, 7);
+    }
+};
+
+template <class O>
+struct StoreEpilogue : product::Nothing {
+    static constexpr bool kDual = false;
+    Matrix<O> out[2];
+    bool accumulate;
+    __device__ __forceinline__ void operator()(int group, int64_t row, int64_t col, int count, const float (&v)[8],
+                                               const float (&)[8], float) const {
+        const Matrix<O>& o = out[group];
+        if (!accumulate) return o.store(row, col, count, v, 8);
+        float old[8];
+        o.load(row, col, count, old, 9);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) old[i] += v[i];
+        o.store(row, col, count, old, 8);
+    }
+};
+
+// dst[r, 0..cols) = src[r, 0..cols), rows dst_ld (a multiple of 8) apart
+__global__ void __launch_bounds__(256) copy_rows_kernel(const uint16_t* src, int64_t src_ld, int64_t rows, int64_t cols,
+                                                        uint16_t* dst, int64_t dst_ld) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t across = dst_ld / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * across; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / across, c = (i - r * across) * 8;
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint16_t* p = src + r * src_ld + c + k;
+            if (c + k < cols && check::in(p, 2, src, (size_t)((rows - 1) * src_ld + cols) * 2, 10))
+                w[k / 2] |= (uint32_t)*p << (16 * (k & 1));
+        }
+        uint4* q = reinterpret_cast<uint4*>(dst + r * dst_ld + c);
+        if (check::in(q, 16, dst, (size_t)(rows * dst_ld) * 2, 11)) *q = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Parts of a workspace, each at a multiple of 256 bytes.
+struct Parts {
+    char* base;
+    size_t used = 0;
+    void* take(size_t bytes) {
+        void* p = base + used;
+        used += (bytes + 255) / 256 * 256;
+        return p;
+    }
+};
+
+size_t part(int64_t rows, int64_t cols) { return ((size_t)(rows * product::padded(cols)) * 2 + 255) / 256 * 256; }
+
+int steps_of(int64_t k) { return (int)((k + 63) / 64); }
+
+// A 16-bit operand [rows, cols] with rows that tensor maps can read: itself, or its copy in the workspace.
+struct Operand16 {
+    CUtensorMap map;
+    cudaError_t make(bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+        return encode_16bit_map(&map, bf16, p, rows, cols, ld) ? cudaSuccess : cudaErrorInvalidValue;
+    }
+    cudaError_t make(bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, Parts& ws, cudaStream_t stream) {
+        const int64_t wide = product::padded(cols);
+        if (wide == cols) return make(bf16, p, rows, cols, ld);
+        uint16_t* copy = static_cast<uint16_t*>(ws.take((size_t)(rows * wide) * 2));
+        const int64_t vectors = rows * (wide / 8);
+        const int64_t blocks = (vectors + 255) / 256;
+        const cudaError_t e = ops::launch_early(copy_rows_kernel, dim3((unsigned)(blocks < 2432 ? blocks : 2432)), dim3(256),
+                                                0, stream, static_cast<const uint16_t*>(p), ld, rows, cols, copy, wide);
+        return e != cudaSuccess ? e : make(bf16, copy, rows, cols, wide);
+    }
+};
+
+template <class T>
+Matrix<T> matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+    return {static_cast<T*>(const_cast<void*>(p)), ld, p == nullptr ? 0 : (size_t)((rows - 1) * ld + cols)};
+}
+
+#define MHCM_TRY(call)                          \
+    do {                                        \
+        const cudaError_t e_ = (call);          \
+        if (e_ != cudaSuccess) return e_;       \
+    } while (0)
+
+template <class T>
+cudaError_t forward_as(const Args& a, cudaStream_t stream) {
+    const int64_t T_ = a.T, D = a.D, F = a.F, Fp = product::padded(F);
+    const bool bf16 = a.type == MHCPB_BF16;
+    Parts ws{static_cast<char*>(a.workspace)};
+    void* hidden = ws.take((size_t)(T_ * Fp) * 2);
+    Operand16 x, wg, wu, wd, h;
+    MHCM_TRY(x.make(bf16, a.x, T_, D, a.x_stride, ws, stream));
+    MHCM_TRY(wg.make(bf16, a.w_gate, F, D, D, ws, stream));
+    MHCM_TRY(wu.make(bf16, a.w_up, F, D, D, ws, stream));
+    MHCM_TRY(wd.make(bf16, a.w_down, D, F, F, ws, stream));
+    MHCM_TRY(h.make(bf16, hidden, T_, F, Fp));
+    Shape s{};
+    s.bf16 = bf16;
+    s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
+    const GatedEpilogue<T> gated{{}, matrix<T>(hidden, T_, F, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
+                                 a.activation};
+    MHCM_TRY(product::launch(s, gated, &x.map, nullptr, &wg.map, &wu.map, stream));
+    s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain;
+    const StoreEpilogue<T> store{{}, {matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
+    return product::launch(s, store, &h.map, nullptr, &wd.map, nullptr, stream);
+}
+
+// dWd, or dWg and dWu together or one of them: C = A^T B over the tokens
+template <class O>
+cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const CUtensorMap* a0, const CUtensorMap* a1,
+                            const CUtensorMap* b, void* out0, void* out1, cudaStream_t stream) {
+    Shape s{};
+    s.bf16 = a.type == MHCPB_BF16;
+    s.M = M, s.N = N, s.k_steps = steps_of(a.T), s.mode = mode;
+    s.a_mn = s.b_mn = 1;
+    const StoreEpilogue<O> store{{}, {matrix<O>(out0, M, N, N), matrix<O>(out1, M, N, N)}, a.accumulate};
+    return product::launch(s, store, a0, a1, b, b, stream);
+}
+
+template <class T, class O>
+cudaError_t backward_as(const Args& a, cudaStream_t stream) {
+    const int64_t T_ = a.T, D = a.D, F = a.F, Fp = product::padded(F);
+    const bool bf16 = a.type == MHCPB_BF16;
+    Parts ws{static_cast<char*>(a.workspace)};
+    const size_t tf = (size_t)(T_ * Fp) * 2;
+    void *hidden = ws.take(tf), *grad_gate = ws.take(tf), *grad_up = ws.take(tf);
+    Operand16 x, dy, wg, wu, wd, h, dg, du;
+    MHCM_TRY(dy.make(bf16, a.grad_y, T_, D, a.gy_stride, ws, stream));
+    MHCM_TRY(wd.make(bf16, a.w_down, D, F, F, ws, stream));
+    if (a.grad_w[0] || a.grad_w[1]) MHCM_TRY(x.make(bf16, a.x, T_, D, a.x_stride, ws, stream));
+    if (a.grad_x) {
+        MHCM_TRY(wg.make(bf16, a.w_gate, F, D, D, ws, stream));
+        MHCM_TRY(wu.make(bf16, a.w_up, F, D, D, ws, stream));
+    }
+    MHCM_TRY(h.make(bf16, hidden, T_, F, Fp));
+    MHCM_TRY(dg.make(bf16, grad_gate, T_, F, Fp));
+    MHCM_TRY(du.make(bf16, grad_up, T_, F, Fp));
+
+    Shape s{};
+    s.bf16 = bf16;
+    s.stall = a.stall;
+    s.M = T_, s.N = F, s.k_steps = steps_of(D), s.b_mn = 1;
+    const GradEpilogue<T> grad{{}, matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, F, Fp),
+                               matrix<T>(grad_up, T_, F, Fp), matrix<T>(hidden, T_, F, Fp), a.activation};
+    MHCM_TRY(product::launch(s, grad, &dy.map, nullptr, &wd.map, nullptr, stream));
+    s.stall = 0;
+    if (a.grad_x) {
+        s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
+        const StoreEpilogue<T> store{{}, {matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
+        MHCM_TRY(product::launch(s, store, &dg.map, &du.map, &wg.map, &wu.map, stream));
+    }
+    if (a.grad_w[0] && a.grad_w[1])
+        MHCM_TRY(weight_gradient<O>(a, product::kGroups, F, D, &dg.map, &du.map, &x.map, a.grad_w[0], a.grad_w[1], stream));
+    else if (a.grad_w[0] || a.grad_w[1])
+        MHCM_TRY(weight_gradient<O>(a, product::kPlain, F, D, a.grad_w[0] ? &dg.map : &du.map, nullptr, &x.map,
+                                    a.grad_w[0] ? a.grad_w[0] : a.grad_w[1], nullptr, stream));
+    if (a.grad_w[2])
+        MHCM_TRY(weight_gradient<O>(a, product::kPlain, D, F, &dy.map, nullptr, &h.map, a.grad_w[2], nullptr, stream));
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t forward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
+    size_t n = part(T, F);
+    if (D % 8) n += part(T, D) + 2 * part(F, D);
+    if (F % 8) n += part(D, F);
+    return n;
+}
+
+size_t backward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
+    size_t n = 3 * part(T, F);
+    if (D % 8) n += 2 * part(T, D) + 2 * part(F, D);
+    if (F % 8) n += part(D, F);
+    return n;
+}
+
+cudaError_t forward(const Args& a, cudaStream_t stream) {
+    return a.type == MHCPB_BF16 ? forward_as<__nv_bfloat16>(a, stream) : forward_as<__half>(a, stream);
+}
+
+cudaError_t backward(const Args& a, cudaStream_t stream) {
+    if (a.T == 0) {   // sums over no tokens
+        const size_t bytes = (size_t)(a.D * a.F) * (a.grad_type == MHCPB_FP32 ? 4 : 2);
+        for (void* w : a.grad_w)
+            if (w != nullptr && !a.accumulate) MHCM_TRY(cudaMemsetAsync(w, 0, bytes, stream));
+        return cudaSuccess;
+    }
+    if (a.type == MHCPB_BF16)
+        return a.grad_type == MHCPB_FP32 ? backward_as<__nv_bfloat16, float>(a, stream)
+                                         : backward_as<__nv_bfloat16, __nv_bfloat16>(a, stream);
+    return a.grad_type == MHCPB_FP32 ? backward_as<__half, float>(a, stream) : backward_as<__half, __half>(a, stream);
+}
+
+cudaError_t setup() {
+    MHCM_TRY(product::allow<GatedEpilogue<__nv_bfloat16>>());
+    MHCM_TRY(product::allow<GatedEpilogue<__half>>());
+    MHCM_TRY(product::allow<GradEpilogue<__nv_bfloat16>>());
+    MHCM_TRY(product::allow<GradEpilogue<__half>>());
+    MHCM_TRY(product::allow<StoreEpilogue<__nv_bfloat16>>());
+    MHCM_TRY(product::allow<StoreEpilogue<__half>>());
+    return product::allow<StoreEpilogue<float>>();
+}
+cudaError_t checked_site(uint32_t* site) { return check::read_and_clear(site); }
+cudaError_t device_status(uint32_t* status, bool clear) { return product::read_status(status, clear); }
+
+}  // namespace ffn
+}  // namespace mhcpb

@@ -1,0 +1,89 @@
+// Internal interface of the matrix operators: the product (mhcm_product.cuh),
+// the feed-forward block (mhcm_ffn.cu), the orthogonalised update (mhcm_orth.cu)
+// and their host checks (mhcm_api.cu).
+#pragma once
+#include "mhcs_internal.h"
+
+namespace mhcpb {
+
+// Tensor map over a 16-bit matrix [rows, cols], rows `ld` elements apart (a
+// multiple of 8; base 16-byte aligned): boxes of 64 x 64, 128-byte swizzle
+// (defined in mhcpb_api.cu).
+bool encode_16bit_map(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld);
+
+namespace product {
+
+enum Mode {
+    kPlain = 0,
+    kSideBySide = 1,   // two products of one A, with B of b0 and of b1 (C has N columns of each)
+    kLongK = 2,        // the sum of two products, a0 b0 + a1 b1
+    kGroups = 3,       // two products, a0 b0 and a1 b1
+    kSymmetric = 4     // C is symmetric: tiles on and above the diagonal, written twice
+};
+struct Shape {
+    int64_t M, N;
+    int k_steps;       // of 64, per product
+    int mode;
+    int a_mn, b_mn;    // the operand's rows are k (else its rows are m, or n)
+    int bf16;          // else FP16
+    int stall;         // a test's: the MMA issuer waits for what nothing signals
+    // set by launch()
+    int m_tiles, n_tiles, tiles, split;
+};
+struct Choice {
+    bool pair;
+    int m_tiles, n_tiles, tiles, split, grid;
+};
+Choice choose(const Shape& s);
+
+inline int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+
+}  // namespace product
+
+namespace ffn {
+struct Args {
+    int64_t T, D, F;
+    int type, activation;
+    const void *x, *w_gate, *w_up, *w_down;
+    int64_t x_stride;
+    void* y;
+    int64_t y_stride;
+    void *gate, *up;              // [T, F]; the forward's may be null
+    const void* grad_y;
+    int64_t gy_stride;
+    void* grad_x;                 // may be null
+    int64_t gx_stride;
+    void* grad_w[3];              // gate, up, down; each may be null
+    int grad_type;
+    bool accumulate, stall;
+    void* workspace;
+};
+size_t forward_workspace_bytes(int64_t T, int64_t D, int64_t F);
+size_t backward_workspace_bytes(int64_t T, int64_t D, int64_t F);
+cudaError_t forward(const Args& a, cudaStream_t stream);
+cudaError_t backward(const Args& a, cudaStream_t stream);
+cudaError_t setup();
+cudaError_t checked_site(uint32_t* site);
+cudaError_t device_status(uint32_t* status, bool clear);
+}  // namespace ffn
+
+namespace orth {
+struct Args {
+    int64_t m, n;
+    int type;
+    const void* g;
+    int64_t g_stride;
+    void* out;                    // BF16
+    int64_t out_stride;
+    int steps;
+    float eps;
+    float scale;
+    void* workspace;
+};
+size_t workspace_bytes(int64_t m, int64_t n);
+cudaError_t orthogonalize(const Args& a, cudaStream_t stream);
+cudaError_t setup();
+cudaError_t checked_site(uint32_t* site);
+cudaError_t device_status(uint32_t* status, bool clear);
+}  // namespace orth
+}  // namespace mhcpb

@@ -1,0 +1,302 @@
+// The orthogonalised update (sm_103a): with X = G / (|G|_F + eps), `steps` times
+//
+//   A = X X^T (or X^T X, by the shorter side),  B = b A + c A^2,  X = a X + B X (or X B)
+//
+// (a, b, c) = (3.4445, -4.7750, 2.0315): every singular value s of X goes to
+// a s + b s^3 + c s^5, which takes (0, 1] to about [0.7, 1.2] in five steps
+// (Jordan et al., "Muon", 2024).  Singular vectors stay as they are.
+//
+// Rounding.  Products take FP16 operands: X, A and B are bounded whatever G is
+// (|X| <= 1.21 in the 2-norm after any step, so |A| <= 1.46 and |B| <= 2.81), so
+// powers of two put them at the top of FP16's range and 11 bits of each are kept
+// down to 2^-29 of the bound.  The rounding of X must not pass from step to step,
+// since a direction that G hardly has grows by a factor of a in each: X itself is
+// kept in FP32, a X is formed from that, and only B X sees the FP16 copy (B's range
+// is the space of X, so noise outside that space does not enter).
+// A and A^2 are symmetric: tiles on and above the diagonal, written twice.
+#include "mhcm_product.cuh"
+
+namespace mhcpb {
+namespace orth {
+
+namespace {
+
+using product::Matrix;
+using product::Shape;
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScaleX = 32768.f, kScaleA = 32768.f, kScaleB = 16384.f;   // 1.21, 1.46 and 2.81 times these < 65504
+
+// 1 / (|G|_F + eps) as a product that neither overflows nor loses bits: three factors.
+struct Inverse {
+    float p, q, r;
+};
+__device__ __forceinline__ float scaled(float g, const Inverse& f) { return g * f.p * f.q * f.r; }
+
+// G's elements by its type
+struct Input {
+    const void* ptr;
+    int type;
+    int64_t rows, ld, cols;
+    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
+        const size_t n = (size_t)((rows - 1) * ld + cols);
+        if (type == MHCPB_FP32)
+            Matrix<const float>{static_cast<const float*>(ptr), ld, n}.load(row, col, count, v, site);
+        else if (type == MHCPB_BF16)
+            Matrix<const __nv_bfloat16>{static_cast<const __nv_bfloat16*>(ptr), ld, n}.load(row, col, count, v, site);
+        else
+            Matrix<const __half>{static_cast<const __half*>(ptr), ld, n}.load(row, col, count, v, site);
+    }
+};
+
+constexpr int kNormBlocks = 608, kNormThreads = 256;
+
+// Sums of squares of the small, middling and large elements apart, the outer two
+// scaled, so that none overflows or vanishes (Blue, ACM TOMS 4, 1978).
+struct Squares {
+    float low = 0.f, mid = 0.f, high = 0.f;
+    __device__ __forceinline__ void add(float v) {
+        const float m = fabsf(v);
+        if (m > 0x1p50f) {
+            const float t = v * 0x1p-80f;
+            high = fmaf(t, t, high);
+        } else if (m < 0x1p-50f) {
+            const float t = v * 0x1p80f;
+            low = fmaf(t, t, low);
+        } else {
+            mid = fmaf(v, v, mid);   // NaN too
+        }
+    }
+    __device__ __forceinline__ double sum() const { return (double)mid + (double)high * 0x1p160 + (double)low * 0x1p-160; }
+};
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double warps[kNormThreads / 32];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < kNormThreads / 32; ++i) v += warps[i];
+    return v;
+}
+
+__global__ void __launch_bounds__(kNormThreads) squares_kernel(const Input g, double* partial) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t across = (g.cols + 7) / 8, units = g.rows * across;
+    Squares s;
+    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < units; i += (int64_t)kNormBlocks * kNormThreads) {
+        const int64_t r = i / across, c = (i - r * across) * 8;
+        float v[8];
+        g.load(r, c, (int)min((int64_t)8, g.cols - c), v, 0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s.add(v[k]);
+    }
+    const double total = block_sum(s.sum());
+    if (threadIdx.x == 0 && check::in(partial + blockIdx.x, 8, partial, kNormBlocks * 8, 1)) partial[blockIdx.x] = total;
+}
+
+// FP16 copy of G / (|G| + eps), and the factors for later.
+__global__ void __launch_bounds__(kNormThreads)
+    first_copy_kernel(const Input g, const double* partial, double eps, Inverse* inverse, Matrix<__half> x) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    double total = 0.0;
+    for (int i = threadIdx.x; i < kNormBlocks; i += kNormThreads) total += partial[i];
+    total = sqrt(block_sum(total)) + eps;
+    int e;
+    const double f = frexp(total, &e);   // total = f 2^e, f in [1/2, 1)
+    e = min(max(e, -240), 240);
+    Inverse inv;
+    inv.r = (float)(1.0 / f);
+    inv.p = exp2f((float)(-e / 2));
+    inv.q = exp2f((float)(-(e - e / 2)));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *inverse = inv;
+    const int64_t across = (g.cols + 7) / 8, units = g.rows * across;
+    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < units; i += (int64_t)gridDim.x * kNormThreads) {
+        const int64_t r = i / across, c = (i - r * across) * 8;
+        const int count = (int)min((int64_t)8, g.cols - c);
+        float v[8];
+        g.load(r, c, count, v, 2);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = scaled(v[k], inv) * kScaleX;
+        x.store(r, c, count, v, 3);
+    }
+}
+
+// A (add: none): out = fp16(alpha C).  B: out = fp16(alpha C + beta add - d kScaleB I), and *shift = d.
+struct SymmetricEpilogue {
+    static constexpr bool kDual = false;
+    Matrix<__half> out;
+    Matrix<const __half> add;
+    float alpha, beta;
+    float* shift;
+    int64_t size;
+    __device__ __forceinline__ float prepare(int lane) const {
+        if (add.ptr == nullptr) return 0.f;
+        float t = 0.f;
+        for (int64_t i = lane; i < size; i += 32) {
+            const __half* p = add.ptr + i * add.ld + i;
+            if (add.ok(p, 1, 11)) t += __half2float(*p);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+        t /= (float)size * kScaleA;
+        const float d = (kB + kC * t) * t;
+        if (blockIdx.x == 0 && lane == 0) *shift = d;   // (the same value from every warp)
+        return d;
+    }
+    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&v)[8],
+                                               const float (&)[8], float extra) const {
+        float r[8];
+        if (add.ptr != nullptr) {
+            add.load(row, col, count, r, 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                r[i] = fmaf(alpha, v[i], beta * r[i]);
+                if (row == col + i) r[i] -= extra * kScaleB;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = alpha * v[i];
+        }
+        out.store(row, col, count, r, 5);
+    }
+};
+
+// X = (a + d) X + alpha C
+struct UpdateEpilogue : product::Nothing {
+    static constexpr bool kDual = false;
+    Input g;                    // the first step's X, times *inverse
+    const Inverse* inverse;     // null after the first step
+    const float* shift;         // d
+    Matrix<float> x;            // X between the steps
+    Matrix<__half> copy;        // its FP16 copy
+    Matrix<__nv_bfloat16> out;  // the last step's X, times scale; null before
+    float alpha, scale;
+    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&v)[8],
+                                               const float (&)[8], float) const {
+        float r[8];
+        const float a = kA + *shift;
+        if (inverse != nullptr) {
+            const Inverse inv = *inverse;
+            g.load(row, col, count, r, 6);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = scaled(r[i], inv);
+        } else {
+            x.load(row, col, count, r, 7);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = fmaf(a, r[i], alpha * v[i]);
+        if (out.ptr != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] *= scale;
+            out.store(row, col, count, r, 8);
+            return;
+        }
+        x.store(row, col, count, r, 9);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] *= kScaleX;
+        copy.store(row, col, count, r, 10);
+    }
+};
+
+size_t up(size_t bytes) { return (bytes + 255) / 256 * 256; }
+int steps_of(int64_t k) { return (int)((k + 63) / 64); }
+
+struct Layout {
+    size_t partial, inverse, shift, x, copy[2], gram, poly, bytes;
+};
+Layout layout(int64_t m, int64_t n) {
+    const int64_t s = m < n ? m : n, np = product::padded(n), sp = product::padded(s);
+    Layout l{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at += up(bytes);
+        return p;
+    };
+    l.partial = take(kNormBlocks * sizeof(double));
+    l.inverse = take(sizeof(Inverse));
+    l.shift = take(sizeof(float));
+    l.x = take((size_t)(m * np) * 4);
+    l.copy[0] = take((size_t)(m * np) * 2);
+    l.copy[1] = take((size_t)(m * np) * 2);
+    l.gram = take((size_t)(s * sp) * 2);
+    l.poly = take((size_t)(s * sp) * 2);
+    l.bytes = at;
+    return l;
+}
+
+#define MHCM_TRY(call)                          \
+    do {                                        \
+        const cudaError_t e_ = (call);          \
+        if (e_ != cudaSuccess) return e_;       \
+    } while (0)
+
+}  // namespace
+
+size_t workspace_bytes(int64_t m, int64_t n) { return layout(m, n).bytes; }
+
+cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
+    const int64_t m = a.m, n = a.n, s = m < n ? m : n, np = product::padded(n), sp = product::padded(s);
+    const bool tall = m > n;
+    const Layout l = layout(m, n);
+    char* ws = static_cast<char*>(a.workspace);
+    double* partial = reinterpret_cast<double*>(ws + l.partial);
+    Inverse* inverse = reinterpret_cast<Inverse*>(ws + l.inverse);
+    float* shift = reinterpret_cast<float*>(ws + l.shift);
+    const Input g{a.g, a.type, m, a.g_stride, n};
+    auto half_matrix = [&](size_t at, int64_t rows, int64_t cols, int64_t ld) {
+        return Matrix<__half>{reinterpret_cast<__half*>(ws + at), ld, (size_t)((rows - 1) * ld + cols)};
+    };
+    const Matrix<__half> copies[2] = {half_matrix(l.copy[0], m, n, np), half_matrix(l.copy[1], m, n, np)};
+    const Matrix<__half> gram = half_matrix(l.gram, s, s, sp), poly = half_matrix(l.poly, s, s, sp);
+    const Matrix<const __half> gram_in{gram.ptr, gram.ld, gram.elements};
+    const Matrix<float> x{reinterpret_cast<float*>(ws + l.x), np, (size_t)((m - 1) * np + n)};
+    const Matrix<__nv_bfloat16> out{static_cast<__nv_bfloat16*>(a.out), a.out_stride, (size_t)((m - 1) * a.out_stride + n)};
+    CUtensorMap map_x[2], map_gram, map_poly;
+    if (!encode_16bit_map(&map_x[0], false, copies[0].ptr, m, n, np) ||
+        !encode_16bit_map(&map_x[1], false, copies[1].ptr, m, n, np) ||
+        !encode_16bit_map(&map_gram, false, gram.ptr, s, s, sp) || !encode_16bit_map(&map_poly, false, poly.ptr, s, s, sp))
+        return cudaErrorInvalidValue;
+
+    const int64_t units = m * ((n + 7) / 8), blocks = (units + kNormThreads - 1) / kNormThreads;
+    MHCM_TRY(ops::launch_early(squares_kernel, dim3(kNormBlocks), dim3(kNormThreads), 0, stream, g, partial));
+    MHCM_TRY(ops::launch_early(first_copy_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(kNormThreads), 0,
+                               stream, g, static_cast<const double*>(partial), static_cast<double>(a.eps), inverse, copies[0]));
+    for (int i = 0; i < a.steps; ++i) {
+        const CUtensorMap* cur = &map_x[i & 1];
+        Shape p{};
+        p.mode = product::kSymmetric;
+        p.M = p.N = s, p.k_steps = steps_of(tall ? m : n), p.a_mn = p.b_mn = tall;
+        const SymmetricEpilogue first{gram, {nullptr, 0, 0}, kScaleA / (kScaleX * kScaleX), 0.f, nullptr, 0};
+        MHCM_TRY(product::launch(p, first, cur, nullptr, cur, nullptr, stream));
+        p.k_steps = steps_of(s), p.a_mn = p.b_mn = 0;
+        const SymmetricEpilogue second{poly, gram_in, kC * kScaleB / (kScaleA * kScaleA), kB * kScaleB / kScaleA,
+                                       shift, s};
+        MHCM_TRY(product::launch(p, second, &map_gram, nullptr, &map_gram, nullptr, stream));
+        p.mode = product::kPlain;
+        p.M = m, p.N = n, p.k_steps = steps_of(s), p.b_mn = !tall;
+        const bool last = i + 1 == a.steps;
+        const UpdateEpilogue update{{}, g, i == 0 ? inverse : nullptr, shift, x, copies[(i + 1) & 1],
+                                    last ? out : Matrix<__nv_bfloat16>{nullptr, 0, 0}, 1.f / (kScaleB * kScaleX), a.scale};
+        if (tall)
+            MHCM_TRY(product::launch(p, update, cur, nullptr, &map_poly, nullptr, stream));
+        else
+            MHCM_TRY(product::launch(p, update, &map_poly, nullptr, cur, nullptr, stream));
+    }
+    return cudaSuccess;
+}
+
+cudaError_t setup() {
+    MHCM_TRY(product::allow<SymmetricEpilogue>());
+    return product::allow<UpdateEpilogue>();
+}
+cudaError_t checked_site(uint32_t* site) { return check::read_and_clear(site); }
+cudaError_t device_status(uint32_t* status, bool clear) { return product::read_status(status, clear); }
+
+}  // namespace orth
+}  // namespace mhcpb

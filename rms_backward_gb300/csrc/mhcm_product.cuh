@@ -1,0 +1,527 @@
+// The matrix product that the feed-forward block and the orthogonalised update
+// are made of (sm_103a): C = sum_k A[m, k] B[n, k] on the tensor cores, 16-bit
+// operands, FP32 accumulators, and an epilogue that takes eight neighbouring
+// elements of C at a time.
+//
+// Either operand may be stored with k or with its other index innermost: one
+// tensor map per matrix, boxes of 64 x 64 elements (8 KiB, 128-byte swizzle),
+// serves both, as the MMA's descriptors say which it is.  What lies outside a
+// matrix is read as zero, so no size has to be a multiple of anything; only the
+// distance between rows is a multiple of 16 bytes (the tensor map's rule).
+//
+// Two shapes of one kernel:
+//  * PAIR: pairs of blocks (cta_group::2), 256 x 256 tiles, one block per SM,
+//    persistent.  Each block holds half of A's and of B's rows: 32 KiB of
+//    operands per 64 k and block, 64 bytes per clock and SM at the full MMA rate.
+//    Two accumulators in TMEM (all 512 columns), so the epilogue of one tile runs
+//    under the products of the next.
+//  * single blocks, 128 x 128 tiles, a cluster of `split` blocks that share the
+//    sum over k of one tile and add their parts, in rank order, through
+//    distributed shared memory: for outputs of few tiles (few tokens, few rows).
+//
+// Warp roles: 0 copies (TMA), 1 MMA issue, 2 TMEM, 4..11 epilogue.  Every wait is
+// bounded; a wait that runs out records a status word, and the block drains its
+// copies and MMAs and leaves.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "mhcm_internal.h"
+#include "mhcm_ptx.cuh"
+#include "mhcpb.h"
+#include "mhcpb_check.cuh"
+
+namespace mhcpb {
+namespace product {
+
+static __device__ uint32_t g_status;   // kDevOk or kDevTimeout, of this translation unit's kernels
+
+constexpr int kBox = 64;                           // box side
+constexpr uint32_t kBoxBytes = kBox * kBox * 2;    // 8 KiB
+constexpr uint32_t kStageBytes = 4 * kBoxBytes;    // 128 rows of A, 128 of B, 64 k
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarp = 4;                   // the first of eight
+constexpr uint64_t kWaitNs = 1000000000ull;        // 1 s
+
+template <bool PAIR>
+struct Cfg {
+    static constexpr int blocks = PAIR ? 2 : 1;
+    static constexpr int tile_m = 128 * blocks, tile_n = 128 * blocks;
+    static constexpr int stages = PAIR ? 5 : 6;
+    static constexpr int accumulators = PAIR ? 2 : 1;
+    static constexpr uint32_t tmem_columns = tile_n * accumulators;
+    // PAIR: 32 rows of 32 FP32 per epilogue warp, 36 apart (vectors without bank conflicts).
+    // Single blocks: the whole accumulator, rows 132 apart, over the (then idle) stages.
+    static constexpr int row = PAIR ? 36 : 132;
+    static constexpr uint32_t scratch = PAIR ? 8 * 32 * row * 4 : 0;
+    static constexpr uint32_t off_scratch = PAIR ? stages * kStageBytes : 0;
+    static constexpr uint32_t off_bar = stages * kStageBytes + scratch;
+    // barriers: full[stages] empty[stages] done[2] free[2] last
+    static constexpr int b_full = 0, b_empty = stages, b_done = 2 * stages, b_free = 2 * stages + 2,
+                         b_last = 2 * stages + 4, bars = 2 * stages + 5;
+    static constexpr uint32_t off_misc = off_bar + bars * 8;
+    static constexpr uint32_t smem = off_misc + 16 + 1024;   // and room to align the base to 1 KiB
+    static_assert(smem <= 232448, "shared memory budget");
+    static_assert(PAIR || 128 * row * 4 <= stages * kStageBytes, "the accumulator fits the stages");
+};
+
+// Which rows and columns of C a tile has.
+struct Tile {
+    int group, m, n;   // first row and column; of each of the two products where two are formed side by side
+    bool mirror;       // symmetric C: the tile is also written transposed
+};
+template <int TILE_M, int TILE_N>
+__device__ __forceinline__ Tile tile_at(const Shape& s, int t) {
+    Tile r;
+    r.group = 0;
+    r.mirror = false;
+    if (s.mode == kSymmetric) {            // tiles on and above the diagonal, row by row
+        int i = 0, left = s.n_tiles;
+        while (t >= left) {
+            t -= left;
+            --left;
+            ++i;
+        }
+        r.m = i * TILE_M;
+        r.n = (i + t) * TILE_N;
+        r.mirror = t > 0;
+        return r;
+    }
+    const int per_group = s.m_tiles * s.n_tiles;
+    if (s.mode == kGroups && t >= per_group) {
+        t -= per_group;
+        r.group = 1;
+    }
+    // eight rows of tiles at a time, so that the tiles in flight share rows of both operands
+    const int band = t / (8 * s.n_tiles), first = band * 8;
+    const int rows = min(8, s.m_tiles - first);
+    t -= band * 8 * s.n_tiles;
+    r.m = (first + t % rows) * TILE_M;
+    r.n = (t / rows) * (s.mode == kSideBySide ? TILE_N / 2 : TILE_N);
+    return r;
+}
+
+// Bounded wait, as wait_bar (mhcpb_wait.cuh); `cluster`: for arrivals from other blocks.
+template <bool CLUSTER>
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, bool honor) {
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t i = 1;; ++i) {
+        if (CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+        if ((i & 31u) == 0) {
+            if (honor && *abort_flag) return false;
+            if (ptx::globaltimer() - t0 > kWaitNs) {
+                *abort_flag = 1u;
+                atomicCAS(&g_status, kDevOk, kDevTimeout);
+                return false;
+            }
+        }
+    }
+}
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, bool honor = true) {
+    if (CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+    return wait_slow<CLUSTER>(bar, parity, abort_flag, honor);
+}
+
+// Epilogue: struct with `static constexpr bool kDual` (two products side by side),
+//   float prepare(int lane) const
+// run by whole warps under the first products, whose result every call gets as `extra`, and
+//   void operator()(int group, int64_t row, int64_t col, int count, const float (&v)[8], const float (&w)[8],
+//                   float extra) const
+// for `count` (1..8) elements of one row of C; w: the second product's (kDual).
+template <bool PAIR, class Epilogue>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const Shape s, const Epilogue epi, const __grid_constant__ CUtensorMap a0,
+                   const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b0,
+                   const __grid_constant__ CUtensorMap b1) {
+    using C = Cfg<PAIR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const uint32_t base = ptx::smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_rank();
+    uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::off_misc);
+    volatile uint32_t* abort_flag = holder + 1;
+    float* shared_extra = reinterpret_cast<float*>(holder + 2);
+    auto bar = [&](int i) { return base + C::off_bar + 8u * (uint32_t)i; };
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0u;
+        for (int i = 0; i < C::stages; ++i) {
+            ptx::mbar_init(bar(C::b_full + i), 1);
+            ptx::mbar_init(bar(C::b_empty + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(C::b_done + i), 1);
+            ptx::mbar_init(bar(C::b_free + i), 8 * C::blocks);
+        }
+        ptx::mbar_init(bar(C::b_last), 1);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&a0);
+        ptx::prefetch_tensormap(&b0);
+    }
+    if (warp == 2) ptx::tmem_get<PAIR>(ptx::smem_u32(holder), C::tmem_columns);
+    ptx::tc_fence_before();
+    ptx::cluster_arrive();   // the pair's barriers are there before either block uses them
+    ptx::cluster_wait();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *holder;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+
+    // Tiles: every gridDim.x / cluster blocks-th one.  k steps of this block: all, or its share of a split sum.
+    const int cluster = PAIR ? 2 : s.split;
+    const int first_tile = blockIdx.x / cluster, step_tile = gridDim.x / cluster;
+    const int steps = s.k_steps * (s.mode == kLongK ? 2 : 1);
+    const int k_begin = PAIR ? 0 : (int)((int64_t)rank * steps / s.split);
+    const int k_end = PAIR ? steps : (int)((int64_t)(rank + 1) * steps / s.split);
+    const bool leader = !PAIR || rank == 0;
+
+    if (warp == 0 && lane == 0) {
+        const uint32_t half = PAIR ? rank : 0;
+        uint32_t n = 0;                                      // steps so far
+        bool ok = true;
+        for (int t = first_tile; ok && t < s.tiles; t += step_tile) {
+            const Tile tile = tile_at<C::tile_m, C::tile_n>(s, t);
+            const int m0 = tile.m + (int)half * 128;
+            const int n0 = tile.n + (s.mode == kSideBySide ? 0 : (int)half * 128);
+            for (int k = k_begin; k < k_end; ++k, ++n) {
+                const uint32_t st = n % C::stages, ph = (n / C::stages) & 1u;
+                if (!wait<PAIR>(bar(C::b_empty + st), ph ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = PAIR ? ptx::map_rank(bar(C::b_full + st), 0) : bar(C::b_full + st);
+                if (leader) ptx::mbar_arrive_expect_tx(bar(C::b_full + st), C::blocks * kStageBytes);
+                const bool second = s.mode == kLongK && k >= s.k_steps;
+                const int k0 = (second ? k - s.k_steps : k) * kBox;
+                const CUtensorMap* am = second || tile.group ? &a1 : &a0;
+                const CUtensorMap* bm = second || tile.group ? &b1 : &b0;
+                const uint32_t dst = base + st * kStageBytes;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int m = m0 + kBox * j;
+                    ptx::tma_load_tile<PAIR>(dst + j * kBoxBytes, am, s.a_mn ? m : k0, s.a_mn ? k0 : m, full);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // side by side: a block of a pair has one product's rows, a single block 64 of each
+                    const bool other = s.mode == kSideBySide && (PAIR ? half == 1 : j == 1);
+                    const int nn = n0 + (s.mode == kSideBySide && !PAIR ? 0 : kBox * j);
+                    ptx::tma_load_tile<PAIR>(dst + (2 + j) * kBoxBytes, other ? &b1 : bm, s.b_mn ? nn : k0,
+                                             s.b_mn ? k0 : nn, full);
+                }
+            }
+        }
+        if (!ok && leader)   // the copies that were started end before the block does
+            for (uint32_t i = n > C::stages ? n - C::stages : 0; i < n; ++i)
+                wait<PAIR>(bar(C::b_full + i % C::stages), (i / C::stages) & 1u, abort_flag, false);
+    } else if (warp == 1 && lane == 0 && leader) {
+        const uint32_t idesc = ptx::idesc_16bit(C::tile_m, C::tile_n, s.bf16, s.a_mn, s.b_mn);
+        // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes
+        const uint32_t a_step = s.a_mn ? 2048 : 32, b_step = s.b_mn ? 2048 : 32;
+        const uint64_t shape = ptx::smem_desc(0, kBoxBytes, 1024, ptx::kLayoutSwizzle128B);
+        uint32_t n = 0, done = 0;
+        bool ok = true;
+        for (int t = first_tile; ok && t < s.tiles; t += step_tile, ++done) {
+            const uint32_t acc = done % C::accumulators, turn = done / C::accumulators;
+            if (!wait<PAIR>(bar(C::b_free + acc), (turn & 1u) ^ 1u, abort_flag)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t d = tmem + acc * C::tile_n;
+            if (s.stall && !wait<PAIR>(bar(C::b_last), 0u, abort_flag)) {   // a test's wait that nothing ends
+                ok = false;
+                break;
+            }
+            for (int k = k_begin; k < k_end; ++k, ++n) {
+                const uint32_t st = n % C::stages, ph = (n / C::stages) & 1u;
+                if (!wait<PAIR>(bar(C::b_full + st), ph, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t a = base + st * kStageBytes, b = a + 2 * kBoxBytes;
+#pragma unroll
+                for (int q = 0; q < kBox / 16; ++q)
+                    ptx::mma_f16<PAIR>(d, shape | (((a + q * a_step) >> 4) & 0x3FFFu),
+                                       shape | (((b + q * b_step) >> 4) & 0x3FFFu), idesc, k > k_begin || q > 0);
+                ptx::mma_commit<PAIR>(bar(C::b_empty + st), 3);
+            }
+            if (ok) ptx::mma_commit<PAIR>(bar(C::b_done + acc), 3);
+        }
+        if (!ok) {           // the MMAs that were issued end before the block does
+            ptx::mma_commit<PAIR>(bar(C::b_last), 1);
+            wait<PAIR>(bar(C::b_last), 0u, abort_flag, false);
+        }
+    } else if (!PAIR && warp == 3) {
+        const float extra = epi.prepare(lane);
+        if (lane == 0) *shared_extra = extra;
+    } else if (warp >= kEpilogueWarp) {
+        const int quad = warp & 3, half = (warp - kEpilogueWarp) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        if constexpr (PAIR) {
+            float* scratch = reinterpret_cast<float*>(smem + C::off_scratch) + (warp - kEpilogueWarp) * 32 * C::row;
+            // 32 columns of this warp's 32 rows into v[q]: row 8 q + lane / 4, columns 8 (lane % 4) ..
+            auto fetch = [&](uint32_t column, float (&v)[4][8]) {
+                uint32_t u[32];
+                ptx::tmem_ld_32x32b_x32(lanes + column, u);
+                ptx::tc_wait_ld_regs(u);
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                    *reinterpret_cast<uint4*>(scratch + lane * C::row + c) = make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4* p = reinterpret_cast<const float4*>(scratch + (8 * q + lane / 4) * C::row + 8 * (lane & 3));
+                    const float4 x = p[0], y = p[1];
+                    v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
+                    v[q][4] = y.x, v[q][5] = y.y, v[q][6] = y.z, v[q][7] = y.w;
+                }
+            };
+            const float extra = epi.prepare(lane);
+            uint32_t done = 0;
+            for (int t = first_tile; t < s.tiles; t += step_tile, ++done) {
+                const uint32_t acc = done & 1u;
+                if (!__all_sync(0xFFFFFFFFu, wait<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag))) break;
+                ptx::tc_fence_after();
+                const Tile tile = tile_at<C::tile_m, C::tile_n>(s, t);
+                const int64_t row0 = tile.m + (int64_t)rank * 128 + quad * 32;
+                const uint32_t d = acc * C::tile_n;
+                constexpr int kChunks = Epilogue::kDual ? 2 : 4;   // of 32 columns per warp
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    const int column = half * kChunks * 32 + c * 32;
+                    const int64_t col0 = tile.n + column;
+                    float v[4][8], w[Epilogue::kDual ? 4 : 1][8];
+                    fetch(d + column, v);
+                    if constexpr (Epilogue::kDual) fetch(d + 128 + column, w);
+                    if (c == kChunks - 1) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(bar(C::b_free + acc), 0));
+                    }
+                    const int64_t col = col0 + 8 * (lane & 3);
+                    const int count = (int)min((int64_t)8, s.N - col);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int64_t row = row0 + 8 * q + lane / 4;
+                        if (row < s.M && count > 0) 
+                            epi(tile.group, row, col, count, v[q], w[Epilogue::kDual ? q : 0], extra);
+                    }
+                    if (tile.mirror) {   // the scratch still has the chunk: column `lane`, eight rows at a time
+                        const int64_t mrow = col0 + lane;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = scratch[(8 * q + i) * C::row + lane];
+                            const int64_t mcol = row0 + 8 * q;
+                            if (mrow < s.N && mcol < s.M) epi(0, mrow, mcol, (int)min((int64_t)8, s.M - mcol), x, x, extra);
+                        }
+                    }
+                }
+            }
+        } else if (__all_sync(0xFFFFFFFFu, wait<PAIR>(bar(C::b_done), 0u, abort_flag))) {
+            ptx::tc_fence_after();
+            float* part = reinterpret_cast<float*>(smem + C::off_scratch);
+            const int row = quad * 32 + lane;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t u[32];
+                const int column = half * 64 + c * 32;
+                ptx::tmem_ld_32x32b_x32(lanes + column, u);
+                ptx::tc_wait_ld_regs(u);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4*>(part + row * C::row + column + i) =
+                        make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+            }
+        }
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_arrive();   // pair: no block leaves while the other's MMAs or arrivals may reach it
+    ptx::cluster_wait();
+    ptx::tc_fence_after();
+    __syncwarp();
+    if (warp == 2) ptx::tmem_free<PAIR>(tmem, C::tmem_columns);
+
+    if constexpr (!PAIR) {
+        // Every block has its part of the tile in shared memory; each adds up its share of the vectors.
+        const Tile tile = tile_at<C::tile_m, C::tile_n>(s, first_tile);
+        const uint32_t part = base + C::off_scratch;
+        const float extra = *shared_extra;
+        constexpr int kWidth = Epilogue::kDual ? 64 : 128;
+        const int rows = (int)min((int64_t)128, s.M - tile.m), cols = (int)min((int64_t)kWidth, s.N - tile.n);
+        auto gather = [&](int r, int c, float (&v)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            for (int z = 0; z < s.split; ++z) {
+                const uint32_t p = ptx::map_rank(part + (uint32_t)(r * C::row + c) * 4, z);
+                const float4 x = ptx::ld_cluster_f32x4(p), y = ptx::ld_cluster_f32x4(p + 16);
+                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+            }
+        };
+        const int across = (cols + 7) / 8;
+        for (int u = (int)rank * kThreads + threadIdx.x; u < rows * across; u += s.split * kThreads) {
+            const int r = u / across, c = (u - r * across) * 8;
+            float v[8], w[8];
+            gather(r, c, v);
+            if constexpr (Epilogue::kDual) gather(r, 64 + c, w);
+            epi(tile.group, (int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c), v, w, extra);
+        }
+        if (tile.mirror) {
+            const int down = (rows + 7) / 8;
+            for (int u = (int)rank * kThreads + threadIdx.x; u < cols * down; u += s.split * kThreads) {
+                const int g = u / cols, c = u - g * cols;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = 0.f;
+                    for (int z = 0; z < s.split; ++z)
+                        x[i] += ptx::ld_cluster_f32(ptx::map_rank(part + (uint32_t)((8 * g + i) * C::row + c) * 4, z));
+                }
+                epi(0, (int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g), x, x, extra);
+            }
+        }
+        ptx::cluster_arrive();   // the parts stay until every block has read them
+        ptx::cluster_wait();
+    }
+}
+
+// ---------------------------------------------------------------- host
+template <class Epilogue>
+cudaError_t allow() {
+    static std::atomic<uint64_t> pair{0}, single{0};
+    cudaError_t e = ops::allow_shared(product_kernel<true, Epilogue>, (int)Cfg<true>::smem, pair);
+    return e != cudaSuccess ? e : ops::allow_shared(product_kernel<false, Epilogue>, (int)Cfg<false>::smem, single);
+}
+
+// a1 and b1 may be null where the mode has one A or B.
+template <class Epilogue>
+cudaError_t launch(Shape s, const Epilogue& epi, const CUtensorMap* a0, const CUtensorMap* a1, const CUtensorMap* b0,
+                   const CUtensorMap* b1, cudaStream_t stream) {
+    cudaError_t e = allow<Epilogue>();
+    if (e != cudaSuccess) return e;
+    const Choice c = choose(s);
+    s.m_tiles = c.m_tiles;
+    s.n_tiles = c.n_tiles;
+    s.tiles = c.tiles;
+    s.split = c.split;
+    cudaLaunchConfig_t config{};
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = c.pair ? 2 : (unsigned)c.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    config.attrs = attr;
+    config.numAttrs = 2;
+    config.blockDim = kThreads;
+    config.gridDim = (unsigned)c.grid;
+    config.dynamicSmemBytes = c.pair ? Cfg<true>::smem : Cfg<false>::smem;
+    config.stream = stream;
+    if (a1 == nullptr) a1 = a0;
+    if (b1 == nullptr) b1 = b0;
+    return c.pair ? cudaLaunchKernelEx(&config, product_kernel<true, Epilogue>, s, epi, *a0, *a1, *b0, *b1)
+                  : cudaLaunchKernelEx(&config, product_kernel<false, Epilogue>, s, epi, *a0, *a1, *b0, *b1);
+}
+
+// This translation unit's status word, then cleared if asked (current device).
+static inline cudaError_t read_status(uint32_t* status, bool clear) {
+    const uint32_t zero = kDevOk;
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(uint32_t));
+    if (e == cudaSuccess && clear && *status != kDevOk) e = cudaMemcpyToSymbol(g_status, &zero, sizeof(uint32_t));
+    return e;
+}
+
+// ---------------------------------------------------------------- eight neighbours in memory
+template <class T>
+struct Pair16;
+template <>
+struct Pair16<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+    }
+};
+template <>
+struct Pair16<__half> {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __half2 p = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    }
+};
+__device__ __forceinline__ bool whole(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// What an epilogue without a value of its own has to prepare.
+struct Nothing {
+    __device__ __forceinline__ float prepare(int) const { return 0.f; }
+};
+template <class T>
+__device__ __forceinline__ float to_float(T v) {
+    return (float)v;
+}
+
+// A matrix in memory; `elements` (of the whole matrix) bounds the accesses of a checked build.
+template <class T>
+struct Matrix {
+    T* ptr;
+    int64_t ld;
+    size_t elements;
+
+    __device__ __forceinline__ bool ok(const T* p, int count, uint32_t site) const {
+        return check::in(p, (size_t)count * sizeof(T), ptr, elements * sizeof(T), site);
+    }
+    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
+        const T* p = ptr + row * ld + col;
+        if (!ok(p, count, site)) return;
+        if (count == 8 && whole(p)) {
+            if constexpr (sizeof(T) == 2) {
+                using P = Pair16<std::remove_const_t<T>>;
+                const uint4 u = *reinterpret_cast<const uint4*>(p);
+                const float2 a = P::unpack(u.x), b = P::unpack(u.y), c = P::unpack(u.z), d = P::unpack(u.w);
+                v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
+            } else {
+                const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < count ? to_float(p[i]) : 0.f;
+    }
+    __device__ __forceinline__ void store(int64_t row, int64_t col, int count, const float (&v)[8], uint32_t site) const {
+        T* p = ptr + row * ld + col;
+        if (!ok(p, count, site)) return;
+        if constexpr (sizeof(T) == 2) {
+            if (count == 8 && whole(p)) {
+                *reinterpret_cast<uint4*>(p) = make_uint4(Pair16<T>::pack(v[0], v[1]), Pair16<T>::pack(v[2], v[3]),
+                                                          Pair16<T>::pack(v[4], v[5]), Pair16<T>::pack(v[6], v[7]));
+                return;
+            }
+        } else if (count == 8 && whole(p)) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < count) p[i] = (T)v[i];
+    }
+};
+
+}  // namespace product
+}  // namespace mhcpb

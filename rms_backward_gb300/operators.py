@@ -1,7 +1,7 @@
 """The operators around the projection stage on torch CUDA tensors: embedding
 into the residual streams, layer norm, dropout, stream collapse with its norm,
-and stream update, each with its gradient (``include/mhcpb.h`` has the
-formulas).
+stream update and the gated feed-forward block, each with its gradient, and the
+orthogonalised update of a weight (``include/mhcpb.h`` has the formulas).
 
 Every function writes into tensors the caller passes and returns nothing; it
 allocates nothing and does not wait.  Types, shapes and strides are checked
@@ -257,3 +257,100 @@ def mhc_update_backward(x, y, h, grad_x_out, grad_y, grad_h, rng=None, *, p: flo
                                           _need(grad_h, "grad_h", (T, 24), _F32), _handle(stream, x))
     if status:
         abi._check(status, "mhcpb_update_backward")
+
+
+# ---------------------------------------------------------------- gated feed-forward
+_ACTIVATIONS = {"silu": abi.MHCPB_SILU, "gelu": abi.MHCPB_GELU}
+
+
+def _activation(name):
+    try:
+        return _ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation: expected one of {', '.join(_ACTIVATIONS)}, got {name!r}") from None
+
+
+def _ffn(x, w_gate, w_up, w_down):
+    """(T, D, F, type, x's and the weights' pointers) of a block's inputs."""
+    T, D = shape = _two_dims(x, "x")
+    F, _ = _two_dims(w_gate, "w_gate")
+    dtype = x.dtype
+    if dtype is not _BF16 and dtype is not torch.float16:
+        raise ValueError(f"x: expected bfloat16 or float16, got {dtype}")
+    return (T, D, F, _TYPES[dtype], *_rows(x, "x", shape, dtype), _need(w_gate, "w_gate", (F, D), dtype),
+            _need(w_up, "w_up", (F, D), dtype), _need(w_down, "w_down", (D, F), dtype))
+
+
+def mhc_ffn_forward_workspace_bytes(T: int, D: int, F: int) -> int:
+    """Scratch bytes of :func:`mhc_ffn_forward`."""
+    return abi.mhcpb_ffn_forward_workspace_bytes(T, D, F)
+
+
+def mhc_ffn_forward(x, w_gate, w_up, w_down, y, workspace, gate=None, up=None, *, activation: str = "silu",
+                    stream=None):
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T: x, y [T, D] (BF16 or FP16, with
+    row strides), w_gate, w_up [F, D], w_down [D, F] of the same type; activation
+    "silu" or "gelu" (by erf).  gate, up [T, F] receive the two projections for
+    :func:`mhc_ffn_backward`, both None where none follows."""
+    T, D, F, kind, xp, xs, wg, wu, wd = _ffn(x, w_gate, w_up, w_down)
+    dtype = x.dtype
+    yp, ys = _rows(y, "y", (T, D), dtype)
+    status = _lib().mhcpb_ffn_forward(T, D, F, kind, _activation(activation), xp, xs, wg, wu, wd, yp, ys,
+                                      _maybe(gate, "gate", (T, F), dtype), _maybe(up, "up", (T, F), dtype),
+                                      *_scratch(workspace), _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_ffn_forward")
+
+
+def mhc_ffn_backward_workspace_bytes(T: int, D: int, F: int) -> int:
+    """Scratch bytes of :func:`mhc_ffn_backward`."""
+    return abi.mhcpb_ffn_backward_workspace_bytes(T, D, F)
+
+
+def mhc_ffn_backward(x, w_gate, w_up, w_down, gate, up, grad_y, grad_x, grad_w_gate, grad_w_up, grad_w_down, workspace, *,
+                     activation: str = "silu", accumulate: bool = False, stream=None):
+    """grad_x [T, D] and the weights' gradients (of the weights' type, or all FP32;
+    added to with ``accumulate``) from the forward's inputs, gate, up and grad_y
+    [T, D].  Each of the four outputs may be None."""
+    T, D, F, kind, xp, xs, wg, wu, wd = _ffn(x, w_gate, w_up, w_down)
+    dtype = x.dtype
+    grads = [(g, name, shape) for g, name, shape in ((grad_w_gate, "grad_w_gate", (F, D)), (grad_w_up, "grad_w_up", (F, D)),
+                                                     (grad_w_down, "grad_w_down", (D, F)))]
+    gtype = next((g.dtype for g, _, _ in grads if g is not None), dtype)
+    if gtype is not dtype and gtype is not _F32:
+        raise ValueError(f"weight gradients: expected {dtype} or {_F32}, got {gtype}")
+    gp, gs = _rows(grad_y, "grad_y", (T, D), dtype)
+    dp, ds = (None, D) if grad_x is None else _rows(grad_x, "grad_x", (T, D), dtype)
+    status = _lib().mhcpb_ffn_backward(T, D, F, kind, _activation(activation), xp, xs, wg, wu, wd,
+                                       _need(gate, "gate", (T, F), dtype), _need(up, "up", (T, F), dtype), gp, gs, dp,
+                                       ds, _TYPES[gtype], *(_maybe(g, name, shape, gtype) for g, name, shape in grads),
+                                       abi.MHCPB_ACCUMULATE_DW if accumulate else 0, *_scratch(workspace),
+                                       _handle(stream, x))
+    if status:
+        abi._check(status, "mhcpb_ffn_backward")
+
+
+# ---------------------------------------------------------------- orthogonalised update
+def mhc_orthogonalize_workspace_bytes(m: int, n: int) -> int:
+    """Scratch bytes of :func:`mhc_orthogonalize`."""
+    return abi.mhcpb_orthogonalize_workspace_bytes(m, n)
+
+
+def mhc_orthogonalize(g, out, workspace, *, steps: int = 5, eps: float = 1e-7, scale: float = 1.0, stream=None):
+    """out [m, n] BF16 = scale times g [m, n] (BF16, FP16 or FP32) with its singular
+    values brought near 1 by ``steps`` Newton-Schulz steps; g and out may have a
+    row stride."""
+    m, n = shape = _two_dims(g, "g")
+    gp, gs = _rows(g, "g", shape, g.dtype)
+    op, os = _rows(out, "out", shape, _BF16)
+    status = _lib().mhcpb_orthogonalize(m, n, _type(g, "g"), gp, gs, steps, eps, scale, op, os, *_scratch(workspace),
+                                        _handle(stream, g))
+    if status:
+        abi._check(status, "mhcpb_orthogonalize")
+
+
+def mhc_operators_device_status(clear: bool = False) -> int:
+    """0, or ``MHCPB_ERR_DEVICE_TIMEOUT`` once a wait inside a kernel of the
+    feed-forward block or the orthogonalised update has run out on the current
+    device (their outputs are then wrong).  Waits for the device."""
+    return abi.mhcpb_operators_device_status(clear)
