@@ -25,7 +25,7 @@ using product::Shape;
 // act(g) and act'(g)
 __device__ __forceinline__ float2 activate(float g, int kind) {
     if (kind == MHCPB_SILU) {
-        const float q = __fdividef(1.f, 1.f + __expf(-g));
+        const float q = __frcp_rn(1.f + __expf(-g));   // (__fdividef gives 0 beyond 2^126)
         return make_float2(g * q, q * (1.f + g * (1.f - q)));
     }
     const float p = 0.5f * erfcf(g * -0.70710678f);   // the normal distribution function, accurate in its tail
@@ -33,12 +33,12 @@ __device__ __forceinline__ float2 activate(float g, int kind) {
 }
 
 template <class T>
-struct GatedEpilogue : product::Nothing {
+struct GatedEpilogue {
     static constexpr bool kDual = true;
     Matrix<T> hidden, gate, up;
     int activation;
     __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&g)[8],
-                                               const float (&u)[8], float) const {
+                                               const float (&u)[8]) const {
         float a[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] = activate(g[i], activation).x * u[i];
@@ -51,12 +51,12 @@ struct GatedEpilogue : product::Nothing {
 };
 
 template <class T>
-struct GradEpilogue : product::Nothing {
+struct GradEpilogue {
     static constexpr bool kDual = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
     int activation;
     __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&da)[8],
-                                               const float (&)[8], float) const {
+                                               const float (&)[8]) const {
         float g[8], u[8], a[8];
         gate.load(row, col, count, g, 3);
         up.load(row, col, count, u, 4);
@@ -74,12 +74,12 @@ struct GradEpilogue : product::Nothing {
 };
 
 template <class O>
-struct StoreEpilogue : product::Nothing {
+struct StoreEpilogue {
     static constexpr bool kDual = false;
     Matrix<O> out[2];
     bool accumulate;
     __device__ __forceinline__ void operator()(int group, int64_t row, int64_t col, int count, const float (&v)[8],
-                                               const float (&)[8], float) const {
+                                               const float (&)[8]) const {
         const Matrix<O>& o = out[group];
         if (!accumulate) return o.store(row, col, count, v, 8);
         float old[8];
@@ -169,11 +169,11 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     Shape s{};
     s.bf16 = bf16;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
-    const GatedEpilogue<T> gated{{}, matrix<T>(hidden, T_, F, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
+    const GatedEpilogue<T> gated{matrix<T>(hidden, T_, F, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
                                  a.activation};
     MHCM_TRY(product::launch(s, gated, &x.map, nullptr, &wg.map, &wu.map, stream));
     s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain;
-    const StoreEpilogue<T> store{{}, {matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
+    const StoreEpilogue<T> store{{matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
     return product::launch(s, store, &h.map, nullptr, &wd.map, nullptr, stream);
 }
 
@@ -185,7 +185,7 @@ cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const
     s.bf16 = a.type == MHCPB_BF16;
     s.M = M, s.N = N, s.k_steps = steps_of(a.T), s.mode = mode;
     s.a_mn = s.b_mn = 1;
-    const StoreEpilogue<O> store{{}, {matrix<O>(out0, M, N, N), matrix<O>(out1, M, N, N)}, a.accumulate};
+    const StoreEpilogue<O> store{{matrix<O>(out0, M, N, N), matrix<O>(out1, M, N, N)}, a.accumulate};
     return product::launch(s, store, a0, a1, b, b, stream);
 }
 
@@ -212,13 +212,13 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     s.bf16 = bf16;
     s.stall = a.stall;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.b_mn = 1;
-    const GradEpilogue<T> grad{{}, matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, F, Fp),
+    const GradEpilogue<T> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, F, Fp),
                                matrix<T>(grad_up, T_, F, Fp), matrix<T>(hidden, T_, F, Fp), a.activation};
     MHCM_TRY(product::launch(s, grad, &dy.map, nullptr, &wd.map, nullptr, stream));
     s.stall = 0;
     if (a.grad_x) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
-        const StoreEpilogue<T> store{{}, {matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
+        const StoreEpilogue<T> store{{matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
         MHCM_TRY(product::launch(s, store, &dg.map, &du.map, &wg.map, &wu.map, stream));
     }
     if (a.grad_w[0] && a.grad_w[1])

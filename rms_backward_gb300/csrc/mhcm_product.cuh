@@ -125,11 +125,8 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
     return wait_slow<CLUSTER>(bar, parity, abort_flag, honor);
 }
 
-// Epilogue: struct with `static constexpr bool kDual` (two products side by side),
-//   float prepare(int lane) const
-// run by whole warps under the first products, whose result every call gets as `extra`, and
-//   void operator()(int group, int64_t row, int64_t col, int count, const float (&v)[8], const float (&w)[8],
-//                   float extra) const
+// Epilogue: struct with `static constexpr bool kDual` (two products side by side) and
+//   void operator()(int group, int64_t row, int64_t col, int count, const float (&v)[8], const float (&w)[8]) const
 // for `count` (1..8) elements of one row of C; w: the second product's (kDual).
 template <bool PAIR, class Epilogue>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -144,7 +141,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rank = ptx::cluster_rank();
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::off_misc);
     volatile uint32_t* abort_flag = holder + 1;
-    float* shared_extra = reinterpret_cast<float*>(holder + 2);
     auto bar = [&](int i) { return base + C::off_bar + 8u * (uint32_t)i; };
 
     if (threadIdx.x == 0) {
@@ -257,9 +253,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mma_commit<PAIR>(bar(C::b_last), 1);
             wait<PAIR>(bar(C::b_last), 0u, abort_flag, false);
         }
-    } else if (!PAIR && warp == 3) {
-        const float extra = epi.prepare(lane);
-        if (lane == 0) *shared_extra = extra;
     } else if (warp >= kEpilogueWarp) {
         const int quad = warp & 3, half = (warp - kEpilogueWarp) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -283,7 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[q][4] = y.x, v[q][5] = y.y, v[q][6] = y.z, v[q][7] = y.w;
                 }
             };
-            const float extra = epi.prepare(lane);
             uint32_t done = 0;
             for (int t = first_tile; t < s.tiles; t += step_tile, ++done) {
                 const uint32_t acc = done & 1u;
@@ -310,8 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int64_t row = row0 + 8 * q + lane / 4;
-                        if (row < s.M && count > 0) 
-                            epi(tile.group, row, col, count, v[q], w[Epilogue::kDual ? q : 0], extra);
+                        if (row < s.M && count > 0) epi(tile.group, row, col, count, v[q], w[Epilogue::kDual ? q : 0]);
                     }
                     if (tile.mirror) {   // the scratch still has the chunk: column `lane`, eight rows at a time
                         const int64_t mrow = col0 + lane;
@@ -321,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) x[i] = scratch[(8 * q + i) * C::row + lane];
                             const int64_t mcol = row0 + 8 * q;
-                            if (mrow < s.N && mcol < s.M) epi(0, mrow, mcol, (int)min((int64_t)8, s.M - mcol), x, x, extra);
+                            if (mrow < s.N && mcol < s.M) epi(0, mrow, mcol, (int)min((int64_t)8, s.M - mcol), x, x);
                         }
                     }
                 }
@@ -356,7 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Every block has its part of the tile in shared memory; each adds up its share of the vectors.
         const Tile tile = tile_at<C::tile_m, C::tile_n>(s, first_tile);
         const uint32_t part = base + C::off_scratch;
-        const float extra = *shared_extra;
         constexpr int kWidth = Epilogue::kDual ? 64 : 128;
         const int rows = (int)min((int64_t)128, s.M - tile.m), cols = (int)min((int64_t)kWidth, s.N - tile.n);
         auto gather = [&](int r, int c, float (&v)[8]) {
@@ -375,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[8], w[8];
             gather(r, c, v);
             if constexpr (Epilogue::kDual) gather(r, 64 + c, w);
-            epi(tile.group, (int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c), v, w, extra);
+            epi(tile.group, (int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c), v, w);
         }
         if (tile.mirror) {
             const int down = (rows + 7) / 8;
@@ -388,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int z = 0; z < s.split; ++z)
                         x[i] += ptx::ld_cluster_f32(ptx::map_rank(part + (uint32_t)((8 * g + i) * C::row + c) * 4, z));
                 }
-                epi(0, (int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g), x, x, extra);
+                epi(0, (int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g), x, x);
             }
         }
         ptx::cluster_arrive();   // the parts stay until every block has read them
@@ -466,10 +456,6 @@ struct Pair16<__half> {
     }
 };
 __device__ __forceinline__ bool whole(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-// What an epilogue without a value of its own has to prepare.
-struct Nothing {
-    __device__ __forceinline__ float prepare(int) const { return 0.f; }
-};
 template <class T>
 __device__ __forceinline__ float to_float(T v) {
     return (float)v;
