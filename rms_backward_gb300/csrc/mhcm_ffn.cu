@@ -37,8 +37,10 @@ struct GatedEpilogue {
     static constexpr bool kDual = true;
     Matrix<T> hidden, gate, up;
     int activation;
-    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&g)[8],
-                                               const float (&u)[8]) const {
+    struct Read {};
+    __device__ __forceinline__ Read read(int64_t, int64_t, int) const { return {}; }
+    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&g)[8],
+                                          const float (&u)[8], const Read&) const {
         float a[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] = activate(g[i], activation).x * u[i];
@@ -55,11 +57,17 @@ struct GradEpilogue {
     static constexpr bool kDual = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
     int activation;
-    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&da)[8],
-                                               const float (&)[8]) const {
+    struct Read {
+        typename Matrix<T>::Raw g, u;
+    };
+    __device__ __forceinline__ Read read(int64_t row, int64_t col, int count) const {
+        return {gate.raw(row, col, count, 3), up.raw(row, col, count, 4)};
+    }
+    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&da)[8],
+                                          const float (&)[8], const Read& in) const {
         float g[8], u[8], a[8];
-        gate.load(row, col, count, g, 3);
-        up.load(row, col, count, u, 4);
+        in.g.to(g);
+        in.u.to(u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 f = activate(g[i], activation);
@@ -78,8 +86,10 @@ struct StoreEpilogue {
     static constexpr bool kDual = false;
     Matrix<O> out[2];
     bool accumulate;
-    __device__ __forceinline__ void operator()(int group, int64_t row, int64_t col, int count, const float (&v)[8],
-                                               const float (&)[8]) const {
+    struct Read {};
+    __device__ __forceinline__ Read read(int64_t, int64_t, int) const { return {}; }
+    __device__ __forceinline__ void write(int group, int64_t row, int64_t col, int count, const float (&v)[8],
+                                          const float (&)[8], const Read&) const {
         const Matrix<O>& o = out[group];
         if (!accumulate) return o.store(row, col, count, v, 8);
         float old[8];
@@ -180,11 +190,12 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
 // dWd, or dWg and dWu together or one of them: C = A^T B over the tokens
 template <class O>
 cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const CUtensorMap* a0, const CUtensorMap* a1,
-                            const CUtensorMap* b, void* out0, void* out1, cudaStream_t stream) {
+                            const CUtensorMap* b, void* out0, void* out1, bool beside, cudaStream_t stream) {
     Shape s{};
     s.bf16 = a.type == MHCPB_BF16;
     s.M = M, s.N = N, s.k_steps = steps_of(a.T), s.mode = mode;
     s.a_mn = s.b_mn = 1;
+    s.beside = beside;
     const StoreEpilogue<O> store{{matrix<O>(out0, M, N, N), matrix<O>(out1, M, N, N)}, a.accumulate};
     return product::launch(s, store, a0, a1, b, b, stream);
 }
@@ -215,19 +226,28 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     const GradEpilogue<T> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, F, Fp),
                                matrix<T>(grad_up, T_, F, Fp), matrix<T>(hidden, T_, F, Fp), a.activation};
     MHCM_TRY(product::launch(s, grad, &dy.map, nullptr, &wd.map, nullptr, stream));
+    // The products that are left need only what the first wrote: each starts as soon as the one
+    // before it leaves room (its last tiles keep a part of the GPU busy), not when that has ended.
     s.stall = 0;
+    bool beside = false;
     if (a.grad_x) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
         const StoreEpilogue<T> store{{matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
         MHCM_TRY(product::launch(s, store, &dg.map, &du.map, &wg.map, &wu.map, stream));
+        beside = true;
     }
-    if (a.grad_w[0] && a.grad_w[1])
-        MHCM_TRY(weight_gradient<O>(a, product::kGroups, F, D, &dg.map, &du.map, &x.map, a.grad_w[0], a.grad_w[1], stream));
-    else if (a.grad_w[0] || a.grad_w[1])
+    if (a.grad_w[0] && a.grad_w[1]) {
+        MHCM_TRY(weight_gradient<O>(a, product::kGroups, F, D, &dg.map, &du.map, &x.map, a.grad_w[0], a.grad_w[1], beside,
+                                    stream));
+        beside = true;
+    } else if (a.grad_w[0] || a.grad_w[1]) {
         MHCM_TRY(weight_gradient<O>(a, product::kPlain, F, D, a.grad_w[0] ? &dg.map : &du.map, nullptr, &x.map,
-                                    a.grad_w[0] ? a.grad_w[0] : a.grad_w[1], nullptr, stream));
+                                    a.grad_w[0] ? a.grad_w[0] : a.grad_w[1], nullptr, beside, stream));
+        beside = true;
+    }
     if (a.grad_w[2])
-        MHCM_TRY(weight_gradient<O>(a, product::kPlain, D, F, &dy.map, nullptr, &h.map, a.grad_w[2], nullptr, stream));
+        MHCM_TRY(weight_gradient<O>(a, product::kPlain, D, F, &dy.map, nullptr, &h.map, a.grad_w[2], nullptr, beside,
+                                    stream));
     return cudaSuccess;
 }
 

@@ -26,6 +26,9 @@ struct Shape {
     int mode;
     int a_mn, b_mn;    // the operand's rows are k (else its rows are m, or n)
     int bf16;          // else FP16
+    int beside;        // needs nothing of the launch before it, only of one before that (which the launch
+                       // before it waited for): it does not wait for that one to end before its work, but
+                       // before its own end, so that it still ends after it
     int stall;         // a test's: the MMA issuer waits for what nothing signals
     // set by launch()
     int m_tiles, n_tiles, tiles, split;

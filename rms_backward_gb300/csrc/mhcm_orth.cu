@@ -43,14 +43,28 @@ struct Input {
     const void* ptr;
     int type;
     int64_t rows, ld, cols;
-    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
+    // eight elements as they are stored (two words of four, the first alone for 16-bit types), and as FP32
+    __device__ __forceinline__ void raw(int64_t row, int64_t col, int count, uint4 (&u)[2], uint32_t site) const {
         const size_t n = (size_t)((rows - 1) * ld + cols);
+        if (type == MHCPB_FP32) {
+            const auto r = Matrix<const float>{static_cast<const float*>(ptr), ld, n}.raw(row, col, count, site);
+            u[0] = r.u[0], u[1] = r.u[1];
+        } else {
+            u[0] = Matrix<const __half>{static_cast<const __half*>(ptr), ld, n}.raw(row, col, count, site).u[0];
+        }
+    }
+    __device__ __forceinline__ void to(const uint4 (&u)[2], float (&v)[8]) const {
         if (type == MHCPB_FP32)
-            Matrix<const float>{static_cast<const float*>(ptr), ld, n}.load(row, col, count, v, site);
+            Matrix<float>::Raw{u[0], u[1]}.to(v);
         else if (type == MHCPB_BF16)
-            Matrix<const __nv_bfloat16>{static_cast<const __nv_bfloat16*>(ptr), ld, n}.load(row, col, count, v, site);
+            Matrix<__nv_bfloat16>::Raw{u[0]}.to(v);
         else
-            Matrix<const __half>{static_cast<const __half*>(ptr), ld, n}.load(row, col, count, v, site);
+            Matrix<__half>::Raw{u[0]}.to(v);
+    }
+    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
+        uint4 u[2];
+        raw(row, col, count, u, site);
+        to(u, v);
     }
 };
 
@@ -153,8 +167,10 @@ struct GramEpilogue {
     static constexpr bool kDual = false;
     Matrix<__half> out;
     Diagonal lost;
-    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&v)[8],
-                                               const float (&)[8]) const {
+    struct Read {};
+    __device__ __forceinline__ Read read(int64_t, int64_t, int) const { return {}; }
+    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&v)[8],
+                                          const float (&)[8], const Read&) const {
         float r[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[i] = v[i] * (kScaleA / (kScaleX * kScaleX));
@@ -170,10 +186,16 @@ struct PolynomialEpilogue {
     Matrix<__half> out;
     Matrix<const __half> gram;
     Diagonal gram_lost, lost;
-    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&v)[8],
-                                               const float (&)[8]) const {
+    struct Read {
+        Matrix<const __half>::Raw gram;
+    };
+    __device__ __forceinline__ Read read(int64_t row, int64_t col, int count) const {
+        return {gram.raw(row, col, count, 6)};
+    }
+    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&v)[8],
+                                          const float (&)[8], const Read& in) const {
         float r[8];
-        gram.load(row, col, count, r, 6);
+        in.gram.to(r);
         const float l = gram_lost.at(row, 7);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -197,16 +219,29 @@ struct UpdateEpilogue {
     Matrix<__half> copy;        // its FP16 copy
     Matrix<__nv_bfloat16> out;  // the last step's X, times scale; null before
     float scale;
-    __device__ __forceinline__ void operator()(int, int64_t row, int64_t col, int count, const float (&v)[8],
-                                               const float (&)[8]) const {
+    struct Read {
+        uint4 u[2];
+    };
+    __device__ __forceinline__ Read read(int64_t row, int64_t col, int count) const {
+        Read r{};
+        if (inverse != nullptr) {
+            g.raw(row, col, count, r.u, 11);
+        } else {
+            const Matrix<float>::Raw w = x.raw(row, col, count, 12);
+            r.u[0] = w.u[0], r.u[1] = w.u[1];
+        }
+        return r;
+    }
+    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&v)[8],
+                                          const float (&)[8], const Read& in) const {
         float r[8];
         if (inverse != nullptr) {
             const Inverse inv = *inverse;
-            g.load(row, col, count, r, 11);
+            g.to(in.u, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i] = scaled(r[i], inv);
         } else {
-            x.load(row, col, count, r, 12);
+            Matrix<float>::Raw{in.u[0], in.u[1]}.to(r);
         }
         const float by_row = tall ? 0.f : lost.at(row, 13);
 #pragma unroll

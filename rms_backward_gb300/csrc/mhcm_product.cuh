@@ -125,9 +125,14 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
     return wait_slow<CLUSTER>(bar, parity, abort_flag, honor);
 }
 
-// Epilogue: struct with `static constexpr bool kDual` (two products side by side) and
-//   void operator()(int group, int64_t row, int64_t col, int count, const float (&v)[8], const float (&w)[8]) const
+// Epilogue: struct with
+//   static constexpr bool kDual                    two products side by side
+//   struct Read                                    what an element's result needs from memory
+//   Read read(int64_t row, int64_t col, int count) const
+//   void write(int group, int64_t row, int64_t col, int count, const float (&v)[8], const float (&w)[8],
+//              const Read&) const
 // for `count` (1..8) elements of one row of C; w: the second product's (kDual).
+// Several reads are under way before the first write.
 template <bool PAIR, class Epilogue>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const Shape s, const Epilogue epi, const __grid_constant__ CUtensorMap a0,
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
-    ptx::grid_dependency_wait();
+    if (!s.beside) ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
 
     // Tiles: every gridDim.x / cluster blocks-th one.  k steps of this block: all, or its share of a split sum.
@@ -279,16 +284,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t done = 0;
             for (int t = first_tile; t < s.tiles; t += step_tile, ++done) {
                 const uint32_t acc = done & 1u;
-                if (!__all_sync(0xFFFFFFFFu, wait<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag))) break;
-                ptx::tc_fence_after();
                 const Tile tile = tile_at<C::tile_m, C::tile_n>(s, t);
                 const int64_t row0 = tile.m + (int64_t)rank * 128 + quad * 32;
                 const uint32_t d = acc * C::tile_n;
                 constexpr int kChunks = Epilogue::kDual ? 2 : 4;   // of 32 columns per warp
+                bool ok = true;
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
                     const int column = half * kChunks * 32 + c * 32;
                     const int64_t col0 = tile.n + column;
+                    const int64_t col = col0 + 8 * (lane & 3);
+                    const int count = (int)min((int64_t)8, s.N - col);
+                    // the transposed chunk: row `lane` of its columns, eight of its rows at a time
+                    const int64_t mrow = col0 + lane;
+                    typename Epilogue::Read read[4], mread[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int64_t row = row0 + 8 * q + lane / 4;
+                        if (row < s.M && count > 0) read[q] = epi.read(row, col, count);
+                    }
+                    if (tile.mirror) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int64_t mcol = row0 + 8 * q;
+                            if (mrow < s.N && mcol < s.M) mread[q] = epi.read(mrow, mcol, (int)min((int64_t)8, s.M - mcol));
+                        }
+                    }
+                    if (c == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                    }
                     float v[4][8], w[Epilogue::kDual ? 4 : 1][8];
                     fetch(d + column, v);
                     if constexpr (Epilogue::kDual) fetch(d + 128 + column, w);
@@ -297,25 +323,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(bar(C::b_free + acc), 0));
                     }
-                    const int64_t col = col0 + 8 * (lane & 3);
-                    const int count = (int)min((int64_t)8, s.N - col);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int64_t row = row0 + 8 * q + lane / 4;
-                        if (row < s.M && count > 0) epi(tile.group, row, col, count, v[q], w[Epilogue::kDual ? q : 0]);
+                        if (row < s.M && count > 0)
+                            epi.write(tile.group, row, col, count, v[q], w[Epilogue::kDual ? q : 0], read[q]);
                     }
-                    if (tile.mirror) {   // the scratch still has the chunk: column `lane`, eight rows at a time
-                        const int64_t mrow = col0 + lane;
+                    if (tile.mirror) {   // the scratch still has the chunk
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             float x[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) x[i] = scratch[(8 * q + i) * C::row + lane];
                             const int64_t mcol = row0 + 8 * q;
-                            if (mrow < s.N && mcol < s.M) epi(0, mrow, mcol, (int)min((int64_t)8, s.M - mcol), x, x);
+                            if (mrow < s.N && mcol < s.M)
+                                epi.write(0, mrow, mcol, (int)min((int64_t)8, s.M - mcol), x, x, mread[q]);
                         }
                     }
                 }
+                if (!ok) break;
             }
         } else if (__all_sync(0xFFFFFFFFu, wait<PAIR>(bar(C::b_done), 0u, abort_flag))) {
             ptx::tc_fence_after();
@@ -359,31 +385,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
             }
         };
-        const int across = (cols + 7) / 8;
-        for (int u = (int)rank * kThreads + threadIdx.x; u < rows * across; u += s.split * kThreads) {
-            const int r = u / across, c = (u - r * across) * 8;
-            float v[8], w[8];
-            gather(r, c, v);
-            if constexpr (Epilogue::kDual) gather(r, 64 + c, w);
-            epi(tile.group, (int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c), v, w);
-        }
-        if (tile.mirror) {
-            const int down = (rows + 7) / 8;
-            for (int u = (int)rank * kThreads + threadIdx.x; u < cols * down; u += s.split * kThreads) {
-                const int g = u / cols, c = u - g * cols;
-                float x[8];
+        // Four vectors per thread at a time: their reads and the parts' are all under way before the first write.
+        const int threads = s.split * kThreads, me = (int)rank * kThreads + threadIdx.x;
+        const int across = (cols + 7) / 8, units = rows * across;
+        for (int first = me; first < units; first += 4 * threads) {
+            typename Epilogue::Read read[4];
+            float v[4][8], w[Epilogue::kDual ? 4 : 1][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = 0.f;
-                    for (int z = 0; z < s.split; ++z)
-                        x[i] += ptx::ld_cluster_f32(ptx::map_rank(part + (uint32_t)((8 * g + i) * C::row + c) * 4, z));
+            for (int q = 0; q < 4; ++q) {
+                const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
+                if (u < units) read[q] = epi.read((int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c));
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
+                if (u >= units) break;
+                gather(r, c, v[q]);
+                if constexpr (Epilogue::kDual) gather(r, 64 + c, w[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
+                if (u >= units) break;
+                epi.write(tile.group, (int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c), v[q],
+                          w[Epilogue::kDual ? q : 0], read[q]);
+            }
+        }
+        if (tile.mirror) {   // transposed: eight rows of one column
+            const int down = (rows + 7) / 8, flipped = cols * down;
+            for (int first = me; first < flipped; first += 4 * threads) {
+                typename Epilogue::Read read[4];
+                float v[4][8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
+                    if (u < flipped) read[q] = epi.read((int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g));
                 }
-                epi(0, (int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g), x, x);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
+                    if (u >= flipped) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[q][i] = 0.f;
+                    for (int z = 0; z < s.split; ++z) {
+                        const uint32_t p = ptx::map_rank(part + (uint32_t)(8 * g * C::row + c) * 4, z);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[q][i] += ptx::ld_cluster_f32(p + i * C::row * 4);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
+                    if (u >= flipped) break;
+                    epi.write(0, (int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g), v[q], v[q], read[q]);
+                }
             }
         }
         ptx::cluster_arrive();   // the parts stay until every block has read them
         ptx::cluster_wait();
     }
+    if (s.beside) ptx::grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- host
@@ -456,10 +517,6 @@ struct Pair16<__half> {
     }
 };
 __device__ __forceinline__ bool whole(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-template <class T>
-__device__ __forceinline__ float to_float(T v) {
-    return (float)v;
-}
 
 // A matrix in memory; `elements` (of the whole matrix) bounds the accesses of a checked build.
 template <class T>
@@ -471,23 +528,48 @@ struct Matrix {
     __device__ __forceinline__ bool ok(const T* p, int count, uint32_t site) const {
         return check::in(p, (size_t)count * sizeof(T), ptr, elements * sizeof(T), site);
     }
-    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
-        const T* p = ptr + row * ld + col;
-        if (!ok(p, count, site)) return;
-        if (count == 8 && whole(p)) {
+    // Eight elements as they are stored.
+    struct Raw {
+        uint4 u[sizeof(T) / 2];
+        __device__ __forceinline__ void to(float (&v)[8]) const {
             if constexpr (sizeof(T) == 2) {
                 using P = Pair16<std::remove_const_t<T>>;
-                const uint4 u = *reinterpret_cast<const uint4*>(p);
-                const float2 a = P::unpack(u.x), b = P::unpack(u.y), c = P::unpack(u.z), d = P::unpack(u.w);
+                const float2 a = P::unpack(u[0].x), b = P::unpack(u[0].y), c = P::unpack(u[0].z), d = P::unpack(u[0].w);
                 v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
             } else {
-                const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            }
-            return;
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < count ? to_float(p[i]) : 0.f;
+                for (int i = 0; i < 2; ++i) {
+                    v[4 * i] = __uint_as_float(u[i].x), v[4 * i + 1] = __uint_as_float(u[i].y);
+                    v[4 * i + 2] = __uint_as_float(u[i].z), v[4 * i + 3] = __uint_as_float(u[i].w);
+                }
+            }
+        }
+    };
+    __device__ __forceinline__ Raw raw(int64_t row, int64_t col, int count, uint32_t site) const {
+        const T* p = ptr + row * ld + col;
+        Raw r;
+        if (!ok(p, count, site)) return r = Raw{};
+        if (count == 8 && whole(p)) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+            return r;
+        }
+        uint32_t* w = reinterpret_cast<uint32_t*>(r.u);
+        if constexpr (sizeof(T) == 2) {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a = 2 * i < count ? h[2 * i] : 0, b = 2 * i + 1 < count ? h[2 * i + 1] : 0;
+                w[i] = a | b << 16;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = i < count ? reinterpret_cast<const uint32_t*>(p)[i] : 0;
+        }
+        return r;
+    }
+    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
+        raw(row, col, count, site).to(v);
     }
     __device__ __forceinline__ void store(int64_t row, int64_t col, int count, const float (&v)[8], uint32_t site) const {
         T* p = ptr + row * ld + col;
