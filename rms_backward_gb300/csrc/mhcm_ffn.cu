@@ -135,23 +135,18 @@ size_t part(int64_t rows, int64_t cols) { return ((size_t)(rows * product::padde
 
 int steps_of(int64_t k) { return (int)((k + 63) / 64); }
 
-// A 16-bit operand [rows, cols] with rows that tensor maps can read: itself, or its copy in the workspace.
-struct Operand16 {
-    CUtensorMap map;
-    cudaError_t make(bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld) {
-        return encode_16bit_map(&map, bf16, p, rows, cols, ld) ? cudaSuccess : cudaErrorInvalidValue;
-    }
-    cudaError_t make(bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, Parts& ws, cudaStream_t stream) {
-        const int64_t wide = product::padded(cols);
-        if (wide == cols) return make(bf16, p, rows, cols, ld);
-        uint16_t* copy = static_cast<uint16_t*>(ws.take((size_t)(rows * wide) * 2));
-        const int64_t vectors = rows * (wide / 8);
-        const int64_t blocks = (vectors + 255) / 256;
-        const cudaError_t e = ops::launch_early(copy_rows_kernel, dim3((unsigned)(blocks < 2432 ? blocks : 2432)), dim3(256),
-                                                0, stream, static_cast<const uint16_t*>(p), ld, rows, cols, copy, wide);
-        return e != cudaSuccess ? e : make(bf16, copy, rows, cols, wide);
-    }
-};
+// A factor with rows that tensor maps can read: the matrix itself, or its copy in the workspace.
+cudaError_t make(product::Factor& f, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, Parts& ws,
+                 cudaStream_t stream) {
+    const int64_t wide = product::padded(cols);
+    if (wide == cols) return f.make(bf16, p, rows, cols, ld);
+    uint16_t* copy = static_cast<uint16_t*>(ws.take((size_t)(rows * wide) * 2));
+    const int64_t vectors = rows * (wide / 8);
+    const int64_t blocks = (vectors + 255) / 256;
+    const cudaError_t e = ops::launch_early(copy_rows_kernel, dim3((unsigned)(blocks < 2432 ? blocks : 2432)), dim3(256), 0,
+                                            stream, static_cast<const uint16_t*>(p), ld, rows, cols, copy, wide);
+    return e != cudaSuccess ? e : f.make(bf16, copy, rows, cols, wide);
+}
 
 template <class T>
 Matrix<T> matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
@@ -170,27 +165,27 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     const bool bf16 = a.type == MHCPB_BF16;
     Parts ws{static_cast<char*>(a.workspace)};
     void* hidden = ws.take((size_t)(T_ * Fp) * 2);
-    Operand16 x, wg, wu, wd, h;
-    MHCM_TRY(x.make(bf16, a.x, T_, D, a.x_stride, ws, stream));
-    MHCM_TRY(wg.make(bf16, a.w_gate, F, D, D, ws, stream));
-    MHCM_TRY(wu.make(bf16, a.w_up, F, D, D, ws, stream));
-    MHCM_TRY(wd.make(bf16, a.w_down, D, F, F, ws, stream));
+    product::Factor x, wg, wu, wd, h;
+    MHCM_TRY(make(x, bf16, a.x, T_, D, a.x_stride, ws, stream));
+    MHCM_TRY(make(wg, bf16, a.w_gate, F, D, D, ws, stream));
+    MHCM_TRY(make(wu, bf16, a.w_up, F, D, D, ws, stream));
+    MHCM_TRY(make(wd, bf16, a.w_down, D, F, F, ws, stream));
     MHCM_TRY(h.make(bf16, hidden, T_, F, Fp));
     Shape s{};
     s.bf16 = bf16;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
     const GatedEpilogue<T> gated{matrix<T>(hidden, T_, F, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
                                  a.activation};
-    MHCM_TRY(product::launch(s, gated, &x.map, nullptr, &wg.map, &wu.map, stream));
+    MHCM_TRY(product::launch(s, gated, &x, nullptr, &wg, &wu, stream));
     s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain;
     const StoreEpilogue<T> store{{matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
-    return product::launch(s, store, &h.map, nullptr, &wd.map, nullptr, stream);
+    return product::launch(s, store, &h, nullptr, &wd, nullptr, stream);
 }
 
 // dWd, or dWg and dWu together or one of them: C = A^T B over the tokens
 template <class O>
-cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const CUtensorMap* a0, const CUtensorMap* a1,
-                            const CUtensorMap* b, void* out0, void* out1, bool beside, cudaStream_t stream) {
+cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const product::Factor* a0, const product::Factor* a1,
+                            const product::Factor* b, void* out0, void* out1, bool beside, cudaStream_t stream) {
     Shape s{};
     s.bf16 = a.type == MHCPB_BF16;
     s.M = M, s.N = N, s.k_steps = steps_of(a.T), s.mode = mode;
@@ -207,13 +202,13 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     Parts ws{static_cast<char*>(a.workspace)};
     const size_t tf = (size_t)(T_ * Fp) * 2;
     void *hidden = ws.take(tf), *grad_gate = ws.take(tf), *grad_up = ws.take(tf);
-    Operand16 x, dy, wg, wu, wd, h, dg, du;
-    MHCM_TRY(dy.make(bf16, a.grad_y, T_, D, a.gy_stride, ws, stream));
-    MHCM_TRY(wd.make(bf16, a.w_down, D, F, F, ws, stream));
-    if (a.grad_w[0] || a.grad_w[1]) MHCM_TRY(x.make(bf16, a.x, T_, D, a.x_stride, ws, stream));
+    product::Factor x, dy, wg, wu, wd, h, dg, du;
+    MHCM_TRY(make(dy, bf16, a.grad_y, T_, D, a.gy_stride, ws, stream));
+    MHCM_TRY(make(wd, bf16, a.w_down, D, F, F, ws, stream));
+    if (a.grad_w[0] || a.grad_w[1]) MHCM_TRY(make(x, bf16, a.x, T_, D, a.x_stride, ws, stream));
     if (a.grad_x) {
-        MHCM_TRY(wg.make(bf16, a.w_gate, F, D, D, ws, stream));
-        MHCM_TRY(wu.make(bf16, a.w_up, F, D, D, ws, stream));
+        MHCM_TRY(make(wg, bf16, a.w_gate, F, D, D, ws, stream));
+        MHCM_TRY(make(wu, bf16, a.w_up, F, D, D, ws, stream));
     }
     MHCM_TRY(h.make(bf16, hidden, T_, F, Fp));
     MHCM_TRY(dg.make(bf16, grad_gate, T_, F, Fp));
@@ -225,7 +220,7 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.b_mn = 1;
     const GradEpilogue<T> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, F, Fp),
                                matrix<T>(grad_up, T_, F, Fp), matrix<T>(hidden, T_, F, Fp), a.activation};
-    MHCM_TRY(product::launch(s, grad, &dy.map, nullptr, &wd.map, nullptr, stream));
+    MHCM_TRY(product::launch(s, grad, &dy, nullptr, &wd, nullptr, stream));
     // The products that are left need only what the first wrote: each starts as soon as the one
     // before it leaves room (its last tiles keep a part of the GPU busy), not when that has ended.
     s.stall = 0;
@@ -233,20 +228,20 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     if (a.grad_x) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
         const StoreEpilogue<T> store{{matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
-        MHCM_TRY(product::launch(s, store, &dg.map, &du.map, &wg.map, &wu.map, stream));
+        MHCM_TRY(product::launch(s, store, &dg, &du, &wg, &wu, stream));
         beside = true;
     }
     if (a.grad_w[0] && a.grad_w[1]) {
-        MHCM_TRY(weight_gradient<O>(a, product::kGroups, F, D, &dg.map, &du.map, &x.map, a.grad_w[0], a.grad_w[1], beside,
+        MHCM_TRY(weight_gradient<O>(a, product::kGroups, F, D, &dg, &du, &x, a.grad_w[0], a.grad_w[1], beside,
                                     stream));
         beside = true;
     } else if (a.grad_w[0] || a.grad_w[1]) {
-        MHCM_TRY(weight_gradient<O>(a, product::kPlain, F, D, a.grad_w[0] ? &dg.map : &du.map, nullptr, &x.map,
+        MHCM_TRY(weight_gradient<O>(a, product::kPlain, F, D, a.grad_w[0] ? &dg : &du, nullptr, &x,
                                     a.grad_w[0] ? a.grad_w[0] : a.grad_w[1], nullptr, beside, stream));
         beside = true;
     }
     if (a.grad_w[2])
-        MHCM_TRY(weight_gradient<O>(a, product::kPlain, D, F, &dy.map, nullptr, &h.map, a.grad_w[2], nullptr, beside,
+        MHCM_TRY(weight_gradient<O>(a, product::kPlain, D, F, &dy, nullptr, &h, a.grad_w[2], nullptr, beside,
                                     stream));
     return cudaSuccess;
 }

@@ -7,9 +7,10 @@
 namespace mhcpb {
 
 // Tensor map over a 16-bit matrix [rows, cols], rows `ld` elements apart (a
-// multiple of 8; base 16-byte aligned): boxes of 64 x 64, 128-byte swizzle
-// (defined in mhcpb_api.cu).
-bool encode_16bit_map(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld);
+// multiple of 8; base 16-byte aligned): boxes of 64 columns and box_rows rows,
+// 128-byte swizzle (defined in mhcpb_api.cu).
+bool encode_16bit_map(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                      uint32_t box_rows);
 
 namespace product {
 
@@ -30,14 +31,40 @@ struct Shape {
                        // before it waited for): it does not wait for that one to end before its work, but
                        // before its own end, so that it still ends after it
     int stall;         // a test's: the MMA issuer waits for what nothing signals
-    // set by launch()
-    int m_tiles, n_tiles, tiles, split;
+    // set by choose()
+    int m_tiles, n_tiles, tiles;
+    int tile_n;        // columns of C per tile (of each product, side by side)
+    int split;         // blocks that share a tile's sum
+    int b_box;         // rows of B in one box, 0: boxes of 64
+    int stages, part_row, tmem_columns;   // single blocks: see product_kernel
+    uint32_t b_bytes;
 };
 struct Choice {
     bool pair;
-    int m_tiles, n_tiles, tiles, split, grid;
+    int grid;
+    uint32_t smem;     // of a single block
 };
-Choice choose(const Shape& s);
+Choice choose(Shape& s);
+
+constexpr int kBox = 64;                           // columns, and mostly rows, of a box
+constexpr uint32_t kBoxBytes = kBox * kBox * 2;    // 8 KiB
+constexpr int kMaxStages = 8;
+constexpr uint32_t kSharedMost = 232448;           // per block; two blocks share 233,472 with 1 KiB each for the system
+
+// A 16-bit factor of a product, and its map with boxes of 64 rows.
+struct Factor {
+    CUtensorMap map;
+    const void* ptr;
+    int64_t rows, cols, ld;
+    bool bf16;
+    bool encode(CUtensorMap* m, int box_rows) const {
+        return encode_16bit_map(m, bf16, ptr, rows, cols, ld, (uint32_t)box_rows);
+    }
+    cudaError_t make(bool is_bf16, const void* p, int64_t r, int64_t c, int64_t distance) {
+        ptr = p, rows = r, cols = c, ld = distance, bf16 = is_bf16;
+        return encode(&map, kBox) ? cudaSuccess : cudaErrorInvalidValue;
+    }
+};
 
 inline int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
 

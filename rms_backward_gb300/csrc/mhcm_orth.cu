@@ -317,34 +317,34 @@ cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
     const Matrix<const __half> gram_in{gram.ptr, gram.ld, gram.elements};
     const Matrix<float> x{reinterpret_cast<float*>(ws + l.x), np, (size_t)((m - 1) * np + n)};
     const Matrix<__nv_bfloat16> out{static_cast<__nv_bfloat16*>(a.out), a.out_stride, (size_t)((m - 1) * a.out_stride + n)};
-    CUtensorMap map_x[2], map_gram, map_poly;
-    if (!encode_16bit_map(&map_x[0], false, copies[0].ptr, m, n, np) ||
-        !encode_16bit_map(&map_x[1], false, copies[1].ptr, m, n, np) ||
-        !encode_16bit_map(&map_gram, false, gram.ptr, s, s, sp) || !encode_16bit_map(&map_poly, false, poly.ptr, s, s, sp))
-        return cudaErrorInvalidValue;
+    product::Factor factor_x[2], factor_gram, factor_poly;
+    MHCM_TRY(factor_x[0].make(false, copies[0].ptr, m, n, np));
+    MHCM_TRY(factor_x[1].make(false, copies[1].ptr, m, n, np));
+    MHCM_TRY(factor_gram.make(false, gram.ptr, s, s, sp));
+    MHCM_TRY(factor_poly.make(false, poly.ptr, s, s, sp));
 
     const int64_t units = m * ((n + 7) / 8), blocks = (units + kNormThreads - 1) / kNormThreads;
     MHCM_TRY(ops::launch_early(squares_kernel, dim3(kNormBlocks), dim3(kNormThreads), 0, stream, g, partial));
     MHCM_TRY(ops::launch_early(first_copy_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(kNormThreads), 0,
                                stream, g, static_cast<const double*>(partial), static_cast<double>(a.eps), inverse, copies[0]));
     for (int i = 0; i < a.steps; ++i) {
-        const CUtensorMap* cur = &map_x[i & 1];
+        const product::Factor* cur = &factor_x[i & 1];
         Shape p{};
         p.mode = product::kSymmetric;
         p.M = p.N = s, p.k_steps = steps_of(tall ? m : n), p.a_mn = p.b_mn = tall;
         MHCM_TRY(product::launch(p, GramEpilogue{gram, gram_lost}, cur, nullptr, cur, nullptr, stream));
         p.k_steps = steps_of(s), p.a_mn = p.b_mn = 0;
         const PolynomialEpilogue polynomial{poly, gram_in, gram_lost, poly_lost};
-        MHCM_TRY(product::launch(p, polynomial, &map_gram, nullptr, &map_gram, nullptr, stream));
+        MHCM_TRY(product::launch(p, polynomial, &factor_gram, nullptr, &factor_gram, nullptr, stream));
         p.mode = product::kPlain;
         p.M = m, p.N = n, p.k_steps = steps_of(s), p.b_mn = !tall;
         const bool last = i + 1 == a.steps;
         const UpdateEpilogue update{g, i == 0 ? inverse : nullptr, poly_lost, tall, x, copies[(i + 1) & 1],
                                     last ? out : Matrix<__nv_bfloat16>{nullptr, 0, 0}, a.scale};
         if (tall)
-            MHCM_TRY(product::launch(p, update, cur, nullptr, &map_poly, nullptr, stream));
+            MHCM_TRY(product::launch(p, update, cur, nullptr, &factor_poly, nullptr, stream));
         else
-            MHCM_TRY(product::launch(p, update, &map_poly, nullptr, cur, nullptr, stream));
+            MHCM_TRY(product::launch(p, update, &factor_poly, nullptr, cur, nullptr, stream));
     }
     return cudaSuccess;
 }

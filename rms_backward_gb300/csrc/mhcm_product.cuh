@@ -15,11 +15,13 @@
 //    operands per 64 k and block, 64 bytes per clock and SM at the full MMA rate.
 //    Two accumulators in TMEM (all 512 columns), so the epilogue of one tile runs
 //    under the products of the next.
-//  * single blocks, 128 x 128 tiles, a cluster of `split` blocks that share the
-//    sum over k of one tile and add their parts, in rank order, through
-//    distributed shared memory: for outputs of few tiles (few tokens, few rows).
+//  * single blocks, tiles of 128 rows and up to 256 columns, one or two blocks per
+//    SM, and clusters of `split` blocks that share the sum over k of one tile and
+//    add their parts, in rank order, through distributed shared memory: for outputs
+//    of few tiles (few tokens, few rows).  Where B's rows are k its rows per tile
+//    are chosen (with the split) to give every SM the same share of B.
 //
-// Warp roles: 0 copies (TMA), 1 MMA issue, 2 TMEM, 4..11 epilogue.  Every wait is
+// Warp roles: 0 copies (TMA), 1 MMA issue, 2 TMEM, 4.. epilogue (eight, or four).  Every wait is
 // bounded; a wait that runs out records a status word, and the block drains its
 // copies and MMAs and leaves.
 #pragma once
@@ -38,33 +40,28 @@ namespace product {
 
 static __device__ uint32_t g_status;   // kDevOk or kDevTimeout, of this translation unit's kernels
 
-constexpr int kBox = 64;                           // box side
-constexpr uint32_t kBoxBytes = kBox * kBox * 2;    // 8 KiB
-constexpr uint32_t kStageBytes = 4 * kBoxBytes;    // 128 rows of A, 128 of B, 64 k
-constexpr int kThreads = 384;
-constexpr int kEpilogueWarp = 4;                   // the first of eight
+constexpr uint32_t kPairStage = 4 * kBoxBytes;     // 128 rows of A, 128 of B, 64 k
+constexpr int kEpilogueWarp = 4;                   // the first one
 constexpr uint64_t kWaitNs = 1000000000ull;        // 1 s
 
+// PAIR: compile-time layout.  Single blocks: the number of stages and a tile's columns are the launch's.
 template <bool PAIR>
 struct Cfg {
     static constexpr int blocks = PAIR ? 2 : 1;
-    static constexpr int tile_m = 128 * blocks, tile_n = 128 * blocks;
-    static constexpr int stages = PAIR ? 5 : 6;
+    static constexpr int threads = PAIR ? 384 : 256;
+    static constexpr int tile_m = 128 * blocks;
+    static constexpr int stages = PAIR ? 5 : kMaxStages;
     static constexpr int accumulators = PAIR ? 2 : 1;
-    static constexpr uint32_t tmem_columns = tile_n * accumulators;
-    // PAIR: 32 rows of 32 FP32 per epilogue warp, 36 apart (vectors without bank conflicts).
-    // Single blocks: the whole accumulator, rows 132 apart, over the (then idle) stages.
-    static constexpr int row = PAIR ? 36 : 132;
+    // PAIR: 32 rows of 32 FP32 per epilogue warp, 36 apart (vectors without bank conflicts), behind the stages.
+    static constexpr int row = 36;
     static constexpr uint32_t scratch = PAIR ? 8 * 32 * row * 4 : 0;
-    static constexpr uint32_t off_scratch = PAIR ? stages * kStageBytes : 0;
-    static constexpr uint32_t off_bar = stages * kStageBytes + scratch;
-    // barriers: full[stages] empty[stages] done[2] free[2] last
+    // barriers (at the front): full[stages] empty[stages] done[2] free[2] last; then TMEM's address and the abort flag
     static constexpr int b_full = 0, b_empty = stages, b_done = 2 * stages, b_free = 2 * stages + 2,
                          b_last = 2 * stages + 4, bars = 2 * stages + 5;
-    static constexpr uint32_t off_misc = off_bar + bars * 8;
-    static constexpr uint32_t smem = off_misc + 16 + 1024;   // and room to align the base to 1 KiB
-    static_assert(smem <= 232448, "shared memory budget");
-    static_assert(PAIR || 128 * row * 4 <= stages * kStageBytes, "the accumulator fits the stages");
+    static constexpr uint32_t off_misc = bars * 8, off_stages = 1024;
+    static_assert(off_misc + 8 <= off_stages, "the barriers' part");
+    static constexpr uint32_t smem = PAIR ? 1024 + off_stages + stages * kPairStage + scratch : 0;   // 1 KiB to align
+    static_assert(smem <= kSharedMost, "shared memory budget");
 };
 
 // Which rows and columns of C a tile has.
@@ -72,7 +69,7 @@ struct Tile {
     int group, m, n;   // first row and column; of each of the two products where two are formed side by side
     bool mirror;       // symmetric C: the tile is also written transposed
 };
-template <int TILE_M, int TILE_N>
+template <int TILE_M>
 __device__ __forceinline__ Tile tile_at(const Shape& s, int t) {
     Tile r;
     r.group = 0;
@@ -85,7 +82,7 @@ __device__ __forceinline__ Tile tile_at(const Shape& s, int t) {
             ++i;
         }
         r.m = i * TILE_M;
-        r.n = (i + t) * TILE_N;
+        r.n = (i + t) * s.tile_n;
         r.mirror = t > 0;
         return r;
     }
@@ -99,7 +96,7 @@ __device__ __forceinline__ Tile tile_at(const Shape& s, int t) {
     const int rows = min(8, s.m_tiles - first);
     t -= band * 8 * s.n_tiles;
     r.m = (first + t % rows) * TILE_M;
-    r.n = (t / rows) * (s.mode == kSideBySide ? TILE_N / 2 : TILE_N);
+    r.n = (t / rows) * s.tile_n;
     return r;
 }
 
@@ -125,6 +122,12 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
     return wait_slow<CLUSTER>(bar, parity, abort_flag, honor);
 }
 
+// wait by a whole warp: true where every lane's was
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+    return __all_sync(0xFFFFFFFFu, wait<CLUSTER>(bar, parity, abort_flag));
+}
+
 // Epilogue: struct with
 //   static constexpr bool kDual                    two products side by side
 //   struct Read                                    what an element's result needs from memory
@@ -134,19 +137,24 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
 // for `count` (1..8) elements of one row of C; w: the second product's (kDual).
 // Several reads are under way before the first write.
 template <bool PAIR, class Epilogue>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
     product_kernel(const Shape s, const Epilogue epi, const __grid_constant__ CUtensorMap a0,
                    const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b0,
                    const __grid_constant__ CUtensorMap b1) {
     using C = Cfg<PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const uint32_t base = ptx::smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = ptx::smem_u32(smem), stage0 = base + C::off_stages;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_rank();
     uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::off_misc);
     volatile uint32_t* abort_flag = holder + 1;
-    auto bar = [&](int i) { return base + C::off_bar + 8u * (uint32_t)i; };
+    auto bar = [&](int i) { return base + 8u * (uint32_t)i; };
+    // columns of the accumulator (of both products side by side), stages and what one holds
+    const uint32_t width = PAIR ? 256 : (uint32_t)(s.mode == kSideBySide ? 2 * s.tile_n : s.tile_n);
+    const uint32_t stages = PAIR ? C::stages : (uint32_t)s.stages;
+    const uint32_t stage_bytes = PAIR ? kPairStage : 2 * kBoxBytes + s.b_bytes;
+    const uint32_t tmem_columns = PAIR ? 512 : (uint32_t)s.tmem_columns;
 
     if (threadIdx.x == 0) {
         *abort_flag = 0u;
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tensormap(&a0);
         ptx::prefetch_tensormap(&b0);
     }
-    if (warp == 2) ptx::tmem_get<PAIR>(ptx::smem_u32(holder), C::tmem_columns);
+    if (warp == 2) ptx::tmem_get<PAIR>(ptx::smem_u32(holder), tmem_columns);
     ptx::tc_fence_before();
     ptx::cluster_arrive();   // the pair's barriers are there before either block uses them
     ptx::cluster_wait();
@@ -180,89 +188,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int k_end = PAIR ? steps : (int)((int64_t)(rank + 1) * steps / s.split);
     const bool leader = !PAIR || rank == 0;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         const uint32_t half = PAIR ? rank : 0;
-        uint32_t n = 0;                                      // steps so far
+        uint32_t st = 0, ph = 0, n = 0;                      // stage, its turn's parity, steps so far
         bool ok = true;
         for (int t = first_tile; ok && t < s.tiles; t += step_tile) {
-            const Tile tile = tile_at<C::tile_m, C::tile_n>(s, t);
+            const Tile tile = tile_at<C::tile_m>(s, t);
             const int m0 = tile.m + (int)half * 128;
             const int n0 = tile.n + (s.mode == kSideBySide ? 0 : (int)half * 128);
+            // (a single block leaves out the half of A's rows that no token has: their results are not read)
+            const int a_boxes = !PAIR && s.M - tile.m <= kBox ? 1 : 2;
+            const uint32_t bytes = PAIR ? 2 * kPairStage : a_boxes * kBoxBytes + s.b_bytes;
             for (int k = k_begin; k < k_end; ++k, ++n) {
-                const uint32_t st = n % C::stages, ph = (n / C::stages) & 1u;
-                if (!wait<PAIR>(bar(C::b_empty + st), ph ^ 1u, abort_flag)) {
+                if (!wait_all<PAIR>(bar(C::b_empty + st), ph ^ 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
                 const uint32_t full = PAIR ? ptx::map_rank(bar(C::b_full + st), 0) : bar(C::b_full + st);
-                if (leader) ptx::mbar_arrive_expect_tx(bar(C::b_full + st), C::blocks * kStageBytes);
+                if (leader) ptx::mbar_expect_one(bar(C::b_full + st), bytes);
                 const bool second = s.mode == kLongK && k >= s.k_steps;
                 const int k0 = (second ? k - s.k_steps : k) * kBox;
                 const CUtensorMap* am = second || tile.group ? &a1 : &a0;
                 const CUtensorMap* bm = second || tile.group ? &b1 : &b0;
-                const uint32_t dst = base + st * kStageBytes;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int m = m0 + kBox * j;
-                    ptx::tma_load_tile<PAIR>(dst + j * kBoxBytes, am, s.a_mn ? m : k0, s.a_mn ? k0 : m, full);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                const uint32_t dst = stage0 + st * stage_bytes, dst_b = dst + 2 * kBoxBytes;
+                ptx::tma_load_one<PAIR>(dst, am, s.a_mn ? m0 : k0, s.a_mn ? k0 : m0, full);
+                if (a_boxes == 2)
+                    ptx::tma_load_one<PAIR>(dst + kBoxBytes, am, s.a_mn ? m0 + kBox : k0, s.a_mn ? k0 : m0 + kBox, full);
+                if (!PAIR && s.b_box != 0) {   // all of a product's rows in one box
+                    ptx::tma_load_one<PAIR>(dst_b, bm, k0, n0, full);
+                    if (s.mode == kSideBySide)
+                        ptx::tma_load_one<PAIR>(dst_b + (uint32_t)s.tile_n * (kBox * 2), &b1, k0, n0, full);
+                } else {
                     // side by side: a block of a pair has one product's rows, a single block 64 of each
-                    const bool other = s.mode == kSideBySide && (PAIR ? half == 1 : j == 1);
-                    const int nn = n0 + (s.mode == kSideBySide && !PAIR ? 0 : kBox * j);
-                    ptx::tma_load_tile<PAIR>(dst + (2 + j) * kBoxBytes, other ? &b1 : bm, s.b_mn ? nn : k0,
-                                             s.b_mn ? k0 : nn, full);
+                    const bool side = s.mode == kSideBySide;
+                    const int n1 = side && !PAIR ? n0 : n0 + kBox;
+                    const CUtensorMap* b_first = side && PAIR && half == 1 ? &b1 : bm;
+                    const CUtensorMap* b_second = side && (!PAIR || half == 1) ? &b1 : bm;
+                    ptx::tma_load_one<PAIR>(dst_b, b_first, s.b_mn ? n0 : k0, s.b_mn ? k0 : n0, full);
+                    ptx::tma_load_one<PAIR>(dst_b + kBoxBytes, b_second, s.b_mn ? n1 : k0, s.b_mn ? k0 : n1, full);
                 }
+                if (++st == stages) st = 0, ph ^= 1u;
             }
         }
         if (!ok && leader)   // the copies that were started end before the block does
-            for (uint32_t i = n > C::stages ? n - C::stages : 0; i < n; ++i)
-                wait<PAIR>(bar(C::b_full + i % C::stages), (i / C::stages) & 1u, abort_flag, false);
-    } else if (warp == 1 && lane == 0 && leader) {
-        const uint32_t idesc = ptx::idesc_16bit(C::tile_m, C::tile_n, s.bf16, s.a_mn, s.b_mn);
-        // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes
-        const uint32_t a_step = s.a_mn ? 2048 : 32, b_step = s.b_mn ? 2048 : 32;
-        const uint64_t shape = ptx::smem_desc(0, kBoxBytes, 1024, ptx::kLayoutSwizzle128B);
-        uint32_t n = 0, done = 0;
+            for (uint32_t i = n > stages ? n - stages : 0; i < n; ++i)
+                wait<PAIR>(bar(C::b_full + i % stages), (i / stages) & 1u, abort_flag, false);
+    } else if (warp == 1 && leader) {
+        const uint32_t idesc = ptx::idesc_16bit(C::tile_m, width, s.bf16, s.a_mn, s.b_mn);
+        // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes (in descriptors' units of 16)
+        const uint64_t a_step = s.a_mn ? 128 : 2, b_step = s.b_mn ? 128 : 2;
+        const uint64_t first = ptx::smem_desc(stage0, kBoxBytes, 1024, ptx::kLayoutSwizzle128B);
+        uint32_t st = 0, ph = 0, done = 0;
         bool ok = true;
         for (int t = first_tile; ok && t < s.tiles; t += step_tile, ++done) {
             const uint32_t acc = done % C::accumulators, turn = done / C::accumulators;
-            if (!wait<PAIR>(bar(C::b_free + acc), (turn & 1u) ^ 1u, abort_flag)) {
+            if (!wait_all<PAIR>(bar(C::b_free + acc), (turn & 1u) ^ 1u, abort_flag)) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            const uint32_t d = tmem + acc * C::tile_n;
-            if (s.stall && !wait<PAIR>(bar(C::b_last), 0u, abort_flag)) {   // a test's wait that nothing ends
+            const uint32_t d = tmem + acc * width;
+            if (s.stall && !wait_all<PAIR>(bar(C::b_last), 0u, abort_flag)) {   // a test's wait that nothing ends
                 ok = false;
                 break;
             }
-            for (int k = k_begin; k < k_end; ++k, ++n) {
-                const uint32_t st = n % C::stages, ph = (n / C::stages) & 1u;
-                if (!wait<PAIR>(bar(C::b_full + st), ph, abort_flag)) {
+            for (int k = k_begin; k < k_end; ++k) {
+                if (!wait_all<PAIR>(bar(C::b_full + st), ph, abort_flag)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t a = base + st * kStageBytes, b = a + 2 * kBoxBytes;
-#pragma unroll
-                for (int q = 0; q < kBox / 16; ++q)
-                    ptx::mma_f16<PAIR>(d, shape | (((a + q * a_step) >> 4) & 0x3FFFu),
-                                       shape | (((b + q * b_step) >> 4) & 0x3FFFu), idesc, k > k_begin || q > 0);
-                ptx::mma_commit<PAIR>(bar(C::b_empty + st), 3);
+                const uint64_t a = first + ((st * stage_bytes) >> 4);
+                ptx::mma64_one<PAIR>(d, a, a + (2 * kBoxBytes >> 4), idesc, a_step, b_step, k > k_begin);
+                ptx::mma_commit_one<PAIR>(bar(C::b_empty + st), 3);
+                if (++st == stages) st = 0, ph ^= 1u;
             }
-            if (ok) ptx::mma_commit<PAIR>(bar(C::b_done + acc), 3);
+            if (ok) ptx::mma_commit_one<PAIR>(bar(C::b_done + acc), 3);
         }
         if (!ok) {           // the MMAs that were issued end before the block does
-            ptx::mma_commit<PAIR>(bar(C::b_last), 1);
+            ptx::mma_commit_one<PAIR>(bar(C::b_last), 1);
             wait<PAIR>(bar(C::b_last), 0u, abort_flag, false);
         }
     } else if (warp >= kEpilogueWarp) {
-        const int quad = warp & 3, half = (warp - kEpilogueWarp) >> 2;
+        const int quad = warp & 3, half = (warp - kEpilogueWarp) >> 2;   // half: 0 where there are four warps
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         if constexpr (PAIR) {
-            float* scratch = reinterpret_cast<float*>(smem + C::off_scratch) + (warp - kEpilogueWarp) * 32 * C::row;
+            float* scratch = 
+                reinterpret_cast<float*>(smem + C::off_stages + C::stages * kPairStage) + (warp - kEpilogueWarp) * 32 * C::row;
             // 32 columns of this warp's 32 rows into v[q]: row 8 q + lane / 4, columns 8 (lane % 4) ..
             auto fetch = [&](uint32_t column, float (&v)[4][8]) {
                 uint32_t u[32];
@@ -284,9 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t done = 0;
             for (int t = first_tile; t < s.tiles; t += step_tile, ++done) {
                 const uint32_t acc = done & 1u;
-                const Tile tile = tile_at<C::tile_m, C::tile_n>(s, t);
+                const Tile tile = tile_at<C::tile_m>(s, t);
                 const int64_t row0 = tile.m + (int64_t)rank * 128 + quad * 32;
-                const uint32_t d = acc * C::tile_n;
+                const uint32_t d = acc * width;
                 constexpr int kChunks = Epilogue::kDual ? 2 : 4;   // of 32 columns per warp
                 bool ok = true;
 #pragma unroll 1
@@ -311,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (c == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, wait<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag));
+                        ok = wait_all<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag);
                         if (!ok) break;
                         ptx::tc_fence_after();
                     }
@@ -343,21 +355,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
             }
-        } else if (__all_sync(0xFFFFFFFFu, wait<PAIR>(bar(C::b_done), 0u, abort_flag))) {
+        } else if (wait_all<PAIR>(bar(C::b_done), 0u, abort_flag)) {
             ptx::tc_fence_after();
-            float* part = reinterpret_cast<float*>(smem + C::off_scratch);
+            float* part = reinterpret_cast<float*>(smem + C::off_stages);   // over the (now idle) stages
             const int row = quad * 32 + lane;
+            if (quad * 32 < s.M - tile_at<C::tile_m>(s, first_tile).m)
+                for (int c = 0; c < (int)width; c += 32) {
+                    uint32_t u[32];
+                    ptx::tmem_ld_32x32b_x32(lanes + c, u);
+                    ptx::tc_wait_ld_regs(u);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t u[32];
-                const int column = half * 64 + c * 32;
-                ptx::tmem_ld_32x32b_x32(lanes + column, u);
-                ptx::tc_wait_ld_regs(u);
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<uint4*>(part + row * C::row + column + i) =
-                        make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
-            }
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(part + row * s.part_row + c + i) =
+                            make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                }
         }
     }
 
@@ -367,26 +378,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_wait();
     ptx::tc_fence_after();
     __syncwarp();
-    if (warp == 2) ptx::tmem_free<PAIR>(tmem, C::tmem_columns);
+    if (warp == 2) ptx::tmem_free<PAIR>(tmem, tmem_columns);
 
     if constexpr (!PAIR) {
         // Every block has its part of the tile in shared memory; each adds up its share of the vectors.
-        const Tile tile = tile_at<C::tile_m, C::tile_n>(s, first_tile);
-        const uint32_t part = base + C::off_scratch;
-        constexpr int kWidth = Epilogue::kDual ? 64 : 128;
-        const int rows = (int)min((int64_t)128, s.M - tile.m), cols = (int)min((int64_t)kWidth, s.N - tile.n);
+        const Tile tile = tile_at<C::tile_m>(s, first_tile);
+        const int rows = (int)min((int64_t)128, s.M - tile.m), cols = (int)min((int64_t)s.tile_n, s.N - tile.n);
         auto gather = [&](int r, int c, float (&v)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = 0.f;
             for (int z = 0; z < s.split; ++z) {
-                const uint32_t p = ptx::map_rank(part + (uint32_t)(r * C::row + c) * 4, z);
+                const uint32_t p = ptx::map_rank(stage0 + (uint32_t)(r * s.part_row + c) * 4, z);
                 const float4 x = ptx::ld_cluster_f32x4(p), y = ptx::ld_cluster_f32x4(p + 16);
                 v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
                 v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
             }
         };
         // Four vectors per thread at a time: their reads and the parts' are all under way before the first write.
-        const int threads = s.split * kThreads, me = (int)rank * kThreads + threadIdx.x;
+        const int threads = s.split * C::threads, me = (int)rank * C::threads + threadIdx.x;
         const int across = (cols + 7) / 8, units = rows * across;
         for (int first = me; first < units; first += 4 * threads) {
             typename Epilogue::Read read[4];
@@ -401,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
                 if (u >= units) break;
                 gather(r, c, v[q]);
-                if constexpr (Epilogue::kDual) gather(r, 64 + c, w[q]);
+                if constexpr (Epilogue::kDual) gather(r, s.tile_n + c, w[q]);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -428,9 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[q][i] = 0.f;
                     for (int z = 0; z < s.split; ++z) {
-                        const uint32_t p = ptx::map_rank(part + (uint32_t)(8 * g * C::row + c) * 4, z);
+                        const uint32_t p = ptx::map_rank(stage0 + (uint32_t)(8 * g * s.part_row + c) * 4, z);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[q][i] += ptx::ld_cluster_f32(p + i * C::row * 4);
+                        for (int i = 0; i < 8; ++i) v[q][i] += ptx::ld_cluster_f32(p + i * s.part_row * 4);
                     }
                 }
 #pragma unroll
@@ -452,37 +461,37 @@ template <class Epilogue>
 cudaError_t allow() {
     static std::atomic<uint64_t> pair{0}, single{0};
     cudaError_t e = ops::allow_shared(product_kernel<true, Epilogue>, (int)Cfg<true>::smem, pair);
-    return e != cudaSuccess ? e : ops::allow_shared(product_kernel<false, Epilogue>, (int)Cfg<false>::smem, single);
+    return e != cudaSuccess ? e : ops::allow_shared(product_kernel<false, Epilogue>, (int)kSharedMost, single);
 }
 
 // a1 and b1 may be null where the mode has one A or B.
 template <class Epilogue>
-cudaError_t launch(Shape s, const Epilogue& epi, const CUtensorMap* a0, const CUtensorMap* a1, const CUtensorMap* b0,
-                   const CUtensorMap* b1, cudaStream_t stream) {
+cudaError_t launch(Shape s, const Epilogue& epi, const Factor* a0, const Factor* a1, const Factor* b0, const Factor* b1,
+                   cudaStream_t stream) {
     cudaError_t e = allow<Epilogue>();
     if (e != cudaSuccess) return e;
     const Choice c = choose(s);
-    s.m_tiles = c.m_tiles;
-    s.n_tiles = c.n_tiles;
-    s.tiles = c.tiles;
-    s.split = c.split;
+    const CUtensorMap *mb0 = &b0->map, *mb1 = b1 ? &b1->map : mb0, *ma0 = &a0->map, *ma1 = a1 ? &a1->map : ma0;
+    CUtensorMap own[2];
+    if (s.b_box != 0) {   // boxes of as many rows as a tile takes
+        if (!b0->encode(&own[0], s.b_box) || (b1 && !b1->encode(&own[1], s.b_box))) return cudaErrorInvalidValue;
+        mb0 = &own[0], mb1 = b1 ? &own[1] : &own[0];
+    }
     cudaLaunchConfig_t config{};
     cudaLaunchAttribute attr[2]{};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = c.pair ? 2 : (unsigned)c.split;
+    attr[1].val.clusterDim.x = c.pair ? 2 : (unsigned)s.split;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     config.attrs = attr;
     config.numAttrs = 2;
-    config.blockDim = kThreads;
+    config.blockDim = c.pair ? Cfg<true>::threads : Cfg<false>::threads;
     config.gridDim = (unsigned)c.grid;
-    config.dynamicSmemBytes = c.pair ? Cfg<true>::smem : Cfg<false>::smem;
+    config.dynamicSmemBytes = c.pair ? Cfg<true>::smem : c.smem;
     config.stream = stream;
-    if (a1 == nullptr) a1 = a0;
-    if (b1 == nullptr) b1 = b0;
-    return c.pair ? cudaLaunchKernelEx(&config, product_kernel<true, Epilogue>, s, epi, *a0, *a1, *b0, *b1)
-                  : cudaLaunchKernelEx(&config, product_kernel<false, Epilogue>, s, epi, *a0, *a1, *b0, *b1);
+    return c.pair ? cudaLaunchKernelEx(&config, product_kernel<true, Epilogue>, s, epi, *ma0, *ma1, *mb0, *mb1)
+                  : cudaLaunchKernelEx(&config, product_kernel<false, Epilogue>, s, epi, *ma0, *ma1, *mb0, *mb1);
 }
 
 // This translation unit's status word, then cleared if asked (current device).

@@ -53,20 +53,36 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
+// The wrappers below whose name ends in _one are called by a whole warp with the
+// same arguments in every lane, and issue their instructions in one lane (always the
+// same: elect.sync is deterministic).  So the operands stay in uniform registers; under
+// a branch on the lane number each TMA or tcgen05 instruction costs some 200 clocks.
+__device__ __forceinline__ void mbar_expect_one(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
 // 2-D tiled load into this block's shared memory, counted on `bar`: with PAIR a
 // barrier of either block of the pair (a shared::cluster address).
 template <bool PAIR>
-__device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+__device__ __forceinline__ void tma_load_one(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
     if constexpr (PAIR)
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "{\n\t.reg .pred q;\n\t"
+            "elect.sync _|q, 0xFFFFFFFF;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "{\n\t.reg .pred q;\n\t"
+            "elect.sync _|q, 0xFFFFFFFF;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
             : "memory");
 }
@@ -91,31 +107,50 @@ __device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t columns) {
         tmem_dealloc(taddr, columns);
 }
 
-// D[tmem] (+)= A[smem] B[smem], 16-bit operands, FP32 accumulation.
+// D[tmem] (+)= A[smem] B[smem] over 64 k: four MMAs of 16-bit operands with FP32
+// accumulation, the descriptors a_step and b_step apart.
+#define MHCM_MMA64(GROUP)                                                                      \
+    asm volatile(                                                                              \
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 x, y;\n\t"                                     \
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"                                                     \
+        "setp.ne.b32 p, %6, 0;\n\t"                                                           \
+        "setp.eq.b32 t, 0, 0;\n\t"                                                            \
+        "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], %1, %2, %3, p;\n\t"               \
+        "add.s64 x, %1, %4;\n\tadd.s64 y, %2, %5;\n\t"                                       \
+        "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], x, y, %3, t;\n\t"                 \
+        "add.s64 x, x, %4;\n\tadd.s64 y, y, %5;\n\t"                                         \
+        "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], x, y, %3, t;\n\t"                 \
+        "add.s64 x, x, %4;\n\tadd.s64 y, y, %5;\n\t"                                         \
+        "@q tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),      \
+        "l"(a), "l"(b), "r"(idesc), "l"(a_step), "l"(b_step), "r"(accumulate)                  \
+        : "memory")
 template <bool PAIR>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma64_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t a_step,
+                                          uint64_t b_step, uint32_t accumulate) {
     if constexpr (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-            : "memory");
+        MHCM_MMA64("2");
     else
-        mma_bf16(d, a, b, idesc, accumulate);
+        MHCM_MMA64("1");
 }
-// One arrival, when this thread's MMAs so far are done, on the barrier at this
+#undef MHCM_MMA64
+// One arrival, when this warp's MMAs so far are done, on the barrier at this
 // offset in each block whose bit is set in `mask` (without PAIR: in this block).
 template <bool PAIR>
-__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t mask) {
+__device__ __forceinline__ void mma_commit_one(uint32_t bar, uint16_t mask) {
     if constexpr (PAIR)
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                bar),
+            "{\n\t.reg .pred q;\n\t"
+            "elect.sync _|q, 0xFFFFFFFF;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            "\n\t}" ::"r"(bar),
             "h"(mask)
             : "memory");
     else
-        tc_commit(bar);
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "elect.sync _|q, 0xFFFFFFFF;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+            : "memory");
 }
 
 // Instruction descriptor of kind::f16 with FP32 accumulators: as idesc_bf16_f32,

@@ -163,12 +163,13 @@ const char* encode_tc_maps(CUtensorMap (&m)[6], int64_t T, int64_t K, const void
                            const void* r) {
     return encode_maps(m, T, K, x, dx, add, gp, gr, r);
 }
-bool encode_16bit_map(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld) {
+bool encode_16bit_map(CUtensorMap* m, bool bf16, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                      uint32_t box_rows) {
     EncodeTiledFn enc = get_encode();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, 64};
+    const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
