@@ -12,6 +12,7 @@
 // are rounded to the operands' 16-bit type; everything else is FP32 until the
 // output is stored.  Rows that are not a multiple of 8 elements long are copied
 // to rows that are (the tensor maps' 16-byte rule).
+#include "mhcm_ffn.cuh"
 #include "mhcm_product.cuh"
 
 namespace mhcpb {
@@ -21,16 +22,6 @@ namespace {
 
 using product::Matrix;
 using product::Shape;
-
-// act(g) and act'(g)
-__device__ __forceinline__ float2 activate(float g, int kind) {
-    if (kind == MHCPB_SILU) {
-        const float q = __frcp_rn(1.f + __expf(-g));   // (__fdividef gives 0 beyond 2^126)
-        return make_float2(g * q, q * (1.f + g * (1.f - q)));
-    }
-    const float p = 0.5f * erfcf(g * -0.70710678f);   // the normal distribution function, accurate in its tail
-    return make_float2(g * p, p + g * (0.39894228f * __expf(-0.5f * g * g)));
-}
 
 template <class T>
 struct GatedEpilogue {
@@ -250,6 +241,7 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
 
 size_t forward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
     size_t n = part(T, F);
+    if (few_tokens(T, D, F)) return n;
     if (D % 8) n += part(T, D) + 2 * part(F, D);
     if (F % 8) n += part(D, F);
     return n;
@@ -263,6 +255,7 @@ size_t backward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
 }
 
 cudaError_t forward(const Args& a, cudaStream_t stream) {
+    if (few_tokens(a.T, a.D, a.F)) return few_tokens_forward(a, stream);
     return a.type == MHCPB_BF16 ? forward_as<__nv_bfloat16>(a, stream) : forward_as<__half>(a, stream);
 }
 
@@ -288,7 +281,12 @@ cudaError_t setup() {
     MHCM_TRY(product::allow<StoreEpilogue<__half>>());
     return product::allow<StoreEpilogue<float>>();
 }
-cudaError_t checked_site(uint32_t* site) { return check::read_and_clear(site); }
+cudaError_t checked_site(uint32_t* site) {
+    uint32_t other = 0;
+    const cudaError_t e = check::read_and_clear(site), f = few_tokens_site(&other);
+    if (*site == 0) *site = other;
+    return e != cudaSuccess ? e : f;
+}
 cudaError_t device_status(uint32_t* status, bool clear) { return product::read_status(status, clear); }
 
 }  // namespace ffn

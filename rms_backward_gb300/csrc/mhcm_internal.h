@@ -88,6 +88,10 @@ struct Args {
     bool accumulate, stall;
     void* workspace;
 };
+// few tokens (mhcm_token.cu): whether the sizes are taken, and the forward
+bool few_tokens(int64_t T, int64_t D, int64_t F);
+cudaError_t few_tokens_forward(const Args& a, cudaStream_t stream);
+cudaError_t few_tokens_site(uint32_t* site);
 size_t forward_workspace_bytes(int64_t T, int64_t D, int64_t F);
 size_t backward_workspace_bytes(int64_t T, int64_t D, int64_t F);
 cudaError_t forward(const Args& a, cudaStream_t stream);

@@ -16,20 +16,46 @@ int64_t tiles_of(const Shape& s, int64_t tile_m, int64_t tile_n) {
     return s.mode == kSymmetric ? n * (n + 1) / 2 : m * n * (s.mode == kGroups ? 2 : 1);
 }
 
-// Clocks that a product takes, roughly: what each SM has to do one after another,
-// at the rates that were seen (per SM and clock 46 bytes from L2, 24 from HBM, the
-// MMA's 4096 products), and what a block's start and end cost.
-constexpr double kFromL2 = 46, kFromHbm = 24, kStart = 6000, kStartAgain = 3000, kPairStart = 11000, kPairAgain = 3000;
+// Blocks of clusters of 1 to 8 that the GPU holds at once, with one and with two
+// blocks to an SM (its processing clusters do not all have the same number of SMs).
+constexpr int kPlaces[2][9] = {{0, 152, 152, 138, 144, 140, 138, 105, 120}, {0, 304, 304, 291, 296, 290, 276, 266, 288}};
 
-double single_cost(const Shape& s, int64_t steps, int64_t tile_n, int split) {
-    const int64_t columns = s.mode == kSideBySide ? 2 * tile_n : tile_n, rows = s.M < 128 ? s.M : 128;
-    const int64_t blocks = tiles_of(s, 128, tile_n) * split, turns = over(blocks, kSms);
-    // B is read once if there is one row of tiles, and then comes from HBM
-    const double b_rate = s.M <= 128 ? kFromHbm : kFromL2;
-    double step = columns * 128 / b_rate + rows * 128 / kFromL2;
-    if (step < 2.0 * columns) step = 2.0 * columns;
-    // two blocks or more share an SM: one's start and end are under another's products, or wait for a place
-    return (double)turns * over(steps, split) * step + kStart + (turns - 1) * kStartAgain + 400.0 * (split - 1);
+// What a single block of `columns` of B holds: stages, and shared memory in all.
+struct Layout {
+    int stages;
+    uint32_t smem;
+};
+Layout layout(const Shape& s, int columns, uint32_t b_bytes, int per_sm) {
+    const uint32_t fixed = 2048, stage = 2 * kBoxBytes + b_bytes;
+    const uint32_t rows = s.M < 128 ? (uint32_t)over(s.M, 32) * 32 : 128;
+    const uint32_t part = rows * ((uint32_t)over(columns, 32) * 32 + 4) * 4;
+    const uint32_t room = (per_sm == 2 ? 233472 / 2 - 1024 : kSharedMost) - fixed;
+    if (part > room || room / stage < 2) return {0, 0};
+    const uint32_t n = room / stage, stages = n < (uint32_t)kMaxStages ? n : kMaxStages;
+    return {(int)stages, fixed + (stages * stage > part ? stages * stage : part)};
+}
+
+// Clocks that a product takes, roughly, from what was seen: a step of 64 k takes a
+// block 500 to issue, and its bytes 1500 from L2 (2200 from HBM) with as many in
+// flight as it has stages; per SM and clock there are 46 bytes from L2, 24 from HBM
+// and 4096 products.
+constexpr double kFromL2 = 46, kFromHbm = 24, kIssue = 500, kStart = 8000, kAgain = 4000, kPairStart = 12000,
+                 kPairAgain = 3000;
+
+double single_cost(const Shape& s, int64_t steps, int64_t blocks, int split, int columns, uint32_t b_bytes, int stages,
+                   int per_sm) {
+    const double a_bytes = (s.M < 128 ? s.M : 128) * 128.0;
+    const bool once = s.M <= 128;   // B is read once and comes from HBM
+    const double turns = (double)over(blocks, kPlaces[per_sm - 1][split]);
+    const double sharing = blocks < kPlaces[per_sm - 1][split] ? (double)over(blocks, kSms) : per_sm;
+    double step = kIssue;
+    const double waiting = (once ? 2200.0 : 1500.0) / stages;
+    const double rate = sharing * (a_bytes / kFromL2 + b_bytes / (once ? kFromHbm : kFromL2));
+    const double products = sharing * 2.0 * columns;
+    if (step < waiting) step = waiting;
+    if (step < rate) step = rate;
+    if (step < products) step = products;
+    return turns * ((double)over(steps, split) * step + kAgain) + kStart - kAgain + 500.0 * (split - 1);
 }
 
 }  // namespace
@@ -43,19 +69,36 @@ Choice choose(Shape& s) {
     const double pair_step = 32768 / kFromL2 < 512 ? 512 : 32768 / kFromL2;
     const double pair_cost = waves * steps * pair_step + kPairStart + (waves - 1) * kPairAgain;
 
-    // single blocks: B's rows per tile free where its rows are k and C is not symmetric
+    // single blocks: B's rows per tile free where its rows are k and C is not symmetric; tried are those
+    // that fill the GPU's places once or twice
     const bool free_n = !s.b_mn && s.mode != kSymmetric;
-    const int64_t unit = side ? 8 : 16, most_n = side ? 128 : 256, fixed_n = side ? 64 : 128;
+    const int64_t unit = side ? 8 : 16, most = side ? 128 : 256, fixed = side ? 64 : 128, m_tiles = over(s.M, 128);
     double best = 1e300;
+    Layout best_layout{};
     for (int split = 1; split <= 8 && split <= steps; ++split)
-        for (int64_t n = free_n ? unit : fixed_n; n <= (free_n ? most_n : fixed_n); n += unit) {
-            const double cost = single_cost(s, steps, n, split);
-            if (cost < best) {
-                best = cost;
-                s.tile_n = (int)n;
-                s.split = split;
+        for (int per_sm = 1; per_sm <= 2; ++per_sm)
+            for (int turns = 1; turns <= 2; ++turns) {
+                int64_t n = fixed;
+                if (free_n) {
+                    const int64_t room = (int64_t)kPlaces[per_sm - 1][split] * turns / (split * m_tiles);
+                    n = room < 1 ? most : over(over(s.N, room), unit) * unit;
+                    if (n > most) n = most;
+                } else if (turns == 2) {
+                    continue;
+                }
+                const int columns = (int)(side ? 2 * n : n);
+                const uint32_t b_bytes = free_n ? (uint32_t)columns * 128 : 2 * kBoxBytes;
+                const Layout l = layout(s, columns, b_bytes, per_sm);
+                if (l.stages == 0) continue;
+                const int64_t blocks = tiles_of(s, 128, n) * split;
+                const double cost = single_cost(s, steps, blocks, split, columns, b_bytes, l.stages, per_sm);
+                if (cost < best) {
+                    best = cost;
+                    best_layout = l;
+                    s.tile_n = (int)n;
+                    s.split = split;
+                }
             }
-        }
     if (s.M > 128 && pair_cost <= best) {
         c.pair = true;
         s.tile_n = (int)pair_n;
@@ -77,13 +120,8 @@ Choice choose(Shape& s) {
     s.tmem_columns = 32;
     while (s.tmem_columns < columns) s.tmem_columns *= 2;
     s.part_row = (columns + 31) / 32 * 32 + 4;   // 4 more: vectors of neighbouring rows in different banks
-    // stages: as many as fit, for one block per SM or for two
-    const uint32_t fixed = 2048, stage = 2 * kBoxBytes + s.b_bytes;
-    const uint32_t part = (uint32_t)((s.M < 128 ? (s.M + 31) / 32 * 32 : 128) * s.part_row * 4);
-    uint32_t room = (c.grid > kSms ? 233472 / 2 - 1024 : kSharedMost) - fixed;
-    if (part > room) room = kSharedMost - fixed;
-    s.stages = (int)(room / stage < (uint32_t)kMaxStages ? room / stage : kMaxStages);
-    c.smem = fixed + (s.stages * stage > part ? s.stages * stage : part);
+    s.stages = best_layout.stages;
+    c.smem = best_layout.smem;
     return c;
 }
 

@@ -1,0 +1,298 @@
+// The feed-forward block for one to four tokens (sm_103a): its time is the weights'
+// way from memory (6 D F bytes), so this is a matrix-vector product that keeps HBM
+// busy, on the CUDA cores: every weight is multiplied once per token, and a product
+// with tensor cores would fill 127 of 128 rows with nothing.
+//
+// One block of 16 warps per SM; the block's rows of weights are a contiguous 152nd
+// of all.  Four warps share a row's k (quarters), four such groups take two pairs of
+// gate and up rows (or four rows of the second product) at a time: eight 16-byte
+// loads per thread are under way, 64 KB per SM.  x lies in shared memory in FP32.
+// Sums are FP32 in a fixed order: per thread, over the lanes, over the quarters.
+// Rows that do not start at 16 bytes are read as 4-byte words, with x shifted by one
+// element for rows that start in the middle of one.
+#include "mhcm_ffn.cuh"
+#include "mhcm_product.cuh"
+
+namespace mhcpb {
+namespace ffn {
+
+namespace {
+
+constexpr int kBlocks = 152, kThreads = 512, kQuarters = 4, kGroups = kThreads / 32 / kQuarters;
+constexpr int kRows = 4;       // weight rows of a warp at a time
+constexpr int kUnroll = 2;
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float sum_of(uint64_t v) {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    return lo + hi;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+template <class T>
+struct TokenArgs {
+    const T *w0, *w1;      // [R, K]; w1: the up projection (dual)
+    int64_t R;
+    int K;
+    const T* x;            // [tokens, K], rows x_ld apart
+    int64_t x_ld;
+    int tokens;
+    T* out;                // [tokens, R], rows out_ld apart: act(g) u, or the products
+    int64_t out_ld;
+    T *gate, *up;          // [tokens, R] or null
+    int activation;
+    int after;             // x comes from the launch before, the weights do not
+};
+
+// Elements of x in shared memory per token.  WIDE: the first and the second four of every eight apart
+// (vectors without bank conflicts).  Else twice, the second copy one element later, with zeros around.
+template <bool WIDE>
+__host__ __device__ constexpr int x_floats(int K) {
+    return WIDE ? K : 2 * ((K + 4) / 2 * 2);
+}
+template <bool WIDE>
+size_t token_smem(int tokens, int K, int64_t R, bool dual) {
+    const int64_t rows = (R + kBlocks - 1) / kBlocks + 1;
+    return ((size_t)tokens * x_floats<WIDE>(K) + (size_t)rows * (dual ? 2 : 1) * kQuarters * tokens) * 4;
+}
+
+template <class T, int NT, bool DUAL, bool WIDE>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) token_kernel(const TokenArgs<T> a) {
+    extern __shared__ float4 shared[];
+    float* xs = reinterpret_cast<float*>(shared);
+    constexpr int kOutputs = DUAL ? kRows / 2 : kRows;     // rows of the output per warp and turn
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) % kQuarters, group = threadIdx.x / (32 * kQuarters);
+    const int K = a.K, xn = x_floats<WIDE>(K);
+    float* part = xs + (size_t)NT * xn;                    // [row of the block][which of two][quarter][token]
+    const int64_t first = blockIdx.x * a.R / gridDim.x, end = (blockIdx.x + 1) * a.R / gridDim.x;
+    const size_t weight_bytes = (size_t)a.R * K * sizeof(T);
+
+    if (a.after)   // the block's first weights on their way while the launch before ends
+        for (int64_t i = first * K * (int64_t)sizeof(T) + threadIdx.x * 128;
+             i < end * K * (int64_t)sizeof(T) && i < first * K * (int64_t)sizeof(T) + 131072; i += kThreads * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(a.w0) + i));
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+
+    const size_t x_bytes = ((a.tokens - 1) * a.x_ld + K) * sizeof(T);
+    if constexpr (WIDE) {
+        for (int i = threadIdx.x; i < NT * (K / 8); i += kThreads) {
+            const int t = NT == 1 ? 0 : i / (K / 8), v = i - t * (K / 8);
+            const T* p = a.x + t * a.x_ld + v * 8;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (t < a.tokens && check::in(p, 16, a.x, x_bytes, 12)) u = *reinterpret_cast<const uint4*>(p);
+            const float2 e0 = product::Pair16<T>::unpack(u.x), e1 = product::Pair16<T>::unpack(u.y),
+                         e2 = product::Pair16<T>::unpack(u.z), e3 = product::Pair16<T>::unpack(u.w);
+            *reinterpret_cast<float4*>(xs + t * xn + v * 4) = make_float4(e0.x, e0.y, e1.x, e1.y);
+            *reinterpret_cast<float4*>(xs + t * xn + K / 2 + v * 4) = make_float4(e2.x, e2.y, e3.x, e3.y);
+        }
+    } else {
+        for (int i = threadIdx.x; i < NT * K; i += kThreads) {
+            const int t = i / K, k = i - t * K;
+            const T* p = a.x + t * a.x_ld + k;
+            const float v = t < a.tokens && check::in(p, sizeof(T), a.x, x_bytes, 12) ? (float)*p : 0.f;
+            xs[t * xn + k] = xs[t * xn + xn / 2 + k + 1] = v;
+        }
+    }
+    if constexpr (!WIDE)
+        for (int t = threadIdx.x; t < NT; t += kThreads) {
+            xs[t * xn + xn / 2] = 0.f;
+            for (int k = K; k < xn / 2; ++k) xs[t * xn + k] = 0.f;
+            for (int k = K + 1; k < xn / 2; ++k) xs[t * xn + xn / 2 + k] = 0.f;
+        }
+    __syncthreads();
+
+    const int vectors = WIDE ? K / 8 : (K + 2) / 2;        // (a row from the middle of a word has one more)
+    const int v0 = (int)((int64_t)quarter * vectors / kQuarters), v1 = (int)((int64_t)(quarter + 1) * vectors / kQuarters);
+    for (int64_t f = first + group * kOutputs; f < end; f += kGroups * kOutputs) {
+        uint64_t acc[NT][kRows];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) acc[t][r] = 0;
+        const T* row[kRows];
+        bool valid[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t i = f + (DUAL ? r / 2 : r);
+            valid[r] = i < end;
+            row[r] = (DUAL && (r & 1) ? a.w1 : a.w0) + i * K;
+        }
+        for (int v = v0 + lane; v < v1; v += 32 * kUnroll) {
+            if constexpr (WIDE) {
+                uint4 u[kUnroll][kRows];
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        u[j][r] = make_uint4(0, 0, 0, 0);
+                        const T* p = row[r] + (int64_t)(v + 32 * j) * 8;
+                        if (valid[r] && v + 32 * j < v1 &&
+                            check::in(p, 16, DUAL && (r & 1) ? a.w1 : a.w0, weight_bytes, 13))
+                            u[j][r] = __ldcs(reinterpret_cast<const uint4*>(p));
+                    }
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j) {
+                    if (v + 32 * j >= v1) break;
+                    uint64_t x[NT][4];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const float4 lo = *reinterpret_cast<const float4*>(xs + t * xn + (v + 32 * j) * 4);
+                        const float4 hi = *reinterpret_cast<const float4*>(xs + t * xn + K / 2 + (v + 32 * j) * 4);
+                        x[t][0] = pair(lo.x, lo.y), x[t][1] = pair(lo.z, lo.w);
+                        x[t][2] = pair(hi.x, hi.y), x[t][3] = pair(hi.z, hi.w);
+                    }
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        const uint32_t w[4] = {u[j][r].x, u[j][r].y, u[j][r].z, u[j][r].w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 e = product::Pair16<T>::unpack(w[q]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) acc[t][r] = fma2(pair(e.x, e.y), x[t][q], acc[t][r]);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j)
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        // word i of the row: elements 2 i - odd and 2 i + 1 - odd, where they are the row's
+                        const int i = v + 32 * j;
+                        const int odd = (int)((reinterpret_cast<uintptr_t>(row[r]) >> 1) & 1);
+                        if (!valid[r] || i >= v1 || 2 * i - odd >= K) continue;
+                        const T* p = row[r] + 2 * i - odd;
+                        const T* const base = DUAL && (r & 1) ? a.w1 : a.w0;
+                        const bool both = 2 * i + 1 - odd < K;
+                        float2 e = make_float2(0.f, 0.f);
+                        if (2 * i - odd >= 0 && both) {
+                            if (check::in(p, 4, base, weight_bytes, 14))
+                                e = product::Pair16<T>::unpack(*reinterpret_cast<const uint32_t*>(p));
+                        } else if (both) {
+                            if (check::in(p + 1, 2, base, weight_bytes, 14)) e.y = (float)p[1];
+                        } else if (check::in(p, 2, base, weight_bytes, 14)) {
+                            e.x = (float)p[0];
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const float2 x = *reinterpret_cast<const float2*>(xs + t * xn + (odd ? xn / 2 : 0) + 2 * i);
+                            acc[t][r] = fma2(pair(e.x, e.y), pair(x.x, x.y), acc[t][r]);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                float v = sum_of(acc[t][r]);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+                if (lane == 0 && valid[r])
+                    part[(((f - first) * (DUAL ? 2 : 1) + r) * kQuarters + quarter) * NT + t] = v;
+            }
+    }
+    __syncthreads();
+    const int rows = (int)(end - first);
+    for (int i = threadIdx.x; i < rows * NT; i += kThreads) {
+        const int t = i / rows, r = i - t * rows;
+        if (t >= a.tokens) continue;
+        auto total = [&](int line) {
+            float v = 0.f;
+#pragma unroll
+            for (int q = 0; q < kQuarters; ++q) v += part[(line * kQuarters + q) * NT + t];
+            return v;
+        };
+        const int64_t f = first + r;
+        T* o = a.out + t * a.out_ld + f;
+        const bool ok = check::in(o, sizeof(T), a.out, ((a.tokens - 1) * a.out_ld + a.R) * sizeof(T), 15);
+        if constexpr (DUAL) {
+            const float g = total(2 * r), u = total(2 * r + 1);
+            if (ok) *o = (T)(activate(g, a.activation).x * u);
+            if (a.gate != nullptr && check::in(a.gate + t * a.R + f, sizeof(T), a.gate, a.tokens * a.R * sizeof(T), 16)) {
+                a.gate[t * a.R + f] = (T)g;
+                a.up[t * a.R + f] = (T)u;
+            }
+        } else if (ok) {
+            *o = (T)total(r);
+        }
+    }
+}
+
+template <class T, int NT, bool DUAL, bool WIDE>
+cudaError_t launch(const TokenArgs<T>& a, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    auto* kernel = token_kernel<T, NT, DUAL, WIDE>;
+    const cudaError_t e = ops::allow_shared(kernel, (int)product::kSharedMost, done);
+    if (e != cudaSuccess) return e;
+    return ops::launch_early(kernel, dim3(kBlocks), dim3(kThreads), token_smem<WIDE>(NT, a.K, a.R, DUAL), stream, a);
+}
+template <class T, bool DUAL, bool WIDE>
+cudaError_t by_tokens(const TokenArgs<T>& a, cudaStream_t stream) {
+    return a.tokens == 1 ? launch<T, 1, DUAL, WIDE>(a, stream)
+                         : a.tokens == 2 ? launch<T, 2, DUAL, WIDE>(a, stream) : launch<T, 4, DUAL, WIDE>(a, stream);
+}
+template <class T, bool DUAL>
+cudaError_t by_rows(const TokenArgs<T>& a, cudaStream_t stream) {
+    return a.K % 8 == 0 ? by_tokens<T, DUAL, true>(a, stream) : by_tokens<T, DUAL, false>(a, stream);
+}
+
+template <class T>
+cudaError_t forward_as(const Args& a, cudaStream_t stream) {
+    TokenArgs<T> t{};
+    t.w0 = static_cast<const T*>(a.w_gate);
+    t.w1 = static_cast<const T*>(a.w_up);
+    t.R = a.F;
+    t.K = (int)a.D;
+    t.x = static_cast<const T*>(a.x);
+    t.x_ld = a.x_stride;
+    t.tokens = (int)a.T;
+    t.out = static_cast<T*>(a.workspace);
+    t.out_ld = a.F;
+    t.gate = static_cast<T*>(a.gate);
+    t.up = static_cast<T*>(a.up);
+    t.activation = a.activation;
+    const cudaError_t e = by_rows<T, true>(t, stream);
+    if (e != cudaSuccess) return e;
+    t = {};
+    t.w0 = static_cast<const T*>(a.w_down);
+    t.R = a.D;
+    t.K = (int)a.F;
+    t.x = static_cast<const T*>(a.workspace);
+    t.x_ld = a.F;
+    t.tokens = (int)a.T;
+    t.out = static_cast<T*>(a.y);
+    t.out_ld = a.y_stride;
+    t.after = 1;
+    return by_rows<T, false>(t, stream);
+}
+
+bool fits(int tokens, int64_t K, int64_t R, bool dual) {
+    return (K % 8 == 0 ? token_smem<true>(tokens, (int)K, R, dual) : token_smem<false>(tokens, (int)K, R, dual)) <=
+           product::kSharedMost;
+}
+
+}  // namespace
+
+bool few_tokens(int64_t T, int64_t D, int64_t F) {
+    if (T > 4) return false;
+    const int tokens = T == 3 ? 4 : (int)T;
+    return fits(tokens, D, F, true) && fits(tokens, F, D, false);
+}
+cudaError_t few_tokens_forward(const Args& a, cudaStream_t stream) {
+    return a.type == MHCPB_BF16 ? forward_as<__nv_bfloat16>(a, stream) : forward_as<__half>(a, stream);
+}
+cudaError_t few_tokens_site(uint32_t* site) { return check::read_and_clear(site); }
+
+}  // namespace ffn
+}  // namespace mhcpb

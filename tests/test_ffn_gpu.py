@@ -14,7 +14,7 @@ from matrix_cases import DEV, f64
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
 
-SMALL = [(1, 1, 1), (1, 8, 8), (1, 64, 64), (2, 7, 3), (1, 136, 1000), (5, 1000, 136), (8, 2048, 72), (64, 256, 512),
+SMALL = [(3, 75, 141), (4, 1001, 77), (2, 2048, 4096), (1, 1027, 515), (1, 1, 1), (1, 8, 8), (1, 64, 64), (2, 7, 3), (1, 136, 1000), (5, 1000, 136), (8, 2048, 72), (64, 256, 512),
          (127, 129, 131), (128, 128, 128), (129, 320, 257), (257, 200, 264), (300, 65, 700)]
 # tiles of 256 x 256 in every product, in some, odd ones
 LARGE = [(1100, 1601, 1600), (300, 2600, 2568), (2049, 136, 2500), (700, 1032, 3432)]
