@@ -128,6 +128,11 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
     return __all_sync(0xFFFFFFFFu, wait<CLUSTER>(bar, parity, abort_flag));
 }
 
+__device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float4& y) {
+    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+}
+
 // Epilogue: struct with
 //   static constexpr bool kDual                    two products side by side
 //   struct Read                                    what an element's result needs from memory
@@ -384,70 +389,86 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         // Every block has its part of the tile in shared memory; each adds up its share of the vectors.
         const Tile tile = tile_at<C::tile_m>(s, first_tile);
         const int rows = (int)min((int64_t)128, s.M - tile.m), cols = (int)min((int64_t)s.tile_n, s.N - tile.n);
-        auto gather = [&](int r, int c, float (&v)[8]) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-            for (int z = 0; z < s.split; ++z) {
-                const uint32_t p = ptx::map_rank(stage0 + (uint32_t)(r * s.part_row + c) * 4, z);
-                const float4 x = ptx::ld_cluster_f32x4(p), y = ptx::ld_cluster_f32x4(p + 16);
-                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-                v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-            }
+        const float* own = reinterpret_cast<const float*>(smem + C::off_stages);
+        auto part_at = [&](uint32_t i, int z) {
+            return z == (int)rank ? *reinterpret_cast<const float4*>(own + i)
+                                  : ptx::ld_cluster_f32x4(ptx::map_rank(stage0 + 4 * i, z));
         };
-        // Four vectors per thread at a time: their reads and the parts' are all under way before the first write.
+        auto element_at = [&](uint32_t i, int z) {
+            return z == (int)rank ? own[i] : ptx::ld_cluster_f32(ptx::map_rank(stage0 + 4 * i, z));
+        };
+        // Some vectors per thread at a time: their reads, and the loads of one block's part, are all under
+        // way before the first is used (each trip to another block's shared memory takes some 500 clocks).
+        constexpr int kBatch = Epilogue::kDual ? 2 : 4;
         const int threads = s.split * C::threads, me = (int)rank * C::threads + threadIdx.x;
         const int across = (cols + 7) / 8, units = rows * across;
-        for (int first = me; first < units; first += 4 * threads) {
-            typename Epilogue::Read read[4];
-            float v[4][8], w[Epilogue::kDual ? 4 : 1][8];
+        for (int first = me; first < units; first += kBatch * threads) {
+            typename Epilogue::Read read[kBatch];
+            float v[kBatch][8], w[Epilogue::kDual ? kBatch : 1][8];
+            int row[kBatch], col[kBatch];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
-                if (u < units) read[q] = epi.read((int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c));
+            for (int q = 0; q < kBatch; ++q) {
+                const int u = first + q * threads;
+                row[q] = u / across, col[q] = (u - row[q] * across) * 8;
+                if (u < units) read[q] = epi.read((int64_t)tile.m + row[q], (int64_t)tile.n + col[q], min(8, cols - col[q]));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[q][i] = w[Epilogue::kDual ? q : 0][i] = 0.f;
+            }
+            for (int z = 0; z < s.split; ++z) {
+                float4 x[kBatch][Epilogue::kDual ? 4 : 2];
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    if (first + q * threads < units)
+#pragma unroll
+                        for (int h = 0; h < (Epilogue::kDual ? 4 : 2); ++h)
+                            x[q][h] = part_at((uint32_t)(row[q] * s.part_row + col[q] + (h >> 1) * s.tile_n + (h & 1) * 4), z);
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    if (first + q * threads < units) {
+                        add8(v[q], x[q][0], x[q][1]);
+                        if constexpr (Epilogue::kDual) add8(w[q], x[q][2], x[q][3]);
+                    }
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
-                if (u >= units) break;
-                gather(r, c, v[q]);
-                if constexpr (Epilogue::kDual) gather(r, s.tile_n + c, w[q]);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
-                if (u >= units) break;
-                epi.write(tile.group, (int64_t)tile.m + r, (int64_t)tile.n + c, min(8, cols - c), v[q],
-                          w[Epilogue::kDual ? q : 0], read[q]);
-            }
+            for (int q = 0; q < kBatch; ++q)
+                if (first + q * threads < units)
+                    epi.write(tile.group, (int64_t)tile.m + row[q], (int64_t)tile.n + col[q], min(8, cols - col[q]), v[q],
+                              w[Epilogue::kDual ? q : 0], read[q]);
         }
         if (tile.mirror) {   // transposed: eight rows of one column
             const int down = (rows + 7) / 8, flipped = cols * down;
-            for (int first = me; first < flipped; first += 4 * threads) {
-                typename Epilogue::Read read[4];
-                float v[4][8];
+            for (int first = me; first < flipped; first += kBatch * threads) {
+                typename Epilogue::Read read[kBatch];
+                float v[kBatch][8];
+                int row[kBatch], col[kBatch];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
-                    if (u < flipped) read[q] = epi.read((int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g));
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
-                    if (u >= flipped) break;
+                for (int q = 0; q < kBatch; ++q) {
+                    const int u = first + q * threads, g = u / cols;
+                    row[q] = 8 * g, col[q] = u - g * cols;
+                    if (u < flipped)
+                        read[q] = epi.read((int64_t)tile.n + col[q], (int64_t)tile.m + row[q], min(8, rows - row[q]));
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[q][i] = 0.f;
-                    for (int z = 0; z < s.split; ++z) {
-                        const uint32_t p = ptx::map_rank(stage0 + (uint32_t)(8 * g * s.part_row + c) * 4, z);
+                }
+                for (int z = 0; z < s.split; ++z) {
+                    float x[kBatch][8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[q][i] += ptx::ld_cluster_f32(p + i * s.part_row * 4);
-                    }
+                    for (int q = 0; q < kBatch; ++q)
+                        if (first + q * threads < flipped)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                x[q][i] = element_at((uint32_t)((row[q] + i) * s.part_row + col[q]), z);
+#pragma unroll
+                    for (int q = 0; q < kBatch; ++q)
+                        if (first + q * threads < flipped)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[q][i] += x[q][i];
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
-                    if (u >= flipped) break;
-                    epi.write(0, (int64_t)tile.n + c, (int64_t)tile.m + 8 * g, min(8, rows - 8 * g), v[q], v[q], read[q]);
-                }
+                for (int q = 0; q < kBatch; ++q)
+                    if (first + q * threads < flipped)
+                        epi.write(0, (int64_t)tile.n + col[q], (int64_t)tile.m + row[q], min(8, rows - row[q]), v[q], v[q],
+                                  read[q]);
             }
         }
         ptx::cluster_arrive();   // the parts stay until every block has read them

@@ -81,7 +81,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) token_kernel(const 
              i < end * K * (int64_t)sizeof(T) && i < first * K * (int64_t)sizeof(T) + 131072; i += kThreads * 128)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(a.w0) + i));
     ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
 
     const size_t x_bytes = ((a.tokens - 1) * a.x_ld + K) * sizeof(T);
     if constexpr (WIDE) {
@@ -202,6 +201,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) token_kernel(const 
                     part[(((f - first) * (DUAL ? 2 : 1) + r) * kQuarters + quarter) * NT + t] = v;
             }
     }
+    // (not earlier: what the next launch prefetches would be gone again before it is used)
+    ptx::grid_launch_dependents();
     __syncthreads();
     const int rows = (int)(end - first);
     for (int i = threadIdx.x; i < rows * NT; i += kThreads) {
