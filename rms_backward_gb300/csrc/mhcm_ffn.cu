@@ -28,17 +28,22 @@ struct GatedEpilogue {
     static constexpr bool kDual = true;
     Matrix<T> hidden, gate, up;
     int activation;
+    template <class Span>
     struct Read {};
-    __device__ __forceinline__ Read read(int64_t, int64_t, int) const { return {}; }
-    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&g)[8],
-                                          const float (&u)[8], const Read&) const {
-        float a[8];
+    template <class Span>
+    __device__ __forceinline__ Read<Span> read(int, const Span&) const {
+        return {};
+    }
+    template <class Span>
+    __device__ __forceinline__ void write(int, const Span& at, const float (&g)[Span::n], const float (&u)[Span::n],
+                                          const Read<Span>&) const {
+        float a[Span::n];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = activate(g[i], activation).x * u[i];
-        hidden.store(row, col, count, a, 0);
+        for (int i = 0; i < Span::n; ++i) a[i] = activate(g[i], activation).x * u[i];
+        hidden.store(at, a, 0);
         if (gate.ptr != nullptr) {
-            gate.store(row, col, count, g, 1);
-            up.store(row, col, count, u, 2);
+            gate.store(at, g, 1);
+            up.store(at, u, 2);
         }
     }
 };
@@ -48,27 +53,30 @@ struct GradEpilogue {
     static constexpr bool kDual = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
     int activation;
+    template <class Span>
     struct Read {
-        typename Matrix<T>::Raw g, u;
+        product::Raw<T, Span> g, u;
     };
-    __device__ __forceinline__ Read read(int64_t row, int64_t col, int count) const {
-        return {gate.raw(row, col, count, 3), up.raw(row, col, count, 4)};
+    template <class Span>
+    __device__ __forceinline__ Read<Span> read(int, const Span& at) const {
+        return {gate.raw(at, 3), up.raw(at, 4)};
     }
-    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&da)[8],
-                                          const float (&)[8], const Read& in) const {
-        float g[8], u[8], a[8];
+    template <class Span>
+    __device__ __forceinline__ void write(int, const Span& at, const float (&da)[Span::n], const float (&)[Span::n],
+                                          const Read<Span>& in) const {
+        float g[Span::n], u[Span::n], a[Span::n];
         in.g.to(g);
         in.u.to(u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < Span::n; ++i) {
             const float2 f = activate(g[i], activation);
             a[i] = f.x * u[i];
             g[i] = da[i] * u[i] * f.y;
             u[i] = da[i] * f.x;
         }
-        grad_gate.store(row, col, count, g, 5);
-        grad_up.store(row, col, count, u, 6);
-        hidden.store(row, col, count, a, 7);
+        grad_gate.store(at, g, 5);
+        grad_up.store(at, u, 6);
+        hidden.store(at, a, 7);
     }
 };
 
@@ -77,17 +85,22 @@ struct StoreEpilogue {
     static constexpr bool kDual = false;
     Matrix<O> out[2];
     bool accumulate;
-    struct Read {};
-    __device__ __forceinline__ Read read(int64_t, int64_t, int) const { return {}; }
-    __device__ __forceinline__ void write(int group, int64_t row, int64_t col, int count, const float (&v)[8],
-                                          const float (&)[8], const Read&) const {
-        const Matrix<O>& o = out[group];
-        if (!accumulate) return o.store(row, col, count, v, 8);
-        float old[8];
-        o.load(row, col, count, old, 9);
+    template <class Span>
+    struct Read {
+        product::Raw<O, Span> old;
+    };
+    template <class Span>
+    __device__ __forceinline__ Read<Span> read(int group, const Span& at) const {
+        return accumulate ? Read<Span>{out[group].raw(at, 9)} : Read<Span>{};
+    }
+    template <class Span>
+    __device__ __forceinline__ void write(int group, const Span& at, const float (&v)[Span::n], const float (&)[Span::n],
+                                          const Read<Span>& in) const {
+        float r[Span::n];
+        in.old.to(r);   // (zeros where nothing is added to)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) old[i] += v[i];
-        o.store(row, col, count, old, 8);
+        for (int i = 0; i < Span::n; ++i) r[i] = accumulate ? r[i] + v[i] : v[i];
+        out[group].store(at, r, 8);
     }
 };
 
@@ -167,9 +180,11 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
     const GatedEpilogue<T> gated{matrix<T>(hidden, T_, F, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
                                  a.activation};
+    s.narrow = !gated.gate.even();
     MHCM_TRY(product::launch(s, gated, &x, nullptr, &wg, &wu, stream));
     s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain;
     const StoreEpilogue<T> store{{matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
+    s.narrow = !store.out[0].even();
     return product::launch(s, store, &h, nullptr, &wd, nullptr, stream);
 }
 
@@ -183,6 +198,7 @@ cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const
     s.a_mn = s.b_mn = 1;
     s.beside = beside;
     const StoreEpilogue<O> store{{matrix<O>(out0, M, N, N), matrix<O>(out1, M, N, N)}, a.accumulate};
+    s.narrow = !store.out[0].even();
     return product::launch(s, store, a0, a1, b, b, stream);
 }
 
@@ -211,6 +227,7 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.b_mn = 1;
     const GradEpilogue<T> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, F, Fp),
                                matrix<T>(grad_up, T_, F, Fp), matrix<T>(hidden, T_, F, Fp), a.activation};
+    s.narrow = !grad.gate.even();
     MHCM_TRY(product::launch(s, grad, &dy, nullptr, &wd, nullptr, stream));
     // The products that are left need only what the first wrote: each starts as soon as the one
     // before it leaves room (its last tiles keep a part of the GPU busy), not when that has ended.
@@ -219,6 +236,7 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     if (a.grad_x) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
         const StoreEpilogue<T> store{{matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
+        s.narrow = !store.out[0].even();
         MHCM_TRY(product::launch(s, store, &dg, &du, &wg, &wu, stream));
         beside = true;
     }

@@ -43,28 +43,33 @@ struct Input {
     const void* ptr;
     int type;
     int64_t rows, ld, cols;
-    // eight elements as they are stored (two words of four, the first alone for 16-bit types), and as FP32
-    __device__ __forceinline__ void raw(int64_t row, int64_t col, int count, uint4 (&u)[2], uint32_t site) const {
+    // elements as they are stored (a 16-bit type's in the first half of the words), and as FP32
+    template <class Span>
+    __device__ __forceinline__ product::Raw<float, Span> raw(const Span& at, uint32_t site) const {
         const size_t n = (size_t)((rows - 1) * ld + cols);
-        if (type == MHCPB_FP32) {
-            const auto r = Matrix<const float>{static_cast<const float*>(ptr), ld, n}.raw(row, col, count, site);
-            u[0] = r.u[0], u[1] = r.u[1];
-        } else {
-            u[0] = Matrix<const __half>{static_cast<const __half*>(ptr), ld, n}.raw(row, col, count, site).u[0];
+        if (type == MHCPB_FP32) return Matrix<const float>{static_cast<const float*>(ptr), ld, n}.raw(at, site);
+        const auto h = Matrix<const __half>{static_cast<const __half*>(ptr), ld, n}.raw(at, site);
+        product::Raw<float, Span> r{};
+#pragma unroll
+        for (int i = 0; i < h.words; ++i) r.u[i] = h.u[i];
+        return r;
+    }
+    template <class Span>
+    __device__ __forceinline__ void to(const product::Raw<float, Span>& r, float (&v)[Span::n]) const {
+        if (type == MHCPB_FP32) return r.to(v);
+        if (type == MHCPB_BF16) {
+            product::Raw<__nv_bfloat16, Span> h;
+#pragma unroll
+            for (int i = 0; i < h.words; ++i) h.u[i] = r.u[i];
+            return h.to(v);
         }
+        product::Raw<__half, Span> h;
+#pragma unroll
+        for (int i = 0; i < h.words; ++i) h.u[i] = r.u[i];
+        h.to(v);
     }
-    __device__ __forceinline__ void to(const uint4 (&u)[2], float (&v)[8]) const {
-        if (type == MHCPB_FP32)
-            Matrix<float>::Raw{u[0], u[1]}.to(v);
-        else if (type == MHCPB_BF16)
-            Matrix<__nv_bfloat16>::Raw{u[0]}.to(v);
-        else
-            Matrix<__half>::Raw{u[0]}.to(v);
-    }
-    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
-        uint4 u[2];
-        raw(row, col, count, u, site);
-        to(u, v);
+    __device__ __forceinline__ void load(const product::Eight& at, float (&v)[8], uint32_t site) const {
+        to(raw(at, site), v);
     }
 };
 
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kNormThreads) squares_kernel(const Input g, do
     for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < units; i += (int64_t)kNormBlocks * kNormThreads) {
         const int64_t r = i / across, c = (i - r * across) * 8;
         float v[8];
-        g.load(r, c, (int)min((int64_t)8, g.cols - c), v, 0);
+        g.load(product::Eight{r, c, (int)min((int64_t)8, g.cols - c)}, v, 0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) s.add(v[k]);
     }
@@ -136,12 +141,12 @@ __global__ void __launch_bounds__(kNormThreads)
     const int64_t across = (g.cols + 7) / 8, units = g.rows * across;
     for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < units; i += (int64_t)gridDim.x * kNormThreads) {
         const int64_t r = i / across, c = (i - r * across) * 8;
-        const int count = (int)min((int64_t)8, g.cols - c);
+        const product::Eight at{r, c, (int)min((int64_t)8, g.cols - c)};
         float v[8];
-        g.load(r, c, count, v, 2);
+        g.load(at, v, 2);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = scaled(v[k], inv) * kScaleX;
-        x.store(r, c, count, v, 3);
+        x.store(at, v, 3);
     }
 }
 
@@ -152,13 +157,13 @@ struct Diagonal {
     __device__ __forceinline__ float at(int64_t i, uint32_t site) const {
         return check::in(lost + i, 4, lost, (size_t)size * 4, site) ? lost[i] : 0.f;
     }
-    // of row `row`, if its diagonal element is among the `count` scaled ones from column `col`
-    __device__ __forceinline__ void keep(int64_t row, int64_t col, int count, const float (&v)[8], float scale,
-                                         uint32_t site) const {
+    // of a row whose diagonal element is among these scaled ones
+    template <class Span>
+    __device__ __forceinline__ void keep(const Span& at, const float (&v)[Span::n], float scale, uint32_t site) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < count && row == col + i && check::in(lost + row, 4, lost, (size_t)size * 4, site))
-                lost[row] = (v[i] - __half2float(__float2half_rn(v[i]))) / scale;
+        for (int i = 0; i < Span::n; ++i)
+            if (at.valid(i) && at.row == at.column(i) && check::in(lost + at.row, 4, lost, (size_t)size * 4, site))
+                lost[at.row] = (v[i] - __half2float(__float2half_rn(v[i]))) / scale;
     }
 };
 
@@ -167,15 +172,20 @@ struct GramEpilogue {
     static constexpr bool kDual = false;
     Matrix<__half> out;
     Diagonal lost;
+    template <class Span>
     struct Read {};
-    __device__ __forceinline__ Read read(int64_t, int64_t, int) const { return {}; }
-    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&v)[8],
-                                          const float (&)[8], const Read&) const {
-        float r[8];
+    template <class Span>
+    __device__ __forceinline__ Read<Span> read(int, const Span&) const {
+        return {};
+    }
+    template <class Span>
+    __device__ __forceinline__ void write(int, const Span& at, const float (&v)[Span::n], const float (&)[Span::n],
+                                          const Read<Span>&) const {
+        float r[Span::n];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = v[i] * (kScaleA / (kScaleX * kScaleX));
-        out.store(row, col, count, r, 4);
-        lost.keep(row, col, count, r, kScaleA, 5);
+        for (int i = 0; i < Span::n; ++i) r[i] = v[i] * (kScaleA / (kScaleX * kScaleX));
+        out.store(at, r, 4);
+        lost.keep(at, r, kScaleA, 5);
     }
 };
 
@@ -186,25 +196,28 @@ struct PolynomialEpilogue {
     Matrix<__half> out;
     Matrix<const __half> gram;
     Diagonal gram_lost, lost;
+    template <class Span>
     struct Read {
-        Matrix<const __half>::Raw gram;
+        product::Raw<__half, Span> gram;
     };
-    __device__ __forceinline__ Read read(int64_t row, int64_t col, int count) const {
-        return {gram.raw(row, col, count, 6)};
+    template <class Span>
+    __device__ __forceinline__ Read<Span> read(int, const Span& at) const {
+        return {gram.raw(at, 6)};
     }
-    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&v)[8],
-                                          const float (&)[8], const Read& in) const {
-        float r[8];
+    template <class Span>
+    __device__ __forceinline__ void write(int, const Span& at, const float (&v)[Span::n], const float (&)[Span::n],
+                                          const Read<Span>& in) const {
+        float r[Span::n];
         in.gram.to(r);
-        const float l = gram_lost.at(row, 7);
+        const float l = gram_lost.at(at.row, 7);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float k = i < count ? gram_lost.at(col + i, 8) : 0.f;
+        for (int i = 0; i < Span::n; ++i) {
+            const float k = at.valid(i) ? gram_lost.at(at.column(i), 8) : 0.f;
             r[i] = fmaf(kC * kScaleB / (kScaleA * kScaleA), v[i], (kB + kC * (l + k)) * (kScaleB / kScaleA) * r[i]);
-            if (row == col + i) r[i] += kScaleB * (kB + kC * l) * l;
+            if (at.row == at.column(i)) r[i] += kScaleB * (kB + kC * l) * l;
         }
-        out.store(row, col, count, r, 9);
-        lost.keep(row, col, count, r, kScaleB, 10);
+        out.store(at, r, 9);
+        lost.keep(at, r, kScaleB, 10);
     }
 };
 
@@ -219,46 +232,40 @@ struct UpdateEpilogue {
     Matrix<__half> copy;        // its FP16 copy
     Matrix<__nv_bfloat16> out;  // the last step's X, times scale; null before
     float scale;
-    struct Read {
-        uint4 u[2];
-    };
-    __device__ __forceinline__ Read read(int64_t row, int64_t col, int count) const {
-        Read r{};
-        if (inverse != nullptr) {
-            g.raw(row, col, count, r.u, 11);
-        } else {
-            const Matrix<float>::Raw w = x.raw(row, col, count, 12);
-            r.u[0] = w.u[0], r.u[1] = w.u[1];
-        }
-        return r;
+    template <class Span>
+    using Read = product::Raw<float, Span>;
+    template <class Span>
+    __device__ __forceinline__ Read<Span> read(int, const Span& at) const {
+        return inverse != nullptr ? g.raw(at, 11) : x.raw(at, 12);
     }
-    __device__ __forceinline__ void write(int, int64_t row, int64_t col, int count, const float (&v)[8],
-                                          const float (&)[8], const Read& in) const {
-        float r[8];
+    template <class Span>
+    __device__ __forceinline__ void write(int, const Span& at, const float (&v)[Span::n], const float (&)[Span::n],
+                                          const Read<Span>& in) const {
+        float r[Span::n];
         if (inverse != nullptr) {
             const Inverse inv = *inverse;
-            g.to(in.u, r);
+            g.to(in, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = scaled(r[i], inv);
+            for (int i = 0; i < Span::n; ++i) r[i] = scaled(r[i], inv);
         } else {
-            Matrix<float>::Raw{in.u[0], in.u[1]}.to(r);
+            in.to(r);
         }
-        const float by_row = tall ? 0.f : lost.at(row, 13);
+        const float by_row = tall || !at.valid(0) ? 0.f : lost.at(at.row, 13);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float l = tall && i < count ? lost.at(col + i, 14) : by_row;
+        for (int i = 0; i < Span::n; ++i) {
+            const float l = tall && at.valid(i) ? lost.at(at.column(i), 14) : by_row;
             r[i] = fmaf(kA + l, r[i], v[i] * (1.f / (kScaleB * kScaleX)));
         }
         if (out.ptr != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] *= scale;
-            out.store(row, col, count, r, 15);
+            for (int i = 0; i < Span::n; ++i) r[i] *= scale;
+            out.store(at, r, 15);
             return;
         }
-        x.store(row, col, count, r, 16);
+        x.store(at, r, 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] *= kScaleX;
-        copy.store(row, col, count, r, 17);
+        for (int i = 0; i < Span::n; ++i) r[i] *= kScaleX;
+        copy.store(at, r, 17);
     }
 };
 
@@ -341,6 +348,9 @@ cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
         const bool last = i + 1 == a.steps;
         const UpdateEpilogue update{g, i == 0 ? inverse : nullptr, poly_lost, tall, x, copies[(i + 1) & 1],
                                     last ? out : Matrix<__nv_bfloat16>{nullptr, 0, 0}, a.scale};
+        // G in the first step and the output in the last may have rows that do not start at 16 bytes
+        const bool g_even = a.g_stride * (a.type == MHCPB_FP32 ? 4 : 2) % 16 == 0;
+        p.narrow = (i == 0 && !g_even) || (last && !out.even());
         if (tall)
             MHCM_TRY(product::launch(p, update, cur, nullptr, &factor_poly, nullptr, stream));
         else

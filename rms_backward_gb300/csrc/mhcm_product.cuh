@@ -133,14 +133,29 @@ __device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float
     v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
 }
 
+// The elements of one row of C that an epilogue takes at a time: eight neighbours (the last ones of a
+// row fewer), or, for matrices whose rows do not start at 16 bytes, one (a warp then has 32 neighbours).
+struct Eight {
+    static constexpr int n = 8;
+    int64_t row, col;
+    int count;
+    __device__ __forceinline__ int64_t column(int i) const { return col + i; }
+    __device__ __forceinline__ bool valid(int i) const { return i < count; }
+};
+struct One {
+    static constexpr int n = 1;
+    int64_t row, col;
+    bool is;             // an element of C
+    __device__ __forceinline__ int64_t column(int) const { return col; }
+    __device__ __forceinline__ bool valid(int) const { return is; }
+};
+
 // Epilogue: struct with
 //   static constexpr bool kDual                    two products side by side
-//   struct Read                                    what an element's result needs from memory
-//   Read read(int64_t row, int64_t col, int count) const
-//   void write(int group, int64_t row, int64_t col, int count, const float (&v)[8], const float (&w)[8],
-//              const Read&) const
-// for `count` (1..8) elements of one row of C; w: the second product's (kDual).
-// Several reads are under way before the first write.
+//   template <class Span> struct Read              what elements' results need from memory
+//   Read<Span> read(int group, const Span&) const
+//   void write(int group, const Span&, const float (&v)[Span::n], const float (&w)[Span::n], const Read<Span>&) const
+// (Span: Eight or One; w: the second product's, where kDual).  Several reads are under way before the first write.
 template <bool PAIR, class Epilogue>
 __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
     product_kernel(const Shape s, const Epilogue epi, const __grid_constant__ CUtensorMap a0,
@@ -280,8 +295,8 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         if constexpr (PAIR) {
             float* scratch = 
                 reinterpret_cast<float*>(smem + C::off_stages + C::stages * kPairStage) + (warp - kEpilogueWarp) * 32 * C::row;
-            // 32 columns of this warp's 32 rows into v[q]: row 8 q + lane / 4, columns 8 (lane % 4) ..
-            auto fetch = [&](uint32_t column, float (&v)[4][8]) {
+            // 32 columns of this warp's 32 rows into its scratch
+            auto stage = [&](uint32_t column) {
                 uint32_t u[32];
                 ptx::tmem_ld_32x32b_x32(lanes + column, u);
                 ptx::tc_wait_ld_regs(u);
@@ -290,13 +305,6 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 for (int c = 0; c < 32; c += 4)
                     *reinterpret_cast<uint4*>(scratch + lane * C::row + c) = make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]);
                 __syncwarp();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4* p = reinterpret_cast<const float4*>(scratch + (8 * q + lane / 4) * C::row + 8 * (lane & 3));
-                    const float4 x = p[0], y = p[1];
-                    v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
-                    v[q][4] = y.x, v[q][5] = y.y, v[q][6] = y.z, v[q][7] = y.w;
-                }
             };
             uint32_t done = 0;
             for (int t = first_tile; t < s.tiles; t += step_tile, ++done) {
@@ -310,51 +318,95 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 for (int c = 0; c < kChunks; ++c) {
                     const int column = half * kChunks * 32 + c * 32;
                     const int64_t col0 = tile.n + column;
+                    auto ready = [&] {   // the first chunk's reads are under way: now the accumulator
+                        if (c == 0) {
+                            ok = wait_all<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag);
+                            if (ok) ptx::tc_fence_after();
+                        }
+                        return ok;
+                    };
+                    auto drained = [&] {   // the last chunk has left TMEM
+                        if (c == kChunks - 1) {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(bar(C::b_free + acc), 0));
+                        }
+                    };
+                    if (s.narrow) {
+                        // column `lane` of each row, sixteen rows' reads at a time, the first before the wait
+                        typename Epilogue::template Read<One> read[16];
+                        auto at = [&](int row) {
+                            return One{row0 + row, col0 + lane, col0 + lane < s.N && row0 + row < s.M};
+                        };
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) read[q] = epi.read(tile.group, at(q));
+                        if (!ready()) break;
+                        float w[Epilogue::kDual ? 32 : 1];
+                        if constexpr (Epilogue::kDual) {
+                            stage(d + 128 + column);
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) w[q] = scratch[q * C::row + lane];
+                        }
+                        stage(d + column);
+                        drained();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) {
+                            if (q == 16)
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) read[r] = epi.read(tile.group, at(16 + r));
+                            const float v[1] = {scratch[q * C::row + lane]};
+                            const float u[1] = {w[Epilogue::kDual ? q : 0]};
+                            epi.write(tile.group, at(q), v, u, read[q & 15]);
+                        }
+                        continue;
+                    }
+                    // eight columns of rows 8 q + lane / 4; transposed: of row `lane` of the chunk's columns
+                    Eight at[4], mat[4];
+                    typename Epilogue::template Read<Eight> read[4], mread[4];
                     const int64_t col = col0 + 8 * (lane & 3);
-                    const int count = (int)min((int64_t)8, s.N - col);
-                    // the transposed chunk: row `lane` of its columns, eight of its rows at a time
-                    const int64_t mrow = col0 + lane;
-                    typename Epilogue::Read read[4], mread[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int64_t row = row0 + 8 * q + lane / 4;
-                        if (row < s.M && count > 0) read[q] = epi.read(row, col, count);
+                        at[q] = {row0 + 8 * q + lane / 4, col, (int)min((int64_t)8, s.N - col)};
+                        if (at[q].row >= s.M) at[q].count = 0;
+                        if (at[q].count > 0) read[q] = epi.read(tile.group, at[q]);
                     }
                     if (tile.mirror) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int64_t mcol = row0 + 8 * q;
-                            if (mrow < s.N && mcol < s.M) mread[q] = epi.read(mrow, mcol, (int)min((int64_t)8, s.M - mcol));
+                            mat[q] = {col0 + lane, row0 + 8 * q, (int)min((int64_t)8, s.M - (row0 + 8 * q))};
+                            if (mat[q].row >= s.N) mat[q].count = 0;
+                            if (mat[q].count > 0) mread[q] = epi.read(0, mat[q]);
                         }
                     }
-                    if (c == 0) {
-                        ok = wait_all<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                    }
+                    if (!ready()) break;
                     float v[4][8], w[Epilogue::kDual ? 4 : 1][8];
-                    fetch(d + column, v);
-                    if constexpr (Epilogue::kDual) fetch(d + 128 + column, w);
-                    if (c == kChunks - 1) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(bar(C::b_free + acc), 0));
-                    }
+                    auto vectors = [&](float (&x)[4][8]) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int64_t row = row0 + 8 * q + lane / 4;
-                        if (row < s.M && count > 0)
-                            epi.write(tile.group, row, col, count, v[q], w[Epilogue::kDual ? q : 0], read[q]);
+                        for (int q = 0; q < 4; ++q) {
+                            const float4* p =
+                                reinterpret_cast<const float4*>(scratch + (8 * q + lane / 4) * C::row + 8 * (lane & 3));
+                            const float4 f = p[0], g = p[1];
+                            x[q][0] = f.x, x[q][1] = f.y, x[q][2] = f.z, x[q][3] = f.w;
+                            x[q][4] = g.x, x[q][5] = g.y, x[q][6] = g.z, x[q][7] = g.w;
+                        }
+                    };
+                    stage(d + column);
+                    vectors(v);
+                    if constexpr (Epilogue::kDual) {
+                        stage(d + 128 + column);
+                        vectors(w);
                     }
+                    drained();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (at[q].count > 0) epi.write(tile.group, at[q], v[q], w[Epilogue::kDual ? q : 0], read[q]);
                     if (tile.mirror) {   // the scratch still has the chunk
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             float x[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) x[i] = scratch[(8 * q + i) * C::row + lane];
-                            const int64_t mcol = row0 + 8 * q;
-                            if (mrow < s.N && mcol < s.M)
-                                epi.write(0, mrow, mcol, (int)min((int64_t)8, s.M - mcol), x, x, mread[q]);
+                            if (mat[q].count > 0) epi.write(0, mat[q], x, x, mread[q]);
                         }
                     }
                 }
@@ -399,54 +451,85 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         };
         // Some vectors per thread at a time: their reads, and the loads of one block's part, are all under
         // way before the first is used (each trip to another block's shared memory takes some 500 clocks).
-        constexpr int kBatch = Epilogue::kDual ? 2 : 4;
+        constexpr int kBatch = Epilogue::kDual || sizeof(typename Epilogue::template Read<Eight>) > 16 ? 2 : 4;   // (registers)
         const int threads = s.split * C::threads, me = (int)rank * C::threads + threadIdx.x;
-        const int across = (cols + 7) / 8, units = rows * across;
-        for (int first = me; first < units; first += kBatch * threads) {
-            typename Epilogue::Read read[kBatch];
-            float v[kBatch][8], w[Epilogue::kDual ? kBatch : 1][8];
-            int row[kBatch], col[kBatch];
+        if (s.narrow) {
+            // a warp per row, four times 32 columns at a time
+            constexpr int kColumns = 4;
+            for (int r = (int)rank * (C::threads / 32) + warp; r < rows; r += s.split * (C::threads / 32))
+                for (int first = lane; first < cols; first += 32 * kColumns) {
+                    typename Epilogue::template Read<One> read[kColumns];
+                    float v[kColumns][1] = {}, w[kColumns][1] = {};
+                    auto at = [&](int q) {
+                        const int c = first + 32 * q;
+                        return One{(int64_t)tile.m + r, (int64_t)tile.n + c, c < cols};
+                    };
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-                const int u = first + q * threads;
-                row[q] = u / across, col[q] = (u - row[q] * across) * 8;
-                if (u < units) read[q] = epi.read((int64_t)tile.m + row[q], (int64_t)tile.n + col[q], min(8, cols - col[q]));
+                    for (int q = 0; q < kColumns; ++q) read[q] = epi.read(tile.group, at(q));
+                    for (int z = 0; z < s.split; ++z) {
+                        float x[kColumns][2] = {};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[q][i] = w[Epilogue::kDual ? q : 0][i] = 0.f;
-            }
-            for (int z = 0; z < s.split; ++z) {
-                float4 x[kBatch][Epilogue::kDual ? 4 : 2];
+                        for (int q = 0; q < kColumns; ++q)
+                            if (first + 32 * q < cols) {
+                                const uint32_t i = (uint32_t)(r * s.part_row + first + 32 * q);
+                                x[q][0] = element_at(i, z);
+                                if constexpr (Epilogue::kDual) x[q][1] = element_at(i + s.tile_n, z);
+                            }
 #pragma unroll
-                for (int q = 0; q < kBatch; ++q)
-                    if (first + q * threads < units)
-#pragma unroll
-                        for (int h = 0; h < (Epilogue::kDual ? 4 : 2); ++h)
-                            x[q][h] = part_at((uint32_t)(row[q] * s.part_row + col[q] + (h >> 1) * s.tile_n + (h & 1) * 4), z);
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q)
-                    if (first + q * threads < units) {
-                        add8(v[q], x[q][0], x[q][1]);
-                        if constexpr (Epilogue::kDual) add8(w[q], x[q][2], x[q][3]);
+                        for (int q = 0; q < kColumns; ++q) v[q][0] += x[q][0], w[q][0] += x[q][1];
                     }
-            }
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-                if (first + q * threads < units)
-                    epi.write(tile.group, (int64_t)tile.m + row[q], (int64_t)tile.n + col[q], min(8, cols - col[q]), v[q],
-                              w[Epilogue::kDual ? q : 0], read[q]);
+                    for (int q = 0; q < kColumns; ++q) epi.write(tile.group, at(q), v[q], w[q], read[q]);
+                }
+        } else {
+            const int across = (cols + 7) / 8, units = rows * across;
+            for (int first = me; first < units; first += kBatch * threads) {
+                Eight at[kBatch];
+                typename Epilogue::template Read<Eight> read[kBatch];
+                float v[kBatch][8], w[Epilogue::kDual ? kBatch : 1][8];
+                int line[kBatch];
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
+                    line[q] = r * s.part_row + c;
+                    at[q] = {(int64_t)tile.m + r, (int64_t)tile.n + c, u < units ? min(8, cols - c) : 0};
+                    if (at[q].count > 0) read[q] = epi.read(tile.group, at[q]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[q][i] = w[Epilogue::kDual ? q : 0][i] = 0.f;
+                }
+                for (int z = 0; z < s.split; ++z) {
+                    float4 x[kBatch][Epilogue::kDual ? 4 : 2];
+#pragma unroll
+                    for (int q = 0; q < kBatch; ++q)
+                        if (at[q].count > 0)
+#pragma unroll
+                            for (int h = 0; h < (Epilogue::kDual ? 4 : 2); ++h)
+                                x[q][h] = part_at((uint32_t)(line[q] + (h >> 1) * s.tile_n + (h & 1) * 4), z);
+#pragma unroll
+                    for (int q = 0; q < kBatch; ++q)
+                        if (at[q].count > 0) {
+                            add8(v[q], x[q][0], x[q][1]);
+                            if constexpr (Epilogue::kDual) add8(w[q], x[q][2], x[q][3]);
+                        }
+                }
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    if (at[q].count > 0) epi.write(tile.group, at[q], v[q], w[Epilogue::kDual ? q : 0], read[q]);
+            }
         }
         if (tile.mirror) {   // transposed: eight rows of one column
             const int down = (rows + 7) / 8, flipped = cols * down;
             for (int first = me; first < flipped; first += kBatch * threads) {
-                typename Epilogue::Read read[kBatch];
+                Eight at[kBatch];
+                typename Epilogue::template Read<Eight> read[kBatch];
                 float v[kBatch][8];
-                int row[kBatch], col[kBatch];
+                int line[kBatch];
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q) {
-                    const int u = first + q * threads, g = u / cols;
-                    row[q] = 8 * g, col[q] = u - g * cols;
-                    if (u < flipped)
-                        read[q] = epi.read((int64_t)tile.n + col[q], (int64_t)tile.m + row[q], min(8, rows - row[q]));
+                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
+                    line[q] = 8 * g * s.part_row + c;
+                    at[q] = {(int64_t)tile.n + c, (int64_t)tile.m + 8 * g, u < flipped ? min(8, rows - 8 * g) : 0};
+                    if (at[q].count > 0) read[q] = epi.read(tile.group, at[q]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[q][i] = 0.f;
                 }
@@ -454,21 +537,18 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     float x[kBatch][8];
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q)
-                        if (first + q * threads < flipped)
+                        if (at[q].count > 0)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                x[q][i] = element_at((uint32_t)((row[q] + i) * s.part_row + col[q]), z);
+                            for (int i = 0; i < 8; ++i) x[q][i] = element_at((uint32_t)(line[q] + i * s.part_row), z);
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q)
-                        if (first + q * threads < flipped)
+                        if (at[q].count > 0)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) v[q][i] += x[q][i];
                 }
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q)
-                    if (first + q * threads < flipped)
-                        epi.write(0, (int64_t)tile.n + col[q], (int64_t)tile.m + row[q], min(8, rows - row[q]), v[q], v[q],
-                                  read[q]);
+                    if (at[q].count > 0) epi.write(0, at[q], v[q], v[q], read[q]);
             }
         }
         ptx::cluster_arrive();   // the parts stay until every block has read them
@@ -548,9 +628,30 @@ struct Pair16<__half> {
 };
 __device__ __forceinline__ bool whole(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Elements as they are stored.
+template <class T, class Span>
+struct Raw {
+    static constexpr int words = (Span::n * (int)sizeof(T) + 3) / 4;
+    uint32_t u[words];
+    __device__ __forceinline__ void to(float (&v)[Span::n]) const {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < words; ++i) {
+                const float2 f = Pair16<T>::unpack(u[i]);
+                v[2 * i] = f.x;
+                if (2 * i + 1 < Span::n) v[2 * i + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < words; ++i) v[i] = __uint_as_float(u[i]);
+        }
+    }
+};
+
 // A matrix in memory; `elements` (of the whole matrix) bounds the accesses of a checked build.
 template <class T>
 struct Matrix {
+    using Value = std::remove_const_t<T>;
     T* ptr;
     int64_t ld;
     size_t elements;
@@ -558,67 +659,58 @@ struct Matrix {
     __device__ __forceinline__ bool ok(const T* p, int count, uint32_t site) const {
         return check::in(p, (size_t)count * sizeof(T), ptr, elements * sizeof(T), site);
     }
-    // Eight elements as they are stored.
-    struct Raw {
-        uint4 u[sizeof(T) / 2];
-        __device__ __forceinline__ void to(float (&v)[8]) const {
-            if constexpr (sizeof(T) == 2) {
-                using P = Pair16<std::remove_const_t<T>>;
-                const float2 a = P::unpack(u[0].x), b = P::unpack(u[0].y), c = P::unpack(u[0].z), d = P::unpack(u[0].w);
-                v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
-            } else {
+    __device__ __forceinline__ static uint32_t bits(const T* p) {
+        if constexpr (sizeof(T) == 2)
+            return *reinterpret_cast<const uint16_t*>(p);
+        else
+            return *reinterpret_cast<const uint32_t*>(p);
+    }
+    __device__ __forceinline__ Raw<Value, Eight> raw(const Eight& at, uint32_t site) const {
+        const T* p = ptr + at.row * ld + at.col;
+        Raw<Value, Eight> r{};
+        if (!ok(p, at.count, site)) return r;
+        if (at.count == 8 && whole(p)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    v[4 * i] = __uint_as_float(u[i].x), v[4 * i + 1] = __uint_as_float(u[i].y);
-                    v[4 * i + 2] = __uint_as_float(u[i].z), v[4 * i + 3] = __uint_as_float(u[i].w);
-                }
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+                r.u[4 * i] = q.x, r.u[4 * i + 1] = q.y, r.u[4 * i + 2] = q.z, r.u[4 * i + 3] = q.w;
             }
-        }
-    };
-    __device__ __forceinline__ Raw raw(int64_t row, int64_t col, int count, uint32_t site) const {
-        const T* p = ptr + row * ld + col;
-        Raw r;
-        if (!ok(p, count, site)) return r = Raw{};
-        if (count == 8 && whole(p)) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
             return r;
         }
-        uint32_t* w = reinterpret_cast<uint32_t*>(r.u);
-        if constexpr (sizeof(T) == 2) {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a = 2 * i < count ? h[2 * i] : 0, b = 2 * i + 1 < count ? h[2 * i + 1] : 0;
-                w[i] = a | b << 16;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = i < count ? reinterpret_cast<const uint32_t*>(p)[i] : 0;
-        }
+        for (int i = 0; i < 8; ++i)
+            if (i < at.count) r.u[i * (int)sizeof(T) / 4] |= bits(p + i) << (sizeof(T) == 2 ? 16 * (i & 1) : 0);
         return r;
     }
-    __device__ __forceinline__ void load(int64_t row, int64_t col, int count, float (&v)[8], uint32_t site) const {
-        raw(row, col, count, site).to(v);
+    __device__ __forceinline__ Raw<Value, One> raw(const One& at, uint32_t site) const {
+        const T* p = ptr + at.row * ld + at.col;
+        Raw<Value, One> r{};
+        if (at.is && ok(p, 1, site)) r.u[0] = bits(p);
+        return r;
     }
-    __device__ __forceinline__ void store(int64_t row, int64_t col, int count, const float (&v)[8], uint32_t site) const {
-        T* p = ptr + row * ld + col;
-        if (!ok(p, count, site)) return;
-        if constexpr (sizeof(T) == 2) {
-            if (count == 8 && whole(p)) {
+    __device__ __forceinline__ void store(const Eight& at, const float (&v)[8], uint32_t site) const {
+        T* p = ptr + at.row * ld + at.col;
+        if (!ok(p, at.count, site)) return;
+        if (at.count == 8 && whole(p)) {
+            if constexpr (sizeof(T) == 2) {
                 *reinterpret_cast<uint4*>(p) = make_uint4(Pair16<T>::pack(v[0], v[1]), Pair16<T>::pack(v[2], v[3]),
                                                           Pair16<T>::pack(v[4], v[5]), Pair16<T>::pack(v[6], v[7]));
-                return;
+            } else {
+                reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
-        } else if (count == 8 && whole(p)) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
             return;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < count) p[i] = (T)v[i];
+            if (i < at.count) p[i] = (T)v[i];
     }
+    __device__ __forceinline__ void store(const One& at, const float (&v)[1], uint32_t site) const {
+        T* p = ptr + at.row * ld + at.col;
+        if (at.is && ok(p, 1, site)) *p = (T)v[0];
+    }
+    // whether rows start at 16 bytes (the first one does)
+    bool even() const { return ptr == nullptr || ld * (int64_t)sizeof(T) % 16 == 0; }
 };
 
 }  // namespace product

@@ -5,8 +5,8 @@
 //
 // One block of 16 warps per SM; the block's rows of weights are a contiguous 152nd
 // of all.  Four warps share a row's k (quarters), four such groups take two pairs of
-// gate and up rows (or four rows of the second product) at a time: eight 16-byte
-// loads per thread are under way, 64 KB per SM.  x lies in shared memory in FP32.
+// gate and up rows (or four rows of the second product) at a time: twelve 16-byte
+// loads per thread are under way, 96 KB per SM (eight: 3% slower).  x lies in shared memory in FP32.
 // Sums are FP32 in a fixed order: per thread, over the lanes, over the quarters.
 // Rows that do not start at 16 bytes are read as 4-byte words, with x shifted by one
 // element for rows that start in the middle of one.
@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kBlocks = 152, kThreads = 512, kQuarters = 4, kGroups = kThreads / 32 / kQuarters;
 constexpr int kRows = 4;       // weight rows of a warp at a time
-constexpr int kUnroll = 2;
+constexpr int kUnroll = 3;
 
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
@@ -66,7 +66,7 @@ size_t token_smem(int tokens, int K, int64_t R, bool dual) {
 }
 
 template <class T, int NT, bool DUAL, bool WIDE>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) token_kernel(const TokenArgs<T> a) {
+__global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T> a) {
     extern __shared__ float4 shared[];
     float* xs = reinterpret_cast<float*>(shared);
     constexpr int kOutputs = DUAL ? kRows / 2 : kRows;     // rows of the output per warp and turn
@@ -236,7 +236,10 @@ cudaError_t launch(const TokenArgs<T>& a, cudaStream_t stream) {
     auto* kernel = token_kernel<T, NT, DUAL, WIDE>;
     const cudaError_t e = ops::allow_shared(kernel, (int)product::kSharedMost, done);
     if (e != cudaSuccess) return e;
-    return ops::launch_early(kernel, dim3(kBlocks), dim3(kThreads), token_smem<WIDE>(NT, a.K, a.R, DUAL), stream, a);
+    // at least half of an SM's shared memory: of two blocks that fit one SM, some SMs would get both when
+    // the launch before ends, and others none (the pair of launches took 85 us for 75)
+    const size_t smem = token_smem<WIDE>(NT, a.K, a.R, DUAL), half = 120 * 1024;
+    return ops::launch_early(kernel, dim3(kBlocks), dim3(kThreads), smem > half ? smem : half, stream, a);
 }
 template <class T, bool DUAL, bool WIDE>
 cudaError_t by_tokens(const TokenArgs<T>& a, cudaStream_t stream) {
