@@ -25,7 +25,7 @@ using product::Shape;
 
 template <class T>
 struct GatedEpilogue {
-    static constexpr bool kDual = true;
+    static constexpr bool kDual = true, kMirror = false;
     Matrix<T> hidden, gate, up;
     int activation;
     template <class Span>
@@ -50,7 +50,7 @@ struct GatedEpilogue {
 
 template <class T>
 struct GradEpilogue {
-    static constexpr bool kDual = false;
+    static constexpr bool kDual = false, kMirror = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
     int activation;
     template <class Span>
@@ -82,7 +82,7 @@ struct GradEpilogue {
 
 template <class O>
 struct StoreEpilogue {
-    static constexpr bool kDual = false;
+    static constexpr bool kDual = false, kMirror = false;
     Matrix<O> out[2];
     bool accumulate;
     template <class Span>
@@ -152,6 +152,7 @@ cudaError_t make(product::Factor& f, bool bf16, const void* p, int64_t rows, int
     return e != cudaSuccess ? e : f.make(bf16, copy, rows, cols, wide);
 }
 
+// (a workspace's matrix: cols = ld, its padding may be written)
 template <class T>
 Matrix<T> matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
     return {static_cast<T*>(const_cast<void*>(p)), ld, p == nullptr ? 0 : (size_t)((rows - 1) * ld + cols)};
@@ -178,13 +179,13 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     Shape s{};
     s.bf16 = bf16;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
-    const GatedEpilogue<T> gated{matrix<T>(hidden, T_, F, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
+    const GatedEpilogue<T> gated{matrix<T>(hidden, T_, Fp, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
                                  a.activation};
-    s.narrow = !gated.gate.even();
+    s.narrow = !gated.gate.by_eight(F);
     MHCM_TRY(product::launch(s, gated, &x, nullptr, &wg, &wu, stream));
     s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain;
     const StoreEpilogue<T> store{{matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
-    s.narrow = !store.out[0].even();
+    s.narrow = !store.out[0].by_eight(D);
     return product::launch(s, store, &h, nullptr, &wd, nullptr, stream);
 }
 
@@ -198,7 +199,7 @@ cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const
     s.a_mn = s.b_mn = 1;
     s.beside = beside;
     const StoreEpilogue<O> store{{matrix<O>(out0, M, N, N), matrix<O>(out1, M, N, N)}, a.accumulate};
-    s.narrow = !store.out[0].even();
+    s.narrow = !store.out[0].by_eight(N);
     return product::launch(s, store, a0, a1, b, b, stream);
 }
 
@@ -225,9 +226,9 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     s.bf16 = bf16;
     s.stall = a.stall;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.b_mn = 1;
-    const GradEpilogue<T> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, F, Fp),
-                               matrix<T>(grad_up, T_, F, Fp), matrix<T>(hidden, T_, F, Fp), a.activation};
-    s.narrow = !grad.gate.even();
+    const GradEpilogue<T> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, Fp, Fp),
+                               matrix<T>(grad_up, T_, Fp, Fp), matrix<T>(hidden, T_, Fp, Fp), a.activation};
+    s.narrow = !grad.gate.by_eight(F);
     MHCM_TRY(product::launch(s, grad, &dy, nullptr, &wd, nullptr, stream));
     // The products that are left need only what the first wrote: each starts as soon as the one
     // before it leaves room (its last tiles keep a part of the GPU busy), not when that has ended.
@@ -236,7 +237,7 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     if (a.grad_x) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
         const StoreEpilogue<T> store{{matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
-        s.narrow = !store.out[0].even();
+        s.narrow = !store.out[0].by_eight(D);
         MHCM_TRY(product::launch(s, store, &dg, &du, &wg, &wu, stream));
         beside = true;
     }

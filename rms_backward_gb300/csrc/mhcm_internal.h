@@ -30,7 +30,7 @@ struct Shape {
     int beside;        // needs nothing of the launch before it, only of one before that (which the launch
                        // before it waited for): it does not wait for that one to end before its work, but
                        // before its own end, so that it still ends after it
-    int narrow;        // rows of a matrix of the epilogue do not start at 16 bytes
+    int narrow;        // the epilogue's matrices are taken element by element (see Eight)
     int stall;         // a test's: the MMA issuer waits for what nothing signals
     // set by choose()
     int m_tiles, n_tiles, tiles;

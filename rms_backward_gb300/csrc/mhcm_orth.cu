@@ -44,6 +44,7 @@ struct Input {
     int type;
     int64_t rows, ld, cols;
     // elements as they are stored (a 16-bit type's in the first half of the words), and as FP32
+    bool by_eight() const { return cols % 8 == 0 && ld * (type == MHCPB_FP32 ? 4 : 2) % 16 == 0; }
     template <class Span>
     __device__ __forceinline__ product::Raw<float, Span> raw(const Span& at, uint32_t site) const {
         const size_t n = (size_t)((rows - 1) * ld + cols);
@@ -67,9 +68,6 @@ struct Input {
 #pragma unroll
         for (int i = 0; i < h.words; ++i) h.u[i] = r.u[i];
         h.to(v);
-    }
-    __device__ __forceinline__ void load(const product::Eight& at, float (&v)[8], uint32_t site) const {
-        to(raw(at, site), v);
     }
 };
 
@@ -106,23 +104,49 @@ __device__ __forceinline__ double block_sum(double v) {
     return v;
 }
 
+// The norm's kernels go over G in pieces of 1024 elements of a row, a warp each: eight neighbours per lane
+// four times, or one 32 times.
+template <bool EIGHT, class Each>
+__device__ __forceinline__ void over_pieces(const Input& g, int site, Each each) {
+    constexpr int kWidth = EIGHT ? 8 : 1, kAtOnce = EIGHT ? 4 : 8;
+    using Span = std::conditional_t<EIGHT, product::Eight, product::One>;
+    const int64_t across = (g.cols + 1023) / 1024, pieces = g.rows * across;
+    const int64_t warps = (int64_t)gridDim.x * (kNormThreads / 32);
+    for (int64_t i = (int64_t)blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32; i < pieces; i += warps) {
+        const int64_t row = i / across, end = min(g.cols, (i - row * across + 1) * 1024);
+        for (int64_t col = (i - row * across) * 1024 + (threadIdx.x & 31) * kWidth; col < end; col += 32 * kWidth * kAtOnce) {
+            product::Raw<float, Span> raw[kAtOnce];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const Span at{row, col + 32 * kWidth * q, col + 32 * kWidth * q < end};
+                if (at.is) raw[q] = g.raw(at, site);
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const Span at{row, col + 32 * kWidth * q, col + 32 * kWidth * q < end};
+                if (!at.is) continue;
+                float v[Span::n];
+                g.to(raw[q], v);
+                each(at, v);
+            }
+        }
+    }
+}
+
+template <bool EIGHT>
 __global__ void __launch_bounds__(kNormThreads) squares_kernel(const Input g, double* partial) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int64_t across = (g.cols + 7) / 8, units = g.rows * across;
     Squares s;
-    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < units; i += (int64_t)kNormBlocks * kNormThreads) {
-        const int64_t r = i / across, c = (i - r * across) * 8;
-        float v[8];
-        g.load(product::Eight{r, c, (int)min((int64_t)8, g.cols - c)}, v, 0);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s.add(v[k]);
-    }
+    over_pieces<EIGHT>(g, 0, [&](const auto&, const auto& v) {
+        for (float e : v) s.add(e);
+    });
     const double total = block_sum(s.sum());
     if (threadIdx.x == 0 && check::in(partial + blockIdx.x, 8, partial, kNormBlocks * 8, 1)) partial[blockIdx.x] = total;
 }
 
 // FP16 copy of G / (|G| + eps), and the factors for later.
+template <bool EIGHT>
 __global__ void __launch_bounds__(kNormThreads)
     first_copy_kernel(const Input g, const double* partial, double eps, Inverse* inverse, Matrix<__half> x) {
     ptx::grid_dependency_wait();
@@ -138,16 +162,13 @@ __global__ void __launch_bounds__(kNormThreads)
     inv.p = exp2f((float)(-e / 2));
     inv.q = exp2f((float)(-(e - e / 2)));
     if (blockIdx.x == 0 && threadIdx.x == 0) *inverse = inv;
-    const int64_t across = (g.cols + 7) / 8, units = g.rows * across;
-    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < units; i += (int64_t)gridDim.x * kNormThreads) {
-        const int64_t r = i / across, c = (i - r * across) * 8;
-        const product::Eight at{r, c, (int)min((int64_t)8, g.cols - c)};
-        float v[8];
-        g.load(at, v, 2);
+    over_pieces<EIGHT>(g, 2, [&](const auto& at, const auto& v) {
+        using Span = std::decay_t<decltype(at)>;
+        float r[Span::n];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = scaled(v[k], inv) * kScaleX;
-        x.store(at, v, 3);
-    }
+        for (int k = 0; k < Span::n; ++k) r[k] = scaled(v[k], inv) * kScaleX;
+        x.store(at, r, 3);
+    });
 }
 
 // What an FP16 matrix's diagonal lost to rounding, FP32 [size], in the matrix's units.
@@ -162,14 +183,14 @@ struct Diagonal {
     __device__ __forceinline__ void keep(const Span& at, const float (&v)[Span::n], float scale, uint32_t site) const {
 #pragma unroll
         for (int i = 0; i < Span::n; ++i)
-            if (at.valid(i) && at.row == at.column(i) && check::in(lost + at.row, 4, lost, (size_t)size * 4, site))
+            if (at.row == at.column(i) && check::in(lost + at.row, 4, lost, (size_t)size * 4, site))
                 lost[at.row] = (v[i] - __half2float(__float2half_rn(v[i]))) / scale;
     }
 };
 
 // A = C at kScaleA
 struct GramEpilogue {
-    static constexpr bool kDual = false;
+    static constexpr bool kDual = false, kMirror = true;
     Matrix<__half> out;
     Diagonal lost;
     template <class Span>
@@ -192,7 +213,7 @@ struct GramEpilogue {
 // B = b A + c A^2 at kScaleB from C, the product of the rounded A's, and what the
 // diagonal lost: (A + l)^2 = A^2 + l A + A l + l^2
 struct PolynomialEpilogue {
-    static constexpr bool kDual = false;
+    static constexpr bool kDual = false, kMirror = true;
     Matrix<__half> out;
     Matrix<const __half> gram;
     Diagonal gram_lost, lost;
@@ -212,7 +233,7 @@ struct PolynomialEpilogue {
         const float l = gram_lost.at(at.row, 7);
 #pragma unroll
         for (int i = 0; i < Span::n; ++i) {
-            const float k = at.valid(i) ? gram_lost.at(at.column(i), 8) : 0.f;
+            const float k = gram_lost.at(at.column(i), 8);
             r[i] = fmaf(kC * kScaleB / (kScaleA * kScaleA), v[i], (kB + kC * (l + k)) * (kScaleB / kScaleA) * r[i]);
             if (at.row == at.column(i)) r[i] += kScaleB * (kB + kC * l) * l;
         }
@@ -223,7 +244,7 @@ struct PolynomialEpilogue {
 
 // X = (a + B's lost diagonal) X + C
 struct UpdateEpilogue {
-    static constexpr bool kDual = false;
+    static constexpr bool kDual = false, kMirror = false;
     Input g;                    // the first step's X, times *inverse
     const Inverse* inverse;     // null after the first step
     Diagonal lost;
@@ -250,10 +271,10 @@ struct UpdateEpilogue {
         } else {
             in.to(r);
         }
-        const float by_row = tall || !at.valid(0) ? 0.f : lost.at(at.row, 13);
+        const float by_row = tall || !at.is ? 0.f : lost.at(at.row, 13);
 #pragma unroll
         for (int i = 0; i < Span::n; ++i) {
-            const float l = tall && at.valid(i) ? lost.at(at.column(i), 14) : by_row;
+            const float l = tall && at.is ? lost.at(at.column(i), 14) : by_row;
             r[i] = fmaf(kA + l, r[i], v[i] * (1.f / (kScaleB * kScaleX)));
         }
         if (out.ptr != nullptr) {
@@ -286,8 +307,8 @@ Layout layout(int64_t m, int64_t n) {
     };
     l.partial = take(kNormBlocks * sizeof(double));
     l.inverse = take(sizeof(Inverse));
-    l.lost[0] = take((size_t)s * 4);
-    l.lost[1] = take((size_t)s * 4);
+    l.lost[0] = take((size_t)sp * 4);
+    l.lost[1] = take((size_t)sp * 4);
     l.x = take((size_t)(m * np) * 4);
     l.copy[0] = take((size_t)(m * np) * 2);
     l.copy[1] = take((size_t)(m * np) * 2);
@@ -314,15 +335,15 @@ cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
     char* ws = static_cast<char*>(a.workspace);
     double* partial = reinterpret_cast<double*>(ws + l.partial);
     Inverse* inverse = reinterpret_cast<Inverse*>(ws + l.inverse);
-    const Diagonal gram_lost{reinterpret_cast<float*>(ws + l.lost[0]), s}, poly_lost{reinterpret_cast<float*>(ws + l.lost[1]), s};
+    const Diagonal gram_lost{reinterpret_cast<float*>(ws + l.lost[0]), sp}, poly_lost{reinterpret_cast<float*>(ws + l.lost[1]), sp};
     const Input g{a.g, a.type, m, a.g_stride, n};
-    auto half_matrix = [&](size_t at, int64_t rows, int64_t cols, int64_t ld) {
-        return Matrix<__half>{reinterpret_cast<__half*>(ws + at), ld, (size_t)((rows - 1) * ld + cols)};
+    auto half_matrix = [&](size_t at, int64_t rows, int64_t ld) {
+        return Matrix<__half>{reinterpret_cast<__half*>(ws + at), ld, (size_t)(rows * ld)};
     };
-    const Matrix<__half> copies[2] = {half_matrix(l.copy[0], m, n, np), half_matrix(l.copy[1], m, n, np)};
-    const Matrix<__half> gram = half_matrix(l.gram, s, s, sp), poly = half_matrix(l.poly, s, s, sp);
+    const Matrix<__half> copies[2] = {half_matrix(l.copy[0], m, np), half_matrix(l.copy[1], m, np)};
+    const Matrix<__half> gram = half_matrix(l.gram, s, sp), poly = half_matrix(l.poly, s, sp);
     const Matrix<const __half> gram_in{gram.ptr, gram.ld, gram.elements};
-    const Matrix<float> x{reinterpret_cast<float*>(ws + l.x), np, (size_t)((m - 1) * np + n)};
+    const Matrix<float> x{reinterpret_cast<float*>(ws + l.x), np, (size_t)(m * np)};
     const Matrix<__nv_bfloat16> out{static_cast<__nv_bfloat16*>(a.out), a.out_stride, (size_t)((m - 1) * a.out_stride + n)};
     product::Factor factor_x[2], factor_gram, factor_poly;
     MHCM_TRY(factor_x[0].make(false, copies[0].ptr, m, n, np));
@@ -330,10 +351,13 @@ cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
     MHCM_TRY(factor_gram.make(false, gram.ptr, s, s, sp));
     MHCM_TRY(factor_poly.make(false, poly.ptr, s, s, sp));
 
-    const int64_t units = m * ((n + 7) / 8), blocks = (units + kNormThreads - 1) / kNormThreads;
-    MHCM_TRY(ops::launch_early(squares_kernel, dim3(kNormBlocks), dim3(kNormThreads), 0, stream, g, partial));
-    MHCM_TRY(ops::launch_early(first_copy_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(kNormThreads), 0,
-                               stream, g, static_cast<const double*>(partial), static_cast<double>(a.eps), inverse, copies[0]));
+    const bool eight = g.by_eight();
+    MHCM_TRY(ops::launch_early(eight ? squares_kernel<true> : squares_kernel<false>, dim3(kNormBlocks), dim3(kNormThreads),
+                               0, stream, g, partial));
+    const int64_t blocks = (m * ((n + 1023) / 1024) + kNormThreads / 32 - 1) / (kNormThreads / 32);
+    MHCM_TRY(ops::launch_early(eight ? first_copy_kernel<true> : first_copy_kernel<false>,
+                               dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(kNormThreads), 0, stream, g,
+                               static_cast<const double*>(partial), static_cast<double>(a.eps), inverse, copies[0]));
     for (int i = 0; i < a.steps; ++i) {
         const product::Factor* cur = &factor_x[i & 1];
         Shape p{};
@@ -348,9 +372,8 @@ cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
         const bool last = i + 1 == a.steps;
         const UpdateEpilogue update{g, i == 0 ? inverse : nullptr, poly_lost, tall, x, copies[(i + 1) & 1],
                                     last ? out : Matrix<__nv_bfloat16>{nullptr, 0, 0}, a.scale};
-        // G in the first step and the output in the last may have rows that do not start at 16 bytes
-        const bool g_even = a.g_stride * (a.type == MHCPB_FP32 ? 4 : 2) % 16 == 0;
-        p.narrow = (i == 0 && !g_even) || (last && !out.even());
+        // G in the first step and the output in the last are the caller's
+        p.narrow = (i == 0 && !g.by_eight()) || (last && !out.by_eight(n));
         if (tall)
             MHCM_TRY(product::launch(p, update, cur, nullptr, &factor_poly, nullptr, stream));
         else

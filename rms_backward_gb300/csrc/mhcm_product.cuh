@@ -133,25 +133,25 @@ __device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float
     v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
 }
 
-// The elements of one row of C that an epilogue takes at a time: eight neighbours (the last ones of a
-// row fewer), or, for matrices whose rows do not start at 16 bytes, one (a warp then has 32 neighbours).
+// The elements of one row of C that an epilogue takes at a time: eight neighbours, where the epilogue's
+// matrices have rows that start at 16 bytes and end at them or in a workspace's padding (which may be
+// written), else one (a warp then has 32 neighbours).
 struct Eight {
     static constexpr int n = 8;
     int64_t row, col;
-    int count;
+    bool is;             // elements of C
     __device__ __forceinline__ int64_t column(int i) const { return col + i; }
-    __device__ __forceinline__ bool valid(int i) const { return i < count; }
 };
 struct One {
     static constexpr int n = 1;
     int64_t row, col;
-    bool is;             // an element of C
+    bool is;
     __device__ __forceinline__ int64_t column(int) const { return col; }
-    __device__ __forceinline__ bool valid(int) const { return is; }
 };
 
 // Epilogue: struct with
 //   static constexpr bool kDual                    two products side by side
+//   static constexpr bool kMirror                  C is symmetric; its matrices are a workspace's (Eight always)
 //   template <class Span> struct Read              what elements' results need from memory
 //   Read<Span> read(int group, const Span&) const
 //   void write(int group, const Span&, const float (&v)[Span::n], const float (&w)[Span::n], const Read<Span>&) const
@@ -332,14 +332,11 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                             if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(bar(C::b_free + acc), 0));
                         }
                     };
-                    if (s.narrow) {
-                        // column `lane` of each row, sixteen rows' reads at a time, the first before the wait
-                        typename Epilogue::template Read<One> read[16];
+                    if (!Epilogue::kMirror && s.narrow) {
+                        // column `lane` of each row, eight rows' reads at a time
                         auto at = [&](int row) {
                             return One{row0 + row, col0 + lane, col0 + lane < s.N && row0 + row < s.M};
                         };
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) read[q] = epi.read(tile.group, at(q));
                         if (!ready()) break;
                         float w[Epilogue::kDual ? 32 : 1];
                         if constexpr (Epilogue::kDual) {
@@ -349,14 +346,17 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                         }
                         stage(d + column);
                         drained();
+#pragma unroll(Epilogue::kDual ? 4 : 1)
+                        for (int first = 0; first < 32; first += 8) {
+                            typename Epilogue::template Read<One> read[8];
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) {
-                            if (q == 16)
+                            for (int q = 0; q < 8; ++q) read[q] = epi.read(tile.group, at(first + q));
 #pragma unroll
-                                for (int r = 0; r < 16; ++r) read[r] = epi.read(tile.group, at(16 + r));
-                            const float v[1] = {scratch[q * C::row + lane]};
-                            const float u[1] = {w[Epilogue::kDual ? q : 0]};
-                            epi.write(tile.group, at(q), v, u, read[q & 15]);
+                            for (int q = 0; q < 8; ++q) {
+                                const float v[1] = {scratch[(first + q) * C::row + lane]};
+                                const float u[1] = {w[Epilogue::kDual ? first + q : 0]};
+                                epi.write(tile.group, at(first + q), v, u, read[q]);
+                            }
                         }
                         continue;
                     }
@@ -366,16 +366,14 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     const int64_t col = col0 + 8 * (lane & 3);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        at[q] = {row0 + 8 * q + lane / 4, col, (int)min((int64_t)8, s.N - col)};
-                        if (at[q].row >= s.M) at[q].count = 0;
-                        if (at[q].count > 0) read[q] = epi.read(tile.group, at[q]);
+                        at[q] = {row0 + 8 * q + lane / 4, col, col < s.N && row0 + 8 * q + lane / 4 < s.M};
+                        if (at[q].is) read[q] = epi.read(tile.group, at[q]);
                     }
-                    if (tile.mirror) {
+                    if (Epilogue::kMirror && tile.mirror) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            mat[q] = {col0 + lane, row0 + 8 * q, (int)min((int64_t)8, s.M - (row0 + 8 * q))};
-                            if (mat[q].row >= s.N) mat[q].count = 0;
-                            if (mat[q].count > 0) mread[q] = epi.read(0, mat[q]);
+                            mat[q] = {col0 + lane, row0 + 8 * q, col0 + lane < s.N && row0 + 8 * q < s.M};
+                            if (mat[q].is) mread[q] = epi.read(0, mat[q]);
                         }
                     }
                     if (!ready()) break;
@@ -399,14 +397,14 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     drained();
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        if (at[q].count > 0) epi.write(tile.group, at[q], v[q], w[Epilogue::kDual ? q : 0], read[q]);
-                    if (tile.mirror) {   // the scratch still has the chunk
+                        if (at[q].is) epi.write(tile.group, at[q], v[q], w[Epilogue::kDual ? q : 0], read[q]);
+                    if (Epilogue::kMirror && tile.mirror) {   // the scratch still has the chunk
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             float x[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) x[i] = scratch[(8 * q + i) * C::row + lane];
-                            if (mat[q].count > 0) epi.write(0, mat[q], x, x, mread[q]);
+                            if (mat[q].is) epi.write(0, mat[q], x, x, mread[q]);
                         }
                     }
                 }
@@ -453,7 +451,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         // way before the first is used (each trip to another block's shared memory takes some 500 clocks).
         constexpr int kBatch = Epilogue::kDual || sizeof(typename Epilogue::template Read<Eight>) > 16 ? 2 : 4;   // (registers)
         const int threads = s.split * C::threads, me = (int)rank * C::threads + threadIdx.x;
-        if (s.narrow) {
+        if (!Epilogue::kMirror && s.narrow) {
             // a warp per row, four times 32 columns at a time
             constexpr int kColumns = 4;
             for (int r = (int)rank * (C::threads / 32) + warp; r < rows; r += s.split * (C::threads / 32))
@@ -492,8 +490,8 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 for (int q = 0; q < kBatch; ++q) {
                     const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
                     line[q] = r * s.part_row + c;
-                    at[q] = {(int64_t)tile.m + r, (int64_t)tile.n + c, u < units ? min(8, cols - c) : 0};
-                    if (at[q].count > 0) read[q] = epi.read(tile.group, at[q]);
+                    at[q] = {(int64_t)tile.m + r, (int64_t)tile.n + c, u < units};
+                    if (at[q].is) read[q] = epi.read(tile.group, at[q]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[q][i] = w[Epilogue::kDual ? q : 0][i] = 0.f;
                 }
@@ -501,23 +499,23 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     float4 x[kBatch][Epilogue::kDual ? 4 : 2];
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q)
-                        if (at[q].count > 0)
+                        if (at[q].is)
 #pragma unroll
                             for (int h = 0; h < (Epilogue::kDual ? 4 : 2); ++h)
                                 x[q][h] = part_at((uint32_t)(line[q] + (h >> 1) * s.tile_n + (h & 1) * 4), z);
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q)
-                        if (at[q].count > 0) {
+                        if (at[q].is) {
                             add8(v[q], x[q][0], x[q][1]);
                             if constexpr (Epilogue::kDual) add8(w[q], x[q][2], x[q][3]);
                         }
                 }
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q)
-                    if (at[q].count > 0) epi.write(tile.group, at[q], v[q], w[Epilogue::kDual ? q : 0], read[q]);
+                    if (at[q].is) epi.write(tile.group, at[q], v[q], w[Epilogue::kDual ? q : 0], read[q]);
             }
         }
-        if (tile.mirror) {   // transposed: eight rows of one column
+        if (Epilogue::kMirror && tile.mirror) {   // transposed: eight rows of one column
             const int down = (rows + 7) / 8, flipped = cols * down;
             for (int first = me; first < flipped; first += kBatch * threads) {
                 Eight at[kBatch];
@@ -528,8 +526,8 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 for (int q = 0; q < kBatch; ++q) {
                     const int u = first + q * threads, g = u / cols, c = u - g * cols;
                     line[q] = 8 * g * s.part_row + c;
-                    at[q] = {(int64_t)tile.n + c, (int64_t)tile.m + 8 * g, u < flipped ? min(8, rows - 8 * g) : 0};
-                    if (at[q].count > 0) read[q] = epi.read(tile.group, at[q]);
+                    at[q] = {(int64_t)tile.n + c, (int64_t)tile.m + 8 * g, u < flipped};
+                    if (at[q].is) read[q] = epi.read(tile.group, at[q]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[q][i] = 0.f;
                 }
@@ -537,18 +535,18 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     float x[kBatch][8];
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q)
-                        if (at[q].count > 0)
+                        if (at[q].is)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) x[q][i] = element_at((uint32_t)(line[q] + i * s.part_row), z);
 #pragma unroll
                     for (int q = 0; q < kBatch; ++q)
-                        if (at[q].count > 0)
+                        if (at[q].is)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) v[q][i] += x[q][i];
                 }
 #pragma unroll
                 for (int q = 0; q < kBatch; ++q)
-                    if (at[q].count > 0) epi.write(0, at[q], v[q], v[q], read[q]);
+                    if (at[q].is) epi.write(0, at[q], v[q], v[q], read[q]);
             }
         }
         ptx::cluster_arrive();   // the parts stay until every block has read them
@@ -626,7 +624,6 @@ struct Pair16<__half> {
         return __half22float2(*reinterpret_cast<const __half2*>(&u));
     }
 };
-__device__ __forceinline__ bool whole(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Elements as they are stored.
 template <class T, class Span>
@@ -668,18 +665,12 @@ struct Matrix {
     __device__ __forceinline__ Raw<Value, Eight> raw(const Eight& at, uint32_t site) const {
         const T* p = ptr + at.row * ld + at.col;
         Raw<Value, Eight> r{};
-        if (!ok(p, at.count, site)) return r;
-        if (at.count == 8 && whole(p)) {
+        if (!ok(p, 8, site)) return r;
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-                const uint4 q = reinterpret_cast<const uint4*>(p)[i];
-                r.u[4 * i] = q.x, r.u[4 * i + 1] = q.y, r.u[4 * i + 2] = q.z, r.u[4 * i + 3] = q.w;
-            }
-            return r;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+            r.u[4 * i] = q.x, r.u[4 * i + 1] = q.y, r.u[4 * i + 2] = q.z, r.u[4 * i + 3] = q.w;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < at.count) r.u[i * (int)sizeof(T) / 4] |= bits(p + i) << (sizeof(T) == 2 ? 16 * (i & 1) : 0);
         return r;
     }
     __device__ __forceinline__ Raw<Value, One> raw(const One& at, uint32_t site) const {
@@ -690,27 +681,21 @@ struct Matrix {
     }
     __device__ __forceinline__ void store(const Eight& at, const float (&v)[8], uint32_t site) const {
         T* p = ptr + at.row * ld + at.col;
-        if (!ok(p, at.count, site)) return;
-        if (at.count == 8 && whole(p)) {
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<uint4*>(p) = make_uint4(Pair16<T>::pack(v[0], v[1]), Pair16<T>::pack(v[2], v[3]),
-                                                          Pair16<T>::pack(v[4], v[5]), Pair16<T>::pack(v[6], v[7]));
-            } else {
-                reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-            }
-            return;
+        if (!ok(p, 8, site)) return;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(Pair16<T>::pack(v[0], v[1]), Pair16<T>::pack(v[2], v[3]),
+                                                      Pair16<T>::pack(v[4], v[5]), Pair16<T>::pack(v[6], v[7]));
+        } else {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < at.count) p[i] = (T)v[i];
     }
     __device__ __forceinline__ void store(const One& at, const float (&v)[1], uint32_t site) const {
         T* p = ptr + at.row * ld + at.col;
         if (at.is && ok(p, 1, site)) *p = (T)v[0];
     }
-    // whether rows start at 16 bytes (the first one does)
-    bool even() const { return ptr == nullptr || ld * (int64_t)sizeof(T) % 16 == 0; }
+    // whether a caller's matrix of `cols` columns can be read and written by Eight (its first row starts at 16 bytes)
+    bool by_eight(int64_t cols) const { return ptr == nullptr || (cols % 8 == 0 && ld * (int64_t)sizeof(T) % 16 == 0); }
 };
 
 }  // namespace product
