@@ -104,23 +104,50 @@ struct StoreEpilogue {
     }
 };
 
-// dst[r, 0..cols) = src[r, 0..cols), rows dst_ld (a multiple of 8) apart
-__global__ void __launch_bounds__(256) copy_rows_kernel(const uint16_t* src, int64_t src_ld, int64_t rows, int64_t cols,
-                                                        uint16_t* dst, int64_t dst_ld) {
+// Matrices whose rows are copied to rows `dst_ld` (a multiple of 8) apart, in one launch.
+constexpr int kMaxCopies = 5;
+struct Copy {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t src_ld, dst_ld, rows, cols;
+    int64_t first;   // vectors of eight before this matrix
+};
+struct Copies {
+    Copy c[kMaxCopies];
+    int count;
+    int64_t vectors;
+};
+
+__global__ void __launch_bounds__(256) copy_rows_kernel(const Copies all) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int64_t across = dst_ld / 8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * across; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / across, c = (i - r * across) * 8;
-        uint32_t w[4] = {0, 0, 0, 0};
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all.vectors; i += (int64_t)gridDim.x * 256) {
+        int k = 0;
+        while (k + 1 < all.count && i >= all.c[k + 1].first) ++k;
+        const Copy& c = all.c[k];
+        const uint32_t across = (uint32_t)(c.dst_ld / 8);
+        const int64_t v = i - c.first, r = v / across, col = (v - r * across) * 8;
+        // the words that hold these elements, from the one with the first; the matrix itself starts at one
+        const int64_t e = r * c.src_ld + col;
+        const int odd = (int)(e & 1), left = (int)min((int64_t)8, c.cols - col);
+        const uint16_t* p = c.src + e - odd;
+        const size_t bytes = (size_t)((c.rows - 1) * c.src_ld + c.cols) * 2;
+        uint32_t w[5];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint16_t* p = src + r * src_ld + c + k;
-            if (c + k < cols && check::in(p, 2, src, (size_t)((rows - 1) * src_ld + cols) * 2, 10))
-                w[k / 2] |= (uint32_t)*p << (16 * (k & 1));
+        for (int q = 0; q < 5; ++q) {
+            const int n = left + odd - 2 * q;   // elements from this word on
+            w[q] = 0;
+            if (n >= 2 && check::in(p + 2 * q, 4, c.src, bytes, 10))
+                w[q] = *reinterpret_cast<const uint32_t*>(p + 2 * q);
+            else if (n == 1 && check::in(p + 2 * q, 2, c.src, bytes, 10))
+                w[q] = p[2 * q];
         }
-        uint4* q = reinterpret_cast<uint4*>(dst + r * dst_ld + c);
-        if (check::in(q, 16, dst, (size_t)(rows * dst_ld) * 2, 11)) *q = make_uint4(w[0], w[1], w[2], w[3]);
+        uint4 out = make_uint4(w[0], w[1], w[2], w[3]);
+        if (odd)
+            out = make_uint4(__funnelshift_r(w[0], w[1], 16), __funnelshift_r(w[1], w[2], 16),
+                             __funnelshift_r(w[2], w[3], 16), __funnelshift_r(w[3], w[4], 16));
+        uint4* q = reinterpret_cast<uint4*>(c.dst + r * c.dst_ld + col);
+        if (check::in(q, 16, c.dst, (size_t)(c.rows * c.dst_ld) * 2, 11)) *q = out;
     }
 }
 
@@ -139,17 +166,21 @@ size_t part(int64_t rows, int64_t cols) { return ((size_t)(rows * product::padde
 
 int steps_of(int64_t k) { return (int)((k + 63) / 64); }
 
-// A factor with rows that tensor maps can read: the matrix itself, or its copy in the workspace.
+// A factor with rows that tensor maps can read: the matrix itself, or its copy in the workspace, which
+// `copies` is to make.
 cudaError_t make(product::Factor& f, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, Parts& ws,
-                 cudaStream_t stream) {
+                 Copies& copies) {
     const int64_t wide = product::padded(cols);
     if (wide == cols) return f.make(bf16, p, rows, cols, ld);
-    uint16_t* copy = static_cast<uint16_t*>(ws.take((size_t)(rows * wide) * 2));
-    const int64_t vectors = rows * (wide / 8);
-    const int64_t blocks = (vectors + 255) / 256;
-    const cudaError_t e = ops::launch_early(copy_rows_kernel, dim3((unsigned)(blocks < 2432 ? blocks : 2432)), dim3(256), 0,
-                                            stream, static_cast<const uint16_t*>(p), ld, rows, cols, copy, wide);
-    return e != cudaSuccess ? e : f.make(bf16, copy, rows, cols, wide);
+    uint16_t* to = static_cast<uint16_t*>(ws.take((size_t)(rows * wide) * 2));
+    copies.c[copies.count++] = {static_cast<const uint16_t*>(p), to, ld, wide, rows, cols, copies.vectors};
+    copies.vectors += rows * (wide / 8);
+    return f.make(bf16, to, rows, cols, wide);
+}
+cudaError_t run(const Copies& copies, cudaStream_t stream) {
+    if (copies.count == 0) return cudaSuccess;
+    const int64_t blocks = (copies.vectors + 255) / 256, most = 152 * 8;
+    return ops::launch_early(copy_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, stream, copies);
 }
 
 // (a workspace's matrix: cols = ld, its padding may be written)
@@ -170,12 +201,14 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     const bool bf16 = a.type == MHCPB_BF16;
     Parts ws{static_cast<char*>(a.workspace)};
     void* hidden = ws.take((size_t)(T_ * Fp) * 2);
+    Copies copies{};
     product::Factor x, wg, wu, wd, h;
-    MHCM_TRY(make(x, bf16, a.x, T_, D, a.x_stride, ws, stream));
-    MHCM_TRY(make(wg, bf16, a.w_gate, F, D, D, ws, stream));
-    MHCM_TRY(make(wu, bf16, a.w_up, F, D, D, ws, stream));
-    MHCM_TRY(make(wd, bf16, a.w_down, D, F, F, ws, stream));
+    MHCM_TRY(make(x, bf16, a.x, T_, D, a.x_stride, ws, copies));
+    MHCM_TRY(make(wg, bf16, a.w_gate, F, D, D, ws, copies));
+    MHCM_TRY(make(wu, bf16, a.w_up, F, D, D, ws, copies));
+    MHCM_TRY(make(wd, bf16, a.w_down, D, F, F, ws, copies));
     MHCM_TRY(h.make(bf16, hidden, T_, F, Fp));
+    MHCM_TRY(run(copies, stream));
     Shape s{};
     s.bf16 = bf16;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
@@ -210,17 +243,19 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     Parts ws{static_cast<char*>(a.workspace)};
     const size_t tf = (size_t)(T_ * Fp) * 2;
     void *hidden = ws.take(tf), *grad_gate = ws.take(tf), *grad_up = ws.take(tf);
+    Copies copies{};
     product::Factor x, dy, wg, wu, wd, h, dg, du;
-    MHCM_TRY(make(dy, bf16, a.grad_y, T_, D, a.gy_stride, ws, stream));
-    MHCM_TRY(make(wd, bf16, a.w_down, D, F, F, ws, stream));
-    if (a.grad_w[0] || a.grad_w[1]) MHCM_TRY(make(x, bf16, a.x, T_, D, a.x_stride, ws, stream));
+    MHCM_TRY(make(dy, bf16, a.grad_y, T_, D, a.gy_stride, ws, copies));
+    MHCM_TRY(make(wd, bf16, a.w_down, D, F, F, ws, copies));
+    if (a.grad_w[0] || a.grad_w[1]) MHCM_TRY(make(x, bf16, a.x, T_, D, a.x_stride, ws, copies));
     if (a.grad_x) {
-        MHCM_TRY(make(wg, bf16, a.w_gate, F, D, D, ws, stream));
-        MHCM_TRY(make(wu, bf16, a.w_up, F, D, D, ws, stream));
+        MHCM_TRY(make(wg, bf16, a.w_gate, F, D, D, ws, copies));
+        MHCM_TRY(make(wu, bf16, a.w_up, F, D, D, ws, copies));
     }
     MHCM_TRY(h.make(bf16, hidden, T_, F, Fp));
     MHCM_TRY(dg.make(bf16, grad_gate, T_, F, Fp));
     MHCM_TRY(du.make(bf16, grad_up, T_, F, Fp));
+    MHCM_TRY(run(copies, stream));
 
     Shape s{};
     s.bf16 = bf16;

@@ -115,6 +115,10 @@ struct Args {
     float scale;
     void* workspace;
 };
+// few rows or columns (mhcm_orth_few.cu): whether the sizes are taken, and the call
+bool few_rows(int64_t m, int64_t n);
+cudaError_t few_rows_orthogonalize(const Args& a, cudaStream_t stream);
+cudaError_t few_rows_site(uint32_t* site);
 size_t workspace_bytes(int64_t m, int64_t n);
 cudaError_t orthogonalize(const Args& a, cudaStream_t stream);
 cudaError_t setup();

@@ -19,78 +19,18 @@
 // the exact ones before the output's rounding, without the diagonals 2.5e-3; of one
 // of rank 6, 1.0e-3.
 // A and A^2 are symmetric: tiles on and above the diagonal, written twice.
-#include "mhcm_product.cuh"
+#include "mhcm_orth.cuh"
 
 namespace mhcpb {
 namespace orth {
 
 namespace {
 
-using product::Matrix;
 using product::Shape;
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 32768.f, kScaleA = 32768.f, kScaleB = 16384.f;   // 1.21, 1.46 and 2.81 times these < 65504
 
-// 1 / (|G|_F + eps) as a product that neither overflows nor loses bits: three factors.
-struct Inverse {
-    float p, q, r;
-};
-__device__ __forceinline__ float scaled(float g, const Inverse& f) { return g * f.p * f.q * f.r; }
-
-// G's elements by its type
-struct Input {
-    const void* ptr;
-    int type;
-    int64_t rows, ld, cols;
-    // elements as they are stored (a 16-bit type's in the first half of the words), and as FP32
-    bool by_eight() const { return cols % 8 == 0 && ld * (type == MHCPB_FP32 ? 4 : 2) % 16 == 0; }
-    template <class Span>
-    __device__ __forceinline__ product::Raw<float, Span> raw(const Span& at, uint32_t site) const {
-        const size_t n = (size_t)((rows - 1) * ld + cols);
-        if (type == MHCPB_FP32) return Matrix<const float>{static_cast<const float*>(ptr), ld, n}.raw(at, site);
-        const auto h = Matrix<const __half>{static_cast<const __half*>(ptr), ld, n}.raw(at, site);
-        product::Raw<float, Span> r{};
-#pragma unroll
-        for (int i = 0; i < h.words; ++i) r.u[i] = h.u[i];
-        return r;
-    }
-    template <class Span>
-    __device__ __forceinline__ void to(const product::Raw<float, Span>& r, float (&v)[Span::n]) const {
-        if (type == MHCPB_FP32) return r.to(v);
-        if (type == MHCPB_BF16) {
-            product::Raw<__nv_bfloat16, Span> h;
-#pragma unroll
-            for (int i = 0; i < h.words; ++i) h.u[i] = r.u[i];
-            return h.to(v);
-        }
-        product::Raw<__half, Span> h;
-#pragma unroll
-        for (int i = 0; i < h.words; ++i) h.u[i] = r.u[i];
-        h.to(v);
-    }
-};
-
 constexpr int kNormBlocks = 608, kNormThreads = 256;
-
-// Sums of squares of the small, middling and large elements apart, the outer two
-// scaled, so that none overflows or vanishes (Blue, ACM TOMS 4, 1978).
-struct Squares {
-    float low = 0.f, mid = 0.f, high = 0.f;
-    __device__ __forceinline__ void add(float v) {
-        const float m = fabsf(v);
-        if (m > 0x1p50f) {
-            const float t = v * 0x1p-80f;
-            high = fmaf(t, t, high);
-        } else if (m < 0x1p-50f) {
-            const float t = v * 0x1p80f;
-            low = fmaf(t, t, low);
-        } else {
-            mid = fmaf(v, v, mid);   // NaN too
-        }
-    }
-    __device__ __forceinline__ double sum() const { return (double)mid + (double)high * 0x1p160 + (double)low * 0x1p-160; }
-};
 
 __device__ __forceinline__ double block_sum(double v) {
     __shared__ double warps[kNormThreads / 32];
@@ -153,14 +93,11 @@ __global__ void __launch_bounds__(kNormThreads)
     ptx::grid_launch_dependents();
     double total = 0.0;
     for (int i = threadIdx.x; i < kNormBlocks; i += kNormThreads) total += partial[i];
-    total = sqrt(block_sum(total)) + eps;
-    int e;
-    const double f = frexp(total, &e);   // total = f 2^e, f in [1/2, 1)
-    e = min(max(e, -240), 240);
-    Inverse inv;
-    inv.r = (float)(1.0 / f);
-    inv.p = exp2f((float)(-e / 2));
-    inv.q = exp2f((float)(-(e - e / 2)));
+    total = block_sum(total);
+    __shared__ Inverse shared;
+    if (threadIdx.x == 0) shared = inverse_of(sqrt(total) + eps);   // (FP64: by one thread)
+    __syncthreads();
+    const Inverse inv = shared;
     if (blockIdx.x == 0 && threadIdx.x == 0) *inverse = inv;
     over_pieces<EIGHT>(g, 2, [&](const auto& at, const auto& v) {
         using Span = std::decay_t<decltype(at)>;
@@ -326,9 +263,10 @@ Layout layout(int64_t m, int64_t n) {
 
 }  // namespace
 
-size_t workspace_bytes(int64_t m, int64_t n) { return layout(m, n).bytes; }
+size_t workspace_bytes(int64_t m, int64_t n) { return few_rows(m, n) ? 0 : layout(m, n).bytes; }
 
 cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
+    if (few_rows(a.m, a.n)) return few_rows_orthogonalize(a, stream);
     const int64_t m = a.m, n = a.n, s = m < n ? m : n, np = product::padded(n), sp = product::padded(s);
     const bool tall = m > n;
     const Layout l = layout(m, n);
@@ -387,7 +325,12 @@ cudaError_t setup() {
     MHCM_TRY(product::allow<PolynomialEpilogue>());
     return product::allow<UpdateEpilogue>();
 }
-cudaError_t checked_site(uint32_t* site) { return check::read_and_clear(site); }
+cudaError_t checked_site(uint32_t* site) {
+    uint32_t other = 0;
+    const cudaError_t e = check::read_and_clear(site), f = few_rows_site(&other);
+    if (*site == 0) *site = other;
+    return e != cudaSuccess ? e : f;
+}
 cudaError_t device_status(uint32_t* status, bool clear) { return product::read_status(status, clear); }
 
 }  // namespace orth

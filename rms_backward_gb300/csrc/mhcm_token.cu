@@ -18,25 +18,13 @@ namespace ffn {
 
 namespace {
 
+using ptx::fma2;
+using ptx::pair;
+using ptx::sum_of;
+
 constexpr int kBlocks = 152, kThreads = 512, kQuarters = 4, kGroups = kThreads / 32 / kQuarters;
 constexpr int kRows = 4;       // weight rows of a warp at a time
 constexpr int kUnroll = 3;
-
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float sum_of(uint64_t v) {
-    float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-    return lo + hi;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 template <class T>
 struct TokenArgs {

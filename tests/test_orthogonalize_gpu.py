@@ -12,7 +12,7 @@ from matrix_cases import DEV, f64
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 
-SHAPES = [(1, 1), (1, 9), (9, 1), (2, 3), (16, 16), (24, 2048), (2048, 24), (64, 200), (100, 100), (127, 129), (129, 128),
+SHAPES = [(1, 20), (8, 4000), (20480, 24), (32, 25000), (32, 30000), (33, 2000), (17, 5), (1, 1), (1, 9), (9, 1), (2, 3), (16, 16), (24, 2048), (2048, 24), (64, 200), (100, 100), (127, 129), (129, 128),
           (257, 130), (300, 1000), (1001, 303), (640, 640)]
 
 
