@@ -439,114 +439,63 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         // Every block has its part of the tile in shared memory; each adds up its share of the vectors.
         const Tile tile = tile_at<C::tile_m>(s, first_tile);
         const int rows = (int)min((int64_t)128, s.M - tile.m), cols = (int)min((int64_t)s.tile_n, s.N - tile.n);
-        const float* own = reinterpret_cast<const float*>(smem + C::off_stages);
-        auto part_at = [&](uint32_t i, int z) {
-            return z == (int)rank ? *reinterpret_cast<const float4*>(own + i)
-                                  : ptx::ld_cluster_f32x4(ptx::map_rank(stage0 + 4 * i, z));
-        };
-        auto element_at = [&](uint32_t i, int z) {
-            return z == (int)rank ? own[i] : ptx::ld_cluster_f32(ptx::map_rank(stage0 + 4 * i, z));
-        };
-        // Some vectors per thread at a time: their reads, and the loads of one block's part, are all under
-        // way before the first is used (each trip to another block's shared memory takes some 500 clocks).
-        constexpr int kBatch = Epilogue::kDual || sizeof(typename Epilogue::template Read<Eight>) > 16 ? 2 : 4;   // (registers)
+        auto part_at = [&](uint32_t i, int z) { return ptx::map_rank(stage0 + 4 * i, z); };
+        // One vector per thread at a time, in loops that are not unrolled: these launches are short, and
+        // what they cost is the way of their instructions from memory (with four vectors at a time, their
+        // loads side by side, 512 x 512 orthogonalised took 223 us for 155).
         const int threads = s.split * C::threads, me = (int)rank * C::threads + threadIdx.x;
         if (!Epilogue::kMirror && s.narrow) {
-            // a warp per row, four times 32 columns at a time
-            constexpr int kColumns = 4;
+            // a warp per row, 32 columns at a time
             for (int r = (int)rank * (C::threads / 32) + warp; r < rows; r += s.split * (C::threads / 32))
-                for (int first = lane; first < cols; first += 32 * kColumns) {
-                    typename Epilogue::template Read<One> read[kColumns];
-                    float v[kColumns][1] = {}, w[kColumns][1] = {};
-                    auto at = [&](int q) {
-                        const int c = first + 32 * q;
-                        return One{(int64_t)tile.m + r, (int64_t)tile.n + c, c < cols};
-                    };
-#pragma unroll
-                    for (int q = 0; q < kColumns; ++q) read[q] = epi.read(tile.group, at(q));
+#pragma unroll 1
+                for (int c = lane; c < cols; c += 32) {
+                    const One at{(int64_t)tile.m + r, (int64_t)tile.n + c, true};
+                    const auto read = epi.read(tile.group, at);
+                    float v[1] = {}, w[1] = {};
+#pragma unroll 1
                     for (int z = 0; z < s.split; ++z) {
-                        float x[kColumns][2] = {};
-#pragma unroll
-                        for (int q = 0; q < kColumns; ++q)
-                            if (first + 32 * q < cols) {
-                                const uint32_t i = (uint32_t)(r * s.part_row + first + 32 * q);
-                                x[q][0] = element_at(i, z);
-                                if constexpr (Epilogue::kDual) x[q][1] = element_at(i + s.tile_n, z);
-                            }
-#pragma unroll
-                        for (int q = 0; q < kColumns; ++q) v[q][0] += x[q][0], w[q][0] += x[q][1];
+                        const uint32_t p = part_at((uint32_t)(r * s.part_row + c), z);
+                        v[0] += ptx::ld_cluster_f32(p);
+                        if constexpr (Epilogue::kDual) w[0] += ptx::ld_cluster_f32(p + 4 * s.tile_n);
                     }
-#pragma unroll
-                    for (int q = 0; q < kColumns; ++q) epi.write(tile.group, at(q), v[q], w[q], read[q]);
+                    epi.write(tile.group, at, v, w, read);
                 }
         } else {
             const int across = (cols + 7) / 8, units = rows * across;
-            for (int first = me; first < units; first += kBatch * threads) {
-                Eight at[kBatch];
-                typename Epilogue::template Read<Eight> read[kBatch];
-                float v[kBatch][8], w[Epilogue::kDual ? kBatch : 1][8];
-                int line[kBatch];
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q) {
-                    const int u = first + q * threads, r = u / across, c = (u - r * across) * 8;
-                    line[q] = r * s.part_row + c;
-                    at[q] = {(int64_t)tile.m + r, (int64_t)tile.n + c, u < units};
-                    if (at[q].is) read[q] = epi.read(tile.group, at[q]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[q][i] = w[Epilogue::kDual ? q : 0][i] = 0.f;
-                }
+#pragma unroll 1
+            for (int u = me; u < units; u += threads) {
+                const int r = u / across, c = (u - r * across) * 8;
+                const Eight at{(int64_t)tile.m + r, (int64_t)tile.n + c, true};
+                const auto read = epi.read(tile.group, at);
+                float v[8] = {}, w[8] = {};
+#pragma unroll 1
                 for (int z = 0; z < s.split; ++z) {
-                    float4 x[kBatch][Epilogue::kDual ? 4 : 2];
-#pragma unroll
-                    for (int q = 0; q < kBatch; ++q)
-                        if (at[q].is)
-#pragma unroll
-                            for (int h = 0; h < (Epilogue::kDual ? 4 : 2); ++h)
-                                x[q][h] = part_at((uint32_t)(line[q] + (h >> 1) * s.tile_n + (h & 1) * 4), z);
-#pragma unroll
-                    for (int q = 0; q < kBatch; ++q)
-                        if (at[q].is) {
-                            add8(v[q], x[q][0], x[q][1]);
-                            if constexpr (Epilogue::kDual) add8(w[q], x[q][2], x[q][3]);
-                        }
+                    const uint32_t p = part_at((uint32_t)(r * s.part_row + c), z);
+                    add8(v, ptx::ld_cluster_f32x4(p), ptx::ld_cluster_f32x4(p + 16));
+                    if constexpr (Epilogue::kDual)
+                        add8(w, ptx::ld_cluster_f32x4(p + 4 * s.tile_n), ptx::ld_cluster_f32x4(p + 4 * s.tile_n + 16));
                 }
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q)
-                    if (at[q].is) epi.write(tile.group, at[q], v[q], w[Epilogue::kDual ? q : 0], read[q]);
+                epi.write(tile.group, at, v, w, read);
             }
         }
         if (Epilogue::kMirror && tile.mirror) {   // transposed: eight rows of one column
             const int down = (rows + 7) / 8, flipped = cols * down;
-            for (int first = me; first < flipped; first += kBatch * threads) {
-                Eight at[kBatch];
-                typename Epilogue::template Read<Eight> read[kBatch];
-                float v[kBatch][8];
-                int line[kBatch];
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q) {
-                    const int u = first + q * threads, g = u / cols, c = u - g * cols;
-                    line[q] = 8 * g * s.part_row + c;
-                    at[q] = {(int64_t)tile.n + c, (int64_t)tile.m + 8 * g, u < flipped};
-                    if (at[q].is) read[q] = epi.read(tile.group, at[q]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[q][i] = 0.f;
-                }
+#pragma unroll 1
+            for (int u = me; u < flipped; u += threads) {
+                const int g = u / cols, c = u - g * cols;
+                const Eight at{(int64_t)tile.n + c, (int64_t)tile.m + 8 * g, true};
+                const auto read = epi.read(0, at);
+                float v[8] = {};
+#pragma unroll 1
                 for (int z = 0; z < s.split; ++z) {
-                    float x[kBatch][8];
+                    const uint32_t p = part_at((uint32_t)(8 * g * s.part_row + c), z);
+                    float x[8];
 #pragma unroll
-                    for (int q = 0; q < kBatch; ++q)
-                        if (at[q].is)
+                    for (int i = 0; i < 8; ++i) x[i] = ptx::ld_cluster_f32(p + 4 * i * s.part_row);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[q][i] = element_at((uint32_t)(line[q] + i * s.part_row), z);
-#pragma unroll
-                    for (int q = 0; q < kBatch; ++q)
-                        if (at[q].is)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[q][i] += x[q][i];
+                    for (int i = 0; i < 8; ++i) v[i] += x[i];
                 }
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q)
-                    if (at[q].is) epi.write(0, at[q], v[q], v[q], read[q]);
+                epi.write(0, at, v, v, read);
             }
         }
         ptx::cluster_arrive();   // the parts stay until every block has read them
