@@ -34,6 +34,7 @@ struct Shape {
     int stall;         // a test's: the MMA issuer waits for what nothing signals
     // set by choose()
     int m_tiles, n_tiles, tiles;
+    int full;          // tiles from this one on are halves (pairs of blocks)
     int tile_n;        // columns of C per tile (of each product, side by side)
     int split;         // blocks that share a tile's sum
     int b_box;         // rows of B in one box, 0: boxes of 64

@@ -65,9 +65,12 @@ Choice choose(Shape& s) {
     const bool side = s.mode == kSideBySide;
     const int64_t steps = (int64_t)s.k_steps * (s.mode == kLongK ? 2 : 1);
 
-    const int64_t pair_n = side ? 128 : 256, pairs = tiles_of(s, 256, pair_n), waves = over(pairs, kSms / 2);
+    const int64_t pair_n = side ? 128 : 256, pairs = tiles_of(s, 256, pair_n), places = kSms / 2;
+    // a last turn of less than half of the places is one of half tiles
+    const int64_t rest = pairs % places, halves = rest <= places / 2 ? rest : 0;
+    const double waves = (double)((pairs - halves) / places) + (pairs % places > places / 2 ? 1 : 0) + (halves > 0 ? 0.6 : 0);
     const double pair_step = 32768 / kFromL2 < 512 ? 512 : 32768 / kFromL2;
-    const double pair_cost = waves * steps * pair_step + kPairStart + (waves - 1) * kPairAgain;
+    const double pair_cost = waves * steps * pair_step + kPairStart + (waves < 1 ? 0 : waves - 1) * kPairAgain;
 
     // single blocks: B's rows per tile free where its rows are k and C is not symmetric; tried are those
     // that fill the GPU's places once or twice
@@ -106,14 +109,15 @@ Choice choose(Shape& s) {
         s.b_box = 0;
         s.m_tiles = (int)over(s.M, 256);
         s.n_tiles = (int)over(s.N, pair_n);
-        s.tiles = (int)pairs;
-        c.grid = (int)(2 * (pairs < kSms / 2 ? pairs : kSms / 2));
+        s.full = (int)(pairs - halves);
+        s.tiles = (int)(pairs + halves);
+        c.grid = (int)(2 * (s.tiles < places ? s.tiles : places));
         return c;
     }
     const int columns = side ? 2 * s.tile_n : s.tile_n;
     s.m_tiles = (int)over(s.M, 128);
     s.n_tiles = (int)over(s.N, s.tile_n);
-    s.tiles = (int)tiles_of(s, 128, s.tile_n);
+    s.tiles = s.full = (int)tiles_of(s, 128, s.tile_n);
     c.grid = s.tiles * s.split;
     s.b_box = free_n ? s.tile_n : 0;
     s.b_bytes = free_n ? (uint32_t)columns * 128 : 2 * kBoxBytes;

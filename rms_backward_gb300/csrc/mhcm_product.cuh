@@ -11,7 +11,8 @@
 //
 // Two shapes of one kernel:
 //  * PAIR: pairs of blocks (cta_group::2), 256 x 256 tiles, one block per SM,
-//    persistent.  Each block holds half of A's and of B's rows: 32 KiB of
+//    persistent; the tiles that would fill less than half of the last turn are
+//    taken as halves of 128 columns.  Each block holds half of A's and of B's rows: 32 KiB of
 //    operands per 64 k and block, 64 bytes per clock and SM at the full MMA rate.
 //    Two accumulators in TMEM (all 512 columns), so the epilogue of one tile runs
 //    under the products of the next.
@@ -68,12 +69,20 @@ struct Cfg {
 struct Tile {
     int group, m, n;   // first row and column; of each of the two products where two are formed side by side
     bool mirror;       // symmetric C: the tile is also written transposed
+    bool half;         // half of the columns
 };
 template <int TILE_M>
 __device__ __forceinline__ Tile tile_at(const Shape& s, int t) {
     Tile r;
     r.group = 0;
-    r.mirror = false;
+    r.mirror = r.half = false;
+    int right = 0;                         // columns to the right of the tile's first
+    if (t >= s.full) {                     // the last tiles are taken in halves
+        const int h = t - s.full;
+        t = s.full + (h >> 1);
+        r.half = true;
+        right = (h & 1) * (s.tile_n / 2);
+    }
     if (s.mode == kSymmetric) {            // tiles on and above the diagonal, row by row
         int i = 0, left = s.n_tiles;
         while (t >= left) {
@@ -82,7 +91,7 @@ __device__ __forceinline__ Tile tile_at(const Shape& s, int t) {
             ++i;
         }
         r.m = i * TILE_M;
-        r.n = (i + t) * s.tile_n;
+        r.n = (i + t) * s.tile_n + right;
         r.mirror = t > 0;
         return r;
     }
@@ -96,7 +105,7 @@ __device__ __forceinline__ Tile tile_at(const Shape& s, int t) {
     const int rows = min(8, s.m_tiles - first);
     t -= band * 8 * s.n_tiles;
     r.m = (first + t % rows) * TILE_M;
-    r.n = (t / rows) * s.tile_n;
+    r.n = (t / rows) * s.tile_n + right;
     return r;
 }
 
@@ -215,10 +224,10 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         for (int t = first_tile; ok && t < s.tiles; t += step_tile) {
             const Tile tile = tile_at<C::tile_m>(s, t);
             const int m0 = tile.m + (int)half * 128;
-            const int n0 = tile.n + (s.mode == kSideBySide ? 0 : (int)half * 128);
+            const int n0 = tile.n + (s.mode == kSideBySide ? 0 : (int)half * (tile.half ? 64 : 128));
             // (a single block leaves out the half of A's rows that no token has: their results are not read)
             const int a_boxes = !PAIR && s.M - tile.m <= kBox ? 1 : 2;
-            const uint32_t bytes = PAIR ? 2 * kPairStage : a_boxes * kBoxBytes + s.b_bytes;
+            const uint32_t bytes = PAIR ? 2 * kPairStage - (tile.half ? 2 * kBoxBytes : 0) : a_boxes * kBoxBytes + s.b_bytes;
             for (int k = k_begin; k < k_end; ++k, ++n) {
                 if (!wait_all<PAIR>(bar(C::b_empty + st), ph ^ 1u, abort_flag)) {
                     ok = false;
@@ -245,7 +254,8 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     const CUtensorMap* b_first = side && PAIR && half == 1 ? &b1 : bm;
                     const CUtensorMap* b_second = side && (!PAIR || half == 1) ? &b1 : bm;
                     ptx::tma_load_one<PAIR>(dst_b, b_first, s.b_mn ? n0 : k0, s.b_mn ? k0 : n0, full);
-                    ptx::tma_load_one<PAIR>(dst_b + kBoxBytes, b_second, s.b_mn ? n1 : k0, s.b_mn ? k0 : n1, full);
+                    if (!PAIR || !tile.half)
+                        ptx::tma_load_one<PAIR>(dst_b + kBoxBytes, b_second, s.b_mn ? n1 : k0, s.b_mn ? k0 : n1, full);
                 }
                 if (++st == stages) st = 0, ph ^= 1u;
             }
@@ -254,7 +264,8 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
             for (uint32_t i = n > stages ? n - stages : 0; i < n; ++i)
                 wait<PAIR>(bar(C::b_full + i % stages), (i / stages) & 1u, abort_flag, false);
     } else if (warp == 1 && leader) {
-        const uint32_t idesc = ptx::idesc_16bit(C::tile_m, width, s.bf16, s.a_mn, s.b_mn);
+        const uint32_t idesc_whole = ptx::idesc_16bit(C::tile_m, width, s.bf16, s.a_mn, s.b_mn);
+        const uint32_t idesc_half = ptx::idesc_16bit(C::tile_m, width / 2, s.bf16, s.a_mn, s.b_mn);
         // 16 k further: 32 bytes along a row, or 16 rows of 128 bytes (in descriptors' units of 16)
         const uint64_t a_step = s.a_mn ? 128 : 2, b_step = s.b_mn ? 128 : 2;
         const uint64_t first = ptx::smem_desc(stage0, kBoxBytes, 1024, ptx::kLayoutSwizzle128B);
@@ -267,7 +278,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 break;
             }
             ptx::tc_fence_after();
-            const uint32_t d = tmem + acc * width;
+            const uint32_t d = tmem + acc * width, idesc = PAIR && t >= s.full ? idesc_half : idesc_whole;
             if (s.stall && !wait_all<PAIR>(bar(C::b_last), 0u, abort_flag)) {   // a test's wait that nothing ends
                 ok = false;
                 break;
@@ -312,11 +323,12 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 const Tile tile = tile_at<C::tile_m>(s, t);
                 const int64_t row0 = tile.m + (int64_t)rank * 128 + quad * 32;
                 const uint32_t d = acc * width;
-                constexpr int kChunks = Epilogue::kDual ? 2 : 4;   // of 32 columns per warp
+                const int chunks = (Epilogue::kDual ? 2 : 4) >> (tile.half ? 1 : 0);   // of 32 columns per warp
+                const int up = tile.half ? 64 : 128;                                   // the second product's columns
                 bool ok = true;
 #pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    const int column = half * kChunks * 32 + c * 32;
+                for (int c = 0; c < chunks; ++c) {
+                    const int column = half * chunks * 32 + c * 32;
                     const int64_t col0 = tile.n + column;
                     auto ready = [&] {   // the first chunk's reads are under way: now the accumulator
                         if (c == 0) {
@@ -326,7 +338,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                         return ok;
                     };
                     auto drained = [&] {   // the last chunk has left TMEM
-                        if (c == kChunks - 1) {
+                        if (c == chunks - 1) {
                             ptx::tc_fence_before();
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(bar(C::b_free + acc), 0));
@@ -340,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                         if (!ready()) break;
                         float w[Epilogue::kDual ? 32 : 1];
                         if constexpr (Epilogue::kDual) {
-                            stage(d + 128 + column);
+                            stage(d + up + column);
 #pragma unroll
                             for (int q = 0; q < 32; ++q) w[q] = scratch[q * C::row + lane];
                         }
@@ -391,7 +403,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     stage(d + column);
                     vectors(v);
                     if constexpr (Epilogue::kDual) {
-                        stage(d + 128 + column);
+                        stage(d + up + column);
                         vectors(w);
                     }
                     drained();
