@@ -85,10 +85,12 @@ __global__ void __launch_bounds__(kNormThreads) squares_kernel(const Input g, do
     if (threadIdx.x == 0 && check::in(partial + blockIdx.x, 8, partial, kNormBlocks * 8, 1)) partial[blockIdx.x] = total;
 }
 
-// FP16 copy of G / (|G| + eps), and the factors for later.
+// FP16 copy of G / (|G| + eps), and the factors for later; where G's rows are not made of whole vectors also
+// its FP32 copy, which the first step then reads instead of G.
 template <bool EIGHT>
 __global__ void __launch_bounds__(kNormThreads)
-    first_copy_kernel(const Input g, const double* partial, double eps, Inverse* inverse, Matrix<__half> x) {
+    first_copy_kernel(const Input g, const double* partial, double eps, Inverse* inverse, Matrix<__half> x,
+                      Matrix<float> full) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     double total = 0.0;
@@ -103,7 +105,10 @@ __global__ void __launch_bounds__(kNormThreads)
         using Span = std::decay_t<decltype(at)>;
         float r[Span::n];
 #pragma unroll
-        for (int k = 0; k < Span::n; ++k) r[k] = scaled(v[k], inv) * kScaleX;
+        for (int k = 0; k < Span::n; ++k) r[k] = scaled(v[k], inv);
+        if (!EIGHT) full.store(at, r, 20);
+#pragma unroll
+        for (int k = 0; k < Span::n; ++k) r[k] *= kScaleX;
         x.store(at, r, 3);
     });
 }
@@ -295,7 +300,7 @@ cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
     const int64_t blocks = (m * ((n + 1023) / 1024) + kNormThreads / 32 - 1) / (kNormThreads / 32);
     MHCM_TRY(ops::launch_early(eight ? first_copy_kernel<true> : first_copy_kernel<false>,
                                dim3((unsigned)(blocks < 1216 ? blocks : 1216)), dim3(kNormThreads), 0, stream, g,
-                               static_cast<const double*>(partial), static_cast<double>(a.eps), inverse, copies[0]));
+                               static_cast<const double*>(partial), static_cast<double>(a.eps), inverse, copies[0], x));
     for (int i = 0; i < a.steps; ++i) {
         const product::Factor* cur = &factor_x[i & 1];
         Shape p{};
@@ -308,10 +313,9 @@ cudaError_t orthogonalize(const Args& a, cudaStream_t stream) {
         p.mode = product::kPlain;
         p.M = m, p.N = n, p.k_steps = steps_of(s), p.b_mn = !tall;
         const bool last = i + 1 == a.steps;
-        const UpdateEpilogue update{g, i == 0 ? inverse : nullptr, poly_lost, tall, x, copies[(i + 1) & 1],
+        const UpdateEpilogue update{g, i == 0 && eight ? inverse : nullptr, poly_lost, tall, x, copies[(i + 1) & 1],
                                     last ? out : Matrix<__nv_bfloat16>{nullptr, 0, 0}, a.scale};
-        // G in the first step and the output in the last are the caller's
-        p.narrow = (i == 0 && !g.by_eight()) || (last && !out.by_eight(n));
+        p.narrow = last && !out.by_eight(n);   // (the output is the caller's)
         if (tall)
             MHCM_TRY(product::launch(p, update, cur, nullptr, &factor_poly, nullptr, stream));
         else

@@ -457,20 +457,32 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         // loads side by side, 512 x 512 orthogonalised took 223 us for 155).
         const int threads = s.split * C::threads, me = (int)rank * C::threads + threadIdx.x;
         if (!Epilogue::kMirror && s.narrow) {
-            // a warp per row, 32 columns at a time
+            // a warp per row, four times 32 columns at a time (a lane has one element of each: their reads side by side)
+            constexpr int kTimes = 4;
             for (int r = (int)rank * (C::threads / 32) + warp; r < rows; r += s.split * (C::threads / 32))
 #pragma unroll 1
-                for (int c = lane; c < cols; c += 32) {
-                    const One at{(int64_t)tile.m + r, (int64_t)tile.n + c, true};
-                    const auto read = epi.read(tile.group, at);
-                    float v[1] = {}, w[1] = {};
+                for (int first = lane; first < cols; first += 32 * kTimes) {
+                    typename Epilogue::template Read<One> read[kTimes];
+                    float v[kTimes][1] = {}, w[kTimes][1] = {};
+                    auto at = [&](int q) {
+                        return One{(int64_t)tile.m + r, (int64_t)tile.n + first + 32 * q, first + 32 * q < cols};
+                    };
+#pragma unroll
+                    for (int q = 0; q < kTimes; ++q) read[q] = epi.read(tile.group, at(q));
 #pragma unroll 1
                     for (int z = 0; z < s.split; ++z) {
-                        const uint32_t p = part_at((uint32_t)(r * s.part_row + c), z);
-                        v[0] += ptx::ld_cluster_f32(p);
-                        if constexpr (Epilogue::kDual) w[0] += ptx::ld_cluster_f32(p + 4 * s.tile_n);
+                        const uint32_t p = part_at((uint32_t)(r * s.part_row + first), z);
+                        float x[kTimes], y[kTimes];
+#pragma unroll
+                        for (int q = 0; q < kTimes; ++q) {
+                            x[q] = first + 32 * q < cols ? ptx::ld_cluster_f32(p + 128 * q) : 0.f;
+                            y[q] = Epilogue::kDual && first + 32 * q < cols ? ptx::ld_cluster_f32(p + 128 * q + 4 * s.tile_n) : 0.f;
+                        }
+#pragma unroll
+                        for (int q = 0; q < kTimes; ++q) v[q][0] += x[q], w[q][0] += y[q];
                     }
-                    epi.write(tile.group, at, v, w, read);
+#pragma unroll
+                    for (int q = 0; q < kTimes; ++q) epi.write(tile.group, at(q), v[q], w[q], read[q]);
                 }
         } else {
             const int across = (cols + 7) / 8, units = rows * across;
