@@ -104,7 +104,9 @@ struct StoreEpilogue {
     }
 };
 
-// Matrices whose rows are copied to rows `dst_ld` (a multiple of 8) apart, in one launch.
+// Matrices whose rows are copied to rows `dst_ld` (a multiple of 8) apart, in one launch: words of the
+// source, shifted where a row starts in the middle of one.  1000 x 1285 and three weights of 3427 x 1285:
+// 29 MB read, 13 us; bound by the words' loads (a lane's are 16 bytes apart).
 constexpr int kMaxCopies = 5;
 struct Copy {
     const uint16_t* src;

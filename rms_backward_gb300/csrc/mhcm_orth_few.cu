@@ -9,7 +9,9 @@
 //   P = a I + b A + c A^2   by every block
 //   X = P X     four columns per thread, in place
 //
-// FP32 throughout.
+// FP32 throughout.  24 x 20480: 81 us (156 by the general path); a step takes 27,000
+// clocks, 8,600 for A and 14,400 for P X, both at the 128 bytes per clock that shared
+// memory gives an SM's registers; packed FP32 arithmetic keeps below that.
 #include "mhcm_orth.cuh"
 
 namespace mhcpb {
