@@ -23,11 +23,10 @@ namespace {
 using product::Matrix;
 using product::Shape;
 
-template <class T>
+template <class T, int ACT>
 struct GatedEpilogue {
     static constexpr bool kDual = true, kMirror = false;
     Matrix<T> hidden, gate, up;
-    int activation;
     template <class Span>
     struct Read {};
     template <class Span>
@@ -39,7 +38,7 @@ struct GatedEpilogue {
                                           const Read<Span>&) const {
         float a[Span::n];
 #pragma unroll
-        for (int i = 0; i < Span::n; ++i) a[i] = activate(g[i], activation).x * u[i];
+        for (int i = 0; i < Span::n; ++i) a[i] = activate(g[i], ACT).x * u[i];
         hidden.store(at, a, 0);
         if (gate.ptr != nullptr) {
             gate.store(at, g, 1);
@@ -48,11 +47,10 @@ struct GatedEpilogue {
     }
 };
 
-template <class T>
+template <class T, int ACT>
 struct GradEpilogue {
     static constexpr bool kDual = false, kMirror = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
-    int activation;
     template <class Span>
     struct Read {
         product::Raw<T, Span> g, u;
@@ -69,7 +67,7 @@ struct GradEpilogue {
         in.u.to(u);
 #pragma unroll
         for (int i = 0; i < Span::n; ++i) {
-            const float2 f = activate(g[i], activation);
+            const float2 f = activate(g[i], ACT);
             a[i] = f.x * u[i];
             g[i] = da[i] * u[i] * f.y;
             u[i] = da[i] * f.x;
@@ -197,7 +195,7 @@ Matrix<T> matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
         if (e_ != cudaSuccess) return e_;       \
     } while (0)
 
-template <class T>
+template <class T, int ACT>
 cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     const int64_t T_ = a.T, D = a.D, F = a.F, Fp = product::padded(F);
     const bool bf16 = a.type == MHCPB_BF16;
@@ -214,8 +212,7 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     Shape s{};
     s.bf16 = bf16;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
-    const GatedEpilogue<T> gated{matrix<T>(hidden, T_, Fp, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F),
-                                 a.activation};
+    const GatedEpilogue<T, ACT> gated{matrix<T>(hidden, T_, Fp, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F)};
     s.narrow = !gated.gate.by_eight(F);
     MHCM_TRY(product::launch(s, gated, &x, nullptr, &wg, &wu, stream));
     s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain;
@@ -238,7 +235,7 @@ cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const
     return product::launch(s, store, a0, a1, b, b, stream);
 }
 
-template <class T, class O>
+template <class T, int ACT, class O>
 cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     const int64_t T_ = a.T, D = a.D, F = a.F, Fp = product::padded(F);
     const bool bf16 = a.type == MHCPB_BF16;
@@ -263,8 +260,8 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     s.bf16 = bf16;
     s.stall = a.stall;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.b_mn = 1;
-    const GradEpilogue<T> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, Fp, Fp),
-                               matrix<T>(grad_up, T_, Fp, Fp), matrix<T>(hidden, T_, Fp, Fp), a.activation};
+    const GradEpilogue<T, ACT> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, Fp, Fp),
+                               matrix<T>(grad_up, T_, Fp, Fp), matrix<T>(hidden, T_, Fp, Fp)};
     s.narrow = !grad.gate.by_eight(F);
     MHCM_TRY(product::launch(s, grad, &dy, nullptr, &wd, nullptr, stream));
     // The products that are left need only what the first wrote: each starts as soon as the one
@@ -293,6 +290,13 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     return cudaSuccess;
 }
 
+template <class T>
+cudaError_t backward_of(const Args& a, cudaStream_t stream) {
+    if (a.activation == MHCPB_GELU)
+        return a.grad_type == MHCPB_FP32 ? backward_as<T, MHCPB_GELU, float>(a, stream) : backward_as<T, MHCPB_GELU, T>(a, stream);
+    return a.grad_type == MHCPB_FP32 ? backward_as<T, MHCPB_SILU, float>(a, stream) : backward_as<T, MHCPB_SILU, T>(a, stream);
+}
+
 }  // namespace
 
 size_t forward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
@@ -312,7 +316,10 @@ size_t backward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
 
 cudaError_t forward(const Args& a, cudaStream_t stream) {
     if (few_tokens(a.T, a.D, a.F)) return few_tokens_forward(a, stream);
-    return a.type == MHCPB_BF16 ? forward_as<__nv_bfloat16>(a, stream) : forward_as<__half>(a, stream);
+    const bool gelu = a.activation == MHCPB_GELU;
+    if (a.type == MHCPB_BF16)
+        return gelu ? forward_as<__nv_bfloat16, MHCPB_GELU>(a, stream) : forward_as<__nv_bfloat16, MHCPB_SILU>(a, stream);
+    return gelu ? forward_as<__half, MHCPB_GELU>(a, stream) : forward_as<__half, MHCPB_SILU>(a, stream);
 }
 
 cudaError_t backward(const Args& a, cudaStream_t stream) {
@@ -322,17 +329,18 @@ cudaError_t backward(const Args& a, cudaStream_t stream) {
             if (w != nullptr && !a.accumulate) MHCM_TRY(cudaMemsetAsync(w, 0, bytes, stream));
         return cudaSuccess;
     }
-    if (a.type == MHCPB_BF16)
-        return a.grad_type == MHCPB_FP32 ? backward_as<__nv_bfloat16, float>(a, stream)
-                                         : backward_as<__nv_bfloat16, __nv_bfloat16>(a, stream);
-    return a.grad_type == MHCPB_FP32 ? backward_as<__half, float>(a, stream) : backward_as<__half, __half>(a, stream);
+    return a.type == MHCPB_BF16 ? backward_of<__nv_bfloat16>(a, stream) : backward_of<__half>(a, stream);
 }
 
 cudaError_t setup() {
-    MHCM_TRY(product::allow<GatedEpilogue<__nv_bfloat16>>());
-    MHCM_TRY(product::allow<GatedEpilogue<__half>>());
-    MHCM_TRY(product::allow<GradEpilogue<__nv_bfloat16>>());
-    MHCM_TRY(product::allow<GradEpilogue<__half>>());
+    MHCM_TRY((product::allow<GatedEpilogue<__nv_bfloat16, MHCPB_SILU>>()));
+    MHCM_TRY((product::allow<GatedEpilogue<__nv_bfloat16, MHCPB_GELU>>()));
+    MHCM_TRY((product::allow<GatedEpilogue<__half, MHCPB_SILU>>()));
+    MHCM_TRY((product::allow<GatedEpilogue<__half, MHCPB_GELU>>()));
+    MHCM_TRY((product::allow<GradEpilogue<__nv_bfloat16, MHCPB_SILU>>()));
+    MHCM_TRY((product::allow<GradEpilogue<__nv_bfloat16, MHCPB_GELU>>()));
+    MHCM_TRY((product::allow<GradEpilogue<__half, MHCPB_SILU>>()));
+    MHCM_TRY((product::allow<GradEpilogue<__half, MHCPB_GELU>>()));
     MHCM_TRY(product::allow<StoreEpilogue<__nv_bfloat16>>());
     MHCM_TRY(product::allow<StoreEpilogue<__half>>());
     return product::allow<StoreEpilogue<float>>();
