@@ -539,9 +539,11 @@ mhcpb_status_t mhcpb_debug_checked_operator_sites(uint32_t* sites, int* checked)
  *  - every pointer is aligned to 16 bytes (MHCPB_ERR_MISALIGNED);
  *  - a row stride is the row's width, or a larger multiple of 8 (else
  *    MHCPB_ERR_UNSUPPORTED_SHAPE);
- *  - matrix products take 16-bit operands with FP32 accumulators; what a product
- *    reads that another call's line forms (a, dg, du; X, A, B) is rounded to 16 bits
- *    between the two, everything else once, at the output;
+ *  - matrix products take 16-bit operands with FP32 accumulators; what one product
+ *    forms and another reads (a = act(g) u, dg, du; X, A, B) is rounded to 16 bits
+ *    between the two, everything else once, at the output.  Up to 64 tokens what
+ *    that rounding loses is kept beside it (of up to four, a is FP32), but for the
+ *    weights' gradients;
  *  - the waits inside the kernels are bounded (1 s): one that runs out leaves wrong
  *    outputs and is reported by mhcpb_operators_device_status. */
 enum {                      /* activations */

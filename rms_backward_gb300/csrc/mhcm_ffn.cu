@@ -9,8 +9,8 @@
 // u where a backward follows); the backward's first forms da and writes dg, du
 // and a again from the stored g and u, so a is not kept between the two.  dx is
 // one sum over both halves.  a, dg and du are operands of further products and so
-// are rounded to the operands' 16-bit type; everything else is FP32 until the
-// output is stored.  Rows that are not a multiple of 8 elements long are copied
+// are rounded to the operands' 16-bit type (up to 64 tokens with a second number for
+// what that loses, see store_both); everything else is FP32 until the output is stored.  Rows that are not a multiple of 8 elements long are copied
 // to rows that are (the tensor maps' 16-byte rule).
 #include "mhcm_ffn.cuh"
 #include "mhcm_product.cuh"
@@ -23,10 +23,29 @@ namespace {
 using product::Matrix;
 using product::Shape;
 
+// Up to 64 tokens, a, dg and du are kept as two numbers of the type, the second what the first's rounding
+// lost, in row 64 further: the rounding between two products costs nothing to avoid there (the time is
+// the weights'), and with few elements it would not average out.
+constexpr int64_t kLowRows = 64;
+template <class T, class Span>
+__device__ __forceinline__ void store_both(const Matrix<T>& m, Span at, const float (&v)[Span::n], bool both, uint32_t site) {
+    m.store(at, v, site);
+    if (!both) return;
+    float low[Span::n];
+#pragma unroll
+    for (int i = 0; i < Span::n; ++i) {
+        const float high = (float)(T)v[i];
+        low[i] = isfinite(high) ? v[i] - high : 0.f;
+    }
+    at.row += kLowRows;
+    m.store(at, low, site);
+}
+
 template <class T, int ACT>
 struct GatedEpilogue {
     static constexpr bool kDual = true, kMirror = false;
     Matrix<T> hidden, gate, up;
+    bool both;
     template <class Span>
     struct Read {};
     template <class Span>
@@ -39,7 +58,7 @@ struct GatedEpilogue {
         float a[Span::n];
 #pragma unroll
         for (int i = 0; i < Span::n; ++i) a[i] = activate(g[i], ACT).x * u[i];
-        hidden.store(at, a, 0);
+        store_both(hidden, at, a, both, 0);
         if (gate.ptr != nullptr) {
             gate.store(at, g, 1);
             up.store(at, u, 2);
@@ -51,6 +70,7 @@ template <class T, int ACT>
 struct GradEpilogue {
     static constexpr bool kDual = false, kMirror = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
+    bool both;
     template <class Span>
     struct Read {
         product::Raw<T, Span> g, u;
@@ -72,8 +92,8 @@ struct GradEpilogue {
             g[i] = da[i] * u[i] * f.y;
             u[i] = da[i] * f.x;
         }
-        grad_gate.store(at, g, 5);
-        grad_up.store(at, u, 6);
+        store_both(grad_gate, at, g, both, 5);
+        store_both(grad_up, at, u, both, 6);
         hidden.store(at, a, 7);
     }
 };
@@ -166,6 +186,9 @@ size_t part(int64_t rows, int64_t cols) { return ((size_t)(rows * product::padde
 
 int steps_of(int64_t k) { return (int)((k + 63) / 64); }
 
+// Rows of a matrix over the tokens that is kept with what its rounding lost.
+int64_t both_rows(int64_t T) { return T <= kLowRows ? kLowRows + T : T; }
+
 // A factor with rows that tensor maps can read: the matrix itself, or its copy in the workspace, which
 // `copies` is to make.
 cudaError_t make(product::Factor& f, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, Parts& ws,
@@ -200,22 +223,24 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     const int64_t T_ = a.T, D = a.D, F = a.F, Fp = product::padded(F);
     const bool bf16 = a.type == MHCPB_BF16;
     Parts ws{static_cast<char*>(a.workspace)};
-    void* hidden = ws.take((size_t)(T_ * Fp) * 2);
+    const int64_t rows = both_rows(T_);
+    void* hidden = ws.take((size_t)(rows * Fp) * 2);
     Copies copies{};
     product::Factor x, wg, wu, wd, h;
     MHCM_TRY(make(x, bf16, a.x, T_, D, a.x_stride, ws, copies));
     MHCM_TRY(make(wg, bf16, a.w_gate, F, D, D, ws, copies));
     MHCM_TRY(make(wu, bf16, a.w_up, F, D, D, ws, copies));
     MHCM_TRY(make(wd, bf16, a.w_down, D, F, F, ws, copies));
-    MHCM_TRY(h.make(bf16, hidden, T_, F, Fp));
+    MHCM_TRY(h.make(bf16, hidden, rows, F, Fp));
     MHCM_TRY(run(copies, stream));
     Shape s{};
     s.bf16 = bf16;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.mode = product::kSideBySide;
-    const GatedEpilogue<T, ACT> gated{matrix<T>(hidden, T_, Fp, Fp), matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F)};
+    const GatedEpilogue<T, ACT> gated{matrix<T>(hidden, rows, Fp, Fp), matrix<T>(a.gate, T_, F, F),
+                                      matrix<T>(a.up, T_, F, F), rows > T_};
     s.narrow = !gated.gate.by_eight(F);
     MHCM_TRY(product::launch(s, gated, &x, nullptr, &wg, &wu, stream));
-    s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain;
+    s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain, s.twice = rows > T_;
     const StoreEpilogue<T> store{{matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
     s.narrow = !store.out[0].by_eight(D);
     return product::launch(s, store, &h, nullptr, &wd, nullptr, stream);
@@ -240,8 +265,9 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     const int64_t T_ = a.T, D = a.D, F = a.F, Fp = product::padded(F);
     const bool bf16 = a.type == MHCPB_BF16;
     Parts ws{static_cast<char*>(a.workspace)};
-    const size_t tf = (size_t)(T_ * Fp) * 2;
-    void *hidden = ws.take(tf), *grad_gate = ws.take(tf), *grad_up = ws.take(tf);
+    const int64_t rows = both_rows(T_);
+    void* hidden = ws.take((size_t)(T_ * Fp) * 2);
+    void *grad_gate = ws.take((size_t)(rows * Fp) * 2), *grad_up = ws.take((size_t)(rows * Fp) * 2);
     Copies copies{};
     product::Factor x, dy, wg, wu, wd, h, dg, du;
     MHCM_TRY(make(dy, bf16, a.grad_y, T_, D, a.gy_stride, ws, copies));
@@ -260,8 +286,9 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     s.bf16 = bf16;
     s.stall = a.stall;
     s.M = T_, s.N = F, s.k_steps = steps_of(D), s.b_mn = 1;
-    const GradEpilogue<T, ACT> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, T_, Fp, Fp),
-                               matrix<T>(grad_up, T_, Fp, Fp), matrix<T>(hidden, T_, Fp, Fp)};
+    const GradEpilogue<T, ACT> grad{matrix<T>(a.gate, T_, F, F), matrix<T>(a.up, T_, F, F), matrix<T>(grad_gate, rows, Fp, Fp),
+                               matrix<T>(grad_up, rows, Fp, Fp), matrix<T>(hidden, T_, Fp, Fp),
+                                    rows > T_};
     s.narrow = !grad.gate.by_eight(F);
     MHCM_TRY(product::launch(s, grad, &dy, nullptr, &wd, nullptr, stream));
     // The products that are left need only what the first wrote: each starts as soon as the one
@@ -272,7 +299,13 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
         const StoreEpilogue<T> store{{matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
         s.narrow = !store.out[0].by_eight(D);
-        MHCM_TRY(product::launch(s, store, &dg, &du, &wg, &wu, stream));
+        product::Factor dg_both = dg, du_both = du;
+        if (rows > T_) {
+            s.twice = 1;
+            MHCM_TRY(dg_both.make(bf16, grad_gate, rows, F, Fp));
+            MHCM_TRY(du_both.make(bf16, grad_up, rows, F, Fp));
+        }
+        MHCM_TRY(product::launch(s, store, &dg_both, &du_both, &wg, &wu, stream));
         beside = true;
     }
     if (a.grad_w[0] && a.grad_w[1]) {
@@ -300,15 +333,15 @@ cudaError_t backward_of(const Args& a, cudaStream_t stream) {
 }  // namespace
 
 size_t forward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
-    size_t n = part(T, F);
-    if (few_tokens(T, D, F)) return n;
+    if (few_tokens(T, D, F)) return (size_t)((T * F * 4 + 255) / 256 * 256);
+    size_t n = part(both_rows(T), F);
     if (D % 8) n += part(T, D) + 2 * part(F, D);
     if (F % 8) n += part(D, F);
     return n;
 }
 
 size_t backward_workspace_bytes(int64_t T, int64_t D, int64_t F) {
-    size_t n = 3 * part(T, F);
+    size_t n = part(T, F) + 2 * part(both_rows(T), F);
     if (D % 8) n += 2 * part(T, D) + 2 * part(F, D);
     if (F % 8) n += part(D, F);
     return n;

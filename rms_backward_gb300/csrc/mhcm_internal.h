@@ -31,6 +31,8 @@ struct Shape {
                        // before it waited for): it does not wait for that one to end before its work, but
                        // before its own end, so that it still ends after it
     int narrow;        // the epilogue's matrices are taken element by element (see Eight)
+    int twice;         // A's 64 rows are followed by 64 of what their rounding lost, which are multiplied too
+                       // (M <= 64: single blocks)
     int stall;         // a test's: the MMA issuer waits for what nothing signals
     // set by choose()
     int m_tiles, n_tiles, tiles;

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
             const int m0 = tile.m + (int)half * 128;
             const int n0 = tile.n + (s.mode == kSideBySide ? 0 : (int)half * (tile.half ? 64 : 128));
             // (a single block leaves out the half of A's rows that no token has: their results are not read)
-            const int a_boxes = !PAIR && s.M - tile.m <= kBox ? 1 : 2;
+            const int a_boxes = !PAIR && s.M - tile.m <= kBox && !s.twice ? 1 : 2;
             const uint32_t bytes = PAIR ? 2 * kPairStage - (tile.half ? 2 * kBoxBytes : 0) : a_boxes * kBoxBytes + s.b_bytes;
             for (int k = k_begin; k < k_end; ++k, ++n) {
                 if (!wait_all<PAIR>(bar(C::b_empty + st), ph ^ 1u, abort_flag)) {
@@ -300,6 +300,9 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 ptx::tc_fence_after();
                 const uint64_t a = first + ((st * stage_bytes) >> 4);
                 ptx::mma64_one<PAIR>(d, a, a + (2 * kBoxBytes >> 4), idesc, a_step, b_step, k > k_begin);
+                // (the rows of the second half of the tile are then no one's, and not read)
+                if (!PAIR && s.twice)
+                    ptx::mma64_one<PAIR>(d, a + (kBoxBytes >> 4), a + (2 * kBoxBytes >> 4), idesc, a_step, b_step, 1);
                 ptx::mma_commit_one<PAIR>(bar(C::b_empty + st), 3);
                 if (++st == stages) st = 0, ph ^= 1u;
             }

@@ -9,6 +9,7 @@
 // loads per thread are under way, 96 KB per SM (eight: 3% slower).  x lies in shared memory in FP32.
 // One token, 5120 x 12800 BF16: 65.5 us for 393 MB (6.0 TB/s, 88% of the copy rate), of
 // which the first launch 43 and the second 25; by the product kernel 91.
+// act(g) u stays in FP32 between the two launches.
 // Sums are FP32 in a fixed order: per thread, over the lanes, over the quarters.
 // Rows that do not start at 16 bytes are read as 4-byte words, with x shifted by one
 // element for rows that start in the middle of one.
@@ -28,15 +29,18 @@ constexpr int kBlocks = 152, kThreads = 512, kQuarters = 4, kGroups = kThreads /
 constexpr int kRows = 4;       // weight rows of a warp at a time
 constexpr int kUnroll = 3;
 
-template <class T>
+// The first launch (DUAL) leaves act(g) u in FP32 for the second.
+template <class T, bool DUAL>
 struct TokenArgs {
-    const T *w0, *w1;      // [R, K]; w1: the up projection (dual)
+    using X = std::conditional_t<DUAL, T, float>;
+    using Out = std::conditional_t<DUAL, float, T>;
+    const T *w0, *w1;      // [R, K]; w1: the up projection (DUAL)
     int64_t R;
     int K;
-    const T* x;            // [tokens, K], rows x_ld apart
+    const X* x;            // [tokens, K], rows x_ld apart
     int64_t x_ld;
     int tokens;
-    T* out;                // [tokens, R], rows out_ld apart: act(g) u, or the products
+    Out* out;              // [tokens, R], rows out_ld apart: act(g) u, or the products
     int64_t out_ld;
     T *gate, *up;          // [tokens, R] or null
     int activation;
@@ -56,7 +60,9 @@ size_t token_smem(int tokens, int K, int64_t R, bool dual) {
 }
 
 template <class T, int NT, bool DUAL, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T> a) {
+__global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T, DUAL> a) {
+    using X = typename TokenArgs<T, DUAL>::X;
+    using Out = typename TokenArgs<T, DUAL>::Out;
     extern __shared__ float4 shared[];
     float* xs = reinterpret_cast<float*>(shared);
     constexpr int kOutputs = DUAL ? kRows / 2 : kRows;     // rows of the output per warp and turn
@@ -72,23 +78,30 @@ __global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T> a
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(a.w0) + i));
     ptx::grid_dependency_wait();
 
-    const size_t x_bytes = ((a.tokens - 1) * a.x_ld + K) * sizeof(T);
+    const size_t x_bytes = ((a.tokens - 1) * a.x_ld + K) * sizeof(X);
     if constexpr (WIDE) {
         for (int i = threadIdx.x; i < NT * (K / 8); i += kThreads) {
             const int t = NT == 1 ? 0 : i / (K / 8), v = i - t * (K / 8);
-            const T* p = a.x + t * a.x_ld + v * 8;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (t < a.tokens && check::in(p, 16, a.x, x_bytes, 12)) u = *reinterpret_cast<const uint4*>(p);
-            const float2 e0 = product::Pair16<T>::unpack(u.x), e1 = product::Pair16<T>::unpack(u.y),
-                         e2 = product::Pair16<T>::unpack(u.z), e3 = product::Pair16<T>::unpack(u.w);
-            *reinterpret_cast<float4*>(xs + t * xn + v * 4) = make_float4(e0.x, e0.y, e1.x, e1.y);
-            *reinterpret_cast<float4*>(xs + t * xn + K / 2 + v * 4) = make_float4(e2.x, e2.y, e3.x, e3.y);
+            const X* p = a.x + t * a.x_ld + v * 8;
+            float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+            if (t < a.tokens && check::in(p, 8 * sizeof(X), a.x, x_bytes, 12)) {
+                if constexpr (sizeof(X) == 4) {
+                    lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
+                } else {
+                    const uint4 u = *reinterpret_cast<const uint4*>(p);
+                    const float2 e0 = product::Pair16<X>::unpack(u.x), e1 = product::Pair16<X>::unpack(u.y),
+                                 e2 = product::Pair16<X>::unpack(u.z), e3 = product::Pair16<X>::unpack(u.w);
+                    lo = make_float4(e0.x, e0.y, e1.x, e1.y), hi = make_float4(e2.x, e2.y, e3.x, e3.y);
+                }
+            }
+            *reinterpret_cast<float4*>(xs + t * xn + v * 4) = lo;
+            *reinterpret_cast<float4*>(xs + t * xn + K / 2 + v * 4) = hi;
         }
     } else {
         for (int i = threadIdx.x; i < NT * K; i += kThreads) {
             const int t = i / K, k = i - t * K;
-            const T* p = a.x + t * a.x_ld + k;
-            const float v = t < a.tokens && check::in(p, sizeof(T), a.x, x_bytes, 12) ? (float)*p : 0.f;
+            const X* p = a.x + t * a.x_ld + k;
+            const float v = t < a.tokens && check::in(p, sizeof(X), a.x, x_bytes, 12) ? (float)*p : 0.f;
             xs[t * xn + k] = xs[t * xn + xn / 2 + k + 1] = v;
         }
     }
@@ -205,23 +218,23 @@ __global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T> a
             return v;
         };
         const int64_t f = first + r;
-        T* o = a.out + t * a.out_ld + f;
-        const bool ok = check::in(o, sizeof(T), a.out, ((a.tokens - 1) * a.out_ld + a.R) * sizeof(T), 15);
+        Out* o = a.out + t * a.out_ld + f;
+        const bool ok = check::in(o, sizeof(Out), a.out, ((a.tokens - 1) * a.out_ld + a.R) * sizeof(Out), 15);
         if constexpr (DUAL) {
             const float g = total(2 * r), u = total(2 * r + 1);
-            if (ok) *o = (T)(activate(g, a.activation).x * u);
+            if (ok) *o = activate(g, a.activation).x * u;
             if (a.gate != nullptr && check::in(a.gate + t * a.R + f, sizeof(T), a.gate, a.tokens * a.R * sizeof(T), 16)) {
                 a.gate[t * a.R + f] = (T)g;
                 a.up[t * a.R + f] = (T)u;
             }
         } else if (ok) {
-            *o = (T)total(r);
+            *o = (Out)total(r);
         }
     }
 }
 
 template <class T, int NT, bool DUAL, bool WIDE>
-cudaError_t launch(const TokenArgs<T>& a, cudaStream_t stream) {
+cudaError_t launch(const TokenArgs<T, DUAL>& a, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     auto* kernel = token_kernel<T, NT, DUAL, WIDE>;
     const cudaError_t e = ops::allow_shared(kernel, (int)product::kSharedMost, done);
@@ -232,43 +245,44 @@ cudaError_t launch(const TokenArgs<T>& a, cudaStream_t stream) {
     return ops::launch_early(kernel, dim3(kBlocks), dim3(kThreads), smem > half ? smem : half, stream, a);
 }
 template <class T, bool DUAL, bool WIDE>
-cudaError_t by_tokens(const TokenArgs<T>& a, cudaStream_t stream) {
+cudaError_t by_tokens(const TokenArgs<T, DUAL>& a, cudaStream_t stream) {
     return a.tokens == 1 ? launch<T, 1, DUAL, WIDE>(a, stream)
                          : a.tokens == 2 ? launch<T, 2, DUAL, WIDE>(a, stream) : launch<T, 4, DUAL, WIDE>(a, stream);
 }
 template <class T, bool DUAL>
-cudaError_t by_rows(const TokenArgs<T>& a, cudaStream_t stream) {
+cudaError_t by_rows(const TokenArgs<T, DUAL>& a, cudaStream_t stream) {
     return a.K % 8 == 0 ? by_tokens<T, DUAL, true>(a, stream) : by_tokens<T, DUAL, false>(a, stream);
 }
 
 template <class T>
 cudaError_t forward_as(const Args& a, cudaStream_t stream) {
-    TokenArgs<T> t{};
-    t.w0 = static_cast<const T*>(a.w_gate);
-    t.w1 = static_cast<const T*>(a.w_up);
-    t.R = a.F;
-    t.K = (int)a.D;
-    t.x = static_cast<const T*>(a.x);
-    t.x_ld = a.x_stride;
-    t.tokens = (int)a.T;
-    t.out = static_cast<T*>(a.workspace);
-    t.out_ld = a.F;
-    t.gate = static_cast<T*>(a.gate);
-    t.up = static_cast<T*>(a.up);
-    t.activation = a.activation;
-    const cudaError_t e = by_rows<T, true>(t, stream);
+    float* hidden = static_cast<float*>(a.workspace);
+    TokenArgs<T, true> first{};
+    first.w0 = static_cast<const T*>(a.w_gate);
+    first.w1 = static_cast<const T*>(a.w_up);
+    first.R = a.F;
+    first.K = (int)a.D;
+    first.x = static_cast<const T*>(a.x);
+    first.x_ld = a.x_stride;
+    first.tokens = (int)a.T;
+    first.out = hidden;
+    first.out_ld = a.F;
+    first.gate = static_cast<T*>(a.gate);
+    first.up = static_cast<T*>(a.up);
+    first.activation = a.activation;
+    const cudaError_t e = by_rows(first, stream);
     if (e != cudaSuccess) return e;
-    t = {};
-    t.w0 = static_cast<const T*>(a.w_down);
-    t.R = a.D;
-    t.K = (int)a.F;
-    t.x = static_cast<const T*>(a.workspace);
-    t.x_ld = a.F;
-    t.tokens = (int)a.T;
-    t.out = static_cast<T*>(a.y);
-    t.out_ld = a.y_stride;
-    t.after = 1;
-    return by_rows<T, false>(t, stream);
+    TokenArgs<T, false> second{};
+    second.w0 = static_cast<const T*>(a.w_down);
+    second.R = a.D;
+    second.K = (int)a.F;
+    second.x = hidden;
+    second.x_ld = a.F;
+    second.tokens = (int)a.T;
+    second.out = static_cast<T*>(a.y);
+    second.out_ld = a.y_stride;
+    second.after = 1;
+    return by_rows(second, stream);
 }
 
 bool fits(int tokens, int64_t K, int64_t R, bool dual) {

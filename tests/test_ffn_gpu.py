@@ -14,7 +14,7 @@ from matrix_cases import DEV, f64
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
 
-SMALL = [(3, 75, 141), (4, 1001, 77), (2, 2048, 4096), (1, 1027, 515), (1, 1, 1), (1, 8, 8), (1, 64, 64), (2, 7, 3), (1, 136, 1000), (5, 1000, 136), (8, 2048, 72), (64, 256, 512),
+SMALL = [(8, 1024, 2560), (48, 520, 3000), (7, 264, 5000), (64, 72, 136), (65, 72, 136), (3, 75, 141), (4, 1001, 77), (2, 2048, 4096), (1, 1027, 515), (1, 1, 1), (1, 8, 8), (1, 64, 64), (2, 7, 3), (1, 136, 1000), (5, 1000, 136), (8, 2048, 72), (64, 256, 512),
          (127, 129, 131), (128, 128, 128), (129, 320, 257), (257, 200, 264), (300, 65, 700)]
 # tiles of 256 x 256 in every product, in some, odd ones
 LARGE = [(1100, 1601, 1600), (300, 2600, 2568), (2049, 136, 2500), (700, 1032, 3432)]
@@ -62,6 +62,26 @@ def test_added_gradients(T, D, F, type_, grad_type):
 def test_outputs_left_out(which, accumulate):
     M.ffn_backward_case(40, 72, 200, "bf16", which=which, accumulate=accumulate, seed=3)
     M.ffn_backward_case(21, 75, 141, "bf16", which=which, accumulate=accumulate, seed=3)
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 40, 64])
+def test_few_tokens_lose_nothing_between_the_products(T):
+    """Up to 64 tokens the forward's and grad_x's only rounding to 16 bits is the output's: with few
+    elements the ones between the products would not average out.  (FP32 sums and the 16 bits that are
+    kept of a, dg and du: below 2^-13 of the result in the 2-norm.)"""
+    D, F = 72, 264
+    _, x, wg, wu, wd = M.inputs(T, D, F, BF, T)
+    y = torch.empty_like(x)
+    gate, up = (torch.empty(T, F, dtype=BF, device=DEV) for _ in range(2))
+    ws, _ = M.scratch(max(m.mhc_ffn_forward_workspace_bytes(T, D, F), m.mhc_ffn_backward_workspace_bytes(T, D, F)))
+    m.mhc_ffn_forward(x, wg, wu, wd, y, ws, gate, up)
+    m.mhc_ffn_backward(x, wg, wu, wd, gate, up, x, dx := torch.empty_like(x), None, None, None, ws)
+    inputs = list(map(f64, (x, wg, wu, wd)))
+    ref = [O.ffn_forward(*inputs, "silu", "bf16")[0][0], O.ffn_backward(*inputs, f64(gate), f64(up), inputs[0], "silu", "bf16", "bf16")[0][0]]
+    for got, r in zip((y, dx), ref):
+        once = torch.from_numpy(r).float().to(BF).double().numpy()
+        assert abs(f64(got) - r).max() <= (2.0 ** -8 + 2.0 ** -11) * abs(r).max()
+        assert ((f64(got) - r) ** 2).sum() ** 0.5 <= ((once - r) ** 2).sum() ** 0.5 + 2.0 ** -13 * (r ** 2).sum() ** 0.5
 
 
 def test_no_outputs_and_no_tokens():

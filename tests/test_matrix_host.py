@@ -121,10 +121,12 @@ def test_workspace_sizes(lib):
     # one [T, F] of 16 bits, and for odd sizes the copies of x, the projections and w_down in padded rows
     assert m.mhc_ffn_forward_workspace_bytes(100, 64, 200) == up(100 * 200 * 2)
     assert m.mhc_ffn_forward_workspace_bytes(100, 65, 201) == up(100 * 208 * 2) + up(100 * 72 * 2) + 2 * up(201 * 72 * 2) + up(65 * 208 * 2)
-    # few tokens need no copies
-    assert m.mhc_ffn_forward_workspace_bytes(2, 65, 201) == up(2 * 208 * 2)
+    # up to 64 tokens also what its rounding lost, from row 64 on; of few tokens it is FP32, with no copies
+    assert m.mhc_ffn_forward_workspace_bytes(40, 64, 200) == up((64 + 40) * 200 * 2)
+    assert m.mhc_ffn_forward_workspace_bytes(2, 65, 201) == up(2 * 201 * 4)
     # dg, du and a; both inputs and all weights in padded rows
     assert m.mhc_ffn_backward_workspace_bytes(100, 64, 200) == 3 * up(100 * 200 * 2)
+    assert m.mhc_ffn_backward_workspace_bytes(40, 64, 200) == up(40 * 200 * 2) + 2 * up((64 + 40) * 200 * 2)
     assert m.mhc_ffn_backward_workspace_bytes(100, 65, 201) == 3 * up(100 * 208 * 2) + 2 * up(100 * 72 * 2) + 2 * up(201 * 72 * 2) + up(65 * 208 * 2)
     # a short side of at most 32 is held on chip
     assert m.mhc_orthogonalize_workspace_bytes(24, 20480) == 0 == m.mhc_orthogonalize_workspace_bytes(5000, 32)
