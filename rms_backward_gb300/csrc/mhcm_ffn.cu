@@ -10,8 +10,9 @@
 // and a again from the stored g and u, so a is not kept between the two.  dx is
 // one sum over both halves.  a, dg and du are operands of further products and so
 // are rounded to the operands' 16-bit type (up to 64 tokens with a second number for
-// what that loses, see store_both); everything else is FP32 until the output is stored.  Rows that are not a multiple of 8 elements long are copied
-// to rows that are (the tensor maps' 16-byte rule).
+// what that loses, see store_both); everything else is FP32 until the output is
+// stored.  Rows that are not a multiple of 8 elements long are copied to rows that are
+// (the tensor maps' 16-byte rule).
 #include "mhcm_ffn.cuh"
 #include "mhcm_product.cuh"
 
