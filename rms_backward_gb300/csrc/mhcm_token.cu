@@ -11,8 +11,12 @@
 // which the first launch 43 and the second 25; by the product kernel 91.
 // act(g) u stays in FP32 between the two launches.
 // Sums are FP32 in a fixed order: per thread, over the lanes, over the quarters.
-// Rows that do not start at 16 bytes are read as 4-byte words, with x shifted by one
-// element for rows that start in the middle of one.
+// Rows that do not start at 16 bytes are read by the aligned 16-byte vectors that hold
+// them, and x at the shift: element k lies in plane k mod 8 at k / 8, so that the lanes
+// read neighbours whatever the shift is, and one copy of x serves all eight.
+// 7261 x 12360: one token 116 us, two 139 (words of 4 bytes, one element shifted: 710),
+// four 236, bound by reading x, 4 bytes per weight and token (by the product kernel
+// with padded copies of the weights 258).
 #include "mhcm_ffn.cuh"
 #include "mhcm_product.cuh"
 
@@ -47,17 +51,25 @@ struct TokenArgs {
     int after;             // x comes from the launch before, the weights do not
 };
 
+// Vectors of eight elements that hold a row of K, wherever it starts.
+__host__ __device__ constexpr int row_vectors(int K) { return (K + 14) / 8; }
+// Floats of one plane: a zero, the vectors', and what keeps eight planes on different banks.
+__host__ __device__ constexpr int plane_floats(int K) { return (row_vectors(K) + 4) / 8 * 8 + 4; }
 // Elements of x in shared memory per token.  WIDE: the first and the second four of every eight apart
-// (vectors without bank conflicts).  Else twice, the second copy one element later, with zeros around.
+// (vectors without bank conflicts).  Else eight planes.
 template <bool WIDE>
 __host__ __device__ constexpr int x_floats(int K) {
-    return WIDE ? K : 2 * ((K + 4) / 2 * 2);
+    return WIDE ? K : 8 * plane_floats(K);
 }
 template <bool WIDE>
 size_t token_smem(int tokens, int K, int64_t R, bool dual) {
     const int64_t rows = (R + kBlocks - 1) / kBlocks + 1;
     return ((size_t)tokens * x_floats<WIDE>(K) + (size_t)rows * (dual ? 2 : 1) * kQuarters * tokens) * 4;
 }
+
+// Elements of other rows ahead of `row` in the 16 bytes that it starts in.
+template <class T>
+__device__ int ahead(const T* row) { return (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 7); }
 
 template <class T, int NT, bool DUAL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T, DUAL> a) {
@@ -67,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T, D
     float* xs = reinterpret_cast<float*>(shared);
     constexpr int kOutputs = DUAL ? kRows / 2 : kRows;     // rows of the output per warp and turn
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) % kQuarters, group = threadIdx.x / (32 * kQuarters);
-    const int K = a.K, xn = x_floats<WIDE>(K);
+    const int K = a.K, xn = x_floats<WIDE>(K), plane = plane_floats(K);
     float* part = xs + (size_t)NT * xn;                    // [row of the block][which of two][quarter][token]
     const int64_t first = blockIdx.x * a.R / gridDim.x, end = (blockIdx.x + 1) * a.R / gridDim.x;
     const size_t weight_bytes = (size_t)a.R * K * sizeof(T);
@@ -98,22 +110,17 @@ __global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T, D
             *reinterpret_cast<float4*>(xs + t * xn + K / 2 + v * 4) = hi;
         }
     } else {
-        for (int i = threadIdx.x; i < NT * K; i += kThreads) {
-            const int t = i / K, k = i - t * K;
+        const int across = 8 * (plane - 1);                // elements 0 .. K - 1 and zeros on both sides
+        for (int i = threadIdx.x; i < NT * (across + 8); i += kThreads) {
+            const int t = i / (across + 8), k = i - t * (across + 8) - 8;
             const X* p = a.x + t * a.x_ld + k;
-            const float v = t < a.tokens && check::in(p, sizeof(X), a.x, x_bytes, 12) ? (float)*p : 0.f;
-            xs[t * xn + k] = xs[t * xn + xn / 2 + k + 1] = v;
+            const bool is = t < a.tokens && k >= 0 && k < K && check::in(p, sizeof(X), a.x, x_bytes, 12);
+            xs[t * xn + (k & 7) * plane + 1 + (k >> 3)] = is ? (float)*p : 0.f;
         }
     }
-    if constexpr (!WIDE)
-        for (int t = threadIdx.x; t < NT; t += kThreads) {
-            xs[t * xn + xn / 2] = 0.f;
-            for (int k = K; k < xn / 2; ++k) xs[t * xn + k] = 0.f;
-            for (int k = K + 1; k < xn / 2; ++k) xs[t * xn + xn / 2 + k] = 0.f;
-        }
     __syncthreads();
 
-    const int vectors = WIDE ? K / 8 : (K + 2) / 2;        // (a row from the middle of a word has one more)
+    const int vectors = WIDE ? K / 8 : row_vectors(K);
     const int v0 = (int)((int64_t)quarter * vectors / kQuarters), v1 = (int)((int64_t)(quarter + 1) * vectors / kQuarters);
     for (int64_t f = first + group * kOutputs; f < end; f += kGroups * kOutputs) {
         uint64_t acc[NT][kRows];
@@ -165,32 +172,56 @@ __global__ void __launch_bounds__(kThreads, 1) token_kernel(const TokenArgs<T, D
                     }
                 }
             } else {
+                // vector i of a row: elements 8 i - ahead .. 8 i - ahead + 7, of which the first and the last
+                // vector have some of the rows beside it
+                uint4 u[kUnroll][kRows];
 #pragma unroll
                 for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
                     for (int r = 0; r < kRows; ++r) {
-                        // word i of the row: elements 2 i - odd and 2 i + 1 - odd, where they are the row's
-                        const int i = v + 32 * j;
-                        const int odd = (int)((reinterpret_cast<uintptr_t>(row[r]) >> 1) & 1);
-                        if (!valid[r] || i >= v1 || 2 * i - odd >= K) continue;
-                        const T* p = row[r] + 2 * i - odd;
+                        u[j][r] = make_uint4(0, 0, 0, 0);
+                        const int k = 8 * (v + 32 * j) - ahead(row[r]);
+                        const T* p = row[r] + k;
                         const T* const base = DUAL && (r & 1) ? a.w1 : a.w0;
-                        const bool both = 2 * i + 1 - odd < K;
-                        float2 e = make_float2(0.f, 0.f);
-                        if (2 * i - odd >= 0 && both) {
-                            if (check::in(p, 4, base, weight_bytes, 14))
-                                e = product::Pair16<T>::unpack(*reinterpret_cast<const uint32_t*>(p));
-                        } else if (both) {
-                            if (check::in(p + 1, 2, base, weight_bytes, 14)) e.y = (float)p[1];
-                        } else if (check::in(p, 2, base, weight_bytes, 14)) {
-                            e.x = (float)p[0];
-                        }
+                        if (!valid[r] || v + 32 * j >= v1 || k >= K) continue;
+                        if (p >= base && p + 8 <= base + a.R * K) {
+                            if (check::in(p, 16, base, weight_bytes, 14)) u[j][r] = __ldcs(reinterpret_cast<const uint4*>(p));
+                        } else {   // the matrix's first or last
+                            uint32_t w[4] = {};
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            const float2 x = *reinterpret_cast<const float2*>(xs + t * xn + (odd ? xn / 2 : 0) + 2 * i);
-                            acc[t][r] = fma2(pair(e.x, e.y), pair(x.x, x.y), acc[t][r]);
+                            for (int q = 0; q < 8; ++q)
+                                if (k + q >= 0 && k + q < K && check::in(p + q, 2, base, weight_bytes, 14))
+                                    w[q / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[q] << (16 * (q & 1));
+                            u[j][r] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const int shift = ahead(row[r]);
+                    int at[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) at[q] = ((q - shift) & 7) * plane + 1 + ((q - shift) >> 3);
+#pragma unroll
+                    for (int j = 0; j < kUnroll; ++j) {
+                        const int i = v + 32 * j, k = 8 * i - shift;
+                        if (i >= v1) break;
+                        uint32_t w[4] = {u[j][r].x, u[j][r].y, u[j][r].z, u[j][r].w};
+                        if (k < 0 || k + 8 > K) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (k + q < 0 || k + q >= K) w[q / 2] &= q & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 e = product::Pair16<T>::unpack(w[q]);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                const float* x = xs + t * xn + i;
+                                acc[t][r] = fma2(pair(e.x, e.y), pair(x[at[2 * q]], x[at[2 * q + 1]]), acc[t][r]);
+                            }
+                        }
+                    }
+                }
             }
         }
 #pragma unroll

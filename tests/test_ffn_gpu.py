@@ -15,6 +15,7 @@ pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
 
 SMALL = [(8, 1024, 2560), (48, 520, 3000), (7, 264, 5000), (64, 72, 136), (65, 72, 136), (3, 75, 141), (4, 1001, 77), (2, 2048, 4096), (1, 1027, 515), (1, 1, 1), (1, 8, 8), (1, 64, 64), (2, 7, 3), (1, 136, 1000), (5, 1000, 136), (8, 2048, 72), (64, 256, 512),
+         (1, 5003, 2309), (2, 2309, 4501), (4, 1286, 1284),
          (127, 129, 131), (128, 128, 128), (129, 320, 257), (257, 200, 264), (300, 65, 700)]
 # tiles of 256 x 256 in every product, in some, odd ones
 LARGE = [(1100, 1601, 1600), (300, 2600, 2568), (2049, 136, 2500), (700, 1032, 3432)]
@@ -130,6 +131,28 @@ def test_a_token_keeps_its_non_finite_values(T):
     for p, q in zip(clean, got):
         assert torch.equal(p[keep], q[keep]) and not torch.isfinite(q[1]).any()
         assert not torch.isfinite(q[2]).all()
+
+
+@pytest.mark.parametrize("T,D,F", [(1, 1027, 515), (2, 75, 141), (4, 139, 77), (1, 136, 264), (70, 75, 141)])
+def test_a_row_of_weights_keeps_its_non_finite_values(T, D, F):
+    """NaN in some rows of the weights reaches those rows' products only: rows that share 16 bytes do not mix."""
+    _, x, wg, wu, wd = M.inputs(T, D, F, BF, 6)
+    ws, _ = M.scratch(m.mhc_ffn_forward_workspace_bytes(T, D, F))
+    clean = [torch.empty(T, n, dtype=BF, device=DEV) for n in (D, F, F)]
+    m.mhc_ffn_forward(x, wg, wu, wd, clean[0], ws, *clean[1:])
+    got = [torch.empty_like(t) for t in clean]
+    gates, downs = [0, 2, F // 2, F - 1], [1, D // 3, D - 2]
+    bad = wd.clone()
+    bad[downs] = float("nan")
+    m.mhc_ffn_forward(x, wg, wu, bad, got[0], ws, *got[1:])
+    keep = [i for i in range(D) if i not in downs]
+    assert torch.equal(got[0][:, keep], clean[0][:, keep]) and got[0][:, downs].isnan().all()
+    bad, up = wg.clone(), wu.clone()
+    bad[gates], up[gates] = float("nan"), float("inf")
+    m.mhc_ffn_forward(x, bad, up, wd, got[0], ws, *got[1:])
+    keep = [i for i in range(F) if i not in gates]
+    assert all(torch.equal(q[:, keep], c[:, keep]) and not q[:, gates].isfinite().any()
+               for q, c in zip(got[1:], clean[1:]))
 
 
 def test_large_gates():
