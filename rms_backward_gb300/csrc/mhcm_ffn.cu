@@ -47,6 +47,7 @@ struct GatedEpilogue {
     static constexpr bool kDual = true, kMirror = false;
     Matrix<T> hidden, gate, up;
     bool both;
+    __device__ __forceinline__ void ahead(int, int64_t, int64_t, int) const {}
     template <class Span>
     struct Read {};
     template <class Span>
@@ -72,6 +73,8 @@ struct GradEpilogue {
     static constexpr bool kDual = false, kMirror = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
     bool both;
+    // (gate and up sent for ahead: 4,096 tokens took 1% longer, 1,000 the same)
+    __device__ __forceinline__ void ahead(int, int64_t, int64_t, int) const {}
     template <class Span>
     struct Read {
         product::Raw<T, Span> g, u;
@@ -102,15 +105,22 @@ struct GradEpilogue {
 template <class O>
 struct StoreEpilogue {
     static constexpr bool kDual = false, kMirror = false;
-    Matrix<O> out[2];
+    // (not an array: an index that is not known when it is compiled puts the arguments into local memory, and
+    // every access waits for that: the block's gradient of one token, 7264 x 12360, took 406 us for 316, added 985 for 451)
+    Matrix<O> out;
+    O* second;   // the second group's, of the same shape
     bool accumulate;
+    __device__ __forceinline__ Matrix<O> of(int group) const { return {group ? second : out.ptr, out.ld, out.elements}; }
+    __device__ __forceinline__ void ahead(int group, int64_t row, int64_t col, int cols) const {
+        if (accumulate) of(group).ahead(row, col, cols);
+    }
     template <class Span>
     struct Read {
         product::Raw<O, Span> old;
     };
     template <class Span>
     __device__ __forceinline__ Read<Span> read(int group, const Span& at) const {
-        return accumulate ? Read<Span>{out[group].raw(at, 9)} : Read<Span>{};
+        return accumulate ? Read<Span>{of(group).raw(at, 9)} : Read<Span>{};
     }
     template <class Span>
     __device__ __forceinline__ void write(int group, const Span& at, const float (&v)[Span::n], const float (&)[Span::n],
@@ -119,7 +129,7 @@ struct StoreEpilogue {
         in.old.to(r);   // (zeros where nothing is added to)
 #pragma unroll
         for (int i = 0; i < Span::n; ++i) r[i] = accumulate ? r[i] + v[i] : v[i];
-        out[group].store(at, r, 8);
+        of(group).store(at, r, 8);
     }
 };
 
@@ -242,8 +252,8 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
     s.narrow = !gated.gate.by_eight(F);
     MHCM_TRY(product::launch(s, gated, &x, nullptr, &wg, &wu, stream));
     s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain, s.twice = rows > T_;
-    const StoreEpilogue<T> store{{matrix<T>(a.y, T_, D, a.y_stride), {}}, false};
-    s.narrow = !store.out[0].by_eight(D);
+    const StoreEpilogue<T> store{matrix<T>(a.y, T_, D, a.y_stride), nullptr, false};
+    s.narrow = !store.out.by_eight(D);
     return product::launch(s, store, &h, nullptr, &wd, nullptr, stream);
 }
 
@@ -256,8 +266,8 @@ cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const
     s.M = M, s.N = N, s.k_steps = steps_of(a.T), s.mode = mode;
     s.a_mn = s.b_mn = 1;
     s.beside = beside;
-    const StoreEpilogue<O> store{{matrix<O>(out0, M, N, N), matrix<O>(out1, M, N, N)}, a.accumulate};
-    s.narrow = !store.out[0].by_eight(N);
+    const StoreEpilogue<O> store{matrix<O>(out0, M, N, N), static_cast<O*>(out1), a.accumulate != 0};
+    s.narrow = !store.out.by_eight(N);
     return product::launch(s, store, a0, a1, b, b, stream);
 }
 
@@ -298,8 +308,8 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
     bool beside = false;
     if (a.grad_x) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
-        const StoreEpilogue<T> store{{matrix<T>(a.grad_x, T_, D, a.gx_stride), {}}, false};
-        s.narrow = !store.out[0].by_eight(D);
+        const StoreEpilogue<T> store{matrix<T>(a.grad_x, T_, D, a.gx_stride), nullptr, false};
+        s.narrow = !store.out.by_eight(D);
         product::Factor dg_both = dg, du_both = du;
         if (rows > T_) {
             s.twice = 1;

@@ -187,5 +187,14 @@ __host__ __device__ constexpr uint32_t idesc_16bit(uint32_t M, uint32_t N, bool 
            ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// Bytes [p, end) towards L2: the 16-byte vectors that lie in them.
+__device__ __forceinline__ void prefetch_l2(const void* p, const void* end) {
+    const uint64_t from = (reinterpret_cast<uint64_t>(p) + 15) & ~15ull, to = reinterpret_cast<uint64_t>(end) & ~15ull;
+    if (to > from)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(reinterpret_cast<void*>(from))),
+                     "r"((uint32_t)(to - from))
+                     : "memory");
+}
+
 }  // namespace ptx
 }  // namespace mhcpb
