@@ -20,7 +20,7 @@
 // of rank 6, 1.0e-3.
 // A and A^2 are symmetric: tiles on and above the diagonal, written twice.
 //
-// 12800 x 5120 in FP32: 4.3 ms; a step alone takes 206 us for A (1.63 PFLOP/s of the
+// 12800 x 5120 in FP32: 4.2 ms; a step alone takes 206 us for A (1.63 PFLOP/s of the
 // half that is formed), 97 for B and 425 for X (1.58; it also moves 0.8 GB), the norm
 // and the first copy 107 (both read G: 0.6 GB in all).
 #include "mhcm_orth.cuh"

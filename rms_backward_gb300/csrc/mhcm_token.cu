@@ -7,7 +7,7 @@
 // of all.  Four warps share a row's k (quarters), four such groups take two pairs of
 // gate and up rows (or four rows of the second product) at a time: twelve 16-byte
 // loads per thread are under way, 96 KB per SM (eight: 3% slower).  x lies in shared memory in FP32.
-// One token, 5120 x 12800 BF16: 65.5 us for 393 MB (6.0 TB/s, 88% of the copy rate), of
+// One token, 5120 x 12800 BF16: 65 us for 393 MB (6.0 TB/s, 90% of the copy rate), of
 // which the first launch 43 and the second 25; by the product kernel 91.
 // act(g) u stays in FP32 between the two launches.
 // Sums are FP32 in a fixed order: per thread, over the lanes, over the quarters.
