@@ -260,12 +260,11 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
 // dWd, or dWg and dWu together or one of them: C = A^T B over the tokens
 template <class O>
 cudaError_t weight_gradient(const Args& a, int mode, int64_t M, int64_t N, const product::Factor* a0, const product::Factor* a1,
-                            const product::Factor* b, void* out0, void* out1, bool beside, cudaStream_t stream) {
+                            const product::Factor* b, void* out0, void* out1, cudaStream_t stream) {
     Shape s{};
     s.bf16 = a.type == MHCPB_BF16;
     s.M = M, s.N = N, s.k_steps = steps_of(a.T), s.mode = mode;
     s.a_mn = s.b_mn = 1;
-    s.beside = beside;
     const StoreEpilogue<O> store{matrix<O>(out0, M, N, N), static_cast<O*>(out1), a.accumulate != 0};
     s.narrow = !store.out.by_eight(N);
     return product::launch(s, store, a0, a1, b, b, stream);
@@ -302,10 +301,7 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
                                     rows > T_};
     s.narrow = !grad.gate.by_eight(F);
     MHCM_TRY(product::launch(s, grad, &dy, nullptr, &wd, nullptr, stream));
-    // The products that are left need only what the first wrote: each starts as soon as the one
-    // before it leaves room (its last tiles keep a part of the GPU busy), not when that has ended.
     s.stall = 0;
-    bool beside = false;
     if (a.grad_x) {
         s.N = D, s.k_steps = steps_of(F), s.mode = product::kLongK;
         const StoreEpilogue<T> store{matrix<T>(a.grad_x, T_, D, a.gx_stride), nullptr, false};
@@ -317,20 +313,14 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
             MHCM_TRY(du_both.make(bf16, grad_up, rows, F, Fp));
         }
         MHCM_TRY(product::launch(s, store, &dg_both, &du_both, &wg, &wu, stream));
-        beside = true;
     }
     if (a.grad_w[0] && a.grad_w[1]) {
-        MHCM_TRY(weight_gradient<O>(a, product::kGroups, F, D, &dg, &du, &x, a.grad_w[0], a.grad_w[1], beside,
-                                    stream));
-        beside = true;
+        MHCM_TRY(weight_gradient<O>(a, product::kGroups, F, D, &dg, &du, &x, a.grad_w[0], a.grad_w[1], stream));
     } else if (a.grad_w[0] || a.grad_w[1]) {
         MHCM_TRY(weight_gradient<O>(a, product::kPlain, F, D, a.grad_w[0] ? &dg : &du, nullptr, &x,
-                                    a.grad_w[0] ? a.grad_w[0] : a.grad_w[1], nullptr, beside, stream));
-        beside = true;
+                                    a.grad_w[0] ? a.grad_w[0] : a.grad_w[1], nullptr, stream));
     }
-    if (a.grad_w[2])
-        MHCM_TRY(weight_gradient<O>(a, product::kPlain, D, F, &dy, nullptr, &h, a.grad_w[2], nullptr, beside,
-                                    stream));
+    if (a.grad_w[2]) MHCM_TRY(weight_gradient<O>(a, product::kPlain, D, F, &dy, nullptr, &h, a.grad_w[2], nullptr, stream));
     return cudaSuccess;
 }
 

@@ -27,9 +27,6 @@ struct Shape {
     int mode;
     int a_mn, b_mn;    // the operand's rows are k (else its rows are m, or n)
     int bf16;          // else FP16
-    int beside;        // needs nothing of the launch before it, only of one before that (which the launch
-                       // before it waited for): it does not wait for that one to end before its work, but
-                       // before its own end, so that it still ends after it
     int narrow;        // the epilogue's matrices are taken element by element (see Eight)
     int twice;         // A's 64 rows are followed by 64 of what their rounding lost, which are multiplied too
                        // (M <= 64: single blocks)

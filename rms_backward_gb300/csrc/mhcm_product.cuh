@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
     ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem = *holder;
-    if (!s.beside) ptx::grid_dependency_wait();
+    // (every launch: only its own wait makes visible what an earlier one wrote, of the launch before the last one too)
+    ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
 
     // Tiles: every gridDim.x / cluster blocks-th one.  k steps of this block: all, or its share of a split sum.
@@ -554,7 +555,6 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         ptx::cluster_arrive();   // the parts stay until every block has read them
         ptx::cluster_wait();
     }
-    if (s.beside) ptx::grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- host
