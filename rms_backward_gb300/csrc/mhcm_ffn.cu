@@ -44,7 +44,7 @@ __device__ __forceinline__ void store_both(const Matrix<T>& m, Span at, const fl
 
 template <class T, int ACT>
 struct GatedEpilogue {
-    static constexpr bool kDual = true, kMirror = false;
+    static constexpr bool kDual = true, kMirror = false, kTwice = false;
     Matrix<T> hidden, gate, up;
     bool both;
     __device__ __forceinline__ void ahead(int, int64_t, int64_t, int) const {}
@@ -70,7 +70,7 @@ struct GatedEpilogue {
 
 template <class T, int ACT>
 struct GradEpilogue {
-    static constexpr bool kDual = false, kMirror = false;
+    static constexpr bool kDual = false, kMirror = false, kTwice = false;
     Matrix<T> gate, up, grad_gate, grad_up, hidden;   // gate and up are read
     bool both;
     // (gate and up sent for ahead: 4,096 tokens took 1% longer, 1,000 the same)
@@ -104,7 +104,7 @@ struct GradEpilogue {
 
 template <class O>
 struct StoreEpilogue {
-    static constexpr bool kDual = false, kMirror = false;
+    static constexpr bool kDual = false, kMirror = false, kTwice = true;
     // (not an array: an index that is not known when it is compiled puts the arguments into local memory, and
     // every access waits for that: the block's gradient of one token, 7264 x 12360, took 406 us for 316, added 985 for 451)
     Matrix<O> out;

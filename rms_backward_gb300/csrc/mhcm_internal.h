@@ -28,8 +28,8 @@ struct Shape {
     int a_mn, b_mn;    // the operand's rows are k (else its rows are m, or n)
     int bf16;          // else FP16
     int narrow;        // the epilogue's matrices are taken element by element (see Eight)
-    int twice;         // A's 64 rows are followed by 64 of what their rounding lost, which are multiplied too
-                       // (M <= 64: single blocks)
+    int twice;         // A's 64 rows are followed by 64 of what their rounding lost: both are multiplied, as rows
+                       // of one MMA, and the results added at the end (M <= 64: single blocks; Epilogue::kTwice)
     int stall;         // a test's: the MMA issuer waits for what nothing signals
     // set by choose()
     int m_tiles, n_tiles, tiles;

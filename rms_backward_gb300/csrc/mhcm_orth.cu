@@ -136,7 +136,7 @@ struct Diagonal {
 
 // A = C at kScaleA
 struct GramEpilogue {
-    static constexpr bool kDual = false, kMirror = true;
+    static constexpr bool kDual = false, kMirror = true, kTwice = false;
     Matrix<__half> out;
     Diagonal lost;
     __device__ __forceinline__ void ahead(int, int64_t, int64_t, int) const {}
@@ -160,7 +160,7 @@ struct GramEpilogue {
 // B = b A + c A^2 at kScaleB from C, the product of the rounded A's, and what the
 // diagonal lost: (A + l)^2 = A^2 + l A + A l + l^2
 struct PolynomialEpilogue {
-    static constexpr bool kDual = false, kMirror = true;
+    static constexpr bool kDual = false, kMirror = true, kTwice = false;
     Matrix<__half> out;
     Matrix<const __half> gram;
     Diagonal gram_lost, lost;
@@ -192,7 +192,7 @@ struct PolynomialEpilogue {
 
 // X = (a + B's lost diagonal) X + C
 struct UpdateEpilogue {
-    static constexpr bool kDual = false, kMirror = false;
+    static constexpr bool kDual = false, kMirror = false, kTwice = false;
     Input g;                    // the first step's X, times *inverse
     const Inverse* inverse;     // null after the first step
     Diagonal lost;

@@ -26,11 +26,11 @@ struct Layout {
     uint32_t smem;
 };
 Layout layout(const Shape& s, int columns, uint32_t b_bytes, int per_sm) {
-    // (twice: the MMA of A's second 64 rows reads 128 rows from there on, whose last 64 are B's place and,
-    // where B has fewer rows, what follows it: the last stage has to be followed by as much)
+    // (twice: the last stage is followed by what 128 rows from the middle of A's place on would reach, so that
+    // a descriptor may begin at either half)
     const uint32_t after = s.twice && b_bytes < kBoxBytes ? kBoxBytes - b_bytes : 0;
     const uint32_t fixed = 2048 + after, stage = 2 * kBoxBytes + b_bytes;
-    const uint32_t rows = s.M < 128 ? (uint32_t)over(s.M, 32) * 32 : 128;
+    const uint32_t rows = (s.twice ? 64 : 0) + (s.M < 128 ? (uint32_t)over(s.M, 32) * 32 : 128);
     const uint32_t part = rows * ((uint32_t)over(columns, 32) * 32 + 4) * 4;
     const uint32_t room = (per_sm == 2 ? 233472 / 2 - 1024 : kSharedMost) - fixed;
     if (part > room || room / stage < 2) return {0, 0};

@@ -151,6 +151,13 @@ __device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float
     v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
 }
 
+// The products of two numbers' first and of their second, where those of the first are finite.
+template <int N>
+__device__ __forceinline__ void add_second(float (&v)[N], const float (&w)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = isfinite(v[i]) ? v[i] + w[i] : v[i];
+}
+
 // The elements of one row of C that an epilogue takes at a time: eight neighbours, where the epilogue's
 // matrices have rows that start at 16 bytes and end at them or in a workspace's padding (which may be
 // written), else one (a warp then has 32 neighbours).
@@ -170,6 +177,7 @@ struct One {
 // Epilogue: struct with
 //   static constexpr bool kDual                    two products side by side
 //   static constexpr bool kMirror                  C is symmetric; its matrices are a workspace's (Eight always)
+//   static constexpr bool kTwice                   A may be two numbers (Shape::twice)
 //   template <class Span> struct Read              what elements' results need from memory
 //   void ahead(int group, int64_t row, int64_t col, int cols) const   what read() will read of a row, towards L2
 //   Read<Span> read(int group, const Span&) const
@@ -302,9 +310,6 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 ptx::tc_fence_after();
                 const uint64_t a = first + ((st * stage_bytes) >> 4);
                 ptx::mma64_one<PAIR>(d, a, a + (2 * kBoxBytes >> 4), idesc, a_step, b_step, k > k_begin);
-                // (the rows of the second half of the tile are then no one's, and not read)
-                if (!PAIR && s.twice)
-                    ptx::mma64_one<PAIR>(d, a + (kBoxBytes >> 4), a + (2 * kBoxBytes >> 4), idesc, a_step, b_step, 1);
                 ptx::mma_commit_one<PAIR>(bar(C::b_empty + st), 3);
                 if (++st == stages) st = 0, ph ^= 1u;
             }
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
             ptx::tc_fence_after();
             float* part = reinterpret_cast<float*>(smem + C::off_stages);   // over the (now idle) stages
             const int row = quad * 32 + lane;
-            if (ok && quad * 32 < s.M - tile.m)
+            if (ok && (Epilogue::kTwice && s.twice ? quad & 1 : quad) * 32 < s.M - tile.m)
                 for (int c = 0; c < (int)width; c += 32) {
                     uint32_t u[32];
                     ptx::tmem_ld_32x32b_x32(lanes + c, u);
@@ -485,6 +490,11 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         // One vector per thread at a time, in loops that are not unrolled: these launches are short, and
         // what they cost is the way of their instructions from memory (with four vectors at a time, their
         // loads side by side, 512 x 512 orthogonalised took 223 us for 155).
+        // Of an A of two numbers, the second's products are 64 rows further.  They are added where the first's are finite:
+        // an infinite weight makes the first's infinite, and the second's, of what rounding left of the same
+        // number, of any sign, or NaN where that is zero.
+        const bool twice = Epilogue::kTwice && s.twice;
+        const uint32_t further = 4u * 64u * (uint32_t)s.part_row;
         const int threads = s.split * C::threads, me = (int)rank * C::threads + threadIdx.x;
         if (!Epilogue::kMirror && s.narrow) {
             // a warp per row, four times 32 columns at a time (a lane has one element of each: their reads side by side)
@@ -506,13 +516,17 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
 #pragma unroll
                         for (int q = 0; q < kTimes; ++q) {
                             x[q] = first + 32 * q < cols ? ptx::ld_cluster_f32(p + 128 * q) : 0.f;
-                            y[q] = Epilogue::kDual && first + 32 * q < cols ? ptx::ld_cluster_f32(p + 128 * q + 4 * s.tile_n) : 0.f;
+                            y[q] = (Epilogue::kDual || twice) && first + 32 * q < cols
+                                       ? ptx::ld_cluster_f32(p + 128 * q + (Epilogue::kDual ? 4 * s.tile_n : further)) : 0.f;
                         }
 #pragma unroll
                         for (int q = 0; q < kTimes; ++q) v[q][0] += x[q], w[q][0] += y[q];
                     }
 #pragma unroll
-                    for (int q = 0; q < kTimes; ++q) epi.write(tile.group, at(q), v[q], w[q], read[q]);
+                    for (int q = 0; q < kTimes; ++q) {
+                        if (twice) add_second(v[q], w[q]);
+                        epi.write(tile.group, at(q), v[q], w[q], read[q]);
+                    }
                 }
         } else {
             const int across = (cols + 7) / 8, units = rows * across;
@@ -528,7 +542,10 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     add8(v, ptx::ld_cluster_f32x4(p), ptx::ld_cluster_f32x4(p + 16));
                     if constexpr (Epilogue::kDual)
                         add8(w, ptx::ld_cluster_f32x4(p + 4 * s.tile_n), ptx::ld_cluster_f32x4(p + 4 * s.tile_n + 16));
+                    else if (twice)
+                        add8(w, ptx::ld_cluster_f32x4(p + further), ptx::ld_cluster_f32x4(p + further + 16));
                 }
+                if (twice) add_second(v, w);
                 epi.write(tile.group, at, v, w, read);
             }
         }
