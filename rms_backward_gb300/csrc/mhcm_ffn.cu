@@ -26,8 +26,12 @@ using product::Shape;
 
 // Up to 64 tokens, a, dg and du are kept as two numbers of the type, the second what the first's rounding
 // lost, in row 64 further: the rounding between two products costs nothing to avoid there (the time is
-// the weights'), and with few elements it would not average out.
+// the weights'), and with few elements it would not average out.  In FP16 the second number is stored 2^11
+// times: as large as the first at most, and down to steps of 2^-36, where unscaled it would be lost for a
+// first number below 2^-13 (BF16 has the exponents of FP32).
 constexpr int64_t kLowRows = 64;
+template <class T>
+constexpr float kLowScale = std::is_same<T, __half>::value ? 2048.f : 1.f;
 template <class T, class Span>
 __device__ __forceinline__ void store_both(const Matrix<T>& m, Span at, const float (&v)[Span::n], bool both, uint32_t site) {
     m.store(at, v, site);
@@ -36,7 +40,7 @@ __device__ __forceinline__ void store_both(const Matrix<T>& m, Span at, const fl
 #pragma unroll
     for (int i = 0; i < Span::n; ++i) {
         const float high = (float)(T)v[i];
-        low[i] = isfinite(high) ? v[i] - high : 0.f;
+        low[i] = isfinite(high) ? (v[i] - high) * kLowScale<T> : 0.f;
     }
     at.row += kLowRows;
     m.store(at, low, site);
@@ -251,7 +255,7 @@ cudaError_t forward_as(const Args& a, cudaStream_t stream) {
                                       matrix<T>(a.up, T_, F, F), rows > T_};
     s.narrow = !gated.gate.by_eight(F);
     MHCM_TRY(product::launch(s, gated, &x, nullptr, &wg, &wu, stream));
-    s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain, s.twice = rows > T_;
+    s.N = D, s.k_steps = steps_of(F), s.mode = product::kPlain, s.twice = rows > T_, s.second = 1.f / kLowScale<T>;
     const StoreEpilogue<T> store{matrix<T>(a.y, T_, D, a.y_stride), nullptr, false};
     s.narrow = !store.out.by_eight(D);
     return product::launch(s, store, &h, nullptr, &wd, nullptr, stream);
@@ -308,7 +312,7 @@ cudaError_t backward_as(const Args& a, cudaStream_t stream) {
         s.narrow = !store.out.by_eight(D);
         product::Factor dg_both = dg, du_both = du;
         if (rows > T_) {
-            s.twice = 1;
+            s.twice = 1, s.second = 1.f / kLowScale<T>;
             MHCM_TRY(dg_both.make(bf16, grad_gate, rows, F, Fp));
             MHCM_TRY(du_both.make(bf16, grad_up, rows, F, Fp));
         }

@@ -30,6 +30,7 @@ struct Shape {
     int narrow;        // the epilogue's matrices are taken element by element (see Eight)
     int twice;         // A's 64 rows are followed by 64 of what their rounding lost: both are multiplied, as rows
                        // of one MMA, and the results added at the end (M <= 64: single blocks; Epilogue::kTwice)
+    float second;      // twice: what one of those rows' numbers stands for
     int stall;         // a test's: the MMA issuer waits for what nothing signals
     // set by choose()
     int m_tiles, n_tiles, tiles;

@@ -153,9 +153,9 @@ __device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float
 
 // The products of two numbers' first and of their second, where those of the first are finite.
 template <int N>
-__device__ __forceinline__ void add_second(float (&v)[N], const float (&w)[N]) {
+__device__ __forceinline__ void add_second(float (&v)[N], const float (&w)[N], float unit) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = isfinite(v[i]) ? v[i] + w[i] : v[i];
+    for (int i = 0; i < N; ++i) v[i] = isfinite(v[i]) ? fmaf(w[i], unit, v[i]) : v[i];
 }
 
 // The elements of one row of C that an epilogue takes at a time: eight neighbours, where the epilogue's
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     }
 #pragma unroll
                     for (int q = 0; q < kTimes; ++q) {
-                        if (twice) add_second(v[q], w[q]);
+                        if (twice) add_second(v[q], w[q], s.second);
                         epi.write(tile.group, at(q), v[q], w[q], read[q]);
                     }
                 }
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                     else if (twice)
                         add8(w, ptx::ld_cluster_f32x4(p + further), ptx::ld_cluster_f32x4(p + further + 16));
                 }
-                if (twice) add_second(v, w);
+                if (twice) add_second(v, w, s.second);
                 epi.write(tile.group, at, v, w, read);
             }
         }

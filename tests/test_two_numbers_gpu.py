@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.mhcm_oracle as O
 import rms_backward_gb300 as m
 
 import matrix_cases as M
@@ -56,3 +57,28 @@ def test_infinite_weights(T, D, F, type_):
         assert torch.equal(q[:, keep], c[:, keep]), name
         assert not np.isfinite(w[:, cols]).any() and np.isfinite(w[:, keep]).all()
         assert np.array_equal(f64(q[:, cols]), w[:, cols], equal_nan=True), name
+
+
+@pytest.mark.parametrize("type_", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 4, 5, 33, 64])
+@pytest.mark.parametrize("D,F", [(72, 264), (75, 141)])
+def test_small_values_lose_nothing(T, D, F, type_):
+    """a, dg and du of some 2^-18, of which FP16 alone keeps seven bits: y's and grad_x's only rounding to 16
+    bits is the output's.  (What is kept of them beside the first number has steps of 2^-36 in FP16, 16 bits in
+    BF16; with FP32 sums that is below 2^-13 of the result in the 2-norm.)"""
+    dtype = M.TYPES[type_]
+    g, x, wg, wu, wd = M.inputs(T, D, F, dtype, T + F)
+    small, large = 2.0 ** -8, 2.0 ** 8      # (powers of two: the weights stay as they are but for their size)
+    gate, up = (M.put(torch.randn(T, F, generator=g), dtype) for _ in range(2))
+    dy = M.put(2.0 ** -14 * torch.randn(T, D, generator=g), dtype)
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    ws, _ = M.scratch(max(m.mhc_ffn_forward_workspace_bytes(T, D, F), m.mhc_ffn_backward_workspace_bytes(T, D, F)))
+    forward, backward = (x, wg * small, wu * small, wd * large), (x, wg * large, wu * large, wd * 2.0 ** -4)
+    m.mhc_ffn_forward(*forward, y, ws)
+    m.mhc_ffn_backward(*backward, gate, up, dy, dx, None, None, None, ws)
+    ref = [O.ffn_forward(*map(f64, forward), "silu", type_)[0][0],
+           O.ffn_backward(*map(f64, (*backward, gate, up, dy)), "silu", type_, type_)[0][0]]
+    norm = lambda v: (v ** 2).sum() ** 0.5  # noqa: E731
+    for name, got, r in zip(("y", "grad_x"), (y, dx), ref):
+        once = torch.from_numpy(r).to(dtype).double().numpy()
+        assert norm(f64(got) - r) <= norm(once - r) + 2.0 ** -13 * norm(r), name
