@@ -43,6 +43,7 @@ struct Shape {
 };
 struct Choice {
     bool pair;
+    bool long_sum;     // a block's sum has more than kPieceSteps steps and is taken in pieces
     int grid;
     uint32_t smem;     // of a single block
 };
@@ -51,6 +52,10 @@ Choice choose(Shape& s);
 constexpr int kBox = 64;                           // columns, and mostly rows, of a box
 constexpr uint32_t kBoxBytes = kBox * kBox * 2;    // 8 KiB
 constexpr int kMaxStages = 8;
+// The tensor cores cut what they add to an FP32 accumulator, so that a sum of one sign loses some 2^-23 of
+// itself with every 16 terms (2^20 positive ones: 6.4e-3, 0.8 of that).  Sums of more steps of 64 k than this
+// are taken in pieces of as many (32,768 terms: 2e-4), which are added rounded.
+constexpr int kPieceSteps = 512;
 constexpr uint32_t kSharedMost = 232448;           // per block; two blocks share 233,472 with 1 KiB each for the system
 
 // A 16-bit factor of a product, and its map with boxes of 64 rows.

@@ -78,10 +78,12 @@ Choice choose(Shape& s) {
     // single blocks: B's rows per tile free where its rows are k and C is not symmetric; tried are those
     // that fill the GPU's places once or twice
     const bool free_n = !s.b_mn && s.mode != kSymmetric;
-    const int64_t unit = side ? 8 : 16, most = side ? 128 : 256, fixed = side ? 64 : 128, m_tiles = over(s.M, 128);
+    const int64_t unit = side ? 8 : 16, fixed = side ? 64 : 128, m_tiles = over(s.M, 128);
     double best = 1e300;
     Layout best_layout{};
-    for (int split = 1; split <= 8 && split <= steps; ++split)
+    for (int split = 1; split <= 8 && split <= steps; ++split) {
+        // (a long sum has its pieces beside it in TMEM: half of the columns, so that two blocks still share an SM's)
+        const int64_t most = (side ? 128 : 256) / (over(steps, split) > kPieceSteps ? 2 : 1);
         for (int per_sm = 1; per_sm <= 2; ++per_sm)
             for (int turns = 1; turns <= 2; ++turns) {
                 int64_t n = fixed;
@@ -105,10 +107,12 @@ Choice choose(Shape& s) {
                     s.split = split;
                 }
             }
+    }
     if (s.M > 128 && pair_cost <= best) {
         c.pair = true;
         s.tile_n = (int)pair_n;
         s.split = 1;
+        c.long_sum = steps > kPieceSteps;
         s.b_box = 0;
         s.m_tiles = (int)over(s.M, 256);
         s.n_tiles = (int)over(s.N, pair_n);
@@ -126,6 +130,8 @@ Choice choose(Shape& s) {
     s.b_bytes = free_n ? (uint32_t)columns * 128 : 2 * kBoxBytes;
     s.tmem_columns = 32;
     while (s.tmem_columns < columns) s.tmem_columns *= 2;
+    c.long_sum = over(steps, s.split) > kPieceSteps;
+    if (c.long_sum) s.tmem_columns *= 2;
     s.part_row = (columns + 31) / 32 * 32 + 4;   // 4 more: vectors of neighbouring rows in different banks
     s.stages = best_layout.stages;
     c.smem = best_layout.smem;

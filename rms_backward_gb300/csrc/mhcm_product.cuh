@@ -151,6 +151,37 @@ __device__ __forceinline__ void add8(float (&v)[8], const float4& x, const float
     v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
 }
 
+// A long sum's pieces, as the MMAs finish them at `from` (TMEM), added up at `to`: `columns` of them (a multiple
+// of 32), and as many `apart` further where that is not 0.  `done` and `free` are the pieces' barriers, `turn`
+// counts their uses.  False where a wait ran out.  (Out of line: a call that few launches make.)
+template <bool PAIR>
+static __device__ __noinline__ bool join_pieces(uint32_t done, uint32_t free, uint32_t from, uint32_t to, int columns, int apart,
+                                                int pieces, uint32_t turn, volatile uint32_t* abort_flag) {
+    for (int p = 0; p < pieces; ++p, ++turn) {
+        if (!wait_all<PAIR>(done, turn & 1u, abort_flag)) return false;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < (apart != 0 ? 2 : 1) * columns; c += 32) {
+            const uint32_t at = (uint32_t)(c < columns ? c : c - columns + apart);
+            uint32_t u[32], v[32];
+            ptx::tmem_ld_32x32b_x32(from + at, u);
+            ptx::tc_wait_ld_regs(u);
+            if (p > 0) {
+                ptx::tmem_ld_32x32b_x32(to + at, v);
+                ptx::tc_wait_ld_regs(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) + __uint_as_float(v[i]));
+            }
+            ptx::tmem_st_32x32b_x32(to + at, u);
+            ptx::tc_wait_st();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) ptx::mbar_arrive_cluster(free);
+    }
+    return true;
+}
+
 // The products of two numbers' first and of their second, where those of the first are finite.
 template <int N>
 __device__ __forceinline__ void add_second(float (&v)[N], const float (&w)[N], float unit) {
@@ -183,7 +214,9 @@ struct One {
 //   Read<Span> read(int group, const Span&) const
 //   void write(int group, const Span&, const float (&v)[Span::n], const float (&w)[Span::n], const Read<Span>&) const
 // (Span: Eight or One; w: the second product's, where kDual).  Several reads are under way before the first write.
-template <bool PAIR, class Epilogue>
+// LONG: a block's sum has more than kPieceSteps steps.  (A kernel of its own: as a branch of the others it
+// cost 1285 x 3427 orthogonalised 368 us for 363, its gradients 181 for 177.)
+template <bool PAIR, bool LONG, class Epilogue>
 __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
     product_kernel(const Shape s, const Epilogue epi, const __grid_constant__ CUtensorMap a0,
                    const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b0,
@@ -211,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(C::b_done + i), 1);
-            ptx::mbar_init(bar(C::b_free + i), 8 * C::blocks);
+            ptx::mbar_init(bar(C::b_free + i), PAIR ? 16 : 4);   // the epilogue's warps
         }
         ptx::mbar_init(bar(C::b_last), 1);
         ptx::fence_mbar_init();
@@ -235,6 +268,10 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
     const int k_begin = PAIR ? 0 : (int)((int64_t)rank * steps / s.split);
     const int k_end = PAIR ? steps : (int)((int64_t)(rank + 1) * steps / s.split);
     const bool leader = !PAIR || rank == 0;
+    // A long sum is taken in pieces: each is formed in the second half of TMEM's columns and added, rounded, to
+    // what is in the first.
+    const int pieces = LONG ? (k_end - k_begin + kPieceSteps - 1) / kPieceSteps : 1;
+    const uint32_t second_half = PAIR ? width : tmem_columns / 2;
 
     if (warp == 0) {
         const uint32_t half = PAIR ? rank : 0;
@@ -290,30 +327,33 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
         const uint64_t first = ptx::smem_desc(stage0, kBoxBytes, 1024, ptx::kLayoutSwizzle128B);
         uint32_t st = 0, ph = 0, done = 0;
         bool ok = true;
-        for (int t = first_tile; ok && t < s.tiles; t += step_tile, ++done) {
-            const uint32_t acc = done % C::accumulators, turn = done / C::accumulators;
+        for (int t = first_tile, from = k_begin; ok && t < s.tiles; ++done) {
+            const uint32_t acc = LONG ? 1 : done % C::accumulators, turn = LONG ? done : done / C::accumulators;
             if (!wait_all<PAIR>(bar(C::b_free + acc), (turn & 1u) ^ 1u, abort_flag)) {
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            const uint32_t d = tmem + acc * width, idesc = PAIR && t >= s.full ? idesc_half : idesc_whole;
+            const uint32_t d = tmem + acc * second_half, idesc = PAIR && t >= s.full ? idesc_half : idesc_whole;
+            const int to = LONG ? min(from + kPieceSteps, k_end) : k_end;
             if (s.stall && !wait_all<PAIR>(bar(C::b_last), 0u, abort_flag)) {   // a test's wait that nothing ends
                 ok = false;
                 break;
             }
-            for (int k = k_begin; k < k_end; ++k) {
+            for (int k = from; k < to; ++k) {
                 if (!wait_all<PAIR>(bar(C::b_full + st), ph, abort_flag)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
                 const uint64_t a = first + ((st * stage_bytes) >> 4);
-                ptx::mma64_one<PAIR>(d, a, a + (2 * kBoxBytes >> 4), idesc, a_step, b_step, k > k_begin);
+                ptx::mma64_one<PAIR>(d, a, a + (2 * kBoxBytes >> 4), idesc, a_step, b_step, k > from);
                 ptx::mma_commit_one<PAIR>(bar(C::b_empty + st), 3);
                 if (++st == stages) st = 0, ph ^= 1u;
             }
             if (ok) ptx::mma_commit_one<PAIR>(bar(C::b_done + acc), 3);
+            from = to == k_end ? k_begin : to;
+            if (to == k_end) t += step_tile;
         }
         if (!ok) {           // the MMAs that were issued end before the block does
             ptx::mma_commit_one<PAIR>(bar(C::b_last), 1);
@@ -347,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
             Tile tile, next = tile_at<C::tile_m>(s, first_tile);
             ahead(next);
             for (int t = first_tile; t < s.tiles; t += step_tile, ++done) {
-                const uint32_t acc = done & 1u;
+                const uint32_t acc = LONG ? 0 : done & 1u;
                 tile = next;
                 if (t + step_tile < s.tiles) ahead(next = tile_at<C::tile_m>(s, t + step_tile));
                 const int64_t row0 = tile.m + (int64_t)rank * 128 + quad * 32;
@@ -355,19 +395,25 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
                 const int chunks = (Epilogue::kDual ? 2 : 4) >> (tile.half ? 1 : 0);   // of 32 columns per warp
                 const int up = tile.half ? 64 : 128;                                   // the second product's columns
                 bool ok = true;
+                if constexpr (LONG) {
+                    const uint32_t at = lanes + half * chunks * 32;
+                    ok = join_pieces<PAIR>(bar(C::b_done + 1), ptx::map_rank(bar(C::b_free + 1), 0), at + second_half, at,
+                                           chunks * 32, Epilogue::kDual ? up : 0, pieces, done * pieces, abort_flag);
+                    if (!ok) break;
+                }
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
                     const int column = half * chunks * 32 + c * 32;
                     const int64_t col0 = tile.n + column;
                     auto ready = [&] {   // the first chunk's reads are under way: now the accumulator
-                        if (c == 0) {
+                        if (c == 0 && !LONG) {
                             ok = wait_all<PAIR>(bar(C::b_done + acc), (done >> 1) & 1u, abort_flag);
                             if (ok) ptx::tc_fence_after();
                         }
                         return ok;
                     };
                     auto drained = [&] {   // the last chunk has left TMEM
-                        if (c == chunks - 1) {
+                        if (c == chunks - 1 && !LONG) {
                             ptx::tc_fence_before();
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(bar(C::b_free + acc), 0));
@@ -457,7 +503,9 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
             const int own = quad * 32 + lane;
             if (tile.m + own < s.M && own % s.split == (int)rank)
                 epi.ahead(tile.group, tile.m + own, tile.n, (int)min((int64_t)s.tile_n, s.N - tile.n));
-            const bool ok = wait_all<PAIR>(bar(C::b_done), 0u, abort_flag);
+            const bool ok = LONG ? join_pieces<PAIR>(bar(C::b_done + 1), bar(C::b_free + 1), lanes + second_half, lanes,
+                                                     ((int)width + 31) / 32 * 32, 0, pieces, 0u, abort_flag)
+                                 : wait_all<PAIR>(bar(C::b_done), 0u, abort_flag);
             ptx::tc_fence_after();
             float* part = reinterpret_cast<float*>(smem + C::off_stages);   // over the (now idle) stages
             const int row = quad * 32 + lane;
@@ -577,9 +625,12 @@ __global__ void __launch_bounds__(Cfg<PAIR>::threads, PAIR ? 1 : 2)
 // ---------------------------------------------------------------- host
 template <class Epilogue>
 cudaError_t allow() {
-    static std::atomic<uint64_t> pair{0}, single{0};
-    cudaError_t e = ops::allow_shared(product_kernel<true, Epilogue>, (int)Cfg<true>::smem, pair);
-    return e != cudaSuccess ? e : ops::allow_shared(product_kernel<false, Epilogue>, (int)kSharedMost, single);
+    static std::atomic<uint64_t> done[4] = {};
+    cudaError_t e = ops::allow_shared(product_kernel<true, false, Epilogue>, (int)Cfg<true>::smem, done[0]);
+    if (e == cudaSuccess) e = ops::allow_shared(product_kernel<false, false, Epilogue>, (int)kSharedMost, done[1]);
+    if (e == cudaSuccess) e = ops::allow_shared(product_kernel<true, true, Epilogue>, (int)Cfg<true>::smem, done[2]);
+    if (e == cudaSuccess) e = ops::allow_shared(product_kernel<false, true, Epilogue>, (int)kSharedMost, done[3]);
+    return e;
 }
 
 // a1 and b1 may be null where the mode has one A or B.
@@ -608,8 +659,9 @@ cudaError_t launch(Shape s, const Epilogue& epi, const Factor* a0, const Factor*
     config.gridDim = (unsigned)c.grid;
     config.dynamicSmemBytes = c.pair ? Cfg<true>::smem : c.smem;
     config.stream = stream;
-    return c.pair ? cudaLaunchKernelEx(&config, product_kernel<true, Epilogue>, s, epi, *ma0, *ma1, *mb0, *mb1)
-                  : cudaLaunchKernelEx(&config, product_kernel<false, Epilogue>, s, epi, *ma0, *ma1, *mb0, *mb1);
+    auto* kernel = c.pair ? (c.long_sum ? product_kernel<true, true, Epilogue> : product_kernel<true, false, Epilogue>)
+                          : (c.long_sum ? product_kernel<false, true, Epilogue> : product_kernel<false, false, Epilogue>);
+    return cudaLaunchKernelEx(&config, kernel, s, epi, *ma0, *ma1, *mb0, *mb1);
 }
 
 // This translation unit's status word, then cleared if asked (current device).
