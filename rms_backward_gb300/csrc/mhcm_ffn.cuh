@@ -8,7 +8,8 @@ namespace ffn {
 // The normal distribution function at -|g|, from e = exp(-g^2 / 2): e / 2 times the scaled
 // complementary error function of z = |g| / sqrt 2, which is t times a polynomial in
 // t = 1 / (1 + 0.4 z) in [0, 1]: degree 8, fitted by reweighted least squares to the function
-// in FP64, off by 1.3e-7 of it at most (in FP32 arithmetic 4.5e-7), in the tail too.
+// in FP64; with the constants as rounded here off by 2e-7 of it at most (in FP32 arithmetic 4.6e-7), in the
+// tail too.
 __device__ __forceinline__ float normal_tail(float g, float e) {
     const float t = __fdividef(1.f, 1.f + 0.28284271f * fabsf(g));
     float p = 0.05026213f;
