@@ -543,7 +543,11 @@ mhcpb_status_t mhcpb_debug_checked_operator_sites(uint32_t* sites, int* checked)
  *    forms and another reads (a = act(g) u, dg, du; X, A, B) is rounded to 16 bits
  *    between the two, everything else once, at the output.  Up to 64 tokens what
  *    that rounding loses is kept beside it (of up to four, a is FP32), but for the
- *    weights' gradients;
+ *    weights' gradients.  With FP16 operands a, dg and du also have FP16's range:
+ *    beyond 65,504 they are infinite (a from five tokens on), and what is below 2^-25
+ *    is zero (2^-36 up to 64 tokens, but for the weights' gradients), with FP32
+ *    gradients too: grad_y is to be scaled as for any gradient in FP16, and BF16
+ *    taken where act(g) u grows that large;
  *  - the waits inside the kernels are bounded (1 s): one that runs out leaves wrong
  *    outputs and is reported by mhcpb_operators_device_status. */
 enum {                      /* activations */

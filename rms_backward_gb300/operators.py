@@ -291,7 +291,8 @@ def mhc_ffn_forward(x, w_gate, w_up, w_down, y, workspace, gate=None, up=None, *
     """y = (act(x w_gate^T) * (x w_up^T)) w_down^T: x, y [T, D] (BF16 or FP16, with
     row strides), w_gate, w_up [F, D], w_down [D, F] of the same type; activation
     "silu" or "gelu" (by erf).  gate, up [T, F] receive the two projections for
-    :func:`mhc_ffn_backward`, both None where none follows."""
+    :func:`mhc_ffn_backward`, both None where none follows.  In FP16, act(g) u beyond
+    65,504 becomes infinite from five tokens on."""
     T, D, F, kind, xp, xs, wg, wu, wd = _ffn(x, w_gate, w_up, w_down)
     dtype = x.dtype
     yp, ys = _rows(y, "y", (T, D), dtype)
@@ -311,7 +312,9 @@ def mhc_ffn_backward(x, w_gate, w_up, w_down, gate, up, grad_y, grad_x, grad_w_g
                      activation: str = "silu", accumulate: bool = False, stream=None):
     """grad_x [T, D] and the weights' gradients (of the weights' type, or all FP32;
     added to with ``accumulate``) from the forward's inputs, gate, up and grad_y
-    [T, D].  Each of the four outputs may be None."""
+    [T, D].  Each of the four outputs may be None.  In FP16 the gradients of the two
+    projections have FP16's range, with FP32 weights' gradients too: scale grad_y so
+    that they stay above 2^-25."""
     T, D, F, kind, xp, xs, wg, wu, wd = _ffn(x, w_gate, w_up, w_down)
     dtype = x.dtype
     grads = [(g, name, shape) for g, name, shape in ((grad_w_gate, "grad_w_gate", (F, D)), (grad_w_up, "grad_w_up", (F, D)),
