@@ -596,7 +596,8 @@ mhcpb_status_t mhcpb_ffn_backward(int64_t T, int64_t D, int64_t F, int type, int
  * or FP32) [m, n], out: BF16 [m, n], both with row strides.  1 <= m, n <=
  * MHCPB_MAX_K, 1 <= steps <= MHCPB_ORTH_MAX_STEPS, eps finite and >= 0 (a zero G
  * with eps = 0 gives NaN, else 0), scale finite.  A non-finite element makes all
- * of out NaN. */
+ * of out NaN.  A short side of at most 32 takes a cluster of 16 blocks: MHCPB_ERR_CUDA
+ * where a limit on the process's SMs leaves no place for one. */
 #define MHCPB_ORTH_MAX_STEPS 32
 mhcpb_status_t mhcpb_orthogonalize_workspace_bytes(int64_t m, int64_t n, size_t* bytes);
 mhcpb_status_t mhcpb_orthogonalize(int64_t m, int64_t n, int type, const void* g, int64_t g_stride,

@@ -1,8 +1,8 @@
 // The orthogonalised update of a matrix with a short side of at most 32 (sm_103a),
-// such as the projection's weight [24, K]: there the general path is fifteen
-// launches of next to no work, 6 us each at the least.  Here one cluster of 16
-// blocks holds X in its shared memory, in FP32, each block a sixteenth of the long
-// side, and takes all steps in one launch:
+// such as the projection's weight [24, K]: there the general path is seventeen
+// launches of next to no work.  Here one cluster of 16 blocks holds X in its shared
+// memory, in FP32, each block a sixteenth of the long side, and takes all steps in one
+// launch (which fails where the process may not use so many SMs of one GPU cluster):
 //
 //   A = X X^T   per block over its columns, 4 x 4 tiles per thread; the blocks' parts
 //               are added in rank order by every block (distributed shared memory)

@@ -60,8 +60,8 @@ __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
 
 // The wrappers below whose name ends in _one are called by a whole warp with the
 // same arguments in every lane, and issue their instructions in one lane (always the
-// same: elect.sync is deterministic).  So the operands stay in uniform registers; under
-// a branch on the lane number each TMA or tcgen05 instruction costs some 200 clocks.
+// same: elect.sync is deterministic).  Under a branch on the lane number a step of 64 k took
+// 840 clocks to issue, this way 500.
 __device__ __forceinline__ void mbar_expect_one(uint32_t bar, uint32_t bytes) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
